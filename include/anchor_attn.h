@@ -324,6 +324,101 @@ ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_test_forward(const void *Q, con
                                                               int hold_slice, unsigned long long wait_ns,
                                                               int force_recompute, void *stream);
 
+/*
+ * Rows of heads: a [B][heads][n][d] tensor whose last axis is dense.  The three strides are in
+ * elements, multiples of 16 bytes (the base pointer too), and not negative; the stride of an axis
+ * of one entry is not looked at.  An input may repeat rows (a stride of 0); an output may not.
+ */
+typedef struct {
+    void *ptr;
+    long long batch, head, row;
+} anchor_attn_view_t;
+
+/*
+ * Rotary positions, and the norm of each head's query or key with the rotation in the same pass:
+ * front ends of the attention calls, which take their queries and keys (or anchors) as they come.
+ *
+ *   z = weight o x / sqrt(mean(x^2) + eps)           (norm = 1; else z = x)
+ *   y_a = magnitude (z_a cos t - z_b sin t),  y_b = magnitude (z_a sin t + z_b cos t)
+ *
+ * for the pairs (a, b) of the head's first `rot` columns: (p, p + rot / 2), or (2p, 2p + 1) with
+ * interleaved = 1, p < rot / 2; the columns from `rot` on are passed through.  The angle is
+ * t = 2 pi 2^-64 sum_axis position[axis] phases[axis][p], the sum taken modulo 2^64: a phase is
+ * the part of a turn that one position adds, as a 64-bit two's complement fraction, so that an
+ * angle is as exact at position 10^9 as at 0.  Scaling for long contexts is in the phases and in
+ * `magnitude`.  Products, sums and the norm are taken in fp32; y is rounded once.
+ */
+typedef struct {
+    int dtype;                  /* of the rows: 0 = bf16, 1 = fp32                            */
+    int d;                      /* 16, 32, 64 or 128                                          */
+    int rot;                    /* even, 0 <= rot <= d                                        */
+    int axes;                   /* of a position: 1 to 3                                      */
+    int interleaved;            /* 0: halves, 1: neighbours                                   */
+    int norm;                   /* 1: normalise the rows first                                */
+    int weight_f32;             /* type of the weights and their gradients: 0 = the rows', 1 = fp32 */
+    int positions64;            /* type of the positions: 0 = int32, 1 = int64                */
+    float eps;                  /* finite, >= 0                                               */
+    float magnitude;            /* finite                                                     */
+    const long long *phases;    /* device, [axes][rot / 2] (NULL when rot = 0)                */
+} anchor_attn_rope_t;
+
+/* The rows of one tensor: Y from X (forward); dX and dweight from X and dY (backward, where
+ * X and the weight are used with norm = 1 alone). */
+typedef struct {
+    anchor_attn_view_t X, Y, dY, dX;
+    const void *weight;         /* [d] or NULL for ones                                       */
+    void *dweight;              /* [d] or NULL for none; summed over batch, heads and rows    */
+    const void *positions;      /* device, [B][n][axes]; NULL: every axis is start + row      */
+    long long positions_batch;  /* stride between batch entries, in values (0: one for all)   */
+    long long start;
+    int B, heads, n;
+} anchor_attn_rows_t;
+
+/*
+ * Forward and backward for one or two tensors (queries and keys) in one launch; `second` may be
+ * NULL.  Y may be X itself (the same view); otherwise no output may overlap an input or another
+ * output (ANCHOR_ATTN_ERR_ALIAS).  The backward of the rotation alone needs no X; dweight is
+ * given with norm = 1 and a weight or not.  B * n < 2^31 per tensor.  The backward with a
+ * dweight takes a workspace on `stream` and one launch more; its sums run in an order that the
+ * shapes fix, so results are bit-identical from run to run.  A tensor without rows is skipped
+ * (its dweight is set to zero).
+ */
+ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_norm_rope(const anchor_attn_rope_t *how, const anchor_attn_rows_t *first,
+                                                           const anchor_attn_rows_t *second, void *stream);
+ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_norm_rope_backward(const anchor_attn_rope_t *how,
+                                                                    const anchor_attn_rows_t *first,
+                                                                    const anchor_attn_rows_t *second, void *stream);
+
+/*
+ * Cross attention: n queries of each batch entry over the s states of another sequence (an
+ * encoder's), of which the first lengths[b] count:
+ *   lse[i] = ln sum_{j < L} exp(scale q_i . k_j),   H[i] = sum_{j < L} exp(scale q_i . k_j - lse[i]) v_j.
+ * An entry with L = 0 has H = 0 and lse = -infinity.  States from L on are not used, whatever
+ * they hold.  heads is a multiple of kv_heads: query heads h with the same h / (heads / kv_heads)
+ * share a key head.
+ *   Q, H, dH, dQ [B][heads][n][d]; K, V, dK, dV [B][kv_heads][s][d]; lse [B][heads][n] fp32, dense
+ *   lengths: device int32 [B], each taken into [0, s]; NULL: s for all
+ * bf16 in and out (tensor cores: bf16 operands, fp32 accumulators, the weights rounded to bf16
+ * before they meet V) or fp32 (CUDA cores, fp32 throughout).  d in {16, 32, 64, 128}.
+ * The forward writes H, and lse where it is not NULL.  The backward takes them and dH, and
+ * writes dQ, dK, dV (rows of dK and dV from L on are zero; entries that share K or V by a stride
+ * of 0 get gradients of their own).
+ * Sizes: B, heads, n, s >= 0; B * heads * (n + s) < 2^31.  Results are bit-identical from run to run.
+ * Workspaces come from a pool of the library on `stream` and go back on it.  A bounded wait
+ * that gives up is reported by anchor_attn_device_error (bit 0).
+ */
+typedef struct {
+    int dtype;                  /* 0 = bf16, 1 = fp32                                         */
+    int B, heads, kv_heads, n, s, d;
+    float scale;                /* finite                                                     */
+    anchor_attn_view_t Q, K, V, H, dH, dQ, dK, dV;
+    float *lse;
+    const int *lengths;
+} anchor_attn_cross_t;
+
+ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_cross_forward(const anchor_attn_cross_t *p, void *stream);
+ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_cross_backward(const anchor_attn_cross_t *p, void *stream);
+
 /* Human-readable name of a status code (static storage). */
 ANCHOR_ATTN_API const char *anchor_attn_status_string(anchor_attn_status_t status);
 

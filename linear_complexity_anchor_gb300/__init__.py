@@ -12,6 +12,10 @@ import math
 import os
 import threading
 
+from . import _cross, _rope
+from ._cross import cross_backward, cross_forward
+from ._rope import RopeTable, norm_rope, norm_rope_backward, rope, rope_backward, rope_frequencies, rope_table
+
 __all__ = [
     "LIB_PATH", "load", "forward", "anchor_attn_forward", "anchor_attn_forward_f32",
     "anchor_attn_forward_ptr", "anchor_attn_forward_f32_ptr", "anchor_attn_forward_static_scratch_ptr",
@@ -19,6 +23,8 @@ __all__ = [
     "AnchorAttnError", "STATUS", "VARIANTS", "backward", "anchor_attn_backward_ptr", "anchor_attn_backward_f32_ptr",
     "full_forward", "relative_error", "causal_forward", "block_forward", "anchor_attn_block_forward_ptr",
     "forward_host", "anchor_attn_forward_host_ptr", "anchor_attn_forward_host_f32_ptr",
+    "cross_forward", "cross_backward", "rope", "rope_backward", "norm_rope", "norm_rope_backward", "rope_table",
+    "rope_frequencies", "RopeTable",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libanchor_attn.so")
@@ -87,6 +93,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.anchor_attn_device_error.restype = ctypes.c_int
         lib.anchor_attn_status_string.argtypes = [ctypes.c_int]
         lib.anchor_attn_status_string.restype = ctypes.c_char_p
+        _cross.bind(lib)
+        _rope.bind(lib)
         if path is None:
             _lib = lib
         return lib

@@ -1,0 +1,214 @@
+// Cross attention: argument checks, plan and launch; the join of a forward's parts; D = dH . H
+// (formulas and layout in include/anchor_attn.h).
+#include "cross.cuh"
+
+#include <math.h>
+#include <stdlib.h>
+
+namespace anchor {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// One warp per row, lanes over the columns.  H = sum_parts o 2^(m - M) / sum_parts l 2^(m - M),
+// the parts in order.  Reads the parts once: bound by memory, and small next to K and V (a part
+// has two tiles of keys at least for each row tile).
+template <typename T>
+__global__ void __launch_bounds__(256) cross_join_kernel(const CrossProblem p, const CrossParts w, long long total) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const long long f = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (f >= total) return;
+    float M = -INFINITY;
+    for (int q = lane; q < w.parts; q += 32) M = fmaxf(M, w.ml[q * total + f].x);
+    M = warp_max(M);
+    const float shift = M == -INFINITY ? 0.f : M;
+    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    const int per = p.d / 32 > 0 ? p.d / 32 : 1;  // columns of a lane (the upper lanes idle at d = 16)
+    const bool on = lane * per < p.d;
+    for (int q = 0; q < w.parts; ++q) {
+        const float2 ml = w.ml[q * total + f];
+        const float k = exp2f(ml.x - shift);
+        l += ml.y * k;
+        if (!on) continue;
+        const float *src = w.o + (q * total + f) * p.d + lane * per;
+        for (int j = 0; j < per; ++j) o[j] = fmaf(src[j], k, o[j]);
+    }
+    const int r = (int)(f % p.rows);
+    const long long bk = f / p.rows;
+    const int b = (int)(bk / p.kv), k = (int)(bk - (long long)b * p.kv);
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // no state at all
+    if (on) {
+        T *H = (T *)p.H.ptr + cross_row(p, p.H, b, k, r) + lane * per;
+        for (int j = 0; j < per; ++j) H[j] = from_f32<T>(o[j] * inv);
+    }
+    if (p.lse && lane == 0) p.lse[f] = l == 0.f ? -INFINITY : M * (1.f / kLog2e) + logf(l);
+}
+
+// 8 columns of one row per thread, the row's threads (d / 8) next to one another in a warp.
+// Bound by memory.
+template <typename T>
+__global__ void __launch_bounds__(256) cross_delta_kernel(const CrossProblem p, float *delta, long long total) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int per = p.d / 8;
+    const long long f = ((long long)blockIdx.x * 256 + threadIdx.x) / per;
+    const int c = (int)(threadIdx.x % per) * 8;
+    float s = 0.f;
+    if (f < total) {
+        const int r = (int)(f % p.rows);
+        const long long bk = f / p.rows;
+        const int b = (int)(bk / p.kv), k = (int)(bk - (long long)b * p.kv);
+        const T *h = (const T *)p.H.ptr + cross_row(p, p.H, b, k, r) + c;
+        const T *g = (const T *)p.dH.ptr + cross_row(p, p.dH, b, k, r) + c;
+        uint4 a[sizeof(T) / 2], e[sizeof(T) / 2];
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            a[i] = reinterpret_cast<const uint4 *>(h)[i];
+            e[i] = reinterpret_cast<const uint4 *>(g)[i];
+        }
+        const T *x = reinterpret_cast<const T *>(a), *y = reinterpret_cast<const T *>(e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s = fmaf(to_f32(x[i]), to_f32(y[i]), s);
+    }
+    for (int o = per / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (f < total && c == 0) delta[f] = s;
+}
+
+}  // namespace
+
+cudaError_t launch_cross_join(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
+    const long long total = (long long)p.B * p.kv * p.rows;
+    const dim3 grid((unsigned)((total + 7) / 8));
+    return p.f32 ? launch_pdl(cross_join_kernel<float>, grid, dim3(256), 0, stream, p, w, total)
+                 : launch_pdl(cross_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, p, w, total);
+}
+
+cudaError_t launch_cross_delta(const CrossProblem &p, float *delta, cudaStream_t stream) {
+    const long long total = (long long)p.B * p.kv * p.rows;
+    const dim3 grid((unsigned)((total * (p.d / 8) + 255) / 256));
+    return p.f32 ? launch_pdl(cross_delta_kernel<float>, grid, dim3(256), 0, stream, p, delta, total)
+                 : launch_pdl(cross_delta_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, p, delta, total);
+}
+
+namespace {
+
+CrossView lower(const View &v) { return CrossView{v.ptr, v.sb, v.sh, v.sn}; }
+
+anchor_attn_status_t cross(const anchor_attn_cross_t *a, bool bwd, void *stream_v) {
+    if (!a) return ANCHOR_ATTN_ERR_INVALID_ARG;
+    cudaStream_t stream = (cudaStream_t)stream_v;
+    if ((a->dtype != 0 && a->dtype != 1) || a->B < 0 || a->heads < 0 || a->kv_heads < 0 || a->n < 0 || a->s < 0)
+        return ANCHOR_ATTN_ERR_INVALID_ARG;
+    if (a->d != 16 && a->d != 32 && a->d != 64 && a->d != 128) return ANCHOR_ATTN_ERR_UNSUPPORTED;
+    if (!isfinite(a->scale)) return ANCHOR_ATTN_ERR_INVALID_ARG;
+    if (a->B == 0 || a->heads == 0) {
+        return a->heads == 0 && a->kv_heads > 0 && a->B > 0 && a->s > 0 ? ANCHOR_ATTN_ERR_INVALID_ARG : ANCHOR_ATTN_OK;
+    }
+    if (a->kv_heads == 0 || a->heads % a->kv_heads) return ANCHOR_ATTN_ERR_INVALID_ARG;
+    if ((long long)a->n + a->s > 0x7fffffffLL / ((long long)a->B * a->heads)) return ANCHOR_ATTN_ERR_UNSUPPORTED;
+    if (((uintptr_t)a->lse & 3u) || ((uintptr_t)a->lengths & 3u)) return ANCHOR_ATTN_ERR_INVALID_ARG;
+
+    CrossProblem p = {};
+    p.B = a->B, p.heads = a->heads, p.kv = a->kv_heads, p.group = a->heads / a->kv_heads;
+    p.n = a->n, p.s = a->s, p.d = a->d, p.rows = p.group * a->n, p.scale = a->scale, p.f32 = a->dtype == 1;
+    p.lse = a->lse, p.lengths = a->lengths;
+    const int es = p.f32 ? 4 : 2;
+    const bool queries = a->n > 0, states = a->s > 0;
+    View in[6], out[3];
+    const void *in_dense[2] = {a->lengths, bwd ? a->lse : nullptr};
+    const size_t rows_bytes = (size_t)a->B * a->heads * a->n * 4;
+    const size_t in_dense_bytes[2] = {(size_t)a->B * 4, rows_bytes};
+    int nin = 0, nout = 0;
+    anchor_attn_status_t st = ANCHOR_ATTN_OK;
+    auto add = [&](const anchor_attn_view_t &v, bool q, bool writes, CrossView &to) {
+        if (st != ANCHOR_ATTN_OK || !(q ? queries : states)) return;
+        const View w = make_view(v, a->B, q ? a->heads : a->kv_heads, q ? a->n : a->s, a->d, es);
+        st = check_view(w, writes);
+        if (writes) out[nout++] = w;
+        else in[nin++] = w;
+        to = lower(w);
+    };
+    add(a->Q, true, false, p.Q);
+    add(a->K, false, false, p.K);
+    add(a->V, false, false, p.V);
+    add(a->H, true, !bwd, p.H);
+    if (bwd) {
+        add(a->dH, true, false, p.dH);
+        add(a->dQ, true, true, p.dQ);
+        add(a->dK, false, true, p.dK);
+        add(a->dV, false, true, p.dV);
+        if (queries && !a->lse) return ANCHOR_ATTN_ERR_INVALID_ARG;
+    }
+    if (st != ANCHOR_ATTN_OK) return st;
+    for (int o = 0; o < nout; ++o) {
+        for (int i = 0; i < nin; ++i)
+            if (views_overlap(out[o], in[i])) return ANCHOR_ATTN_ERR_ALIAS;
+        for (int i = 0; i < o; ++i)
+            if (views_overlap(out[o], out[i])) return ANCHOR_ATTN_ERR_ALIAS;
+        for (int i = 0; i < 2; ++i)
+            if (in_dense[i] && bytes_overlap(out[o].ptr, (size_t)out[o].extent(), in_dense[i], in_dense_bytes[i]))
+                return ANCHOR_ATTN_ERR_ALIAS;
+        if (!bwd && a->lse && bytes_overlap(out[o].ptr, (size_t)out[o].extent(), a->lse, rows_bytes))
+            return ANCHOR_ATTN_ERR_ALIAS;
+    }
+    if (!bwd && a->lse) {
+        for (int i = 0; i < nin; ++i)
+            if (bytes_overlap(a->lse, rows_bytes, in[i].ptr, (size_t)in[i].extent())) return ANCHOR_ATTN_ERR_ALIAS;
+        if (a->lengths && bytes_overlap(a->lse, rows_bytes, a->lengths, (size_t)a->B * 4)) return ANCHOR_ATTN_ERR_ALIAS;
+    }
+    if (!queries && !(bwd && states)) return ANCHOR_ATTN_OK;
+
+    cudaError_t e = cudaSuccess;
+    void *ws = nullptr;
+    auto take = [&](size_t bytes) -> bool {
+        if (getenv("ANCHOR_ATTN_TEST_FAIL_ALLOC") != nullptr) return false;
+        if (workspace_alloc(&ws, bytes, stream) == cudaSuccess) return true;
+        cudaGetLastError();
+        return false;
+    };
+    if (!bwd) {
+        CrossParts w = {nullptr, nullptr, cross_simt_parts(p)};
+        if (w.parts > 1) {
+            const size_t total = (size_t)p.B * p.kv * p.rows * w.parts;
+            if (!take(total * (p.d * 4 + 8))) return ANCHOR_ATTN_ERR_ALLOC;
+            w.o = (float *)ws;
+            w.ml = (float2 *)(w.o + total * p.d);
+        }
+        e = launch_cross_simt_forward(p, w, stream);
+        if (e == cudaSuccess && w.parts > 1) e = launch_cross_join(p, w, stream);
+    } else {
+        float *delta = nullptr;
+        if (queries) {
+            if (!take(rows_bytes)) return ANCHOR_ATTN_ERR_ALLOC;
+            delta = (float *)ws;
+            e = launch_cross_delta(p, delta, stream);
+        }
+        if (e == cudaSuccess) e = launch_cross_simt_backward(p, delta, stream);
+    }
+    if (ws) {
+        const cudaError_t ef = cudaFreeAsync(ws, stream);
+        if (e == cudaSuccess) e = ef;
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return ANCHOR_ATTN_ERR_CUDA;
+    }
+    return ANCHOR_ATTN_OK;
+}
+
+}  // namespace
+}  // namespace anchor
+
+extern "C" {
+
+anchor_attn_status_t anchor_attn_cross_forward(const anchor_attn_cross_t *p, void *stream) {
+    return anchor::cross(p, false, stream);
+}
+
+anchor_attn_status_t anchor_attn_cross_backward(const anchor_attn_cross_t *p, void *stream) {
+    return anchor::cross(p, true, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,55 @@
+// Cross attention: the problem as the launches see it (formulas and layout in
+// include/anchor_attn.h).  Query rows are taken per key head: row r of key head k is query
+// r % n of head k * group + r / n, so that the heads that share keys fill one tile.
+#pragma once
+
+#include "common.cuh"
+#include "views.cuh"
+
+namespace anchor {
+
+struct CrossView {
+    const void *ptr;
+    long long sb, sh, sn;  // strides in elements
+};
+
+struct CrossProblem {
+    CrossView Q, K, V, H, dH, dQ, dK, dV;
+    float *lse;           // [B][heads][n] or null
+    const int *lengths;   // [B] or null
+    int B, heads, kv, group, n, s, d;
+    int rows;             // group * n
+    float scale;
+    bool f32;
+};
+
+__device__ __forceinline__ int cross_length(const CrossProblem &p, int b) {
+    return p.lengths ? min(max(__ldg(p.lengths + b), 0), p.s) : p.s;
+}
+// row r of key head k: its offset in a [B][heads][n][d] view
+__device__ __forceinline__ long long cross_row(const CrossProblem &p, const CrossView &v, int b, int k, int r) {
+    const int g = r / p.n, i = r - g * p.n;
+    return b * v.sb + (long long)(k * p.group + g) * v.sh + (long long)i * v.sn;
+}
+// ... and in a dense [B][heads][n] array
+__device__ __forceinline__ long long cross_flat(const CrossProblem &p, int b, int k, int r) {
+    return ((long long)b * p.kv + k) * p.rows + r;  // the group's heads follow one another
+}
+
+// The parts of a forward whose keys are cut over several CTAs: unnormalised sums and (maximum in
+// units of log2, sum) per part, [parts][B * kv * rows][d] and [parts][B * kv * rows].
+struct CrossParts {
+    float *o;
+    float2 *ml;
+    int parts;
+};
+cudaError_t launch_cross_join(const CrossProblem &p, const CrossParts &w, cudaStream_t stream);
+// D_r = dH_r . H_r, [B][heads][n]
+cudaError_t launch_cross_delta(const CrossProblem &p, float *delta, cudaStream_t stream);
+
+// CUDA cores, fp32 arithmetic
+int cross_simt_parts(const CrossProblem &p);
+cudaError_t launch_cross_simt_forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream);
+cudaError_t launch_cross_simt_backward(const CrossProblem &p, const float *delta, cudaStream_t stream);
+
+}  // namespace anchor

@@ -1,0 +1,388 @@
+// Cross attention on CUDA cores, fp32 arithmetic, forward and backward (formulas in
+// include/anchor_attn.h).
+//
+// Tiles of BM rows by 64 columns, 256 threads as 16 x 16: a thread has BM / 16 rows (next to one
+// another) and columns tx, tx + 16, tx + 32, tx + 48 of the scores, and BM / 16 rows by d / 16
+// columns of the outputs.  All tiles lie row by row in shared memory with a pitch of d + 4 floats:
+// 16-byte reads along d (scores) and along the columns (outputs) are then free of conflicts, and
+// one copy serves both products.  At BM = 64 each 16-byte read feeds 8 (scores) and 10 (outputs)
+// FMAs a thread.  Fewer rows per tile when there are not CTAs for all SMs.
+//
+// Forward: online softmax, one pass over the keys; with parts, a CTA has a run of key tiles of its
+// entry's own length, and leaves sums that a second launch joins.
+// Backward: P again from lse; one kernel for both products that differ in what stays:
+//   dQ          rows = queries, columns = keys:    dQ += dS K
+//   dK and dV   rows = keys, columns = queries:    dV += P^T dH, dK += dS^T Q
+// so every gradient is summed by one CTA in a fixed order, without atomics.
+#include "common.cuh"
+#include "cross.cuh"
+
+#include <math.h>
+
+namespace anchor {
+namespace {
+
+constexpr int kThreads = 256, kBN = 64;
+constexpr int kPitchS = kBN + 4;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 a = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u), __uint_as_float(a.y << 16),
+                       __uint_as_float(a.y & 0xffff0000u));
+}
+
+// `rows` rows of D elements into shared memory as fp32, zeros where at(r) is null
+template <int D, typename At>
+__device__ __forceinline__ void load_rows(float *dst, int rows, At at) {
+    constexpr int C = D / 4;
+    for (int i = threadIdx.x; i < rows * C; i += kThreads) {
+        const int r = i / C, c = 4 * (i - r * C);
+        const auto *src = at(r);
+        *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) =
+            src ? load4(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+}
+
+// s[i][j] = a row (ty TM + i) . b row (tx + 16 j)
+template <int D, int TM>
+__device__ __forceinline__ void dots(const float *a, const float *b, float (&s)[TM][4]) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < D; k += 4) {
+        float4 x[TM], y[4];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) x[i] = *reinterpret_cast<const float4 *>(a + (ty * TM + i) * (D + 4) + k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(b + (tx + 16 * j) * (D + 4) + k);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
+                s[i][j] = fmaf(x[i].y, y[j].y, s[i][j]);
+                s[i][j] = fmaf(x[i].z, y[j].z, s[i][j]);
+                s[i][j] = fmaf(x[i].w, y[j].w, s[i][j]);
+            }
+    }
+}
+
+// this thread's output columns: D / 16 of them, in runs of up to four
+template <int D> constexpr int kCols = D / 16;
+template <int D> __device__ __forceinline__ int col_of(int j) {
+    const int tx = threadIdx.x & 15;
+    return D >= 64 ? 4 * tx + 64 * (j / 4) + j % 4 : tx * kCols<D> + j;
+}
+
+// o[i][j] += sum_key w[ty TM + i][key] v[key][col j]
+template <int D, int TM>
+__device__ __forceinline__ void accumulate(const float *w, const float *v, float (&o)[TM][kCols<D>]) {
+    const int ty = threadIdx.x >> 4;
+#pragma unroll 2
+    for (int k = 0; k < kBN; k += 4) {
+        float x[TM][4];
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            *reinterpret_cast<float4 *>(x[i]) = *reinterpret_cast<const float4 *>(w + (ty * TM + i) * kPitchS + k);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float y[kCols<D>];
+            if constexpr (kCols<D> >= 4) {
+#pragma unroll
+                for (int j = 0; j < kCols<D>; j += 4)
+                    *reinterpret_cast<float4 *>(y + j) =
+                        *reinterpret_cast<const float4 *>(v + (k + q) * (D + 4) + col_of<D>(j));
+            } else {
+#pragma unroll
+                for (int j = 0; j < kCols<D>; ++j) y[j] = v[(k + q) * (D + 4) + col_of<D>(j)];
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < kCols<D>; ++j) o[i][j] = fmaf(x[i][q], y[j], o[i][j]);
+        }
+    }
+}
+
+template <int D, int TM>
+__device__ __forceinline__ void store_scores(float *dst, const float (&s)[TM][4]) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dst[(ty * TM + i) * kPitchS + tx + 16 * j] = s[i][j];
+}
+
+// over the 16 threads of a row
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+template <int D, int TM> constexpr size_t forward_smem() {
+    return 4 * ((size_t)(16 * TM + 2 * kBN) * (D + 4) + 16 * TM * kPitchS);
+}
+
+template <typename T, int D, int TM>
+__global__ void __launch_bounds__(kThreads) cross_simt_forward_kernel(const CrossProblem p, const CrossParts w, int tiles) {
+    constexpr int BM = 16 * TM;
+    extern __shared__ __align__(16) float sm[];
+    float *sQ = sm, *sK = sQ + BM * (D + 4), *sV = sK + kBN * (D + 4), *sP = sV + kBN * (D + 4);
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int tile = (int)(blockIdx.x % tiles), bk = (int)(blockIdx.x / tiles);
+    const int b = bk / p.kv, k = bk - b * p.kv, r0 = tile * BM;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int L = cross_length(p, b), key_tiles = (L + kBN - 1) / kBN;
+    const int t0 = (int)((long long)key_tiles * blockIdx.y / w.parts), t1 = (int)((long long)key_tiles * (blockIdx.y + 1) / w.parts);
+    const float c = p.scale * kLog2e;
+    const T *Q = (const T *)p.Q.ptr;
+    const T *K = (const T *)p.K.ptr + b * p.K.sb + k * p.K.sh, *V = (const T *)p.V.ptr + b * p.V.sb + k * p.V.sh;
+    load_rows<D>(sQ, BM, [&](int r) { return r0 + r < p.rows ? Q + cross_row(p, p.Q, b, k, r0 + r) : nullptr; });
+    float m[TM], l[TM], o[TM][kCols<D>];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        m[i] = -INFINITY, l[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < kCols<D>; ++j) o[i][j] = 0.f;
+    }
+    for (int t = t0; t < t1; ++t) {
+        __syncthreads();
+        load_rows<D>(sK, kBN, [&](int r) { return t * kBN + r < L ? K + (t * kBN + r) * p.K.sn : nullptr; });
+        load_rows<D>(sV, kBN, [&](int r) { return t * kBN + r < L ? V + (t * kBN + r) * p.V.sn : nullptr; });
+        __syncthreads();
+        float s[TM][4];
+        dots<D, TM>(sQ, sK, s);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            float top = m[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = t * kBN + tx + 16 * j < L ? s[i][j] * c : -INFINITY;
+                top = fmaxf(top, s[i][j]);
+            }
+            top = row_max(top);
+            const float shift = top == -INFINITY ? 0.f : top;  // a row whose scores are all -infinity
+            const float keep = exp2f(m[i] - shift);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = exp2f(s[i][j] - shift);
+                sum += s[i][j];
+            }
+            l[i] = l[i] * keep + row_sum(sum);
+            m[i] = top;
+#pragma unroll
+            for (int j = 0; j < kCols<D>; ++j) o[i][j] *= keep;
+        }
+        store_scores<D, TM>(sP, s);
+        __syncwarp();  // a warp writes and reads its own rows of P
+        accumulate<D, TM>(sP, sV, o);
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int r = r0 + ty * TM + i;
+        if (r >= p.rows) continue;
+        if (w.parts > 1) {
+            const long long f = (long long)blockIdx.y * p.B * p.kv * p.rows + cross_flat(p, b, k, r);
+#pragma unroll
+            for (int j = 0; j < kCols<D>; ++j) w.o[f * D + col_of<D>(j)] = o[i][j];
+            if (tx == 0) w.ml[f] = make_float2(m[i], l[i]);
+            continue;
+        }
+        T *H = (T *)p.H.ptr + cross_row(p, p.H, b, k, r);
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // no state at all
+#pragma unroll
+        for (int j = 0; j < kCols<D>; ++j) H[col_of<D>(j)] = from_f32<T>(o[i][j] * inv);
+        if (p.lse && tx == 0) p.lse[cross_flat(p, b, k, r)] = l[i] == 0.f ? -INFINITY : m[i] * (1.f / kLog2e) + logf(l[i]);
+    }
+}
+
+template <int D, int TM> constexpr size_t backward_smem() {
+    return 4 * ((size_t)(2 * 16 * TM + 2 * kBN) * (D + 4) + 16 * TM * kPitchS + 2 * kBN);
+}
+
+// KEYS: rows are keys, columns the query rows of the key head; else rows are query rows.
+template <typename T, int D, int TM, bool KEYS>
+__global__ void __launch_bounds__(kThreads) cross_simt_backward_kernel(const CrossProblem p, const float *delta, int tiles) {
+    constexpr int BM = 16 * TM;
+    extern __shared__ __align__(16) float sm[];
+    // rows: (Q, dH) or (K, V); columns: (K, V) or (Q, dH)
+    float *sA = sm, *sA2 = sA + BM * (D + 4), *sB = sA2 + BM * (D + 4), *sB2 = sB + kBN * (D + 4), *sW = sB2 + kBN * (D + 4);
+    float *sL = sW + BM * kPitchS, *sD = sL + kBN;  // KEYS: the columns' lse and D
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int tile = (int)(blockIdx.x % tiles), bk = (int)(blockIdx.x / tiles);
+    const int b = bk / p.kv, k = bk - b * p.kv, r0 = tile * BM;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int L = cross_length(p, b);
+    const float c = p.scale * kLog2e;
+    const T *Q = (const T *)p.Q.ptr, *G = (const T *)p.dH.ptr;
+    const T *K = (const T *)p.K.ptr + b * p.K.sb + k * p.K.sh, *V = (const T *)p.V.ptr + b * p.V.sb + k * p.V.sh;
+    auto q_row = [&](int r) { return r < p.rows ? Q + cross_row(p, p.Q, b, k, r) : nullptr; };
+    auto g_row = [&](int r) { return r < p.rows ? G + cross_row(p, p.dH, b, k, r) : nullptr; };
+    auto k_row = [&](int r) { return r < L ? K + r * p.K.sn : nullptr; };
+    auto v_row = [&](int r) { return r < L ? V + r * p.V.sn : nullptr; };
+    load_rows<D>(sA, BM, [&](int r) { return KEYS ? k_row(r0 + r) : q_row(r0 + r); });
+    load_rows<D>(sA2, BM, [&](int r) { return KEYS ? v_row(r0 + r) : g_row(r0 + r); });
+    float o[TM][kCols<D>], o2[KEYS ? TM : 1][kCols<D>], lse2[TM], dl[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+#pragma unroll
+        for (int j = 0; j < kCols<D>; ++j) {
+            o[i][j] = 0.f;
+            if (KEYS) o2[i][j] = 0.f;
+        }
+        const int r = r0 + ty * TM + i;
+        lse2[i] = dl[i] = 0.f;
+        if (!KEYS && r < p.rows) {
+            const long long f = cross_flat(p, b, k, r);
+            lse2[i] = p.lse[f] * kLog2e;
+            dl[i] = delta[f];
+        }
+    }
+    const int cols = KEYS ? (r0 < L ? p.rows : 0) : L;  // a tile of masked keys has no gradient
+    for (int c0 = 0; c0 < cols; c0 += kBN) {
+        __syncthreads();
+        load_rows<D>(sB, kBN, [&](int r) { return KEYS ? q_row(c0 + r) : k_row(c0 + r); });
+        load_rows<D>(sB2, kBN, [&](int r) { return KEYS ? g_row(c0 + r) : v_row(c0 + r); });
+        if (KEYS && threadIdx.x < kBN) {
+            const bool in = c0 + (int)threadIdx.x < p.rows;
+            const long long f = in ? cross_flat(p, b, k, c0 + threadIdx.x) : 0;
+            sL[threadIdx.x] = in ? p.lse[f] * kLog2e : 0.f;
+            sD[threadIdx.x] = in ? delta[f] : 0.f;
+        }
+        __syncthreads();
+        float s[TM][4], g[TM][4];
+        dots<D, TM>(sA, sB, s);
+        dots<D, TM>(sA2, sB2, g);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int col = tx + 16 * j;
+                const bool on = KEYS ? (r0 + ty * TM + i < L && c0 + col < p.rows) : c0 + col < L;
+                s[i][j] = on ? exp2f(fmaf(s[i][j], c, -(KEYS ? sL[col] : lse2[i]))) : 0.f;
+                g[i][j] = on ? s[i][j] * (g[i][j] - (KEYS ? sD[col] : dl[i])) : 0.f;
+            }
+        if constexpr (KEYS) {
+            store_scores<D, TM>(sW, s);
+            __syncwarp();
+            accumulate<D, TM>(sW, sB2, o2);
+            __syncwarp();
+        }
+        store_scores<D, TM>(sW, g);
+        __syncwarp();
+        accumulate<D, TM>(sW, sB, o);
+        __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int r = r0 + ty * TM + i;
+        if (r >= (KEYS ? p.s : p.rows)) continue;
+        T *dst = KEYS ? (T *)p.dK.ptr + b * p.dK.sb + k * p.dK.sh + r * p.dK.sn : (T *)p.dQ.ptr + cross_row(p, p.dQ, b, k, r);
+#pragma unroll
+        for (int j = 0; j < kCols<D>; ++j) dst[col_of<D>(j)] = from_f32<T>(o[i][j] * p.scale);
+        if constexpr (KEYS) {
+            dst = (T *)p.dV.ptr + b * p.dV.sb + k * p.dV.sh + r * p.dV.sn;
+#pragma unroll
+            for (int j = 0; j < kCols<D>; ++j) dst[col_of<D>(j)] = from_f32<T>(o2[i][j]);
+        }
+    }
+}
+
+// rows of a tile: the most of 64, 32 and 16 that still gives every SM a CTA, else 16
+int tile_m(const CrossProblem &p, long long rows) {
+    const long long heads = (long long)p.B * p.kv;
+    int tm = 4;
+    while (tm > 1 && (heads * ((rows + 16 * tm - 1) / (16 * tm)) < kPlanSMs || rows <= 8 * tm)) tm /= 2;
+    return tm;
+}
+
+template <typename Kernel>
+cudaError_t set_smem(Kernel kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename T, int D, int TM>
+cudaError_t forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
+    const int tiles = (p.rows + 16 * TM - 1) / (16 * TM);
+    constexpr size_t smem = forward_smem<D, TM>();
+    const cudaError_t e = set_smem(cross_simt_forward_kernel<T, D, TM>, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(cross_simt_forward_kernel<T, D, TM>, dim3(tiles * p.B * p.kv, w.parts), dim3(kThreads), smem, stream, p, w, tiles);
+}
+
+template <typename T, int D, int TM, bool KEYS>
+cudaError_t backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
+    const int tiles = ((KEYS ? p.s : p.rows) + 16 * TM - 1) / (16 * TM);
+    constexpr size_t smem = backward_smem<D, TM>();
+    const cudaError_t e = set_smem(cross_simt_backward_kernel<T, D, TM, KEYS>, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(cross_simt_backward_kernel<T, D, TM, KEYS>, dim3(tiles * p.B * p.kv), dim3(kThreads), smem, stream, p, delta, tiles);
+}
+
+template <typename T, int D>
+cudaError_t backward_d(const CrossProblem &p, const float *delta, cudaStream_t stream) {
+    const int tq = tile_m(p, p.rows), tk = tile_m(p, p.s);
+    cudaError_t e = cudaSuccess;
+    if (p.rows > 0)
+        e = tq == 4   ? backward<T, D, 4, false>(p, delta, stream)
+            : tq == 2 ? backward<T, D, 2, false>(p, delta, stream)
+                      : backward<T, D, 1, false>(p, delta, stream);
+    if (e != cudaSuccess || p.s == 0) return e;
+    return tk == 4   ? backward<T, D, 4, true>(p, delta, stream)
+           : tk == 2 ? backward<T, D, 2, true>(p, delta, stream)
+                     : backward<T, D, 1, true>(p, delta, stream);
+}
+
+}  // namespace
+
+// Parts of the key axis: none while the row tiles alone fill the SMs; else so many that two CTAs
+// of them do, with two key tiles a part at least.
+int cross_simt_parts(const CrossProblem &p) {
+    const int tm = tile_m(p, p.rows);
+    const long long ctas = (long long)p.B * p.kv * ((p.rows + 16 * tm - 1) / (16 * tm));
+    const long long want = 2 * kPlanSMs / std::max(1LL, ctas), most = (p.s + 2 * kBN - 1) / (2 * kBN);
+    return (int)std::max(1LL, std::min(want, most));
+}
+
+cudaError_t launch_cross_simt_forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
+    const int tm = tile_m(p, p.rows);
+    auto go = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        auto run = [&](auto t) {
+            using T = decltype(t);
+            return tm == 4 ? forward<T, D, 4>(p, w, stream) : tm == 2 ? forward<T, D, 2>(p, w, stream) : forward<T, D, 1>(p, w, stream);
+        };
+        return p.f32 ? run(float{}) : run(__nv_bfloat16{});
+    };
+    switch (p.d) {
+    case 16: return go(std::integral_constant<int, 16>{});
+    case 32: return go(std::integral_constant<int, 32>{});
+    case 64: return go(std::integral_constant<int, 64>{});
+    default: return go(std::integral_constant<int, 128>{});
+    }
+}
+
+cudaError_t launch_cross_simt_backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
+    switch (p.d) {
+    case 16: return p.f32 ? backward_d<float, 16>(p, delta, stream) : backward_d<__nv_bfloat16, 16>(p, delta, stream);
+    case 32: return p.f32 ? backward_d<float, 32>(p, delta, stream) : backward_d<__nv_bfloat16, 32>(p, delta, stream);
+    case 64: return p.f32 ? backward_d<float, 64>(p, delta, stream) : backward_d<__nv_bfloat16, 64>(p, delta, stream);
+    default: return p.f32 ? backward_d<float, 128>(p, delta, stream) : backward_d<__nv_bfloat16, 128>(p, delta, stream);
+    }
+}
+
+}  // namespace anchor

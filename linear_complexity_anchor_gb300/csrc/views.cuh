@@ -1,0 +1,37 @@
+// Strided [B][heads][n][d] views of the C ABI: their checks on the host, and the stream-ordered
+// workspaces of the calls that take them.
+#pragma once
+
+#include "common.cuh"
+
+namespace anchor {
+
+// a view with its sizes
+struct View {
+    const char *ptr = nullptr;
+    long long sb = 0, sh = 0, sn = 0;  // strides in elements
+    long long B = 0, H = 0, N = 0;
+    int d = 0, es = 0;
+
+    long long extent() const { return ((B - 1) * sb + (H - 1) * sh + (N - 1) * sn + d) * es; }  // bytes, first to last
+    bool same(const View &o) const {
+        return ptr == o.ptr && B == o.B && H == o.H && N == o.N && d == o.d && es == o.es && (B < 2 || sb == o.sb) &&
+               (H < 2 || sh == o.sh) && (N < 2 || sn == o.sn);
+    }
+};
+
+View make_view(const anchor_attn_view_t &v, int B, int heads, int n, int d, int es);
+// pointer and strides as the ABI asks; `writes`: no two rows share an element
+anchor_attn_status_t check_view(const View &v, bool writes);
+bool views_overlap(const View &a, const View &b);
+inline bool bytes_overlap(const void *a, size_t an, const void *b, size_t bn) {
+    return (uintptr_t)a < (uintptr_t)b + bn && (uintptr_t)b < (uintptr_t)a + an;
+}
+
+// Stream-ordered device memory from a pool of this library, one per device, that keeps up to
+// kPoolKeep bytes between calls: the device's default pool gives its memory back at every
+// synchronisation, and a call after one would map it again (measured at 0.1 to 0.6 ms).
+constexpr unsigned long long kPoolKeep = 512ull << 20;
+cudaError_t workspace_alloc(void **ptr, size_t bytes, cudaStream_t stream);
+
+}  // namespace anchor

@@ -1,0 +1,291 @@
+"""GPU: cross attention, forward and backward, against its definition in 64 bits, with bounds that count the kernels'
+roundings (tests/ops_reference.py); layouts, lengths, streams, captured graphs and what the results may not depend on."""
+import math
+
+import pytest
+import torch
+
+from tests.conftest import gpu_available
+from tests.ops_reference import assert_within, cross_reference
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a CUDA GPU")]
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def aa():
+    import linear_complexity_anchor_gb300 as pkg
+    pkg.load()
+    yield pkg
+    assert pkg.device_error() == 0
+
+
+def make(seed, B, heads, kv, n, s, d, dtype, tokens=False, gain=1.5):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def one(h, rows, by=1.0):
+        shape = (B, rows, h, d) if tokens else (B, h, rows, d)
+        x = (by * torch.randn(shape, generator=g, device="cuda")).to(DT[dtype])
+        return x.transpose(1, 2) if tokens else x
+
+    return one(heads, n, gain), one(kv, s), one(kv, s), one(heads, n)
+
+
+def lengths_of(kind, B, s):
+    """none; the whole range with empty and full entries in turn; or a number for all."""
+    if kind is None:
+        return None
+    if kind == "mixed":
+        some = [0, s, 1, s // 2, max(0, s - 1), min(s, 64), min(s, 65), min(s, 128), min(s, 129)]
+        return torch.tensor([some[i % len(some)] for i in range(B)], dtype=torch.int32, device="cuda")
+    return torch.full((B,), kind, dtype=torch.int32, device="cuda")
+
+
+def check(aa, seed, B, heads, kv, n, s, d, dtype, lengths=None, tokens=False, train=True, scale=None):
+    Q, K, V, dH = make(seed, B, heads, kv, n, s, d, dtype, tokens)
+    L = lengths_of(lengths, B, s)
+    c = d ** -0.5 if scale is None else scale
+    H, lse = aa.cross_forward(Q, K, V, L, scale=scale, return_lse=True)
+    ref = cross_reference(Q, K, V, L, c, dH if train else None)
+    what = f"{dtype} B{B} heads{heads}/{kv} n{n} s{s} d{d} {lengths}"
+    assert_within(H, ref["H"], "H " + what)
+    assert_within(lse, ref["lse"], "lse " + what)
+    if train:
+        for name, got in zip(("dQ", "dK", "dV"), aa.cross_backward(Q, K, V, H, lse, dH, L, scale=scale)):
+            assert_within(got, ref[name], name + " " + what)
+    return Q, K, V, dH, L, H, lse
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("shape", [(2, 2, 2, 1, 1), (1, 1, 1, 3, 2), (2, 3, 1, 17, 63), (9, 2, 2, 65, 200), (1, 4, 2, 130, 129),
+                                   (2, 2, 1, 300, 515)])
+def test_shapes(aa, dtype, d, shape):
+    check(aa, sum(shape) + d, *shape, d, dtype, lengths="mixed" if shape[0] > 1 else None)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape,lengths", [((9, 4, 2, 1, 700, 64), "mixed"), ((1, 12, 12, 1, 1500, 64), None), ((1, 1, 1, 1, 9000, 128), None),
+                                           ((3, 8, 1, 1, 2050, 128), "mixed"), ((2, 8, 2, 5, 1300, 32), "mixed"), ((1, 32, 1, 4, 640, 128), None),
+                                           ((2, 64, 2, 1, 333, 16), "mixed"), ((4, 2, 2, 2, 5000, 64), 0)])
+def test_few_queries(aa, dtype, shape, lengths):
+    check(aa, 7, *shape, dtype, lengths=lengths, train=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_tiles(aa, dtype):
+    """More row tiles and key tiles than any stage or part, with heads that share keys."""
+    check(aa, 3, 2, 4, 2, 1030, 1100, 64, dtype, lengths="mixed")
+    check(aa, 4, 1, 2, 1, 700, 1290, 128, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.5])
+def test_scales(aa, dtype, scale):
+    check(aa, 5, 2, 2, 2, 70, 150, 64, dtype, lengths="mixed", scale=scale)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_growing_scores(aa, dtype):
+    """Keys whose scores grow tile by tile: the running maximum moves at every tile."""
+    B, heads, n, s, d = 1, 2, 200, 900, 64
+    Q, K, V, dH = make(11, B, heads, heads, n, s, d, dtype)
+    K = (K.float() + Q.float().mean(2, keepdim=True).sign() * (torch.arange(s, device="cuda")[None, None, :, None] / s * 3)).to(K.dtype)
+    Q = (Q.float() * 0.5 + Q.float().mean(2, keepdim=True).sign()).to(Q.dtype)
+    H, lse = aa.cross_forward(Q, K, V, return_lse=True)
+    ref = cross_reference(Q, K, V, None, d ** -0.5, dH)
+    assert_within(H, ref["H"], "H")
+    assert_within(lse, ref["lse"], "lse")
+    for name, got in zip(("dQ", "dK", "dV"), aa.cross_backward(Q, K, V, H, lse, dH)):
+        assert_within(got, ref[name], name)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [32, 128])
+def test_strides(aa, dtype, d):
+    """Token-major projections, and parts of one buffer; results in the same order of axes, or dense."""
+    check(aa, 8, 3, 4, 2, 100, 140, d, dtype, lengths="mixed", tokens=True)
+    B, heads, n, s = 2, 3, 90, 150
+    g = torch.Generator(device="cuda").manual_seed(1)
+    both = torch.randn((B, s, 2, heads, d), generator=g, device="cuda").to(DT[dtype])
+    K, V = both[:, :, 0].transpose(1, 2), both[:, :, 1].transpose(1, 2)
+    Q = torch.randn((B, n, heads, 2 * d), generator=g, device="cuda").to(DT[dtype])[..., :d].transpose(1, 2)
+    dH = torch.randn((B, heads, n, d), generator=g, device="cuda").to(DT[dtype])
+    H, lse = aa.cross_forward(Q, K, V, return_lse=True)
+    ref = cross_reference(Q, K, V, None, d ** -0.5, dH)
+    assert_within(H, ref["H"], "H")
+    for name, got in zip(("dQ", "dK", "dV"), aa.cross_backward(Q, K, V, H, lse, dH)):
+        assert_within(got, ref[name], name)
+    out = torch.full((B, n, heads, d), 7.0, device="cuda", dtype=DT[dtype])
+    assert aa.cross_forward(Q, K, V, H=out.transpose(1, 2)).data_ptr() == out.data_ptr()
+    assert torch.equal(out.transpose(1, 2), H)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_states_shared_by_the_batch(aa, dtype):
+    """K and V expanded over the batch (and over heads): gradients for each entry, their sum the shared one's."""
+    B, heads, n, s, d = 3, 4, 150, 200, 64
+    Q, _, _, dH = make(2, B, heads, heads, n, s, d, dtype)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn((1, 1, s, d), generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    K, V = k.expand(B, heads, s, d), v.expand(B, heads, s, d)
+    L = lengths_of("mixed", B, s)
+    H, lse = aa.cross_forward(Q, K, V, L, return_lse=True)
+    ref = cross_reference(Q, K, V, L, d ** -0.5, dH)
+    assert_within(H, ref["H"], "H")
+    for name, got in zip(("dQ", "dK", "dV"), aa.cross_backward(Q, K, V, H, lse, dH, L)):
+        assert got.shape == ref[name][0].shape
+        assert_within(got, ref[name], name)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 200])
+def test_masked_states_are_not_used(aa, dtype, n):
+    """Infinities and NaN behind an entry's length leave no trace; lengths out of [0, s] are taken into it."""
+    B, heads, s, d = 6, 2, 300, 64
+    Q, K, V, dH = make(6, B, heads, heads, n, s, d, dtype)
+    L = torch.tensor([0, 1, 100, 128, 255, 300], dtype=torch.int32, device="cuda")
+    H, lse = aa.cross_forward(Q, K, V, L, return_lse=True)
+    grads = aa.cross_backward(Q, K, V, H, lse, dH, L)
+    K2, V2 = K.clone(), V.clone()
+    for b, length in enumerate(L.tolist()):
+        K2[b, :, length:] = torch.tensor([math.inf, -math.inf, math.nan, torch.finfo(K.dtype).min], device="cuda").to(K.dtype).repeat(d // 4)
+        V2[b, :, length:] = math.nan
+    H2, lse2 = aa.cross_forward(Q, K2, V2, L, return_lse=True)
+    assert torch.equal(H, H2) and torch.equal(lse, lse2)
+    for a, b in zip(grads, aa.cross_backward(Q, K2, V2, H2, lse2, dH, L)):
+        assert torch.equal(a, b)
+    assert bool((H[0] == 0).all()) and bool((lse[0] == -math.inf).all()) and bool((grads[0][0] == 0).all())
+    for b, length in enumerate(L.tolist()):
+        assert bool((grads[1][b, :, length:] == 0).all()) and bool((grads[2][b, :, length:] == 0).all())
+    wild = torch.tensor([-5, 1, 100, 128, 255, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    assert torch.equal(H, aa.cross_forward(Q, K, V, wild))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_bad_query_stays_in_its_row(aa, dtype):
+    """NaN and infinities in one query row change no other row."""
+    Q, K, V, _ = make(9, 2, 2, 1, 150, 200, 64, dtype)
+    H = aa.cross_forward(Q, K, V)
+    Q2 = Q.clone()
+    Q2[0, 1, 77] = math.nan
+    Q2[1, 0, 0] = math.inf
+    H2 = aa.cross_forward(Q2, K, V)
+    keep = torch.ones(H.shape[:3], dtype=torch.bool, device="cuda")
+    keep[0, 1, 77] = keep[1, 0, 0] = False
+    assert torch.equal(H[keep], H2[keep])
+    assert bool(H2[0, 1, 77].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_nothing_to_do(aa, dtype):
+    for B, heads, kv, n, s in ((0, 2, 2, 5, 5), (2, 2, 1, 0, 5), (2, 2, 1, 5, 0), (2, 2, 1, 0, 0)):
+        Q, K, V, dH = make(1, B, heads, kv, n, s, 64, dtype)
+        H, lse = aa.cross_forward(Q, K, V, return_lse=True)
+        dQ, dK, dV = aa.cross_backward(Q, K, V, H, lse, dH)
+        for t in (H, dQ, dK, dV):
+            assert bool((t == 0).all())
+        assert bool((lse == -math.inf).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_same_bits_again(aa, dtype):
+    """From run to run, with other calls in between, and without lse."""
+    for shape in ((2, 4, 2, 300, 700, 64), (3, 8, 2, 1, 3000, 128)):
+        Q, K, V, dH = make(12, *shape, dtype)
+        L = lengths_of("mixed", shape[0], shape[4])
+        H, lse = aa.cross_forward(Q, K, V, L, return_lse=True)
+        grads = aa.cross_backward(Q, K, V, H, lse, dH, L)
+        other = make(13, 1, 2, 2, 333, 444, 64, dtype)
+        for _ in range(5):
+            aa.cross_forward(*other[:3])
+            H2, lse2 = aa.cross_forward(Q, K, V, L, return_lse=True)
+            assert torch.equal(H, H2) and torch.equal(lse, lse2) and torch.equal(H, aa.cross_forward(Q, K, V, L))
+            for a, b in zip(grads, aa.cross_backward(Q, K, V, H, lse, dH, L)):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_streams_and_graphs(aa, dtype):
+    """Two calls at once on streams of their own, and two captured graphs replayed at once, give the eager bits."""
+    one = make(14, 2, 4, 2, 260, 600, 64, dtype)
+    two = make(15, 4, 8, 2, 1, 2500, 64, dtype)
+
+    def step(x, stream=None):
+        Q, K, V, dH = x
+        H, lse = aa.cross_forward(Q, K, V, return_lse=True, stream=stream)
+        return [H, lse, *aa.cross_backward(Q, K, V, H, lse, dH, stream=stream)]
+
+    want = [step(one), step(two)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        got = [step(x, st) for x, st in zip((one, two), streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(u, v) for u, v in zip(a, b))
+    graphs = []
+    for x, st in zip((one, two), streams):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            out = step(x)
+        graphs.append((graph, out))
+    for _ in range(3):
+        for (graph, out), st in zip(graphs, streams):
+            for t in out:
+                t.fill_(5)
+        torch.cuda.synchronize()
+        for (graph, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+        torch.cuda.synchronize()
+        for (_, out), a in zip(graphs, want):
+            assert all(torch.equal(u, v) for u, v in zip(a, out))
+
+
+def test_gradient_against_differences(aa):
+    """fp32: the loss sum(H o dH) moved along a random direction, against the gradients' inner product with it."""
+    Q, K, V, dH = make(21, 2, 4, 2, 9, 33, 32, "f32")
+    L = torch.tensor([33, 20], dtype=torch.int32, device="cuda")
+    H, lse = aa.cross_forward(Q, K, V, L, return_lse=True)
+    grads = aa.cross_backward(Q, K, V, H, lse, dH, L)
+    g = torch.Generator(device="cuda").manual_seed(22)
+    for i, grad in enumerate(grads):
+        step = torch.randn(grad.shape, generator=g, device="cuda")
+        loss = []
+        for e in (-1, 1):
+            x = [Q, K, V]
+            x[i] = x[i] + e * 2.0 ** -7 * step
+            loss.append(float((aa.cross_forward(*x, L).double() * dH.double()).sum()))
+        got, want = (loss[1] - loss[0]) * 2.0 ** 6, float((grad.double() * step.double()).sum())
+        # the loss is off by about 300 elements' fp32 roundings (1e-6 each, random), times 2^6; the third derivative adds h^2
+        assert abs(got - want) <= 5e-3 * (1 + abs(want)), (i, got, want)
+
+
+def test_refusals(aa):
+    Q, K, V, dH = make(1, 2, 4, 2, 8, 9, 64, "f32")
+    H, lse = aa.cross_forward(Q, K, V, return_lse=True)
+    for bad in ((Q.double(), K, V), (Q, K.bfloat16(), V), (Q, K[:1], V), (Q, K, V[:, :, :5]), (Q[..., :32], K, V), (Q.cpu(), K, V),
+                (Q, K.transpose(-1, -2).contiguous().transpose(-1, -2), V), (Q[0], K, V)):
+        with pytest.raises((TypeError, ValueError)):
+            aa.cross_forward(*bad)
+    with pytest.raises(aa.AnchorAttnError):  # heads not a multiple of kv_heads
+        aa.cross_forward(Q[:, :3], K, V)
+    with pytest.raises(aa.AnchorAttnError):  # d
+        aa.cross_forward(Q[..., :48].contiguous(), K[..., :48].contiguous(), V[..., :48].contiguous())
+    with pytest.raises(aa.AnchorAttnError):
+        aa.cross_forward(Q, K, V, scale=math.nan)
+    with pytest.raises(aa.AnchorAttnError):  # H is Q
+        aa.cross_forward(Q, K, V, H=Q)
+    for bad in (torch.zeros(2, device="cuda"), torch.zeros(2, dtype=torch.int64, device="cuda"), torch.zeros(2, dtype=torch.int32)):
+        with pytest.raises((TypeError, ValueError)):
+            aa.cross_forward(Q, K, V, bad)
+    with pytest.raises(ValueError):
+        aa.cross_forward(Q, K, V, torch.zeros(3, dtype=torch.int32, device="cuda"))
+    for bad in ((H[:, :2], lse, dH), (H, lse.double(), dH), (H, lse[:, :, :4], dH), (H, lse, dH.bfloat16())):
+        with pytest.raises((TypeError, ValueError)):
+            aa.cross_backward(Q, K, V, *bad)
+    odd = torch.zeros(2 * 4 * 8 * 64 + 1, device="cuda")[1:].view(2, 4, 8, 64)  # not on 16 bytes
+    with pytest.raises(aa.AnchorAttnError):
+        aa.cross_forward(odd, K, V)
