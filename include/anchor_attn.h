@@ -327,7 +327,8 @@ ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_test_forward(const void *Q, con
 /*
  * Rows of heads: a [B][heads][n][d] tensor whose last axis is dense.  The three strides are in
  * elements, multiples of 16 bytes (the base pointer too), and not negative; the stride of an axis
- * of one entry is not looked at.  An input may repeat rows (a stride of 0); an output may not.
+ * of one entry is not looked at.  Rows do not overlap (a row stride of d at least); an input may share them
+ * between heads or batch entries (a stride of 0), an output may not.
  */
 typedef struct {
     void *ptr;

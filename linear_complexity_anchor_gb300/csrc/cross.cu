@@ -169,14 +169,14 @@ anchor_attn_status_t cross(const anchor_attn_cross_t *a, bool bwd, void *stream_
         return false;
     };
     if (!bwd) {
-        CrossParts w = {nullptr, nullptr, cross_simt_parts(p)};
+        CrossParts w = {nullptr, nullptr, p.f32 ? cross_simt_parts(p) : cross_tc_parts(p)};
         if (w.parts > 1) {
             const size_t total = (size_t)p.B * p.kv * p.rows * w.parts;
             if (!take(total * (p.d * 4 + 8))) return ANCHOR_ATTN_ERR_ALLOC;
             w.o = (float *)ws;
             w.ml = (float2 *)(w.o + total * p.d);
         }
-        e = launch_cross_simt_forward(p, w, stream);
+        e = p.f32 ? launch_cross_simt_forward(p, w, stream) : launch_cross_tc_forward(p, w, stream);
         if (e == cudaSuccess && w.parts > 1) e = launch_cross_join(p, w, stream);
     } else {
         float *delta = nullptr;

@@ -52,4 +52,9 @@ int cross_simt_parts(const CrossProblem &p);
 cudaError_t launch_cross_simt_forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream);
 cudaError_t launch_cross_simt_backward(const CrossProblem &p, const float *delta, cudaStream_t stream);
 
+// tensor cores, bf16
+int cross_tc_parts(const CrossProblem &p);
+cudaError_t launch_cross_tc_forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream);
+cudaError_t cross_fwd_read_and_clear_error(unsigned *out);
+
 }  // namespace anchor

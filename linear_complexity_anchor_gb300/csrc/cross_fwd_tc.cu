@@ -1,0 +1,435 @@
+// Cross attention forward in bf16 on the tensor cores (formulas in include/anchor_attn.h).
+//
+// A CTA has one or two tiles of 128 query rows of one key head, and walks that head's keys in
+// tiles of 128: S = Q K^T into tensor memory, one thread per row takes the running maximum and
+// sum and leaves P = 2^(c s - m) as bf16 over S's columns, O += P V from there.  Q is loaded with
+// plain 16-byte loads (rows of several heads, any strides), K and V by TMA into a ring, K and V in
+// turn, by a warp of their own; one thread of another warp issues the products.
+//
+// Two tiles: while the rows of one take their exponentials the tensor cores run the other's
+//   P0 V -> O0, Q0 K' -> S0   |   P1 V -> O1, Q1 K' -> S1
+// and each K and V tile is read from L2 once for 256 rows.  S and O of both fill the 512 columns
+// at d = 128, so P lies over S: the products of one CTA run in the order they are issued, and the
+// next S is issued after the P V that reads it.
+// One tile (up to 128 rows, a token of serving above all): bound by reading K and V.  At d = 128
+// S has two buffers, the next S is issued before the softmax of this one, and six stages of 32 KB
+// are in flight; at d = 64 two CTAs share an SM.
+// Few rows and long keys: the key tiles of an entry (of its own length) are cut over gridDim.y
+// CTAs, which leave sums that a second launch joins.
+//
+// The maximum a row is scaled by moves only when it grows by more than 2^8 over the one in use:
+// P stays below 2^8, its relative rounding is the same, and O (in tensor memory) is rescaled
+// rarely.  P is rounded to bf16 (the operand type of the product; its relative error of 2^-9 is that
+// of rounding V); the row sum is taken over the fp32 values.
+// Keys from the entry's length on: S masked by select, so that nothing they hold matters, and
+// their rows of V are zeroed in shared memory (0 times an infinity is not 0).
+#include "cross_tc.cuh"
+
+#include <math.h>
+
+namespace anchor {
+
+__device__ unsigned int g_cross_fwd_error;  // bit 0: a wait gave up
+
+namespace {
+
+using namespace cross_tc;
+
+constexpr float kSlack = 8.f;  // log2 of how far a maximum may be passed before O is rescaled
+
+template <int D, int NQ>
+struct Geo {
+    static constexpr int kStages = D == 128 ? (NQ == 2 ? 5 : 6) : (NQ == 2 ? 8 : 5);
+    static constexpr int kNS = NQ == 1 && D == 128 ? 2 : 1;  // S buffers of a tile
+    static constexpr int kPerSM = NQ == 1 && D == 64 ? 2 : 1;
+    static constexpr int kThreads = 128 * NQ + 64;
+    static constexpr int kQ = 0, kRing = NQ * kTile<D>, kBars = kRing + kStages * kTile<D>;
+    static constexpr int kNBars = NQ + 2 * kStages + 2 * NQ * kNS + NQ + 1;
+    static constexpr int kSmem = kBars + kNBars * 8 + 16 + 1024;
+    static constexpr uint32_t kColO = 128 * NQ * kNS, kCols = kColO + NQ * D <= 256 ? 256 : 512;
+    static_assert(kSmem * kPerSM + kPerSM * 1024 <= 228 * 1024, "shared memory");
+    static_assert(kColO + NQ * D <= 512 && kCols * kPerSM <= 512, "tensor memory");
+};
+
+struct FwdParams {
+    CrossProblem p;
+    CrossParts w;
+    TileMap k, v;
+    int tiles;
+};
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(Geo<D, NQ>::kThreads, Geo<D, NQ>::kPerSM)
+cross_fwd_kernel(const __grid_constant__ FwdParams a) {
+    using G = Geo<D, NQ>;
+    constexpr int NS = G::kNS, ST = G::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G::kBars);
+    uint64_t *q_full = bars, *full = q_full + NQ, *empty = full + ST, *s_full = empty + ST, *p_full = s_full + NQ * NS,
+             *o_full = p_full + NQ * NS, *done = o_full + NQ;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + G::kNBars);
+    const CrossProblem &p = a.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kLoad = 4 * NQ, kIssue = 4 * NQ + 1;
+    const int tile = (int)(blockIdx.x % a.tiles), bk = (int)(blockIdx.x / a.tiles);
+    const int b = bk / p.kv, kh = bk - b * p.kv, r0 = tile * NQ * kRows;
+    const int left = p.rows - r0;                        // rows of this CTA that exist
+    const int nq = NQ == 2 && left > kRows ? 2 : 1;
+
+    if (threadIdx.x == 0) {
+        for (int q = 0; q < NQ; ++q) {
+            const int warps = min(max((left - q * kRows + 31) / 32, 1), 4);  // with a row that exists
+            mbar_init(q_full + q, 4);
+            mbar_init(o_full + q, 1);
+            for (int s = 0; s < NS; ++s) {
+                mbar_init(s_full + q * NS + s, 1);
+                mbar_init(p_full + q * NS + s, warps);
+            }
+        }
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        mbar_init(done, 1);
+        fence_mbar_init();
+    }
+    if (warp == kIssue) tmem_alloc(s_tmem, G::kCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    grid_dependency_wait();
+    grid_dependents_launch();
+
+    const int L = cross_length(p, b), key_tiles = (L + kRows - 1) / kRows;
+    const int t0 = (int)((long long)key_tiles * blockIdx.y / a.w.parts);
+    const int nt = (int)((long long)key_tiles * (blockIdx.y + 1) / a.w.parts) - t0;
+    unsigned int *error = &g_cross_fwd_error;
+
+    if (warp == kLoad) {
+        if (lane == 0 && nt > 0) {
+            tma_prefetch_desc(&a.k.map);
+            tma_prefetch_desc(&a.v.map);
+            int i = 0;
+            for (; i < 2 * nt; ++i) {
+                const int st = i % ST;
+                if (i >= ST && !bwait(empty + st, (uint32_t)((i / ST - 1) & 1), error)) break;
+                load_tile<D>(sm + G::kRing + st * kTile<D>, i & 1 ? a.v : a.k, full + st, (t0 + i / 2) * kRows, kh, b);
+            }
+            // the CTA leaves only once its copies have landed
+            for (int j = max(0, i - ST); j < i; ++j) bwait(full + j % ST, (uint32_t)((j / ST) & 1), error);
+        }
+        __syncwarp();
+    } else if (warp == kIssue) {
+        if (lane == 0 && nt > 0) {
+            const int ksteps = (p.d + 15) / 16;
+            const uint32_t base = smem_u32(sm), ring = base + G::kRing;
+            const uint32_t idO = idesc_bf16_f32(kRows, p.d < D ? p.d : D, false, true);
+            auto cols = [&](int j) { return min(kRows, (L - (t0 + j) * kRows + 15) / 16 * 16); };  // keys of tile j, in 16s
+            auto scores = [&](int q, int j) {  // S of tile j (its K has landed)
+                const uint32_t idS = idesc_bf16_f32(kRows, cols(j), false, false);
+                const uint64_t qd = desc_k(base + G::kQ + q * kTile<D>), kd = desc_k(ring + (2 * j % ST) * kTile<D>);
+                const uint32_t to = tmem + 128 * (q * NS + j % NS);
+                for (int k = 0; k < ksteps; ++k) umma_bf16(to, qd + step_k(k), kd + step_k(k), idS, k > 0 ? 1u : 0u);
+                umma_commit(s_full + q * NS + j % NS);
+            };
+            auto landed = [&](int i) { return bwait(full + i % ST, (uint32_t)((i / ST) & 1), error); };
+            bool ok = landed(0);
+            for (int q = 0; q < nq && ok; ++q) {
+                ok = bwait(q_full + q, 0u, error);
+                tc_fence_after();
+                if (ok) scores(q, 0);
+            }
+            if (ok) umma_commit(empty + 0);
+            if (NS == 2 && ok && nt > 1) {  // S of tile 1 while the rows are at tile 0
+                ok = landed(2);
+                tc_fence_after();
+                if (ok) {
+                    scores(0, 1);
+                    umma_commit(empty + 2 % ST);
+                }
+            }
+            for (int j = 0; j < nt && ok; ++j) {
+                const int v = 2 * j + 1, ahead = j + NS;  // the S issued after this tile's P V
+                for (int q = 0; q < nq && ok; ++q) {
+                    ok = bwait(p_full + q * NS + j % NS, (uint32_t)((j / NS) & 1), error) && (q > 0 || landed(v));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t vd = desc_mn(ring + (v % ST) * kTile<D>);
+                    const uint32_t P = tmem + 128 * (q * NS + j % NS), O = tmem + G::kColO + q * D;
+                    const int steps = cols(j) / 16;
+                    for (int k = 0; k < steps; ++k)
+                        umma_bf16_tmem_a(O, P + 8 * k, vd + step_mn(k), idO, (j > 0 || k > 0) ? 1u : 0u);
+                    umma_commit(o_full + q);
+                    if (q == nq - 1) umma_commit(empty + v % ST);
+                    if (ahead < nt) {
+                        if (q == 0) ok = landed(2 * ahead);
+                        tc_fence_after();
+                        if (!ok) break;
+                        scores(q, ahead);
+                        if (q == nq - 1) umma_commit(empty + 2 * ahead % ST);
+                    }
+                }
+            }
+            umma_commit(done);
+            bwait(done, 0u, error);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------ rows
+        const int q = warp >> 2, w4 = warp & 3;
+        const int row = w4 * 32 + lane;                      // of the tile
+        const int r = r0 + q * kRows + row;                  // of the key head
+        const bool mine = r < p.rows;
+        const bool active = r0 + q * kRows + w4 * 32 < p.rows;  // the warp has a row
+        uint8_t *sQ = sm + G::kQ + q * kTile<D>;
+        // (not 0, so that a masked score stays -infinity; a scale of 0 leaves no trace of any finite one)
+        const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);
+        constexpr int kLanes = D / 8;  // lanes of a row, 16 bytes each
+        if (nt > 0) {
+            // this warp's 32 rows of Q, negated for a negative scale
+            const long long at = mine ? cross_row(p, p.Q, b, kh, r) : -1;
+            const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+            for (int i = 0; i < kLanes; ++i) {
+                const int rr = i * (32 / kLanes) + lane / kLanes, ch = lane % kLanes;
+                const long long o = __shfl_sync(0xffffffffu, at, rr);
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (o >= 0 && ch * 8 < p.d) {
+                    x = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.Q.ptr + o + ch * 8);
+                    x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
+                }
+                *reinterpret_cast<uint4 *>(sQ + chunk_at(w4 * 32 + rr, ch)) = x;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full + q);
+        }
+        const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
+        const uint32_t tO = tmem + lanes + G::kColO + q * D;
+        float m = -INFINITY, l = 0.f;  // maximum in use (of c s) and sum
+        bool ok = true;
+        if (active && q < nq) {
+            for (int j = 0; j < nt && ok; ++j) {
+                const int buf = q * NS + j % NS;
+                const uint32_t tS = tmem + lanes + 128 * buf;
+                if (!bwait(s_full + buf, (uint32_t)((j / NS) & 1), error)) { ok = false; break; }
+                tc_fence_after();
+                const int keys = min(kRows, L - (t0 + j) * kRows);  // that count
+                const int ld = (keys + 31) / 32;                    // 32-column parts with one of them
+                float s[128];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (x < ld) tmem_ld32(tS + 32 * x, s + 32 * x);
+                tmem_ld_wait();
+                if (keys < kRows) {
+#pragma unroll
+                    for (int x = 0; x < 128; ++x)
+                        if (x >= keys) s[x] = -INFINITY;
+                }
+                float t8[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) t8[x] = max3_f32(s[x], s[8 + x], s[16 + x]);
+#pragma unroll
+                for (int y = 24; y < 120; y += 16)
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) t8[x] = max3_f32(t8[x], s[y + x], s[y + 8 + x]);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) t8[x] = fmaxf(t8[x], s[120 + x]);
+                const float top =
+                    c * fmaxf(max3_f32(t8[0], t8[1], t8[2]), max3_f32(t8[3], t8[4], max3_f32(t8[5], t8[6], t8[7])));
+                if (j == 0) {
+                    m = top;
+                } else {
+                    const bool grows = top > m + kSlack;
+                    if (__any_sync(0xffffffffu, grows)) {
+                        // O (complete up to the tile before) to the new maximum
+                        if (!bwait(o_full + q, (uint32_t)((j - 1) & 1), error)) { ok = false; break; }
+                        tc_fence_after();
+                        const float f = grows ? ex2(m - top) : 1.f;
+                        if (grows) m = top;
+                        l *= f;
+                        float o[32];
+#pragma unroll 1
+                        for (int x = 0; x < D; x += 32) {
+                            tmem_ld32(tO + x, o);
+                            tmem_ld_wait();
+                            uint32_t u[32];
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) u[y] = __float_as_uint(o[y] * f);
+                            tmem_st32(tO + x, u);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                const float shift = m == -INFINITY ? 0.f : m;
+                const uint64_t c2 = f32x2(c, c), m2 = f32x2(-shift, -shift);
+                uint64_t z[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if (x >= ld) break;
+                    uint32_t u[16];
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) {
+                        float e0, e1;
+                        f32x2_split(fma_f32x2(f32x2(s[32 * x + 2 * y], s[32 * x + 2 * y + 1]), c2, m2), e0, e1);
+                        e0 = ex2(e0), e1 = ex2(e1);
+                        z[y & 3] = add_f32x2(z[y & 3], f32x2(e0, e1));
+                        u[y] = pack2(e0, e1);
+                    }
+                    tmem_st16(tS + 16 * x, u);
+                }
+                tmem_st_wait();
+                float za, zb;
+                f32x2_split(add_f32x2(add_f32x2(z[0], z[1]), add_f32x2(z[2], z[3])), za, zb);
+                l += za + zb;
+                if (keys < kRows && L < p.s && q == 0) {
+                    // the last tile's rows of V that do not count, once (the other tile's product comes later)
+                    const int i = 2 * j + 1, st = i % ST;
+                    if (!bwait(full + st, (uint32_t)((i / ST) & 1), error)) { ok = false; break; }
+                    const int warps = min((left + 31) / 32, 4);
+                    for (int t = row; t < kRows; t += 32 * warps) zero_rows<D>(sm + G::kRing + st * kTile<D>, t, keys, (keys + 15) / 16 * 16);
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + buf);
+            }
+            if (ok && nt > 0) ok = bwait(o_full + q, (uint32_t)((nt - 1) & 1), error);
+            tc_fence_after();
+        }
+        if (active && q < nq && ok) {
+            const long long f = cross_flat(p, b, kh, mine ? r : 0);
+            if (a.w.parts > 1) {
+                const long long at = (long long)blockIdx.y * p.B * p.kv * p.rows + f;
+                if (mine) a.w.ml[at] = make_float2(nt > 0 ? m : -INFINITY, l);
+                float o[32];
+#pragma unroll 1
+                for (int x = 0; x < p.d; x += 32) {
+                    if (nt > 0) {
+                        tmem_ld32(tO + x, o);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = 0.f;
+                    }
+                    if (!mine) continue;
+                    float4 *dst = reinterpret_cast<float4 *>(a.w.o + at * p.d + x);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        if (x + 4 * y < p.d) dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                }
+            } else {
+                // rows of H through this warp's rows of the Q tile (all scores have been taken)
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                float o[32];
+#pragma unroll 1
+                for (int x = 0; x < p.d; x += 32) {
+                    if (nt > 0) {
+                        tmem_ld32(tO + x, o);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = 0.f;
+                    }
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float *e = o + 8 * y;
+                        *reinterpret_cast<uint4 *>(sQ + chunk_at(row, x / 8 + y)) =
+                            make_uint4(pack2(e[0] * inv, e[1] * inv), pack2(e[2] * inv, e[3] * inv),
+                                       pack2(e[4] * inv, e[5] * inv), pack2(e[6] * inv, e[7] * inv));
+                    }
+                }
+                __syncwarp();
+                const long long at = mine ? cross_row(p, p.H, b, kh, r) : -1;
+#pragma unroll
+                for (int i = 0; i < kLanes; ++i) {
+                    const int rr = i * (32 / kLanes) + lane / kLanes, ch = lane % kLanes;
+                    const long long to = __shfl_sync(0xffffffffu, at, rr);
+                    if (to >= 0 && ch * 8 < p.d)
+                        *reinterpret_cast<uint4 *>((__nv_bfloat16 *)p.H.ptr + to + ch * 8) =
+                            *reinterpret_cast<const uint4 *>(sQ + chunk_at(w4 * 32 + rr, ch));
+                }
+                if (p.lse && mine) p.lse[f] = l == 0.f ? -INFINITY : m * (1.f / kLog2e) + logf(l);
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+    }
+    __syncthreads();
+    if (warp == kIssue) {
+        tc_fence_after();
+        tmem_dealloc(tmem, G::kCols);
+    }
+}
+
+// Two tiles a CTA where rows fill them; one for up to 128 rows.
+int tiles_per_cta(const CrossProblem &p) { return p.rows > kRows ? 2 : 1; }
+
+template <int D, int NQ>
+cudaError_t launch(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
+    using G = Geo<D, NQ>;
+    FwdParams a;
+    a.p = p;
+    a.w = w;
+    a.tiles = (p.rows + NQ * kRows - 1) / (NQ * kRows);
+    if (p.s > 0 && (!make_tile_map(&a.k, p.K, p.B, p.kv, p.s, p.d) || !make_tile_map(&a.v, p.V, p.B, p.kv, p.s, p.d)))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(cross_fwd_kernel<D, NQ>, dim3(a.tiles * p.B * p.kv, w.parts), dim3(G::kThreads), G::kSmem, stream, a);
+}
+
+}  // namespace
+
+namespace cross_tc {
+
+bool make_tile_map(TileMap *m, const CrossView &v, int B, int heads, int rows, int d) {
+    typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                               const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return (Encode)f;
+    }();
+    if (!encode) return false;
+    m->by_head = heads > 1 && v.sh > 0;
+    m->by_batch = B > 1 && v.sb > 0;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)rows, m->by_head ? (cuuint64_t)heads : 1, m->by_batch ? (cuuint64_t)B : 1};
+    // the stride of an axis of one entry is not used, but has to be one
+    const cuuint64_t strides[3] = {(cuuint64_t)(rows > 1 ? v.sn : d) * 2, (cuuint64_t)(m->by_head ? v.sh : d) * 2,
+                                   (cuuint64_t)(m->by_batch ? v.sb : d) * 2};
+    const cuuint32_t box[4] = {64, kRows, 1, 1}, one[4] = {1, 1, 1, 1};
+    return encode(&m->map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(v.ptr), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace cross_tc
+
+int cross_tc_parts(const CrossProblem &p) {
+    const int nq = tiles_per_cta(p), per_sm = nq == 1 && p.d <= 64 ? 2 : 1;
+    const long long ctas = (long long)p.B * p.kv * ((p.rows + nq * kRows - 1) / (nq * kRows));
+    const long long want = (long long)per_sm * kPlanSMs / std::max(1LL, ctas), most = (p.s + 2 * kRows - 1) / (2 * kRows);
+    return (int)std::max(1LL, std::min(want, most));
+}
+
+cudaError_t launch_cross_tc_forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
+    const int nq = tiles_per_cta(p);
+    if (p.d > 64) return nq == 2 ? launch<128, 2>(p, w, stream) : launch<128, 1>(p, w, stream);
+    return nq == 2 ? launch<64, 2>(p, w, stream) : launch<64, 1>(p, w, stream);
+}
+
+cudaError_t cross_fwd_read_and_clear_error(unsigned *out) {
+    unsigned zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_cross_fwd_error, sizeof(unsigned));
+    if (e != cudaSuccess) return e;
+    return cudaMemcpyToSymbol(g_cross_fwd_error, &zero, sizeof(unsigned));
+}
+
+}  // namespace anchor

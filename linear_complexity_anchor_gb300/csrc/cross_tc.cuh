@@ -1,0 +1,93 @@
+// What the tensor-core kernels of cross attention share: bounded waits, 4-D tile loads, tiles in
+// swizzled shared memory, descriptors.
+//
+// A tile is 128 rows of 64 or 128 bf16 columns, in blocks of 64 columns: [128 rows][128 bytes]
+// with the 128-byte swizzle (16-byte chunk c of row r at c ^ (r & 7)), as a TMA box lands.  One
+// copy serves as a K-major operand (contraction over the columns) and as an MN-major one
+// (contraction over the rows).  Heads of 16 and 32 columns are tiles of 64 whose other columns
+// are not read.
+#pragma once
+
+#include "cross.cuh"
+#include "ptx.cuh"
+
+namespace anchor {
+namespace cross_tc {
+
+using namespace ptx;
+
+constexpr int kRows = 128;
+constexpr int kBlock = kRows * 128;  // bytes of a 64-column block
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D> constexpr int kTile = kRows * D * 2;
+
+// A view as a tensor map (d, rows, heads, batch): an axis that does not move (a stride of 0, or
+// one entry) is an axis of one entry whose coordinate is multiplied by 0.
+struct TileMap {
+    CUtensorMap map;
+    int by_head, by_batch;
+};
+bool make_tile_map(TileMap *m, const CrossView &v, int B, int heads, int rows, int d);
+
+// bit 0 of the error word, and false, once a wait has lasted kWaitNs
+__device__ __forceinline__ bool bwait(uint64_t *bar, uint32_t parity, unsigned int *error) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait_sleep(bar, parity, 2000)) {
+        if (globaltimer_ns() - t0 > kWaitNs) {
+            atomicOr(error, 1u);
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+// rows [row, row + 128) of one head; rows and columns outside the tensor are zero
+template <int D>
+__device__ __forceinline__ void load_tile(uint8_t *dst, const TileMap &m, uint64_t *bar, int row, int head, int b) {
+    mbar_arrive_expect_tx(bar, kTile<D>);
+#pragma unroll
+    for (int q = 0; q < D / 64; ++q) tma_load_4d(dst + q * kBlock, &m.map, bar, 64 * q, row, head * m.by_head, b * m.by_batch);
+}
+
+// byte offset of 16-byte chunk c of row r
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return (uint32_t)((c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+// descriptors of a tile, and their advance for step k of 16 along the contraction
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile) { return smem_desc_sw128(tile, 16, 1024); }        // over columns
+__device__ __forceinline__ uint64_t desc_mn(uint32_t tile) { return smem_desc_sw128(tile, kBlock, 1024); }   // over rows
+__device__ __forceinline__ uint64_t step_k(int k) { return (uint64_t)(((k >> 2) * kBlock + (k & 3) * 32) >> 4); }
+__device__ __forceinline__ uint64_t step_mn(int k) { return (uint64_t)(k * 16 * 128 >> 4); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// zeros in rows [from, to) of a tile, one row per thread t of 128
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t *tile, int t, int from, int to) {
+    if (t < from || t >= to) return;
+#pragma unroll
+    for (int q = 0; q < D / 64; ++q)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(tile + q * kBlock + t * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
+}
+
+}  // namespace cross_tc
+}  // namespace anchor

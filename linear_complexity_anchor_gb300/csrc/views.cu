@@ -25,7 +25,7 @@ anchor_attn_status_t check_view(const View &v, bool writes) {
         if (strides[i] > 0 && sizes[i] - 1 > room / strides[i]) return ANCHOR_ATTN_ERR_INVALID_ARG;
         room -= (sizes[i] - 1) * strides[i];
     }
-    if (room < v.d) return ANCHOR_ATTN_ERR_INVALID_ARG;
+    if (room < v.d || (v.N > 1 && v.sn < v.d)) return ANCHOR_ATTN_ERR_INVALID_ARG;
     if (writes) {  // by growing stride, each axis steps over all that the ones before it span
         int order[3] = {0, 1, 2};
         std::sort(order, order + 3, [&](int a, int b) { return strides[a] < strides[b]; });
