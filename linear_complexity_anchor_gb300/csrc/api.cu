@@ -442,7 +442,7 @@ anchor_attn_status_t anchor_attn_query_plan(int dtype, int B, int heads, int n, 
 
 anchor_attn_status_t anchor_attn_device_error(unsigned *code) {
     if (!code) return ANCHOR_ATTN_ERR_INVALID_ARG;
-    unsigned a = 0, b = 0, c = 0, e = 0, f = 0, g = 0, k = 0, l = 0, q = 0, r = 0, w = 0, x = 0;
+    unsigned a = 0, b = 0, c = 0, e = 0, f = 0, g = 0, k = 0, l = 0, q = 0, r = 0, w = 0, x = 0, y = 0;
     if (cudaDeviceSynchronize() != cudaSuccess || anchor::umma_read_and_clear_error(&a) != cudaSuccess ||
         anchor::simt_read_and_clear_error(&b) != cudaSuccess || anchor::bwd_read_and_clear_error(&c) != cudaSuccess ||
         anchor::causal_read_and_clear_error(&e) != cudaSuccess || anchor::block_read_and_clear_error(&f) != cudaSuccess ||
@@ -450,11 +450,12 @@ anchor_attn_status_t anchor_attn_device_error(unsigned *code) {
         anchor::stream_read_and_clear_error(&l) != cudaSuccess || anchor::split_read_and_clear_error(&q) != cudaSuccess ||
         anchor::causal_wide_read_and_clear_error(&r) != cudaSuccess ||
         anchor::bwd_wide_read_and_clear_error(&w) != cudaSuccess ||
-        anchor::cross_fwd_read_and_clear_error(&x) != cudaSuccess) {
+        anchor::cross_fwd_read_and_clear_error(&x) != cudaSuccess ||
+        anchor::cross_bwd_read_and_clear_error(&y) != cudaSuccess) {
         cudaGetLastError();
         return ANCHOR_ATTN_ERR_CUDA;
     }
-    *code = a | b | c | e | f | g | k | l | q | r | w | x;
+    *code = a | b | c | e | f | g | k | l | q | r | w | x | y;
     return ANCHOR_ATTN_OK;
 }
 

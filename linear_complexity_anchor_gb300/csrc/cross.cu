@@ -185,7 +185,8 @@ anchor_attn_status_t cross(const anchor_attn_cross_t *a, bool bwd, void *stream_
             delta = (float *)ws;
             e = launch_cross_delta(p, delta, stream);
         }
-        if (e == cudaSuccess) e = launch_cross_simt_backward(p, delta, stream);
+        if (e == cudaSuccess)
+            e = p.f32 ? launch_cross_simt_backward(p, delta, stream) : launch_cross_tc_backward(p, delta, stream);
     }
     if (ws) {
         const cudaError_t ef = cudaFreeAsync(ws, stream);

@@ -55,6 +55,8 @@ cudaError_t launch_cross_simt_backward(const CrossProblem &p, const float *delta
 // tensor cores, bf16
 int cross_tc_parts(const CrossProblem &p);
 cudaError_t launch_cross_tc_forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream);
+cudaError_t launch_cross_tc_backward(const CrossProblem &p, const float *delta, cudaStream_t stream);
+cudaError_t cross_bwd_read_and_clear_error(unsigned *out);
 cudaError_t cross_fwd_read_and_clear_error(unsigned *out);
 
 }  // namespace anchor

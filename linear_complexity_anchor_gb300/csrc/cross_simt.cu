@@ -1,4 +1,4 @@
-// Cross attention on CUDA cores, fp32 arithmetic, forward and backward (formulas in
+// Cross attention in fp32 on CUDA cores, forward and backward (formulas in
 // include/anchor_attn.h).
 //
 // Tiles of BM rows by 64 columns, 256 threads as 16 x 16: a thread has BM / 16 rows (next to one
@@ -26,22 +26,15 @@ constexpr int kThreads = 256, kBN = 64;
 constexpr int kPitchS = kBN + 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 a = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u), __uint_as_float(a.y << 16),
-                       __uint_as_float(a.y & 0xffff0000u));
-}
-
 // `rows` rows of D elements into shared memory as fp32, zeros where at(r) is null
 template <int D, typename At>
 __device__ __forceinline__ void load_rows(float *dst, int rows, At at) {
     constexpr int C = D / 4;
     for (int i = threadIdx.x; i < rows * C; i += kThreads) {
         const int r = i / C, c = 4 * (i - r * C);
-        const auto *src = at(r);
+        const float *src = at(r);
         *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) =
-            src ? load4(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            src ? *reinterpret_cast<const float4 *>(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
@@ -134,7 +127,7 @@ template <int D, int TM> constexpr size_t forward_smem() {
     return 4 * ((size_t)(16 * TM + 2 * kBN) * (D + 4) + 16 * TM * kPitchS);
 }
 
-template <typename T, int D, int TM>
+template <int D, int TM>
 __global__ void __launch_bounds__(kThreads) cross_simt_forward_kernel(const CrossProblem p, const CrossParts w, int tiles) {
     constexpr int BM = 16 * TM;
     extern __shared__ __align__(16) float sm[];
@@ -147,8 +140,8 @@ __global__ void __launch_bounds__(kThreads) cross_simt_forward_kernel(const Cros
     const int L = cross_length(p, b), key_tiles = (L + kBN - 1) / kBN;
     const int t0 = (int)((long long)key_tiles * blockIdx.y / w.parts), t1 = (int)((long long)key_tiles * (blockIdx.y + 1) / w.parts);
     const float c = p.scale * kLog2e;
-    const T *Q = (const T *)p.Q.ptr;
-    const T *K = (const T *)p.K.ptr + b * p.K.sb + k * p.K.sh, *V = (const T *)p.V.ptr + b * p.V.sb + k * p.V.sh;
+    const float *Q = (const float *)p.Q.ptr;
+    const float *K = (const float *)p.K.ptr + b * p.K.sb + k * p.K.sh, *V = (const float *)p.V.ptr + b * p.V.sb + k * p.V.sh;
     load_rows<D>(sQ, BM, [&](int r) { return r0 + r < p.rows ? Q + cross_row(p, p.Q, b, k, r0 + r) : nullptr; });
     float m[TM], l[TM], o[TM][kCols<D>];
 #pragma unroll
@@ -201,10 +194,10 @@ __global__ void __launch_bounds__(kThreads) cross_simt_forward_kernel(const Cros
             if (tx == 0) w.ml[f] = make_float2(m[i], l[i]);
             continue;
         }
-        T *H = (T *)p.H.ptr + cross_row(p, p.H, b, k, r);
+        float *H = (float *)p.H.ptr + cross_row(p, p.H, b, k, r);
         const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // no state at all
 #pragma unroll
-        for (int j = 0; j < kCols<D>; ++j) H[col_of<D>(j)] = from_f32<T>(o[i][j] * inv);
+        for (int j = 0; j < kCols<D>; ++j) H[col_of<D>(j)] = o[i][j] * inv;
         if (p.lse && tx == 0) p.lse[cross_flat(p, b, k, r)] = l[i] == 0.f ? -INFINITY : m[i] * (1.f / kLog2e) + logf(l[i]);
     }
 }
@@ -214,7 +207,7 @@ template <int D, int TM> constexpr size_t backward_smem() {
 }
 
 // KEYS: rows are keys, columns the query rows of the key head; else rows are query rows.
-template <typename T, int D, int TM, bool KEYS>
+template <int D, int TM, bool KEYS>
 __global__ void __launch_bounds__(kThreads) cross_simt_backward_kernel(const CrossProblem p, const float *delta, int tiles) {
     constexpr int BM = 16 * TM;
     extern __shared__ __align__(16) float sm[];
@@ -228,8 +221,8 @@ __global__ void __launch_bounds__(kThreads) cross_simt_backward_kernel(const Cro
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int L = cross_length(p, b);
     const float c = p.scale * kLog2e;
-    const T *Q = (const T *)p.Q.ptr, *G = (const T *)p.dH.ptr;
-    const T *K = (const T *)p.K.ptr + b * p.K.sb + k * p.K.sh, *V = (const T *)p.V.ptr + b * p.V.sb + k * p.V.sh;
+    const float *Q = (const float *)p.Q.ptr, *G = (const float *)p.dH.ptr;
+    const float *K = (const float *)p.K.ptr + b * p.K.sb + k * p.K.sh, *V = (const float *)p.V.ptr + b * p.V.sb + k * p.V.sh;
     auto q_row = [&](int r) { return r < p.rows ? Q + cross_row(p, p.Q, b, k, r) : nullptr; };
     auto g_row = [&](int r) { return r < p.rows ? G + cross_row(p, p.dH, b, k, r) : nullptr; };
     auto k_row = [&](int r) { return r < L ? K + r * p.K.sn : nullptr; };
@@ -291,13 +284,13 @@ __global__ void __launch_bounds__(kThreads) cross_simt_backward_kernel(const Cro
     for (int i = 0; i < TM; ++i) {
         const int r = r0 + ty * TM + i;
         if (r >= (KEYS ? p.s : p.rows)) continue;
-        T *dst = KEYS ? (T *)p.dK.ptr + b * p.dK.sb + k * p.dK.sh + r * p.dK.sn : (T *)p.dQ.ptr + cross_row(p, p.dQ, b, k, r);
+        float *dst = KEYS ? (float *)p.dK.ptr + b * p.dK.sb + k * p.dK.sh + r * p.dK.sn : (float *)p.dQ.ptr + cross_row(p, p.dQ, b, k, r);
 #pragma unroll
-        for (int j = 0; j < kCols<D>; ++j) dst[col_of<D>(j)] = from_f32<T>(o[i][j] * p.scale);
+        for (int j = 0; j < kCols<D>; ++j) dst[col_of<D>(j)] = o[i][j] * p.scale;
         if constexpr (KEYS) {
-            dst = (T *)p.dV.ptr + b * p.dV.sb + k * p.dV.sh + r * p.dV.sn;
+            dst = (float *)p.dV.ptr + b * p.dV.sb + k * p.dV.sh + r * p.dV.sn;
 #pragma unroll
-            for (int j = 0; j < kCols<D>; ++j) dst[col_of<D>(j)] = from_f32<T>(o2[i][j]);
+            for (int j = 0; j < kCols<D>; ++j) dst[col_of<D>(j)] = o2[i][j];
         }
     }
 }
@@ -315,36 +308,36 @@ cudaError_t set_smem(Kernel kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename T, int D, int TM>
+template <int D, int TM>
 cudaError_t forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
     const int tiles = (p.rows + 16 * TM - 1) / (16 * TM);
     constexpr size_t smem = forward_smem<D, TM>();
-    const cudaError_t e = set_smem(cross_simt_forward_kernel<T, D, TM>, smem);
+    const cudaError_t e = set_smem(cross_simt_forward_kernel<D, TM>, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cross_simt_forward_kernel<T, D, TM>, dim3(tiles * p.B * p.kv, w.parts), dim3(kThreads), smem, stream, p, w, tiles);
+    return launch_pdl(cross_simt_forward_kernel<D, TM>, dim3(tiles * p.B * p.kv, w.parts), dim3(kThreads), smem, stream, p, w, tiles);
 }
 
-template <typename T, int D, int TM, bool KEYS>
+template <int D, int TM, bool KEYS>
 cudaError_t backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
     const int tiles = ((KEYS ? p.s : p.rows) + 16 * TM - 1) / (16 * TM);
     constexpr size_t smem = backward_smem<D, TM>();
-    const cudaError_t e = set_smem(cross_simt_backward_kernel<T, D, TM, KEYS>, smem);
+    const cudaError_t e = set_smem(cross_simt_backward_kernel<D, TM, KEYS>, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cross_simt_backward_kernel<T, D, TM, KEYS>, dim3(tiles * p.B * p.kv), dim3(kThreads), smem, stream, p, delta, tiles);
+    return launch_pdl(cross_simt_backward_kernel<D, TM, KEYS>, dim3(tiles * p.B * p.kv), dim3(kThreads), smem, stream, p, delta, tiles);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t backward_d(const CrossProblem &p, const float *delta, cudaStream_t stream) {
     const int tq = tile_m(p, p.rows), tk = tile_m(p, p.s);
     cudaError_t e = cudaSuccess;
     if (p.rows > 0)
-        e = tq == 4   ? backward<T, D, 4, false>(p, delta, stream)
-            : tq == 2 ? backward<T, D, 2, false>(p, delta, stream)
-                      : backward<T, D, 1, false>(p, delta, stream);
+        e = tq == 4   ? backward<D, 4, false>(p, delta, stream)
+            : tq == 2 ? backward<D, 2, false>(p, delta, stream)
+                      : backward<D, 1, false>(p, delta, stream);
     if (e != cudaSuccess || p.s == 0) return e;
-    return tk == 4   ? backward<T, D, 4, true>(p, delta, stream)
-           : tk == 2 ? backward<T, D, 2, true>(p, delta, stream)
-                     : backward<T, D, 1, true>(p, delta, stream);
+    return tk == 4   ? backward<D, 4, true>(p, delta, stream)
+           : tk == 2 ? backward<D, 2, true>(p, delta, stream)
+                     : backward<D, 1, true>(p, delta, stream);
 }
 
 }  // namespace
@@ -362,11 +355,7 @@ cudaError_t launch_cross_simt_forward(const CrossProblem &p, const CrossParts &w
     const int tm = tile_m(p, p.rows);
     auto go = [&](auto d) {
         constexpr int D = decltype(d)::value;
-        auto run = [&](auto t) {
-            using T = decltype(t);
-            return tm == 4 ? forward<T, D, 4>(p, w, stream) : tm == 2 ? forward<T, D, 2>(p, w, stream) : forward<T, D, 1>(p, w, stream);
-        };
-        return p.f32 ? run(float{}) : run(__nv_bfloat16{});
+        return tm == 4 ? forward<D, 4>(p, w, stream) : tm == 2 ? forward<D, 2>(p, w, stream) : forward<D, 1>(p, w, stream);
     };
     switch (p.d) {
     case 16: return go(std::integral_constant<int, 16>{});
@@ -378,10 +367,10 @@ cudaError_t launch_cross_simt_forward(const CrossProblem &p, const CrossParts &w
 
 cudaError_t launch_cross_simt_backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
     switch (p.d) {
-    case 16: return p.f32 ? backward_d<float, 16>(p, delta, stream) : backward_d<__nv_bfloat16, 16>(p, delta, stream);
-    case 32: return p.f32 ? backward_d<float, 32>(p, delta, stream) : backward_d<__nv_bfloat16, 32>(p, delta, stream);
-    case 64: return p.f32 ? backward_d<float, 64>(p, delta, stream) : backward_d<__nv_bfloat16, 64>(p, delta, stream);
-    default: return p.f32 ? backward_d<float, 128>(p, delta, stream) : backward_d<__nv_bfloat16, 128>(p, delta, stream);
+    case 16: return backward_d<16>(p, delta, stream);
+    case 32: return backward_d<32>(p, delta, stream);
+    case 64: return backward_d<64>(p, delta, stream);
+    default: return backward_d<128>(p, delta, stream);
     }
 }
 
