@@ -11,8 +11,8 @@
 //   keys      a tile of 128 rows of K and V stays, the queries of all heads that share it
 //             stream by: S^T = K Q^T, dP^T = V dH^T, dV += P^T dH, dK += dS^T Q
 //
-// Eight row warps: warp w has lanes 32 (w % 4) .. + 31 of tensor memory (one row a thread) and
-// columns 64 (w / 4) .. + 63.  P^T and dS go back to tensor memory as bf16 operands, each warp's
+// Sixteen row warps: warp w has lanes 32 (w % 4) .. + 31 of tensor memory (one row a thread) and
+// columns 32 (w / 4) .. + 31.  P^T and dS go back to tensor memory as bf16 operands, each warp's
 // over columns that it has read itself.  The products are issued so that the tensor cores have
 // work while the rows are between two of their steps:
 //   keys      after P^T(j): dV += P^T(j) dH, S^T(j + 1)      while the rows make dS^T(j)
@@ -35,17 +35,20 @@ namespace {
 
 using namespace cross_tc;
 
-constexpr int kRowWarps = 8;
+constexpr int kRowWarps = 16, kQuarter = 32;  // columns of a row warp
 constexpr int kLoad = kRowWarps, kStat = kRowWarps + 1, kIssue = kRowWarps + 2;
 constexpr int kThreads = 32 * (kRowWarps + 3);
 constexpr uint32_t kColS = 0, kColP = 128, kColA = 256;  // S, dP, then the sums
 
 template <int D>
 struct Geo {
-    static constexpr int kStages = D == 128 ? 4 : 8;
-    static constexpr int kFix = 0, kRing = 2 * kTile<D>, kStatB = kRing + kStages * kTile<D>;  // 2 x (lse, D) of 128 columns
-    static constexpr int kBars = kStatB + 2 * 2 * kRows * 4;
-    static constexpr int kNBars = 2 * kStages + 11;
+    // Slots of the two tiles that stream by (Q or K, dH or V).  The first of step j is in use from the
+    // middle of step j - 1 to the end of step j, the second from the end of step j - 1: with one slot
+    // more for the first, both are loaded a step and more ahead.
+    static constexpr int kNB = D == 128 ? 2 : 3, kNA = kNB + 1;
+    static constexpr int kFix = 0, kA = 2 * kTile<D>, kB = kA + kNA * kTile<D>, kStatB = kB + kNB * kTile<D>;  // lse, D of 128 columns
+    static constexpr int kBars = kStatB + 2 * kRows * 4;
+    static constexpr int kNBars = kNA + 2 * kNB + 11;
     static constexpr int kSmem = kBars + kNBars * 8 + 16 + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -58,21 +61,17 @@ struct BwdParams {
     int tiles;
 };
 
-// An operand of 128 contraction columns in tensor memory, bf16: the two halves over the first 32 of
-// their own 64 columns.
-__device__ __forceinline__ uint32_t half_step(uint32_t base, int k) { return base + (k < 4 ? 8 * k : 64 + 8 * (k - 4)); }
-
 // KEYS: see above
 template <int D, bool KEYS>
 __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_constant__ BwdParams a) {
     using G = Geo<D>;
-    constexpr int ST = G::kStages;
+    constexpr int NA = G::kNA, NB = G::kNB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G::kBars);
-    uint64_t *full = bars, *empty = full + ST, *fix_full = empty + ST, *s_full = fix_full + 1, *dp_full = s_full + 1,
-             *p_full = dp_full + 1, *ds_full = p_full + 1, *stat_full = ds_full + 1 /* [2] */, *stat_empty = stat_full + 2 /* [2] */,
-             *acc = stat_empty + 2, *done = acc + 1;
+    uint64_t *a_full = bars /* [NA] */, *b_full = a_full + NA /* [NB] */, *empty = b_full + NB /* [NB] */, *fix_full = empty + NB,
+             *s_full = fix_full + 1, *dp_full = s_full + 1, *p_full = dp_full + 1, *ds_full = p_full + 1, *lse_full = ds_full + 1,
+             *lse_empty = lse_full + 1, *d_full = lse_empty + 1, *d_empty = d_full + 1, *acc = d_empty + 1, *done = acc + 1;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + G::kNBars);
     float *stat = reinterpret_cast<float *>(sm + G::kStatB);
     const CrossProblem &p = a.p;
@@ -82,8 +81,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
     unsigned int *error = &g_cross_bwd_error;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < ST; ++s) {
-            mbar_init(full + s, 1);
+        for (int s = 0; s < NA; ++s) mbar_init(a_full + s, 1);
+        for (int s = 0; s < NB; ++s) {
+            mbar_init(b_full + s, 1);
             mbar_init(empty + s, 1);
         }
         mbar_init(fix_full, KEYS ? 1 : kRowWarps);
@@ -91,10 +91,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
         mbar_init(dp_full, 1);
         mbar_init(p_full, kRowWarps);
         mbar_init(ds_full, kRowWarps);
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(stat_full + s, 1);
-            mbar_init(stat_empty + s, kRowWarps);
-        }
+        mbar_init(lse_full, 1);
+        mbar_init(lse_empty, kRowWarps);
+        mbar_init(d_full, 1);
+        mbar_init(d_empty, kRowWarps);
         mbar_init(acc, 1);
         mbar_init(done, 1);
         fence_mbar_init();
@@ -119,98 +119,113 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
         if (lane == 0 && nt > 0) {
             if (KEYS) {
                 mbar_arrive_expect_tx(fix_full, 2 * kTile<D>);
-#pragma unroll
-                for (int q = 0; q < D / 64; ++q) {
-                    tma_load_4d(sm + G::kFix + q * kBlock, &a.fa.map, fix_full, 64 * q, r0, kh * a.fa.by_head, b * a.fa.by_batch);
-                    tma_load_4d(sm + G::kFix + kTile<D> + q * kBlock, &a.fb.map, fix_full, 64 * q, r0, kh * a.fb.by_head,
-                                b * a.fb.by_batch);
-                }
+                load_tile<D>(sm + G::kFix, a.fa, fix_full, r0, kh, b);
+                load_tile<D>(sm + G::kFix + kTile<D>, a.fb, fix_full, r0, kh, b);
             }
-            int i = 0;
-            for (; i < 2 * nt; ++i) {
-                const int st = i % ST, j = i / 2;
-                if (i >= ST && !bwait(empty + st, (uint32_t)((i / ST - 1) & 1), error)) break;
-                const int row = (KEYS ? j % per_head : j) * kRows, head = KEYS ? kh * p.group + j / per_head : kh;
-                load_tile<D>(sm + G::kRing + st * kTile<D>, i & 1 ? a.b : a.a, full + st, row, head, b);
+            auto row_of = [&](int j) { return (KEYS ? j % per_head : j) * kRows; };
+            auto head_of = [&](int j) { return KEYS ? kh * p.group + j / per_head : kh; };
+            auto load_a = [&](int j) {
+                if (j >= nt) return;
+                mbar_arrive_expect_tx(a_full + j % NA, kTile<D>);
+                load_tile<D>(sm + G::kA + j % NA * kTile<D>, a.a, a_full + j % NA, row_of(j), head_of(j), b);
+            };
+            auto load_b = [&](int j) {
+                if (j >= nt) return;
+                mbar_arrive_expect_tx(b_full + j % NB, kTile<D>);
+                load_tile<D>(sm + G::kB + j % NB * kTile<D>, a.b, b_full + j % NB, row_of(j), head_of(j), b);
+            };
+            for (int j = 0; j < NB; ++j) {
+                load_a(j);
+                load_b(j);
+            }
+            load_a(NB);
+            int i = 0;  // steps that are done
+            for (; i < nt - NB; ++i) {
+                if (!bwait(empty + i % NB, (uint32_t)((i / NB) & 1), error)) break;
+                load_b(i + NB);
+                load_a(i + NA);
             }
             // the CTA leaves only once its copies have landed
-            for (int j = max(0, i - ST); j < i; ++j) bwait(full + j % ST, (uint32_t)((j / ST) & 1), error);
+            for (int j = i; j < min(nt, i + NA); ++j) bwait(a_full + j % NA, (uint32_t)((j / NA) & 1), error);
+            for (int j = i; j < min(nt, i + NB); ++j) bwait(b_full + j % NB, (uint32_t)((j / NB) & 1), error);
             if (KEYS) bwait(fix_full, 0u, error);
         }
         __syncwarp();
     } else if (warp == kStat) {
-        if (KEYS) {  // lse (in log2) and D of each step's columns; columns that do not exist: P = 0
-            bool ok = true;
-            for (int j = 0; j < nt && ok; ++j) {
-                if (j >= 2) ok = bwait(stat_empty + (j & 1), (uint32_t)((j / 2 - 1) & 1), error);
-                if (!ok) break;
+        if (KEYS) {
+            // lse (in log2) and D of each step's columns, read a step ahead; columns that do not exist: P = 0
+            float next[8];
+            auto fetch = [&](int j) {
                 const int i0 = (j % per_head) * kRows;
                 const long long f = ((long long)b * p.heads + kh * p.group + j / per_head) * p.n + i0;
-                float *dst = stat + (j & 1) * 2 * kRows;
 #pragma unroll
-                for (int x = 0; x < kRows; x += 32) {
-                    const bool in = i0 + x + lane < p.n;
-                    dst[x + lane] = in ? p.lse[f + x + lane] * kLog2e : INFINITY;
-                    dst[kRows + x + lane] = in ? a.delta[f + x + lane] : 0.f;
+                for (int x = 0; x < 4; ++x) {
+                    const bool in = j < nt && i0 + 32 * x + lane < p.n;
+                    next[x] = in ? p.lse[f + 32 * x + lane] * kLog2e : INFINITY;
+                    next[4 + x] = in ? a.delta[f + 32 * x + lane] : 0.f;
                 }
+            };
+            bool ok = true;
+            if (nt > 0) fetch(0);
+            for (int j = 0; j < nt && ok; ++j) {
+                if (j > 0 && !(ok = bwait(lse_empty, (uint32_t)((j - 1) & 1), error))) break;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) stat[32 * x + lane] = next[x];
                 __syncwarp();
-                if (lane == 0) mbar_arrive(stat_full + (j & 1));
+                if (lane == 0) mbar_arrive(lse_full);
+                if (j > 0 && !(ok = bwait(d_empty, (uint32_t)((j - 1) & 1), error))) break;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) stat[kRows + 32 * x + lane] = next[4 + x];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(d_full);
+                if (j + 1 < nt) fetch(j + 1);
             }
         }
         __syncwarp();
     } else if (warp == kIssue) {
         if (lane == 0 && nt > 0) {
             const int ksteps = (p.d + 15) / 16;
-            const uint32_t base = smem_u32(sm), ring = base + G::kRing;
+            const uint32_t base = smem_u32(sm);
             const uint32_t idA = idesc_bf16_f32(kRows, p.d < D ? p.d : D, false, true);
             const uint64_t f0 = desc_k(base + G::kFix), f1 = desc_k(base + G::kFix + kTile<D>);
-            auto landed = [&](int i) {
-                const bool ok = bwait(full + i % ST, (uint32_t)((i / ST) & 1), error);
-                tc_fence_after();
-                return ok;
-            };
-            // to = (the tile that stays) x (slot i of the ring)^T
-            auto across = [&](uint32_t to, uint64_t fix, int i, uint64_t *bar) {
-                const uint32_t id = idesc_bf16_f32(kRows, width16(i / 2), false, false);
-                const uint64_t d = desc_k(ring + (i % ST) * kTile<D>);
-                for (int k = 0; k < ksteps; ++k) umma_bf16(to, fix + step_k(k), d + step_k(k), id, k > 0 ? 1u : 0u);
+            // (a commit takes this thread 70 cycles, a wait on a complete barrier 80: one barrier frees both
+            // tiles of a step, and what has to have landed is waited for before the rows are)
+            auto slot_a = [&](int j) { return base + G::kA + j % NA * kTile<D>; };
+            auto slot_b = [&](int j) { return base + G::kB + j % NB * kTile<D>; };
+            auto landed_a = [&](int j) { return bwait(a_full + j % NA, (uint32_t)((j / NA) & 1), error); };
+            auto landed_b = [&](int j) { return bwait(b_full + j % NB, (uint32_t)((j / NB) & 1), error); };
+            // to = (a tile that stays) x (a tile of step j)^T
+            auto across = [&](uint32_t to, uint64_t fix, uint32_t tile, int j, uint64_t *bar) {
+                product_k<D>(to, fix, desc_k(tile), idesc_bf16_f32(kRows, width16(j), false, false), ksteps);
                 umma_commit(bar);
             };
-            // sum += (operand in tensor memory) x (slot i of the ring)
-            auto along = [&](uint32_t sum, uint32_t op, int i) {
-                const int steps = width16(i / 2) / 16;
-                const uint64_t d = desc_mn(ring + (i % ST) * kTile<D>);
-                for (int k = 0; k < steps; ++k)
-                    umma_bf16_tmem_a(sum, half_step(op, k), d + step_mn(k), idA, (i > 1 || k > 0) ? 1u : 0u);
+            // sum += (operand in tensor memory) x (a tile of step j)
+            auto along = [&](uint32_t sum, uint32_t op, uint32_t tile, int j) {
+                product_mn<kQuarter / 2>(sum, op, desc_mn(tile), idA, width16(j) / 16, j > 0);
             };
-            bool ok = bwait(fix_full, 0u, error) && landed(0);
+            bool ok = bwait(fix_full, 0u, error) && landed_a(0);
+            tc_fence_after();
             if (ok) {
-                across(tmem + kColS, f0, 0, s_full);
-                ok = landed(1);
-                if (ok) across(tmem + kColP, f1, 1, dp_full);
+                across(tmem + kColS, f0, slot_a(0), 0, s_full);
+                ok = landed_b(0);
+                tc_fence_after();
+                if (ok) across(tmem + kColP, f1, slot_b(0), 0, dp_full);
             }
             for (int j = 0; j < nt && ok; ++j) {
+                const bool more = j + 1 < nt;
                 // the rows have read S(j) (and left P^T(j) over it)
+                if (more && !(ok = landed_a(j + 1))) break;
                 if (!(ok = bwait(p_full, (uint32_t)(j & 1), error))) break;
                 tc_fence_after();
-                if (KEYS) {
-                    along(tmem + kColA, tmem + kColS, 2 * j + 1);  // dV += P^T dH
-                    umma_commit(empty + (2 * j + 1) % ST);
-                }
-                if (j + 1 < nt) {
-                    if (!(ok = landed(2 * j + 2))) break;
-                    across(tmem + kColS, f0, 2 * j + 2, s_full);
-                }
+                if (KEYS) along(tmem + kColA, tmem + kColS, slot_b(j), j);  // dV += P^T dH
+                if (more) across(tmem + kColS, f0, slot_a(j + 1), j + 1, s_full);
                 // the rows have left dS(j) over dP(j)
+                if (more && !(ok = landed_b(j + 1))) break;
                 if (!(ok = bwait(ds_full, (uint32_t)(j & 1), error))) break;
                 tc_fence_after();
-                along(tmem + kColA + (KEYS ? D : 0), tmem + kColP, 2 * j);  // dK += dS^T Q, dQ += dS K
-                umma_commit(empty + 2 * j % ST);
-                if (!KEYS) umma_commit(empty + (2 * j + 1) % ST);  // V: read by dP(j), long done
-                if (j + 1 < nt) {
-                    if (!(ok = landed(2 * j + 3))) break;
-                    across(tmem + kColP, f1, 2 * j + 3, dp_full);
-                }
+                along(tmem + kColA + (KEYS ? D : 0), tmem + kColP, slot_a(j), j);  // dK += dS^T Q, dQ += dS K
+                if (more) across(tmem + kColP, f1, slot_b(j + 1), j + 1, dp_full);
+                umma_commit(empty + j % NB);
             }
             if (ok) umma_commit(acc);
             umma_commit(done);
@@ -219,20 +234,21 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
         __syncwarp();
     } else {
         // ------------------------------------------------------------------ rows
-        const int half = warp >> 2, w4 = warp & 3, row = w4 * 32 + lane, r = r0 + row;
+        const int quarter = warp >> 2, w4 = warp & 3, row = w4 * 32 + lane, r = r0 + row;
         const bool mine = r < (KEYS ? L : p.rows);  // a row that counts
         const uint32_t trow = tmem + ((uint32_t)(w4 * 32) << 16);
         const float c = p.scale * kLog2e;
-        constexpr int kLanes = D / 8;
         float lse2 = INFINITY, dl = 0.f;
         if (!KEYS && nt > 0) {
-            // half 0 loads the 128 rows of Q, half 1 those of dH
-            const CrossView &v = half ? p.dH : p.Q;
+            // quarters 0 and 1 load the 128 rows of Q, by halves of the columns, 2 and 3 those of dH
+            constexpr int kLanes = D / 16;
+            const CrossView &v = quarter >= 2 ? p.dH : p.Q;
             const long long at = mine ? cross_row(p, v, b, kh, r) : -1;
-            uint8_t *dst = sm + G::kFix + half * kTile<D>;
+            uint8_t *dst = sm + G::kFix + (quarter >> 1) * kTile<D>;
+            const int ch = (quarter & 1) * kLanes + lane % kLanes;
 #pragma unroll
             for (int i = 0; i < kLanes; ++i) {
-                const int rr = i * (32 / kLanes) + lane / kLanes, ch = lane % kLanes;
+                const int rr = i * (32 / kLanes) + lane / kLanes;
                 const long long o = __shfl_sync(0xffffffffu, at, rr);
                 uint4 x = make_uint4(0, 0, 0, 0);
                 if (o >= 0 && ch * 8 < p.d) x = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)v.ptr + o + ch * 8);
@@ -247,20 +263,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
                 dl = a.delta[f];
             }
         }
+        const uint32_t tS = trow + kColS + kQuarter * quarter, tP = trow + kColP + kQuarter * quarter;
         bool ok = true;
         for (int j = 0; j < nt && ok; ++j) {
-            const int cols = width(j) - 64 * half;  // of this half that exist (may be none)
-            const uint32_t tS = trow + kColS + 64 * half, tP = trow + kColP + 64 * half;
-            const float *st = stat + (j & 1) * 2 * kRows + 64 * half;
-            float e[64];
+            const int cols = width(j) - kQuarter * quarter;  // of this quarter that exist (may be none)
+            const float *st = stat + kQuarter * quarter;
+            float e[32];
             if (!bwait(s_full, (uint32_t)(j & 1), error)) { ok = false; break; }
-            if (KEYS && !bwait(stat_full + (j & 1), (uint32_t)((j / 2) & 1), error)) { ok = false; break; }
+            if (KEYS && !bwait(lse_full, (uint32_t)(j & 1), error)) { ok = false; break; }
             tc_fence_after();
             tmem_ld32(tS, e);
-            if (cols > 32) tmem_ld32(tS + 32, e + 32);
             tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < 64; x += 4) {
+            for (int x = 0; x < 32; x += 4) {
                 float4 s4 = make_float4(lse2, lse2, lse2, lse2);
                 if (KEYS) s4 = *reinterpret_cast<const float4 *>(st + x);
                 e[x] = ex2(fmaf(e[x], c, -s4.x));
@@ -268,76 +283,79 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
                 e[x + 2] = ex2(fmaf(e[x + 2], c, -s4.z));
                 e[x + 3] = ex2(fmaf(e[x + 3], c, -s4.w));
             }
-            if (!mine || (!KEYS && cols < 64)) {
+            const bool cut = !mine || (!KEYS && cols < 32);
+            if (cut) {
 #pragma unroll
-                for (int x = 0; x < 64; ++x)
+                for (int x = 0; x < 32; ++x)
                     if (!mine || x >= cols) e[x] = 0.f;
             }
             if (KEYS) {
-                uint32_t u[32];
+                uint32_t u[16];
 #pragma unroll
-                for (int x = 0; x < 32; ++x) u[x] = pack2(e[2 * x], e[2 * x + 1]);
-                tmem_st32(tS, u);
+                for (int x = 0; x < 16; ++x) u[x] = pack2(e[2 * x], e[2 * x + 1]);
+                tmem_st16(tS, u);
                 tmem_st_wait();
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_full);
+            if (lane == 0) {
+                if (KEYS) mbar_arrive(lse_empty);
+                mbar_arrive(p_full);
+            }
             // dS
+            if (KEYS && !bwait(d_full, (uint32_t)(j & 1), error)) { ok = false; break; }
             if (!bwait(dp_full, (uint32_t)(j & 1), error)) { ok = false; break; }
             tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            {
                 float g[32];
                 uint32_t u[16];
-                if (x == 1 && cols <= 32) break;
-                tmem_ld32(tP + 32 * x, g);
+                tmem_ld32(tP, g);
                 tmem_ld_wait();
 #pragma unroll
                 for (int y = 0; y < 32; y += 4) {
                     float4 d4 = make_float4(dl, dl, dl, dl);
-                    if (KEYS) d4 = *reinterpret_cast<const float4 *>(st + kRows + 32 * x + y);
-                    const float *q = e + 32 * x + y;
-                    g[y] = q[0] * (g[y] - d4.x);
-                    g[y + 1] = q[1] * (g[y + 1] - d4.y);
-                    g[y + 2] = q[2] * (g[y + 2] - d4.z);
-                    g[y + 3] = q[3] * (g[y + 3] - d4.w);
+                    if (KEYS) d4 = *reinterpret_cast<const float4 *>(st + kRows + y);
+                    g[y] = e[y] * (g[y] - d4.x);
+                    g[y + 1] = e[y + 1] * (g[y + 1] - d4.y);
+                    g[y + 2] = e[y + 2] * (g[y + 2] - d4.z);
+                    g[y + 3] = e[y + 3] * (g[y + 3] - d4.w);
                 }
-                // (a masked state's dP may be anything: zero by select, not by the product)
-                if (!mine || (!KEYS && cols < 64)) {
+                if (cut) {  // (a masked state's dP may be anything: zero by select, not by the product)
 #pragma unroll
                     for (int y = 0; y < 32; ++y)
-                        if (!mine || 32 * x + y >= cols) g[y] = 0.f;
+                        if (!mine || y >= cols) g[y] = 0.f;
                 }
 #pragma unroll
                 for (int y = 0; y < 16; ++y) u[y] = pack2(g[2 * y], g[2 * y + 1]);
-                tmem_st16(tP + 16 * x, u);
+                tmem_st16(tP, u);
             }
             tmem_st_wait();
-            if (!KEYS && j == nt - 1 && half == 0 && L % kRows && L < p.s) {
+            if (!KEYS && j == nt - 1 && quarter == 0 && L % kRows && L < p.s) {
                 // the last tile's rows of K that do not count (S has read them)
-                if (!bwait(full + 2 * j % ST, (uint32_t)((2 * j / ST) & 1), error)) { ok = false; break; }
-                zero_rows<D>(sm + G::kRing + (2 * j % ST) * kTile<D>, row, L % kRows, (L % kRows + 15) / 16 * 16);
+                if (!bwait(a_full + j % NA, (uint32_t)((j / NA) & 1), error)) { ok = false; break; }
+                zero_rows<D>(sm + G::kA + j % NA * kTile<D>, row, L % kRows, (L % kRows + 15) / 16 * 16);
                 fence_proxy_async_smem();
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (KEYS) mbar_arrive(stat_empty + (j & 1));
+                if (KEYS) mbar_arrive(d_empty);
                 mbar_arrive(ds_full);
             }
         }
         if (ok && nt > 0) ok = bwait(acc, 0u, error);
         tc_fence_after();
-        // rows out through shared memory (the tiles that stayed are not needed any more): keys: half 0
-        // dV, half 1 dK; queries: each half its columns of dQ
-        const bool second = KEYS && half == 1;
-        const float by = KEYS && half == 0 ? 1.f : p.scale;
+        // Rows out through shared memory (the tiles that stayed are not needed any more).  Keys: quarters
+        // 0 and 1 halves of dV's columns, 2 and 3 of dK's; queries: quarters of dQ's at d = 128, halves
+        // below.
+        const bool second = KEYS && quarter >= 2;
+        const float by = KEYS && !second ? 1.f : p.scale;
         uint8_t *stage = sm + G::kFix + (second ? kTile<D> : 0);
-        const int from = KEYS ? 0 : half * (D / 2), to = KEYS ? D : from + D / 2;
-        if (ok) {
+        constexpr int kCols = KEYS || D == 64 ? D / 2 : D / 4;  // of a warp
+        const int part = KEYS ? quarter & 1 : quarter, from = part * kCols, to = min(p.d, from + kCols);
+        if (ok && from < p.d) {
 #pragma unroll 1
-            for (int x = from; x < to && x < p.d; x += 32) {
+            for (int x = from; x < to; x += 32) {
                 float o[32];
                 if (nt > 0) {
                     tmem_ld32(trow + kColA + (second ? D : 0) + x, o);
@@ -358,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
             const bool exists = r < (KEYS ? p.s : p.rows);
             const long long at = !exists ? -1 : KEYS ? b * v.sb + kh * v.sh + (long long)r * v.sn : cross_row(p, v, b, kh, r);
             // 16-byte chunks of this warp's rows and columns, a row's chunks by neighbouring lanes
-            constexpr int kW = KEYS ? D / 8 : D / 16;
+            constexpr int kW = kCols / 8;
 #pragma unroll
             for (int i = 0; i < kW; ++i) {
                 const int rr = i * (32 / kW) + lane / kW, ch = from / 8 + lane % kW;

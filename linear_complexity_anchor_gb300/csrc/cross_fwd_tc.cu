@@ -1,8 +1,9 @@
 // Cross attention forward in bf16 on the tensor cores (formulas in include/anchor_attn.h).
 //
 // A CTA has one or two tiles of 128 query rows of one key head, and walks that head's keys in
-// tiles of 128: S = Q K^T into tensor memory, one thread per row takes the running maximum and
-// sum and leaves P = 2^(c s - m) as bf16 over S's columns, O += P V from there.  Q is loaded with
+// tiles of 128: S = Q K^T into tensor memory, two threads per row (64 columns each) take the
+// running maximum and sum and leave P = 2^(c s - m) as bf16 over S's columns, O += P V from there.
+// (One thread per row was bound by its own latency: the tensor pipe 36 % active against NEW.)  Q is loaded with
 // plain 16-byte loads (rows of several heads, any strides), K and V by TMA into a ring, K and V in
 // turn, by a warp of their own; one thread of another warp issues the products.
 //
@@ -12,7 +13,7 @@
 // at d = 128, so P lies over S: the products of one CTA run in the order they are issued, and the
 // next S is issued after the P V that reads it.
 // One tile (up to 128 rows, a token of serving above all): bound by reading K and V.  At d = 128
-// S has two buffers, the next S is issued before the softmax of this one, and six stages of 32 KB
+// S has two buffers, the next S is issued before the softmax of this one, and three stages of 64 KB
 // are in flight; at d = 64 two CTAs share an SM.
 // Few rows and long keys: the key tiles of an entry (of its own length) are cut over gridDim.y
 // CTAs, which leave sums that a second launch joins.
@@ -39,12 +40,13 @@ constexpr float kSlack = 8.f;  // log2 of how far a maximum may be passed before
 
 template <int D, int NQ>
 struct Geo {
-    static constexpr int kStages = D == 128 ? (NQ == 2 ? 5 : 6) : (NQ == 2 ? 8 : 5);
     static constexpr int kNS = NQ == 1 && D == 128 ? 2 : 1;  // S buffers of a tile
+    static constexpr int kStages = NQ == 1 ? (D == 128 ? 3 : 2) : (D == 128 ? 2 : 4);  // of a K and a V tile
     static constexpr int kPerSM = NQ == 1 && D == 64 ? 2 : 1;
-    static constexpr int kThreads = 128 * NQ + 64;
-    static constexpr int kQ = 0, kRing = NQ * kTile<D>, kBars = kRing + kStages * kTile<D>;
-    static constexpr int kNBars = NQ + 2 * kStages + 2 * NQ * kNS + NQ + 1;
+    static constexpr int kThreads = 256 * NQ + 64;
+    static constexpr int kQ = 0, kRing = NQ * kTile<D>, kEx = kRing + kStages * 2 * kTile<D>;
+    static constexpr int kBars = kEx + NQ * 2 * kRows * 4;
+    static constexpr int kNBars = NQ + 2 * kStages + 2 * NQ * kNS + NQ + 4 * NQ + 1;
     static constexpr int kSmem = kBars + kNBars * 8 + 16 + 1024;
     static constexpr uint32_t kColO = 128 * NQ * kNS, kCols = kColO + NQ * D <= 256 ? 256 : 512;
     static_assert(kSmem * kPerSM + kPerSM * 1024 <= 228 * 1024, "shared memory");
@@ -67,11 +69,11 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G::kBars);
     uint64_t *q_full = bars, *full = q_full + NQ, *empty = full + ST, *s_full = empty + ST, *p_full = s_full + NQ * NS,
-             *o_full = p_full + NQ * NS, *done = o_full + NQ;
+             *o_full = p_full + NQ * NS, *pair = o_full + NQ, *done = pair + 4 * NQ;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + G::kNBars);
     const CrossProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kLoad = 4 * NQ, kIssue = 4 * NQ + 1;
+    constexpr int kLoad = 8 * NQ, kIssue = 8 * NQ + 1;
     const int tile = (int)(blockIdx.x % a.tiles), bk = (int)(blockIdx.x / a.tiles);
     const int b = bk / p.kv, kh = bk - b * p.kv, r0 = tile * NQ * kRows;
     const int left = p.rows - r0;                        // rows of this CTA that exist
@@ -80,11 +82,12 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
     if (threadIdx.x == 0) {
         for (int q = 0; q < NQ; ++q) {
             const int warps = min(max((left - q * kRows + 31) / 32, 1), 4);  // with a row that exists
-            mbar_init(q_full + q, 4);
+            mbar_init(q_full + q, 8);
             mbar_init(o_full + q, 1);
+            for (int w = 0; w < 4; ++w) mbar_init(pair + 4 * q + w, 2);
             for (int s = 0; s < NS; ++s) {
                 mbar_init(s_full + q * NS + s, 1);
-                mbar_init(p_full + q * NS + s, warps);
+                mbar_init(p_full + q * NS + s, 2 * warps);
             }
         }
         for (int s = 0; s < ST; ++s) {
@@ -111,11 +114,15 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
         if (lane == 0 && nt > 0) {
             tma_prefetch_desc(&a.k.map);
             tma_prefetch_desc(&a.v.map);
+            // stage i: K of tile i, and V of tile i - NS, which are used at one time
             int i = 0;
-            for (; i < 2 * nt; ++i) {
+            for (; i < nt + NS; ++i) {
                 const int st = i % ST;
                 if (i >= ST && !bwait(empty + st, (uint32_t)((i / ST - 1) & 1), error)) break;
-                load_tile<D>(sm + G::kRing + st * kTile<D>, i & 1 ? a.v : a.k, full + st, (t0 + i / 2) * kRows, kh, b);
+                uint8_t *dst = sm + G::kRing + st * 2 * kTile<D>;
+                mbar_arrive_expect_tx(full + st, (i < nt ? kTile<D> : 0) + (i >= NS ? kTile<D> : 0));
+                if (i >= NS) load_tile<D>(dst + kTile<D>, a.v, full + st, (t0 + i - NS) * kRows, kh, b);
+                if (i < nt) load_tile<D>(dst, a.k, full + st, (t0 + i) * kRows, kh, b);
             }
             // the CTA leaves only once its copies have landed
             for (int j = max(0, i - ST); j < i; ++j) bwait(full + j % ST, (uint32_t)((j / ST) & 1), error);
@@ -123,54 +130,44 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
         __syncwarp();
     } else if (warp == kIssue) {
         if (lane == 0 && nt > 0) {
+            // Between products this thread is what the tensor cores wait for: a commit takes it 70 cycles
+            // and a wait on a barrier that is already complete 80, so K and V of a step share a
+            // stage, and nothing is committed that nobody waits for.
             const int ksteps = (p.d + 15) / 16;
             const uint32_t base = smem_u32(sm), ring = base + G::kRing;
             const uint32_t idO = idesc_bf16_f32(kRows, p.d < D ? p.d : D, false, true);
-            auto cols = [&](int j) { return min(kRows, (L - (t0 + j) * kRows + 15) / 16 * 16); };  // keys of tile j, in 16s
-            auto scores = [&](int q, int j) {  // S of tile j (its K has landed)
-                const uint32_t idS = idesc_bf16_f32(kRows, cols(j), false, false);
-                const uint64_t qd = desc_k(base + G::kQ + q * kTile<D>), kd = desc_k(ring + (2 * j % ST) * kTile<D>);
-                const uint32_t to = tmem + 128 * (q * NS + j % NS);
-                for (int k = 0; k < ksteps; ++k) umma_bf16(to, qd + step_k(k), kd + step_k(k), idS, k > 0 ? 1u : 0u);
-                umma_commit(s_full + q * NS + j % NS);
+            const uint32_t idS = idesc_bf16_f32(kRows, kRows, false, false);
+            const int last16 = (min(kRows, L - (t0 + nt - 1) * kRows) + 15) / 16 * 16;  // keys of the last tile, in 16s
+            const uint32_t idL = idesc_bf16_f32(kRows, last16, false, false);
+            auto scores = [&](int q, int i) {  // S of tile i (its K has landed)
+                product_k<D>(tmem + 128 * (q * NS + i % NS), desc_k(base + G::kQ + q * kTile<D>), desc_k(ring + i % ST * 2 * kTile<D>),
+                             i == nt - 1 ? idL : idS, ksteps);
+                umma_commit(s_full + q * NS + i % NS);
             };
-            auto landed = [&](int i) { return bwait(full + i % ST, (uint32_t)((i / ST) & 1), error); };
-            bool ok = landed(0);
-            for (int q = 0; q < nq && ok; ++q) {
-                ok = bwait(q_full + q, 0u, error);
-                tc_fence_after();
-                if (ok) scores(q, 0);
-            }
-            if (ok) umma_commit(empty + 0);
-            if (NS == 2 && ok && nt > 1) {  // S of tile 1 while the rows are at tile 0
-                ok = landed(2);
-                tc_fence_after();
-                if (ok) {
-                    scores(0, 1);
-                    umma_commit(empty + 2 % ST);
-                }
-            }
-            for (int j = 0; j < nt && ok; ++j) {
-                const int v = 2 * j + 1, ahead = j + NS;  // the S issued after this tile's P V
-                for (int q = 0; q < nq && ok; ++q) {
-                    ok = bwait(p_full + q * NS + j % NS, (uint32_t)((j / NS) & 1), error) && (q > 0 || landed(v));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t vd = desc_mn(ring + (v % ST) * kTile<D>);
-                    const uint32_t P = tmem + 128 * (q * NS + j % NS), O = tmem + G::kColO + q * D;
-                    const int steps = cols(j) / 16;
-                    for (int k = 0; k < steps; ++k)
-                        umma_bf16_tmem_a(O, P + 8 * k, vd + step_mn(k), idO, (j > 0 || k > 0) ? 1u : 0u);
-                    umma_commit(o_full + q);
-                    if (q == nq - 1) umma_commit(empty + v % ST);
-                    if (ahead < nt) {
-                        if (q == 0) ok = landed(2 * ahead);
+            bool ok = true;
+            for (int i = 0; i < NS && ok; ++i) {
+                if (i < nt) {
+                    ok = bwait(full + i % ST, 0u, error);
+                    for (int q = 0; q < nq && ok; ++q) {
+                        if (i == 0) ok = bwait(q_full + q, 0u, error);
                         tc_fence_after();
-                        if (!ok) break;
-                        scores(q, ahead);
-                        if (q == nq - 1) umma_commit(empty + 2 * ahead % ST);
+                        if (ok) scores(q, i);
                     }
                 }
+                umma_commit(empty + i % ST);
+            }
+            for (int j = 0; j < nt && ok; ++j) {
+                const int i = j + NS, st = i % ST;
+                ok = bwait(full + st, (uint32_t)((i / ST) & 1), error);
+                const uint64_t vd = desc_mn(ring + st * 2 * kTile<D> + kTile<D>);
+                for (int q = 0; q < nq && ok; ++q) {
+                    if (!(ok = bwait(p_full + q * NS + j % NS, (uint32_t)((j / NS) & 1), error))) break;
+                    tc_fence_after();
+                    product_mn<32>(tmem + G::kColO + q * D, tmem + 128 * (q * NS + j % NS), vd, idO, j == nt - 1 ? last16 / 16 : 8, j > 0);
+                    if (NS == 2 || j == nt - 1) umma_commit(o_full + q);
+                    if (i < nt) scores(q, i);
+                }
+                umma_commit(empty + st);
             }
             umma_commit(done);
             bwait(done, 0u, error);
@@ -178,7 +175,8 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
         __syncwarp();
     } else {
         // ------------------------------------------------------------------ rows
-        const int q = warp >> 2, w4 = warp & 3;
+        // warp: tile q, columns 64 half .. + 63 of S, lanes 32 w4 .. + 31
+        const int q = warp >> 3, half = (warp >> 2) & 1, w4 = warp & 3;
         const int row = w4 * 32 + lane;                      // of the tile
         const int r = r0 + q * kRows + row;                  // of the key head
         const bool mine = r < p.rows;
@@ -186,21 +184,23 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
         uint8_t *sQ = sm + G::kQ + q * kTile<D>;
         // (not 0, so that a masked score stays -infinity; a scale of 0 leaves no trace of any finite one)
         const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);
-        constexpr int kLanes = D / 8;  // lanes of a row, 16 bytes each
+        // this warp's 32 rows by half of the columns, 16 bytes a lane
+        constexpr int kLanes = D / 16;
+        const int my_row = lane / kLanes, my_chunk = half * kLanes + lane % kLanes;
         if (nt > 0) {
-            // this warp's 32 rows of Q, negated for a negative scale
+            // Q, negated for a negative scale
             const long long at = mine ? cross_row(p, p.Q, b, kh, r) : -1;
             const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
             for (int i = 0; i < kLanes; ++i) {
-                const int rr = i * (32 / kLanes) + lane / kLanes, ch = lane % kLanes;
+                const int rr = i * (32 / kLanes) + my_row;
                 const long long o = __shfl_sync(0xffffffffu, at, rr);
                 uint4 x = make_uint4(0, 0, 0, 0);
-                if (o >= 0 && ch * 8 < p.d) {
-                    x = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.Q.ptr + o + ch * 8);
+                if (o >= 0 && my_chunk * 8 < p.d) {
+                    x = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.Q.ptr + o + my_chunk * 8);
                     x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
                 }
-                *reinterpret_cast<uint4 *>(sQ + chunk_at(w4 * 32 + rr, ch)) = x;
+                *reinterpret_cast<uint4 *>(sQ + chunk_at(w4 * 32 + rr, my_chunk)) = x;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -208,105 +208,121 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
         }
         const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
         const uint32_t tO = tmem + lanes + G::kColO + q * D;
-        float m = -INFINITY, l = 0.f;  // maximum in use (of c s) and sum
+        // the two halves of a row meet over its slots [parity][half], and over a barrier of their two warps
+        // (the maximum in bf16: any value near it will do, if the halves agree)
+        __nv_bfloat16 *ex = reinterpret_cast<__nv_bfloat16 *>(sm + G::kEx + q * 2 * kRows * 4) + row;
+        uint64_t *meet = pair + q * 4 + w4;
+        float m = -INFINITY, l = 0.f;  // maximum in use (of c s), and this half's sum
         bool ok = true;
         if (active && q < nq) {
             for (int j = 0; j < nt && ok; ++j) {
                 const int buf = q * NS + j % NS;
-                const uint32_t tS = tmem + lanes + 128 * buf;
+                const uint32_t tS = tmem + lanes + 128 * buf + 64 * half;
                 if (!bwait(s_full + buf, (uint32_t)((j / NS) & 1), error)) { ok = false; break; }
                 tc_fence_after();
-                const int keys = min(kRows, L - (t0 + j) * kRows);  // that count
-                const int ld = (keys + 31) / 32;                    // 32-column parts with one of them
-                float s[128];
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (x < ld) tmem_ld32(tS + 32 * x, s + 32 * x);
+                const int keys = min(kRows, L - (t0 + j) * kRows) - 64 * half;  // of this half that count (may be none)
+                float s[64];
+                tmem_ld32(tS, s);
+                if (keys > 32) tmem_ld32(tS + 32, s + 32);
                 tmem_ld_wait();
-                if (keys < kRows) {
+                if (keys < 64) {
 #pragma unroll
-                    for (int x = 0; x < 128; ++x)
+                    for (int x = 0; x < 64; ++x)
                         if (x >= keys) s[x] = -INFINITY;
                 }
                 float t8[8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x) t8[x] = max3_f32(s[x], s[8 + x], s[16 + x]);
 #pragma unroll
-                for (int y = 24; y < 120; y += 16)
+                for (int y = 24; y < 56; y += 16)
 #pragma unroll
                     for (int x = 0; x < 8; ++x) t8[x] = max3_f32(t8[x], s[y + x], s[y + 8 + x]);
 #pragma unroll
-                for (int x = 0; x < 8; ++x) t8[x] = fmaxf(t8[x], s[120 + x]);
-                const float top =
-                    c * fmaxf(max3_f32(t8[0], t8[1], t8[2]), max3_f32(t8[3], t8[4], max3_f32(t8[5], t8[6], t8[7])));
+                for (int x = 0; x < 8; ++x) t8[x] = fmaxf(t8[x], s[56 + x]);
+                float top = c * fmaxf(max3_f32(t8[0], t8[1], t8[2]), max3_f32(t8[3], t8[4], max3_f32(t8[5], t8[6], t8[7])));
+                __nv_bfloat16 *slot = ex + (j & 1) * 2 * kRows;
+                slot[half * kRows] = __float2bfloat16_rn(top);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(meet);
+                if (!bwait(meet, (uint32_t)(j & 1), error)) { ok = false; break; }
+                top = fmaxf(__bfloat162float(slot[0]), __bfloat162float(slot[kRows]));
                 if (j == 0) {
                     m = top;
                 } else {
                     const bool grows = top > m + kSlack;
                     if (__any_sync(0xffffffffu, grows)) {
-                        // O (complete up to the tile before) to the new maximum
-                        if (!bwait(o_full + q, (uint32_t)((j - 1) & 1), error)) { ok = false; break; }
+                        // this half of O's columns (complete up to the tile before) to the new maximum
+                        // (one S buffer: this S was issued after the product that O waits for)
+                        if (NS == 2 && !bwait(o_full + q, (uint32_t)((j - 1) & 1), error)) { ok = false; break; }
                         tc_fence_after();
                         const float f = grows ? ex2(m - top) : 1.f;
                         if (grows) m = top;
                         l *= f;
-                        float o[32];
 #pragma unroll 1
-                        for (int x = 0; x < D; x += 32) {
-                            tmem_ld32(tO + x, o);
+                        for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 8) {
+                            uint32_t o[8];
+                            tmem_ld8(tO + x, o);
                             tmem_ld_wait();
-                            uint32_t u[32];
 #pragma unroll
-                            for (int y = 0; y < 32; ++y) u[y] = __float_as_uint(o[y] * f);
-                            tmem_st32(tO + x, u);
+                            for (int y = 0; y < 8; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                            tmem_st8(tO + x, o);
                         }
                         tmem_st_wait();
                     }
                 }
                 const float shift = m == -INFINITY ? 0.f : m;
                 const uint64_t c2 = f32x2(c, c), m2 = f32x2(-shift, -shift);
-                uint64_t z[4] = {0, 0, 0, 0};
+                uint64_t z[2] = {0, 0};
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    if (x >= ld) break;
+                for (int x = 0; x < 2; ++x) {
                     uint32_t u[16];
 #pragma unroll
                     for (int y = 0; y < 16; ++y) {
                         float e0, e1;
                         f32x2_split(fma_f32x2(f32x2(s[32 * x + 2 * y], s[32 * x + 2 * y + 1]), c2, m2), e0, e1);
                         e0 = ex2(e0), e1 = ex2(e1);
-                        z[y & 3] = add_f32x2(z[y & 3], f32x2(e0, e1));
+                        z[y & 1] = add_f32x2(z[y & 1], f32x2(e0, e1));
                         u[y] = pack2(e0, e1);
                     }
-                    tmem_st16(tS + 16 * x, u);
+                    tmem_st16(tS + 16 * x, u);  // over columns that this warp has read
                 }
-                tmem_st_wait();
                 float za, zb;
-                f32x2_split(add_f32x2(add_f32x2(z[0], z[1]), add_f32x2(z[2], z[3])), za, zb);
+                f32x2_split(add_f32x2(z[0], z[1]), za, zb);
                 l += za + zb;
-                if (keys < kRows && L < p.s && q == 0) {
+                tmem_st_wait();
+                if (L < p.s && q == 0 && half == 0 && L - (t0 + j) * kRows < kRows) {
                     // the last tile's rows of V that do not count, once (the other tile's product comes later)
-                    const int i = 2 * j + 1, st = i % ST;
+                    const int i = j + NS, st = i % ST, from = L - (t0 + j) * kRows;
                     if (!bwait(full + st, (uint32_t)((i / ST) & 1), error)) { ok = false; break; }
                     const int warps = min((left + 31) / 32, 4);
-                    for (int t = row; t < kRows; t += 32 * warps) zero_rows<D>(sm + G::kRing + st * kTile<D>, t, keys, (keys + 15) / 16 * 16);
+                    for (int t = row; t < kRows; t += 32 * warps) zero_rows<D>(sm + G::kRing + (2 * st + 1) * kTile<D>, t, from, (from + 15) / 16 * 16);
                     fence_proxy_async_smem();
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + buf);
             }
-            if (ok && nt > 0) ok = bwait(o_full + q, (uint32_t)((nt - 1) & 1), error);
+            if (ok && nt > 0) {
+                // O, then the halves' sums (over the maxima, which all warps have read by then)
+                ok = bwait(o_full + q, (uint32_t)((NS == 2 ? nt - 1 : 0) & 1), error);
+                float *slot = reinterpret_cast<float *>(sm + G::kEx + q * 2 * kRows * 4) + row;
+                slot[half * kRows] = l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(meet);
+                ok = ok && bwait(meet, (uint32_t)(nt & 1), error);
+                l = slot[0] + slot[kRows];
+            }
             tc_fence_after();
         }
         if (active && q < nq && ok) {
             const long long f = cross_flat(p, b, kh, mine ? r : 0);
+            const int to = min(p.d, (half + 1) * (D / 2));
             if (a.w.parts > 1) {
                 const long long at = (long long)blockIdx.y * p.B * p.kv * p.rows + f;
-                if (mine) a.w.ml[at] = make_float2(nt > 0 ? m : -INFINITY, l);
+                if (mine && half == 0) a.w.ml[at] = make_float2(nt > 0 ? m : -INFINITY, l);
                 float o[32];
 #pragma unroll 1
-                for (int x = 0; x < p.d; x += 32) {
+                for (int x = half * (D / 2); x < to; x += 32) {
                     if (nt > 0) {
                         tmem_ld32(tO + x, o);
                         tmem_ld_wait();
@@ -321,11 +337,11 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                         if (x + 4 * y < p.d) dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
                 }
             } else {
-                // rows of H through this warp's rows of the Q tile (all scores have been taken)
+                // rows of H through this warp's rows and columns of the Q tile (all scores have been taken)
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 float o[32];
 #pragma unroll 1
-                for (int x = 0; x < p.d; x += 32) {
+                for (int x = half * (D / 2); x < to; x += 32) {
                     if (nt > 0) {
                         tmem_ld32(tO + x, o);
                         tmem_ld_wait();
@@ -345,13 +361,13 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                 const long long at = mine ? cross_row(p, p.H, b, kh, r) : -1;
 #pragma unroll
                 for (int i = 0; i < kLanes; ++i) {
-                    const int rr = i * (32 / kLanes) + lane / kLanes, ch = lane % kLanes;
-                    const long long to = __shfl_sync(0xffffffffu, at, rr);
-                    if (to >= 0 && ch * 8 < p.d)
-                        *reinterpret_cast<uint4 *>((__nv_bfloat16 *)p.H.ptr + to + ch * 8) =
-                            *reinterpret_cast<const uint4 *>(sQ + chunk_at(w4 * 32 + rr, ch));
+                    const int rr = i * (32 / kLanes) + my_row;
+                    const long long o = __shfl_sync(0xffffffffu, at, rr);
+                    if (o >= 0 && my_chunk * 8 < p.d)
+                        *reinterpret_cast<uint4 *>((__nv_bfloat16 *)p.H.ptr + o + my_chunk * 8) =
+                            *reinterpret_cast<const uint4 *>(sQ + chunk_at(w4 * 32 + rr, my_chunk));
                 }
-                if (p.lse && mine) p.lse[f] = l == 0.f ? -INFINITY : m * (1.f / kLog2e) + logf(l);
+                if (p.lse && mine && half == 0) p.lse[f] = l == 0.f ? -INFINITY : m * (1.f / kLog2e) + logf(l);
             }
         }
         tc_fence_before();

@@ -51,10 +51,10 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, u
         "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
         : "memory");
 }
-// rows [row, row + 128) of one head; rows and columns outside the tensor are zero
+// rows [row, row + 128) of one head; rows and columns outside the tensor are zero.  The caller has
+// announced kTile bytes on `bar`.
 template <int D>
 __device__ __forceinline__ void load_tile(uint8_t *dst, const TileMap &m, uint64_t *bar, int row, int head, int b) {
-    mbar_arrive_expect_tx(bar, kTile<D>);
 #pragma unroll
     for (int q = 0; q < D / 64; ++q) tma_load_4d(dst + q * kBlock, &m.map, bar, 64 * q, row, head * m.by_head, b * m.by_batch);
 }
@@ -69,6 +69,35 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t tile) { return smem_desc_sw
 __device__ __forceinline__ uint64_t step_k(int k) { return (uint64_t)(((k >> 2) * kBlock + (k & 3) * 32) >> 4); }
 __device__ __forceinline__ uint64_t step_mn(int k) { return (uint64_t)(k * 16 * 128 >> 4); }
 
+// Products issued by one thread.  A loop of known length is issued without a pause (descriptors
+// in registers ahead of time); with a length that is read at run time each product waited on the
+// address arithmetic of its own (128 cycles where the tensor pipe takes 64), so the common length
+// has a loop of its own.
+// to = A B^T: both tiles in shared memory, over `steps` 16s of their columns
+template <int D>
+__device__ __forceinline__ void product_k(uint32_t to, uint64_t a, uint64_t b, uint32_t id, int steps) {
+    if (steps == D / 16) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) umma_bf16(to, a + step_k(k), b + step_k(k), id, k > 0 ? 1u : 0u);
+    } else {
+#pragma unroll 1
+        for (int k = 0; k < steps; ++k) umma_bf16(to, a + step_k(k), b + step_k(k), id, k > 0 ? 1u : 0u);
+    }
+}
+// sum (+)= A B: A bf16 in tensor memory, its columns in runs of 2 R (R columns of 32 bits, at the
+// start of their own 2 R columns), B over `steps` 16s of its rows
+template <int R>
+__device__ __forceinline__ void product_mn(uint32_t sum, uint32_t a, uint64_t b, uint32_t id, int steps, bool add) {
+    auto at = [&](int k) { return a + (uint32_t)(8 * k / R * 2 * R + 8 * k % R); };
+    if (steps == kRows / 16) {
+#pragma unroll
+        for (int k = 0; k < kRows / 16; ++k) umma_bf16_tmem_a(sum, at(k), b + step_mn(k), id, k > 0 || add ? 1u : 0u);
+    } else {
+#pragma unroll 1
+        for (int k = 0; k < steps; ++k) umma_bf16_tmem_a(sum, at(k), b + step_mn(k), id, k > 0 || add ? 1u : 0u);
+    }
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -77,6 +106,18 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// 8 columns of a warp's 32 lanes, for paths that have few registers to spare
+__device__ __forceinline__ void tmem_ld8(uint32_t at, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 // zeros in rows [from, to) of a tile, one row per thread t of 128
