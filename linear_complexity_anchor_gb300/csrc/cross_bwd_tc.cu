@@ -111,9 +111,21 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
     // steps over the tiles that stream by: keys of the entry, or the queries of each head in turn
     const int per_head = (p.n + kRows - 1) / kRows;
     const int nt = KEYS ? (r0 < L ? p.group * per_head : 0) : (L + kRows - 1) / kRows;
-    // columns of step j that exist, and the same in 16s
-    auto width = [&](int j) { return KEYS ? min(kRows, p.n - (j % per_head) * kRows) : min(kRows, L - j * kRows); };
-    auto width16 = [&](int j) { return (width(j) + 15) / 16 * 16; };
+    // A walk over the steps: tile t of head g (without divisions, which the issuing thread would wait
+    // for).
+    struct Walk {
+        int t, g, per_head, group;
+        __device__ __forceinline__ void next() {
+            if (++t == per_head) {
+                t = 0;
+                if (++g == group) g = 0;
+            }
+        }
+    };
+    const int around = KEYS ? per_head : nt;
+    const Walk start{0, 0, around, KEYS ? p.group : 1};
+    // columns of a tile that exist
+    auto width = [&](int t) { return min(kRows, (KEYS ? p.n : L) - t * kRows); };
 
     if (warp == kLoad) {
         if (lane == 0 && nt > 0) {
@@ -122,32 +134,36 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
                 load_tile<D>(sm + G::kFix, a.fa, fix_full, r0, kh, b);
                 load_tile<D>(sm + G::kFix + kTile<D>, a.fb, fix_full, r0, kh, b);
             }
-            auto row_of = [&](int j) { return (KEYS ? j % per_head : j) * kRows; };
-            auto head_of = [&](int j) { return KEYS ? kh * p.group + j / per_head : kh; };
-            auto load_a = [&](int j) {
-                if (j >= nt) return;
-                mbar_arrive_expect_tx(a_full + j % NA, kTile<D>);
-                load_tile<D>(sm + G::kA + j % NA * kTile<D>, a.a, a_full + j % NA, row_of(j), head_of(j), b);
+            int ja = 0, jb = 0;  // steps whose tiles have been asked for
+            Walk wa = start, wb = start;
+            auto load_a = [&]() {
+                if (ja >= nt) return;
+                mbar_arrive_expect_tx(a_full + ja % NA, kTile<D>);
+                load_tile<D>(sm + G::kA + ja % NA * kTile<D>, a.a, a_full + ja % NA, wa.t * kRows, KEYS ? kh * p.group + wa.g : kh, b);
+                ++ja;
+                wa.next();
             };
-            auto load_b = [&](int j) {
-                if (j >= nt) return;
-                mbar_arrive_expect_tx(b_full + j % NB, kTile<D>);
-                load_tile<D>(sm + G::kB + j % NB * kTile<D>, a.b, b_full + j % NB, row_of(j), head_of(j), b);
+            auto load_b = [&]() {
+                if (jb >= nt) return;
+                mbar_arrive_expect_tx(b_full + jb % NB, kTile<D>);
+                load_tile<D>(sm + G::kB + jb % NB * kTile<D>, a.b, b_full + jb % NB, wb.t * kRows, KEYS ? kh * p.group + wb.g : kh, b);
+                ++jb;
+                wb.next();
             };
             for (int j = 0; j < NB; ++j) {
-                load_a(j);
-                load_b(j);
+                load_a();
+                load_b();
             }
-            load_a(NB);
+            load_a();
             int i = 0;  // steps that are done
             for (; i < nt - NB; ++i) {
                 if (!bwait(empty + i % NB, (uint32_t)((i / NB) & 1), error)) break;
-                load_b(i + NB);
-                load_a(i + NA);
+                load_b();
+                load_a();
             }
             // the CTA leaves only once its copies have landed
-            for (int j = i; j < min(nt, i + NA); ++j) bwait(a_full + j % NA, (uint32_t)((j / NA) & 1), error);
-            for (int j = i; j < min(nt, i + NB); ++j) bwait(b_full + j % NB, (uint32_t)((j / NB) & 1), error);
+            for (int j = max(0, ja - NA); j < ja; ++j) bwait(a_full + j % NA, (uint32_t)((j / NA) & 1), error);
+            for (int j = max(0, jb - NB); j < jb; ++j) bwait(b_full + j % NB, (uint32_t)((j / NB) & 1), error);
             if (KEYS) bwait(fix_full, 0u, error);
         }
         __syncwarp();
@@ -155,18 +171,20 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
         if (KEYS) {
             // lse (in log2) and D of each step's columns, read a step ahead; columns that do not exist: P = 0
             float next[8];
-            auto fetch = [&](int j) {
-                const int i0 = (j % per_head) * kRows;
-                const long long f = ((long long)b * p.heads + kh * p.group + j / per_head) * p.n + i0;
+            Walk w = start;
+            auto fetch = [&]() {
+                const int i0 = w.t * kRows;
+                const long long f = ((long long)b * p.heads + kh * p.group + w.g) * p.n + i0;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const bool in = j < nt && i0 + 32 * x + lane < p.n;
+                    const bool in = i0 + 32 * x + lane < p.n;
                     next[x] = in ? p.lse[f + 32 * x + lane] * kLog2e : INFINITY;
                     next[4 + x] = in ? a.delta[f + 32 * x + lane] : 0.f;
                 }
+                w.next();
             };
             bool ok = true;
-            if (nt > 0) fetch(0);
+            if (nt > 0) fetch();
             for (int j = 0; j < nt && ok; ++j) {
                 if (j > 0 && !(ok = bwait(lse_empty, (uint32_t)((j - 1) & 1), error))) break;
 #pragma unroll
@@ -178,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
                 for (int x = 0; x < 4; ++x) stat[kRows + 32 * x + lane] = next[4 + x];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(d_full);
-                if (j + 1 < nt) fetch(j + 1);
+                if (j + 1 < nt) fetch();
             }
         }
         __syncwarp();
@@ -194,38 +212,46 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
             auto slot_b = [&](int j) { return base + G::kB + j % NB * kTile<D>; };
             auto landed_a = [&](int j) { return bwait(a_full + j % NA, (uint32_t)((j / NA) & 1), error); };
             auto landed_b = [&](int j) { return bwait(b_full + j % NB, (uint32_t)((j / NB) & 1), error); };
-            // to = (a tile that stays) x (a tile of step j)^T
-            auto across = [&](uint32_t to, uint64_t fix, uint32_t tile, int j, uint64_t *bar) {
-                product_k<D>(to, fix, desc_k(tile), idesc_bf16_f32(kRows, width16(j), false, false), ksteps);
+            // columns of the walk's tiles in 16s: all but a head's (an entry's) last are full
+            const int last16 = (width(around - 1) + 15) / 16;
+            const uint32_t idF = idesc_bf16_f32(kRows, kRows, false, false), idL = idesc_bf16_f32(kRows, 16 * last16, false, false);
+            // to = (a tile that stays) x (a tile that streams by)^T
+            auto across = [&](uint32_t to, uint64_t fix, uint32_t tile, bool last, uint64_t *bar) {
+                product_k<D>(to, fix, desc_k(tile), last ? idL : idF, ksteps);
                 umma_commit(bar);
             };
-            // sum += (operand in tensor memory) x (a tile of step j)
-            auto along = [&](uint32_t sum, uint32_t op, uint32_t tile, int j) {
-                product_mn<kQuarter / 2>(sum, op, desc_mn(tile), idA, width16(j) / 16, j > 0);
+            // sum += (operand in tensor memory) x (a tile that streams by)
+            auto along = [&](uint32_t sum, uint32_t op, uint32_t tile, bool last, bool add) {
+                product_mn<kQuarter / 2>(sum, op, desc_mn(tile), idA, last ? last16 : 8, add);
             };
+            Walk w = start;
+            bool last = w.t == around - 1;
             bool ok = bwait(fix_full, 0u, error) && landed_a(0);
             tc_fence_after();
             if (ok) {
-                across(tmem + kColS, f0, slot_a(0), 0, s_full);
+                across(tmem + kColS, f0, slot_a(0), last, s_full);
                 ok = landed_b(0);
                 tc_fence_after();
-                if (ok) across(tmem + kColP, f1, slot_b(0), 0, dp_full);
+                if (ok) across(tmem + kColP, f1, slot_b(0), last, dp_full);
             }
             for (int j = 0; j < nt && ok; ++j) {
                 const bool more = j + 1 < nt;
+                w.next();
+                const bool then = w.t == around - 1;  // the next step's
                 // the rows have read S(j) (and left P^T(j) over it)
                 if (more && !(ok = landed_a(j + 1))) break;
                 if (!(ok = bwait(p_full, (uint32_t)(j & 1), error))) break;
                 tc_fence_after();
-                if (KEYS) along(tmem + kColA, tmem + kColS, slot_b(j), j);  // dV += P^T dH
-                if (more) across(tmem + kColS, f0, slot_a(j + 1), j + 1, s_full);
+                if (KEYS) along(tmem + kColA, tmem + kColS, slot_b(j), last, j > 0);  // dV += P^T dH
+                if (more) across(tmem + kColS, f0, slot_a(j + 1), then, s_full);
                 // the rows have left dS(j) over dP(j)
                 if (more && !(ok = landed_b(j + 1))) break;
                 if (!(ok = bwait(ds_full, (uint32_t)(j & 1), error))) break;
                 tc_fence_after();
-                along(tmem + kColA + (KEYS ? D : 0), tmem + kColP, slot_a(j), j);  // dK += dS^T Q, dQ += dS K
-                if (more) across(tmem + kColP, f1, slot_b(j + 1), j + 1, dp_full);
+                along(tmem + kColA + (KEYS ? D : 0), tmem + kColP, slot_a(j), last, j > 0);  // dK += dS^T Q, dQ += dS K
+                if (more) across(tmem + kColP, f1, slot_b(j + 1), then, dp_full);
                 umma_commit(empty + j % NB);
+                last = then;
             }
             if (ok) umma_commit(acc);
             umma_commit(done);
@@ -265,8 +291,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
         }
         const uint32_t tS = trow + kColS + kQuarter * quarter, tP = trow + kColP + kQuarter * quarter;
         bool ok = true;
-        for (int j = 0; j < nt && ok; ++j) {
-            const int cols = width(j) - kQuarter * quarter;  // of this quarter that exist (may be none)
+        Walk walk = start;
+        for (int j = 0; j < nt && ok; ++j, walk.next()) {
+            const int cols = width(walk.t) - kQuarter * quarter;  // of this quarter that exist (may be none)
             const float *st = stat + kQuarter * quarter;
             float e[32];
             if (!bwait(s_full, (uint32_t)(j & 1), error)) { ok = false; break; }
@@ -330,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
                 tmem_st16(tP, u);
             }
             tmem_st_wait();
-            if (!KEYS && j == nt - 1 && quarter == 0 && L % kRows && L < p.s) {
+            if (!KEYS && walk.t == nt - 1 && quarter == 0 && L % kRows && L < p.s) {
                 // the last tile's rows of K that do not count (S has read them)
                 if (!bwait(a_full + j % NA, (uint32_t)((j / NA) & 1), error)) { ok = false; break; }
                 zero_rows<D>(sm + G::kA + j % NA * kTile<D>, row, L % kRows, (L % kRows + 15) / 16 * 16);
