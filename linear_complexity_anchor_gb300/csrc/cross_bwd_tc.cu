@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
         __syncwarp();
     } else if (warp == kStat) {
         if (KEYS) {
-            // lse (in log2) and D of each step's columns, read a step ahead; columns that do not exist: P = 0
+            // - lse (in log2) and - D of each step's columns, read a step ahead; columns that do not exist: P = 0
             float next[8];
             Walk w = start;
             auto fetch = [&]() {
@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const bool in = i0 + 32 * x + lane < p.n;
-                    next[x] = in ? p.lse[f + 32 * x + lane] * kLog2e : INFINITY;
-                    next[4 + x] = in ? a.delta[f + 32 * x + lane] : 0.f;
+                    next[x] = in ? -p.lse[f + 32 * x + lane] * kLog2e : -INFINITY;
+                    next[4 + x] = in ? -a.delta[f + 32 * x + lane] : 0.f;
                 }
                 w.next();
             };
@@ -206,50 +206,57 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
             const uint32_t base = smem_u32(sm);
             const uint32_t idA = idesc_bf16_f32(kRows, p.d < D ? p.d : D, false, true);
             const uint64_t f0 = desc_k(base + G::kFix), f1 = desc_k(base + G::kFix + kTile<D>);
-            // (a commit takes this thread 70 cycles, a wait on a complete barrier 80: one barrier frees both
-            // tiles of a step, and what has to have landed is waited for before the rows are)
+            // (a commit takes this thread 70 cycles, a wait on a complete barrier 130: one barrier frees both
+            // tiles of a step, and that the next products' tiles have landed is looked at while these run)
             auto slot_a = [&](int j) { return base + G::kA + j % NA * kTile<D>; };
             auto slot_b = [&](int j) { return base + G::kB + j % NB * kTile<D>; };
-            auto landed_a = [&](int j) { return bwait(a_full + j % NA, (uint32_t)((j / NA) & 1), error); };
-            auto landed_b = [&](int j) { return bwait(b_full + j % NB, (uint32_t)((j / NB) & 1), error); };
+            uint64_t *const a_bar = a_full, *const b_bar = b_full;
+            auto a_par = [](int j) { return (uint32_t)((j / NA) & 1); };
+            auto b_par = [](int j) { return (uint32_t)((j / NB) & 1); };
             // columns of the walk's tiles in 16s: all but a head's (an entry's) last are full
             const int last16 = (width(around - 1) + 15) / 16;
             const uint32_t idF = idesc_bf16_f32(kRows, kRows, false, false), idL = idesc_bf16_f32(kRows, 16 * last16, false, false);
-            // to = (a tile that stays) x (a tile that streams by)^T
-            auto across = [&](uint32_t to, uint64_t fix, uint32_t tile, bool last, uint64_t *bar) {
-                product_k<D>(to, fix, desc_k(tile), last ? idL : idF, ksteps);
-                umma_commit(bar);
-            };
             // sum += (operand in tensor memory) x (a tile that streams by)
             auto along = [&](uint32_t sum, uint32_t op, uint32_t tile, bool last, bool add) {
                 product_mn<kQuarter / 2>(sum, op, desc_mn(tile), idA, last ? last16 : 8, add);
             };
             Walk w = start;
             bool last = w.t == around - 1;
-            bool ok = bwait(fix_full, 0u, error) && landed_a(0);
+            auto nothing = [] {};
+            bool ok = bwait(fix_full, 0u, error) && bwait(a_bar, 0u, error) && bwait(b_bar, 0u, error);
             tc_fence_after();
             if (ok) {
-                across(tmem + kColS, f0, slot_a(0), last, s_full);
-                ok = landed_b(0);
-                tc_fence_after();
-                if (ok) across(tmem + kColP, f1, slot_b(0), last, dp_full);
+                product_k<D>(tmem + kColS, f0, desc_k(slot_a(0)), last ? idL : idF, ksteps, nothing);
+                umma_commit(s_full);
+                product_k<D>(tmem + kColP, f1, desc_k(slot_b(0)), last ? idL : idF, ksteps, nothing);
+                umma_commit(dp_full);
             }
+            bool landed_a = false, landed_b = false;  // the next products' tiles, as seen during these
             for (int j = 0; j < nt && ok; ++j) {
                 const bool more = j + 1 < nt;
+                const uint32_t par = (uint32_t)(j & 1);
                 w.next();
                 const bool then = w.t == around - 1;  // the next step's
                 // the rows have read S(j) (and left P^T(j) over it)
-                if (more && !(ok = landed_a(j + 1))) break;
-                if (!(ok = bwait(p_full, (uint32_t)(j & 1), error))) break;
+                if (more && !landed_a && !(ok = bwait(a_bar + (j + 1) % NA, a_par(j + 1), error))) break;
+                if (!(ok = bwait_now(p_full, par, error))) break;
                 tc_fence_after();
                 if (KEYS) along(tmem + kColA, tmem + kColS, slot_b(j), last, j > 0);  // dV += P^T dH
-                if (more) across(tmem + kColS, f0, slot_a(j + 1), then, s_full);
+                if (more) {
+                    product_k<D>(tmem + kColS, f0, desc_k(slot_a(j + 1)), then ? idL : idF, ksteps,
+                                 [&] { landed_b = mbar_test(b_bar + (j + 1) % NB, b_par(j + 1)); });
+                    umma_commit(s_full);
+                }
                 // the rows have left dS(j) over dP(j)
-                if (more && !(ok = landed_b(j + 1))) break;
-                if (!(ok = bwait(ds_full, (uint32_t)(j & 1), error))) break;
+                if (more && !landed_b && !(ok = bwait(b_bar + (j + 1) % NB, b_par(j + 1), error))) break;
+                if (!(ok = bwait_now(ds_full, par, error))) break;
                 tc_fence_after();
                 along(tmem + kColA + (KEYS ? D : 0), tmem + kColP, slot_a(j), last, j > 0);  // dK += dS^T Q, dQ += dS K
-                if (more) across(tmem + kColP, f1, slot_b(j + 1), then, dp_full);
+                if (more) {
+                    product_k<D>(tmem + kColP, f1, desc_k(slot_b(j + 1)), then ? idL : idF, ksteps,
+                                 [&] { landed_a = mbar_test(a_bar + (j + 2) % NA, a_par(j + 2)); });
+                    umma_commit(dp_full);
+                }
                 umma_commit(empty + j % NB);
                 last = then;
             }
@@ -263,8 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
         const int quarter = warp >> 2, w4 = warp & 3, row = w4 * 32 + lane, r = r0 + row;
         const bool mine = r < (KEYS ? L : p.rows);  // a row that counts
         const uint32_t trow = tmem + ((uint32_t)(w4 * 32) << 16);
-        const float c = p.scale * kLog2e;
-        float lse2 = INFINITY, dl = 0.f;
+        const uint64_t c = f32x2(p.scale * kLog2e, p.scale * kLog2e);
+        uint64_t lse2 = f32x2(-INFINITY, -INFINITY), dl = 0;  // - lse (in log2) and - D of this row, twice
         if (!KEYS && nt > 0) {
             // quarters 0 and 1 load the 128 rows of Q, by halves of the columns, 2 and 3 those of dH
             constexpr int kLanes = D / 16;
@@ -285,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
             if (lane == 0) mbar_arrive(fix_full);
             if (mine) {
                 const long long f = cross_flat(p, b, kh, r);
-                lse2 = p.lse[f] * kLog2e;
-                dl = a.delta[f];
+                const float x = -p.lse[f] * kLog2e, y = -a.delta[f];
+                lse2 = f32x2(x, x), dl = f32x2(y, y);
             }
         }
         const uint32_t tS = trow + kColS + kQuarter * quarter, tP = trow + kColP + kQuarter * quarter;
@@ -296,19 +303,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
             const int cols = width(walk.t) - kQuarter * quarter;  // of this quarter that exist (may be none)
             const float *st = stat + kQuarter * quarter;
             float e[32];
-            if (!bwait(s_full, (uint32_t)(j & 1), error)) { ok = false; break; }
-            if (KEYS && !bwait(lse_full, (uint32_t)(j & 1), error)) { ok = false; break; }
+            if (!bwait_now(s_full, (uint32_t)(j & 1), error)) { ok = false; break; }
+            if (KEYS && !bwait_now(lse_full, (uint32_t)(j & 1), error)) { ok = false; break; }
             tc_fence_after();
             tmem_ld32(tS, e);
             tmem_ld_wait();
 #pragma unroll
             for (int x = 0; x < 32; x += 4) {
-                float4 s4 = make_float4(lse2, lse2, lse2, lse2);
-                if (KEYS) s4 = *reinterpret_cast<const float4 *>(st + x);
-                e[x] = ex2(fmaf(e[x], c, -s4.x));
-                e[x + 1] = ex2(fmaf(e[x + 1], c, -s4.y));
-                e[x + 2] = ex2(fmaf(e[x + 2], c, -s4.z));
-                e[x + 3] = ex2(fmaf(e[x + 3], c, -s4.w));
+                ulonglong2 s4 = make_ulonglong2(lse2, lse2);
+                if (KEYS) s4 = *reinterpret_cast<const ulonglong2 *>(st + x);
+                f32x2_split(fma_f32x2(f32x2(e[x], e[x + 1]), c, s4.x), e[x], e[x + 1]);
+                f32x2_split(fma_f32x2(f32x2(e[x + 2], e[x + 3]), c, s4.y), e[x + 2], e[x + 3]);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) e[x + y] = ex2(e[x + y]);
             }
             const bool cut = !mine || (!KEYS && cols < 32);
             if (cut) {
@@ -330,8 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
                 mbar_arrive(p_full);
             }
             // dS
-            if (KEYS && !bwait(d_full, (uint32_t)(j & 1), error)) { ok = false; break; }
-            if (!bwait(dp_full, (uint32_t)(j & 1), error)) { ok = false; break; }
+            if (KEYS && !bwait_now(d_full, (uint32_t)(j & 1), error)) { ok = false; break; }
+            if (!bwait_now(dp_full, (uint32_t)(j & 1), error)) { ok = false; break; }
             tc_fence_after();
             {
                 float g[32];
@@ -340,12 +347,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
                 tmem_ld_wait();
 #pragma unroll
                 for (int y = 0; y < 32; y += 4) {
-                    float4 d4 = make_float4(dl, dl, dl, dl);
-                    if (KEYS) d4 = *reinterpret_cast<const float4 *>(st + kRows + y);
-                    g[y] = e[y] * (g[y] - d4.x);
-                    g[y + 1] = e[y + 1] * (g[y + 1] - d4.y);
-                    g[y + 2] = e[y + 2] * (g[y + 2] - d4.z);
-                    g[y + 3] = e[y + 3] * (g[y + 3] - d4.w);
+                    ulonglong2 d4 = make_ulonglong2(dl, dl);
+                    if (KEYS) d4 = *reinterpret_cast<const ulonglong2 *>(st + kRows + y);
+                    f32x2_split(mul_f32x2(f32x2(e[y], e[y + 1]), add_f32x2(f32x2(g[y], g[y + 1]), d4.x)), g[y], g[y + 1]);
+                    f32x2_split(mul_f32x2(f32x2(e[y + 2], e[y + 3]), add_f32x2(f32x2(g[y + 2], g[y + 3]), d4.y)), g[y + 2], g[y + 3]);
                 }
                 if (cut) {  // (a masked state's dP may be anything: zero by select, not by the product)
 #pragma unroll
@@ -359,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
             tmem_st_wait();
             if (!KEYS && walk.t == nt - 1 && quarter == 0 && L % kRows && L < p.s) {
                 // the last tile's rows of K that do not count (S has read them)
-                if (!bwait(a_full + j % NA, (uint32_t)((j / NA) & 1), error)) { ok = false; break; }
+                if (!bwait_now(a_full + j % NA, (uint32_t)((j / NA) & 1), error)) { ok = false; break; }
                 zero_rows<D>(sm + G::kA + j % NA * kTile<D>, row, L % kRows, (L % kRows + 15) / 16 * 16);
                 fence_proxy_async_smem();
             }
@@ -370,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
                 mbar_arrive(ds_full);
             }
         }
-        if (ok && nt > 0) ok = bwait(acc, 0u, error);
+        if (ok && nt > 0) ok = bwait_now(acc, 0u, error);
         tc_fence_after();
         // Rows out through shared memory (the tiles that stayed are not needed any more).  Keys: quarters
         // 0 and 1 halves of dV's columns, 2 and 3 of dK's; queries: quarters of dQ's at d = 128, halves

@@ -130,20 +130,19 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
         __syncwarp();
     } else if (warp == kIssue) {
         if (lane == 0 && nt > 0) {
-            // Between products this thread is what the tensor cores wait for: a commit takes it 70 cycles
-            // and a wait on a barrier that is already complete 80, so K and V of a step share a
-            // stage, and nothing is committed that nobody waits for.
+            // A tile's rows wait for S, this thread for their P, the rows for the next S: that round is
+            // what a step takes, so between a P and its products there is nothing to do here but the wait
+            // for it.  (A commit takes 70 cycles, a wait on a complete barrier 130.)  That the step's K
+            // and V, in one stage, have landed is seen behind products.
             const int ksteps = (p.d + 15) / 16;
             const uint32_t base = smem_u32(sm), ring = base + G::kRing;
             const uint32_t idO = idesc_bf16_f32(kRows, p.d < D ? p.d : D, false, true);
             const uint32_t idS = idesc_bf16_f32(kRows, kRows, false, false);
             const int last16 = (min(kRows, L - (t0 + nt - 1) * kRows) + 15) / 16 * 16;  // keys of the last tile, in 16s
             const uint32_t idL = idesc_bf16_f32(kRows, last16, false, false);
-            auto scores = [&](int q, int i) {  // S of tile i (its K has landed)
-                product_k<D>(tmem + 128 * (q * NS + i % NS), desc_k(base + G::kQ + q * kTile<D>), desc_k(ring + i % ST * 2 * kTile<D>),
-                             i == nt - 1 ? idL : idS, ksteps);
-                umma_commit(s_full + q * NS + i % NS);
-            };
+            const uint64_t qd0 = desc_k(base + G::kQ), kd0 = desc_k(ring), vd0 = desc_mn(ring + kTile<D>);
+            constexpr uint64_t kStep = 2 * kTile<D> / 16, kNextQ = kTile<D> / 16;  // of descriptors
+            auto nothing = [] {};
             bool ok = true;
             for (int i = 0; i < NS && ok; ++i) {
                 if (i < nt) {
@@ -151,21 +150,32 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                     for (int q = 0; q < nq && ok; ++q) {
                         if (i == 0) ok = bwait(q_full + q, 0u, error);
                         tc_fence_after();
-                        if (ok) scores(q, i);
+                        if (!ok) break;
+                        product_k<D>(tmem + 128 * (q * NS + i), qd0 + q * kNextQ, kd0 + (i % ST) * kStep, i == nt - 1 ? idL : idS, ksteps, nothing);
+                        umma_commit(s_full + q * NS + i);
                     }
                 }
                 umma_commit(empty + i % ST);
             }
+            bool landed = false;  // this step's stage, as seen during the step before
             for (int j = 0; j < nt && ok; ++j) {
-                const int i = j + NS, st = i % ST;
-                ok = bwait(full + st, (uint32_t)((i / ST) & 1), error);
-                const uint64_t vd = desc_mn(ring + st * 2 * kTile<D> + kTile<D>);
-                for (int q = 0; q < nq && ok; ++q) {
-                    if (!(ok = bwait(p_full + q * NS + j % NS, (uint32_t)((j / NS) & 1), error))) break;
+                const int i = j + NS, st = i % ST, steps = j == nt - 1 ? last16 / 16 : 8;
+                const uint64_t vd = vd0 + st * kStep, kd = kd0 + st * kStep;
+                const uint32_t par = (uint32_t)((j / NS) & 1), id = i == nt - 1 ? idL : idS;
+                if (!landed && !(ok = bwait(full + st, (uint32_t)((i / ST) & 1), error))) break;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    if (q >= nq) break;
+                    const uint32_t S = tmem + 128 * (q * NS + j % NS);
+                    if (!(ok = bwait_now(p_full + q * NS + j % NS, par, error))) break;
                     tc_fence_after();
-                    product_mn<32>(tmem + G::kColO + q * D, tmem + 128 * (q * NS + j % NS), vd, idO, j == nt - 1 ? last16 / 16 : 8, j > 0);
+                    product_mn<32>(tmem + G::kColO + q * D, S, vd, idO, steps, j > 0);
                     if (NS == 2 || j == nt - 1) umma_commit(o_full + q);
-                    if (i < nt) scores(q, i);
+                    if (i >= nt) continue;
+                    product_k<D>(S, qd0 + q * kNextQ, kd, id, ksteps, [&] {
+                        if (q == nq - 1) landed = mbar_test(full + (i + 1) % ST, (uint32_t)(((i + 1) / ST) & 1));
+                    });
+                    umma_commit(s_full + q * NS + j % NS);
                 }
                 umma_commit(empty + st);
             }
@@ -218,7 +228,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
             for (int j = 0; j < nt && ok; ++j) {
                 const int buf = q * NS + j % NS;
                 const uint32_t tS = tmem + lanes + 128 * buf + 64 * half;
-                if (!bwait(s_full + buf, (uint32_t)((j / NS) & 1), error)) { ok = false; break; }
+                if (!bwait_now(s_full + buf, (uint32_t)((j / NS) & 1), error)) { ok = false; break; }
                 tc_fence_after();
                 const int keys = min(kRows, L - (t0 + j) * kRows) - 64 * half;  // of this half that count (may be none)
                 float s[64];
@@ -244,7 +254,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                 slot[half * kRows] = __float2bfloat16_rn(top);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(meet);
-                if (!bwait(meet, (uint32_t)(j & 1), error)) { ok = false; break; }
+                if (!bwait_now(meet, (uint32_t)(j & 1), error)) { ok = false; break; }
                 top = fmaxf(__bfloat162float(slot[0]), __bfloat162float(slot[kRows]));
                 if (j == 0) {
                     m = top;
@@ -253,7 +263,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                     if (__any_sync(0xffffffffu, grows)) {
                         // this half of O's columns (complete up to the tile before) to the new maximum
                         // (one S buffer: this S was issued after the product that O waits for)
-                        if (NS == 2 && !bwait(o_full + q, (uint32_t)((j - 1) & 1), error)) { ok = false; break; }
+                        if (NS == 2 && !bwait_now(o_full + q, (uint32_t)((j - 1) & 1), error)) { ok = false; break; }
                         tc_fence_after();
                         const float f = grows ? ex2(m - top) : 1.f;
                         if (grows) m = top;
@@ -293,7 +303,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                 if (L < p.s && q == 0 && half == 0 && L - (t0 + j) * kRows < kRows) {
                     // the last tile's rows of V that do not count, once (the other tile's product comes later)
                     const int i = j + NS, st = i % ST, from = L - (t0 + j) * kRows;
-                    if (!bwait(full + st, (uint32_t)((i / ST) & 1), error)) { ok = false; break; }
+                    if (!bwait_now(full + st, (uint32_t)((i / ST) & 1), error)) { ok = false; break; }
                     const int warps = min((left + 31) / 32, 4);
                     for (int t = row; t < kRows; t += 32 * warps) zero_rows<D>(sm + G::kRing + (2 * st + 1) * kTile<D>, t, from, (from + 15) / 16 * 16);
                     fence_proxy_async_smem();
@@ -304,12 +314,12 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
             }
             if (ok && nt > 0) {
                 // O, then the halves' sums (over the maxima, which all warps have read by then)
-                ok = bwait(o_full + q, (uint32_t)((NS == 2 ? nt - 1 : 0) & 1), error);
+                ok = bwait_now(o_full + q, (uint32_t)((NS == 2 ? nt - 1 : 0) & 1), error);
                 float *slot = reinterpret_cast<float *>(sm + G::kEx + q * 2 * kRows * 4) + row;
                 slot[half * kRows] = l;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(meet);
-                ok = ok && bwait(meet, (uint32_t)(nt & 1), error);
+                ok = ok && bwait_now(meet, (uint32_t)(nt & 1), error);
                 l = slot[0] + slot[kRows];
             }
             tc_fence_after();

@@ -44,6 +44,20 @@ __device__ __forceinline__ bool bwait(uint64_t *bar, uint32_t parity, unsigned i
     return true;
 }
 
+// the same, with a try that does not sleep first (what the row warps wait for is often there)
+__device__ __forceinline__ bool bwait_now(uint64_t *bar, uint32_t parity, unsigned int *error) {
+    return mbar_try_wait(bar, parity) || bwait(bar, parity, error);
+}
+// whether a phase is complete, without waiting
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2, int c3) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
@@ -73,15 +87,21 @@ __device__ __forceinline__ uint64_t step_mn(int k) { return (uint64_t)(k * 16 * 
 // in registers ahead of time); with a length that is read at run time each product waited on the
 // address arithmetic of its own (128 cycles where the tensor pipe takes 64), so the common length
 // has a loop of its own.
-// to = A B^T: both tiles in shared memory, over `steps` 16s of their columns
-template <int D>
-__device__ __forceinline__ void product_k(uint32_t to, uint64_t a, uint64_t b, uint32_t id, int steps) {
+// to = A B^T: both tiles in shared memory, over `steps` 16s of their columns.  `meanwhile` runs
+// behind the second product: the tensor pipe holds about two, so what takes the thread a hundred
+// cycles costs nothing there.
+template <int D, typename F>
+__device__ __forceinline__ void product_k(uint32_t to, uint64_t a, uint64_t b, uint32_t id, int steps, F meanwhile) {
     if (steps == D / 16) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) umma_bf16(to, a + step_k(k), b + step_k(k), id, k > 0 ? 1u : 0u);
+        for (int k = 0; k < D / 16; ++k) {
+            umma_bf16(to, a + step_k(k), b + step_k(k), id, k > 0 ? 1u : 0u);
+            if (k == 1) meanwhile();
+        }
     } else {
 #pragma unroll 1
         for (int k = 0; k < steps; ++k) umma_bf16(to, a + step_k(k), b + step_k(k), id, k > 0 ? 1u : 0u);
+        meanwhile();
     }
 }
 // sum (+)= A B: A bf16 in tensor memory, its columns in runs of 2 R (R columns of 32 bits, at the
