@@ -3,46 +3,46 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
-from ._views import Launch, View, check, empty_like, rows_dtype, view
+import torch
 
+from ._views import NO_VIEW, VIEW, Launch, empty_like, fail, library, rows_dtype, view
 
-class _Cross(ctypes.Structure):
-    _fields_ = [("dtype", ctypes.c_int), ("B", ctypes.c_int), ("heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
-                ("n", ctypes.c_int), ("s", ctypes.c_int), ("d", ctypes.c_int), ("scale", ctypes.c_float),
-                ("Q", View), ("K", View), ("V", View), ("H", View), ("dH", View), ("dQ", View), ("dK", View),
-                ("dV", View), ("lse", ctypes.c_void_p), ("lengths", ctypes.c_void_p)]
+# anchor_attn_cross_t: dtype, B, heads, kv_heads, n, s, d, scale; Q, K, V, H, dH, dQ, dK, dV; lse, lengths
+_pack = struct.Struct("=7if" + 8 * VIEW + "QQ").pack
 
 
 def bind(lib) -> None:
     for name in ("anchor_attn_cross_forward", "anchor_attn_cross_backward"):
         fn = getattr(lib, name)
-        fn.argtypes = [ctypes.POINTER(_Cross), ctypes.c_void_p]
+        fn.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
         fn.restype = ctypes.c_int
 
 
 def _problem(Q, K, V, lengths, scale):
-    import torch
-    check(Q, "Q")
-    check(K, "K", Q)
-    check(V, "V", Q)
+    """The structure's numbers, its views of Q, K and V, and the lengths' pointer."""
+    kind = rows_dtype(Q, "Q")
+    dtype, device = Q.dtype, Q.device
+    views = (*view(Q, "Q", dtype, device), *view(K, "K", dtype, device), *view(V, "V", dtype, device))
     B, heads, n, d = Q.shape
-    if K.shape[0] != B or K.shape[3] != d or V.shape != K.shape:
+    Bk, kv, s, dk = shape = K.shape
+    if Bk != B or dk != d or V.shape != shape:
         raise ValueError("Q is [B, heads, n, d]; K and V are [B, kv_heads, s, d]")
-    p = _Cross(rows_dtype(Q, "Q"), B, heads, K.shape[1], n, K.shape[2], d, 1.0 / math.sqrt(d) if scale is None else scale,
-               view(Q), view(K), view(V))
+    at = 0
     if lengths is not None:
-        if not isinstance(lengths, torch.Tensor) or lengths.dtype != torch.int32:
+        if not isinstance(lengths, torch.Tensor) or lengths.dtype is not torch.int32:
             raise TypeError("lengths must be an int32 tensor")
-        if lengths.device != Q.device or tuple(lengths.shape) != (B,) or not lengths.is_contiguous():
-            raise ValueError(f"lengths must be dense, [{B}], on {Q.device}")
-        p.lengths = lengths.data_ptr()
-    return p
+        if lengths.device != device or lengths.shape != (B,) or not lengths.is_contiguous():
+            raise ValueError(f"lengths must be dense, [{B}], on {device}")
+        at = lengths.data_ptr()
+    return (kind, B, heads, kv, n, s, d, 1.0 / math.sqrt(d) if scale is None else scale), views, at
 
 
-def _call(fn: str, p, handle) -> None:
-    from . import _raise, load
-    _raise(getattr(load(), fn)(ctypes.byref(p), handle), fn)
+def _call(fn: str, packed: bytes, handle: int) -> None:
+    st = getattr(library(), fn)(packed, handle)
+    if st:
+        fail(st, fn)
 
 
 def cross_forward(Q, K, V, lengths=None, *, H=None, scale: float | None = None, return_lse: bool = False, stream=None):
@@ -53,21 +53,17 @@ def cross_forward(Q, K, V, lengths=None, *, H=None, scale: float | None = None, 
     states.  An entry of length 0 has H = 0.  scale defaults to 1/sqrt(d).  Returns H [B, heads, n, d] in Q's order of
     axes, and with return_lse the logarithm of each row's sum, fp32 [B, heads, n], which ``cross_backward`` takes.
     Asynchronous on ``stream`` or the current stream."""
-    import torch
-    p = _problem(Q, K, V, lengths, scale)
+    numbers, views, at_lengths = _problem(Q, K, V, lengths, scale)
     at, lse = Launch(Q.device, stream), None
     with at as handle:
         if H is None:
             H = empty_like(Q)
-        else:
-            check(H, "H", Q)
-            if H.shape != Q.shape:
-                raise ValueError("H must have Q's shape")
-        p.H = view(H)
+        elif isinstance(H, torch.Tensor) and H.shape != Q.shape:
+            raise ValueError("H must have Q's shape")
         if return_lse:
             lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
-            p.lse = lse.data_ptr()
-        _call("anchor_attn_cross_forward", p, handle)
+        _call("anchor_attn_cross_forward", _pack(*numbers, *views, *view(H, "H", Q.dtype, Q.device), *NO_VIEW, *NO_VIEW, *NO_VIEW, *NO_VIEW,
+                                                 lse.data_ptr() if return_lse else 0, at_lengths), handle)
     at.used((Q, K, V, lengths), (H, lse))
     return (H, lse) if return_lse else H
 
@@ -76,20 +72,20 @@ def cross_backward(Q, K, V, H, lse, dH, lengths=None, *, scale: float | None = N
     """(dQ, dK, dV) for the upstream gradient dH of ``cross_forward``'s H; H and lse are its results for the same
     Q, K, V, lengths and scale.  Rows of dK and dV from an entry's length on are zero.  K or V that entries share by
     an expanded axis get a gradient for each entry."""
-    import torch
-    p = _problem(Q, K, V, lengths, scale)
-    for t, name in ((H, "H"), (dH, "dH")):
-        check(t, name, Q)
-        if t.shape != Q.shape:
-            raise ValueError(f"{name} must have Q's shape")
-    if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or lse.device != Q.device:
-        raise TypeError(f"lse must be a float32 tensor on {Q.device}")
-    if lse.shape != Q.shape[:3] or not lse.is_contiguous():
+    numbers, views, at_lengths = _problem(Q, K, V, lengths, scale)
+    dtype, device, shape = Q.dtype, Q.device, Q.shape
+    views += (*view(H, "H", dtype, device), *view(dH, "dH", dtype, device))
+    if H.shape != shape or dH.shape != shape:
+        raise ValueError("H and dH must have Q's shape")
+    if not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32 or lse.device != device:
+        raise TypeError(f"lse must be a float32 tensor on {device}")
+    if lse.shape != shape[:3] or not lse.is_contiguous():
         raise ValueError("lse must be dense, [B, heads, n]")
-    at = Launch(Q.device, stream)
+    at = Launch(device, stream)
     with at as handle:
         dQ, dK, dV = empty_like(Q), empty_like(K), empty_like(V)
-        p.H, p.dH, p.dQ, p.dK, p.dV, p.lse = view(H), view(dH), view(dQ), view(dK), view(dV), lse.data_ptr()
-        _call("anchor_attn_cross_backward", p, handle)
+        for t, name in ((dQ, "dQ"), (dK, "dK"), (dV, "dV")):
+            views += view(t, name, dtype, device)
+        _call("anchor_attn_cross_backward", _pack(*numbers, *views, lse.data_ptr(), at_lengths), handle)
     at.used((Q, K, V, H, lse, dH, lengths), (dQ, dK, dV))
     return dQ, dK, dV

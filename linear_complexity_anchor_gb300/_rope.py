@@ -3,9 +3,12 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import NamedTuple
 
-from ._views import NO_VIEW, Launch, View, check, empty_like, rows_dtype, view
+import torch
+
+from ._views import NO_VIEW, VIEW, Launch, empty_like, fail, library, rows_dtype, view
 
 
 class RopeTable(NamedTuple):
@@ -15,23 +18,16 @@ class RopeTable(NamedTuple):
     magnitude: float = 1.0
 
 
-class _Rope(ctypes.Structure):
-    _fields_ = [("dtype", ctypes.c_int), ("d", ctypes.c_int), ("rot", ctypes.c_int), ("axes", ctypes.c_int),
-                ("interleaved", ctypes.c_int), ("norm", ctypes.c_int), ("weight_f32", ctypes.c_int),
-                ("positions64", ctypes.c_int), ("eps", ctypes.c_float), ("magnitude", ctypes.c_float),
-                ("phases", ctypes.c_void_p)]
-
-
-class _Rows(ctypes.Structure):
-    _fields_ = [("X", View), ("Y", View), ("dY", View), ("dX", View), ("weight", ctypes.c_void_p),
-                ("dweight", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("positions_batch", ctypes.c_longlong),
-                ("start", ctypes.c_longlong), ("B", ctypes.c_int), ("heads", ctypes.c_int), ("n", ctypes.c_int)]
+# anchor_attn_rope_t: dtype, d, rot, axes, interleaved, norm, weight_f32, positions64; eps, magnitude; phases
+_pack_how = struct.Struct("=8i2fQ").pack
+# anchor_attn_rows_t: X, Y, dY, dX; weight, dweight, positions; positions_batch, start; B, heads, n
+_pack_rows = struct.Struct("=" + 4 * VIEW + "QQQqq3i4x").pack
 
 
 def bind(lib) -> None:
     for name in ("anchor_attn_norm_rope", "anchor_attn_norm_rope_backward"):
         fn = getattr(lib, name)
-        fn.argtypes = [ctypes.POINTER(_Rope), ctypes.POINTER(_Rows), ctypes.POINTER(_Rows), ctypes.c_void_p]
+        fn.argtypes = [ctypes.c_void_p] * 4
         fn.restype = ctypes.c_int
 
 
@@ -83,7 +79,6 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str | None = N
 
 def rope_table(rot: int, base: float = 10000.0, *, device="cuda", **how) -> RopeTable:
     """The table that ``rope`` and ``norm_rope`` take, for ``rope_frequencies(rot, base, **how)``; made once."""
-    import torch
     theta, magnitude = rope_frequencies(rot, base, **how)
     turns = [[int(round(t / (2 * math.pi) * 2 ** 64)) % 2 ** 64 for t in row] for row in theta]
     signed = [[t - 2 ** 64 if t >= 2 ** 63 else t for t in row] for row in turns]
@@ -91,80 +86,83 @@ def rope_table(rot: int, base: float = 10000.0, *, device="cuda", **how) -> Rope
 
 
 def _how(x, table, interleaved, norm, eps, weights, positions):
-    import torch
-    how = _Rope(dtype=rows_dtype(x, "the rows"), d=x.size(-1), axes=1, interleaved=1 if interleaved else 0, norm=norm, eps=eps,
-                magnitude=1.0)
+    """The packed anchor_attn_rope_t, and (d, rot, axes)."""
+    kind = rows_dtype(x, "the rows")
+    axes, rot, magnitude, at = 1, 0, 1.0, 0
     if table is not None:
         phases, magnitude = table
-        check(phases, "the table's phases", dim=2)
-        if phases.dtype != torch.int64 or not phases.is_contiguous():
-            raise TypeError("the table's phases must be contiguous int64")
+        if not isinstance(phases, torch.Tensor) or phases.dtype is not torch.int64 or phases.dim() != 2 or not phases.is_contiguous():
+            raise TypeError("the table's phases must be a contiguous int64 tensor [axes, rot / 2]")
         if phases.device != x.device:
             raise ValueError(f"the table must be on {x.device}")
-        how.axes, how.rot, how.magnitude, how.phases = phases.size(0), 2 * phases.size(1), magnitude, phases.data_ptr()
-    kinds = {p.dtype for p in positions if p is not None}
-    if kinds:
-        if len(kinds) > 1 or kinds - {torch.int32, torch.int64}:
-            raise TypeError("positions must be int32 or int64, of one type")
-        how.positions64 = 1 if torch.int64 in kinds else 0
-    kinds = {w.dtype for w in weights if w is not None}
-    if kinds:
-        if len(kinds) > 1 or kinds - {x.dtype, torch.float32}:
-            raise TypeError("weights must be of the rows' type or float32, and of one type")
-        how.weight_f32 = 1 if torch.float32 in kinds else 0
-    return how
+        axes, rot = phases.shape
+        rot, at = 2 * rot, phases.data_ptr()
+    wide = long = -1  # not yet known
+    for p in positions:
+        if p is not None:
+            here = 1 if p.dtype is torch.int64 else 0
+            if (not here and p.dtype is not torch.int32) or long == 1 - here:
+                raise TypeError("positions must be int32 or int64, of one type")
+            long = here
+    for w in weights:
+        if w is not None:
+            here = 1 if w.dtype is torch.float32 else 0
+            if (not here and w.dtype is not x.dtype) or wide == 1 - here:
+                raise TypeError("weights must be of the rows' type or float32, and of one type")
+            wide = here
+    d = x.shape[-1]
+    return _pack_how(kind, d, rot, axes, 1 if interleaved else 0, norm, max(wide, 0), max(long, 0), eps, magnitude, at), (d, rot, axes)
 
 
-def _rows(how, x, positions, start, weight, name):
-    B, heads, n, d = x.shape
-    if d != how.d:
-        raise ValueError(f"{name} must have heads of {how.d}, got {d}")
-    r = _Rows(X=NO_VIEW, Y=NO_VIEW, dY=NO_VIEW, dX=NO_VIEW, start=int(start), B=B, heads=heads, n=n)
-    if positions is not None and how.rot:
-        last = () if how.axes == 1 else (how.axes,)
-        shape = tuple(positions.shape)
-        if shape not in ((n, *last), (B, n, *last)):
-            raise ValueError(f"positions of {name} must be {[n, *last]} or {[B, n, *last]}, got {list(shape)}")
-        if not positions.is_cuda or positions.device != x.device:
-            raise ValueError(f"positions must be on {x.device}")
+def _rows(size, like, X, Y, dY, dX, shape, positions, start, weight, dweight, name):
+    """The packed anchor_attn_rows_t of one tensor of this shape; X ... dX are its views."""
+    d, rot, axes = size
+    B, heads, n, width = shape
+    if width != d:
+        raise ValueError(f"{name} must have heads of {d}, got {width}")
+    at = batch = 0
+    if positions is not None and rot:
+        last = () if axes == 1 else (axes,)
+        of = positions.shape
+        if of == (B, n, *last):
+            batch = n * axes
+        elif of != (n, *last):
+            raise ValueError(f"positions of {name} must be {[n, *last]} or {[B, n, *last]}, got {list(of)}")
+        if positions.device != like.device:
+            raise ValueError(f"positions must be on {like.device}")
         if not positions.is_contiguous():
             raise ValueError("positions must be contiguous")
-        r.positions = positions.data_ptr()
-        r.positions_batch = n * how.axes if len(shape) == 2 + len(last) else 0
-    if weight is not None:
-        check(weight, f"the weight of {name}", dim=1)
-        if weight.size(0) != d or weight.device != x.device:
-            raise ValueError(f"the weight of {name} must be [{d}] on {x.device}")
-        r.weight = weight.data_ptr()
-    return r
+        at = positions.data_ptr()
+    if weight is not None and (weight.shape != (d,) or weight.device != like.device or not weight.is_contiguous()):
+        raise ValueError(f"the weight of {name} must be dense, [{d}], on {like.device}")
+    return _pack_rows(*X, *Y, *dY, *dX, 0 if weight is None else weight.data_ptr(), 0 if dweight is None else dweight.data_ptr(),
+                      at, batch, start, B, heads, n)
 
 
-def _call(fn: str, how, first, second, handle) -> None:
-    from . import _raise, load
-    st = getattr(load(), fn)(ctypes.byref(how), ctypes.byref(first), ctypes.byref(second) if second is not None else None, handle)
-    _raise(st, fn)
+def _call(fn: str, how: bytes, first: bytes, second, handle: int) -> None:
+    st = getattr(library(), fn)(how, first, second, handle)
+    if st:
+        fail(st, fn)
 
 
 def _forward(X, table, positions, starts, weights, norm, eps, interleaved, out, stream):
     like = X[0]
-    for x, name in zip(X, "QK"):
-        if x is not None:
-            check(x, name, like)
-    how = _how(like, table, interleaved, norm, eps, weights, positions)
-    rows = [None if x is None else _rows(how, x, p, s, w, name)
-            for x, p, s, w, name in zip(X, positions, starts, weights, "QK")]
-    at, Y = Launch(like.device, stream), []
+    how, size = _how(like, table, interleaved, norm, eps, weights, positions)
+    dtype, device = like.dtype, like.device
+    views = [None if x is None else view(x, name, dtype, device) for x, name in zip(X, "QK")]
+    at, Y, rows = Launch(device, stream), [], []
     with at as handle:
-        for x, r, y, name in zip(X, rows, out, "QK"):
-            if x is not None:
-                if y is None:
-                    y = empty_like(x)
-                else:
-                    check(y, f"the output for {name}", x)
-                    if y.shape != x.shape:
-                        raise ValueError(f"the output for {name} must have its shape")
-                r.X, r.Y = view(x), view(y)
+        for x, v, y, p, s, w, name in zip(X, views, out, positions, starts, weights, "QK"):
+            if x is None:
+                Y.append(None)
+                rows.append(None)
+                continue
+            if y is None:
+                y = empty_like(x)
+            elif isinstance(y, torch.Tensor) and y.shape != x.shape:
+                raise ValueError(f"the output for {name} must have its shape")
             Y.append(y)
+            rows.append(_rows(size, like, v, view(y, f"the output for {name}", dtype, device), NO_VIEW, NO_VIEW, x.shape, p, s, w, None, name))
         _call("anchor_attn_norm_rope", how, rows[0], rows[1], handle)
     at.used((*X, *positions, *weights, table[0] if table is not None else None), Y)
     return Y
@@ -187,14 +185,13 @@ def rope_backward(dY, table, positions=None, *, start: int = 0, interleaved: boo
     """dX for the upstream gradient dY of ``rope`` (turned back, by the same magnitude)."""
     if table is None:
         raise ValueError("rope_backward needs a table")
-    check(dY, "dY")
-    how = _how(dY, table, interleaved, 0, 0.0, (), (positions,))
-    r = _rows(how, dY, positions, start, None, "dY")
+    how, size = _how(dY, table, interleaved, 0, 0.0, (), (positions,))
+    g = view(dY, "dY", dY.dtype, dY.device)
     at = Launch(dY.device, stream)
     with at as handle:
         dX = empty_like(dY)
-        r.dY, r.dX = view(dY), view(dX)
-        _call("anchor_attn_norm_rope_backward", how, r, None, handle)
+        rows = _rows(size, dY, NO_VIEW, NO_VIEW, g, view(dX, "dX", dY.dtype, dY.device), dY.shape, positions, start, None, None, "dY")
+        _call("anchor_attn_norm_rope_backward", how, rows, None, handle)
     at.used((dY, positions, table[0]), (dX,))
     return dX
 
@@ -217,23 +214,20 @@ def norm_rope_backward(Q, K, dQ, dK, table, *, q_weight=None, k_weight=None, q_p
     X, G, W, P = (Q, K), (dQ, dK), (q_weight, k_weight), (q_positions, k_positions)
     if K is None:
         G, W, P = (dQ, None), (q_weight, None), (q_positions, None)
-    for x, g, name in zip(X, G, "QK"):
-        if x is not None:
-            check(x, name, Q)
-            check(g, f"d{name}", Q)
-            if g.shape != x.shape:
-                raise ValueError(f"d{name} must have {name}'s shape")
-    how = _how(Q, table, interleaved, 1, eps, W, P)
-    rows = [None if x is None else _rows(how, x, p, s, w, name) for x, p, s, w, name in zip(X, P, (q_start, k_start), W, "QK")]
-    at, dX, dW = Launch(Q.device, stream), [], []
+    how, size = _how(Q, table, interleaved, 1, eps, W, P)
+    dtype, device = Q.dtype, Q.device
+    views = [None if x is None else (view(x, name, dtype, device), view(g, f"d{name}", dtype, device)) for x, g, name in zip(X, G, "QK")]
+    at, dX, dW, rows = Launch(device, stream), [], [], []
     with at as handle:
-        import torch
-        for x, g, w, r in zip(X, G, W, rows):
+        for x, v, g, p, s, w, name in zip(X, views, G, P, (q_start, k_start), W, "QK"):
             dX.append(None if x is None else empty_like(x))
             dW.append(None if w is None else torch.empty_like(w))
-            if x is not None:
-                r.X, r.dY, r.dX = view(x), view(g), view(dX[-1])
-                r.dweight = None if w is None else dW[-1].data_ptr()
+            if x is None:
+                rows.append(None)
+                continue
+            if g.shape != x.shape:
+                raise ValueError(f"d{name} must have {name}'s shape")
+            rows.append(_rows(size, Q, v[0], NO_VIEW, v[1], view(dX[-1], f"d{name}", dtype, device), x.shape, p, s, w, dW[-1], name))
         _call("anchor_attn_norm_rope_backward", how, rows[0], rows[1], handle)
     at.used((*X, *G, *W, *P, table[0] if table is not None else None), (*dX, *dW))
     return dX[0], dX[1], dW[0], dW[1]

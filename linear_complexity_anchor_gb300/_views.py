@@ -1,97 +1,103 @@
-"""Marshalling of strided [B, heads, n, d] tensors and of streams for the calls that take views."""
+"""Marshalling of strided [B, heads, n, d] tensors and of streams for the calls that take views.
+
+A call's arguments go to the library as one packed structure of include/anchor_attn.h: the smallest calls take a few
+microseconds on the device, and building ctypes structures field by field took longer than that."""
 from __future__ import annotations
 
-import contextlib
-import ctypes
+import torch
 
-DTYPES = {"torch.bfloat16": 0, "torch.float32": 1}
+DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+VIEW = "Qqqq"              # anchor_attn_view_t: pointer, batch, head and row strides
+NO_VIEW = (0, 0, 0, 0)
 
-
-class View(ctypes.Structure):
-    _fields_ = [("ptr", ctypes.c_void_p), ("batch", ctypes.c_longlong), ("head", ctypes.c_longlong),
-                ("row", ctypes.c_longlong)]
-
-
-NO_VIEW = View()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def view(t) -> View:
-    sb, sh, sn, _ = t.stride()
-    return View(t.data_ptr(), sb, sh, sn)
+_package = None
+
+
+def library():
+    """The package's loaded library."""
+    global _package
+    if _package is None:
+        import linear_complexity_anchor_gb300
+        _package = linear_complexity_anchor_gb300
+    return _package._lib or _package.load()
+
+
+def fail(status: int, what: str) -> None:
+    _package._raise(status, what)
 
 
 def rows_dtype(t, name: str) -> int:
-    dt = DTYPES.get(str(t.dtype))
+    """The ABI's number of a CUDA tensor's type."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dt = DTYPES.get(t.dtype)
     if dt is None:
         raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
     return dt
 
 
-def check(t, name: str, like=None, dim: int = 4) -> None:
-    """A CUDA tensor of `like`'s type and device, whose last axis is dense."""
-    import torch
+def view(t, name: str, dtype, device) -> tuple:
+    """(pointer, strides) of a four-axis CUDA tensor of this type and device whose last axis is dense."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if like is not None:
-        if t.dtype != like.dtype:
-            raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-        if t.device != like.device:
-            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    if t.dim() != dim:
-        raise ValueError(f"{name} must have {dim} axes, got {t.dim()}")
-    if t.size(-1) > 1 and t.stride(-1) != 1:
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    strides = t.stride()
+    if len(strides) != 4:
+        raise ValueError(f"{name} must have 4 axes, got {len(strides)}")
+    if strides[3] != 1 and t.size(3) > 1:
         raise ValueError(f"the last axis of {name} must be dense")
+    return t.data_ptr(), strides[0], strides[1], strides[2]
 
 
 def empty_like(t):
     """A tensor of t's shape, with t's order of axes where t is dense."""
-    import torch
     r = torch.empty_like(t)
-    return r if r.size(-1) <= 1 or r.stride(-1) == 1 else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-
-
-@contextlib.contextmanager
-def _both(device, stream):
-    import torch
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield
+    return r if r.stride(3) == 1 or r.size(3) <= 1 else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 class Launch:
-    """The device and stream of one call: `with Launch(device, stream) as handle`.  Tensors made
-    inside belong to that stream; `used(...)` tells the allocator of tensors that are used on a
-    stream other than their own."""
+    """The device and stream of one call: `with Launch(device, stream) as handle`.  Tensors made inside belong to that
+    stream; `used(...)` tells the allocator of tensors that are used on a stream other than their own."""
 
-    __slots__ = ("device", "stream", "current", "guard")
+    __slots__ = ("device", "handle", "stream", "current", "guards")
 
     def __init__(self, device, stream=None):
-        import torch
-        self.device = device
+        self.device, self.stream, self.guards = device, None, ()
+        if stream is None and _raw_stream is not None:
+            self.handle = _raw_stream(device.index)
+            return
         self.current = torch.cuda.current_stream(device)
-        self.stream = self.current if stream is None else stream
-        if self.stream.device != device:
-            raise ValueError(f"stream is on {self.stream.device}, the tensors on {device}")
-        self.guard = None
+        stream = self.current if stream is None else stream
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        self.handle = stream.cuda_stream
+        if stream != self.current:
+            self.stream = stream
 
     def __enter__(self) -> int:
-        import torch
-        if self.stream != self.current:
-            self.guard = _both(self.device, self.stream)
-        elif torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream.cuda_stream
+        if self.stream is not None:
+            self.guards = (torch.cuda.device(self.device), torch.cuda.stream(self.stream))
+        elif _current_device() != self.device.index:
+            self.guards = (torch.cuda.device(self.device),)
+        for g in self.guards:
+            g.__enter__()
+        return self.handle
 
     def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-            self.guard = None
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
 
     def used(self, inputs, outputs=()) -> None:
-        if self.stream != self.current:
+        if self.stream is not None:
             for t in inputs:
                 if t is not None:
                     t.record_stream(self.stream)

@@ -441,7 +441,8 @@ cudaError_t launch(const CrossProblem &p, const float *delta, cudaStream_t strea
     if (KEYS && p.n > 0 && (!make_tile_map(&q, p.Q, p.B, p.heads, p.n, p.d) || !make_tile_map(&g, p.dH, p.B, p.heads, p.n, p.d)))
         return cudaErrorInvalidValue;
     a.a = KEYS ? q : k, a.b = KEYS ? g : v, a.fa = k, a.fb = v;
-    const cudaError_t e = cudaFuncSetAttribute(cross_bwd_kernel<D, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
+    static SmemOnce allow;
+    const cudaError_t e = allow(cross_bwd_kernel<D, KEYS>, G::kSmem);
     if (e != cudaSuccess) return e;
     return launch_pdl(cross_bwd_kernel<D, KEYS>, dim3(a.tiles * p.B * p.kv), dim3(kThreads), G::kSmem, stream, a);
 }

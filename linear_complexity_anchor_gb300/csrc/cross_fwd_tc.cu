@@ -402,7 +402,8 @@ cudaError_t launch(const CrossProblem &p, const CrossParts &w, cudaStream_t stre
     a.tiles = (p.rows + NQ * kRows - 1) / (NQ * kRows);
     if (p.s > 0 && (!make_tile_map(&a.k, p.K, p.B, p.kv, p.s, p.d) || !make_tile_map(&a.v, p.V, p.B, p.kv, p.s, p.d)))
         return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
+    static SmemOnce allow;
+    const cudaError_t e = allow(cross_fwd_kernel<D, NQ>, G::kSmem);
     if (e != cudaSuccess) return e;
     return launch_pdl(cross_fwd_kernel<D, NQ>, dim3(a.tiles * p.B * p.kv, w.parts), dim3(G::kThreads), G::kSmem, stream, a);
 }

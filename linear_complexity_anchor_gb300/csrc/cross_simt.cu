@@ -303,16 +303,12 @@ int tile_m(const CrossProblem &p, long long rows) {
     return tm;
 }
 
-template <typename Kernel>
-cudaError_t set_smem(Kernel kernel, size_t bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 template <int D, int TM>
 cudaError_t forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
     const int tiles = (p.rows + 16 * TM - 1) / (16 * TM);
     constexpr size_t smem = forward_smem<D, TM>();
-    const cudaError_t e = set_smem(cross_simt_forward_kernel<D, TM>, smem);
+    static SmemOnce allow;
+    const cudaError_t e = allow(cross_simt_forward_kernel<D, TM>, smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(cross_simt_forward_kernel<D, TM>, dim3(tiles * p.B * p.kv, w.parts), dim3(kThreads), smem, stream, p, w, tiles);
 }
@@ -321,7 +317,8 @@ template <int D, int TM, bool KEYS>
 cudaError_t backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
     const int tiles = ((KEYS ? p.s : p.rows) + 16 * TM - 1) / (16 * TM);
     constexpr size_t smem = backward_smem<D, TM>();
-    const cudaError_t e = set_smem(cross_simt_backward_kernel<D, TM, KEYS>, smem);
+    static SmemOnce allow;
+    const cudaError_t e = allow(cross_simt_backward_kernel<D, TM, KEYS>, smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(cross_simt_backward_kernel<D, TM, KEYS>, dim3(tiles * p.B * p.kv), dim3(kThreads), smem, stream, p, delta, tiles);
 }

@@ -4,6 +4,8 @@
 
 #include "common.cuh"
 
+#include <atomic>
+
 namespace anchor {
 
 // a view with its sizes
@@ -33,5 +35,20 @@ inline bool bytes_overlap(const void *a, size_t an, const void *b, size_t bn) {
 // synchronisation, and a call after one would map it again (measured at 0.1 to 0.6 ms).
 constexpr unsigned long long kPoolKeep = 512ull << 20;
 cudaError_t workspace_alloc(void **ptr, size_t bytes, cudaStream_t stream);
+
+// Allows a kernel `bytes` of dynamic shared memory, once per device (one object for each kernel).
+struct SmemOnce {
+    std::atomic<unsigned long long> done{0};  // bit: device
+    template <typename Kernel> cudaError_t operator()(Kernel kernel, size_t bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+        if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+};
 
 }  // namespace anchor

@@ -9,6 +9,38 @@ INVALID, UNSUPPORTED, ALIAS = 1, 2, 3
 A = 1 << 32
 
 
+I, F, L, P = ctypes.c_int, ctypes.c_float, ctypes.c_longlong, ctypes.c_void_p
+
+
+class View(ctypes.Structure):
+    _fields_ = [("ptr", P), ("batch", L), ("head", L), ("row", L)]
+
+
+class Cross(ctypes.Structure):
+    _fields_ = [(n, I) for n in ("dtype", "B", "heads", "kv_heads", "n", "s", "d")] + [("scale", F)] + [
+        (n, View) for n in ("Q", "K", "V", "H", "dH", "dQ", "dK", "dV")] + [("lse", P), ("lengths", P)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [(n, I) for n in ("dtype", "d", "rot", "axes", "interleaved", "norm", "weight_f32", "positions64")] + [
+        ("eps", F), ("magnitude", F), ("phases", P)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [(n, View) for n in ("X", "Y", "dY", "dX")] + [("weight", P), ("dweight", P), ("positions", P), ("positions_batch", L),
+                                                              ("start", L), ("B", I), ("heads", I), ("n", I)]
+
+
+def test_packed_sizes(pkg):
+    """What the binding packs is as long as the structures."""
+    import struct
+    from linear_complexity_anchor_gb300._views import VIEW
+    assert struct.calcsize("=" + VIEW) == ctypes.sizeof(View) == 32
+    assert struct.calcsize("=7if" + 8 * VIEW + "QQ") == ctypes.sizeof(Cross)
+    assert struct.calcsize("=8i2fQ") == ctypes.sizeof(Rope)
+    assert struct.calcsize("=" + 4 * VIEW + "QQQqq3i4x") == ctypes.sizeof(Rows)
+
+
 @pytest.fixture(scope="module")
 def pkg():
     from linear_complexity_anchor_gb300 import _build
@@ -19,15 +51,13 @@ def pkg():
 
 
 def dense(at, heads, n, d):
-    from linear_complexity_anchor_gb300._views import View
     return View(at, heads * n * d, n * d, d)
 
 
 def cross(pkg, backward=False, **change):
-    from linear_complexity_anchor_gb300._cross import _Cross
     z = dict(dtype=0, B=2, heads=4, kv_heads=2, n=8, s=16, d=64, scale=0.125)
     z.update({k: v for k, v in change.items() if k in z})
-    p = _Cross(**z)
+    p = Cross(**z)
     for i, name in enumerate(("Q", "K", "V", "H", "dH", "dQ", "dK", "dV")):
         q = name in ("Q", "H", "dH", "dQ")
         setattr(p, name, dense(A * (i + 1), z["heads"] if q else z["kv_heads"], z["n"] if q else z["s"], z["d"]))
@@ -42,7 +72,6 @@ def cross(pkg, backward=False, **change):
 @pytest.mark.parametrize("backward", [False, True])
 def test_cross_refusals(pkg, backward):
     c = lambda **kw: cross(pkg, backward, **kw)  # noqa: E731
-    View = type(dense(0, 1, 1, 1))
     for name in ("dtype", "B", "heads", "kv_heads", "n", "s"):
         assert c(**{name: -1}) == INVALID
     assert c(dtype=2) == INVALID and c(d=48) == UNSUPPORTED and c(d=0) == UNSUPPORTED
@@ -70,15 +99,14 @@ def test_cross_refusals(pkg, backward):
 
 
 def rope(pkg, backward=False, second=False, how={}, **change):
-    from linear_complexity_anchor_gb300._rope import _Rope, _Rows
-    h = _Rope(dtype=0, d=64, rot=64, axes=1, interleaved=0, norm=1, weight_f32=0, positions64=0, eps=1e-6, magnitude=1.0, phases=A * 30)
+    h = Rope(dtype=0, d=64, rot=64, axes=1, interleaved=0, norm=1, weight_f32=0, positions64=0, eps=1e-6, magnitude=1.0, phases=A * 30)
     for k, v in how.items():
         setattr(h, k, v)
     z = dict(B=2, heads=4, n=8)
     z.update({k: v for k, v in change.items() if k in z})
 
     def rows(base):
-        r = _Rows(**z)
+        r = Rows(**z)
         for i, name in enumerate(("X", "Y", "dY", "dX")):
             setattr(r, name, dense(base + A * (i + 1), z["heads"], z["n"], 64))
         r.weight, r.positions, r.positions_batch = A * 31, A * 32, 8
@@ -96,7 +124,6 @@ def rope(pkg, backward=False, second=False, how={}, **change):
 @pytest.mark.parametrize("backward", [False, True])
 def test_rope_refusals(pkg, backward, second):
     c = lambda how={}, **kw: rope(pkg, backward, second, how, **kw)  # noqa: E731
-    View = type(dense(0, 1, 1, 1))
     for bad in (dict(dtype=2), dict(interleaved=2), dict(norm=-1), dict(weight_f32=3), dict(positions64=2), dict(rot=-2), dict(rot=3),
                 dict(rot=66), dict(axes=0), dict(axes=4), dict(eps=-1.0), dict(eps=math.nan), dict(magnitude=math.inf), dict(phases=0),
                 dict(phases=A + 4)):
