@@ -29,10 +29,9 @@
 namespace anchor {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kBatch = 4;          // heads in flight per thread: 128 bytes of loads
-constexpr int kFill = 152 * 6;     // blocks that fill the GPU, below which heads are cut into groups
-constexpr int kBwdBlocks = 152 * 4;  // most blocks of a tensor whose dweight is summed
+constexpr int kThreads = 128;
+constexpr int kFill = 152 * 12;      // blocks that fill the GPU, below which heads are cut into groups
+constexpr int kBwdBlocks = 152 * 8;  // most blocks of a tensor whose dweight is summed
 
 enum Mode { kHalves = 0, kNeighbours = 1, kOddHalves = 2 };
 
@@ -193,8 +192,13 @@ __device__ __forceinline__ void load_weight(const Params &p, const void *w, int 
 // BWD: y receives dx; with a norm x is read too.  Every lane of a warp runs every step (the
 // shuffles and __syncwarp), lanes without a token or head on row 0 without loads and stores.
 template <typename T, int MODE, bool BWD>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, MODE == kOddHalves ? (BWD ? 3 : 4) : BWD ? (sizeof(T) == 2 ? 3 : 4) : 5) norm_rope_kernel(const Params p) {
     constexpr int V = kV<T>;
+    // Heads whose rows are on their way.  bf16: a head's place is refilled as soon as it is unpacked
+    // (4 x 32 heads x 16384 rows of 128: 170 us against 179 for three at a time).  fp32 is not unpacked,
+    // its place stays in use: refilled behind the batch (67 us against 80, 8 x 24 x 4200 rows of 64).
+    constexpr bool kRefill = sizeof(T) == 2;
+    constexpr int kAhead = MODE == kOddHalves ? 2 : kRefill ? 3 : 4;
     extern __shared__ float sh[];  // odd halves: [groups][d + 4]; backward: the block's dweight [groups][d]
     grid_dependency_wait();
     grid_dependents_launch();
@@ -227,30 +231,39 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const Params p) {
         turn.angles(p, r, bi, i);
         const long long xo = bi * r.xb + i * r.xn, yo = bi * r.yb + i * r.yn, go = bi * r.gb + i * r.gn;
         const bool need_x = !BWD || p.norm;
-        for (int h = h0; h < h1; h += kBatch) {
-            Raw<T> xr[kBatch], gr[BWD ? kBatch : 1];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                xr[k].a = xr[k].b = make_uint4(0, 0, 0, 0);
-                if (BWD) gr[k].a = gr[k].b = make_uint4(0, 0, 0, 0);
-                if (!live || h + k >= h1) continue;
-                if (need_x) {
-                    const T *x = X + xo + (long long)(h + k) * r.xh;
-                    xr[k].a = *reinterpret_cast<const uint4 *>(x + turn.a);
-                    xr[k].b = *reinterpret_cast<const uint4 *>(x + turn.b);
-                }
-                if (BWD) {
-                    const T *y = DY + go + (long long)(h + k) * r.gh;
-                    gr[k].a = *reinterpret_cast<const uint4 *>(y + turn.a);
-                    gr[k].b = *reinterpret_cast<const uint4 *>(y + turn.b);
-                }
+        Raw<T> xr[kAhead], gr[BWD ? kAhead : 1];
+        auto fetch = [&](int k, int h) {
+            if (!live || h >= h1) return;
+            if (need_x) {
+                const T *x = X + xo + (long long)h * r.xh;
+                xr[k].a = *reinterpret_cast<const uint4 *>(x + turn.a);
+                xr[k].b = *reinterpret_cast<const uint4 *>(x + turn.b);
             }
+            if (BWD) {
+                const T *y = DY + go + (long long)h * r.gh;
+                gr[k].a = *reinterpret_cast<const uint4 *>(y + turn.a);
+                gr[k].b = *reinterpret_cast<const uint4 *>(y + turn.b);
+            }
+        };
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
+        for (int k = 0; k < kAhead; ++k) {
+            xr[k].a = xr[k].b = make_uint4(0, 0, 0, 0);
+            if (BWD) gr[k].a = gr[k].b = make_uint4(0, 0, 0, 0);
+            fetch(k, h0 + k);
+        }
+        for (int h = h0; h < h1; h += kAhead) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
                 if (h + k >= h1) break;  // the same for all lanes
                 float v[2 * V];
                 unpack<T>(xr[k].a, v);
                 unpack<T>(xr[k].b, v + V);
+                float z[BWD ? 2 * V : 1];
+                if (BWD) {
+                    unpack<T>(gr[k].a, z);
+                    unpack<T>(gr[k].b, z + V);
+                }
+                if (kRefill) fetch(k, h + k + kAhead);
                 float rs = 1.f;
                 if (p.norm) {
                     float q = 0.f;
@@ -265,9 +278,6 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const Params p) {
                     }
                     turn.apply(p, v, 1.f, row);
                 } else {
-                    float z[2 * V];
-                    unpack<T>(gr[k].a, z);
-                    unpack<T>(gr[k].b, z + V);
                     turn.apply(p, z, -1.f, row);
                     if (p.norm) {
                         float q = 0.f;
@@ -291,6 +301,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const Params p) {
                     store_chunk(y + turn.a, v);
                     store_chunk(y + turn.b, v + V);
                 }
+            }
+            if (!kRefill) {
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) fetch(k, h + k + kAhead);
             }
         }
     }
