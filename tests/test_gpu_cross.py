@@ -74,6 +74,15 @@ def test_few_queries(aa, dtype, shape, lengths):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [16, 64, 128])
+@pytest.mark.parametrize("s", [1, 16, 31, 77, 112, 127, 128])
+def test_short_states(aa, dtype, d, s):
+    """All states in one tile: rows of several tiles, of shared heads, and single ones."""
+    check(aa, s, 9, 4, 2, 197, s, d, dtype, lengths="mixed", train=s == 77)
+    check(aa, s, 9, 8, 2, 1, s, d, dtype, lengths="mixed", train=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_many_tiles(aa, dtype):
     """More row tiles and key tiles than any stage or part, with heads that share keys."""
     check(aa, 3, 2, 4, 2, 1030, 1100, 64, dtype, lengths="mixed")
