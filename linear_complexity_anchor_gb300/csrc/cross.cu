@@ -112,7 +112,9 @@ anchor_attn_status_t cross(const anchor_attn_cross_t *a, bool bwd, void *stream_
 
     CrossProblem p = {};
     p.B = a->B, p.heads = a->heads, p.kv = a->kv_heads, p.group = a->heads / a->kv_heads;
-    p.n = a->n, p.s = a->s, p.d = a->d, p.rows = p.group * a->n, p.scale = a->scale, p.f32 = a->dtype == 1;
+    p.n = a->n, p.s = a->s, p.d = a->d, p.rows = p.group * a->n;
+    p.by_n = Divide((uint32_t)std::max(1, a->n)), p.by_kv = Divide((uint32_t)a->kv_heads);
+    p.scale = a->scale, p.f32 = a->dtype == 1;
     p.lse = a->lse, p.lengths = a->lengths;
     const int es = p.f32 ? 4 : 2;
     const bool queries = a->n > 0, states = a->s > 0;

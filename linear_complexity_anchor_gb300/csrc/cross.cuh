@@ -13,12 +13,26 @@ struct CrossView {
     long long sb, sh, sn;  // strides in elements
 };
 
+// Division by a number that the launch knows, as a product: for d > 0 and x < 2^31,
+// x / d = (x + hi(x m)) >> l with l = ceil(log2 d), m = floor(2^32 (2^l - d) / d) + 1 (Granlund and
+// Montgomery, "Division by invariant integers using multiplication", 1994).
+struct Divide {
+    uint32_t d = 1, m = 1, l = 0;
+    Divide() = default;
+    explicit Divide(uint32_t by) : d(by) {
+        while ((1ull << l) < by) ++l;
+        m = (uint32_t)(((1ull << 32) * ((1ull << l) - by)) / by + 1);
+    }
+    __device__ __forceinline__ int of(int x) const { return (int)((__umulhi(m, (uint32_t)x) + (uint32_t)x) >> l); }
+};
+
 struct CrossProblem {
     CrossView Q, K, V, H, dH, dQ, dK, dV;
     float *lse;           // [B][heads][n] or null
     const int *lengths;   // [B] or null
     int B, heads, kv, group, n, s, d;
     int rows;             // group * n
+    Divide by_n, by_kv;
     float scale;
     bool f32;
 };
@@ -28,7 +42,7 @@ __device__ __forceinline__ int cross_length(const CrossProblem &p, int b) {
 }
 // row r of key head k: its offset in a [B][heads][n][d] view
 __device__ __forceinline__ long long cross_row(const CrossProblem &p, const CrossView &v, int b, int k, int r) {
-    const int g = r / p.n, i = r - g * p.n;
+    const int g = p.by_n.of(r), i = r - g * p.n;
     return b * v.sb + (long long)(k * p.group + g) * v.sh + (long long)i * v.sn;
 }
 // ... and in a dense [B][heads][n] array

@@ -59,6 +59,7 @@ struct BwdParams {
     TileMap a, b;  // queries: K, V stream; keys: Q, dH stream
     TileMap fa, fb;  // keys: K, V stay
     int tiles;
+    Divide by_tiles;
 };
 
 // KEYS: see above
@@ -76,8 +77,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
     float *stat = reinterpret_cast<float *>(sm + G::kStatB);
     const CrossProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tile = (int)(blockIdx.x % a.tiles), bk = (int)(blockIdx.x / a.tiles);
-    const int b = bk / p.kv, kh = bk - b * p.kv, r0 = tile * kRows;
+    const int bk = a.by_tiles.of((int)blockIdx.x), tile = (int)blockIdx.x - bk * a.tiles;
+    const int b = p.by_kv.of(bk), kh = bk - b * p.kv, r0 = tile * kRows;
     unsigned int *error = &g_cross_bwd_error;
 
     if (threadIdx.x == 0) {
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
                 const bool then = w.t == around - 1;  // the next step's
                 // the rows have read S(j) (and left P^T(j) over it)
                 if (more && !landed_a && !(ok = bwait(a_bar + (j + 1) % NA, a_par(j + 1), error))) break;
-                if (!(ok = bwait_now(p_full, par, error))) break;
+                if (!(ok = bwait(p_full, par, error))) break;
                 tc_fence_after();
                 if (KEYS) along(tmem + kColA, tmem + kColS, slot_b(j), last, j > 0);  // dV += P^T dH
                 if (more) {
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
                 }
                 // the rows have left dS(j) over dP(j)
                 if (more && !landed_b && !(ok = bwait(b_bar + (j + 1) % NB, b_par(j + 1), error))) break;
-                if (!(ok = bwait_now(ds_full, par, error))) break;
+                if (!(ok = bwait(ds_full, par, error))) break;
                 tc_fence_after();
                 along(tmem + kColA + (KEYS ? D : 0), tmem + kColP, slot_a(j), last, j > 0);  // dK += dS^T Q, dQ += dS K
                 if (more) {
@@ -276,17 +277,16 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
             // quarters 0 and 1 load the 128 rows of Q, by halves of the columns, 2 and 3 those of dH
             constexpr int kLanes = D / 16;
             const CrossView &v = quarter >= 2 ? p.dH : p.Q;
-            const long long at = mine ? cross_row(p, v, b, kh, r) : -1;
             uint8_t *dst = sm + G::kFix + (quarter >> 1) * kTile<D>;
             const int ch = (quarter & 1) * kLanes + lane % kLanes;
+            uint4 x[kLanes];
+            each_row<kLanes>(mine ? cross_row(p, v, b, kh, r) : -1, v.sn, [&](int i, int, long long o) {
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (o >= 0 && ch * 8 < p.d) x[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)v.ptr + o + ch * 8);
+            });
 #pragma unroll
-            for (int i = 0; i < kLanes; ++i) {
-                const int rr = i * (32 / kLanes) + lane / kLanes;
-                const long long o = __shfl_sync(0xffffffffu, at, rr);
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (o >= 0 && ch * 8 < p.d) x = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)v.ptr + o + ch * 8);
-                *reinterpret_cast<uint4 *>(dst + chunk_at(w4 * 32 + rr, ch)) = x;
-            }
+            for (int i = 0; i < kLanes; ++i)
+                *reinterpret_cast<uint4 *>(dst + chunk_at(w4 * 32 + i * (32 / kLanes) + lane / kLanes, ch)) = x[i];
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(fix_full);
@@ -303,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
             const int cols = width(walk.t) - kQuarter * quarter;  // of this quarter that exist (may be none)
             const float *st = stat + kQuarter * quarter;
             float e[32];
-            if (!bwait_now(s_full, (uint32_t)(j & 1), error)) { ok = false; break; }
-            if (KEYS && !bwait_now(lse_full, (uint32_t)(j & 1), error)) { ok = false; break; }
+            if (!bwait(s_full, (uint32_t)(j & 1), error)) { ok = false; break; }
+            if (KEYS && !bwait(lse_full, (uint32_t)(j & 1), error)) { ok = false; break; }
             tc_fence_after();
             tmem_ld32(tS, e);
             tmem_ld_wait();
@@ -337,8 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
                 mbar_arrive(p_full);
             }
             // dS
-            if (KEYS && !bwait_now(d_full, (uint32_t)(j & 1), error)) { ok = false; break; }
-            if (!bwait_now(dp_full, (uint32_t)(j & 1), error)) { ok = false; break; }
+            if (KEYS && !bwait(d_full, (uint32_t)(j & 1), error)) { ok = false; break; }
+            if (!bwait(dp_full, (uint32_t)(j & 1), error)) { ok = false; break; }
             tc_fence_after();
             {
                 float g[32];
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
             tmem_st_wait();
             if (!KEYS && walk.t == nt - 1 && quarter == 0 && L % kRows && L < p.s) {
                 // the last tile's rows of K that do not count (S has read them)
-                if (!bwait_now(a_full + j % NA, (uint32_t)((j / NA) & 1), error)) { ok = false; break; }
+                if (!bwait(a_full + j % NA, (uint32_t)((j / NA) & 1), error)) { ok = false; break; }
                 zero_rows<D>(sm + G::kA + j % NA * kTile<D>, row, L % kRows, (L % kRows + 15) / 16 * 16);
                 fence_proxy_async_smem();
             }
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
                 mbar_arrive(ds_full);
             }
         }
-        if (ok && nt > 0) ok = bwait_now(acc, 0u, error);
+        if (ok && nt > 0) ok = bwait(acc, 0u, error);
         tc_fence_after();
         // Rows out through shared memory (the tiles that stayed are not needed any more).  Keys: quarters
         // 0 and 1 halves of dV's columns, 2 and 3 of dK's; queries: quarters of dQ's at d = 128, halves
@@ -409,14 +409,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
             const long long at = !exists ? -1 : KEYS ? b * v.sb + kh * v.sh + (long long)r * v.sn : cross_row(p, v, b, kh, r);
             // 16-byte chunks of this warp's rows and columns, a row's chunks by neighbouring lanes
             constexpr int kW = kCols / 8;
-#pragma unroll
-            for (int i = 0; i < kW; ++i) {
-                const int rr = i * (32 / kW) + lane / kW, ch = from / 8 + lane % kW;
-                const long long o = __shfl_sync(0xffffffffu, at, rr);
+            const int ch = from / 8 + lane % kW;
+            each_row<kW>(at, v.sn, [&](int, int rr, long long o) {
                 if (o >= 0 && ch * 8 < p.d)
                     *reinterpret_cast<uint4 *>((__nv_bfloat16 *)v.ptr + o + ch * 8) =
                         *reinterpret_cast<const uint4 *>(stage + chunk_at(w4 * 32 + rr, ch));
-            }
+            });
         }
         tc_fence_before();
         __syncwarp();
@@ -435,6 +433,7 @@ cudaError_t launch(const CrossProblem &p, const float *delta, cudaStream_t strea
     a.p = p;
     a.delta = delta;
     a.tiles = ((KEYS ? p.s : p.rows) + kRows - 1) / kRows;
+    a.by_tiles = Divide((uint32_t)a.tiles);
     TileMap k, v, q, g;
     if (p.s > 0 && (!make_tile_map(&k, p.K, p.B, p.kv, p.s, p.d) || !make_tile_map(&v, p.V, p.B, p.kv, p.s, p.d)))
         return cudaErrorInvalidValue;

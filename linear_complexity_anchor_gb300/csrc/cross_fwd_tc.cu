@@ -58,6 +58,7 @@ struct FwdParams {
     CrossParts w;
     TileMap k, v;
     int tiles;
+    Divide by_tiles;
 };
 
 template <int D, int NQ>
@@ -74,8 +75,8 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
     const CrossProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kLoad = 8 * NQ, kIssue = 8 * NQ + 1;
-    const int tile = (int)(blockIdx.x % a.tiles), bk = (int)(blockIdx.x / a.tiles);
-    const int b = bk / p.kv, kh = bk - b * p.kv, r0 = tile * NQ * kRows;
+    const int bk = a.by_tiles.of((int)blockIdx.x), tile = (int)blockIdx.x - bk * a.tiles;
+    const int b = p.by_kv.of(bk), kh = bk - b * p.kv, r0 = tile * NQ * kRows;
     const int left = p.rows - r0;                        // rows of this CTA that exist
     const int nq = NQ == 2 && left > kRows ? 2 : 1;
 
@@ -167,7 +168,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                 for (int q = 0; q < NQ; ++q) {
                     if (q >= nq) break;
                     const uint32_t S = tmem + 128 * (q * NS + j % NS);
-                    if (!(ok = bwait_now(p_full + q * NS + j % NS, par, error))) break;
+                    if (!(ok = bwait(p_full + q * NS + j % NS, par, error))) break;
                     tc_fence_after();
                     product_mn<32>(tmem + G::kColO + q * D, S, vd, idO, steps, j > 0);
                     if (NS == 2 || j == nt - 1) umma_commit(o_full + q);
@@ -199,18 +200,16 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
         const int my_row = lane / kLanes, my_chunk = half * kLanes + lane % kLanes;
         if (nt > 0) {
             // Q, negated for a negative scale
-            const long long at = mine ? cross_row(p, p.Q, b, kh, r) : -1;
             const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+            uint4 x[kLanes];
+            each_row<kLanes>(mine ? cross_row(p, p.Q, b, kh, r) : -1, p.Q.sn, [&](int i, int, long long o) {
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (o >= 0 && my_chunk * 8 < p.d) x[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.Q.ptr + o + my_chunk * 8);
+            });
 #pragma unroll
             for (int i = 0; i < kLanes; ++i) {
-                const int rr = i * (32 / kLanes) + my_row;
-                const long long o = __shfl_sync(0xffffffffu, at, rr);
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (o >= 0 && my_chunk * 8 < p.d) {
-                    x = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.Q.ptr + o + my_chunk * 8);
-                    x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-                }
-                *reinterpret_cast<uint4 *>(sQ + chunk_at(w4 * 32 + rr, my_chunk)) = x;
+                x[i].x ^= flip, x[i].y ^= flip, x[i].z ^= flip, x[i].w ^= flip;
+                *reinterpret_cast<uint4 *>(sQ + chunk_at(w4 * 32 + i * (32 / kLanes) + my_row, my_chunk)) = x[i];
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -228,7 +227,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
             for (int j = 0; j < nt && ok; ++j) {
                 const int buf = q * NS + j % NS;
                 const uint32_t tS = tmem + lanes + 128 * buf + 64 * half;
-                if (!bwait_now(s_full + buf, (uint32_t)((j / NS) & 1), error)) { ok = false; break; }
+                if (!bwait(s_full + buf, (uint32_t)((j / NS) & 1), error)) { ok = false; break; }
                 tc_fence_after();
                 const int keys = min(kRows, L - (t0 + j) * kRows) - 64 * half;  // of this half that count (may be none)
                 float s[64];
@@ -254,7 +253,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                 slot[half * kRows] = __float2bfloat16_rn(top);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(meet);
-                if (!bwait_now(meet, (uint32_t)(j & 1), error)) { ok = false; break; }
+                if (!bwait(meet, (uint32_t)(j & 1), error)) { ok = false; break; }
                 top = fmaxf(__bfloat162float(slot[0]), __bfloat162float(slot[kRows]));
                 if (j == 0) {
                     m = top;
@@ -263,7 +262,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                     if (__any_sync(0xffffffffu, grows)) {
                         // this half of O's columns (complete up to the tile before) to the new maximum
                         // (one S buffer: this S was issued after the product that O waits for)
-                        if (NS == 2 && !bwait_now(o_full + q, (uint32_t)((j - 1) & 1), error)) { ok = false; break; }
+                        if (NS == 2 && !bwait(o_full + q, (uint32_t)((j - 1) & 1), error)) { ok = false; break; }
                         tc_fence_after();
                         const float f = grows ? ex2(m - top) : 1.f;
                         if (grows) m = top;
@@ -303,7 +302,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                 if (L < p.s && q == 0 && half == 0 && L - (t0 + j) * kRows < kRows) {
                     // the last tile's rows of V that do not count, once (the other tile's product comes later)
                     const int i = j + NS, st = i % ST, from = L - (t0 + j) * kRows;
-                    if (!bwait_now(full + st, (uint32_t)((i / ST) & 1), error)) { ok = false; break; }
+                    if (!bwait(full + st, (uint32_t)((i / ST) & 1), error)) { ok = false; break; }
                     const int warps = min((left + 31) / 32, 4);
                     for (int t = row; t < kRows; t += 32 * warps) zero_rows<D>(sm + G::kRing + (2 * st + 1) * kTile<D>, t, from, (from + 15) / 16 * 16);
                     fence_proxy_async_smem();
@@ -314,12 +313,12 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
             }
             if (ok && nt > 0) {
                 // O, then the halves' sums (over the maxima, which all warps have read by then)
-                ok = bwait_now(o_full + q, (uint32_t)((NS == 2 ? nt - 1 : 0) & 1), error);
+                ok = bwait(o_full + q, (uint32_t)((NS == 2 ? nt - 1 : 0) & 1), error);
                 float *slot = reinterpret_cast<float *>(sm + G::kEx + q * 2 * kRows * 4) + row;
                 slot[half * kRows] = l;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(meet);
-                ok = ok && bwait_now(meet, (uint32_t)(nt & 1), error);
+                ok = ok && bwait(meet, (uint32_t)(nt & 1), error);
                 l = slot[0] + slot[kRows];
             }
             tc_fence_after();
@@ -368,15 +367,11 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                     }
                 }
                 __syncwarp();
-                const long long at = mine ? cross_row(p, p.H, b, kh, r) : -1;
-#pragma unroll
-                for (int i = 0; i < kLanes; ++i) {
-                    const int rr = i * (32 / kLanes) + my_row;
-                    const long long o = __shfl_sync(0xffffffffu, at, rr);
-                    if (o >= 0 && my_chunk * 8 < p.d)
-                        *reinterpret_cast<uint4 *>((__nv_bfloat16 *)p.H.ptr + o + my_chunk * 8) =
+                each_row<kLanes>(mine ? cross_row(p, p.H, b, kh, r) : -1, p.H.sn, [&](int, int rr, long long to) {
+                    if (to >= 0 && my_chunk * 8 < p.d)
+                        *reinterpret_cast<uint4 *>((__nv_bfloat16 *)p.H.ptr + to + my_chunk * 8) =
                             *reinterpret_cast<const uint4 *>(sQ + chunk_at(w4 * 32 + rr, my_chunk));
-                }
+                });
                 if (p.lse && mine && half == 0) p.lse[f] = l == 0.f ? -INFINITY : m * (1.f / kLog2e) + logf(l);
             }
         }
@@ -414,8 +409,8 @@ __global__ void __launch_bounds__(kRows, Short<D>::kPerSM) cross_short_kernel(co
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(o_full + 1);
     const CrossProblem &p = a.p;
     const int row = threadIdx.x, warp = row >> 5, lane = row & 31;
-    const int tile = (int)(blockIdx.x % a.tiles), bk = (int)(blockIdx.x / a.tiles);
-    const int b = bk / p.kv, kh = bk - b * p.kv, r = tile * kRows + row;
+    const int bk = a.by_tiles.of((int)blockIdx.x), tile = (int)blockIdx.x - bk * a.tiles;
+    const int b = p.by_kv.of(bk), kh = bk - b * p.kv, r = tile * kRows + row;
     const bool mine = r < p.rows, active = tile * kRows + 32 * warp < p.rows;
     unsigned int *error = &g_cross_fwd_error;
     if (row == 0) {
@@ -433,24 +428,37 @@ __global__ void __launch_bounds__(kRows, Short<D>::kPerSM) cross_short_kernel(co
         mbar_arrive_expect_tx(v_full, kTile<D>);
         load_tile<D>(sm + G::kVv, a.v, v_full, 0, kh, b);
     }
+    // Q, K and V of the CTA that will follow on this SM, into L2
+    const long long then = (long long)blockIdx.x + G::kPerSM * kPlanSMs;
+    if (then < (long long)gridDim.x) {
+        const int bk2 = a.by_tiles.of((int)then), tile2 = (int)then - bk2 * a.tiles, b2 = p.by_kv.of(bk2), kh2 = bk2 - b2 * p.kv;
+        if (tile2 * kRows + row < p.rows) {
+            const char *q = (const char *)((const __nv_bfloat16 *)p.Q.ptr + cross_row(p, p.Q, b2, kh2, tile2 * kRows + row));
+            for (int x = 0; x < 2 * p.d; x += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + x));
+        }
+        if (tile2 == 0 && row == 0) {
+#pragma unroll
+            for (int q = 0; q < D / 64; ++q) {
+                prefetch_tile(&a.k.map, 64 * q, 0, kh2 * a.k.by_head, b2 * a.k.by_batch);
+                prefetch_tile(&a.v.map, 64 * q, 0, kh2 * a.v.by_head, b2 * a.v.by_batch);
+            }
+        }
+    }
     const int L = cross_length(p, b);
     uint8_t *sQ = sm + G::kQ;
     constexpr int kLanes = D / 8;
     {
-        const long long at = mine ? cross_row(p, p.Q, b, kh, r) : -1;
         const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+        const int ch = lane % kLanes;
         uint4 x[kLanes];
-#pragma unroll
-        for (int i = 0; i < kLanes; ++i) {
-            const long long o = __shfl_sync(0xffffffffu, at, i * (32 / kLanes) + lane / kLanes);
-            const int ch = lane % kLanes;
+        each_row<kLanes>(mine ? cross_row(p, p.Q, b, kh, r) : -1, p.Q.sn, [&](int i, int, long long o) {
             x[i] = make_uint4(0, 0, 0, 0);
             if (o >= 0 && ch * 8 < p.d) x[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.Q.ptr + o + ch * 8);
-        }
+        });
 #pragma unroll
         for (int i = 0; i < kLanes; ++i) {
             x[i].x ^= flip, x[i].y ^= flip, x[i].z ^= flip, x[i].w ^= flip;
-            *reinterpret_cast<uint4 *>(sQ + chunk_at(warp * 32 + i * (32 / kLanes) + lane / kLanes, lane % kLanes)) = x[i];
+            *reinterpret_cast<uint4 *>(sQ + chunk_at(warp * 32 + i * (32 / kLanes) + lane / kLanes, ch)) = x[i];
         }
     }
     fence_proxy_async_smem();
@@ -463,7 +471,7 @@ __global__ void __launch_bounds__(kRows, Short<D>::kPerSM) cross_short_kernel(co
     const int l16 = (L + 15) / 16;
     bool ok = true;
     if (row == 0 && L > 0) {
-        ok = bwait_now(k_full, 0u, error);
+        ok = bwait(k_full, 0u, error);
         tc_fence_after();
         if (ok)
             product_k<D>(tmem, desc_k(smem_u32(sQ)), desc_k(smem_u32(sm + G::kK)), idesc_bf16_f32(kRows, 16 * l16, false, false), (p.d + 15) / 16,
@@ -474,7 +482,7 @@ __global__ void __launch_bounds__(kRows, Short<D>::kPerSM) cross_short_kernel(co
     const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);  // (see above)
     float m = -INFINITY, l = 0.f;
     if (L > 0) {
-        ok = bwait_now(s_full, 0u, error) && ok;
+        ok = bwait(s_full, 0u, error) && ok;
         tc_fence_after();
         if (ok && active) {
             float s[32];
@@ -524,7 +532,7 @@ __global__ void __launch_bounds__(kRows, Short<D>::kPerSM) cross_short_kernel(co
             tmem_st_wait();
         }
         if (L < p.s) {  // rows of V that do not count
-            ok = bwait_now(v_full, 0u, error) && ok;
+            ok = bwait(v_full, 0u, error) && ok;
             zero_rows<D>(sm + G::kVv, row, L, 16 * l16);
             fence_proxy_async_smem();
         }
@@ -534,7 +542,7 @@ __global__ void __launch_bounds__(kRows, Short<D>::kPerSM) cross_short_kernel(co
     tc_fence_after();
     if (row == 0) {
         // (both copies have landed before the CTA leaves)
-        const bool landed = bwait_now(v_full, 0u, error) && bwait_now(k_full, 0u, error);
+        const bool landed = bwait(v_full, 0u, error) && bwait(k_full, 0u, error);
         if (L > 0) {
             tc_fence_after();
             if (landed && ok)
@@ -544,7 +552,7 @@ __global__ void __launch_bounds__(kRows, Short<D>::kPerSM) cross_short_kernel(co
     }
     __syncwarp();
     if (L > 0) {
-        ok = bwait_now(o_full, 0u, error) && ok;
+        ok = bwait(o_full, 0u, error) && ok;
         tc_fence_after();
     }
     if (ok && active) {
@@ -568,15 +576,12 @@ __global__ void __launch_bounds__(kRows, Short<D>::kPerSM) cross_short_kernel(co
             }
         }
         __syncwarp();
-        const long long at = mine ? cross_row(p, p.H, b, kh, r) : -1;
-#pragma unroll
-        for (int i = 0; i < kLanes; ++i) {
-            const int rr = i * (32 / kLanes) + lane / kLanes, ch = lane % kLanes;
-            const long long to = __shfl_sync(0xffffffffu, at, rr);
+        const int ch = lane % kLanes;
+        each_row<kLanes>(mine ? cross_row(p, p.H, b, kh, r) : -1, p.H.sn, [&](int, int rr, long long to) {
             if (to >= 0 && ch * 8 < p.d)
                 *reinterpret_cast<uint4 *>((__nv_bfloat16 *)p.H.ptr + to + ch * 8) =
                     *reinterpret_cast<const uint4 *>(sQ + chunk_at(warp * 32 + rr, ch));
-        }
+        });
         if (p.lse && mine) p.lse[cross_flat(p, b, kh, r)] = l == 0.f ? -INFINITY : m * (1.f / kLog2e) + logf(l);
     }
     tc_fence_before();
@@ -599,6 +604,7 @@ cudaError_t launch(const CrossProblem &p, const CrossParts &w, cudaStream_t stre
     a.p = p;
     a.w = w;
     a.tiles = (p.rows + NQ * kRows - 1) / (NQ * kRows);
+    a.by_tiles = Divide((uint32_t)a.tiles);
     if (p.s > 0 && (!make_tile_map(&a.k, p.K, p.B, p.kv, p.s, p.d) || !make_tile_map(&a.v, p.V, p.B, p.kv, p.s, p.d)))
         return cudaErrorInvalidValue;
     static SmemOnce allow;
@@ -613,6 +619,7 @@ cudaError_t launch_short(const CrossProblem &p, cudaStream_t stream) {
     a.p = p;
     a.w = CrossParts{nullptr, nullptr, 1};
     a.tiles = (p.rows + kRows - 1) / kRows;
+    a.by_tiles = Divide((uint32_t)a.tiles);
     if (!make_tile_map(&a.k, p.K, p.B, p.kv, p.s, p.d) || !make_tile_map(&a.v, p.V, p.B, p.kv, p.s, p.d)) return cudaErrorInvalidValue;
     static SmemOnce allow;
     const cudaError_t e = allow(cross_short_kernel<D>, Short<D>::kSmem);

@@ -31,7 +31,8 @@ struct TileMap {
 };
 bool make_tile_map(TileMap *m, const CrossView &v, int B, int heads, int rows, int d);
 
-// bit 0 of the error word, and false, once a wait has lasted kWaitNs
+// bit 0 of the error word, and false, once a wait has lasted kWaitNs.  (In line: a call in the loops
+// that wait costs them their registers, 62 -> 69 us in the forward of 8 heads, 9728 x 2048.)
 __device__ __forceinline__ bool bwait(uint64_t *bar, uint32_t parity, unsigned int *error) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
@@ -44,10 +45,6 @@ __device__ __forceinline__ bool bwait(uint64_t *bar, uint32_t parity, unsigned i
     return true;
 }
 
-// the same, with a try that does not sleep first (what the row warps wait for is often there)
-__device__ __forceinline__ bool bwait_now(uint64_t *bar, uint32_t parity, unsigned int *error) {
-    return mbar_try_wait(bar, parity) || bwait(bar, parity, error);
-}
 // whether a phase is complete, without waiting
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
@@ -65,12 +62,39 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, u
         "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
         : "memory");
 }
+// a box into L2, nothing else
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap *map, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"((uint64_t)map), "r"(c0), "r"(c1),
+                 "r"(c2), "r"(c3)
+                 : "memory");
+}
 // rows [row, row + 128) of one head; rows and columns outside the tensor are zero.  The caller has
 // announced kTile bytes on `bar`.
 template <int D>
 __device__ __forceinline__ void load_tile(uint8_t *dst, const TileMap &m, uint64_t *bar, int row, int head, int b) {
 #pragma unroll
     for (int q = 0; q < D / 64; ++q) tma_load_4d(dst + q * kBlock, &m.map, bar, 64 * q, row, head * m.by_head, b * m.by_batch);
+}
+
+// A warp's 32 rows of a view, `lanes` lanes of 16 bytes a row: calls f(i, row of the warp, offset of
+// the row in the view, or -1) for its 32 / lanes rows of each of `lanes` passes.  `at`: the offset of
+// this lane's own row.  Rows that follow one another (all but those around the end of a head) are
+// addressed by their step, others by asking the lane that has them.
+template <int lanes, typename F>
+__device__ __forceinline__ void each_row(long long at, long long step, F f) {
+    const int lane = threadIdx.x & 31, first = lane / lanes;
+    const long long base = __shfl_sync(0xffffffffu, at, 0);
+    if (__all_sync(0xffffffffu, base >= 0 && at == base + lane * step)) {
+        long long o = base + first * step;
+#pragma unroll
+        for (int i = 0; i < lanes; ++i, o += (32 / lanes) * step) f(i, i * (32 / lanes) + first, o);
+    } else {
+#pragma unroll
+        for (int i = 0; i < lanes; ++i) {
+            const int row = i * (32 / lanes) + first;
+            f(i, row, __shfl_sync(0xffffffffu, at, row));
+        }
+    }
 }
 
 // byte offset of 16-byte chunk c of row r
