@@ -132,22 +132,22 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
         if (lane == 0 && nt > 0) {
             if (KEYS) {
                 mbar_arrive_expect_tx(fix_full, 2 * kTile<D>);
-                load_tile<D>(sm + G::kFix, a.fa, fix_full, r0, kh, b);
-                load_tile<D>(sm + G::kFix + kTile<D>, a.fb, fix_full, r0, kh, b);
+                load_tile<D, kRows, kRows>(sm + G::kFix, a.fa, fix_full, r0, kh, b);
+                load_tile<D, kRows, kRows>(sm + G::kFix + kTile<D>, a.fb, fix_full, r0, kh, b);
             }
             int ja = 0, jb = 0;  // steps whose tiles have been asked for
             Walk wa = start, wb = start;
             auto load_a = [&]() {
                 if (ja >= nt) return;
                 mbar_arrive_expect_tx(a_full + ja % NA, kTile<D>);
-                load_tile<D>(sm + G::kA + ja % NA * kTile<D>, a.a, a_full + ja % NA, wa.t * kRows, KEYS ? kh * p.group + wa.g : kh, b);
+                load_tile<D, kRows, kRows>(sm + G::kA + ja % NA * kTile<D>, a.a, a_full + ja % NA, wa.t * kRows, KEYS ? kh * p.group + wa.g : kh, b);
                 ++ja;
                 wa.next();
             };
             auto load_b = [&]() {
                 if (jb >= nt) return;
                 mbar_arrive_expect_tx(b_full + jb % NB, kTile<D>);
-                load_tile<D>(sm + G::kB + jb % NB * kTile<D>, a.b, b_full + jb % NB, wb.t * kRows, KEYS ? kh * p.group + wb.g : kh, b);
+                load_tile<D, kRows, kRows>(sm + G::kB + jb % NB * kTile<D>, a.b, b_full + jb % NB, wb.t * kRows, KEYS ? kh * p.group + wb.g : kh, b);
                 ++jb;
                 wb.next();
             };
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
             const uint32_t idF = idesc_bf16_f32(kRows, kRows, false, false), idL = idesc_bf16_f32(kRows, 16 * last16, false, false);
             // sum += (operand in tensor memory) x (a tile that streams by)
             auto along = [&](uint32_t sum, uint32_t op, uint32_t tile, bool last, bool add) {
-                product_mn<kQuarter / 2>(sum, op, desc_mn(tile), idA, last ? last16 : 8, add);
+                product_mn<kQuarter / 2, kRows>(sum, op, desc_mn(tile), idA, last ? last16 : 8, add);
             };
             Walk w = start;
             bool last = w.t == around - 1;
@@ -435,9 +435,9 @@ cudaError_t launch(const CrossProblem &p, const float *delta, cudaStream_t strea
     a.tiles = ((KEYS ? p.s : p.rows) + kRows - 1) / kRows;
     a.by_tiles = Divide((uint32_t)a.tiles);
     TileMap k, v, q, g;
-    if (p.s > 0 && (!make_tile_map(&k, p.K, p.B, p.kv, p.s, p.d) || !make_tile_map(&v, p.V, p.B, p.kv, p.s, p.d)))
+    if (p.s > 0 && (!make_tile_map(&k, p.K, p.B, p.kv, p.s, p.d, kRows) || !make_tile_map(&v, p.V, p.B, p.kv, p.s, p.d, kRows)))
         return cudaErrorInvalidValue;
-    if (KEYS && p.n > 0 && (!make_tile_map(&q, p.Q, p.B, p.heads, p.n, p.d) || !make_tile_map(&g, p.dH, p.B, p.heads, p.n, p.d)))
+    if (KEYS && p.n > 0 && (!make_tile_map(&q, p.Q, p.B, p.heads, p.n, p.d, kRows) || !make_tile_map(&g, p.dH, p.B, p.heads, p.n, p.d, kRows)))
         return cudaErrorInvalidValue;
     a.a = KEYS ? q : k, a.b = KEYS ? g : v, a.fa = k, a.fb = v;
     static SmemOnce allow;

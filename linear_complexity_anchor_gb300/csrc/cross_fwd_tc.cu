@@ -38,18 +38,21 @@ using namespace cross_tc;
 
 constexpr float kSlack = 8.f;  // log2 of how far a maximum may be passed before O is rescaled
 
-template <int D, int NQ>
+// D columns (heads of 16 and 32 are 64), NQ row tiles, key tiles of KT.
+template <int D, int NQ, int KT>
 struct Geo {
+    static constexpr int kNH = KT / 64;                      // threads of a row, 64 columns of S each
     static constexpr int kNS = NQ == 1 && D == 128 ? 2 : 1;  // S buffers of a tile
-    static constexpr int kStages = NQ == 1 ? (D == 128 ? 3 : 2) : (D == 128 ? 2 : 4);  // of a K and a V tile
-    static constexpr int kPerSM = NQ == 1 && D == 64 ? 2 : 1;
-    static constexpr int kThreads = 256 * NQ + 64;
-    static constexpr int kQ = 0, kRing = NQ * kTile<D>, kEx = kRing + kStages * 2 * kTile<D>;
+    static constexpr int kStages = D == 128 ? (NQ == 1 ? 3 : 2) : (NQ == 1 ? 2 : 3);  // of a K and a V tile
+    static constexpr int kPerSM = D == 64 ? 2 : 1;
+    static constexpr int kRowWarps = 4 * kNH * NQ, kThreads = 32 * kRowWarps + 64;
+    static constexpr int kStage = 2 * kTile<D, KT>;
+    static constexpr int kQ = 0, kRing = NQ * kTile<D>, kEx = kRing + kStages * kStage;
     static constexpr int kBars = kEx + NQ * 2 * kRows * 4;
     static constexpr int kNBars = NQ + 2 * kStages + 2 * NQ * kNS + NQ + 4 * NQ + 1;
     static constexpr int kSmem = kBars + kNBars * 8 + 16 + 1024;
-    static constexpr uint32_t kColO = 128 * NQ * kNS, kCols = kColO + NQ * D <= 256 ? 256 : 512;
-    static_assert(kSmem * kPerSM + kPerSM * 1024 <= 228 * 1024, "shared memory");
+    static constexpr uint32_t kColO = KT * NQ * kNS, kCols = kColO + NQ * D <= 256 ? 256 : 512;
+    static_assert((kSmem + 1024) * kPerSM <= 228 * 1024, "shared memory");
     static_assert(kColO + NQ * D <= 512 && kCols * kPerSM <= 512, "tensor memory");
 };
 
@@ -61,11 +64,11 @@ struct FwdParams {
     Divide by_tiles;
 };
 
-template <int D, int NQ>
-__global__ void __launch_bounds__(Geo<D, NQ>::kThreads, Geo<D, NQ>::kPerSM)
+template <int D, int NQ, int KT>
+__global__ void __launch_bounds__(Geo<D, NQ, KT>::kThreads, Geo<D, NQ, KT>::kPerSM)
 cross_fwd_kernel(const __grid_constant__ FwdParams a) {
-    using G = Geo<D, NQ>;
-    constexpr int NS = G::kNS, ST = G::kStages;
+    using G = Geo<D, NQ, KT>;
+    constexpr int NS = G::kNS, ST = G::kStages, NH = G::kNH;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G::kBars);
@@ -74,7 +77,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + G::kNBars);
     const CrossProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kLoad = 8 * NQ, kIssue = 8 * NQ + 1;
+    constexpr int kLoad = G::kRowWarps, kIssue = kLoad + 1;
     const int bk = a.by_tiles.of((int)blockIdx.x), tile = (int)blockIdx.x - bk * a.tiles;
     const int b = p.by_kv.of(bk), kh = bk - b * p.kv, r0 = tile * NQ * kRows;
     const int left = p.rows - r0;                        // rows of this CTA that exist
@@ -83,12 +86,12 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
     if (threadIdx.x == 0) {
         for (int q = 0; q < NQ; ++q) {
             const int warps = min(max((left - q * kRows + 31) / 32, 1), 4);  // with a row that exists
-            mbar_init(q_full + q, 8);
+            mbar_init(q_full + q, 4 * NH);
             mbar_init(o_full + q, 1);
             for (int w = 0; w < 4; ++w) mbar_init(pair + 4 * q + w, 2);
             for (int s = 0; s < NS; ++s) {
                 mbar_init(s_full + q * NS + s, 1);
-                mbar_init(p_full + q * NS + s, 2 * warps);
+                mbar_init(p_full + q * NS + s, NH * warps);
             }
         }
         for (int s = 0; s < ST; ++s) {
@@ -106,7 +109,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
     grid_dependency_wait();
     grid_dependents_launch();
 
-    const int L = cross_length(p, b), key_tiles = (L + kRows - 1) / kRows;
+    const int L = cross_length(p, b), key_tiles = (L + KT - 1) / KT;
     const int t0 = (int)((long long)key_tiles * blockIdx.y / a.w.parts);
     const int nt = (int)((long long)key_tiles * (blockIdx.y + 1) / a.w.parts) - t0;
     unsigned int *error = &g_cross_fwd_error;
@@ -120,10 +123,10 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
             for (; i < nt + NS; ++i) {
                 const int st = i % ST;
                 if (i >= ST && !bwait(empty + st, (uint32_t)((i / ST - 1) & 1), error)) break;
-                uint8_t *dst = sm + G::kRing + st * 2 * kTile<D>;
-                mbar_arrive_expect_tx(full + st, (i < nt ? kTile<D> : 0) + (i >= NS ? kTile<D> : 0));
-                if (i >= NS) load_tile<D>(dst + kTile<D>, a.v, full + st, (t0 + i - NS) * kRows, kh, b);
-                if (i < nt) load_tile<D>(dst, a.k, full + st, (t0 + i) * kRows, kh, b);
+                uint8_t *dst = sm + G::kRing + st * G::kStage;
+                mbar_arrive_expect_tx(full + st, (i < nt ? kTile<D, KT> : 0) + (i >= NS ? kTile<D, KT> : 0));
+                if (i >= NS) load_tile<D, KT, KT>(dst + kTile<D, KT>, a.v, full + st, (t0 + i - NS) * KT, kh, b);
+                if (i < nt) load_tile<D, KT, KT>(dst, a.k, full + st, (t0 + i) * KT, kh, b);
             }
             // the CTA leaves only once its copies have landed
             for (int j = max(0, i - ST); j < i; ++j) bwait(full + j % ST, (uint32_t)((j / ST) & 1), error);
@@ -138,11 +141,11 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
             const int ksteps = (p.d + 15) / 16;
             const uint32_t base = smem_u32(sm), ring = base + G::kRing;
             const uint32_t idO = idesc_bf16_f32(kRows, p.d < D ? p.d : D, false, true);
-            const uint32_t idS = idesc_bf16_f32(kRows, kRows, false, false);
-            const int last16 = (min(kRows, L - (t0 + nt - 1) * kRows) + 15) / 16 * 16;  // keys of the last tile, in 16s
+            const uint32_t idS = idesc_bf16_f32(kRows, KT, false, false);
+            const int last16 = (min(KT, L - (t0 + nt - 1) * KT) + 15) / 16 * 16;  // keys of the last tile, in 16s
             const uint32_t idL = idesc_bf16_f32(kRows, last16, false, false);
-            const uint64_t qd0 = desc_k(base + G::kQ), kd0 = desc_k(ring), vd0 = desc_mn(ring + kTile<D>);
-            constexpr uint64_t kStep = 2 * kTile<D> / 16, kNextQ = kTile<D> / 16;  // of descriptors
+            const uint64_t qd0 = desc_k(base + G::kQ), kd0 = desc_k(ring), vd0 = desc_mn(ring + kTile<D, KT>);
+            constexpr uint64_t kStep = G::kStage / 16, kNextQ = kTile<D> / 16;  // of descriptors
             auto nothing = [] {};
             bool ok = true;
             for (int i = 0; i < NS && ok; ++i) {
@@ -152,7 +155,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                         if (i == 0) ok = bwait(q_full + q, 0u, error);
                         tc_fence_after();
                         if (!ok) break;
-                        product_k<D>(tmem + 128 * (q * NS + i), qd0 + q * kNextQ, kd0 + (i % ST) * kStep, i == nt - 1 ? idL : idS, ksteps, nothing);
+                        product_k<D>(tmem + KT * (q * NS + i), qd0 + q * kNextQ, kd0 + (i % ST) * kStep, i == nt - 1 ? idL : idS, ksteps, nothing);
                         umma_commit(s_full + q * NS + i);
                     }
                 }
@@ -160,17 +163,17 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
             }
             bool landed = false;  // this step's stage, as seen during the step before
             for (int j = 0; j < nt && ok; ++j) {
-                const int i = j + NS, st = i % ST, steps = j == nt - 1 ? last16 / 16 : 8;
+                const int i = j + NS, st = i % ST, steps = j == nt - 1 ? last16 / 16 : KT / 16;
                 const uint64_t vd = vd0 + st * kStep, kd = kd0 + st * kStep;
                 const uint32_t par = (uint32_t)((j / NS) & 1), id = i == nt - 1 ? idL : idS;
                 if (!landed && !(ok = bwait(full + st, (uint32_t)((i / ST) & 1), error))) break;
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
                     if (q >= nq) break;
-                    const uint32_t S = tmem + 128 * (q * NS + j % NS);
+                    const uint32_t S = tmem + KT * (q * NS + j % NS);
                     if (!(ok = bwait(p_full + q * NS + j % NS, par, error))) break;
                     tc_fence_after();
-                    product_mn<32>(tmem + G::kColO + q * D, S, vd, idO, steps, j > 0);
+                    product_mn<32, KT>(tmem + G::kColO + q * D, S, vd, idO, steps, j > 0);
                     if (NS == 2 || j == nt - 1) umma_commit(o_full + q);
                     if (i >= nt) continue;
                     product_k<D>(S, qd0 + q * kNextQ, kd, id, ksteps, [&] {
@@ -187,7 +190,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
     } else {
         // ------------------------------------------------------------------ rows
         // warp: tile q, columns 64 half .. + 63 of S, lanes 32 w4 .. + 31
-        const int q = warp >> 3, half = (warp >> 2) & 1, w4 = warp & 3;
+        const int q = warp / (4 * NH), half = NH == 2 ? (warp >> 2) & 1 : 0, w4 = warp & 3;
         const int row = w4 * 32 + lane;                      // of the tile
         const int r = r0 + q * kRows + row;                  // of the key head
         const bool mine = r < p.rows;
@@ -195,8 +198,8 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
         uint8_t *sQ = sm + G::kQ + q * kTile<D>;
         // (not 0, so that a masked score stays -infinity; a scale of 0 leaves no trace of any finite one)
         const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);
-        // this warp's 32 rows by half of the columns, 16 bytes a lane
-        constexpr int kLanes = D / 16;
+        // this warp's 32 rows by its part of the columns, 16 bytes a lane
+        constexpr int kLanes = D / (8 * NH), kPart = D / NH;
         const int my_row = lane / kLanes, my_chunk = half * kLanes + lane % kLanes;
         if (nt > 0) {
             // Q, negated for a negative scale
@@ -226,10 +229,10 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
         if (active && q < nq) {
             for (int j = 0; j < nt && ok; ++j) {
                 const int buf = q * NS + j % NS;
-                const uint32_t tS = tmem + lanes + 128 * buf + 64 * half;
+                const uint32_t tS = tmem + lanes + KT * buf + 64 * half;
                 if (!bwait(s_full + buf, (uint32_t)((j / NS) & 1), error)) { ok = false; break; }
                 tc_fence_after();
-                const int keys = min(kRows, L - (t0 + j) * kRows) - 64 * half;  // of this half that count (may be none)
+                const int keys = min(KT, L - (t0 + j) * KT) - 64 * half;  // of this half that count (may be none)
                 float s[64];
                 tmem_ld32(tS, s);
                 if (keys > 32) tmem_ld32(tS + 32, s + 32);
@@ -249,12 +252,14 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
 #pragma unroll
                 for (int x = 0; x < 8; ++x) t8[x] = fmaxf(t8[x], s[56 + x]);
                 float top = c * fmaxf(max3_f32(t8[0], t8[1], t8[2]), max3_f32(t8[3], t8[4], max3_f32(t8[5], t8[6], t8[7])));
-                __nv_bfloat16 *slot = ex + (j & 1) * 2 * kRows;
-                slot[half * kRows] = __float2bfloat16_rn(top);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(meet);
-                if (!bwait(meet, (uint32_t)(j & 1), error)) { ok = false; break; }
-                top = fmaxf(__bfloat162float(slot[0]), __bfloat162float(slot[kRows]));
+                if (NH == 2) {
+                    __nv_bfloat16 *slot = ex + (j & 1) * 2 * kRows;
+                    slot[half * kRows] = __float2bfloat16_rn(top);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(meet);
+                    if (!bwait(meet, (uint32_t)(j & 1), error)) { ok = false; break; }
+                    top = fmaxf(__bfloat162float(slot[0]), __bfloat162float(slot[kRows]));
+                }
                 if (j == 0) {
                     m = top;
                 } else {
@@ -268,7 +273,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                         if (grows) m = top;
                         l *= f;
 #pragma unroll 1
-                        for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 8) {
+                        for (int x = half * kPart; x < (half + 1) * kPart; x += 8) {
                             uint32_t o[8];
                             tmem_ld8(tO + x, o);
                             tmem_ld_wait();
@@ -299,12 +304,12 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                 f32x2_split(add_f32x2(z[0], z[1]), za, zb);
                 l += za + zb;
                 tmem_st_wait();
-                if (L < p.s && q == 0 && half == 0 && L - (t0 + j) * kRows < kRows) {
+                if (L < p.s && q == 0 && half == 0 && L - (t0 + j) * KT < KT) {
                     // the last tile's rows of V that do not count, once (the other tile's product comes later)
-                    const int i = j + NS, st = i % ST, from = L - (t0 + j) * kRows;
+                    const int i = j + NS, st = i % ST, from = L - (t0 + j) * KT;
                     if (!bwait(full + st, (uint32_t)((i / ST) & 1), error)) { ok = false; break; }
                     const int warps = min((left + 31) / 32, 4);
-                    for (int t = row; t < kRows; t += 32 * warps) zero_rows<D>(sm + G::kRing + (2 * st + 1) * kTile<D>, t, from, (from + 15) / 16 * 16);
+                    for (int t = row; t < KT; t += 32 * warps) zero_rows<D>(sm + G::kRing + st * G::kStage + kTile<D, KT>, t, from, (from + 15) / 16 * 16);
                     fence_proxy_async_smem();
                 }
                 tc_fence_before();
@@ -314,24 +319,26 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
             if (ok && nt > 0) {
                 // O, then the halves' sums (over the maxima, which all warps have read by then)
                 ok = bwait(o_full + q, (uint32_t)((NS == 2 ? nt - 1 : 0) & 1), error);
-                float *slot = reinterpret_cast<float *>(sm + G::kEx + q * 2 * kRows * 4) + row;
-                slot[half * kRows] = l;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(meet);
-                ok = ok && bwait(meet, (uint32_t)(nt & 1), error);
-                l = slot[0] + slot[kRows];
+                if (NH == 2) {
+                    float *slot = reinterpret_cast<float *>(sm + G::kEx + q * 2 * kRows * 4) + row;
+                    slot[half * kRows] = l;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(meet);
+                    ok = ok && bwait(meet, (uint32_t)(nt & 1), error);
+                    l = slot[0] + slot[kRows];
+                }
             }
             tc_fence_after();
         }
         if (active && q < nq && ok) {
             const long long f = cross_flat(p, b, kh, mine ? r : 0);
-            const int to = min(p.d, (half + 1) * (D / 2));
+            const int to = min(p.d, (half + 1) * kPart);
             if (a.w.parts > 1) {
                 const long long at = (long long)blockIdx.y * p.B * p.kv * p.rows + f;
                 if (mine && half == 0) a.w.ml[at] = make_float2(nt > 0 ? m : -INFINITY, l);
                 float o[32];
 #pragma unroll 1
-                for (int x = half * (D / 2); x < to; x += 32) {
+                for (int x = half * kPart; x < to; x += 32) {
                     if (nt > 0) {
                         tmem_ld32(tO + x, o);
                         tmem_ld_wait();
@@ -350,7 +357,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 float o[32];
 #pragma unroll 1
-                for (int x = half * (D / 2); x < to; x += 32) {
+                for (int x = half * kPart; x < to; x += 32) {
                     if (nt > 0) {
                         tmem_ld32(tO + x, o);
                         tmem_ld_wait();
@@ -424,9 +431,9 @@ __global__ void __launch_bounds__(kRows, Short<D>::kPerSM) cross_short_kernel(co
     grid_dependency_wait();
     if (row == 0) {
         mbar_arrive_expect_tx(k_full, kTile<D>);
-        load_tile<D>(sm + G::kK, a.k, k_full, 0, kh, b);
+        load_tile<D, kRows, kRows>(sm + G::kK, a.k, k_full, 0, kh, b);
         mbar_arrive_expect_tx(v_full, kTile<D>);
-        load_tile<D>(sm + G::kVv, a.v, v_full, 0, kh, b);
+        load_tile<D, kRows, kRows>(sm + G::kVv, a.v, v_full, 0, kh, b);
     }
     // Q, K and V of the CTA that will follow on this SM, into L2
     const long long then = (long long)blockIdx.x + G::kPerSM * kPlanSMs;
@@ -546,7 +553,7 @@ __global__ void __launch_bounds__(kRows, Short<D>::kPerSM) cross_short_kernel(co
         if (L > 0) {
             tc_fence_after();
             if (landed && ok)
-                product_mn<64>(tmem + G::kColO, tmem, desc_mn(smem_u32(sm + G::kVv)), idesc_bf16_f32(kRows, p.d < D ? p.d : D, false, true), l16, false);
+                product_mn<64, kRows>(tmem + G::kColO, tmem, desc_mn(smem_u32(sm + G::kVv)), idesc_bf16_f32(kRows, p.d < D ? p.d : D, false, true), l16, false);
             umma_commit(o_full);
         }
     }
@@ -597,20 +604,20 @@ bool is_short(const CrossProblem &p) { return p.s <= kRows; }
 // Two tiles a CTA where rows fill them; one for up to 128 rows.
 int tiles_per_cta(const CrossProblem &p) { return p.rows > kRows ? 2 : 1; }
 
-template <int D, int NQ>
+template <int D, int NQ, int KT>
 cudaError_t launch(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
-    using G = Geo<D, NQ>;
+    using G = Geo<D, NQ, KT>;
     FwdParams a;
     a.p = p;
     a.w = w;
     a.tiles = (p.rows + NQ * kRows - 1) / (NQ * kRows);
     a.by_tiles = Divide((uint32_t)a.tiles);
-    if (p.s > 0 && (!make_tile_map(&a.k, p.K, p.B, p.kv, p.s, p.d) || !make_tile_map(&a.v, p.V, p.B, p.kv, p.s, p.d)))
+    if (p.s > 0 && (!make_tile_map(&a.k, p.K, p.B, p.kv, p.s, p.d, KT) || !make_tile_map(&a.v, p.V, p.B, p.kv, p.s, p.d, KT)))
         return cudaErrorInvalidValue;
     static SmemOnce allow;
-    const cudaError_t e = allow(cross_fwd_kernel<D, NQ>, G::kSmem);
+    const cudaError_t e = allow(cross_fwd_kernel<D, NQ, KT>, G::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cross_fwd_kernel<D, NQ>, dim3(a.tiles * p.B * p.kv, w.parts), dim3(G::kThreads), G::kSmem, stream, a);
+    return launch_pdl(cross_fwd_kernel<D, NQ, KT>, dim3(a.tiles * p.B * p.kv, w.parts), dim3(G::kThreads), G::kSmem, stream, a);
 }
 
 template <int D>
@@ -620,7 +627,8 @@ cudaError_t launch_short(const CrossProblem &p, cudaStream_t stream) {
     a.w = CrossParts{nullptr, nullptr, 1};
     a.tiles = (p.rows + kRows - 1) / kRows;
     a.by_tiles = Divide((uint32_t)a.tiles);
-    if (!make_tile_map(&a.k, p.K, p.B, p.kv, p.s, p.d) || !make_tile_map(&a.v, p.V, p.B, p.kv, p.s, p.d)) return cudaErrorInvalidValue;
+    if (!make_tile_map(&a.k, p.K, p.B, p.kv, p.s, p.d, kRows) || !make_tile_map(&a.v, p.V, p.B, p.kv, p.s, p.d, kRows))
+        return cudaErrorInvalidValue;
     static SmemOnce allow;
     const cudaError_t e = allow(cross_short_kernel<D>, Short<D>::kSmem);
     if (e != cudaSuccess) return e;
@@ -631,7 +639,7 @@ cudaError_t launch_short(const CrossProblem &p, cudaStream_t stream) {
 
 namespace cross_tc {
 
-bool make_tile_map(TileMap *m, const CrossView &v, int B, int heads, int rows, int d) {
+bool make_tile_map(TileMap *m, const CrossView &v, int B, int heads, int rows, int d, int box_rows) {
     typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                                const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -650,7 +658,7 @@ bool make_tile_map(TileMap *m, const CrossView &v, int B, int heads, int rows, i
     // the stride of an axis of one entry is not used, but has to be one
     const cuuint64_t strides[3] = {(cuuint64_t)(rows > 1 ? v.sn : d) * 2, (cuuint64_t)(m->by_head ? v.sh : d) * 2,
                                    (cuuint64_t)(m->by_batch ? v.sb : d) * 2};
-    const cuuint32_t box[4] = {64, kRows, 1, 1}, one[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1}, one[4] = {1, 1, 1, 1};
     return encode(&m->map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(v.ptr), dims, strides, box, one,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -660,7 +668,7 @@ bool make_tile_map(TileMap *m, const CrossView &v, int B, int heads, int rows, i
 
 int cross_tc_parts(const CrossProblem &p) {
     if (is_short(p)) return 1;
-    const int nq = tiles_per_cta(p), per_sm = nq == 1 && p.d <= 64 ? 2 : 1;
+    const int nq = tiles_per_cta(p), per_sm = p.d <= 64 ? 2 : 1;
     const long long ctas = (long long)p.B * p.kv * ((p.rows + nq * kRows - 1) / (nq * kRows));
     const long long want = (long long)per_sm * kPlanSMs / std::max(1LL, ctas), most = (p.s + 2 * kRows - 1) / (2 * kRows);
     return (int)std::max(1LL, std::min(want, most));
@@ -669,8 +677,8 @@ int cross_tc_parts(const CrossProblem &p) {
 cudaError_t launch_cross_tc_forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
     const int nq = tiles_per_cta(p);
     if (is_short(p) && p.s > 0) return p.d > 64 ? launch_short<128>(p, stream) : launch_short<64>(p, stream);
-    if (p.d > 64) return nq == 2 ? launch<128, 2>(p, w, stream) : launch<128, 1>(p, w, stream);
-    return nq == 2 ? launch<64, 2>(p, w, stream) : launch<64, 1>(p, w, stream);
+    if (p.d > 64) return nq == 2 ? launch<128, 2, 128>(p, w, stream) : launch<128, 1, 128>(p, w, stream);
+    return nq == 2 ? launch<64, 2, 64>(p, w, stream) : launch<64, 1, 128>(p, w, stream);
 }
 
 cudaError_t cross_fwd_read_and_clear_error(unsigned *out) {

@@ -1,7 +1,7 @@
 // What the tensor-core kernels of cross attention share: bounded waits, 4-D tile loads, tiles in
 // swizzled shared memory, descriptors.
 //
-// A tile is 128 rows of 64 or 128 bf16 columns, in blocks of 64 columns: [128 rows][128 bytes]
+// A tile is 128 rows (tiles that stream by also 64, at 64 columns) of 64 or 128 bf16 columns, in blocks of 64 columns: [128 rows][128 bytes]
 // with the 128-byte swizzle (16-byte chunk c of row r at c ^ (r & 7)), as a TMA box lands.  One
 // copy serves as a K-major operand (contraction over the columns) and as an MN-major one
 // (contraction over the rows).  Heads of 16 and 32 columns are tiles of 64 whose other columns
@@ -21,7 +21,7 @@ constexpr int kBlock = kRows * 128;  // bytes of a 64-column block
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D> constexpr int kTile = kRows * D * 2;
+template <int D, int rows = kRows> constexpr int kTile = rows * D * 2;
 
 // A view as a tensor map (d, rows, heads, batch): an axis that does not move (a stride of 0, or
 // one entry) is an axis of one entry whose coordinate is multiplied by 0.
@@ -29,7 +29,7 @@ struct TileMap {
     CUtensorMap map;
     int by_head, by_batch;
 };
-bool make_tile_map(TileMap *m, const CrossView &v, int B, int heads, int rows, int d);
+bool make_tile_map(TileMap *m, const CrossView &v, int B, int heads, int rows, int d, int box_rows);
 
 // bit 0 of the error word, and false, once a wait has lasted kWaitNs.  (In line: a call in the loops
 // that wait costs them their registers, 62 -> 69 us in the forward of 8 heads, 9728 x 2048.)
@@ -68,12 +68,16 @@ __device__ __forceinline__ void prefetch_tile(const CUtensorMap *map, int c0, in
                  "r"(c2), "r"(c3)
                  : "memory");
 }
-// rows [row, row + 128) of one head; rows and columns outside the tensor are zero.  The caller has
-// announced kTile bytes on `bar`.
-template <int D>
+// a tile's rows from `row` on, of one head, in boxes of `box` rows; rows and columns outside the tensor
+// are zero.  The caller has announced the bytes on `bar`.
+template <int D, int rows, int box>
 __device__ __forceinline__ void load_tile(uint8_t *dst, const TileMap &m, uint64_t *bar, int row, int head, int b) {
+    static_assert(rows == kRows || D == 64, "a tile of more than one block has 128 rows");
 #pragma unroll
-    for (int q = 0; q < D / 64; ++q) tma_load_4d(dst + q * kBlock, &m.map, bar, 64 * q, row, head * m.by_head, b * m.by_batch);
+    for (int q = 0; q < D / 64; ++q)
+#pragma unroll
+        for (int r = 0; r < rows; r += box)
+            tma_load_4d(dst + q * kBlock + r * 128, &m.map, bar, 64 * q, row + r, head * m.by_head, b * m.by_batch);
 }
 
 // A warp's 32 rows of a view, `lanes` lanes of 16 bytes a row: calls f(i, row of the warp, offset of
@@ -130,12 +134,12 @@ __device__ __forceinline__ void product_k(uint32_t to, uint64_t a, uint64_t b, u
 }
 // sum (+)= A B: A bf16 in tensor memory, its columns in runs of 2 R (R columns of 32 bits, at the
 // start of their own 2 R columns), B over `steps` 16s of its rows
-template <int R>
+template <int R, int rows>
 __device__ __forceinline__ void product_mn(uint32_t sum, uint32_t a, uint64_t b, uint32_t id, int steps, bool add) {
     auto at = [&](int k) { return a + (uint32_t)(8 * k / R * 2 * R + 8 * k % R); };
-    if (steps == kRows / 16) {
+    if (steps == rows / 16) {
 #pragma unroll
-        for (int k = 0; k < kRows / 16; ++k) umma_bf16_tmem_a(sum, at(k), b + step_mn(k), id, k > 0 || add ? 1u : 0u);
+        for (int k = 0; k < rows / 16; ++k) umma_bf16_tmem_a(sum, at(k), b + step_mn(k), id, k > 0 || add ? 1u : 0u);
     } else {
 #pragma unroll 1
         for (int k = 0; k < steps; ++k) umma_bf16_tmem_a(sum, at(k), b + step_mn(k), id, k > 0 || add ? 1u : 0u);
