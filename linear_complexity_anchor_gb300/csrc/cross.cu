@@ -46,31 +46,22 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossProblem p, c
     if (p.lse && lane == 0) p.lse[f] = l == 0.f ? -INFINITY : M * (1.f / kLog2e) + logf(l);
 }
 
-// 8 columns of one row per thread, the row's threads (d / 8) next to one another in a warp.
-// Bound by memory.
-template <typename T>
+// 4 columns of one row per thread, the row's threads (d / 4) next to one another in a warp.  Bound by
+// memory.
 __global__ void __launch_bounds__(256) cross_delta_kernel(const CrossProblem p, float *delta, long long total) {
     grid_dependency_wait();
     grid_dependents_launch();
-    const int per = p.d / 8;
+    const int per = p.d / 4;
     const long long f = ((long long)blockIdx.x * 256 + threadIdx.x) / per;
-    const int c = (int)(threadIdx.x % per) * 8;
+    const int c = (int)(threadIdx.x % per) * 4;
     float s = 0.f;
     if (f < total) {
         const int r = (int)(f % p.rows);
         const long long bk = f / p.rows;
         const int b = (int)(bk / p.kv), k = (int)(bk - (long long)b * p.kv);
-        const T *h = (const T *)p.H.ptr + cross_row(p, p.H, b, k, r) + c;
-        const T *g = (const T *)p.dH.ptr + cross_row(p, p.dH, b, k, r) + c;
-        uint4 a[sizeof(T) / 2], e[sizeof(T) / 2];
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-            a[i] = reinterpret_cast<const uint4 *>(h)[i];
-            e[i] = reinterpret_cast<const uint4 *>(g)[i];
-        }
-        const T *x = reinterpret_cast<const T *>(a), *y = reinterpret_cast<const T *>(e);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s = fmaf(to_f32(x[i]), to_f32(y[i]), s);
+        const float4 h = *reinterpret_cast<const float4 *>((const float *)p.H.ptr + cross_row(p, p.H, b, k, r) + c);
+        const float4 g = *reinterpret_cast<const float4 *>((const float *)p.dH.ptr + cross_row(p, p.dH, b, k, r) + c);
+        s = fmaf(h.x, g.x, fmaf(h.y, g.y, fmaf(h.z, g.z, h.w * g.w)));
     }
     for (int o = per / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (f < total && c == 0) delta[f] = s;
@@ -87,9 +78,8 @@ cudaError_t launch_cross_join(const CrossProblem &p, const CrossParts &w, cudaSt
 
 cudaError_t launch_cross_delta(const CrossProblem &p, float *delta, cudaStream_t stream) {
     const long long total = (long long)p.B * p.kv * p.rows;
-    const dim3 grid((unsigned)((total * (p.d / 8) + 255) / 256));
-    return p.f32 ? launch_pdl(cross_delta_kernel<float>, grid, dim3(256), 0, stream, p, delta, total)
-                 : launch_pdl(cross_delta_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, p, delta, total);
+    const dim3 grid((unsigned)((total * (p.d / 4) + 255) / 256));
+    return launch_pdl(cross_delta_kernel, grid, dim3(256), 0, stream, p, delta, total);
 }
 
 namespace {
@@ -185,7 +175,7 @@ anchor_attn_status_t cross(const anchor_attn_cross_t *a, bool bwd, void *stream_
         if (queries) {
             if (!take(rows_bytes)) return ANCHOR_ATTN_ERR_ALLOC;
             delta = (float *)ws;
-            e = launch_cross_delta(p, delta, stream);
+            if (p.f32) e = launch_cross_delta(p, delta, stream);  // (bf16: its kernel makes D itself)
         }
         if (e == cudaSuccess)
             e = p.f32 ? launch_cross_simt_backward(p, delta, stream) : launch_cross_tc_backward(p, delta, stream);

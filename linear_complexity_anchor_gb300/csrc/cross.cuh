@@ -58,7 +58,7 @@ struct CrossParts {
     int parts;
 };
 cudaError_t launch_cross_join(const CrossProblem &p, const CrossParts &w, cudaStream_t stream);
-// D_r = dH_r . H_r, [B][heads][n]
+// D_r = dH_r . H_r, [B][heads][n] (fp32)
 cudaError_t launch_cross_delta(const CrossProblem &p, float *delta, cudaStream_t stream);
 
 // CUDA cores, fp32 arithmetic
@@ -69,7 +69,7 @@ cudaError_t launch_cross_simt_backward(const CrossProblem &p, const float *delta
 // tensor cores, bf16
 int cross_tc_parts(const CrossProblem &p);
 cudaError_t launch_cross_tc_forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream);
-cudaError_t launch_cross_tc_backward(const CrossProblem &p, const float *delta, cudaStream_t stream);
+cudaError_t launch_cross_tc_backward(const CrossProblem &p, float *delta, cudaStream_t stream);  // writes delta
 cudaError_t cross_bwd_read_and_clear_error(unsigned *out);
 cudaError_t cross_fwd_read_and_clear_error(unsigned *out);
 

@@ -11,15 +11,17 @@
 //   keys      a tile of 128 rows of K and V stays, the queries of all heads that share it
 //             stream by: S^T = K Q^T, dP^T = V dH^T, dV += P^T dH, dK += dS^T Q
 //
-// Sixteen row warps: warp w has lanes 32 (w % 4) .. + 31 of tensor memory (one row a thread) and
-// columns 32 (w / 4) .. + 31.  P^T and dS go back to tensor memory as bf16 operands, each warp's
+// Streaming tiles of W = 128 rows at d = 128, where S, dP, dV and dK fill tensor memory; of 64 below,
+// which leaves room for two CTAs an SM (one fetches its rows while the other computes).  Row warps
+// take 32 columns of S and dP each, a row a thread: warp w has lanes 32 (w % 4) .. + 31 of tensor memory
+// and columns 32 (w / 4) .. + 31.  P^T and dS go back to tensor memory as bf16 operands, each warp's
 // over columns that it has read itself.  The products are issued so that the tensor cores have
 // work while the rows are between two of their steps:
 //   keys      after P^T(j): dV += P^T(j) dH, S^T(j + 1)      while the rows make dS^T(j)
 //             after dS^T(j): dK += dS^T(j) Q, dP^T(j + 1)    while the rows make P^T(j + 1)
 //   queries   after S(j) is read: S(j + 1);  after dS(j): dQ += dS(j) K, dP(j + 1)
-// (a product that overwrites an operand is issued after the one that reads it).  S, dP, dV and dK
-// fill tensor memory at d = 128.  P and dS are rounded to bf16, the operands' type; S, dP, P in dS,
+// (a product that overwrites an operand is issued after the one that reads it).  The queries' kernel
+// also makes D, of the rows of dH that it loads, for both.  P and dS are rounded to bf16, the operands' type; S, dP, P in dS,
 // and all sums are fp32.
 // States from the length on: P and dS are zero there by select, and rows of K that meet a zero of dS
 // are zeroed in shared memory.
@@ -35,27 +37,33 @@ namespace {
 
 using namespace cross_tc;
 
-constexpr int kRowWarps = 16, kQuarter = 32;  // columns of a row warp
-constexpr int kLoad = kRowWarps, kStat = kRowWarps + 1, kIssue = kRowWarps + 2;
-constexpr int kThreads = 32 * (kRowWarps + 3);
-constexpr uint32_t kColS = 0, kColP = 128, kColA = 256;  // S, dP, then the sums
+constexpr int kSlice = 32;  // columns of S and dP that a row warp takes
 
-template <int D>
+// D columns (heads of 16 and 32 are 64), streaming tiles of W rows.
+template <int D, int W>
 struct Geo {
+    static constexpr int kSlices = W / kSlice, kRowWarps = 4 * kSlices;
+    static constexpr int kLoad = kRowWarps, kStat = kRowWarps + 1, kIssue = kRowWarps + 2, kThreads = 32 * (kRowWarps + 3);
+    static constexpr int kPerSM = D == 64 ? 2 : 1;
     // Slots of the two tiles that stream by (Q or K, dH or V).  The first of step j is in use from the
     // middle of step j - 1 to the end of step j, the second from the end of step j - 1: with one slot
     // more for the first, both are loaded a step and more ahead.
-    static constexpr int kNB = D == 128 ? 2 : 3, kNA = kNB + 1;
-    static constexpr int kFix = 0, kA = 2 * kTile<D>, kB = kA + kNA * kTile<D>, kStatB = kB + kNB * kTile<D>;  // lse, D of 128 columns
+    static constexpr int kNB = D == 128 ? 2 : 4, kNA = kNB + 1;
+    static constexpr int kSlot = kTile<D, W>;
+    static constexpr int kFix = 0, kA = 2 * kTile<D>, kB = kA + kNA * kSlot;
+    static constexpr int kStatB = kB + kNB * kSlot;  // keys: lse, D of W columns; queries: parts of D of 128 rows
     static constexpr int kBars = kStatB + 2 * kRows * 4;
     static constexpr int kNBars = kNA + 2 * kNB + 11;
     static constexpr int kSmem = kBars + kNBars * 8 + 16 + 1024;
-    static_assert(kSmem <= 227 * 1024, "shared memory");
+    static constexpr uint32_t kColS = 0, kColP = W, kColA = 2 * W;  // S, dP, then the sums
+    static constexpr uint32_t kCols = 2 * W + 2 * D;                // of tensor memory
+    static_assert((kSmem + 1024) * kPerSM <= 228 * 1024, "shared memory");
+    static_assert(kCols * kPerSM <= 512 && (kCols == 256 || kCols == 512), "tensor memory");
 };
 
 struct BwdParams {
     CrossProblem p;
-    const float *delta;
+    float *delta;    // D: written by the queries' kernel, read by the keys'
     TileMap a, b;  // queries: K, V stream; keys: Q, dH stream
     TileMap fa, fb;  // keys: K, V stay
     int tiles;
@@ -63,9 +71,11 @@ struct BwdParams {
 };
 
 // KEYS: see above
-template <int D, bool KEYS>
-__global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_constant__ BwdParams a) {
-    using G = Geo<D>;
+template <int D, bool KEYS, int W>
+__global__ void __launch_bounds__(Geo<D, W>::kThreads, Geo<D, W>::kPerSM) cross_bwd_kernel(const __grid_constant__ BwdParams a) {
+    using G = Geo<D, W>;
+    constexpr int kRowWarps = G::kRowWarps, kLoad = G::kLoad, kStat = G::kStat, kIssue = G::kIssue;
+    constexpr uint32_t kColS = G::kColS, kColP = G::kColP, kColA = G::kColA;
     constexpr int NA = G::kNA, NB = G::kNB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -100,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
         mbar_init(done, 1);
         fence_mbar_init();
     }
-    if (warp == kIssue) tmem_alloc(s_tmem, 512);
+    if (warp == kIssue) tmem_alloc(s_tmem, G::kCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -110,8 +120,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
 
     const int L = cross_length(p, b);
     // steps over the tiles that stream by: keys of the entry, or the queries of each head in turn
-    const int per_head = (p.n + kRows - 1) / kRows;
-    const int nt = KEYS ? (r0 < L ? p.group * per_head : 0) : (L + kRows - 1) / kRows;
+    const int per_head = (p.n + W - 1) / W;
+    const int nt = KEYS ? (r0 < L ? p.group * per_head : 0) : (L + W - 1) / W;
     // A walk over the steps: tile t of head g (without divisions, which the issuing thread would wait
     // for).
     struct Walk {
@@ -126,28 +136,28 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
     const int around = KEYS ? per_head : nt;
     const Walk start{0, 0, around, KEYS ? p.group : 1};
     // columns of a tile that exist
-    auto width = [&](int t) { return min(kRows, (KEYS ? p.n : L) - t * kRows); };
+    auto width = [&](int t) { return min(W, (KEYS ? p.n : L) - t * W); };
 
     if (warp == kLoad) {
         if (lane == 0 && nt > 0) {
             if (KEYS) {
                 mbar_arrive_expect_tx(fix_full, 2 * kTile<D>);
-                load_tile<D, kRows, kRows>(sm + G::kFix, a.fa, fix_full, r0, kh, b);
-                load_tile<D, kRows, kRows>(sm + G::kFix + kTile<D>, a.fb, fix_full, r0, kh, b);
+                load_tile<D, kRows, W>(sm + G::kFix, a.fa, fix_full, r0, kh, b);
+                load_tile<D, kRows, W>(sm + G::kFix + kTile<D>, a.fb, fix_full, r0, kh, b);
             }
             int ja = 0, jb = 0;  // steps whose tiles have been asked for
             Walk wa = start, wb = start;
             auto load_a = [&]() {
                 if (ja >= nt) return;
-                mbar_arrive_expect_tx(a_full + ja % NA, kTile<D>);
-                load_tile<D, kRows, kRows>(sm + G::kA + ja % NA * kTile<D>, a.a, a_full + ja % NA, wa.t * kRows, KEYS ? kh * p.group + wa.g : kh, b);
+                mbar_arrive_expect_tx(a_full + ja % NA, G::kSlot);
+                load_tile<D, W, W>(sm + G::kA + ja % NA * G::kSlot, a.a, a_full + ja % NA, wa.t * W, KEYS ? kh * p.group + wa.g : kh, b);
                 ++ja;
                 wa.next();
             };
             auto load_b = [&]() {
                 if (jb >= nt) return;
-                mbar_arrive_expect_tx(b_full + jb % NB, kTile<D>);
-                load_tile<D, kRows, kRows>(sm + G::kB + jb % NB * kTile<D>, a.b, b_full + jb % NB, wb.t * kRows, KEYS ? kh * p.group + wb.g : kh, b);
+                mbar_arrive_expect_tx(b_full + jb % NB, G::kSlot);
+                load_tile<D, W, W>(sm + G::kB + jb % NB * G::kSlot, a.b, b_full + jb % NB, wb.t * W, KEYS ? kh * p.group + wb.g : kh, b);
                 ++jb;
                 wb.next();
             };
@@ -171,16 +181,17 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
     } else if (warp == kStat) {
         if (KEYS) {
             // - lse (in log2) and - D of each step's columns, read a step ahead; columns that do not exist: P = 0
-            float next[8];
+            constexpr int kX = W / 32;
+            float next[2 * kX];
             Walk w = start;
             auto fetch = [&]() {
-                const int i0 = w.t * kRows;
+                const int i0 = w.t * W;
                 const long long f = ((long long)b * p.heads + kh * p.group + w.g) * p.n + i0;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
+                for (int x = 0; x < kX; ++x) {
                     const bool in = i0 + 32 * x + lane < p.n;
                     next[x] = in ? -p.lse[f + 32 * x + lane] * kLog2e : -INFINITY;
-                    next[4 + x] = in ? -a.delta[f + 32 * x + lane] : 0.f;
+                    next[kX + x] = in ? -a.delta[f + 32 * x + lane] : 0.f;
                 }
                 w.next();
             };
@@ -189,12 +200,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
             for (int j = 0; j < nt && ok; ++j) {
                 if (j > 0 && !(ok = bwait(lse_empty, (uint32_t)((j - 1) & 1), error))) break;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) stat[32 * x + lane] = next[x];
+                for (int x = 0; x < kX; ++x) stat[32 * x + lane] = next[x];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(lse_full);
                 if (j > 0 && !(ok = bwait(d_empty, (uint32_t)((j - 1) & 1), error))) break;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) stat[kRows + 32 * x + lane] = next[4 + x];
+                for (int x = 0; x < kX; ++x) stat[W + 32 * x + lane] = next[kX + x];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(d_full);
                 if (j + 1 < nt) fetch();
@@ -209,17 +220,17 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
             const uint64_t f0 = desc_k(base + G::kFix), f1 = desc_k(base + G::kFix + kTile<D>);
             // (a commit takes this thread 70 cycles, a wait on a complete barrier 130: one barrier frees both
             // tiles of a step, and that the next products' tiles have landed is looked at while these run)
-            auto slot_a = [&](int j) { return base + G::kA + j % NA * kTile<D>; };
-            auto slot_b = [&](int j) { return base + G::kB + j % NB * kTile<D>; };
+            auto slot_a = [&](int j) { return base + G::kA + j % NA * G::kSlot; };
+            auto slot_b = [&](int j) { return base + G::kB + j % NB * G::kSlot; };
             uint64_t *const a_bar = a_full, *const b_bar = b_full;
             auto a_par = [](int j) { return (uint32_t)((j / NA) & 1); };
             auto b_par = [](int j) { return (uint32_t)((j / NB) & 1); };
             // columns of the walk's tiles in 16s: all but a head's (an entry's) last are full
             const int last16 = (width(around - 1) + 15) / 16;
-            const uint32_t idF = idesc_bf16_f32(kRows, kRows, false, false), idL = idesc_bf16_f32(kRows, 16 * last16, false, false);
+            const uint32_t idF = idesc_bf16_f32(kRows, W, false, false), idL = idesc_bf16_f32(kRows, 16 * last16, false, false);
             // sum += (operand in tensor memory) x (a tile that streams by)
             auto along = [&](uint32_t sum, uint32_t op, uint32_t tile, bool last, bool add) {
-                product_mn<kQuarter / 2, kRows>(sum, op, desc_mn(tile), idA, last ? last16 : 8, add);
+                product_mn<kSlice / 2, W>(sum, op, desc_mn(tile), idA, last ? last16 : W / 16, add);
             };
             Walk w = start;
             bool last = w.t == around - 1;
@@ -274,11 +285,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
         const uint64_t c = f32x2(p.scale * kLog2e, p.scale * kLog2e);
         uint64_t lse2 = f32x2(-INFINITY, -INFINITY), dl = 0;  // - lse (in log2) and - D of this row, twice
         if (!KEYS && nt > 0) {
-            // quarters 0 and 1 load the 128 rows of Q, by halves of the columns, 2 and 3 those of dH
-            constexpr int kLanes = D / 16;
-            const CrossView &v = quarter >= 2 ? p.dH : p.Q;
-            uint8_t *dst = sm + G::kFix + (quarter >> 1) * kTile<D>;
-            const int ch = (quarter & 1) * kLanes + lane % kLanes;
+            // The first half of the warps load the 128 rows of Q, each its part of the columns, the others
+            // those of dH, and of H for D = dH . H: over the lanes of a row, then over the parts.
+            constexpr int kParts = G::kSlices / 2, kLanes = D / (8 * kParts);
+            const bool second = quarter >= kParts;
+            const int part = quarter % kParts, ch = part * kLanes + lane % kLanes;
+            const CrossView &v = second ? p.dH : p.Q;
+            uint8_t *dst = sm + G::kFix + (second ? kTile<D> : 0);
             uint4 x[kLanes];
             each_row<kLanes>(mine ? cross_row(p, v, b, kh, r) : -1, v.sn, [&](int i, int, long long o) {
                 x[i] = make_uint4(0, 0, 0, 0);
@@ -287,21 +300,45 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
 #pragma unroll
             for (int i = 0; i < kLanes; ++i)
                 *reinterpret_cast<uint4 *>(dst + chunk_at(w4 * 32 + i * (32 / kLanes) + lane / kLanes, ch)) = x[i];
+            if (second) {
+                uint4 y[kLanes];
+                each_row<kLanes>(mine ? cross_row(p, p.H, b, kh, r) : -1, p.H.sn, [&](int i, int, long long o) {
+                    y[i] = make_uint4(0, 0, 0, 0);
+                    if (o >= 0 && ch * 8 < p.d) y[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.H.ptr + o + ch * 8);
+                });
+#pragma unroll
+                for (int i = 0; i < kLanes; ++i) {
+                    const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+                    float sum = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        sum = fmaf(__uint_as_float(u[k] << 16), __uint_as_float(w[k] << 16), sum);
+                        sum = fmaf(__uint_as_float(u[k] & 0xffff0000u), __uint_as_float(w[k] & 0xffff0000u), sum);
+                    }
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (lane % kLanes == 0) stat[part * kRows + w4 * 32 + i * (32 / kLanes) + lane / kLanes] = sum;
+                }
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(fix_full);
             if (mine) {
-                const long long f = cross_flat(p, b, kh, r);
-                const float x = -p.lse[f] * kLog2e, y = -a.delta[f];
-                lse2 = f32x2(x, x), dl = f32x2(y, y);
+                const float x2 = -p.lse[cross_flat(p, b, kh, r)] * kLog2e;
+                lse2 = f32x2(x2, x2);
             }
+            bwait(fix_full, 0u, error);
+            float dv = stat[row];
+            if (kParts == 2) dv += stat[kRows + row];
+            if (mine && quarter == 0) a.delta[cross_flat(p, b, kh, r)] = dv;
+            dl = f32x2(-dv, -dv);
         }
-        const uint32_t tS = trow + kColS + kQuarter * quarter, tP = trow + kColP + kQuarter * quarter;
+        const uint32_t tS = trow + kColS + kSlice * quarter, tP = trow + kColP + kSlice * quarter;
         bool ok = true;
         Walk walk = start;
         for (int j = 0; j < nt && ok; ++j, walk.next()) {
-            const int cols = width(walk.t) - kQuarter * quarter;  // of this quarter that exist (may be none)
-            const float *st = stat + kQuarter * quarter;
+            const int cols = width(walk.t) - kSlice * quarter;  // of this quarter that exist (may be none)
+            const float *st = stat + kSlice * quarter;
             float e[32];
             if (!bwait(s_full, (uint32_t)(j & 1), error)) { ok = false; break; }
             if (KEYS && !bwait(lse_full, (uint32_t)(j & 1), error)) { ok = false; break; }
@@ -317,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
 #pragma unroll
                 for (int y = 0; y < 4; ++y) e[x + y] = ex2(e[x + y]);
             }
-            const bool cut = !mine || (!KEYS && cols < 32);
+            const bool cut = !mine || (!KEYS && cols < kSlice);
             if (cut) {
 #pragma unroll
                 for (int x = 0; x < 32; ++x)
@@ -348,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
 #pragma unroll
                 for (int y = 0; y < 32; y += 4) {
                     ulonglong2 d4 = make_ulonglong2(dl, dl);
-                    if (KEYS) d4 = *reinterpret_cast<const ulonglong2 *>(st + kRows + y);
+                    if (KEYS) d4 = *reinterpret_cast<const ulonglong2 *>(st + W + y);
                     f32x2_split(mul_f32x2(f32x2(e[y], e[y + 1]), add_f32x2(f32x2(g[y], g[y + 1]), d4.x)), g[y], g[y + 1]);
                     f32x2_split(mul_f32x2(f32x2(e[y + 2], e[y + 3]), add_f32x2(f32x2(g[y + 2], g[y + 3]), d4.y)), g[y + 2], g[y + 3]);
                 }
@@ -362,10 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
                 tmem_st16(tP, u);
             }
             tmem_st_wait();
-            if (!KEYS && walk.t == nt - 1 && quarter == 0 && L % kRows && L < p.s) {
+            if (!KEYS && walk.t == nt - 1 && quarter == 0 && L % W && L < p.s) {
                 // the last tile's rows of K that do not count (S has read them)
                 if (!bwait(a_full + j % NA, (uint32_t)((j / NA) & 1), error)) { ok = false; break; }
-                zero_rows<D>(sm + G::kA + j % NA * kTile<D>, row, L % kRows, (L % kRows + 15) / 16 * 16);
+                zero_rows<D>(sm + G::kA + j % NA * G::kSlot, row, L % W, (L % W + 15) / 16 * 16);
                 fence_proxy_async_smem();
             }
             tc_fence_before();
@@ -377,14 +414,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
         }
         if (ok && nt > 0) ok = bwait(acc, 0u, error);
         tc_fence_after();
-        // Rows out through shared memory (the tiles that stayed are not needed any more).  Keys: quarters
-        // 0 and 1 halves of dV's columns, 2 and 3 of dK's; queries: quarters of dQ's at d = 128, halves
-        // below.
-        const bool second = KEYS && quarter >= 2;
+        // Rows out through shared memory (the tiles that stayed are not needed any more).  Keys: the first
+        // half of the warps dV, the others dK, each its part of the columns; queries: all of them dQ.
+        constexpr int kParts = KEYS ? G::kSlices / 2 : G::kSlices, kCols = D / kParts;  // of a warp
+        const bool second = KEYS && quarter >= kParts;
         const float by = KEYS && !second ? 1.f : p.scale;
         uint8_t *stage = sm + G::kFix + (second ? kTile<D> : 0);
-        constexpr int kCols = KEYS || D == 64 ? D / 2 : D / 4;  // of a warp
-        const int part = KEYS ? quarter & 1 : quarter, from = part * kCols, to = min(p.d, from + kCols);
+        const int from = quarter % kParts * kCols, to = min(p.d, from + kCols);
         if (ok && from < p.d) {
 #pragma unroll 1
             for (int x = from; x < to; x += 32) {
@@ -422,41 +458,41 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const __grid_con
     __syncthreads();
     if (warp == kIssue) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, G::kCols);
     }
 }
 
-template <int D, bool KEYS>
-cudaError_t launch(const CrossProblem &p, const float *delta, cudaStream_t stream) {
-    using G = Geo<D>;
+template <int D, bool KEYS, int W>
+cudaError_t launch(const CrossProblem &p, float *delta, cudaStream_t stream) {
+    using G = Geo<D, W>;
     BwdParams a;
     a.p = p;
     a.delta = delta;
     a.tiles = ((KEYS ? p.s : p.rows) + kRows - 1) / kRows;
     a.by_tiles = Divide((uint32_t)a.tiles);
     TileMap k, v, q, g;
-    if (p.s > 0 && (!make_tile_map(&k, p.K, p.B, p.kv, p.s, p.d, kRows) || !make_tile_map(&v, p.V, p.B, p.kv, p.s, p.d, kRows)))
+    if (p.s > 0 && (!make_tile_map(&k, p.K, p.B, p.kv, p.s, p.d, W) || !make_tile_map(&v, p.V, p.B, p.kv, p.s, p.d, W)))
         return cudaErrorInvalidValue;
-    if (KEYS && p.n > 0 && (!make_tile_map(&q, p.Q, p.B, p.heads, p.n, p.d, kRows) || !make_tile_map(&g, p.dH, p.B, p.heads, p.n, p.d, kRows)))
+    if (KEYS && p.n > 0 && (!make_tile_map(&q, p.Q, p.B, p.heads, p.n, p.d, W) || !make_tile_map(&g, p.dH, p.B, p.heads, p.n, p.d, W)))
         return cudaErrorInvalidValue;
     a.a = KEYS ? q : k, a.b = KEYS ? g : v, a.fa = k, a.fb = v;
     static SmemOnce allow;
-    const cudaError_t e = allow(cross_bwd_kernel<D, KEYS>, G::kSmem);
+    const cudaError_t e = allow(cross_bwd_kernel<D, KEYS, W>, G::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cross_bwd_kernel<D, KEYS>, dim3(a.tiles * p.B * p.kv), dim3(kThreads), G::kSmem, stream, a);
+    return launch_pdl(cross_bwd_kernel<D, KEYS, W>, dim3(a.tiles * p.B * p.kv), dim3(G::kThreads), G::kSmem, stream, a);
 }
 
-template <int D>
-cudaError_t backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
-    cudaError_t e = p.rows > 0 ? launch<D, false>(p, delta, stream) : cudaSuccess;
-    if (e == cudaSuccess && p.s > 0) e = launch<D, true>(p, delta, stream);
+template <int D, int W>
+cudaError_t backward(const CrossProblem &p, float *delta, cudaStream_t stream) {
+    cudaError_t e = p.rows > 0 ? launch<D, false, W>(p, delta, stream) : cudaSuccess;
+    if (e == cudaSuccess && p.s > 0) e = launch<D, true, W>(p, delta, stream);
     return e;
 }
 
 }  // namespace
 
-cudaError_t launch_cross_tc_backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
-    return p.d > 64 ? backward<128>(p, delta, stream) : backward<64>(p, delta, stream);
+cudaError_t launch_cross_tc_backward(const CrossProblem &p, float *delta, cudaStream_t stream) {
+    return p.d > 64 ? backward<128, 128>(p, delta, stream) : backward<64, 64>(p, delta, stream);
 }
 
 cudaError_t cross_bwd_read_and_clear_error(unsigned *out) {
