@@ -10,40 +10,48 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// One warp per row, lanes over the columns.  H = sum_parts o 2^(m - M) / sum_parts l 2^(m - M),
-// the parts in order.  Reads the parts once: bound by memory, and small next to K and V (a part
-// has two tiles of keys at least for each row tile).
+// One CTA per row: H = sum_parts o 2^(m - M) / sum_parts l 2^(m - M).  A warp takes every eighth part,
+// lanes over the columns, and the warps' sums are added in order (with one warp for all parts its loads
+// followed one another: 84 us for 152 parts).  Bound by the latency of a few loads.
 template <typename T>
 __global__ void __launch_bounds__(256) cross_join_kernel(const CrossProblem p, const CrossParts w, long long total) {
+    __shared__ float s_o[8][128];
+    __shared__ float s_l[8];
     grid_dependency_wait();
     grid_dependents_launch();
-    const long long f = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (f >= total) return;
+    const long long f = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float M = -INFINITY;
-    for (int q = lane; q < w.parts; q += 32) M = fmaxf(M, w.ml[q * total + f].x);
+    for (int q = lane; q < w.parts; q += 32) M = fmaxf(M, w.ml[q * total + f].x);  // every warp for itself
     M = warp_max(M);
     const float shift = M == -INFINITY ? 0.f : M;
     float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    const int per = p.d / 32 > 0 ? p.d / 32 : 1;  // columns of a lane (the upper lanes idle at d = 16)
-    const bool on = lane * per < p.d;
-    for (int q = 0; q < w.parts; ++q) {
+#pragma unroll 4
+    for (int q = warp; q < w.parts; q += 8) {
         const float2 ml = w.ml[q * total + f];
         const float k = exp2f(ml.x - shift);
         l += ml.y * k;
-        if (!on) continue;
-        const float *src = w.o + (q * total + f) * p.d + lane * per;
-        for (int j = 0; j < per; ++j) o[j] = fmaf(src[j], k, o[j]);
+        const float *src = w.o + (q * total + f) * p.d;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (32 * j + lane < p.d) o[j] = fmaf(src[32 * j + lane], k, o[j]);
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s_o[warp][32 * j + lane] = o[j];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    const int c = threadIdx.x;
+    if (c >= p.d) return;
+    float sum = 0.f;
+    l = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum += s_o[q][c], l += s_l[q];
     const int r = (int)(f % p.rows);
     const long long bk = f / p.rows;
     const int b = (int)(bk / p.kv), k = (int)(bk - (long long)b * p.kv);
     const float inv = l == 0.f ? 0.f : 1.f / l;  // no state at all
-    if (on) {
-        T *H = (T *)p.H.ptr + cross_row(p, p.H, b, k, r) + lane * per;
-        for (int j = 0; j < per; ++j) H[j] = from_f32<T>(o[j] * inv);
-    }
-    if (p.lse && lane == 0) p.lse[f] = l == 0.f ? -INFINITY : M * (1.f / kLog2e) + logf(l);
+    ((T *)p.H.ptr)[cross_row(p, p.H, b, k, r) + c] = from_f32<T>(sum * inv);
+    if (p.lse && c == 0) p.lse[f] = l == 0.f ? -INFINITY : M * (1.f / kLog2e) + logf(l);
 }
 
 // 4 columns of one row per thread, the row's threads (d / 4) next to one another in a warp.  Bound by
@@ -71,7 +79,7 @@ __global__ void __launch_bounds__(256) cross_delta_kernel(const CrossProblem p, 
 
 cudaError_t launch_cross_join(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
     const long long total = (long long)p.B * p.kv * p.rows;
-    const dim3 grid((unsigned)((total + 7) / 8));
+    const dim3 grid((unsigned)total);
     return p.f32 ? launch_pdl(cross_join_kernel<float>, grid, dim3(256), 0, stream, p, w, total)
                  : launch_pdl(cross_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, p, w, total);
 }
@@ -161,15 +169,17 @@ anchor_attn_status_t cross(const anchor_attn_cross_t *a, bool bwd, void *stream_
         return false;
     };
     if (!bwd) {
-        CrossParts w = {nullptr, nullptr, p.f32 ? cross_simt_parts(p) : cross_tc_parts(p)};
-        if (w.parts > 1) {
+        CrossPlan plan = p.f32 ? CrossPlan{cross_simt_parts(p), true} : cross_tc_plan(p);
+        CrossParts w = {nullptr, nullptr, plan.parts};
+        const bool join = plan.parts > 1 && plan.workspace;
+        if (join) {
             const size_t total = (size_t)p.B * p.kv * p.rows * w.parts;
             if (!take(total * (p.d * 4 + 8))) return ANCHOR_ATTN_ERR_ALLOC;
             w.o = (float *)ws;
             w.ml = (float2 *)(w.o + total * p.d);
         }
         e = p.f32 ? launch_cross_simt_forward(p, w, stream) : launch_cross_tc_forward(p, w, stream);
-        if (e == cudaSuccess && w.parts > 1) e = launch_cross_join(p, w, stream);
+        if (e == cudaSuccess && join) e = launch_cross_join(p, w, stream);
     } else {
         float *delta = nullptr;
         if (queries) {

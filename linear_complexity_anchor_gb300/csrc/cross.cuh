@@ -67,7 +67,11 @@ cudaError_t launch_cross_simt_forward(const CrossProblem &p, const CrossParts &w
 cudaError_t launch_cross_simt_backward(const CrossProblem &p, const float *delta, cudaStream_t stream);
 
 // tensor cores, bf16
-int cross_tc_parts(const CrossProblem &p);
+struct CrossPlan {
+    int parts;       // of the key axis
+    bool workspace;  // their sums go through a workspace and a second launch
+};
+CrossPlan cross_tc_plan(const CrossProblem &p);
 cudaError_t launch_cross_tc_forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream);
 cudaError_t launch_cross_tc_backward(const CrossProblem &p, float *delta, cudaStream_t stream);  // writes delta
 cudaError_t cross_bwd_read_and_clear_error(unsigned *out);

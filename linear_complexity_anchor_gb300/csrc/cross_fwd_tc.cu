@@ -24,6 +24,7 @@
 // of rounding V); the row sum is taken over the fp32 values.
 // Keys from the entry's length on: S masked by select, so that nothing they hold matters, and
 // their rows of V are zeroed in shared memory (0 times an infinity is not 0).
+#include "cluster.cuh"
 #include "cross_tc.cuh"
 
 #include <math.h>
@@ -51,6 +52,9 @@ struct Geo {
     static constexpr int kBars = kEx + NQ * 2 * kRows * 4;
     static constexpr int kNBars = NQ + 2 * kStages + 2 * NQ * kNS + NQ + 4 * NQ + 1;
     static constexpr int kSmem = kBars + kNBars * 8 + 16 + 1024;
+    // the join's sums and (m, l), over the ring
+    static constexpr int kJoinPitch = D + 4, kJoinMl = kRing + kRows * kJoinPitch * 4;
+    static_assert(NQ == 2 || kRows * (kJoinPitch * 4 + 8) <= kStages * kStage, "the join fits the ring");
     static constexpr uint32_t kColO = KT * NQ * kNS, kCols = kColO + NQ * D <= 256 ? 256 : 512;
     static_assert((kSmem + 1024) * kPerSM <= 228 * 1024, "shared memory");
     static_assert(kColO + NQ * D <= 512 && kCols * kPerSM <= 512, "tensor memory");
@@ -62,6 +66,7 @@ struct FwdParams {
     TileMap k, v;
     int tiles;
     Divide by_tiles;
+    bool cluster;  // the parts are a cluster's CTAs, which join them
 };
 
 template <int D, int NQ, int KT>
@@ -333,7 +338,25 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
         if (active && q < nq && ok) {
             const long long f = cross_flat(p, b, kh, mine ? r : 0);
             const int to = min(p.d, (half + 1) * kPart);
-            if (a.w.parts > 1) {
+            if (a.cluster) {
+                // sums and (m, l) to this CTA's ring (the copies and products are done), for the cluster's join
+                float *sO = reinterpret_cast<float *>(sm + G::kRing) + row * G::kJoinPitch;
+                if (half == 0) reinterpret_cast<float2 *>(sm + G::kJoinMl)[row] = make_float2(nt > 0 ? m : -INFINITY, l);
+                float o[32];
+#pragma unroll 1
+                for (int x = half * kPart; x < to; x += 32) {
+                    if (nt > 0) {
+                        tmem_ld32(tO + x, o);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = 0.f;
+                    }
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        *reinterpret_cast<float4 *>(sO + x + 4 * y) = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                }
+            } else if (a.w.parts > 1) {
                 const long long at = (long long)blockIdx.y * p.B * p.kv * p.rows + f;
                 if (mine && half == 0) a.w.ml[at] = make_float2(nt > 0 ? m : -INFINITY, l);
                 float o[32];
@@ -389,6 +412,33 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
     if (warp == kIssue) {
         tc_fence_after();
         tmem_dealloc(tmem, G::kCols);
+    }
+    if constexpr (NQ == 1) {
+        if (!a.cluster) return;
+        // The parts of a cluster joined over distributed shared memory, in rank order: 8 columns of a row a
+        // thread, the rows spread over the cluster's CTAs.  Every CTA gets here (its waits are bounded).
+        cl::sync_all();
+        const int parts = a.w.parts, per = p.d / 8, rows = min(left, kRows);
+        const uint32_t sO = smem_u32(sm + G::kRing), sMl = smem_u32(sm + G::kJoinMl);
+        for (int i = (int)blockIdx.y * G::kThreads + (int)threadIdx.x; i < rows * per; i += parts * G::kThreads) {
+            const int row = i / per, c = i - row * per, r = r0 + row;
+            float m = -INFINITY, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            for (int q = 0; q < parts; ++q) m = fmaxf(m, cl::ld_f32(cl::map_shared(sMl + row * 8, q)));
+            const float shift = m == -INFINITY ? 0.f : m;
+            for (int q = 0; q < parts; ++q) {
+                const uint32_t ml = cl::map_shared(sMl + row * 8, q), at = cl::map_shared(sO + (row * G::kJoinPitch + 8 * c) * 4, q);
+                const float k = ex2(cl::ld_f32(ml) - shift);
+                const float4 x = cl::ld_f4(at), y = cl::ld_f4(at + 16);
+                l = fmaf(cl::ld_f32(ml + 4), k, l);
+                o[0] = fmaf(x.x, k, o[0]), o[1] = fmaf(x.y, k, o[1]), o[2] = fmaf(x.z, k, o[2]), o[3] = fmaf(x.w, k, o[3]);
+                o[4] = fmaf(y.x, k, o[4]), o[5] = fmaf(y.y, k, o[5]), o[6] = fmaf(y.z, k, o[6]), o[7] = fmaf(y.w, k, o[7]);
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            *reinterpret_cast<uint4 *>((__nv_bfloat16 *)p.H.ptr + cross_row(p, p.H, b, kh, r) + 8 * c) =
+                make_uint4(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv), pack2(o[4] * inv, o[5] * inv), pack2(o[6] * inv, o[7] * inv));
+            if (p.lse && c == 0) p.lse[cross_flat(p, b, kh, r)] = l == 0.f ? -INFINITY : m * (1.f / kLog2e) + logf(l);
+        }
+        cl::sync_all();  // no CTA leaves while another reads its sums
     }
 }
 
@@ -617,6 +667,22 @@ cudaError_t launch(const CrossProblem &p, const CrossParts &w, cudaStream_t stre
     static SmemOnce allow;
     const cudaError_t e = allow(cross_fwd_kernel<D, NQ, KT>, G::kSmem);
     if (e != cudaSuccess) return e;
+    a.cluster = NQ == 1 && w.parts > 1 && !w.o;
+    if (a.cluster) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(a.tiles * p.B * p.kv, w.parts);
+        cfg.blockDim = dim3(G::kThreads);
+        cfg.dynamicSmemBytes = G::kSmem;
+        cfg.stream = stream;
+        cudaLaunchAttribute at[2];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = 1, at[1].val.clusterDim.y = (unsigned)w.parts, at[1].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, cross_fwd_kernel<D, NQ, KT>, a);
+    }
     return launch_pdl(cross_fwd_kernel<D, NQ, KT>, dim3(a.tiles * p.B * p.kv, w.parts), dim3(G::kThreads), G::kSmem, stream, a);
 }
 
@@ -666,12 +732,20 @@ bool make_tile_map(TileMap *m, const CrossView &v, int B, int heads, int rows, i
 
 }  // namespace cross_tc
 
-int cross_tc_parts(const CrossProblem &p) {
-    if (is_short(p)) return 1;
+// Parts of the key axis: none while the row tiles alone fill the SMs; else so many that they do.  Up to
+// kCluster of them are the CTAs of a cluster, which joins them itself: a token of 12 heads over 1500
+// states takes one launch and no workspace.  More (a second launch joins them) where each of the
+// cluster's would have more than kClusterTiles tiles.
+constexpr int kCluster = 8, kClusterTiles = 8;
+CrossPlan cross_tc_plan(const CrossProblem &p) {
+    if (is_short(p)) return CrossPlan{1, false};
     const int nq = tiles_per_cta(p), per_sm = p.d <= 64 ? 2 : 1;
     const long long ctas = (long long)p.B * p.kv * ((p.rows + nq * kRows - 1) / (nq * kRows));
-    const long long want = (long long)per_sm * kPlanSMs / std::max(1LL, ctas), most = (p.s + 2 * kRows - 1) / (2 * kRows);
-    return (int)std::max(1LL, std::min(want, most));
+    const long long want = (long long)per_sm * kPlanSMs / std::max(1LL, ctas), tiles = (p.s + kRows - 1) / kRows;
+    if (nq == 1 && want > 1 && (want <= kCluster || tiles <= kCluster * kClusterTiles))
+        return CrossPlan{(int)std::min(std::min(want, (long long)kCluster), tiles), false};
+    const int parts = (int)std::max(1LL, std::min(want, (tiles + 1) / 2));
+    return CrossPlan{parts, parts > 1};
 }
 
 cudaError_t launch_cross_tc_forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
