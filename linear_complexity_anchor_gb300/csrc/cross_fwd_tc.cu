@@ -137,6 +137,21 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
             for (int j = max(0, i - ST); j < i; ++j) bwait(full + j % ST, (uint32_t)((j / ST) & 1), error);
         }
         __syncwarp();
+        // the rows and the first stages of the CTA that will follow on this SM, into L2
+        const long long then = (long long)blockIdx.x + G::kPerSM * kPlanSMs;
+        if (a.w.parts == 1 && then < (long long)gridDim.x) {
+            const int bk2 = a.by_tiles.of((int)then), tile2 = (int)then - bk2 * a.tiles, b2 = p.by_kv.of(bk2), kh2 = bk2 - b2 * p.kv;
+            if (lane < 2 && tile2 == 0) {
+                const TileMap &m = lane ? a.v : a.k;
+                for (int t = 0; t < ST && t * KT < p.s; ++t)
+#pragma unroll
+                    for (int q = 0; q < D / 64; ++q) prefetch_tile(&m.map, 64 * q, t * KT, kh2 * m.by_head, b2 * m.by_batch);
+            }
+            for (int x = tile2 * NQ * kRows + lane; x < min(p.rows, (tile2 + 1) * NQ * kRows); x += 32) {
+                const char *q = (const char *)((const __nv_bfloat16 *)p.Q.ptr + cross_row(p, p.Q, b2, kh2, x));
+                for (int y = 0; y < 2 * p.d; y += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + y));
+            }
+        }
     } else if (warp == kIssue) {
         if (lane == 0 && nt > 0) {
             // A tile's rows wait for S, this thread for their P, the rows for the next S: that round is
