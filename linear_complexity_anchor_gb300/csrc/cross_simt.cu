@@ -16,6 +16,7 @@
 // so every gradient is summed by one CTA in a fixed order, without atomics.
 #include "common.cuh"
 #include "cross.cuh"
+#include "ptx.cuh"
 
 #include <math.h>
 
@@ -26,17 +27,22 @@ constexpr int kThreads = 256, kBN = 64;
 constexpr int kPitchS = kBN + 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// `rows` rows of D elements into shared memory as fp32, zeros where at(r) is null
+// `rows` rows of D elements into shared memory, zeros where at(r) is null: asynchronous copies, one
+// group a call
 template <int D, typename At>
 __device__ __forceinline__ void load_rows(float *dst, int rows, At at) {
     constexpr int C = D / 4;
     for (int i = threadIdx.x; i < rows * C; i += kThreads) {
         const int r = i / C, c = 4 * (i - r * C);
         const float *src = at(r);
-        *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) =
-            src ? *reinterpret_cast<const float4 *>(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(dst + r * (D + 4) + c)),
+                     "l"(src ? src + c : nullptr), "r"(src ? 16 : 0)
+                     : "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
 }
+// all but the `left` groups begun last have landed
+template <int left> __device__ __forceinline__ void landed() { asm volatile("cp.async.wait_group %0;" ::"n"(left) : "memory"); }
 
 // s[i][j] = a row (ty TM + i) . b row (tx + 16 j)
 template <int D, int TM>
@@ -142,7 +148,13 @@ __global__ void __launch_bounds__(kThreads) cross_simt_forward_kernel(const Cros
     const float c = p.scale * kLog2e;
     const float *Q = (const float *)p.Q.ptr;
     const float *K = (const float *)p.K.ptr + b * p.K.sb + k * p.K.sh, *V = (const float *)p.V.ptr + b * p.V.sb + k * p.V.sh;
+    auto load_k = [&](int t) { load_rows<D>(sK, kBN, [&](int r) { return t * kBN + r < L ? K + (t * kBN + r) * p.K.sn : nullptr; }); };
+    auto load_v = [&](int t) { load_rows<D>(sV, kBN, [&](int r) { return t * kBN + r < L ? V + (t * kBN + r) * p.V.sn : nullptr; }); };
     load_rows<D>(sQ, BM, [&](int r) { return r0 + r < p.rows ? Q + cross_row(p, p.Q, b, k, r0 + r) : nullptr; });
+    if (t0 < t1) {
+        load_k(t0);
+        load_v(t0);
+    }
     float m[TM], l[TM], o[TM][kCols<D>];
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -150,13 +162,14 @@ __global__ void __launch_bounds__(kThreads) cross_simt_forward_kernel(const Cros
 #pragma unroll
         for (int j = 0; j < kCols<D>; ++j) o[i][j] = 0.f;
     }
+    // each of K and V is fetched again as soon as its tile has been used, while the other is
     for (int t = t0; t < t1; ++t) {
-        __syncthreads();
-        load_rows<D>(sK, kBN, [&](int r) { return t * kBN + r < L ? K + (t * kBN + r) * p.K.sn : nullptr; });
-        load_rows<D>(sV, kBN, [&](int r) { return t * kBN + r < L ? V + (t * kBN + r) * p.V.sn : nullptr; });
+        landed<1>();  // K (and Q)
         __syncthreads();
         float s[TM][4];
         dots<D, TM>(sQ, sK, s);
+        __syncthreads();
+        if (t + 1 < t1) load_k(t + 1);
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             float top = m[i];
@@ -179,10 +192,15 @@ __global__ void __launch_bounds__(kThreads) cross_simt_forward_kernel(const Cros
 #pragma unroll
             for (int j = 0; j < kCols<D>; ++j) o[i][j] *= keep;
         }
-        store_scores<D, TM>(sP, s);
-        __syncwarp();  // a warp writes and reads its own rows of P
+        store_scores<D, TM>(sP, s);  // a warp writes and reads its own rows of P
+        if (t + 1 < t1) landed<1>();
+        else landed<0>();
+        __syncthreads();  // V
         accumulate<D, TM>(sP, sV, o);
+        __syncthreads();
+        if (t + 1 < t1) load_v(t + 1);
     }
+    landed<0>();
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int r = r0 + ty * TM + i;
@@ -203,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) cross_simt_forward_kernel(const Cros
 }
 
 template <int D, int TM> constexpr size_t backward_smem() {
-    return 4 * ((size_t)(2 * 16 * TM + 2 * kBN) * (D + 4) + 16 * TM * kPitchS + 2 * kBN);
+    return 4 * ((size_t)(2 * 16 * TM + 3 * kBN) * (D + 4) + 16 * TM * kPitchS + 2 * 2 * kBN);
 }
 
 // KEYS: rows are keys, columns the query rows of the key head; else rows are query rows.
@@ -212,8 +230,8 @@ __global__ void __launch_bounds__(kThreads) cross_simt_backward_kernel(const Cro
     constexpr int BM = 16 * TM;
     extern __shared__ __align__(16) float sm[];
     // rows: (Q, dH) or (K, V); columns: (K, V) or (Q, dH)
-    float *sA = sm, *sA2 = sA + BM * (D + 4), *sB = sA2 + BM * (D + 4), *sB2 = sB + kBN * (D + 4), *sW = sB2 + kBN * (D + 4);
-    float *sL = sW + BM * kPitchS, *sD = sL + kBN;  // KEYS: the columns' lse and D
+    float *sA = sm, *sA2 = sA + BM * (D + 4), *sB = sA2 + BM * (D + 4) /* [2] */, *sB2 = sB + 2 * kBN * (D + 4), *sW = sB2 + kBN * (D + 4);
+    float *sLD = sW + BM * kPitchS;  // KEYS: the columns' lse and D, [2][2][kBN]
     grid_dependency_wait();
     grid_dependents_launch();
     const int tile = (int)(blockIdx.x % tiles), bk = (int)(blockIdx.x / tiles);
@@ -246,20 +264,36 @@ __global__ void __launch_bounds__(kThreads) cross_simt_backward_kernel(const Cro
         }
     }
     const int cols = KEYS ? (r0 < L ? p.rows : 0) : L;  // a tile of masked keys has no gradient
-    for (int c0 = 0; c0 < cols; c0 += kBN) {
-        __syncthreads();
-        load_rows<D>(sB, kBN, [&](int r) { return KEYS ? q_row(c0 + r) : k_row(c0 + r); });
-        load_rows<D>(sB2, kBN, [&](int r) { return KEYS ? g_row(c0 + r) : v_row(c0 + r); });
+    // The first of the streaming tiles (used last) is fetched a step ahead into its other place, the
+    // second as soon as it has been used.
+    auto load_b = [&](int c0) {
+        const int at = (c0 / kBN) & 1;
         if (KEYS && threadIdx.x < kBN) {
             const bool in = c0 + (int)threadIdx.x < p.rows;
             const long long f = in ? cross_flat(p, b, k, c0 + threadIdx.x) : 0;
-            sL[threadIdx.x] = in ? p.lse[f] * kLog2e : 0.f;
-            sD[threadIdx.x] = in ? delta[f] : 0.f;
+            sLD[at * 2 * kBN + threadIdx.x] = in ? p.lse[f] * kLog2e : 0.f;
+            sLD[at * 2 * kBN + kBN + threadIdx.x] = in ? delta[f] : 0.f;
         }
+        load_rows<D>(sB + at * kBN * (D + 4), kBN, [&](int r) { return KEYS ? q_row(c0 + r) : k_row(c0 + r); });
+    };
+    auto load_b2 = [&](int c0) { load_rows<D>(sB2, kBN, [&](int r) { return KEYS ? g_row(c0 + r) : v_row(c0 + r); }); };
+    if (cols > 0) {
+        load_b(0);
+        load_b2(0);
+    }
+    for (int c0 = 0; c0 < cols; c0 += kBN) {
+        const bool more = c0 + kBN < cols;
+        const float *sB0 = sB + ((c0 / kBN) & 1) * kBN * (D + 4), *sL = sLD + ((c0 / kBN) & 1) * 2 * kBN, *sD = sL + kBN;
+        landed<0>();
         __syncthreads();
+        if (more) load_b(c0 + kBN);
         float s[TM][4], g[TM][4];
-        dots<D, TM>(sA, sB, s);
+        dots<D, TM>(sA, sB0, s);
         dots<D, TM>(sA2, sB2, g);
+        if (!KEYS) {
+            __syncthreads();
+            if (more) load_b2(c0 + kBN);
+        }
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -273,13 +307,15 @@ __global__ void __launch_bounds__(kThreads) cross_simt_backward_kernel(const Cro
             store_scores<D, TM>(sW, s);
             __syncwarp();
             accumulate<D, TM>(sW, sB2, o2);
-            __syncwarp();
+            __syncthreads();
+            if (more) load_b2(c0 + kBN);
         }
         store_scores<D, TM>(sW, g);
         __syncwarp();
-        accumulate<D, TM>(sW, sB, o);
+        accumulate<D, TM>(sW, sB0, o);
         __syncwarp();
     }
+    landed<0>();
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int r = r0 + ty * TM + i;
