@@ -1,12 +1,14 @@
 // Cross attention in fp32 on CUDA cores, forward and backward (formulas in
 // include/anchor_attn.h).
 //
-// Tiles of BM rows by 64 columns, 256 threads as 16 x 16: a thread has BM / 16 rows (next to one
-// another) and columns tx, tx + 16, tx + 32, tx + 48 of the scores, and BM / 16 rows by d / 16
-// columns of the outputs.  All tiles lie row by row in shared memory with a pitch of d + 4 floats:
-// 16-byte reads along d (scores) and along the columns (outputs) are then free of conflicts, and
-// one copy serves both products.  At BM = 64 each 16-byte read feeds 8 (scores) and 10 (outputs)
-// FMAs a thread.  Fewer rows per tile when there are not CTAs for all SMs.
+// Tiles of BM = 64, 32 or 16 rows by 64 columns.  Threads stand as 16 to a group of rows: one has TM
+// rows (next to one another) and columns tx, tx + 16, tx + 32, tx + 48 of the scores, and TM rows by
+// d / 16 columns of the outputs.  All tiles lie row by row in shared memory with a pitch of d + 4
+// floats: 16-byte reads along d (scores) and along the columns (outputs) are then free of conflicts,
+// and one copy serves both products.  What bounds it is those reads: at TM = 8 twelve of them feed 128
+// FMAs a thread, at TM = 4 eight feed 64 (2 x 8 heads, 2048 x 2048, d = 64: 480 against 548 us; paired
+// FMAs, half the instructions, gave 4 % at the most).  Fewer rows per tile when there are not CTAs for
+// all SMs.  Tiles that stream by are copied asynchronously, each as soon as its place is free.
 //
 // Forward: online softmax, one pass over the keys; with parts, a CTA has a run of key tiles of its
 // entry's own length, and leaves sums that a second launch joins.
@@ -23,7 +25,11 @@
 namespace anchor {
 namespace {
 
-constexpr int kThreads = 256, kBN = 64;
+constexpr int kBN = 64;
+// threads of a CTA, 16 to a row group: 128, with up to 8 rows each; at d = 128 256, with up to 4 (its
+// tiles leave room for one CTA an SM)
+template <int D> constexpr int kThreads = D == 128 ? 256 : 128;
+template <int D> constexpr int kTY = kThreads<D> / 16;
 constexpr int kPitchS = kBN + 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -32,7 +38,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 template <int D, typename At>
 __device__ __forceinline__ void load_rows(float *dst, int rows, At at) {
     constexpr int C = D / 4;
-    for (int i = threadIdx.x; i < rows * C; i += kThreads) {
+    for (int i = threadIdx.x; i < rows * C; i += kThreads<D>) {
         const int r = i / C, c = 4 * (i - r * C);
         const float *src = at(r);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(dst + r * (D + 4) + c)),
@@ -130,12 +136,12 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 template <int D, int TM> constexpr size_t forward_smem() {
-    return 4 * ((size_t)(16 * TM + 2 * kBN) * (D + 4) + 16 * TM * kPitchS);
+    return 4 * ((size_t)(kTY<D> * TM + 2 * kBN) * (D + 4) + kTY<D> * TM * kPitchS);
 }
 
 template <int D, int TM>
-__global__ void __launch_bounds__(kThreads) cross_simt_forward_kernel(const CrossProblem p, const CrossParts w, int tiles) {
-    constexpr int BM = 16 * TM;
+__global__ void __launch_bounds__(kThreads<D>) cross_simt_forward_kernel(const CrossProblem p, const CrossParts w, int tiles) {
+    constexpr int BM = kTY<D> * TM;
     extern __shared__ __align__(16) float sm[];
     float *sQ = sm, *sK = sQ + BM * (D + 4), *sV = sK + kBN * (D + 4), *sP = sV + kBN * (D + 4);
     grid_dependency_wait();
@@ -221,13 +227,13 @@ __global__ void __launch_bounds__(kThreads) cross_simt_forward_kernel(const Cros
 }
 
 template <int D, int TM> constexpr size_t backward_smem() {
-    return 4 * ((size_t)(2 * 16 * TM + 3 * kBN) * (D + 4) + 16 * TM * kPitchS + 2 * 2 * kBN);
+    return 4 * ((size_t)(2 * kTY<D> * TM + 3 * kBN) * (D + 4) + kTY<D> * TM * kPitchS + 2 * 2 * kBN);
 }
 
 // KEYS: rows are keys, columns the query rows of the key head; else rows are query rows.
 template <int D, int TM, bool KEYS>
-__global__ void __launch_bounds__(kThreads) cross_simt_backward_kernel(const CrossProblem p, const float *delta, int tiles) {
-    constexpr int BM = 16 * TM;
+__global__ void __launch_bounds__(kThreads<D>) cross_simt_backward_kernel(const CrossProblem p, const float *delta, int tiles) {
+    constexpr int BM = kTY<D> * TM;
     extern __shared__ __align__(16) float sm[];
     // rows: (Q, dH) or (K, V); columns: (K, V) or (Q, dH)
     float *sA = sm, *sA2 = sA + BM * (D + 4), *sB = sA2 + BM * (D + 4) /* [2] */, *sB2 = sB + 2 * kBN * (D + 4), *sW = sB2 + kBN * (D + 4);
@@ -331,46 +337,45 @@ __global__ void __launch_bounds__(kThreads) cross_simt_backward_kernel(const Cro
     }
 }
 
-// rows of a tile: the most of 64, 32 and 16 that still gives every SM a CTA, else 16
-int tile_m(const CrossProblem &p, long long rows) {
+// rows of a tile: the most of 64, 32 and 16 whose tiles still give every SM a CTA, else 16
+int tile_rows(const CrossProblem &p, long long rows) {
     const long long heads = (long long)p.B * p.kv;
-    int tm = 4;
-    while (tm > 1 && (heads * ((rows + 16 * tm - 1) / (16 * tm)) < kPlanSMs || rows <= 8 * tm)) tm /= 2;
-    return tm;
+    int bm = 64;
+    while (bm > 16 && (heads * ((rows + bm - 1) / bm) < kPlanSMs || rows <= bm / 2)) bm /= 2;
+    return bm;
 }
 
 template <int D, int TM>
 cudaError_t forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
-    const int tiles = (p.rows + 16 * TM - 1) / (16 * TM);
+    const int tiles = (p.rows + kTY<D> * TM - 1) / (kTY<D> * TM);
     constexpr size_t smem = forward_smem<D, TM>();
     static SmemOnce allow;
     const cudaError_t e = allow(cross_simt_forward_kernel<D, TM>, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cross_simt_forward_kernel<D, TM>, dim3(tiles * p.B * p.kv, w.parts), dim3(kThreads), smem, stream, p, w, tiles);
+    return launch_pdl(cross_simt_forward_kernel<D, TM>, dim3(tiles * p.B * p.kv, w.parts), dim3(kThreads<D>), smem, stream, p, w, tiles);
 }
 
 template <int D, int TM, bool KEYS>
 cudaError_t backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
-    const int tiles = ((KEYS ? p.s : p.rows) + 16 * TM - 1) / (16 * TM);
+    const int tiles = ((KEYS ? p.s : p.rows) + kTY<D> * TM - 1) / (kTY<D> * TM);
     constexpr size_t smem = backward_smem<D, TM>();
     static SmemOnce allow;
     const cudaError_t e = allow(cross_simt_backward_kernel<D, TM, KEYS>, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cross_simt_backward_kernel<D, TM, KEYS>, dim3(tiles * p.B * p.kv), dim3(kThreads), smem, stream, p, delta, tiles);
+    return launch_pdl(cross_simt_backward_kernel<D, TM, KEYS>, dim3(tiles * p.B * p.kv), dim3(kThreads<D>), smem, stream, p, delta, tiles);
 }
 
+template <int D, bool KEYS>
+cudaError_t backward_rows(const CrossProblem &p, const float *delta, cudaStream_t stream) {
+    const int bm = tile_rows(p, KEYS ? p.s : p.rows);
+    return bm == 64   ? backward<D, 64 / kTY<D>, KEYS>(p, delta, stream)
+           : bm == 32 ? backward<D, 32 / kTY<D>, KEYS>(p, delta, stream)
+                      : backward<D, 16 / kTY<D>, KEYS>(p, delta, stream);
+}
 template <int D>
 cudaError_t backward_d(const CrossProblem &p, const float *delta, cudaStream_t stream) {
-    const int tq = tile_m(p, p.rows), tk = tile_m(p, p.s);
-    cudaError_t e = cudaSuccess;
-    if (p.rows > 0)
-        e = tq == 4   ? backward<D, 4, false>(p, delta, stream)
-            : tq == 2 ? backward<D, 2, false>(p, delta, stream)
-                      : backward<D, 1, false>(p, delta, stream);
-    if (e != cudaSuccess || p.s == 0) return e;
-    return tk == 4   ? backward<D, 4, true>(p, delta, stream)
-           : tk == 2 ? backward<D, 2, true>(p, delta, stream)
-                     : backward<D, 1, true>(p, delta, stream);
+    const cudaError_t e = p.rows > 0 ? backward_rows<D, false>(p, delta, stream) : cudaSuccess;
+    return e != cudaSuccess || p.s == 0 ? e : backward_rows<D, true>(p, delta, stream);
 }
 
 }  // namespace
@@ -378,17 +383,19 @@ cudaError_t backward_d(const CrossProblem &p, const float *delta, cudaStream_t s
 // Parts of the key axis: none while the row tiles alone fill the SMs; else so many that two CTAs
 // of them do, with two key tiles a part at least.
 int cross_simt_parts(const CrossProblem &p) {
-    const int tm = tile_m(p, p.rows);
-    const long long ctas = (long long)p.B * p.kv * ((p.rows + 16 * tm - 1) / (16 * tm));
+    const int bm = tile_rows(p, p.rows);
+    const long long ctas = (long long)p.B * p.kv * ((p.rows + bm - 1) / bm);
     const long long want = 2 * kPlanSMs / std::max(1LL, ctas), most = (p.s + 2 * kBN - 1) / (2 * kBN);
     return (int)std::max(1LL, std::min(want, most));
 }
 
 cudaError_t launch_cross_simt_forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
-    const int tm = tile_m(p, p.rows);
+    const int bm = tile_rows(p, p.rows);
     auto go = [&](auto d) {
         constexpr int D = decltype(d)::value;
-        return tm == 4 ? forward<D, 4>(p, w, stream) : tm == 2 ? forward<D, 2>(p, w, stream) : forward<D, 1>(p, w, stream);
+        return bm == 64   ? forward<D, 64 / kTY<D>>(p, w, stream)
+               : bm == 32 ? forward<D, 32 / kTY<D>>(p, w, stream)
+                          : forward<D, 16 / kTY<D>>(p, w, stream);
     };
     switch (p.d) {
     case 16: return go(std::integral_constant<int, 16>{});
