@@ -187,6 +187,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                 const uint64_t vd = vd0 + st * kStep, kd = kd0 + st * kStep;
                 const uint32_t par = (uint32_t)((j / NS) & 1), id = i == nt - 1 ? idL : idS;
                 if (!landed && !(ok = bwait(full + st, (uint32_t)((i / ST) & 1), error))) break;
+                landed = false;
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
                     if (q >= nq) break;
@@ -280,14 +281,16 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                     if (!bwait(meet, (uint32_t)(j & 1), error)) { ok = false; break; }
                     top = fmaxf(__bfloat162float(slot[0]), __bfloat162float(slot[kRows]));
                 }
+                // Two S buffers: O up to the tile before.  Waited for at every step: S runs ahead of it, and a
+                // warp two phases behind a barrier would take the older phase for the one it wants.
+                // (One: this S was issued after the product that O waits for.)
+                if (NS == 2 && j > 0 && !bwait(o_full + q, (uint32_t)((j - 1) & 1), error)) { ok = false; break; }
                 if (j == 0) {
                     m = top;
                 } else {
                     const bool grows = top > m + kSlack;
                     if (__any_sync(0xffffffffu, grows)) {
                         // this half of O's columns (complete up to the tile before) to the new maximum
-                        // (one S buffer: this S was issued after the product that O waits for)
-                        if (NS == 2 && !bwait(o_full + q, (uint32_t)((j - 1) & 1), error)) { ok = false; break; }
                         tc_fence_after();
                         const float f = grows ? ex2(m - top) : 1.f;
                         if (grows) m = top;

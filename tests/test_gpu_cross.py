@@ -74,6 +74,15 @@ def test_few_queries(aa, dtype, shape, lengths):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_queries_of_many_entries(aa, dtype, d):
+    """A token of so many entries that no key axis is cut; what is summed last counts, and every time the same."""
+    Q, K, V, _, L, H, _ = check(aa, 17, 40, 16, 8, 1, 2900, d, dtype, lengths="mixed", train=False)
+    for _ in range(20):
+        assert torch.equal(H, aa.cross_forward(Q, K, V, L))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [16, 64, 128])
 @pytest.mark.parametrize("s", [1, 16, 31, 77, 112, 127, 128])
 def test_short_states(aa, dtype, d, s):
