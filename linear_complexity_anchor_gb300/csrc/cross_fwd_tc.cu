@@ -241,9 +241,8 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
         }
         const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
         const uint32_t tO = tmem + lanes + G::kColO + q * D;
-        // the two halves of a row meet over its slots [parity][half], and over a barrier of their two warps
-        // (the maximum in bf16: any value near it will do, if the halves agree)
-        __nv_bfloat16 *ex = reinterpret_cast<__nv_bfloat16 *>(sm + G::kEx + q * 2 * kRows * 4) + row;
+        // the two halves of a row meet over its slots [half], and over a barrier of their two warps
+        float *ex = reinterpret_cast<float *>(sm + G::kEx + q * 2 * kRows * 4) + row;
         uint64_t *meet = pair + q * 4 + w4;
         float m = -INFINITY, l = 0.f;  // maximum in use (of c s), and this half's sum
         bool ok = true;
@@ -273,18 +272,18 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
 #pragma unroll
                 for (int x = 0; x < 8; ++x) t8[x] = fmaxf(t8[x], s[56 + x]);
                 float top = c * fmaxf(max3_f32(t8[0], t8[1], t8[2]), max3_f32(t8[3], t8[4], max3_f32(t8[5], t8[6], t8[7])));
-                if (NH == 2) {
-                    __nv_bfloat16 *slot = ex + (j & 1) * 2 * kRows;
-                    slot[half * kRows] = __float2bfloat16_rn(top);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(meet);
-                    if (!bwait(meet, (uint32_t)(j & 1), error)) { ok = false; break; }
-                    top = fmaxf(__bfloat162float(slot[0]), __bfloat162float(slot[kRows]));
-                }
-                // Two S buffers: O up to the tile before.  Waited for at every step: S runs ahead of it, and a
+                // Two S buffers: O up to the tile before, waited for at every step: S runs ahead of it, and a
                 // warp two phases behind a barrier would take the older phase for the one it wants.
                 // (One: this S was issued after the product that O waits for.)
                 if (NS == 2 && j > 0 && !bwait(o_full + q, (uint32_t)((j - 1) & 1), error)) { ok = false; break; }
+                if (NH == 2) {
+                    // (that product has read P of both halves, so both have read the slots)
+                    ex[half * kRows] = top;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(meet);
+                    if (!bwait(meet, (uint32_t)(j & 1), error)) { ok = false; break; }
+                    top = fmaxf(ex[0], ex[kRows]);
+                }
                 if (j == 0) {
                     m = top;
                 } else {
@@ -343,12 +342,11 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                 // O, then the halves' sums (over the maxima, which all warps have read by then)
                 ok = bwait(o_full + q, (uint32_t)((NS == 2 ? nt - 1 : 0) & 1), error);
                 if (NH == 2) {
-                    float *slot = reinterpret_cast<float *>(sm + G::kEx + q * 2 * kRows * 4) + row;
-                    slot[half * kRows] = l;
+                    ex[half * kRows] = l;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(meet);
                     ok = ok && bwait(meet, (uint32_t)(nt & 1), error);
-                    l = slot[0] + slot[kRows];
+                    l = ex[0] + ex[kRows];
                 }
             }
             tc_fence_after();

@@ -41,15 +41,29 @@ anchor_attn_status_t check_view(const View &v, bool writes) {
 
 bool views_overlap(const View &a, const View &b) {
     if (!bytes_overlap(a.ptr, (size_t)a.extent(), b.ptr, (size_t)b.extent())) return false;
-    // Parts of one token-major buffer ([B][n][all heads][d]): every row of either lies at a fixed
-    // place of a cell of `cell` elements, and the two places may be apart.
-    const long long cell = std::max(a.sn, b.sn);
-    const bool celled = cell > 0 && a.es == b.es && (a.N < 2 || a.sn == cell) && (b.N < 2 || b.sn == cell) &&
-                        a.sb % cell == 0 && b.sb % cell == 0;
-    if (!celled) return true;
-    const long long na = (a.H - 1) * a.sh + a.d, nb = (b.H - 1) * b.sh + b.d;
-    const long long delta = ((b.ptr - a.ptr) / a.es % cell + cell) % cell;
-    return !(delta >= na && delta + nb <= cell);
+    // Parts of one buffer (queries, keys and values of one projection, in any order of the axes): with a
+    // cell of `c` elements, if every stride of both that is not below c is a multiple of it, every row of
+    // either lies within a fixed part of a cell, and the two parts may be apart.
+    if (a.es != b.es) return true;
+    const long long strides[6] = {a.sb, a.sh, a.sn, b.sb, b.sh, b.sn};
+    for (long long c : strides) {
+        if (c <= 0) continue;
+        auto part = [&](const View &v) {  // elements of a cell that a row and its neighbours take; -1: no fixed part
+            const long long st[3] = {v.sb, v.sh, v.sn}, sizes[3] = {v.B, v.H, v.N};
+            long long span = v.d;
+            for (int i = 0; i < 3; ++i) {
+                if (sizes[i] < 2 || st[i] == 0) continue;
+                if (st[i] < c) span += (sizes[i] - 1) * st[i];
+                else if (st[i] % c) return -1LL;
+            }
+            return span;
+        };
+        const long long na = part(a), nb = part(b);
+        if (na < 0 || nb < 0) continue;
+        const long long delta = ((b.ptr - a.ptr) / a.es % c + c) % c;
+        if (delta >= na && delta + nb <= c) return false;
+    }
+    return true;
 }
 
 namespace {

@@ -120,6 +120,54 @@ def test_growing_scores(aa, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 2, 2, 150, 300, 64), (2, 4, 2, 300, 260, 128), (2, 8, 1, 1, 700, 128), (3, 2, 2, 40, 100, 64), (40, 8, 4, 1, 900, 128)])
+def test_huge_scores(aa, dtype, shape):
+    """Scores of tens of thousands: one state takes a row's whole weight, and exponents differ by more than fp32 has."""
+    Q, K, V, _ = make(31, *shape, dtype)
+    Q, K = Q * 300, K * 30
+    H, lse = aa.cross_forward(Q, K, V, return_lse=True)
+    x = (Q.double() @ K.double().repeat_interleave(shape[1] // shape[2], 1).mT) * shape[5] ** -0.5
+    assert float(x.abs().max()) > 1.5e4 and bool(H.isfinite().all())
+    # scores are off by d roundings of fp32 of their products at the most: rows whose best state is ahead by more than that
+    two = x.topk(2, -1)
+    off = (shape[5] + 20) * 2.0 ** -23 * (Q.double().abs() @ K.double().abs().repeat_interleave(shape[1] // shape[2], 1).mT).amax(-1) * shape[5] ** -0.5
+    sure = two.values[..., 0] - two.values[..., 1] > 40 + 2 * off
+    assert float(sure.double().mean()) > 0.5
+    best = V.repeat_interleave(shape[1] // shape[2], 1).gather(2, two.indices[..., :1].expand(*H.shape))
+    # H = p v / p for one weight p: p is 2 to the rounding of c times the maximum, 2^(2^-24 c x) and not 1, and is
+    # rounded once (bf16: half a step u) before it meets v; the product, the quotient and H are rounded once each
+    assert bool(((H - best).double().abs()[sure] <= (2 + 2.0 ** -6) * torch.finfo(DT[dtype]).eps / 2 * best.double().abs()[sure]
+                 * (1 if dtype == "bf16" else 2)).all())
+    assert bool(((lse.double() - two.values[..., 0]).abs()[sure] <= off[sure] + 2.0 ** -20 * two.values[..., 0].abs()[sure]).all())
+
+
+def test_offsets_past_32_bits(aa):
+    """Batch entries, heads and rows further apart than 2^32 bytes, and 2^31 elements, of one buffer."""
+    buf = torch.zeros(3 * 2 ** 31, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    # (the last: whether parts of one buffer can be told apart, which the heads' stride decides)
+    for shape, strides, inside in (((2, 2, 70, 64), (2 ** 32, 2 ** 12, 2 ** 14, 1), True), ((2, 2, 130, 64), (2 ** 12, 2 ** 32, 2 ** 13, 1), False),
+                                   ((1, 2, 140, 64), (64, 2 ** 12, 2 ** 25, 1), True)):
+        views = [buf.as_strided(shape, strides, i * 2 ** 10) for i in range(3)]
+        for v in views:
+            v.copy_(torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16))
+        Q, K, V = (v.contiguous() for v in views)
+        H, lse = aa.cross_forward(*views, return_lse=True)
+        assert torch.equal(H, aa.cross_forward(Q, K, V))
+        out = buf.as_strided(shape, strides, 3 * 2 ** 10) if inside else torch.empty_like(H)
+        aa.cross_forward(*views, H=out)
+        assert torch.equal(out, H)
+        dH = Q * 0.5
+        for a, b in zip(aa.cross_backward(*views, out, lse, dH), aa.cross_backward(Q, K, V, H, lse, dH)):
+            assert torch.equal(a, b)
+        table = aa.rope_table(64)
+        assert torch.equal(aa.rope(views[0], table), aa.rope(Q, table))
+        want = aa.norm_rope(Q, K, table)
+        got = aa.norm_rope(views[0], views[1], table, out=(out, None))
+        assert torch.equal(out, want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [32, 128])
 def test_strides(aa, dtype, d):
     """Token-major projections, and parts of one buffer; results in the same order of axes, or dense."""

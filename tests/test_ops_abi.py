@@ -156,6 +156,25 @@ def test_rope_refusals(pkg, backward, second):
     assert c(**{out: buf(0), read: buf(3)}) == ALIAS
 
 
+def test_parts_of_one_buffer(pkg, monkeypatch):
+    """Which parts of one buffer count as overlapping, in every order of the axes that a projection's output has: what gets
+    past the checks ends at the workspace, which the environment refuses."""
+    ALLOC = 4
+    monkeypatch.setenv("ANCHOR_ATTN_TEST_FAIL_ALLOC", "1")
+    d, n, H = 64, 8, 4
+    call = lambda dX, dY: rope(pkg, True, False, {}, dX=dX, dY=dY, dweight=A * 40)  # noqa: E731
+    # [B, n, part, head, d], [B, n, head, part, d], [B, part, head, n, d], [part, B, head, n, d]: batch, head, row, part
+    for sb, sh, sn, part in ((3 * H * n * d, d, 3 * H * d, H * d), (3 * H * n * d, 3 * d, 3 * H * d, d),
+                             (3 * H * n * d, n * d, d, H * n * d), (H * n * d, n * d, d, 2 * H * n * d)):
+        at = lambda k, more=0: View(50 * A + 2 * (part * k + more), sb, sh, sn)  # noqa: E731
+        for i in range(3):
+            for j in range(3):
+                assert call(at(i), at(j)) == (ALIAS if i == j else ALLOC), (sb, sh, sn, part, i, j)
+            assert call(at(i, 8), at(i)) == ALIAS
+    # heads of one tensor over those of the next
+    assert call(View(50 * A + 2 * 3 * d, 2 * H * n * d, d, 2 * H * d), View(50 * A, 2 * H * n * d, d, 2 * H * d)) == ALIAS
+
+
 def test_rope_frequencies(pkg):
     theta, magnitude = pkg.rope_frequencies(8, 10000.0)
     assert magnitude == 1.0 and theta == [[1.0, pytest.approx(0.1), pytest.approx(0.01), pytest.approx(0.001)]]
