@@ -145,6 +145,11 @@ def test_in_place_and_parts_of_one_buffer(aa, dtype):
     want = aa.rope(k, table, interleaved=True)
     aa.rope(k, table, interleaved=True, out=k)
     assert torch.equal(k, want) and torch.equal(v, keep)
+    buf = torch.randn((B, n, kv, 3, d), generator=g, device="cuda").to(DT[dtype])  # the parts of a head next to one another
+    q2, k2, v2 = (buf[:, :, :, i].transpose(1, 2) for i in range(3))
+    want, keep = aa.norm_rope(q2, k2, table), v2.clone()
+    aa.norm_rope(q2, k2, table, out=(q2, k2))
+    assert torch.equal(q2, want[0]) and torch.equal(k2, want[1]) and torch.equal(v2, keep)
     with pytest.raises(aa.AnchorAttnError):  # an output over the other tensor
         aa.norm_rope(q, k, table, out=(q, q[:, :kv]))
 
