@@ -31,7 +31,11 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kFill = 152 * 12;      // blocks that fill the GPU, below which heads are cut into groups
-constexpr int kBwdBlocks = 152 * 8;  // most blocks of a tensor whose dweight is summed
+// Most blocks of a backward whose dweight is summed: bf16, all tensors together as many as are resident
+// at once (three an SM), so that no tail is left and few blocks' sums remain (8 x 24 x 4200 rows of 64: 61
+// us against 70 with 1216 a tensor); fp32, whose threads have more in flight, 1216 a tensor (101 us
+// against 111).
+constexpr int kBwdBlocks16 = 152 * 3, kBwdBlocks32 = 152 * 8;
 
 enum Mode { kHalves = 0, kNeighbours = 1, kOddHalves = 2 };
 
@@ -322,27 +326,34 @@ __global__ void __launch_bounds__(kThreads, MODE == kOddHalves ? (BWD ? 3 : 4) :
     }
 }
 
-// dweight[e] = sum over the blocks' sums: 8 columns of one tensor per CTA, 32 runs of blocks each
-// added in order, then the runs in order.
+// dweight[e] = sum over the blocks' sums: 4 columns of one tensor per CTA, 64 runs of blocks each added
+// in order, then the runs in order.  Bound by the latency of a run's loads, of which eight are in
+// flight.
 __global__ void __launch_bounds__(256)
 norm_weight_kernel(const float *part0, int blocks0, void *out0, const float *part1, int blocks1, void *out1, int d, int f32) {
-    __shared__ float run[32][8];
+    __shared__ float run[64][4];
     grid_dependency_wait();
     grid_dependents_launch();
     const float *part = blockIdx.y ? part1 : part0;
     void *out = blockIdx.y ? out1 : out0;
     const int blocks = blockIdx.y ? blocks1 : blocks0;
     if (!out) return;
-    const int e = blockIdx.x * 8 + (threadIdx.x & 7), q = threadIdx.x >> 3;
-    const int each = (blocks + 31) / 32, from = min(q * each, blocks), to = min(from + each, blocks);
+    const int e = blockIdx.x * 4 + (threadIdx.x & 3), q = threadIdx.x >> 2;
+    const int each = (blocks + 63) / 64, from = min(q * each, blocks), to = min(from + each, blocks);
     float s = 0.f;
-#pragma unroll 4
-    for (int b = from; b < to; ++b) s += part[(size_t)b * d + e];
-    run[q][threadIdx.x & 7] = s;
+    for (int b = from; b < to; b += 8) {
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = b + k < to ? part[(size_t)(b + k) * d + e] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += x[k];
+    }
+    run[q][threadIdx.x & 3] = s;
     __syncthreads();
     if (q == 0) {
         float a = 0.f;
-        for (int k = 0; k < 32; ++k) a += run[k][threadIdx.x];
+#pragma unroll
+        for (int k = 0; k < 64; ++k) a += run[k][threadIdx.x];
         if (f32) reinterpret_cast<float *>(out)[e] = a;
         else reinterpret_cast<__nv_bfloat16 *>(out)[e] = __float2bfloat16_rn(a);
     }
@@ -368,7 +379,7 @@ cudaError_t launch(const Params &p, int mode, bool bwd, cudaStream_t stream) {
 bool finite_not_negative(float x) { return isfinite(x) && x >= 0.f; }
 
 // The checks of one tensor, and its part of the launch.
-anchor_attn_status_t check_rows(const anchor_attn_rope_t &how, const anchor_attn_rows_t &t, bool bwd, Rows &r, View *in,
+anchor_attn_status_t check_rows(const anchor_attn_rope_t &how, const anchor_attn_rows_t &t, bool bwd, int tensors, Rows &r, View *in,
                                 int &nin, View *out, int &nout) {
     if (t.B < 0 || t.heads < 0 || t.n < 0 || t.positions_batch < 0) return ANCHOR_ATTN_ERR_INVALID_ARG;
     if (t.dweight && (!bwd || !how.norm)) return ANCHOR_ATTN_ERR_INVALID_ARG;
@@ -399,7 +410,10 @@ anchor_attn_status_t check_rows(const anchor_attn_rope_t &how, const anchor_attn
     r.groups = std::min(r.heads, std::max(1, kFill / r.token_blocks));
     r.heads_per = (r.heads + r.groups - 1) / r.groups;
     r.groups = (r.heads + r.heads_per - 1) / r.heads_per;
-    if (t.dweight) r.token_blocks = std::min(r.token_blocks, std::max(1, kBwdBlocks / r.groups));
+    if (t.dweight) {
+        const int most = how.dtype ? kBwdBlocks32 : kBwdBlocks16 / tensors;
+        r.token_blocks = std::min(r.token_blocks, std::max(1, most / r.groups));
+    }
     if ((long long)r.token_blocks * r.groups > 0x3fffffffLL) return ANCHOR_ATTN_ERR_UNSUPPORTED;
     r.blocks = r.token_blocks * r.groups;
     return ANCHOR_ATTN_OK;
@@ -424,7 +438,7 @@ anchor_attn_status_t norm_rope(const anchor_attn_rope_t *how, const anchor_attn_
     const anchor_attn_rows_t *t[2] = {first, second};
     for (int i = 0; i < 2; ++i) {
         if (!t[i]) continue;
-        const anchor_attn_status_t st = check_rows(a, *t[i], bwd, p.r[i], in, nin, out, nout);
+        const anchor_attn_status_t st = check_rows(a, *t[i], bwd, second ? 2 : 1, p.r[i], in, nin, out, nout);
         if (st != ANCHOR_ATTN_OK) return st;
     }
     // an output may be its own tensor's X (forward): a row is read whole before it is written
@@ -489,7 +503,7 @@ anchor_attn_status_t norm_rope(const anchor_attn_rope_t *how, const anchor_attn_
     e = a.dtype ? launch<float>(p, mode, bwd, stream) : launch<__nv_bfloat16>(p, mode, bwd, stream);
     if (sums) {
         if (e == cudaSuccess)
-            e = launch_pdl(norm_weight_kernel, dim3(a.d / 8, 2), dim3(256), 0, stream, (const float *)p.r[0].part,
+            e = launch_pdl(norm_weight_kernel, dim3(a.d / 4, 2), dim3(256), 0, stream, (const float *)p.r[0].part,
                            p.r[0].blocks, p.r[0].part ? first->dweight : nullptr, (const float *)p.r[1].part, p.r[1].blocks,
                            p.r[1].part ? second->dweight : nullptr, a.d, p.w_f32);
         const cudaError_t ef = cudaFreeAsync(ws, stream);
