@@ -91,7 +91,7 @@ __device__ __forceinline__ void dots(const float *a, const float *b, float (&s)[
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < kNJ; ++j) c[i][j] = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < D; k += 4) {
         ulonglong2 x[TM], y[kNJ];
 #pragma unroll
@@ -135,7 +135,7 @@ __device__ __forceinline__ void accumulate(const float *w, const float *v, float
 #pragma unroll
             for (int j = 0; j < C2; ++j) c[i][j] = pair(o[i][2 * j], o[i][2 * j + 1]);
     }
-#pragma unroll 2
+#pragma unroll 4
     for (int k = 0; k < keys; k += 4) {
         float x[TM][4];
 #pragma unroll

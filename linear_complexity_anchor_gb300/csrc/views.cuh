@@ -32,7 +32,8 @@ inline bool bytes_overlap(const void *a, size_t an, const void *b, size_t bn) {
 
 // Stream-ordered device memory from a pool of this library, one per device, that keeps up to
 // kPoolKeep bytes between calls: the device's default pool gives its memory back at every
-// synchronisation, and a call after one would map it again (measured at 0.1 to 0.6 ms).
+// synchronisation, and a call after one maps it again (one query of 32 heads over 65536 states, waited
+// for: 66 us against 249; a backward of 8 x 12 heads, 1000 x 1000: 167 against 369).
 constexpr unsigned long long kPoolKeep = 512ull << 20;
 cudaError_t workspace_alloc(void **ptr, size_t bytes, cudaStream_t stream);
 
