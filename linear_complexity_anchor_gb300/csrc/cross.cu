@@ -54,24 +54,25 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossProblem p, c
     if (p.lse && c == 0) p.lse[f] = l == 0.f ? -INFINITY : M * (1.f / kLog2e) + logf(l);
 }
 
-// 4 columns of one row per thread, the row's threads (d / 4) next to one another in a warp.  Bound by
+// 16 bytes of a row per thread, the row's threads (2^log2 of them) next to one another in a warp.  Bound by
 // memory.
-__global__ void __launch_bounds__(256) cross_delta_kernel(const CrossProblem p, float *delta, long long total) {
+template <typename T>
+__global__ void __launch_bounds__(256) cross_delta_kernel(const CrossProblem p, float *delta, int total, int log2, Divide by_rows) {
+    constexpr int V = 16 / sizeof(T);
     grid_dependency_wait();
     grid_dependents_launch();
-    const int per = p.d / 4;
-    const long long f = ((long long)blockIdx.x * 256 + threadIdx.x) / per;
-    const int c = (int)(threadIdx.x % per) * 4;
+    const int f = (int)(blockIdx.x * (256u >> log2) + (threadIdx.x >> log2));
+    const int c = (int)(threadIdx.x & ((1u << log2) - 1)) * V;
     float s = 0.f;
     if (f < total) {
-        const int r = (int)(f % p.rows);
-        const long long bk = f / p.rows;
-        const int b = (int)(bk / p.kv), k = (int)(bk - (long long)b * p.kv);
-        const float4 h = *reinterpret_cast<const float4 *>((const float *)p.H.ptr + cross_row(p, p.H, b, k, r) + c);
-        const float4 g = *reinterpret_cast<const float4 *>((const float *)p.dH.ptr + cross_row(p, p.dH, b, k, r) + c);
-        s = fmaf(h.x, g.x, fmaf(h.y, g.y, fmaf(h.z, g.z, h.w * g.w)));
+        const int bk = by_rows.of(f), r = f - bk * p.rows, b = p.by_kv.of(bk), k = bk - b * p.kv;
+        T h[V], g[V];
+        *reinterpret_cast<uint4 *>(h) = *reinterpret_cast<const uint4 *>((const T *)p.H.ptr + cross_row(p, p.H, b, k, r) + c);
+        *reinterpret_cast<uint4 *>(g) = *reinterpret_cast<const uint4 *>((const T *)p.dH.ptr + cross_row(p, p.dH, b, k, r) + c);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s = fmaf(to_f32(h[i]), to_f32(g[i]), s);
     }
-    for (int o = per / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int o = 1 << log2 >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (f < total && c == 0) delta[f] = s;
 }
 
@@ -85,9 +86,13 @@ cudaError_t launch_cross_join(const CrossProblem &p, const CrossParts &w, cudaSt
 }
 
 cudaError_t launch_cross_delta(const CrossProblem &p, float *delta, cudaStream_t stream) {
-    const long long total = (long long)p.B * p.kv * p.rows;
-    const dim3 grid((unsigned)((total * (p.d / 4) + 255) / 256));
-    return launch_pdl(cross_delta_kernel, grid, dim3(256), 0, stream, p, delta, total);
+    const int total = p.B * p.kv * p.rows;
+    int log2 = 0;
+    while ((16 << log2) < p.d * (p.f32 ? 4 : 2)) ++log2;
+    const dim3 grid((unsigned)(((long long)total + (256 >> log2) - 1) / (256 >> log2)));
+    const Divide by_rows((uint32_t)p.rows);
+    return p.f32 ? launch_pdl(cross_delta_kernel<float>, grid, dim3(256), 0, stream, p, delta, total, log2, by_rows)
+                 : launch_pdl(cross_delta_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, p, delta, total, log2, by_rows);
 }
 
 namespace {
@@ -185,7 +190,7 @@ anchor_attn_status_t cross(const anchor_attn_cross_t *a, bool bwd, void *stream_
         if (queries) {
             if (!take(rows_bytes)) return ANCHOR_ATTN_ERR_ALLOC;
             delta = (float *)ws;
-            if (p.f32) e = launch_cross_delta(p, delta, stream);  // (bf16: its kernel makes D itself)
+            e = launch_cross_delta(p, delta, stream);
         }
         if (e == cudaSuccess)
             e = p.f32 ? launch_cross_simt_backward(p, delta, stream) : launch_cross_tc_backward(p, delta, stream);

@@ -2,9 +2,11 @@
 //   P = 2^(c S - lse), S = Q K^T;  dS = P o (dH V^T - D), D = dH . H;
 //   dQ = scale dS K;  dV = P^T dH;  dK = scale dS^T Q.
 //
-// Two kernels, one that keeps queries and one that keeps keys, so that every gradient is summed in
+// Two kinds of CTAs, one that keeps queries and one that keeps keys, so that every gradient is summed in
 // tensor memory by one CTA in a fixed order, without atomics.  S and dP are made twice for
-// that: seven products where five would do.
+// that: seven products where five would do.  Both are of one launch, those that take longer first, so that
+// the others fill the SMs that they leave (D comes from a launch before; with the queries first and
+// D made by them, in a launch of their own, 2 x 16 heads over 4, 2049 x 1500, d = 128: 188 us against 152).
 //
 //   queries   a tile of 128 rows of Q and dH stays, the keys of the entry stream by:
 //             S = Q K^T, dP = dH V^T, dQ += dS K
@@ -20,12 +22,13 @@
 //   keys      after P^T(j): dV += P^T(j) dH, S^T(j + 1)      while the rows make dS^T(j)
 //             after dS^T(j): dK += dS^T(j) Q, dP^T(j + 1)    while the rows make P^T(j + 1)
 //   queries   after S(j) is read: S(j + 1);  after dS(j): dQ += dS(j) K, dP(j + 1)
-// (a product that overwrites an operand is issued after the one that reads it).  The queries' kernel
-// also makes D, of the rows of dH that it loads, for both.  P and dS are rounded to bf16, the operands' type; S, dP, P in dS,
-// and all sums are fp32.
+// (a product that overwrites an operand is issued after the one that reads it).  P and dS are rounded to
+// bf16, the operands' type; S, dP, P in dS, and all sums are fp32.
 // States from the length on: P and dS are zero there by select, and rows of K that meet a zero of dS
 // are zeroed in shared memory.
 #include "cross_tc.cuh"
+
+#include <algorithm>
 
 #include <math.h>
 
@@ -51,8 +54,8 @@ struct Geo {
     static constexpr int kNB = D == 128 ? 2 : 4, kNA = kNB + 1;
     static constexpr int kSlot = kTile<D, W>;
     static constexpr int kFix = 0, kA = 2 * kTile<D>, kB = kA + kNA * kSlot;
-    static constexpr int kStatB = kB + kNB * kSlot;  // keys: lse, D of W columns; queries: parts of D of 128 rows
-    static constexpr int kBars = kStatB + 2 * kRows * 4;
+    static constexpr int kStatB = kB + kNB * kSlot;  // keys: lse, D of W columns
+    static constexpr int kBars = kStatB + 2 * W * 4;
     static constexpr int kNBars = kNA + 2 * kNB + 11;
     static constexpr int kSmem = kBars + kNBars * 8 + 16 + 1024;
     static constexpr uint32_t kColS = 0, kColP = W, kColA = 2 * W;  // S, dP, then the sums
@@ -63,16 +66,17 @@ struct Geo {
 
 struct BwdParams {
     CrossProblem p;
-    float *delta;    // D: written by the queries' kernel, read by the keys'
-    TileMap a, b;  // queries: K, V stream; keys: Q, dH stream
-    TileMap fa, fb;  // keys: K, V stay
-    int tiles;
-    Divide by_tiles;
+    const float *delta;  // D
+    TileMap q, g, k, v;  // g: dH
+    int tiles[2];        // of the queries and of the keys of a key head
+    Divide by_tiles[2];
+    int first;           // CTAs of the kind that comes first
+    bool keys_first;
 };
 
-// KEYS: see above
+// The work of CTA `index` of its kind (KEYS: see above).
 template <int D, bool KEYS, int W>
-__global__ void __launch_bounds__(Geo<D, W>::kThreads, Geo<D, W>::kPerSM) cross_bwd_kernel(const __grid_constant__ BwdParams a) {
+__device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
     using G = Geo<D, W>;
     constexpr int kRowWarps = G::kRowWarps, kLoad = G::kLoad, kStat = G::kStat, kIssue = G::kIssue;
     constexpr uint32_t kColS = G::kColS, kColP = G::kColP, kColA = G::kColA;
@@ -87,7 +91,8 @@ __global__ void __launch_bounds__(Geo<D, W>::kThreads, Geo<D, W>::kPerSM) cross_
     float *stat = reinterpret_cast<float *>(sm + G::kStatB);
     const CrossProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int bk = a.by_tiles.of((int)blockIdx.x), tile = (int)blockIdx.x - bk * a.tiles;
+    const int bk = a.by_tiles[KEYS].of(index), tile = index - bk * a.tiles[KEYS];
+    const TileMap &map_a = KEYS ? a.q : a.k, &map_b = KEYS ? a.g : a.v;  // the tiles that stream by
     const int b = p.by_kv.of(bk), kh = bk - b * p.kv, r0 = tile * kRows;
     unsigned int *error = &g_cross_bwd_error;
 
@@ -142,22 +147,22 @@ __global__ void __launch_bounds__(Geo<D, W>::kThreads, Geo<D, W>::kPerSM) cross_
         if (lane == 0 && nt > 0) {
             if (KEYS) {
                 mbar_arrive_expect_tx(fix_full, 2 * kTile<D>);
-                load_tile<D, kRows, W>(sm + G::kFix, a.fa, fix_full, r0, kh, b);
-                load_tile<D, kRows, W>(sm + G::kFix + kTile<D>, a.fb, fix_full, r0, kh, b);
+                load_tile<D, kRows, W>(sm + G::kFix, a.k, fix_full, r0, kh, b);
+                load_tile<D, kRows, W>(sm + G::kFix + kTile<D>, a.v, fix_full, r0, kh, b);
             }
             int ja = 0, jb = 0;  // steps whose tiles have been asked for
             Walk wa = start, wb = start;
             auto load_a = [&]() {
                 if (ja >= nt) return;
                 mbar_arrive_expect_tx(a_full + ja % NA, G::kSlot);
-                load_tile<D, W, W>(sm + G::kA + ja % NA * G::kSlot, a.a, a_full + ja % NA, wa.t * W, KEYS ? kh * p.group + wa.g : kh, b);
+                load_tile<D, W, W>(sm + G::kA + ja % NA * G::kSlot, map_a, a_full + ja % NA, wa.t * W, KEYS ? kh * p.group + wa.g : kh, b);
                 ++ja;
                 wa.next();
             };
             auto load_b = [&]() {
                 if (jb >= nt) return;
                 mbar_arrive_expect_tx(b_full + jb % NB, G::kSlot);
-                load_tile<D, W, W>(sm + G::kB + jb % NB * G::kSlot, a.b, b_full + jb % NB, wb.t * W, KEYS ? kh * p.group + wb.g : kh, b);
+                load_tile<D, W, W>(sm + G::kB + jb % NB * G::kSlot, map_b, b_full + jb % NB, wb.t * W, KEYS ? kh * p.group + wb.g : kh, b);
                 ++jb;
                 wb.next();
             };
@@ -285,11 +290,10 @@ __global__ void __launch_bounds__(Geo<D, W>::kThreads, Geo<D, W>::kPerSM) cross_
         const uint64_t c = f32x2(p.scale * kLog2e, p.scale * kLog2e);
         uint64_t lse2 = f32x2(-INFINITY, -INFINITY), dl = 0;  // - lse (in log2) and - D of this row, twice
         if (!KEYS && nt > 0) {
-            // The first half of the warps load the 128 rows of Q, each its part of the columns, the others
-            // those of dH, and of H for D = dH . H: over the lanes of a row, then over the parts.
+            // the first half of the warps load the 128 rows of Q, each its part of the columns, the others those of dH
             constexpr int kParts = G::kSlices / 2, kLanes = D / (8 * kParts);
             const bool second = quarter >= kParts;
-            const int part = quarter % kParts, ch = part * kLanes + lane % kLanes;
+            const int ch = quarter % kParts * kLanes + lane % kLanes;
             const CrossView &v = second ? p.dH : p.Q;
             uint8_t *dst = sm + G::kFix + (second ? kTile<D> : 0);
             uint4 x[kLanes];
@@ -300,38 +304,14 @@ __global__ void __launch_bounds__(Geo<D, W>::kThreads, Geo<D, W>::kPerSM) cross_
 #pragma unroll
             for (int i = 0; i < kLanes; ++i)
                 *reinterpret_cast<uint4 *>(dst + chunk_at(w4 * 32 + i * (32 / kLanes) + lane / kLanes, ch)) = x[i];
-            if (second) {
-                uint4 y[kLanes];
-                each_row<kLanes>(mine ? cross_row(p, p.H, b, kh, r) : -1, p.H.sn, [&](int i, int, long long o) {
-                    y[i] = make_uint4(0, 0, 0, 0);
-                    if (o >= 0 && ch * 8 < p.d) y[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.H.ptr + o + ch * 8);
-                });
-#pragma unroll
-                for (int i = 0; i < kLanes; ++i) {
-                    const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
-                    float sum = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        sum = fmaf(__uint_as_float(u[k] << 16), __uint_as_float(w[k] << 16), sum);
-                        sum = fmaf(__uint_as_float(u[k] & 0xffff0000u), __uint_as_float(w[k] & 0xffff0000u), sum);
-                    }
-#pragma unroll
-                    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if (lane % kLanes == 0) stat[part * kRows + w4 * 32 + i * (32 / kLanes) + lane / kLanes] = sum;
-                }
-            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(fix_full);
             if (mine) {
-                const float x2 = -p.lse[cross_flat(p, b, kh, r)] * kLog2e;
-                lse2 = f32x2(x2, x2);
+                const long long f = cross_flat(p, b, kh, r);
+                const float x2 = -p.lse[f] * kLog2e, d2 = -a.delta[f];
+                lse2 = f32x2(x2, x2), dl = f32x2(d2, d2);
             }
-            bwait(fix_full, 0u, error);
-            float dv = stat[row];
-            if (kParts == 2) dv += stat[kRows + row];
-            if (mine && quarter == 0) a.delta[cross_flat(p, b, kh, r)] = dv;
-            dl = f32x2(-dv, -dv);
         }
         const uint32_t tS = trow + kColS + kSlice * quarter, tP = trow + kColP + kSlice * quarter;
         bool ok = true;
@@ -462,36 +442,38 @@ __global__ void __launch_bounds__(Geo<D, W>::kThreads, Geo<D, W>::kPerSM) cross_
     }
 }
 
-template <int D, bool KEYS, int W>
-cudaError_t launch(const CrossProblem &p, float *delta, cudaStream_t stream) {
+template <int D, int W>
+__global__ void __launch_bounds__(Geo<D, W>::kThreads, Geo<D, W>::kPerSM) cross_bwd_kernel(const __grid_constant__ BwdParams a) {
+    const bool head = (int)blockIdx.x < a.first;
+    const int index = (int)blockIdx.x - (head ? 0 : a.first);
+    if (head == a.keys_first) cross_bwd<D, true, W>(a, index);
+    else cross_bwd<D, false, W>(a, index);
+}
+
+template <int D, int W>
+cudaError_t backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
     using G = Geo<D, W>;
     BwdParams a;
     a.p = p;
     a.delta = delta;
-    a.tiles = ((KEYS ? p.s : p.rows) + kRows - 1) / kRows;
-    a.by_tiles = Divide((uint32_t)a.tiles);
-    TileMap k, v, q, g;
-    if (p.s > 0 && (!make_tile_map(&k, p.K, p.B, p.kv, p.s, p.d, W) || !make_tile_map(&v, p.V, p.B, p.kv, p.s, p.d, W)))
+    const int ctas[2] = {(p.rows + kRows - 1) / kRows, (p.s + kRows - 1) / kRows};
+    for (int i = 0; i < 2; ++i) a.tiles[i] = ctas[i], a.by_tiles[i] = Divide((uint32_t)std::max(1, ctas[i]));
+    // first those that take longer: four products over the queries against three over the keys
+    a.keys_first = 4LL * p.rows >= 3LL * p.s;
+    a.first = a.tiles[a.keys_first] * p.B * p.kv;
+    if (p.s > 0 && (!make_tile_map(&a.k, p.K, p.B, p.kv, p.s, p.d, W) || !make_tile_map(&a.v, p.V, p.B, p.kv, p.s, p.d, W)))
         return cudaErrorInvalidValue;
-    if (KEYS && p.n > 0 && (!make_tile_map(&q, p.Q, p.B, p.heads, p.n, p.d, W) || !make_tile_map(&g, p.dH, p.B, p.heads, p.n, p.d, W)))
+    if (p.s > 0 && p.n > 0 && (!make_tile_map(&a.q, p.Q, p.B, p.heads, p.n, p.d, W) || !make_tile_map(&a.g, p.dH, p.B, p.heads, p.n, p.d, W)))
         return cudaErrorInvalidValue;
-    a.a = KEYS ? q : k, a.b = KEYS ? g : v, a.fa = k, a.fb = v;
     static SmemOnce allow;
-    const cudaError_t e = allow(cross_bwd_kernel<D, KEYS, W>, G::kSmem);
+    const cudaError_t e = allow(cross_bwd_kernel<D, W>, G::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cross_bwd_kernel<D, KEYS, W>, dim3(a.tiles * p.B * p.kv), dim3(G::kThreads), G::kSmem, stream, a);
-}
-
-template <int D, int W>
-cudaError_t backward(const CrossProblem &p, float *delta, cudaStream_t stream) {
-    cudaError_t e = p.rows > 0 ? launch<D, false, W>(p, delta, stream) : cudaSuccess;
-    if (e == cudaSuccess && p.s > 0) e = launch<D, true, W>(p, delta, stream);
-    return e;
+    return launch_pdl(cross_bwd_kernel<D, W>, dim3((a.tiles[0] + a.tiles[1]) * p.B * p.kv), dim3(G::kThreads), G::kSmem, stream, a);
 }
 
 }  // namespace
 
-cudaError_t launch_cross_tc_backward(const CrossProblem &p, float *delta, cudaStream_t stream) {
+cudaError_t launch_cross_tc_backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
     return p.d > 64 ? backward<128, 128>(p, delta, stream) : backward<64, 64>(p, delta, stream);
 }
 
