@@ -8,22 +8,21 @@
 //
 // What bounds it: the FMAs and those reads together.  A warp's 16-byte read takes two cycles of shared memory
 // for two rows of eight different places, and four for sixteen places in each half of the warp: with
-// 4 x 8 threads a warp, its lanes in pairs of the same place, every read takes two, ten of them for 24
+// 4 x 8 threads a warp, its lanes in pairs of the same place, every read takes two, ten of them for 48
 // FMAs of two each (2 x 8 heads, 2048 x 2048, a training step: 2168 -> 2079 us at d = 64 against 2 x 16
-// threads a warp, 4133 -> 4050 at d = 128).  Two FMAs an instruction, which leaves issue slots to the
-// reads: 2156 -> 2079 and 4307 -> 4050.  It runs at 38 to 40 TFLOP/s, half of the card's fp32 rate; at
-// d = 128 one CTA fits an SM, and 512 of them on 152 are a last wave that is a third full.  Fewer
-// rows per tile when there are not CTAs for all SMs.
+// threads a warp, 4133 -> 4050 at d = 128).  Two FMAs an instruction leave issue slots to the reads: 2156 ->
+// 2079 and 4307 -> 4050.  Now 1804 and 3535: 43 TFLOP/s, 0.54 of the FMAs' rate.
 //
 // Forward: online softmax, one pass over the keys, every other tile of them by each half, whose sums are
 // joined at the end; K and V are each fetched again as soon as their tile has been used.  With parts, a CTA
 // has a run of key tiles of its entry's own length, and leaves sums that a second launch joins.
-// Backward: P again from lse; one kernel for both products that differ in what stays:
+// Backward: P again from lse; two kinds of CTAs that differ in what stays:
 //   dQ          rows = queries, columns = keys:    dQ += dS K
 //   dK and dV   rows = keys, columns = queries:    dV += P^T dH, dK += dS^T Q
+// in one launch, the longer CTAs first (two launches: 2011 us at d = 64, 3915 at 128).
 // The first half makes S and P and sums dV, the second dP and dS and sums dK; of dQ each sums half of the
 // keys.  Every gradient is summed by one CTA in a fixed order, without atomics.  (One half that did both:
-// 4 x 6 heads, 197 x 300, d = 64, a training step of 122 us against 98.)
+// 4 x 6 heads, 197 x 300, d = 64, a training step of 122 us against 98 in two launches.)
 #include "common.cuh"
 #include "cross.cuh"
 #include "ptx.cuh"
@@ -324,9 +323,10 @@ template <int D, int BM> constexpr size_t backward_smem() {
     return 4 * ((size_t)(2 * BM + 4 * kBN) * (D + 4) + 2 * BM * kPitchS + 2 * 2 * kBN);
 }
 
-// KEYS: rows are keys, columns the query rows of the key head; else rows are query rows.
+// KEYS: rows are keys, columns the query rows of the key head; else rows are query rows.  `index`: of the
+// CTA among those of its kind, `tiles` of them a key head.
 template <int D, int BM, bool KEYS>
-__global__ void __launch_bounds__(kThreads, kPerSM<D>) cross_simt_backward_kernel(const CrossProblem p, const float *delta, int tiles) {
+__device__ __forceinline__ void cross_simt_backward(const CrossProblem &p, const float *delta, int index, int tiles) {
     constexpr int TM = kTM<BM>, C = kCols<D>, kTile = kBN * (D + 4);
     static_assert(BM * D <= 2 * kTile, "the second half's sums fit the tiles");
     extern __shared__ __align__(16) float sm[];
@@ -334,10 +334,8 @@ __global__ void __launch_bounds__(kThreads, kPerSM<D>) cross_simt_backward_kerne
     float *sA = sm, *sA2 = sA + BM * (D + 4), *sB = sA2 + BM * (D + 4), *sB2 = sB + 2 * kTile;
     float *sP = sB2 + 2 * kTile, *sS = sP + BM * kPitchS;
     float *sLD = sS + BM * kPitchS;  // KEYS: the columns' lse and D, [2][2][kBN]
-    grid_dependency_wait();
-    grid_dependents_launch();
     const int h = half();
-    const int tile = (int)(blockIdx.x % tiles), bk = (int)(blockIdx.x / tiles);
+    const int tile = index % tiles, bk = index / tiles;
     const int b = bk / p.kv, k = bk - b * p.kv, r0 = tile * BM;
     const int tx = lane_x(), ty = lane_y();
     const int L = cross_length(p, b);
@@ -437,11 +435,24 @@ __global__ void __launch_bounds__(kThreads, kPerSM<D>) cross_simt_backward_kerne
     }
 }
 
-// rows of a tile: the most of 64, 32 and 16 whose tiles still give every SM a CTA, else 16
-int tile_rows(const CrossProblem &p, long long rows) {
-    const long long heads = (long long)p.B * p.kv;
+template <int D, int BM>
+__global__ void __launch_bounds__(kThreads, kPerSM<D>)
+cross_simt_backward_kernel(const CrossProblem p, const float *delta, int q_tiles, int k_tiles, int first, bool keys_first) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const bool head = (int)blockIdx.x < first;
+    const int index = (int)blockIdx.x - (head ? 0 : first);
+    if (head == keys_first) cross_simt_backward<D, BM, true>(p, delta, index, k_tiles);
+    else cross_simt_backward<D, BM, false>(p, delta, index, q_tiles);
+}
+
+// Rows of a tile: the most of 64, 32 and 16 whose tiles still give every SM a CTA, else 16.  Backward (keys > 0),
+// whose CTAs are of two lengths, below d = 128: the two that fit (4 x 6 heads, 197 x 300, d = 64, a training
+// step: 79 us, 87 with 64 rows, 98 with 16; the forward with 16: 30 against 27).
+int tile_rows(const CrossProblem &p, int queries, int keys) {
+    const long long heads = (long long)p.B * p.kv, want = keys > 0 && p.d < 128 ? 2 * kPlanSMs : kPlanSMs;
     int bm = 64;
-    while (bm > 16 && (heads * ((rows + bm - 1) / bm) < kPlanSMs || rows <= bm / 2)) bm /= 2;
+    while (bm > 16 && (heads * ((queries + bm - 1) / bm + (keys + bm - 1) / bm) < want || std::max(queries, keys) <= bm / 2)) bm /= 2;
     return bm;
 }
 
@@ -455,27 +466,18 @@ cudaError_t forward(const CrossProblem &p, const CrossParts &w, cudaStream_t str
     return launch_pdl(cross_simt_forward_kernel<D, BM>, dim3(tiles * p.B * p.kv, w.parts), dim3(kThreads), smem, stream, p, w, tiles);
 }
 
-template <int D, int BM, bool KEYS>
+template <int D, int BM>
 cudaError_t backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
-    const int tiles = ((KEYS ? p.s : p.rows) + BM - 1) / BM;
+    const int q_tiles = (p.rows + BM - 1) / BM, k_tiles = (p.s + BM - 1) / BM;
+    // first those that take longer: four products over the queries against three over the keys
+    const bool keys_first = 4LL * p.rows >= 3LL * p.s;
+    const int first = (keys_first ? k_tiles : q_tiles) * p.B * p.kv;
     constexpr size_t smem = backward_smem<D, BM>();
     static SmemOnce allow;
-    const cudaError_t e = allow(cross_simt_backward_kernel<D, BM, KEYS>, smem);
+    const cudaError_t e = allow(cross_simt_backward_kernel<D, BM>, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cross_simt_backward_kernel<D, BM, KEYS>, dim3(tiles * p.B * p.kv), dim3(kThreads), smem, stream, p, delta, tiles);
-}
-
-template <int D, bool KEYS>
-cudaError_t backward_rows(const CrossProblem &p, const float *delta, cudaStream_t stream) {
-    const int bm = tile_rows(p, KEYS ? p.s : p.rows);
-    return bm == 64   ? backward<D, 64, KEYS>(p, delta, stream)
-           : bm == 32 ? backward<D, 32, KEYS>(p, delta, stream)
-                      : backward<D, 16, KEYS>(p, delta, stream);
-}
-template <int D>
-cudaError_t backward_d(const CrossProblem &p, const float *delta, cudaStream_t stream) {
-    const cudaError_t e = p.rows > 0 ? backward_rows<D, false>(p, delta, stream) : cudaSuccess;
-    return e != cudaSuccess || p.s == 0 ? e : backward_rows<D, true>(p, delta, stream);
+    return launch_pdl(cross_simt_backward_kernel<D, BM>, dim3((q_tiles + k_tiles) * p.B * p.kv), dim3(kThreads), smem, stream, p, delta,
+                      q_tiles, k_tiles, first, keys_first);
 }
 
 }  // namespace
@@ -483,14 +485,14 @@ cudaError_t backward_d(const CrossProblem &p, const float *delta, cudaStream_t s
 // Parts of the key axis: none while the row tiles alone fill the SMs; else so many that two CTAs
 // of them do, with two key tiles a part at least.
 int cross_simt_parts(const CrossProblem &p) {
-    const int bm = tile_rows(p, p.rows);
+    const int bm = tile_rows(p, p.rows, 0);
     const long long ctas = (long long)p.B * p.kv * ((p.rows + bm - 1) / bm);
     const long long want = 2 * kPlanSMs / std::max(1LL, ctas), most = (p.s + 2 * kBN - 1) / (2 * kBN);
     return (int)std::max(1LL, std::min(want, most));
 }
 
 cudaError_t launch_cross_simt_forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
-    const int bm = tile_rows(p, p.rows);
+    const int bm = tile_rows(p, p.rows, 0);
     auto go = [&](auto d) {
         constexpr int D = decltype(d)::value;
         return bm == 64   ? forward<D, 64>(p, w, stream)
@@ -506,11 +508,16 @@ cudaError_t launch_cross_simt_forward(const CrossProblem &p, const CrossParts &w
 }
 
 cudaError_t launch_cross_simt_backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
+    const int bm = tile_rows(p, p.rows, p.s);
+    auto go = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        return bm == 64 ? backward<D, 64>(p, delta, stream) : bm == 32 ? backward<D, 32>(p, delta, stream) : backward<D, 16>(p, delta, stream);
+    };
     switch (p.d) {
-    case 16: return backward_d<16>(p, delta, stream);
-    case 32: return backward_d<32>(p, delta, stream);
-    case 64: return backward_d<64>(p, delta, stream);
-    default: return backward_d<128>(p, delta, stream);
+    case 16: return go(std::integral_constant<int, 16>{});
+    case 32: return go(std::integral_constant<int, 32>{});
+    case 64: return go(std::integral_constant<int, 64>{});
+    default: return go(std::integral_constant<int, 128>{});
     }
 }
 
