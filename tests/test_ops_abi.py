@@ -77,6 +77,7 @@ def test_cross_refusals(pkg, backward):
     assert c(dtype=2) == INVALID and c(d=48) == UNSUPPORTED and c(d=0) == UNSUPPORTED
     assert c(heads=3) == INVALID and c(kv_heads=0) == INVALID and c(scale=math.inf) == INVALID
     assert c(n=1 << 30) == UNSUPPORTED and c(B=1 << 28, n=64) == UNSUPPORTED
+    assert c(B=1 << 29, heads=2, kv_heads=2, n=1, s=0) == UNSUPPORTED
     assert c(Q=View(0, 1, 1, 1)) == INVALID
     assert c(Q=View(A + 8, 2048, 512, 64)) == INVALID          # base not on 16 bytes
     assert c(K=View(2 * A, 2048, 1024, 68)) == INVALID         # stride not of 16 bytes
