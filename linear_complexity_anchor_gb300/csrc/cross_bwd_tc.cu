@@ -23,7 +23,7 @@
 //             after dS^T(j): dK += dS^T(j) Q, dP^T(j + 1)    while the rows make P^T(j + 1)
 //   queries   after S(j) is read: S(j + 1);  after dS(j): dQ += dS(j) K, dP(j + 1)
 // (a product that overwrites an operand is issued after the one that reads it).  P and dS are rounded to
-// bf16, the operands' type; S, dP, P in dS, and all sums are fp32.
+// bf16, the operands' type (with few states dS to two of them, see kFine); S, dP, P in dS, and all sums are fp32.
 // States from the length on: P and dS are zero there by select, and rows of K that meet a zero of dS
 // are zeroed in shared memory.
 #include "cross_tc.cuh"
@@ -41,6 +41,13 @@ namespace {
 using namespace cross_tc;
 
 constexpr int kSlice = 32;  // columns of S and dP that a row warp takes
+
+// Up to so many states dS meets K and Q as two bf16 numbers, the second what the rounding of the first left: an
+// eighth product and a ninth.  dQ and dK carry the rounding of dS, their own, and that of H through D, which
+// is 2^-9 of dP over the root of the number of states that weigh: with few of them the three together are
+// up to 1.8 times a lone rounding of the result (8 states; 1.56 at 50, 1.50 at 256, 1.46 at 1000), and with two
+// numbers 1.46, 1.19, 1.08, 1.05.  It takes 6 % of time at 77 states, 10 at 300, 18 at 600, 25 at 1000 and more.
+constexpr int kFine = 384;
 
 // D columns (heads of 16 and 32 are 64), streaming tiles of W rows.
 template <int D, int W>
@@ -74,8 +81,8 @@ struct BwdParams {
     bool keys_first;
 };
 
-// The work of CTA `index` of its kind (KEYS: see above).
-template <int D, bool KEYS, int W>
+// The work of CTA `index` of its kind (KEYS: see above).  FINE: dS as two numbers.
+template <int D, bool KEYS, int W, bool FINE>
 __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
     using G = Geo<D, W>;
     constexpr int kRowWarps = G::kRowWarps, kLoad = G::kLoad, kStat = G::kStat, kIssue = G::kIssue;
@@ -268,7 +275,9 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
                 if (more && !landed_b && !(ok = bwait(b_bar + (j + 1) % NB, b_par(j + 1), error))) break;
                 if (!(ok = bwait(ds_full, par, error))) break;
                 tc_fence_after();
-                along(tmem + kColA + (KEYS ? D : 0), tmem + kColP, slot_a(j), last, j > 0);  // dK += dS^T Q, dQ += dS K
+                const uint32_t sum = tmem + kColA + (KEYS ? D : 0);
+                along(sum, tmem + kColP, slot_a(j), last, j > 0);  // dK += dS^T Q, dQ += dS K
+                if (FINE) along(sum, tmem + kColP + kSlice / 2, slot_a(j), last, true);
                 if (more) {
                     product_k<D>(tmem + kColP, f1, desc_k(slot_b(j + 1)), then ? idL : idF, ksteps,
                                  [&] { landed_a = mbar_test(a_bar + (j + 2) % NA, a_par(j + 2)); });
@@ -377,6 +386,12 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
 #pragma unroll
                 for (int y = 0; y < 16; ++y) u[y] = pack2(g[2 * y], g[2 * y + 1]);
                 tmem_st16(tP, u);
+                if constexpr (FINE) {  // what the rounding left, over the slice's other columns
+#pragma unroll
+                    for (int y = 0; y < 16; ++y)
+                        u[y] = pack2(g[2 * y] - __uint_as_float(u[y] << 16), g[2 * y + 1] - __uint_as_float(u[y] & 0xffff0000u));
+                    tmem_st16(tP + kSlice / 2, u);
+                }
             }
             tmem_st_wait();
             if (!KEYS && walk.t == nt - 1 && quarter == 0 && L % W && L < p.s) {
@@ -442,15 +457,15 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
     }
 }
 
-template <int D, int W>
+template <int D, int W, bool FINE>
 __global__ void __launch_bounds__(Geo<D, W>::kThreads, Geo<D, W>::kPerSM) cross_bwd_kernel(const __grid_constant__ BwdParams a) {
     const bool head = (int)blockIdx.x < a.first;
     const int index = (int)blockIdx.x - (head ? 0 : a.first);
-    if (head == a.keys_first) cross_bwd<D, true, W>(a, index);
-    else cross_bwd<D, false, W>(a, index);
+    if (head == a.keys_first) cross_bwd<D, true, W, FINE>(a, index);
+    else cross_bwd<D, false, W, FINE>(a, index);
 }
 
-template <int D, int W>
+template <int D, int W, bool FINE>
 cudaError_t backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
     using G = Geo<D, W>;
     BwdParams a;
@@ -466,15 +481,16 @@ cudaError_t backward(const CrossProblem &p, const float *delta, cudaStream_t str
     if (p.s > 0 && p.n > 0 && (!make_tile_map(&a.q, p.Q, p.B, p.heads, p.n, p.d, W) || !make_tile_map(&a.g, p.dH, p.B, p.heads, p.n, p.d, W)))
         return cudaErrorInvalidValue;
     static SmemOnce allow;
-    const cudaError_t e = allow(cross_bwd_kernel<D, W>, G::kSmem);
+    const cudaError_t e = allow(cross_bwd_kernel<D, W, FINE>, G::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cross_bwd_kernel<D, W>, dim3((a.tiles[0] + a.tiles[1]) * p.B * p.kv), dim3(G::kThreads), G::kSmem, stream, a);
+    return launch_pdl(cross_bwd_kernel<D, W, FINE>, dim3((a.tiles[0] + a.tiles[1]) * p.B * p.kv), dim3(G::kThreads), G::kSmem, stream, a);
 }
 
 }  // namespace
 
 cudaError_t launch_cross_tc_backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
-    return p.d > 64 ? backward<128, 128>(p, delta, stream) : backward<64, 64>(p, delta, stream);
+    if (p.s <= kFine) return p.d > 64 ? backward<128, 128, true>(p, delta, stream) : backward<64, 64, true>(p, delta, stream);
+    return p.d > 64 ? backward<128, 128, false>(p, delta, stream) : backward<64, 64, false>(p, delta, stream);
 }
 
 cudaError_t cross_bwd_read_and_clear_error(unsigned *out) {

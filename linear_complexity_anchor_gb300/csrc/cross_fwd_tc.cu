@@ -1,22 +1,26 @@
 // Cross attention forward in bf16 on the tensor cores (formulas in include/anchor_attn.h).
 //
-// A CTA has one or two tiles of 128 query rows of one key head, and walks that head's keys in
-// tiles of 128: S = Q K^T into tensor memory, two threads per row (64 columns each) take the
-// running maximum and sum and leave P = 2^(c s - m) as bf16 over S's columns, O += P V from there.
-// (One thread per row was bound by its own latency: the tensor pipe 36 % active against NEW.)  Q is loaded with
-// plain 16-byte loads (rows of several heads, any strides), K and V by TMA into a ring, K and V in
-// turn, by a warp of their own; one thread of another warp issues the products.
+// A CTA has one or two tiles of 128 query rows of one key head, and walks that head's keys in tiles of KT:
+// S = Q K^T into tensor memory, a thread takes 64 columns of a row (two threads a row for KT = 128), the
+// running maximum and sum, and leaves P = 2^(c s - m) as bf16 over S's columns, O += P V from there.
+// (One thread for 128 columns was bound by its own latency: the tensor pipe 36 % active against 62 in 8 heads,
+// 9728 x 2048, d = 128.)  Q is loaded with plain 16-byte loads (rows of several heads, any strides), K
+// and V by TMA into a ring, K and V in turn, by a warp of their own; one thread of another warp issues
+// the products.
 //
 // Two tiles: while the rows of one take their exponentials the tensor cores run the other's
 //   P0 V -> O0, Q0 K' -> S0   |   P1 V -> O1, Q1 K' -> S1
 // and each K and V tile is read from L2 once for 256 rows.  S and O of both fill the 512 columns
 // at d = 128, so P lies over S: the products of one CTA run in the order they are issued, and the
-// next S is issued after the P V that reads it.
-// One tile (up to 128 rows, a token of serving above all): bound by reading K and V.  At d = 128
-// S has two buffers, the next S is issued before the softmax of this one, and three stages of 64 KB
-// are in flight; at d = 64 two CTAs share an SM.
+// next S is issued after the P V that reads it.  Bound by that round of a tile, S, its rows, P V; 8 heads,
+// 9728 x 2048, d = 128: 62 us, 1.3 PFLOP/s, and at 8 times that the card's power.  At d = 64 keys go in tiles
+// of 64, a thread a row, and two CTAs share an SM: 4 x 12 heads, 4200 x 1000: 75 us against 91 for tiles of 128.
+// One tile (up to 128 rows, a token of serving above all): bound by reading K and V (64 entries of 5000 states,
+// 8 heads of 128: 197 us, 6.6 TB/s).  At d = 128 S has two buffers, the next S is issued before the softmax
+// of this one, and three stages of 64 KB are in flight; at d = 64 two CTAs share an SM.
 // Few rows and long keys: the key tiles of an entry (of its own length) are cut over gridDim.y
-// CTAs, which leave sums that a second launch joins.
+// CTAs.  Up to eight are a cluster, which joins their sums over distributed shared memory; more leave them
+// for a second launch (rule and reason at cross_tc_plan).
 //
 // The maximum a row is scaled by moves only when it grows by more than 2^8 over the one in use:
 // P stays below 2^8, its relative rounding is the same, and O (in tensor memory) is rescaled
@@ -463,7 +467,8 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
 // warps of their own for loads and products; O lies over the half of S's columns that P leaves free
 // (d <= 64), so that four CTAs share the 512 columns of an SM (d = 128: two).  S is read twice, for
 // the maximum and for the exponentials, instead of being kept in 128 registers.  256 x 12 heads, 197
-// queries over up to 77 states at d = 64: 69 us against 130 for the walk.
+// queries over up to 77 states at d = 64: 57 us against 130 for the walk: bound by
+// each CTA's own chain of loads, products and rows, four of which an SM overlaps (half of the issue slots).
 template <int D>
 struct Short {
     static constexpr int kQ = 0, kK = kTile<D>, kVv = 2 * kTile<D>, kBars = 3 * kTile<D>;
