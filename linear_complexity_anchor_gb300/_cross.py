@@ -21,9 +21,9 @@ def bind(lib) -> None:
 
 
 def _problem(Q, K, V, lengths, scale):
-    """The structure's numbers, its views of Q, K and V, and the lengths' pointer."""
+    """The device, the structure's numbers, its views of Q, K and V, and the lengths' pointer."""
     kind = rows_dtype(Q, "Q")
-    dtype, device = Q.dtype, Q.device
+    dtype, device = Q.dtype, Q.get_device()
     views = (*view(Q, "Q", dtype, device), *view(K, "K", dtype, device), *view(V, "V", dtype, device))
     B, heads, n, d = Q.shape
     Bk, kv, s, dk = shape = K.shape
@@ -33,10 +33,10 @@ def _problem(Q, K, V, lengths, scale):
     if lengths is not None:
         if not isinstance(lengths, torch.Tensor) or lengths.dtype is not torch.int32:
             raise TypeError("lengths must be an int32 tensor")
-        if lengths.device != device or lengths.shape != (B,) or not lengths.is_contiguous():
-            raise ValueError(f"lengths must be dense, [{B}], on {device}")
+        if lengths.get_device() != device or lengths.shape != (B,) or not lengths.is_contiguous():
+            raise ValueError(f"lengths must be dense, [{B}], on cuda:{device}")
         at = lengths.data_ptr()
-    return (kind, B, heads, kv, n, s, d, 1.0 / math.sqrt(d) if scale is None else scale), views, at
+    return device, (kind, B, heads, kv, n, s, d, 1.0 / math.sqrt(d) if scale is None else scale), views, at
 
 
 def _call(fn: str, packed: bytes, handle: int) -> None:
@@ -53,18 +53,21 @@ def cross_forward(Q, K, V, lengths=None, *, H=None, scale: float | None = None, 
     states.  An entry of length 0 has H = 0.  scale defaults to 1/sqrt(d).  Returns H [B, heads, n, d] in Q's order of
     axes, and with return_lse the logarithm of each row's sum, fp32 [B, heads, n], which ``cross_backward`` takes.
     Asynchronous on ``stream`` or the current stream."""
-    numbers, views, at_lengths = _problem(Q, K, V, lengths, scale)
-    at, lse = Launch(Q.device, stream), None
+    device, numbers, views, at_lengths = _problem(Q, K, V, lengths, scale)
+    at, lse = Launch(device, stream), None
     with at as handle:
         if H is None:
-            H = empty_like(Q)
-        elif isinstance(H, torch.Tensor) and H.shape != Q.shape:
-            raise ValueError("H must have Q's shape")
+            H, to = empty_like(Q)
+        else:
+            to = view(H, "H", Q.dtype, device)
+            if H.shape != Q.shape:
+                raise ValueError("H must have Q's shape")
         if return_lse:
             lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
-        _call("anchor_attn_cross_forward", _pack(*numbers, *views, *view(H, "H", Q.dtype, Q.device), *NO_VIEW, *NO_VIEW, *NO_VIEW, *NO_VIEW,
+        _call("anchor_attn_cross_forward", _pack(*numbers, *views, *to, *NO_VIEW, *NO_VIEW, *NO_VIEW, *NO_VIEW,
                                                  lse.data_ptr() if return_lse else 0, at_lengths), handle)
-    at.used((Q, K, V, lengths), (H, lse))
+    if at.stream is not None:
+        at.used((Q, K, V, lengths), (H, lse))
     return (H, lse) if return_lse else H
 
 
@@ -72,20 +75,19 @@ def cross_backward(Q, K, V, H, lse, dH, lengths=None, *, scale: float | None = N
     """(dQ, dK, dV) for the upstream gradient dH of ``cross_forward``'s H; H and lse are its results for the same
     Q, K, V, lengths and scale.  Rows of dK and dV from an entry's length on are zero.  K or V that entries share by
     an expanded axis get a gradient for each entry."""
-    numbers, views, at_lengths = _problem(Q, K, V, lengths, scale)
-    dtype, device, shape = Q.dtype, Q.device, Q.shape
+    device, numbers, views, at_lengths = _problem(Q, K, V, lengths, scale)
+    dtype, shape = Q.dtype, Q.shape
     views += (*view(H, "H", dtype, device), *view(dH, "dH", dtype, device))
     if H.shape != shape or dH.shape != shape:
         raise ValueError("H and dH must have Q's shape")
-    if not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32 or lse.device != device:
-        raise TypeError(f"lse must be a float32 tensor on {device}")
+    if not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32 or lse.get_device() != device:
+        raise TypeError(f"lse must be a float32 tensor on cuda:{device}")
     if lse.shape != shape[:3] or not lse.is_contiguous():
         raise ValueError("lse must be dense, [B, heads, n]")
     at = Launch(device, stream)
     with at as handle:
-        dQ, dK, dV = empty_like(Q), empty_like(K), empty_like(V)
-        for t, name in ((dQ, "dQ"), (dK, "dK"), (dV, "dV")):
-            views += view(t, name, dtype, device)
-        _call("anchor_attn_cross_backward", _pack(*numbers, *views, lse.data_ptr(), at_lengths), handle)
-    at.used((Q, K, V, H, lse, dH, lengths), (dQ, dK, dV))
+        (dQ, to_q), (dK, to_k), (dV, to_v) = empty_like(Q), empty_like(K), empty_like(V)
+        _call("anchor_attn_cross_backward", _pack(*numbers, *views, *to_q, *to_k, *to_v, lse.data_ptr(), at_lengths), handle)
+    if at.stream is not None:
+        at.used((Q, K, V, H, lse, dH, lengths), (dQ, dK, dV))
     return dQ, dK, dV

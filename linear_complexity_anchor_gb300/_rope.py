@@ -86,15 +86,15 @@ def rope_table(rot: int, base: float = 10000.0, *, device="cuda", **how) -> Rope
 
 
 def _how(x, table, interleaved, norm, eps, weights, positions):
-    """The packed anchor_attn_rope_t, and (d, rot, axes)."""
-    kind = rows_dtype(x, "the rows")
+    """The packed anchor_attn_rope_t, and (d, rot, axes, device)."""
+    kind, dtype, device = rows_dtype(x, "the rows"), x.dtype, x.get_device()
     axes, rot, magnitude, at = 1, 0, 1.0, 0
     if table is not None:
         phases, magnitude = table
         if not isinstance(phases, torch.Tensor) or phases.dtype is not torch.int64 or phases.dim() != 2 or not phases.is_contiguous():
             raise TypeError("the table's phases must be a contiguous int64 tensor [axes, rot / 2]")
-        if phases.device != x.device:
-            raise ValueError(f"the table must be on {x.device}")
+        if phases.get_device() != device:
+            raise ValueError(f"the table must be on cuda:{device}")
         axes, rot = phases.shape
         rot, at = 2 * rot, phases.data_ptr()
     wide = long = -1  # not yet known
@@ -107,16 +107,16 @@ def _how(x, table, interleaved, norm, eps, weights, positions):
     for w in weights:
         if w is not None:
             here = 1 if w.dtype is torch.float32 else 0
-            if (not here and w.dtype is not x.dtype) or wide == 1 - here:
+            if (not here and w.dtype is not dtype) or wide == 1 - here:
                 raise TypeError("weights must be of the rows' type or float32, and of one type")
             wide = here
     d = x.shape[-1]
-    return _pack_how(kind, d, rot, axes, 1 if interleaved else 0, norm, max(wide, 0), max(long, 0), eps, magnitude, at), (d, rot, axes)
+    return _pack_how(kind, d, rot, axes, 1 if interleaved else 0, norm, max(wide, 0), max(long, 0), eps, magnitude, at), (d, rot, axes, device)
 
 
-def _rows(size, like, X, Y, dY, dX, shape, positions, start, weight, dweight, name):
+def _rows(size, X, Y, dY, dX, shape, positions, start, weight, dweight, name):
     """The packed anchor_attn_rows_t of one tensor of this shape; X ... dX are its views."""
-    d, rot, axes = size
+    d, rot, axes, device = size
     B, heads, n, width = shape
     if width != d:
         raise ValueError(f"{name} must have heads of {d}, got {width}")
@@ -128,13 +128,13 @@ def _rows(size, like, X, Y, dY, dX, shape, positions, start, weight, dweight, na
             batch = n * axes
         elif of != (n, *last):
             raise ValueError(f"positions of {name} must be {[n, *last]} or {[B, n, *last]}, got {list(of)}")
-        if positions.device != like.device:
-            raise ValueError(f"positions must be on {like.device}")
+        if positions.get_device() != device:
+            raise ValueError(f"positions must be on cuda:{device}")
         if not positions.is_contiguous():
             raise ValueError("positions must be contiguous")
         at = positions.data_ptr()
-    if weight is not None and (weight.shape != (d,) or weight.device != like.device or not weight.is_contiguous()):
-        raise ValueError(f"the weight of {name} must be dense, [{d}], on {like.device}")
+    if weight is not None and (weight.shape != (d,) or weight.get_device() != device or not weight.is_contiguous()):
+        raise ValueError(f"the weight of {name} must be dense, [{d}], on cuda:{device}")
     return _pack_rows(*X, *Y, *dY, *dX, 0 if weight is None else weight.data_ptr(), 0 if dweight is None else dweight.data_ptr(),
                       at, batch, start, B, heads, n)
 
@@ -146,25 +146,26 @@ def _call(fn: str, how: bytes, first: bytes, second, handle: int) -> None:
 
 
 def _forward(X, table, positions, starts, weights, norm, eps, interleaved, out, stream):
-    like = X[0]
-    how, size = _how(like, table, interleaved, norm, eps, weights, positions)
-    dtype, device = like.dtype, like.device
+    how, size = _how(X[0], table, interleaved, norm, eps, weights, positions)
+    dtype, device = X[0].dtype, size[3]
     views = [None if x is None else view(x, name, dtype, device) for x, name in zip(X, "QK")]
-    at, Y, rows = Launch(device, stream), [], []
+    at, Y, rows = Launch(device, stream), [None, None], [None, None]
     with at as handle:
-        for x, v, y, p, s, w, name in zip(X, views, out, positions, starts, weights, "QK"):
+        for i, x in enumerate(X):
             if x is None:
-                Y.append(None)
-                rows.append(None)
                 continue
+            name, y, shape = "QK"[i], out[i], x.shape
             if y is None:
-                y = empty_like(x)
-            elif isinstance(y, torch.Tensor) and y.shape != x.shape:
-                raise ValueError(f"the output for {name} must have its shape")
-            Y.append(y)
-            rows.append(_rows(size, like, v, view(y, f"the output for {name}", dtype, device), NO_VIEW, NO_VIEW, x.shape, p, s, w, None, name))
+                y, to = empty_like(x)
+            else:
+                to = view(y, f"the output for {name}", dtype, device)
+                if y.shape != shape:
+                    raise ValueError(f"the output for {name} must have its shape")
+            Y[i] = y
+            rows[i] = _rows(size, views[i], to, NO_VIEW, NO_VIEW, shape, positions[i], starts[i], weights[i], None, name)
         _call("anchor_attn_norm_rope", how, rows[0], rows[1], handle)
-    at.used((*X, *positions, *weights, table[0] if table is not None else None), Y)
+    if at.stream is not None:
+        at.used((*X, *positions, *weights, table[0] if table is not None else None), Y)
     return Y
 
 
@@ -186,13 +187,14 @@ def rope_backward(dY, table, positions=None, *, start: int = 0, interleaved: boo
     if table is None:
         raise ValueError("rope_backward needs a table")
     how, size = _how(dY, table, interleaved, 0, 0.0, (), (positions,))
-    g = view(dY, "dY", dY.dtype, dY.device)
-    at = Launch(dY.device, stream)
+    g = view(dY, "dY", dY.dtype, size[3])
+    at = Launch(size[3], stream)
     with at as handle:
-        dX = empty_like(dY)
-        rows = _rows(size, dY, NO_VIEW, NO_VIEW, g, view(dX, "dX", dY.dtype, dY.device), dY.shape, positions, start, None, None, "dY")
+        dX, to = empty_like(dY)
+        rows = _rows(size, NO_VIEW, NO_VIEW, g, to, dY.shape, positions, start, None, None, "dY")
         _call("anchor_attn_norm_rope_backward", how, rows, None, handle)
-    at.used((dY, positions, table[0]), (dX,))
+    if at.stream is not None:
+        at.used((dY, positions, table[0]), (dX,))
     return dX
 
 
@@ -215,19 +217,21 @@ def norm_rope_backward(Q, K, dQ, dK, table, *, q_weight=None, k_weight=None, q_p
     if K is None:
         G, W, P = (dQ, None), (q_weight, None), (q_positions, None)
     how, size = _how(Q, table, interleaved, 1, eps, W, P)
-    dtype, device = Q.dtype, Q.device
+    dtype, device = Q.dtype, size[3]
     views = [None if x is None else (view(x, name, dtype, device), view(g, f"d{name}", dtype, device)) for x, g, name in zip(X, G, "QK")]
-    at, dX, dW, rows = Launch(device, stream), [], [], []
+    at, dX, dW, rows = Launch(device, stream), [None, None], [None, None], [None, None]
     with at as handle:
-        for x, v, g, p, s, w, name in zip(X, views, G, P, (q_start, k_start), W, "QK"):
-            dX.append(None if x is None else empty_like(x))
-            dW.append(None if w is None else torch.empty_like(w))
+        for i, x in enumerate(X):
             if x is None:
-                rows.append(None)
                 continue
-            if g.shape != x.shape:
+            name, shape, w = "QK"[i], x.shape, W[i]
+            dX[i], to = empty_like(x)
+            if w is not None:
+                dW[i] = torch.empty_like(w)
+            if G[i].shape != shape:
                 raise ValueError(f"d{name} must have {name}'s shape")
-            rows.append(_rows(size, Q, v[0], NO_VIEW, v[1], view(dX[-1], f"d{name}", dtype, device), x.shape, p, s, w, dW[-1], name))
+            rows[i] = _rows(size, views[i][0], NO_VIEW, views[i][1], to, shape, P[i], (q_start, k_start)[i], w, dW[i], name)
         _call("anchor_attn_norm_rope_backward", how, rows[0], rows[1], handle)
-    at.used((*X, *G, *W, *P, table[0] if table is not None else None), (*dX, *dW))
+    if at.stream is not None:
+        at.used((*X, *G, *W, *P, table[0] if table is not None else None), (*dX, *dW))
     return dX[0], dX[1], dW[0], dW[1]

@@ -37,19 +37,19 @@ def rows_dtype(t, name: str) -> int:
     dt = DTYPES.get(t.dtype)
     if dt is None:
         raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-    if not t.is_cuda:
+    if t.get_device() < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     return dt
 
 
-def view(t, name: str, dtype, device) -> tuple:
-    """(pointer, strides) of a four-axis CUDA tensor of this type and device whose last axis is dense."""
+def view(t, name: str, dtype, device: int) -> tuple:
+    """(pointer, strides) of a four-axis tensor of this type, on this CUDA device, whose last axis is dense."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
     strides = t.stride()
     if len(strides) != 4:
         raise ValueError(f"{name} must have 4 axes, got {len(strides)}")
@@ -59,26 +59,31 @@ def view(t, name: str, dtype, device) -> tuple:
 
 
 def empty_like(t):
-    """A tensor of t's shape, with t's order of axes where t is dense."""
+    """A tensor of t's shape, with t's order of axes where t is dense, and its view."""
     r = torch.empty_like(t)
-    return r if r.stride(3) == 1 or r.size(3) <= 1 else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    strides = r.stride()
+    if strides[3] != 1 and r.size(3) > 1:
+        r = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        strides = r.stride()
+    return r, (r.data_ptr(), strides[0], strides[1], strides[2])
 
 
 class Launch:
     """The device and stream of one call: `with Launch(device, stream) as handle`.  Tensors made inside belong to that
-    stream; `used(...)` tells the allocator of tensors that are used on a stream other than their own."""
+    stream; where `stream` is not None, `used(...)` tells the allocator of tensors that are used on a
+    stream other than their own."""
 
     __slots__ = ("device", "handle", "stream", "current", "guards")
 
-    def __init__(self, device, stream=None):
+    def __init__(self, device: int, stream=None):
         self.device, self.stream, self.guards = device, None, ()
         if stream is None and _raw_stream is not None:
-            self.handle = _raw_stream(device.index)
+            self.handle = _raw_stream(device)
             return
         self.current = torch.cuda.current_stream(device)
         stream = self.current if stream is None else stream
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        if stream.device.index != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{device}")
         self.handle = stream.cuda_stream
         if stream != self.current:
             self.stream = stream
@@ -86,7 +91,7 @@ class Launch:
     def __enter__(self) -> int:
         if self.stream is not None:
             self.guards = (torch.cuda.device(self.device), torch.cuda.stream(self.stream))
-        elif _current_device() != self.device.index:
+        elif _current_device() != self.device:
             self.guards = (torch.cuda.device(self.device),)
         for g in self.guards:
             g.__enter__()
@@ -97,10 +102,10 @@ class Launch:
             g.__exit__(*exc)
 
     def used(self, inputs, outputs=()) -> None:
-        if self.stream is not None:
-            for t in inputs:
-                if t is not None:
-                    t.record_stream(self.stream)
-            for t in outputs:
-                if t is not None:
-                    t.record_stream(self.current)
+        """For a call whose `stream` is not None."""
+        for t in inputs:
+            if t is not None:
+                t.record_stream(self.stream)
+        for t in outputs:
+            if t is not None:
+                t.record_stream(self.current)
