@@ -757,14 +757,22 @@ bool make_tile_map(TileMap *m, const CrossView &v, int B, int heads, int rows, i
 // kCluster of them are the CTAs of a cluster, which joins them itself: a token of 12 heads over 1500
 // states takes one launch and no workspace.  More (a second launch joins them) where each of the
 // cluster's would have more than kClusterTiles tiles.
-constexpr int kCluster = 8, kClusterTiles = 8;
+// One tile of rows, CTAs enough for the SMs but long: parts of kLong tiles and more, a cluster's, where the last
+// wave would be long and thin: entries of lengths of their own, for a few waves, or, longer still, hardly more CTAs
+// than places (64 x 8 key heads, up to 8192 states, d = 128: 215 -> 204 us; 24 x 8, up to 16384: 193 -> 155; 20 x 8,
+// 65536 each: 1089 -> 773; 20 x 8, 32768 each, d = 64: 348 -> 239; but 200 x 12, up to 8200, d = 64: 523 -> 544; 32 x
+// 8, 8192 each, d = 128: 153 -> 169; 14 x 8: 69 -> 82).  The join takes about 5 us of each of a cluster's CTAs: 128 x 8, up
+// to 2048: 110 -> 149.
+constexpr int kCluster = 8, kClusterTiles = 8, kLong = 32;
 CrossPlan cross_tc_plan(const CrossProblem &p) {
     if (is_short(p)) return CrossPlan{1, false};
     const int nq = tiles_per_cta(p), per_sm = p.d <= 64 ? 2 : 1;
-    const long long ctas = (long long)p.B * p.kv * ((p.rows + nq * kRows - 1) / (nq * kRows));
-    const long long want = (long long)per_sm * kPlanSMs / std::max(1LL, ctas), tiles = (p.s + kRows - 1) / kRows;
+    const long long ctas = (long long)p.B * p.kv * ((p.rows + nq * kRows - 1) / (nq * kRows)), places = (long long)per_sm * kPlanSMs;
+    const long long want = places / std::max(1LL, ctas), tiles = (p.s + kRows - 1) / kRows;
     if (nq == 1 && want > 1 && (want <= kCluster || tiles <= kCluster * kClusterTiles))
         return CrossPlan{(int)std::min(std::min(want, (long long)kCluster), tiles), false};
+    if (nq == 1 && want <= 1 && (p.lengths ? tiles >= 2 * kLong && ctas < 6 * places : tiles >= 4 * kLong && 3 * ctas < 4 * places))
+        return CrossPlan{(int)std::min(tiles / kLong, (long long)kCluster), false};
     const int parts = (int)std::max(1LL, std::min(want, (tiles + 1) / 2));
     return CrossPlan{parts, parts > 1};
 }

@@ -68,7 +68,8 @@ def test_shapes(aa, dtype, d, shape):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape,lengths", [((9, 4, 2, 1, 700, 64), "mixed"), ((1, 12, 12, 1, 1500, 64), None), ((1, 1, 1, 1, 9000, 128), None),
                                            ((3, 8, 1, 1, 2050, 128), "mixed"), ((2, 8, 2, 5, 1300, 32), "mixed"), ((1, 32, 1, 4, 640, 128), None),
-                                           ((2, 64, 2, 1, 333, 16), "mixed"), ((4, 2, 2, 2, 5000, 64), 0)])
+                                           ((2, 64, 2, 1, 333, 16), "mixed"), ((4, 2, 2, 2, 5000, 64), 0),
+                                           ((20, 16, 8, 1, 8200, 128), "mixed"), ((20, 8, 8, 3, 16400, 64), None)])
 def test_few_queries(aa, dtype, shape, lengths):
     check(aa, 7, *shape, dtype, lengths=lengths, train=False)
 
