@@ -192,7 +192,7 @@ anchor_attn_status_t cross(const anchor_attn_cross_t *a, bool bwd, void *stream_
         if (queries) {
             if (!take(rows_bytes)) return ANCHOR_ATTN_ERR_ALLOC;
             delta = (float *)ws;
-            e = launch_cross_delta(p, delta, stream);
+            if (p.f32) e = launch_cross_delta(p, delta, stream);  // (bf16: with its own)
         }
         if (e == cudaSuccess)
             e = p.f32 ? launch_cross_simt_backward(p, delta, stream) : launch_cross_tc_backward(p, delta, stream);

@@ -5,7 +5,7 @@
 // Two kinds of CTAs, one that keeps queries and one that keeps keys, so that every gradient is summed in
 // tensor memory by one CTA in a fixed order, without atomics.  S and dP are made twice for
 // that: seven products where five would do.  Both are of one launch, those that take longer first, so that
-// the others fill the SMs that they leave (D comes from a launch before; with the queries first and
+// the others fill the SMs that they leave (D comes from a launch before, but see kFine; with the queries first and
 // D made by them, in a launch of their own, 2 x 16 heads over 4, 2049 x 1500, d = 128: 188 us against 152).
 //
 //   queries   a tile of 128 rows of Q and dH stays, the keys of the entry stream by:
@@ -23,7 +23,7 @@
 //             after dS^T(j): dK += dS^T(j) Q, dP^T(j + 1)    while the rows make P^T(j + 1)
 //   queries   after S(j) is read: S(j + 1);  after dS(j): dQ += dS(j) K, dP(j + 1)
 // (a product that overwrites an operand is issued after the one that reads it).  P and dS are rounded to
-// bf16, the operands' type (with few states dS to two of them, see kFine); S, dP, P in dS, and all sums are fp32.
+// bf16, the operands' type (dS to two of them at times, see kFine); S, dP, P in dS, and all sums are fp32.
 // States from the length on: P and dS are zero there by select, and rows of K that meet a zero of dS
 // are zeroed in shared memory.
 #include "cross_tc.cuh"
@@ -42,12 +42,16 @@ using namespace cross_tc;
 
 constexpr int kSlice = 32;  // columns of S and dP that a row warp takes
 
-// Up to so many states dS meets K and Q as two bf16 numbers, the second what the rounding of the first left: an
+// Up to kFine states dS meets K and Q as two bf16 numbers, the second what the rounding of the first left: an
 // eighth product and a ninth.  dQ and dK carry the rounding of dS, their own, and that of H through D, which
 // is 2^-9 of dP over the root of the number of states that weigh: with few of them the three together are
-// up to 1.8 times a lone rounding of the result (8 states; 1.56 at 50, 1.50 at 256, 1.46 at 1000), and with two
-// numbers 1.46, 1.19, 1.08, 1.05.  It takes 6 % of time at 77 states, 10 at 300, 18 at 600, 25 at 1000 and more.
-constexpr int kFine = 384;
+// up to 1.8 times a lone rounding of the result (8 states; 1.56 at 50, 1.50 at 256), and with two numbers 1.46,
+// 1.19, 1.07.  It takes 6 % of time at 77 states, 10 at 300, 18 at 600, 25 at 1000 and more.
+// One tile of states: the queries' CTAs make D from P and dP instead (1.00 at 8 and 50), and the keys' CTAs follow in
+// a launch of their own (256 x 12 heads, 49 x 49: 130 us against 133 with D from H).
+// More than kFine, d <= 64: in every kSome-th step of the queries', whose dQ is 1.49 to 1.53 roundings off
+// without and 1.40 to 1.44 with, for 2.5 % of a training step's time (dK: 1.40 to 1.46).
+constexpr int kFine = 384, kSome = 4;
 
 // D columns (heads of 16 and 32 are 64), streaming tiles of W rows.
 template <int D, int W>
@@ -63,7 +67,7 @@ struct Geo {
     static constexpr int kFix = 0, kA = 2 * kTile<D>, kB = kA + kNA * kSlot;
     static constexpr int kStatB = kB + kNB * kSlot;  // keys: lse, D of W columns
     static constexpr int kBars = kStatB + 2 * W * 4;
-    static constexpr int kNBars = kNA + 2 * kNB + 11;
+    static constexpr int kNBars = kNA + 2 * kNB + 15;
     static constexpr int kSmem = kBars + kNBars * 8 + 16 + 1024;
     static constexpr uint32_t kColS = 0, kColP = W, kColA = 2 * W;  // S, dP, then the sums
     static constexpr uint32_t kCols = 2 * W + 2 * D;                // of tensor memory
@@ -73,12 +77,13 @@ struct Geo {
 
 struct BwdParams {
     CrossProblem p;
-    const float *delta;  // D
+    float *delta;        // D
     TileMap q, g, k, v;  // g: dH
     int tiles[2];        // of the queries and of the keys of a key head
     Divide by_tiles[2];
     int first;           // CTAs of the kind that comes first
     bool keys_first;
+    bool exact;          // one tile of states: the queries' CTAs make D themselves
 };
 
 // The work of CTA `index` of its kind (KEYS: see above).  FINE: dS as two numbers.
@@ -93,7 +98,8 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G::kBars);
     uint64_t *a_full = bars /* [NA] */, *b_full = a_full + NA /* [NB] */, *empty = b_full + NB /* [NB] */, *fix_full = empty + NB,
              *s_full = fix_full + 1, *dp_full = s_full + 1, *p_full = dp_full + 1, *ds_full = p_full + 1, *lse_full = ds_full + 1,
-             *lse_empty = lse_full + 1, *d_full = lse_empty + 1, *d_empty = d_full + 1, *acc = d_empty + 1, *done = acc + 1;
+             *lse_empty = lse_full + 1, *d_full = lse_empty + 1, *d_empty = d_full + 1, *acc = d_empty + 1, *done = acc + 1,
+             *meet = done + 1 /* [4] */;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + G::kNBars);
     float *stat = reinterpret_cast<float *>(sm + G::kStatB);
     const CrossProblem &p = a.p;
@@ -120,6 +126,7 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
         mbar_init(d_empty, kRowWarps);
         mbar_init(acc, 1);
         mbar_init(done, 1);
+        for (int s = 0; s < 4; ++s) mbar_init(meet + s, G::kSlices);
         fence_mbar_init();
     }
     if (warp == kIssue) tmem_alloc(s_tmem, G::kCols);
@@ -147,6 +154,7 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
     };
     const int around = KEYS ? per_head : nt;
     const Walk start{0, 0, around, KEYS ? p.group : 1};
+    auto two = [](int j) { return FINE || (D == 64 && !KEYS && j % kSome == 0); };  // dS of step j is two numbers
     // columns of a tile that exist
     auto width = [&](int t) { return min(W, (KEYS ? p.n : L) - t * W); };
 
@@ -306,7 +314,7 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
                 tc_fence_after();
                 const uint32_t sum = tmem + kColA + (KEYS ? D : 0);
                 along(sum, tmem + kColP, slot_a(j), last, j > 0);  // dK += dS^T Q, dQ += dS K
-                if (FINE) along(sum, tmem + kColP + kSlice / 2, slot_a(j), last, true);
+                if (two(j)) along(sum, tmem + kColP + kSlice / 2, slot_a(j), last, true);
                 if (more) {
                     product_k<D>(tmem + kColP, f1, desc_k(slot_b(j + 1)), then ? idL : idF, ksteps,
                                  [&] { landed_a = mbar_test(a_bar + (j + 2) % NA, a_par(j + 2)); });
@@ -347,8 +355,12 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
             if (lane == 0) mbar_arrive(fix_full);
             if (mine) {
                 const long long f = cross_flat(p, b, kh, r);
-                const float x2 = -p.lse[f] * kLog2e, d2 = -a.delta[f];
-                lse2 = f32x2(x2, x2), dl = f32x2(d2, d2);
+                const float x2 = -p.lse[f] * kLog2e;
+                lse2 = f32x2(x2, x2);
+                if (!FINE || !a.exact) {
+                    const float d2 = -a.delta[f];
+                    dl = f32x2(d2, d2);
+                }
             }
         }
         const uint32_t tS = trow + kColS + kSlice * quarter, tP = trow + kColP + kSlice * quarter;
@@ -400,6 +412,23 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
                 uint32_t u[16];
                 tmem_ld32(tP, g);
                 tmem_ld_wait();
+                if constexpr (FINE && !KEYS) {
+                    if (a.exact) {  // D = sum_j P dP, over this warp's columns, then over the slices (a slot that one step leaves free)
+                        float sum = 0.f;
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) sum += cut && (!mine || y >= cols) ? 0.f : e[y] * g[y];
+                        float *parts = reinterpret_cast<float *>(sm + G::kA + G::kSlot) + row;
+                        parts[quarter * kRows] = sum;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(meet + w4);
+                        if (!bwait(meet + w4, 0u, error)) { ok = false; break; }
+                        sum = 0.f;
+#pragma unroll
+                        for (int x = 0; x < G::kSlices; ++x) sum += parts[x * kRows];
+                        if (mine && quarter == 0) a.delta[cross_flat(p, b, kh, r)] = sum;
+                        dl = f32x2(-sum, -sum);
+                    }
+                }
 #pragma unroll
                 for (int y = 0; y < 32; y += 4) {
                     ulonglong2 d4 = make_ulonglong2(dl, dl);
@@ -415,7 +444,7 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
 #pragma unroll
                 for (int y = 0; y < 16; ++y) u[y] = pack2(g[2 * y], g[2 * y + 1]);
                 tmem_st16(tP, u);
-                if constexpr (FINE) {  // what the rounding left, over the slice's other columns
+                if (two(j)) {  // what the rounding left, over the slice's other columns
 #pragma unroll
                     for (int y = 0; y < 16; ++y)
                         u[y] = pack2(g[2 * y] - __uint_as_float(u[y] << 16), g[2 * y + 1] - __uint_as_float(u[y] & 0xffff0000u));
@@ -495,29 +524,38 @@ __global__ void __launch_bounds__(Geo<D, W>::kThreads, Geo<D, W>::kPerSM) cross_
 }
 
 template <int D, int W, bool FINE>
-cudaError_t backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
+cudaError_t backward(const CrossProblem &p, float *delta, cudaStream_t stream) {
     using G = Geo<D, W>;
     BwdParams a;
     a.p = p;
     a.delta = delta;
-    const int ctas[2] = {(p.rows + kRows - 1) / kRows, (p.s + kRows - 1) / kRows};
-    for (int i = 0; i < 2; ++i) a.tiles[i] = ctas[i], a.by_tiles[i] = Divide((uint32_t)std::max(1, ctas[i]));
-    // first those that take longer: four products over the queries against three over the keys
-    a.keys_first = 4LL * p.rows >= 3LL * p.s;
-    a.first = a.tiles[a.keys_first] * p.B * p.kv;
+    int ctas[2] = {(p.rows + kRows - 1) / kRows, (p.s + kRows - 1) / kRows};
+    for (int i = 0; i < 2; ++i) a.tiles[i] = ctas[i], a.by_tiles[i] = Divide((uint32_t)std::max(1, ctas[i])), ctas[i] *= p.B * p.kv;
     if (p.s > 0 && (!make_tile_map(&a.k, p.K, p.B, p.kv, p.s, p.d, W) || !make_tile_map(&a.v, p.V, p.B, p.kv, p.s, p.d, W)))
         return cudaErrorInvalidValue;
     if (p.s > 0 && p.n > 0 && (!make_tile_map(&a.q, p.Q, p.B, p.heads, p.n, p.d, W) || !make_tile_map(&a.g, p.dH, p.B, p.heads, p.n, p.d, W)))
         return cudaErrorInvalidValue;
     static SmemOnce allow;
-    const cudaError_t e = allow(cross_bwd_kernel<D, W, FINE>, G::kSmem);
+    cudaError_t e = allow(cross_bwd_kernel<D, W, FINE>, G::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cross_bwd_kernel<D, W, FINE>, dim3((a.tiles[0] + a.tiles[1]) * p.B * p.kv), dim3(G::kThreads), G::kSmem, stream, a);
+    auto run = [&](int grid) { return launch_pdl(cross_bwd_kernel<D, W, FINE>, dim3(grid), dim3(G::kThreads), G::kSmem, stream, a); };
+    a.exact = p.s <= W;
+    if (a.exact) {  // the keys' CTAs after the queries', who make D
+        a.keys_first = false, a.first = ctas[0];
+        if (ctas[0] > 0) e = run(ctas[0]);
+        a.keys_first = true, a.first = ctas[1];
+        return e != cudaSuccess || ctas[1] == 0 ? e : run(ctas[1]);
+    }
+    if (ctas[0] > 0) e = launch_cross_delta(p, delta, stream);
+    // first those that take longer: four products over the queries against three over the keys
+    a.keys_first = 4LL * p.rows >= 3LL * p.s;
+    a.first = ctas[a.keys_first];
+    return e != cudaSuccess ? e : run(ctas[0] + ctas[1]);
 }
 
 }  // namespace
 
-cudaError_t launch_cross_tc_backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
+cudaError_t launch_cross_tc_backward(const CrossProblem &p, float *delta, cudaStream_t stream) {
     if (p.s <= kFine) return p.d > 64 ? backward<128, 128, true>(p, delta, stream) : backward<64, 64, true>(p, delta, stream);
     return p.d > 64 ? backward<128, 128, false>(p, delta, stream) : backward<64, 64, false>(p, delta, stream);
 }

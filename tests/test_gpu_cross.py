@@ -334,15 +334,17 @@ def test_gradient_against_differences(aa):
 def test_few_states_lose_little(aa, s, d):
     """Up to 384 states dQ and dK are off by little more than their own rounding.  With scores near 0 all s states weigh
     alike.  H is off by its rounding and by that of the weights, together at most 1.1 * sqrt(2) of a rounding's root mean
-    square e; D = dH . H by that much of dP over sqrt(s); so dQ and dK by e sqrt(1 + 2.42 / s).  (A dS rounded once
-    would make it e sqrt(2 + 2.42 / s).)  A tenth more is left for chance: they have 10^5 elements and more."""
+    square e; D = dH . H by that much of dP over sqrt(s); so dQ and dK by e sqrt(1 + 2.42 / s), and by e alone where one
+    tile (64 states, 128 at d = 128) has D from P and dP.  (A dS rounded once would make it e sqrt(2 + 2.42 / s).)  A tenth
+    more is left for chance: they have 10^5 elements and more, 10^4 at 8 states."""
     Q, K, V, dH = make(31 + s, 4, 4, 4, 300, s, d, "bf16", gain=0.1)
     H, lse = aa.cross_forward(Q, K, V, return_lse=True)
     ref = cross_reference(Q, K, V, None, d ** -0.5, dH)
+    of_h = 2.42 / s if s > (64 if d <= 64 else 128) else 0.0
     for name, got in zip(("dQ", "dK"), aa.cross_backward(Q, K, V, H, lse, dH)):
         exact = ref[name][0]
         own = float((exact.to(torch.bfloat16).double() - exact).norm())
-        assert float((got.double() - exact).norm()) <= 1.1 * math.sqrt(1 + 2.42 / s) * own, name
+        assert float((got.double() - exact).norm()) <= 1.1 * math.sqrt(1 + of_h) * own, name
 
 
 def test_refusals(aa):
