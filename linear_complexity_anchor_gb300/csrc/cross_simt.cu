@@ -446,14 +446,22 @@ cross_simt_backward_kernel(const CrossProblem p, const float *delta, int q_tiles
     else cross_simt_backward<D, BM, false>(p, delta, index, q_tiles);
 }
 
-// Rows of a tile: the most of 64, 32 and 16 whose tiles still give every SM a CTA, else 16.  Backward (keys > 0),
-// whose CTAs are of two lengths, below d = 128: the two that fit (4 x 6 heads, 197 x 300, d = 64, a training
-// step: 79 us, 87 with 64 rows, 98 with 16; the forward with 16: 30 against 27).
-int tile_rows(const CrossProblem &p, int queries, int keys) {
-    const long long heads = (long long)p.B * p.kv, want = keys > 0 && p.d < 128 ? 2 * kPlanSMs : kPlanSMs;
+// Rows of a forward's tile: the most of 64, 32 and 16 whose tiles still give every SM a CTA, else 16.
+int tile_rows(const CrossProblem &p) {
+    const long long heads = (long long)p.B * p.kv;
     int bm = 64;
-    while (bm > 16 && (heads * ((queries + bm - 1) / bm + (keys + bm - 1) / bm) < want || std::max(queries, keys) <= bm / 2)) bm /= 2;
+    while (bm > 16 && (heads * ((p.rows + bm - 1) / bm) < kPlanSMs || p.rows <= bm / 2)) bm /= 2;
     return bm;
+}
+
+// Rows of a backward's tiles: the least of the longest CTA's time and all CTAs' spread over the SMs' places,
+// whichever is more, where a row costs a quarter more in tiles of 32 and twice as much in tiles of 16 (a training
+// step of 4 x 6 heads, 197 x 300, d = 64: 79 us with 32, 87 with 64, 98 with 16; of 11 x 4 heads over 1, 119 x 8152: 1837
+// with 64, 1500 with 32).
+int backward_rows(const CrossProblem &p) {
+    const double longest = std::max(3. * p.s, 4. * p.rows), all = 7. * p.B * p.kv * p.rows * (double)p.s / (kPlanSMs * (p.d < 128 ? 2 : 1));
+    const double t64 = std::max(64 * longest, all), t32 = 1.25 * std::max(32 * longest, all), t16 = 2 * std::max(16 * longest, all);
+    return t64 <= std::min(t32, t16) ? 64 : t32 <= t16 ? 32 : 16;
 }
 
 template <int D, int BM>
@@ -485,14 +493,14 @@ cudaError_t backward(const CrossProblem &p, const float *delta, cudaStream_t str
 // Parts of the key axis: none while the row tiles alone fill the SMs; else so many that two CTAs
 // of them do, with two key tiles a part at least.
 int cross_simt_parts(const CrossProblem &p) {
-    const int bm = tile_rows(p, p.rows, 0);
+    const int bm = tile_rows(p);
     const long long ctas = (long long)p.B * p.kv * ((p.rows + bm - 1) / bm);
     const long long want = 2 * kPlanSMs / std::max(1LL, ctas), most = (p.s + 2 * kBN - 1) / (2 * kBN);
     return (int)std::max(1LL, std::min(want, most));
 }
 
 cudaError_t launch_cross_simt_forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
-    const int bm = tile_rows(p, p.rows, 0);
+    const int bm = tile_rows(p);
     auto go = [&](auto d) {
         constexpr int D = decltype(d)::value;
         return bm == 64   ? forward<D, 64>(p, w, stream)
@@ -508,7 +516,7 @@ cudaError_t launch_cross_simt_forward(const CrossProblem &p, const CrossParts &w
 }
 
 cudaError_t launch_cross_simt_backward(const CrossProblem &p, const float *delta, cudaStream_t stream) {
-    const int bm = tile_rows(p, p.rows, p.s);
+    const int bm = backward_rows(p);
     auto go = [&](auto d) {
         constexpr int D = decltype(d)::value;
         return bm == 64 ? backward<D, 64>(p, delta, stream) : bm == 32 ? backward<D, 32>(p, delta, stream) : backward<D, 16>(p, delta, stream);
