@@ -446,11 +446,18 @@ cross_simt_backward_kernel(const CrossProblem p, const float *delta, int q_tiles
     else cross_simt_backward<D, BM, false>(p, delta, index, q_tiles);
 }
 
-// Rows of a forward's tile: the most of 64, 32 and 16 whose tiles still give every SM a CTA, else 16.
+// Parts of a forward's keys that make many CTAs out of few: of twelve tiles and more each (d < 128).
+long long long_parts(const CrossProblem &p) { return p.d < 128 ? (p.s + kBN - 1) / kBN / 12 : 0; }
+
+// Rows of a forward's tile: the most of 64, 32 and 16 whose tiles, or long parts of them, still give every SM a CTA
+// (parts: two), else 16.
 int tile_rows(const CrossProblem &p) {
-    const long long heads = (long long)p.B * p.kv;
     int bm = 64;
-    while (bm > 16 && (heads * ((p.rows + bm - 1) / bm) < kPlanSMs || p.rows <= bm / 2)) bm /= 2;
+    auto few = [&] {
+        const long long ctas = (long long)p.B * p.kv * ((p.rows + bm - 1) / bm);
+        return ctas < kPlanSMs && ctas * long_parts(p) < 2 * kPlanSMs;
+    };
+    while (bm > 16 && (few() || p.rows <= bm / 2)) bm /= 2;
     return bm;
 }
 
@@ -490,13 +497,16 @@ cudaError_t backward(const CrossProblem &p, const float *delta, cudaStream_t str
 
 }  // namespace
 
-// Parts of the key axis: none while the row tiles alone fill the SMs; else so many that two CTAs
-// of them do, with two key tiles a part at least.
+// Parts of the key axis: none while the row tiles alone fill the SMs; else so many that two CTAs of them do, with
+// two key tiles a part at least.  Below d = 128, with few CTAs or very long keys, four times the places in long
+// parts, which even out (11 x 4 heads over 1, 119 x 8152, d = 64: 516 -> 295 us; 16 heads, 128 x 8000: 197 -> 117; 64 x 8 heads, 1 x 8000: 735 -> 650; but 32
+// heads, 500 x 2000: 226 -> 251, and at d = 128 3 x 8 heads, 300 x 3000: 360 -> 380).
 int cross_simt_parts(const CrossProblem &p) {
     const int bm = tile_rows(p);
-    const long long ctas = (long long)p.B * p.kv * ((p.rows + bm - 1) / bm);
-    const long long want = 2 * kPlanSMs / std::max(1LL, ctas), most = (p.s + 2 * kBN - 1) / (2 * kBN);
-    return (int)std::max(1LL, std::min(want, most));
+    const long long ctas = std::max(1LL, (long long)p.B * p.kv * ((p.rows + bm - 1) / bm)), tiles = (p.s + kBN - 1) / kBN;
+    const long long some = std::min(2 * kPlanSMs / ctas, (tiles + 1) / 2);
+    const long long many = ctas < kPlanSMs || tiles >= 96 ? std::min(8 * kPlanSMs / ctas, long_parts(p)) : 0;
+    return (int)std::max({1LL, some, many});
 }
 
 cudaError_t launch_cross_simt_forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream) {
