@@ -188,14 +188,16 @@ anchor_attn_status_t cross(const anchor_attn_cross_t *a, bool bwd, void *stream_
         e = p.f32 ? launch_cross_simt_forward(p, w, stream) : launch_cross_tc_forward(p, w, stream);
         if (e == cudaSuccess && join) e = launch_cross_join(p, w, stream);
     } else {
-        float *delta = nullptr;
-        if (queries) {
-            if (!take(rows_bytes)) return ANCHOR_ATTN_ERR_ALLOC;
-            delta = (float *)ws;
-            if (p.f32) e = launch_cross_delta(p, delta, stream);  // (bf16: with its own)
+        // D, and the sums of a backward whose steps are cut into parts
+        const size_t d_bytes = (rows_bytes + 255) / 256 * 256, sums_bytes = p.f32 || !queries ? 0 : cross_tc_backward_sums(p);
+        if (queries && !take(d_bytes + sums_bytes)) return ANCHOR_ATTN_ERR_ALLOC;
+        float *delta = (float *)ws, *sums = queries ? delta + d_bytes / 4 : nullptr;
+        if (p.f32) {
+            if (queries) e = launch_cross_delta(p, delta, stream);
+            if (e == cudaSuccess) e = launch_cross_simt_backward(p, delta, stream);
+        } else {
+            e = launch_cross_tc_backward(p, delta, sums, stream);
         }
-        if (e == cudaSuccess)
-            e = p.f32 ? launch_cross_simt_backward(p, delta, stream) : launch_cross_tc_backward(p, delta, stream);
     }
     if (ws) {
         const cudaError_t ef = cudaFreeAsync(ws, stream);

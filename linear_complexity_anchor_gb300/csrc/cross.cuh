@@ -73,7 +73,9 @@ struct CrossPlan {
 };
 CrossPlan cross_tc_plan(const CrossProblem &p);
 cudaError_t launch_cross_tc_forward(const CrossProblem &p, const CrossParts &w, cudaStream_t stream);
-cudaError_t launch_cross_tc_backward(const CrossProblem &p, float *delta, cudaStream_t stream);  // delta: a workspace
+// workspaces: D [B][heads][n], and sums of this many bytes
+size_t cross_tc_backward_sums(const CrossProblem &p);
+cudaError_t launch_cross_tc_backward(const CrossProblem &p, float *delta, float *sums, cudaStream_t stream);
 cudaError_t cross_bwd_read_and_clear_error(unsigned *out);
 cudaError_t cross_fwd_read_and_clear_error(unsigned *out);
 

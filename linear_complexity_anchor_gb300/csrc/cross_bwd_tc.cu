@@ -6,7 +6,8 @@
 // tensor memory by one CTA in a fixed order, without atomics.  S and dP are made twice for
 // that: seven products where five would do.  Both are of one launch, those that take longer first, so that
 // the others fill the SMs that they leave (D comes from a launch before, but see kFine; with the queries first and
-// D made by them, in a launch of their own, 2 x 16 heads over 4, 2049 x 1500, d = 128: 188 us against 152).
+// D made by them, in a launch of their own, 2 x 16 heads over 4, 2049 x 1500, d = 128: 188 us against 152).  CTAs that walk long are cut into
+// parts (see Parts).
 //
 //   queries   a tile of 128 rows of Q and dH stays, the keys of the entry stream by:
 //             S = Q K^T, dP = dH V^T, dQ += dS K
@@ -31,6 +32,8 @@
 #include <algorithm>
 
 #include <math.h>
+
+#include <type_traits>
 
 namespace anchor {
 
@@ -81,13 +84,17 @@ struct BwdParams {
     TileMap q, g, k, v;  // g: dH
     int tiles[2];        // of the queries and of the keys of a key head
     Divide by_tiles[2];
+    int parts[2];        // of the steps of a tile
+    Divide by_parts[2];
+    float *sums[2];      // with parts: [part][B * kv * rows of the kind][d] (queries), [2 d] (keys: dV, dK)
     int first;           // CTAs of the kind that comes first
     bool keys_first;
     bool exact;          // one tile of states: the queries' CTAs make D themselves
 };
 
-// The work of CTA `index` of its kind (KEYS: see above).  FINE: dS as two numbers.
-template <int D, bool KEYS, int W, bool FINE>
+// The work of CTA `index` of its kind (KEYS: see above).  FINE: dS as two numbers.  CUT:
+// steps in parts (a kernel of its own: 5 % more time for all where the numbers of parts are read).
+template <int D, bool KEYS, int W, bool FINE, bool CUT>
 __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
     using G = Geo<D, W>;
     constexpr int kRowWarps = G::kRowWarps, kLoad = G::kLoad, kStat = G::kStat, kIssue = G::kIssue;
@@ -104,7 +111,8 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
     float *stat = reinterpret_cast<float *>(sm + G::kStatB);
     const CrossProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int bk = a.by_tiles[KEYS].of(index), tile = index - bk * a.tiles[KEYS];
+    const int parts = CUT ? a.parts[KEYS] : 1, item = CUT ? a.by_parts[KEYS].of(index) : index, part = CUT ? index - item * parts : 0;
+    const int bk = a.by_tiles[KEYS].of(item), tile = item - bk * a.tiles[KEYS];
     const TileMap &map_a = KEYS ? a.q : a.k, &map_b = KEYS ? a.g : a.v;  // the tiles that stream by
     const int b = p.by_kv.of(bk), kh = bk - b * p.kv, r0 = tile * kRows;
     unsigned int *error = &g_cross_bwd_error;
@@ -140,7 +148,9 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
     const int L = cross_length(p, b);
     // steps over the tiles that stream by: keys of the entry, or the queries of each head in turn
     const int per_head = (p.n + W - 1) / W;
-    const int nt = KEYS ? (r0 < L ? p.group * per_head : 0) : (L + W - 1) / W;
+    const int steps = KEYS ? (r0 < L ? p.group * per_head : 0) : (L + W - 1) / W;
+    const int j0 = CUT ? (int)((long long)steps * part / parts) : 0;
+    const int nt = CUT ? (int)((long long)steps * (part + 1) / parts) - j0 : steps;
     // A walk over the steps: tile t of head g (without divisions, which the issuing thread would wait
     // for).
     struct Walk {
@@ -152,8 +162,8 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
             }
         }
     };
-    const int around = KEYS ? per_head : nt;
-    const Walk start{0, 0, around, KEYS ? p.group : 1};
+    const int around = KEYS ? per_head : steps, g0 = CUT && KEYS && part > 0 ? j0 / per_head : 0;
+    const Walk start{j0 - g0 * per_head, g0, around, KEYS ? p.group : 1};
     auto two = [](int j) { return FINE || (D == 64 && !KEYS && j % kSome == 0); };  // dS of step j is two numbers
     // columns of a tile that exist
     auto width = [&](int t) { return min(W, (KEYS ? p.n : L) - t * W); };
@@ -202,7 +212,7 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
         // heads, 197 x 300, d = 128: 182 -> 174 us; with many it takes 1 % more).
         if constexpr (FINE) {
             const int then = index + G::kPerSM * kPlanSMs;
-            if (then < a.tiles[KEYS] * p.B * p.kv) {
+            if (parts == 1 && then < a.tiles[KEYS] * p.B * p.kv) {
                 const int bk2 = a.by_tiles[KEYS].of(then), tile2 = then - bk2 * a.tiles[KEYS], b2 = p.by_kv.of(bk2), kh2 = bk2 - b2 * p.kv;
                 if (lane < 2) {
                     const TileMap &stay = lane ? a.v : a.k, &by = lane ? map_b : map_a;
@@ -452,7 +462,7 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
                 }
             }
             tmem_st_wait();
-            if (!KEYS && walk.t == nt - 1 && quarter == 0 && L % W && L < p.s) {
+            if (!KEYS && walk.t == steps - 1 && quarter == 0 && L % W && L < p.s) {
                 // the last tile's rows of K that do not count (S has read them)
                 if (!bwait(a_full + j % NA, (uint32_t)((j / NA) & 1), error)) { ok = false; break; }
                 zero_rows<D>(sm + G::kA + j % NA * G::kSlot, row, L % W, (L % W + 15) / 16 * 16);
@@ -483,6 +493,16 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
                     tmem_ld_wait();
                 }
                 const bool some = nt > 0 && mine;
+                if (CUT && parts > 1) {  // (cross_sums_kernel scales and rounds)
+                    const int rows = KEYS ? p.s : p.rows, width = KEYS ? 2 * p.d : p.d;
+                    float *dst = a.sums[KEYS] + (((long long)part * p.B * p.kv + bk) * rows + r) * width + (second ? p.d : 0) + x;
+#pragma unroll
+                    for (int y = 0; y < 32; y += 4)
+                        if (r < rows && x + y < p.d)
+                            *reinterpret_cast<float4 *>(dst + y) =
+                                some ? make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    continue;
+                }
 #pragma unroll
                 for (int y = 0; y < 32; ++y) o[y] = some ? o[y] * by : 0.f;
 #pragma unroll
@@ -494,7 +514,7 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
             }
             __syncwarp();
             const CrossView &v = KEYS ? (second ? p.dK : p.dV) : p.dQ;
-            const bool exists = r < (KEYS ? p.s : p.rows);
+            const bool exists = parts == 1 && r < (KEYS ? p.s : p.rows);
             const long long at = !exists ? -1 : KEYS ? b * v.sb + kh * v.sh + (long long)r * v.sn : cross_row(p, v, b, kh, r);
             // 16-byte chunks of this warp's rows and columns, a row's chunks by neighbouring lanes
             constexpr int kW = kCols / 8;
@@ -515,49 +535,128 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
     }
 }
 
-template <int D, int W, bool FINE>
+template <int D, int W, bool FINE, bool CUT>
 __global__ void __launch_bounds__(Geo<D, W>::kThreads, Geo<D, W>::kPerSM) cross_bwd_kernel(const __grid_constant__ BwdParams a) {
     const bool head = (int)blockIdx.x < a.first;
     const int index = (int)blockIdx.x - (head ? 0 : a.first);
-    if (head == a.keys_first) cross_bwd<D, true, W, FINE>(a, index);
-    else cross_bwd<D, false, W, FINE>(a, index);
+    if (head == a.keys_first) cross_bwd<D, true, W, FINE, CUT>(a, index);
+    else cross_bwd<D, false, W, FINE, CUT>(a, index);
 }
 
-template <int D, int W, bool FINE>
-cudaError_t backward(const CrossProblem &p, float *delta, cudaStream_t stream) {
+// The sums of parts, in order, scaled and rounded: eight columns of a row a thread.  Bound by memory.
+template <bool KEYS>
+__global__ void __launch_bounds__(256) cross_sums_kernel(const CrossProblem p, const float *sums, int parts) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int rows = KEYS ? p.s : p.rows, width = KEYS ? 2 * p.d : p.d, per = width / 8;
+    const long long total = (long long)p.B * p.kv * rows, i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long f = i / per;
+    if (f >= total) return;
+    int c = 8 * (int)(i - f * per);
+    float o[8] = {};
+    for (int q = 0; q < parts; ++q) {
+        const float4 *src = reinterpret_cast<const float4 *>(sums + (q * total + f) * width + c);
+        const float4 x = src[0], y = src[1];
+        o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w, o[4] += y.x, o[5] += y.y, o[6] += y.z, o[7] += y.w;
+    }
+    const bool second = c >= p.d;
+    if (second) c -= p.d;
+    const float by = KEYS && !second ? 1.f : p.scale;
+    const int bk = (int)(f / rows), r = (int)(f - (long long)bk * rows), b = bk / p.kv, k = bk - b * p.kv;
+    const CrossView &v = KEYS ? (second ? p.dK : p.dV) : p.dQ;
+    const long long at = KEYS ? b * v.sb + k * v.sh + (long long)r * v.sn : cross_row(p, v, b, k, r);
+    *reinterpret_cast<uint4 *>((__nv_bfloat16 *)v.ptr + at + c) =
+        make_uint4(pack2(o[0] * by, o[1] * by), pack2(o[2] * by, o[3] * by), pack2(o[4] * by, o[5] * by), pack2(o[6] * by, o[7] * by));
+}
+
+template <bool KEYS>
+cudaError_t add_up(const CrossProblem &p, const float *sums, int parts, cudaStream_t stream) {
+    const long long threads = (long long)p.B * p.kv * (KEYS ? 2LL * p.s : p.rows) * p.d / 8;
+    return launch_pdl(cross_sums_kernel<KEYS>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, p, sums, parts);
+}
+
+// Parts of a kind's steps.  A CTA that walks longer than all CTAs spread over the SMs' places would take is cut, into
+// parts of kSteps steps and more, whose sums a launch of its own adds in order.  With few states and many queries,
+// above all, each key tile's CTA walks all queries (3 x 32 heads over 8, 1582 x 87, d = 16: the
+// backward 125 us in one part, 60 in eight; 2 x 4 heads, 100 x 8192, d = 64: 131 against 34).
+constexpr int kSteps = 8;
+struct Parts {
+    int of[2];
+    size_t bytes[2];
+};
+Parts plan(const CrossProblem &p) {
+    const int W = p.d > 64 ? 128 : 64, heads = p.B * p.kv;
+    const long long places = (p.d > 64 ? 1 : 2) * (long long)kPlanSMs;
+    const long long steps[2] = {(p.s + W - 1) / W, (long long)p.group * ((p.n + W - 1) / W)};
+    const long long ctas[2] = {(long long)heads * ((p.rows + kRows - 1) / kRows), (long long)heads * ((p.s + kRows - 1) / kRows)};
+    const long long cost[2] = {3 * steps[0], 4 * steps[1]};  // of a CTA, in products of a step
+    const bool together = p.s > W;                           // (else the kinds' launches follow one another)
+    Parts r = {{1, 1}, {0, 0}};
+    if (p.rows == 0 || p.s == 0) return r;
+    for (int i = 0; i < 2; ++i) {
+        const long long all = ctas[i] * cost[i] + (together ? ctas[1 - i] * cost[1 - i] : 0), even = std::max(1LL, all / places);
+        r.of[i] = (int)std::max(1LL, std::min((cost[i] + even - 1) / even, steps[i] / kSteps));
+        r.bytes[i] = r.of[i] > 1 ? (size_t)r.of[i] * heads * (i ? 2ll * p.s : p.rows) * p.d * 4 : 0;
+    }
+    return r;
+}
+
+template <int D, int W, bool FINE, bool CUT>
+cudaError_t backward(const CrossProblem &p, const Parts &parts, float *delta, float *sums, cudaStream_t stream) {
     using G = Geo<D, W>;
     BwdParams a;
     a.p = p;
     a.delta = delta;
+    a.sums[0] = sums, a.sums[1] = sums + parts.bytes[0] / 4;
     int ctas[2] = {(p.rows + kRows - 1) / kRows, (p.s + kRows - 1) / kRows};
-    for (int i = 0; i < 2; ++i) a.tiles[i] = ctas[i], a.by_tiles[i] = Divide((uint32_t)std::max(1, ctas[i])), ctas[i] *= p.B * p.kv;
+    for (int i = 0; i < 2; ++i) {
+        a.tiles[i] = ctas[i], a.by_tiles[i] = Divide((uint32_t)std::max(1, ctas[i]));
+        a.parts[i] = parts.of[i], a.by_parts[i] = Divide((uint32_t)parts.of[i]);
+        ctas[i] *= p.B * p.kv * parts.of[i];
+    }
     if (p.s > 0 && (!make_tile_map(&a.k, p.K, p.B, p.kv, p.s, p.d, W) || !make_tile_map(&a.v, p.V, p.B, p.kv, p.s, p.d, W)))
         return cudaErrorInvalidValue;
     if (p.s > 0 && p.n > 0 && (!make_tile_map(&a.q, p.Q, p.B, p.heads, p.n, p.d, W) || !make_tile_map(&a.g, p.dH, p.B, p.heads, p.n, p.d, W)))
         return cudaErrorInvalidValue;
     static SmemOnce allow;
-    cudaError_t e = allow(cross_bwd_kernel<D, W, FINE>, G::kSmem);
+    cudaError_t e = allow(cross_bwd_kernel<D, W, FINE, CUT>, G::kSmem);
     if (e != cudaSuccess) return e;
-    auto run = [&](int grid) { return launch_pdl(cross_bwd_kernel<D, W, FINE>, dim3(grid), dim3(G::kThreads), G::kSmem, stream, a); };
+    auto run = [&](int grid) { return launch_pdl(cross_bwd_kernel<D, W, FINE, CUT>, dim3(grid), dim3(G::kThreads), G::kSmem, stream, a); };
     a.exact = p.s <= W;
     if (a.exact) {  // the keys' CTAs after the queries', who make D
         a.keys_first = false, a.first = ctas[0];
         if (ctas[0] > 0) e = run(ctas[0]);
         a.keys_first = true, a.first = ctas[1];
-        return e != cudaSuccess || ctas[1] == 0 ? e : run(ctas[1]);
+        if (e == cudaSuccess && ctas[1] > 0) e = run(ctas[1]);
+    } else {
+        if (ctas[0] > 0) e = launch_cross_delta(p, delta, stream);
+        // first those that take longer: four products over the queries against three over the keys
+        a.keys_first = 4LL * p.rows * parts.of[0] >= 3LL * p.s * parts.of[1];
+        a.first = ctas[a.keys_first];
+        if (e == cudaSuccess) e = run(ctas[0] + ctas[1]);
     }
-    if (ctas[0] > 0) e = launch_cross_delta(p, delta, stream);
-    // first those that take longer: four products over the queries against three over the keys
-    a.keys_first = 4LL * p.rows >= 3LL * p.s;
-    a.first = ctas[a.keys_first];
-    return e != cudaSuccess ? e : run(ctas[0] + ctas[1]);
+    if (e == cudaSuccess && parts.of[0] > 1) e = add_up<false>(p, a.sums[0], parts.of[0], stream);
+    if (e == cudaSuccess && parts.of[1] > 1) e = add_up<true>(p, a.sums[1], parts.of[1], stream);
+    return e;
 }
 
 }  // namespace
 
-cudaError_t launch_cross_tc_backward(const CrossProblem &p, float *delta, cudaStream_t stream) {
-    if (p.s <= kFine) return p.d > 64 ? backward<128, 128, true>(p, delta, stream) : backward<64, 64, true>(p, delta, stream);
-    return p.d > 64 ? backward<128, 128, false>(p, delta, stream) : backward<64, 64, false>(p, delta, stream);
+size_t cross_tc_backward_sums(const CrossProblem &p) {
+    const Parts parts = plan(p);
+    return parts.bytes[0] + parts.bytes[1];
+}
+
+cudaError_t launch_cross_tc_backward(const CrossProblem &p, float *delta, float *sums, cudaStream_t stream) {
+    const Parts parts = plan(p);
+    auto fine = [&](auto f) {
+        auto cut = [&](auto c) {
+            constexpr bool F = decltype(f)::value, C = decltype(c)::value;
+            return p.d > 64 ? backward<128, 128, F, C>(p, parts, delta, sums, stream) : backward<64, 64, F, C>(p, parts, delta, sums, stream);
+        };
+        return std::max(parts.of[0], parts.of[1]) > 1 ? cut(std::true_type{}) : cut(std::false_type{});
+    };
+    return p.s <= kFine ? fine(std::true_type{}) : fine(std::false_type{});
 }
 
 cudaError_t cross_bwd_read_and_clear_error(unsigned *out) {

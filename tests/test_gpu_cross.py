@@ -330,6 +330,17 @@ def test_gradient_against_differences(aa):
         assert abs(got - want) <= 5e-3 * (1 + abs(want)), (i, got, want)
 
 
+@pytest.mark.parametrize("d", [16, 64, 128])
+@pytest.mark.parametrize("shape,lengths", [((1, 4, 2, 1500, 50), None), ((3, 4, 1, 700, 200), "mixed"), ((2, 2, 2, 4100, 77), None),
+                                           ((1, 2, 2, 40, 3000), None), ((9, 4, 2, 70, 2500), "mixed"), ((1, 1, 1, 2100, 2300), None)])
+def test_backward_in_parts(aa, d, shape, lengths):
+    """Few tiles that walk long: their steps are cut, and the parts' sums added by another launch, the same bits each time."""
+    Q, K, V, dH, L, H, lse = check(aa, 41 + d, *shape, d, "bf16", lengths=lengths)
+    first = aa.cross_backward(Q, K, V, H, lse, dH, L)
+    for a, b in zip(first, aa.cross_backward(Q, K, V, H, lse, dH, L)):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("s,d", [(8, 64), (64, 64), (64, 128), (384, 64), (300, 128)])
 def test_few_states_lose_little(aa, s, d):
     """Up to 384 states dQ and dK are off by little more than their own rounding.  With scores near 0 all s states weigh
