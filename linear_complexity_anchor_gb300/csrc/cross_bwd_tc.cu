@@ -5,9 +5,9 @@
 // Two kinds of CTAs, one that keeps queries and one that keeps keys, so that every gradient is summed in
 // tensor memory by one CTA in a fixed order, without atomics.  S and dP are made twice for
 // that: seven products where five would do.  Both are of one launch, those that take longer first, so that
-// the others fill the SMs that they leave (D comes from a launch before, but see kFine; with the queries first and
-// D made by them, in a launch of their own, 2 x 16 heads over 4, 2049 x 1500, d = 128: 188 us against 152).  CTAs that walk long are cut into
-// parts (see Parts).
+// the others fill the SMs that they leave (D comes from a launch before, but see kFine; with the queries
+// first and D made by them, in a launch of their own, 2 x 16 heads over 4, 2049 x 1500, d = 128: 188 us
+// against 152).  CTAs that walk long are cut into parts (see Parts).
 //
 //   queries   a tile of 128 rows of Q and dH stays, the keys of the entry stream by:
 //             S = Q K^T, dP = dH V^T, dQ += dS K
