@@ -274,9 +274,10 @@ def test_same_bits_again(aa, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_streams_and_graphs(aa, dtype):
+@pytest.mark.parametrize("first", [(2, 4, 2, 260, 600, 64), (2, 4, 2, 1100, 50, 64)])
+def test_streams_and_graphs(aa, dtype, first):
     """Two calls at once on streams of their own, and two captured graphs replayed at once, give the eager bits."""
-    one = make(14, 2, 4, 2, 260, 600, 64, dtype)
+    one = make(14, *first, dtype)
     two = make(15, 4, 8, 2, 1, 2500, 64, dtype)
 
     def step(x, stream=None):
