@@ -54,9 +54,9 @@ def cross_forward(Q, K, V, lengths=None, *, H=None, scale: float | None = None, 
     axes, and with return_lse the logarithm of each row's sum, fp32 [B, heads, n], which ``cross_backward`` takes.
     Asynchronous on ``stream`` or the current stream."""
     device, numbers, views, at_lengths = _problem(Q, K, V, lengths, scale)
-    at, lse = Launch(device, stream), None
+    at, lse, given = Launch(device, stream), None, H
     with at as handle:
-        if H is None:
+        if given is None:
             H, to = empty_like(Q)
         else:
             to = view(H, "H", Q.dtype, device)
@@ -67,7 +67,7 @@ def cross_forward(Q, K, V, lengths=None, *, H=None, scale: float | None = None, 
         _call("anchor_attn_cross_forward", _pack(*numbers, *views, *to, *NO_VIEW, *NO_VIEW, *NO_VIEW, *NO_VIEW,
                                                  lse.data_ptr() if return_lse else 0, at_lengths), handle)
     if at.stream is not None:
-        at.used((Q, K, V, lengths), (H, lse))
+        at.used((Q, K, V, lengths, given), (H if given is None else None, lse))
     return (H, lse) if return_lse else H
 
 

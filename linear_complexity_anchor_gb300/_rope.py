@@ -165,7 +165,7 @@ def _forward(X, table, positions, starts, weights, norm, eps, interleaved, out, 
             rows[i] = _rows(size, views[i], to, NO_VIEW, NO_VIEW, shape, positions[i], starts[i], weights[i], None, name)
         _call("anchor_attn_norm_rope", how, rows[0], rows[1], handle)
     if at.stream is not None:
-        at.used((*X, *positions, *weights, table[0] if table is not None else None), Y)
+        at.used((*X, *positions, *weights, table[0] if table is not None else None, *out), [y for y, o in zip(Y, out) if o is None])
     return Y
 
 

@@ -101,11 +101,12 @@ class Launch:
         for g in reversed(self.guards):
             g.__exit__(*exc)
 
-    def used(self, inputs, outputs=()) -> None:
-        """For a call whose `stream` is not None."""
-        for t in inputs:
+    def used(self, given, made=()) -> None:
+        """For a call whose `stream` is not None: the caller's tensors, outputs among them, are used on it; those made
+        inside are the stream's own, and the caller uses them on its current one."""
+        for t in given:
             if t is not None:
                 t.record_stream(self.stream)
-        for t in outputs:
+        for t in made:
             if t is not None:
                 t.record_stream(self.current)
