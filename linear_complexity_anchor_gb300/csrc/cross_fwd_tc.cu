@@ -43,6 +43,26 @@ using namespace cross_tc;
 
 constexpr float kSlack = 8.f;  // log2 of how far a maximum may be passed before O is rescaled
 
+// What scores are scaled by, in log2 (the sign is Q's).  Not 0, so that a masked score stays -infinity: with a
+// scale of 0 the scores are 0, by Q.
+__device__ __forceinline__ float score_scale(const CrossProblem &p) { return p.scale == 0.f ? 1.f : fabsf(p.scale) * kLog2e; }
+
+// A lane's part of Q with the scale's sign; with a scale of 0, times 0 (infinities and NaN are NaN then).
+template <int n> __device__ __forceinline__ void scale_sign(uint4 (&x)[n], float scale) {
+    uint32_t *u = &x[0].x;
+    const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int i = 0; i < 4 * n; ++i) u[i] ^= flip;
+    if (scale == 0.f) {
+        const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+#pragma unroll
+        for (int i = 0; i < 4 * n; ++i) {
+            const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(u + i), zero);
+            u[i] = *reinterpret_cast<const uint32_t *>(&y);
+        }
+    }
+}
+
 // D columns (heads of 16 and 32 are 64), NQ row tiles, key tiles of KT.
 template <int D, int NQ, int KT>
 struct Geo {
@@ -221,24 +241,20 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
         const bool mine = r < p.rows;
         const bool active = r0 + q * kRows + w4 * 32 < p.rows;  // the warp has a row
         uint8_t *sQ = sm + G::kQ + q * kTile<D>;
-        // (not 0, so that a masked score stays -infinity; a scale of 0 leaves no trace of any finite one)
-        const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);
+        const float c = score_scale(p);
         // this warp's 32 rows by its part of the columns, 16 bytes a lane
         constexpr int kLanes = D / (8 * NH), kPart = D / NH;
         const int my_row = lane / kLanes, my_chunk = half * kLanes + lane % kLanes;
         if (nt > 0) {
-            // Q, negated for a negative scale
-            const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+            // Q, with the scale's sign
             uint4 x[kLanes];
             each_row<kLanes>(mine ? cross_row(p, p.Q, b, kh, r) : -1, p.Q.sn, [&](int i, int, long long o) {
                 x[i] = make_uint4(0, 0, 0, 0);
                 if (o >= 0 && my_chunk * 8 < p.d) x[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.Q.ptr + o + my_chunk * 8);
             });
+            scale_sign(x, p.scale);
 #pragma unroll
-            for (int i = 0; i < kLanes; ++i) {
-                x[i].x ^= flip, x[i].y ^= flip, x[i].z ^= flip, x[i].w ^= flip;
-                *reinterpret_cast<uint4 *>(sQ + chunk_at(w4 * 32 + i * (32 / kLanes) + my_row, my_chunk)) = x[i];
-            }
+            for (int i = 0; i < kLanes; ++i) *reinterpret_cast<uint4 *>(sQ + chunk_at(w4 * 32 + i * (32 / kLanes) + my_row, my_chunk)) = x[i];
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full + q);
@@ -526,18 +542,15 @@ __global__ void __launch_bounds__(kRows, Short<D>::kPerSM) cross_short_kernel(co
     uint8_t *sQ = sm + G::kQ;
     constexpr int kLanes = D / 8;
     {
-        const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
         const int ch = lane % kLanes;
         uint4 x[kLanes];
         each_row<kLanes>(mine ? cross_row(p, p.Q, b, kh, r) : -1, p.Q.sn, [&](int i, int, long long o) {
             x[i] = make_uint4(0, 0, 0, 0);
             if (o >= 0 && ch * 8 < p.d) x[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.Q.ptr + o + ch * 8);
         });
+        scale_sign(x, p.scale);
 #pragma unroll
-        for (int i = 0; i < kLanes; ++i) {
-            x[i].x ^= flip, x[i].y ^= flip, x[i].z ^= flip, x[i].w ^= flip;
-            *reinterpret_cast<uint4 *>(sQ + chunk_at(warp * 32 + i * (32 / kLanes) + lane / kLanes, ch)) = x[i];
-        }
+        for (int i = 0; i < kLanes; ++i) *reinterpret_cast<uint4 *>(sQ + chunk_at(warp * 32 + i * (32 / kLanes) + lane / kLanes, ch)) = x[i];
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -557,7 +570,7 @@ __global__ void __launch_bounds__(kRows, Short<D>::kPerSM) cross_short_kernel(co
         umma_commit(s_full);
     }
     __syncwarp();
-    const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);  // (see above)
+    const float c = score_scale(p);
     float m = -INFINITY, l = 0.f;
     if (L > 0) {
         ok = bwait(s_full, 0u, error) && ok;
