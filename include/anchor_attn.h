@@ -404,6 +404,8 @@ ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_norm_rope_backward(const anchor
  * The forward writes H, and lse where it is not NULL.  The backward takes them and dH, and
  * writes dQ, dK, dV (rows of dK and dV from L on are zero; entries that share K or V by a stride
  * of 0 get gradients of their own).
+ * Scores and lse are fp32 numbers, rounded as such.  The backward has P from lse: rows whose |lse| passes some
+ * thousands lose accuracy by its rounding, past 7e5 P is kept at most 1 (it may be 0), so that gradients stay finite.
  * Sizes: B, heads, n, s >= 0; B * heads * (n + s) < 2^31; B * kv_heads <= 2^29.  Results are
  * bit-identical from run to run.
  * Workspaces come from a pool of the library on `stream` and go back on it.  A bounded wait

@@ -50,6 +50,13 @@ __device__ __forceinline__ long long cross_flat(const CrossProblem &p, int b, in
     return ((long long)b * p.kv + k) * p.rows + r;  // the group's heads follow one another
 }
 
+// From here on scores (and lse, in log2) are rounded too coarsely for c s - m in one rounding.
+constexpr float kFar = 0x1p20f;
+// lse in log2 as the backward takes it, P = 2^(c s - lse).  It has been rounded six times (m, two factors, a product and a
+// sum in the forward, its product with log2 e here; half a step each), which would take P past any range where lse is far.
+// There it is raised by three and a half steps, so that P is at most 1.
+__device__ __forceinline__ float far_lse(float x) { return fabsf(x) > kFar ? fmaf(fabsf(x), 0x1.cp-22f, x) : x; }
+
 // The parts of a forward whose keys are cut over several CTAs: unnormalised sums and (maximum in
 // units of log2, sum) per part, [parts][B * kv * rows][d] and [parts][B * kv * rows].
 struct CrossParts {

@@ -249,7 +249,7 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
 #pragma unroll
                 for (int x = 0; x < kX; ++x) {
                     const bool in = i0 + 32 * x + lane < p.n;
-                    next[x] = in ? -p.lse[f + 32 * x + lane] * kLog2e : -INFINITY;
+                    next[x] = in ? -far_lse(p.lse[f + 32 * x + lane] * kLog2e) : -INFINITY;
                     next[kX + x] = in ? -a.delta[f + 32 * x + lane] : 0.f;
                 }
                 w.next();
@@ -365,7 +365,7 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
             if (lane == 0) mbar_arrive(fix_full);
             if (mine) {
                 const long long f = cross_flat(p, b, kh, r);
-                const float x2 = -p.lse[f] * kLog2e;
+                const float x2 = -far_lse(p.lse[f] * kLog2e);
                 lse2 = f32x2(x2, x2);
                 if (!FINE || !a.exact) {
                     const float d2 = -a.delta[f];

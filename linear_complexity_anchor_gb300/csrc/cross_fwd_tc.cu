@@ -264,7 +264,11 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
         // the two halves of a row meet over its slots [half], and over a barrier of their two warps
         float *ex = reinterpret_cast<float *>(sm + G::kEx + q * 2 * kRows * 4) + row;
         uint64_t *meet = pair + q * 4 + w4;
-        float m = -INFINITY, l = 0.f;  // maximum in use (of c s), and this half's sum
+        // The maximum in use (of s), what it takes to move it, and this half's sum.  A score's exponent is c s - m in one
+        // rounding, m = c u rounded before: P and its sum share 2^(what that left), up to 2^(2^-24 |m|), which H
+        // does not see until it overflows.  A row whose m is far moves at every tile, where u is taken from s
+        // instead, and shift, otherwise m, is 0.
+        float u_max = -INFINITY, shift = 0.f, limit = -INFINITY, l = 0.f;
         bool ok = true;
         if (active && q < nq) {
             for (int j = 0; j < nt && ok; ++j) {
@@ -291,7 +295,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                     for (int x = 0; x < 8; ++x) t8[x] = max3_f32(t8[x], s[y + x], s[y + 8 + x]);
 #pragma unroll
                 for (int x = 0; x < 8; ++x) t8[x] = fmaxf(t8[x], s[56 + x]);
-                float top = c * fmaxf(max3_f32(t8[0], t8[1], t8[2]), max3_f32(t8[3], t8[4], max3_f32(t8[5], t8[6], t8[7])));
+                float top = fmaxf(max3_f32(t8[0], t8[1], t8[2]), max3_f32(t8[3], t8[4], max3_f32(t8[5], t8[6], t8[7])));
                 // Two S buffers: O up to the tile before, waited for at every step: S runs ahead of it, and a
                 // warp two phases behind a barrier would take the older phase for the one it wants.
                 // (One: this S was issued after the product that O waits for.)
@@ -304,15 +308,19 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                     if (!bwait(meet, (uint32_t)(j & 1), error)) { ok = false; break; }
                     top = fmaxf(ex[0], ex[kRows]);
                 }
-                if (j == 0) {
-                    m = top;
-                } else {
-                    const bool grows = top > m + kSlack;
-                    if (__any_sync(0xffffffffu, grows)) {
+                const bool moves = c * top > limit;
+                if (__any_sync(0xffffffffu, moves)) {
+                    float f = 1.f;
+                    if (moves && !(limit == -INFINITY && top <= u_max)) {
+                        const float m = __fmul_rn(c, top);
+                        const bool far = fabsf(m) > kFar;
+                        f = ex2(far ? c * (u_max - top) : __fmul_rn(c, u_max) - m);
+                        u_max = top;
+                        shift = far ? 0.f : m, limit = far ? -INFINITY : __fadd_rn(m, kSlack);
+                    }
+                    if (j > 0) {
                         // this half of O's columns (complete up to the tile before) to the new maximum
                         tc_fence_after();
-                        const float f = grows ? ex2(m - top) : 1.f;
-                        if (grows) m = top;
                         l *= f;
 #pragma unroll 1
                         for (int x = half * kPart; x < (half + 1) * kPart; x += 8) {
@@ -325,8 +333,11 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
                         }
                         tmem_st_wait();
                     }
+                    if (moves && limit == -INFINITY) {
+#pragma unroll
+                        for (int x = 0; x < 64; ++x) s[x] -= u_max;
+                    }
                 }
-                const float shift = m == -INFINITY ? 0.f : m;
                 const uint64_t c2 = f32x2(c, c), m2 = f32x2(-shift, -shift);
                 uint64_t z[2] = {0, 0};
 #pragma unroll
@@ -371,6 +382,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
             }
             tc_fence_after();
         }
+        const float m = __fmul_rn(c, u_max);
         if (active && q < nq && ok) {
             const long long f = cross_flat(p, b, kh, mine ? r : 0);
             const int to = min(p.d, (half + 1) * kPart);
@@ -593,18 +605,24 @@ __global__ void __launch_bounds__(kRows, Short<D>::kPerSM) cross_short_kernel(co
                     for (int z = 0; z < 4; ++z) t4[z] = max3_f32(t4[z], s[y + z], s[y + 4 + z]);
                 m = fmaxf(max3_f32(t4[0], t4[1], t4[2]), t4[3]);
             }
+            // (a row whose maximum is far: as above)
+            const float u_max = m;
             m *= c;
-            const float shift = m == -INFINITY ? 0.f : m;
+            const bool far = fabsf(m) > kFar && m != -INFINITY;
+            const float shift = far || m == -INFINITY ? 0.f : m;
+            const int whole = __any_sync(0xffffffffu, far) ? 0 : L - 31;  // from here on scores need a look
             const uint64_t c2 = f32x2(c, c), m2 = f32x2(-shift, -shift);
             uint64_t z2[2] = {0, 0};
 #pragma unroll 1
             for (int x = 0; x < L; x += 32) {
                 tmem_ld32(mine_at + x, s);
                 tmem_ld_wait();
-                if (L - x < 32) {
+                if (x >= whole) {
 #pragma unroll
-                    for (int y = 0; y < 32; ++y)
+                    for (int y = 0; y < 32; ++y) {
                         if (x + y >= L) s[y] = -INFINITY;
+                        if (far) s[y] -= u_max;
+                    }
                 }
                 uint32_t u[16];
 #pragma unroll

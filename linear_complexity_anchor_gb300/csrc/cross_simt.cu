@@ -357,7 +357,7 @@ __device__ __forceinline__ void cross_simt_backward(const CrossProblem &p, const
         stat[i] = 0.f;
         if (!KEYS && r < p.rows) {
             const long long f = cross_flat(p, b, k, r);
-            stat[i] = h == 0 ? p.lse[f] * kLog2e : delta[f];
+            stat[i] = h == 0 ? far_lse(p.lse[f] * kLog2e) : delta[f];
         }
     }
     const int cols = KEYS ? (r0 < L ? p.rows : 0) : L;  // a tile of masked keys has no gradient
@@ -366,7 +366,7 @@ __device__ __forceinline__ void cross_simt_backward(const CrossProblem &p, const
         if (KEYS && threadIdx.x < kBN) {
             const bool in = c0 + (int)threadIdx.x < p.rows;
             const long long f = in ? cross_flat(p, b, k, c0 + threadIdx.x) : 0;
-            sLD[at * 2 * kBN + threadIdx.x] = in ? p.lse[f] * kLog2e : 0.f;
+            sLD[at * 2 * kBN + threadIdx.x] = in ? far_lse(p.lse[f] * kLog2e) : 0.f;
             sLD[at * 2 * kBN + kBN + threadIdx.x] = in ? delta[f] : 0.f;
         }
         load_rows<D, kThreads>(sB + at * kTile, kBN, [&](int r) { return KEYS ? q_row(c0 + r) : k_row(c0 + r); });

@@ -1,11 +1,11 @@
-"""GPU: cross attention with scales of 0 and close to it."""
+"""GPU: cross attention where scores are far outside of what fp32 tells apart, and scales of 0 and close to it."""
 import math
 
 import pytest
 import torch
 
 from tests.conftest import gpu_available
-from tests.ops_reference import assert_within, cross_reference
+from tests.ops_reference import assert_within, cross_reference, half_step
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a CUDA GPU")]
 
@@ -28,6 +28,36 @@ def make(seed, B, heads, kv, n, s, d, dtype, gain):
     g = torch.Generator(device="cuda").manual_seed(seed)
     return [(by * torch.randn((B, h, rows, d), generator=g, device="cuda")).to(DT[dtype])
             for h, rows, by in ((heads, n, 1.5 * gain), (kv, s, gain), (kv, s, 1.0), (heads, n, 1.0))]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gain", [1e3, 1e4, 3e5])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_far_scores(aa, dtype, gain, shape):
+    """Scores of 10^6 to 10^11: a row's best state has the whole weight, and the gradients are within what P <= 1 allows."""
+    B, heads, kv, n, s, d = shape
+    Q, K, V, dH = make(31, *shape, dtype, gain)
+    H, lse = aa.cross_forward(Q, K, V, return_lse=True)
+    assert bool(H.isfinite().all()) and bool(lse.isfinite().all())
+    k, v, g = K.double().repeat_interleave(heads // kv, 1), V.double().repeat_interleave(heads // kv, 1), dH.double()
+    x = (Q.double() @ k.mT) * d ** -0.5
+    # scores are off by d roundings of fp32 of their products at the most: rows whose best state is ahead by more than that
+    two = x.topk(2, -1)
+    off = (d + 20) * 2.0 ** -23 * (Q.double().abs() @ k.abs().mT).amax(-1) * d ** -0.5
+    sure = two.values[..., 0] - two.values[..., 1] > 40 + 2 * off
+    assert float(sure.double().mean()) > 0.5
+    best = v.gather(2, two.indices[..., :1].expand(*H.shape))
+    # H = p v / p for one weight p, rounded once (bf16: half a step) before it meets v; the product, the quotient and H
+    # are rounded once each
+    assert bool(((H.double() - best).abs()[sure] <= (2 + 2.0 ** -6) * half_step(DT[dtype]) * best.abs()[sure] * (1 if dtype == "bf16" else 2)).all())
+    assert bool(((lse.double() - two.values[..., 0]).abs()[sure] <= off[sure] + 2.0 ** -20 * two.values[..., 0].abs()[sure]).all())
+    dQ, dK, dV = aa.cross_backward(Q, K, V, H, lse, dH)
+    # P <= 1 and |dS| <= |dH . v| + |dH . H|, whatever lse's rounding makes of P; a hundredth for the roundings
+    back = lambda t: t.unflatten(1, (kv, heads // kv)).sum(2)  # noqa: E731
+    dS = (g @ v.mT).abs() + (g * H.double()).sum(-1, keepdim=True).abs()
+    for got, most in ((dQ, d ** -0.5 * dS @ k.abs()), (dK, d ** -0.5 * back(dS.mT @ Q.double().abs())),
+                      (dV, back(g.abs().sum(2, keepdim=True)).expand(V.shape))):
+        assert bool((got.double().abs() <= 1.01 * most).all())
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
