@@ -406,7 +406,7 @@ ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_norm_rope_backward(const anchor
  * of 0 get gradients of their own).
  * Scores and lse are fp32 numbers, rounded as such.  The backward has P from lse: rows whose |lse| passes some
  * thousands lose accuracy by its rounding, past 7e5 P is kept at most 1 (it may be 0), so that gradients stay finite.
- * Sizes: B, heads, n, s >= 0; B * heads * (n + s) < 2^31; B * kv_heads <= 2^29.  Results are
+ * Sizes: B, heads, n, s >= 0; B * heads * (n + s) <= 2^31 - 1024; B * kv_heads <= 2^29.  Results are
  * bit-identical from run to run.
  * Workspaces come from a pool of the library on `stream` and go back on it.  A bounded wait
  * that gives up is reported by anchor_attn_device_error (bit 0).

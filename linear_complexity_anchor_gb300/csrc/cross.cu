@@ -110,7 +110,8 @@ anchor_attn_status_t cross(const anchor_attn_cross_t *a, bool bwd, void *stream_
         return a->heads == 0 && a->kv_heads > 0 && a->B > 0 && a->s > 0 ? ANCHOR_ATTN_ERR_INVALID_ARG : ANCHOR_ATTN_OK;
     }
     if (a->kv_heads == 0 || a->heads % a->kv_heads) return ANCHOR_ATTN_ERR_INVALID_ARG;
-    if ((long long)a->n + a->s > 0x7fffffffLL / ((long long)a->B * a->heads)) return ANCHOR_ATTN_ERR_UNSUPPORTED;
+    // (room for the tiles that counts and walks add to a size, in 32 bits)
+    if ((long long)a->n + a->s > (0x80000000LL - 1024) / ((long long)a->B * a->heads)) return ANCHOR_ATTN_ERR_UNSUPPORTED;
     // (a backward has a tile and more of each kind for each of them, in one grid)
     if ((long long)a->B * a->kv_heads > 1LL << 29) return ANCHOR_ATTN_ERR_UNSUPPORTED;
     if (((uintptr_t)a->lse & 3u) || ((uintptr_t)a->lengths & 3u)) return ANCHOR_ATTN_ERR_INVALID_ARG;
