@@ -52,9 +52,13 @@ constexpr int kSlice = 32;  // columns of S and dP that a row warp takes
 // 1.19, 1.07.  It takes 6 % of time at 77 states, 10 at 300, 18 at 600, 25 at 1000 and more.
 // One tile of states: the queries' CTAs make D from P and dP instead (1.00 at 8 and 50), and the keys' CTAs follow in
 // a launch of their own (256 x 12 heads, 49 x 49: 130 us against 133 with D from H).
-// More than kFine, d <= 64: in every kSome-th step of the queries', whose dQ is 1.49 to 1.53 roundings off
-// without and 1.40 to 1.44 with, for 2.5 % of a training step's time (dK: 1.40 to 1.46).
-constexpr int kFine = 384, kSome = 4;
+// More than kFine, d <= 64: for dQ in some of the key tiles, so that no gradient is much further off than a rounding of its
+// own and one of dS, which is where dK (1.41 to 1.45) and d = 128 (1.45 to 1.48) are anyway.  dQ at d = 64 and 32, 390 to
+// 8000 states: 1.47 to 1.52 with none, 1.37 to 1.42 with every fourth tile, 1.04 to 1.09 with all; at d = 16 1.66 with
+// none, 1.58 with every fourth, 1.17 with all: there every second, 1.46.  The backward of 8 x 12 heads, 4200 x 1000, d = 64:
+// 454 us with none, 470 with every fourth, 498 with all.  Which tiles is a matter of their place among the entry's states alone.
+constexpr int kFine = 384;
+__device__ __forceinline__ int fine_tiles(int d) { return d > 16 ? 4 : 2; }
 
 // D columns (heads of 16 and 32 are 64), streaming tiles of W rows.
 template <int D, int W>
@@ -164,7 +168,8 @@ __device__ __forceinline__ void cross_bwd(const BwdParams &a, int index) {
     };
     const int around = KEYS ? per_head : steps, g0 = CUT && KEYS && part > 0 ? j0 / per_head : 0;
     const Walk start{j0 - g0 * per_head, g0, around, KEYS ? p.group : 1};
-    auto two = [](int j) { return FINE || (D == 64 && !KEYS && j % kSome == 0); };  // dS of step j is two numbers
+    const int some = fine_tiles(p.d) - 1;
+    auto two = [=](int j) { return FINE || (D == 64 && !KEYS && ((j0 + j) & some) == 0); };  // dS of step j is two numbers
     // columns of a tile that exist
     auto width = [&](int t) { return min(W, (KEYS ? p.n : L) - t * W); };
 
