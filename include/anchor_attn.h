@@ -408,8 +408,8 @@ ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_norm_rope_backward(const anchor
  * thousands lose accuracy by its rounding, past 7e5 P is kept at most 1 (it may be 0), so that gradients stay finite.
  * Sizes: B, heads, n, s >= 0; B * heads * (n + s) <= 2^31 - 1024; B * kv_heads <= 2^29.  Results are
  * bit-identical from run to run.
- * Workspaces come from a pool of the library on `stream` and go back on it.  A bounded wait
- * that gives up is reported by anchor_attn_device_error (bit 0).
+ * Workspaces come from a pool of the library on `stream` and go back on it (see
+ * anchor_attn_release_workspaces).  A bounded wait that gives up is reported by anchor_attn_device_error (bit 0).
  */
 typedef struct {
     int dtype;                  /* 0 = bf16, 1 = fp32                                         */
@@ -422,6 +422,14 @@ typedef struct {
 
 ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_cross_forward(const anchor_attn_cross_t *p, void *stream);
 ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_cross_backward(const anchor_attn_cross_t *p, void *stream);
+
+/*
+ * Workspaces of cross attention and of the norms' weight gradients come from a pool of the library, one per device, which
+ * keeps up to 512 MB of them between calls (a call after a synchronisation would otherwise map its workspace again,
+ * 0.2 ms).  This gives what the current device's pool keeps back to the device; workspaces of calls that have not been
+ * waited for stay.  Later calls take memory anew.
+ */
+ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_release_workspaces(void);
 
 /* Human-readable name of a status code (static storage). */
 ANCHOR_ATTN_API const char *anchor_attn_status_string(anchor_attn_status_t status);

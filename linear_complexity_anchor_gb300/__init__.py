@@ -24,7 +24,7 @@ __all__ = [
     "full_forward", "relative_error", "causal_forward", "block_forward", "anchor_attn_block_forward_ptr",
     "forward_host", "anchor_attn_forward_host_ptr", "anchor_attn_forward_host_f32_ptr",
     "cross_forward", "cross_backward", "rope", "rope_backward", "norm_rope", "norm_rope_backward", "rope_table",
-    "rope_frequencies", "RopeTable",
+    "rope_frequencies", "RopeTable", "release_workspaces",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libanchor_attn.so")
@@ -91,6 +91,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.anchor_attn_static_scratch_bytes.restype = ctypes.c_size_t
         lib.anchor_attn_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint)]
         lib.anchor_attn_device_error.restype = ctypes.c_int
+        lib.anchor_attn_release_workspaces.argtypes = []
+        lib.anchor_attn_release_workspaces.restype = ctypes.c_int
         lib.anchor_attn_status_string.argtypes = [ctypes.c_int]
         lib.anchor_attn_status_string.restype = ctypes.c_char_p
         _cross.bind(lib)
@@ -169,6 +171,12 @@ def device_error() -> int:
     code = ctypes.c_uint(0)
     _raise(load().anchor_attn_device_error(ctypes.byref(code)), "device_error")
     return int(code.value)
+
+
+def release_workspaces() -> None:
+    """Give the workspaces that cross attention and the norms' backward keep between calls (up to 512 MB a device, outside
+    of torch's allocator) back to the current device; those of calls that have not been waited for stay."""
+    _raise(load().anchor_attn_release_workspaces(), "release_workspaces")
 
 
 def query_plan(dtype: str, B: int, heads: int, n: int, m: int, d: int) -> dict:

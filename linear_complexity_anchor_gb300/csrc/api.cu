@@ -440,6 +440,14 @@ anchor_attn_status_t anchor_attn_query_plan(int dtype, int B, int heads, int n, 
     return ANCHOR_ATTN_OK;
 }
 
+anchor_attn_status_t anchor_attn_release_workspaces(void) {
+    if (anchor::workspace_release() != cudaSuccess) {
+        cudaGetLastError();
+        return ANCHOR_ATTN_ERR_CUDA;
+    }
+    return ANCHOR_ATTN_OK;
+}
+
 anchor_attn_status_t anchor_attn_device_error(unsigned *code) {
     if (!code) return ANCHOR_ATTN_ERR_INVALID_ARG;
     unsigned a = 0, b = 0, c = 0, e = 0, f = 0, g = 0, k = 0, l = 0, q = 0, r = 0, w = 0, x = 0, y = 0;

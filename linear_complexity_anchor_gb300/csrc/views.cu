@@ -1,6 +1,7 @@
 // Checks of strided views and the workspace pool (see views.cuh).
 #include "views.cuh"
 
+#include <algorithm>
 #include <mutex>
 
 namespace anchor {
@@ -98,6 +99,15 @@ cudaError_t workspace_alloc(void **ptr, size_t bytes, cudaStream_t stream) {
         pool = g_pools[dev];
     }
     return pool ? cudaMallocFromPoolAsync(ptr, bytes, pool, stream) : cudaMallocAsync(ptr, bytes, stream);
+}
+
+cudaError_t workspace_release() {
+    std::lock_guard<std::mutex> hold(g_pool_lock);
+    if (std::all_of(g_pools, g_pools + kMaxDevices, [](cudaMemPool_t p) { return p == nullptr; })) return cudaSuccess;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    return dev < kMaxDevices && g_pools[dev] ? cudaMemPoolTrimTo(g_pools[dev], 0) : cudaSuccess;
 }
 
 }  // namespace anchor

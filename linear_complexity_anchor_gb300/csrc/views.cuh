@@ -36,6 +36,8 @@ inline bool bytes_overlap(const void *a, size_t an, const void *b, size_t bn) {
 // for: 66 us against 249; a backward of 8 x 12 heads, 1000 x 1000: 167 against 369).
 constexpr unsigned long long kPoolKeep = 512ull << 20;
 cudaError_t workspace_alloc(void **ptr, size_t bytes, cudaStream_t stream);
+// what the current device's pool keeps goes back to the device
+cudaError_t workspace_release();
 
 // Allows a kernel `bytes` of dynamic shared memory, once per device (one object for each kernel).
 struct SmemOnce {

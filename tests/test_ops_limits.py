@@ -30,3 +30,8 @@ def test_largest_sizes(pkg, monkeypatch, dtype, B, heads, kv, many):  # noqa: F8
         if total < 2 ** 31 + B * heads:
             assert call(total) == UNSUPPORTED
             assert call(total, backward=False) == UNSUPPORTED
+
+
+def test_nothing_to_release(pkg):  # noqa: F811
+    """Without a workspace there is no pool, and no device is touched."""
+    assert pkg.load().anchor_attn_release_workspaces() == 0 and pkg.release_workspaces() is None
