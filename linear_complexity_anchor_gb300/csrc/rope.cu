@@ -139,7 +139,8 @@ struct Turn {
             unsigned long long t = at[0] * __ldg(ph);
             if (p.axes > 1) t += at[1] * __ldg(ph + p.rot / 2);
             if (p.axes > 2) t += at[2] * __ldg(ph + p.rot);
-            // the upper 32 bits as half turns in [-1, 1): off by 2^-32 of a turn at most
+            // the upper 32 bits as half turns in [-1, 1]: 2^-32 of a turn is cut off at most, and rounding to fp32 moves
+            // it by up to 2^-26 (near half a turn; 1e-7 rad)
             const float half_turns = (float)(int)(t >> 32) * 0x1p-31f;
             sincospif(half_turns, &s[i], &c[i]);
             s[i] *= p.magnitude, c[i] *= p.magnitude;
