@@ -47,20 +47,11 @@ constexpr float kSlack = 8.f;  // log2 of how far a maximum may be passed before
 // scale of 0 the scores are 0, by Q.
 __device__ __forceinline__ float score_scale(const CrossProblem &p) { return p.scale == 0.f ? 1.f : fabsf(p.scale) * kLog2e; }
 
-// A lane's part of Q with the scale's sign; with a scale of 0, times 0 (infinities and NaN are NaN then).
-template <int n> __device__ __forceinline__ void scale_sign(uint4 (&x)[n], float scale) {
-    uint32_t *u = &x[0].x;
-    const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
+// With a scale of 0: eight elements of Q times 0 (infinities and NaN are NaN then).
+__device__ __forceinline__ void times_zero(uint4 *q) {
+    __nv_bfloat162 *x = reinterpret_cast<__nv_bfloat162 *>(q);
 #pragma unroll
-    for (int i = 0; i < 4 * n; ++i) u[i] ^= flip;
-    if (scale == 0.f) {
-        const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-#pragma unroll
-        for (int i = 0; i < 4 * n; ++i) {
-            const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(u + i), zero);
-            u[i] = *reinterpret_cast<const uint32_t *>(&y);
-        }
-    }
+    for (int i = 0; i < 4; ++i) x[i] = __hmul2(x[i], __float2bfloat162_rn(0.f));
 }
 
 // D columns (heads of 16 and 32 are 64), NQ row tiles, key tiles of KT.
@@ -246,15 +237,20 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
         constexpr int kLanes = D / (8 * NH), kPart = D / NH;
         const int my_row = lane / kLanes, my_chunk = half * kLanes + lane % kLanes;
         if (nt > 0) {
-            // Q, with the scale's sign
+            // Q, negated for a negative scale
+            const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
             uint4 x[kLanes];
             each_row<kLanes>(mine ? cross_row(p, p.Q, b, kh, r) : -1, p.Q.sn, [&](int i, int, long long o) {
                 x[i] = make_uint4(0, 0, 0, 0);
                 if (o >= 0 && my_chunk * 8 < p.d) x[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.Q.ptr + o + my_chunk * 8);
             });
-            scale_sign(x, p.scale);
 #pragma unroll
-            for (int i = 0; i < kLanes; ++i) *reinterpret_cast<uint4 *>(sQ + chunk_at(w4 * 32 + i * (32 / kLanes) + my_row, my_chunk)) = x[i];
+            for (int i = 0; i < kLanes; ++i) {
+                x[i].x ^= flip, x[i].y ^= flip, x[i].z ^= flip, x[i].w ^= flip;
+                *reinterpret_cast<uint4 *>(sQ + chunk_at(w4 * 32 + i * (32 / kLanes) + my_row, my_chunk)) = x[i];
+            }
+            if (p.scale == 0.f)
+                for (int i = 0; i < kLanes; ++i) times_zero(reinterpret_cast<uint4 *>(sQ + chunk_at(w4 * 32 + i * (32 / kLanes) + my_row, my_chunk)));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full + q);
@@ -337,6 +333,7 @@ cross_fwd_kernel(const __grid_constant__ FwdParams a) {
 #pragma unroll
                         for (int x = 0; x < 64; ++x) s[x] -= u_max;
                     }
+                    __syncwarp();
                 }
                 const uint64_t c2 = f32x2(c, c), m2 = f32x2(-shift, -shift);
                 uint64_t z[2] = {0, 0};
@@ -554,15 +551,20 @@ __global__ void __launch_bounds__(kRows, Short<D>::kPerSM) cross_short_kernel(co
     uint8_t *sQ = sm + G::kQ;
     constexpr int kLanes = D / 8;
     {
+        const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
         const int ch = lane % kLanes;
         uint4 x[kLanes];
         each_row<kLanes>(mine ? cross_row(p, p.Q, b, kh, r) : -1, p.Q.sn, [&](int i, int, long long o) {
             x[i] = make_uint4(0, 0, 0, 0);
             if (o >= 0 && ch * 8 < p.d) x[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.Q.ptr + o + ch * 8);
         });
-        scale_sign(x, p.scale);
 #pragma unroll
-        for (int i = 0; i < kLanes; ++i) *reinterpret_cast<uint4 *>(sQ + chunk_at(warp * 32 + i * (32 / kLanes) + lane / kLanes, ch)) = x[i];
+        for (int i = 0; i < kLanes; ++i) {
+            x[i].x ^= flip, x[i].y ^= flip, x[i].z ^= flip, x[i].w ^= flip;
+            *reinterpret_cast<uint4 *>(sQ + chunk_at(warp * 32 + i * (32 / kLanes) + lane / kLanes, ch)) = x[i];
+        }
+        if (p.scale == 0.f)
+            for (int i = 0; i < kLanes; ++i) times_zero(reinterpret_cast<uint4 *>(sQ + chunk_at(warp * 32 + i * (32 / kLanes) + lane / kLanes, ch)));
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -619,10 +621,13 @@ __global__ void __launch_bounds__(kRows, Short<D>::kPerSM) cross_short_kernel(co
                 tmem_ld_wait();
                 if (x >= whole) {
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) {
+                    for (int y = 0; y < 32; ++y)
                         if (x + y >= L) s[y] = -INFINITY;
-                        if (far) s[y] -= u_max;
+                    if (far) {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) s[y] -= u_max;
                     }
+                    __syncwarp();
                 }
                 uint32_t u[16];
 #pragma unroll
