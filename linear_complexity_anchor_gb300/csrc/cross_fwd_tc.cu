@@ -13,7 +13,7 @@
 // and each K and V tile is read from L2 once for 256 rows.  S and O of both fill the 512 columns
 // at d = 128, so P lies over S: the products of one CTA run in the order they are issued, and the
 // next S is issued after the P V that reads it.  Bound by that round of a tile, S, its rows, P V; 8 heads,
-// 9728 x 2048, d = 128: 62 us, 1.3 PFLOP/s, and at 8 times that the card's power.  At d = 64 keys go in tiles
+// 9728 x 2048, d = 128: 62 us, 1.3 PFLOP/s; 8 times that 1.36, with the power cap at 3 % of the clock.  At d = 64 keys go in tiles
 // of 64, a thread a row, and two CTAs share an SM: 4 x 12 heads, 4200 x 1000: 75 us against 91 for tiles of 128.
 // One tile (up to 128 rows, a token of serving above all): bound by reading K and V (64 entries of 5000 states,
 // 8 heads of 128: 197 us, 6.6 TB/s).  At d = 128 S has two buffers, the next S is issued before the softmax
