@@ -427,7 +427,7 @@ ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_cross_backward(const anchor_att
  * Workspaces of cross attention and of the norms' weight gradients come from a pool of the library, one per device, which
  * keeps up to 512 MB of them between calls (a call after a synchronisation would otherwise map its workspace again,
  * 0.2 ms).  This gives what the current device's pool keeps back to the device; workspaces of calls that have not been
- * waited for stay.  Later calls take memory anew.
+ * waited for stay.  Later calls take memory anew.  Not to be called while a stream is captured.
  */
 ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_release_workspaces(void);
 
