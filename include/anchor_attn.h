@@ -424,6 +424,96 @@ ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_cross_forward(const anchor_attn
 ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_cross_backward(const anchor_attn_cross_t *p, void *stream);
 
 /*
+ * Attention with decaying states: linear attention (no softmax) whose state, a d x d matrix for each
+ * batch entry and head, loses a part of itself with every token,
+ *   X_t = g X_(t-1) + k_t v_t^T,  h_t = scale X_t^T q_t,  g = exp(log_decay[head]),
+ * which is h_i = scale (g^(i+1) q_i X_before + sum_{j <= i} g^(i-j) (q_i . k_j) v_j): O(n d^2).
+ * The gradients, with E the gradient of the state behind the last token (dlast, or zero):
+ *   F_j = scale sum_{i >= j} g^(i-j) q_i dh_i^T + g^(L-1-j) E,  dk_j = F_j v_j,  dv_j = F_j^T k_j,
+ *   dq_i = scale X_i dh_i,  dstate = g F_0  (E where L is 0).
+ * The decays are constants of the model: they get no gradient.  A log_decay above 0 counts as 0 (nothing is lost);
+ * -infinity keeps the token alone.
+ *   Q, K, V, H, dH, dQ, dK, dV [B][heads][n][d] views; log_decay: device fp32 [heads]
+ *   lengths: device int32 [B], each taken into [0, n]: the tokens of an entry that count; NULL: n for all
+ *   state, last, dlast, dstate: fp32, dense [B][heads][d (of k)][d (of v)], on 16 bytes: the states before the first
+ *   token (NULL: zeros) and behind the last one that counts (NULL: not wanted), and their gradients
+ * Rows of H, dQ, dK and dV from an entry's length on are zero; what the inputs hold there does not matter.  (Before it
+ * an infinity or a NaN at a token may reach the rows of up to 127 tokens before it.)  Heads or entries that share
+ * rows by a stride of 0 get gradients of their own.
+ * bf16 in and out (tensor cores: bf16 operands and fp32 accumulators; the weights of pairs and the state are rounded
+ * to bf16 where they meet c and a, the state itself is kept in fp32) or fp32 (CUDA cores, fp32 throughout).
+ * d in {16, 32, 64, 128}; B * heads <= 2^24, B * heads * n <= 2^31 - 1024.  No output may overlap an input or another
+ * output (ANCHOR_ATTN_ERR_ALIAS).  Results are bit-identical from run to run.  Workspaces come from the library's pool on
+ * `stream`, as cross attention's.
+ */
+typedef struct {
+    int dtype;                  /* 0 = bf16, 1 = fp32                                         */
+    int B, heads, n, d;
+    float scale;                /* finite                                                     */
+    anchor_attn_view_t Q, K, V, H, dH, dQ, dK, dV;
+    const float *log_decay;
+    const int *lengths;
+    const float *state;
+    float *last;                /* forward                                                    */
+    const float *dlast;         /* backward                                                   */
+    float *dstate;              /* backward                                                   */
+} anchor_attn_decay_t;
+
+ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_decay_forward(const anchor_attn_decay_t *p, void *stream);
+ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_decay_backward(const anchor_attn_decay_t *p, void *stream);
+
+/*
+ * The same token by token, for serving: n (few) tokens of B requests whose states lie in a pool and are moved on in place.
+ *   states: fp32, dense [slot_count][heads][d][d], on 16 bytes; slots: device int32 [B], where each request's state
+ *   lies; NULL: request b's is b (slot_count >= B)
+ * A request whose slot is negative or not below slot_count has H = 0 and moves no state.  Requests that share a slot
+ * are taken one after the other, in their order.  Slots of no request are left as they are.
+ */
+typedef struct {
+    int dtype;
+    int B, heads, n, d;
+    int slot_count;
+    float scale;
+    anchor_attn_view_t Q, K, V, H;
+    const float *log_decay;
+    float *states;
+    const int *slots;
+} anchor_attn_decay_step_t;
+
+ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_decay_step(const anchor_attn_decay_step_t *p, void *stream);
+
+/*
+ * The RMS norm of a residual sum: rows of D columns,
+ *   s = x + r (rounded to the rows' type),  y = weight o s / sqrt(mean(s^2) + eps),
+ * with y in the rows' type, or (bits8 = 1) as e4m3 numbers with fp32 scales for each row, or for each
+ * `group` columns of it: scale = max |y| / 448, y8 = y / scale, rounded to nearest.  Where max |y| is 0 the
+ * scale is 0.  An infinity or a NaN in a row shows in its y and scales.  Sums are taken in fp32; the norm is that
+ * of s as it is written.  R.ptr = NULL: s is x, and S is not written.  S may be X or R itself (the same view).
+ * Backward, from s, dy and (dS.ptr may be NULL) the gradient ds that reaches s by another way, xhat = s / sqrt(...):
+ *   dx = (weight o dy - xhat mean(weight o dy o xhat)) / sqrt(...) + ds,  dweight = sum over rows of dy o xhat;
+ * dx is the gradient of x and of r.  dX may be dY or dS itself.  Otherwise no output may overlap an input or another
+ * output (ANCHOR_ATTN_ERR_ALIAS).
+ * Rows lie in [B][n][D] views (of one head: `head` is not looked at).  D is a multiple of 16, 16 to 16384;
+ * B * n <= 2^31 - 1025.  The backward with a dweight takes a workspace on `stream` and one launch more; results are
+ * bit-identical from run to run.  Without rows dweight is set to zero.
+ */
+typedef struct {
+    int dtype;                  /* of the rows: 0 = bf16, 1 = fp32                            */
+    int B, n, D;
+    int weight_f32;             /* type of weight and dweight: 0 = the rows', 1 = fp32        */
+    int bits8;                  /* forward: 1: Y is e4m3                                      */
+    int group;                  /* columns of a scale: 0 (the row), 32, 64 or 128             */
+    float eps;                  /* finite, >= 0                                               */
+    anchor_attn_view_t X, R, S, Y, dY, dS, dX;
+    const void *weight;         /* [D], on 16 bytes, or NULL for ones                         */
+    void *dweight;              /* backward: [D] or NULL for none                             */
+    float *scales;              /* [B * n][D / group, rounded up]                             */
+} anchor_attn_add_norm_t;
+
+ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_add_norm(const anchor_attn_add_norm_t *p, void *stream);
+ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_add_norm_backward(const anchor_attn_add_norm_t *p, void *stream);
+
+/*
  * Workspaces of cross attention and of the norms' weight gradients come from a pool of the library, one per device, which
  * keeps up to 512 MB of them between calls (a call after a synchronisation would otherwise map its workspace again,
  * 0.2 ms).  This gives what the current device's pool keeps back to the device; workspaces of calls that have not been

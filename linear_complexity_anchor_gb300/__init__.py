@@ -12,8 +12,10 @@ import math
 import os
 import threading
 
-from . import _cross, _rope
+from . import _cross, _decay, _norm, _rope
 from ._cross import cross_backward, cross_forward
+from ._decay import decay_backward, decay_forward, decay_step
+from ._norm import add_norm, add_norm_8bit, add_norm_backward
 from ._rope import RopeTable, norm_rope, norm_rope_backward, rope, rope_backward, rope_frequencies, rope_table
 
 __all__ = [
@@ -24,7 +26,8 @@ __all__ = [
     "full_forward", "relative_error", "causal_forward", "block_forward", "anchor_attn_block_forward_ptr",
     "forward_host", "anchor_attn_forward_host_ptr", "anchor_attn_forward_host_f32_ptr",
     "cross_forward", "cross_backward", "rope", "rope_backward", "norm_rope", "norm_rope_backward", "rope_table",
-    "rope_frequencies", "RopeTable", "release_workspaces",
+    "rope_frequencies", "RopeTable", "decay_forward", "decay_backward", "decay_step",
+    "add_norm", "add_norm_8bit", "add_norm_backward", "release_workspaces",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libanchor_attn.so")
@@ -97,6 +100,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.anchor_attn_status_string.restype = ctypes.c_char_p
         _cross.bind(lib)
         _rope.bind(lib)
+        _decay.bind(lib)
+        _norm.bind(lib)
         if path is None:
             _lib = lib
         return lib

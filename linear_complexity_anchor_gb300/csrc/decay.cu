@@ -1,0 +1,238 @@
+// Attention with decaying states: argument checks, plan and launch; the states that segments begin with
+// (formulas and layout in include/anchor_attn.h and decay.cuh).
+#include "decay.cuh"
+
+#include <stdlib.h>
+
+namespace anchor {
+namespace {
+
+// Four elements of one slice's states a thread: along the segments in time, the sums of a segment alone
+// are replaced by the state before it.  Bound by memory (the sums come from L2).
+__global__ void __launch_bounds__(256) decay_prefix_kernel(const __grid_constant__ DecayProblem p) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int dd = p.d * p.d, per = dd / 4;
+    const long long f = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int kind = blockIdx.y;
+    if (f >= p.slices() * per) return;
+    const long long slice = f / per;
+    const int e = (int)(f - slice * per) * 4, b = (int)(slice / p.heads), h = (int)(slice - (long long)b * p.heads);
+    int which = 0;
+    while (p.pass[which].kind != kind) ++which;
+    const bool back = p.pass[which].back;
+    const float *first = p.pass[which].state;
+    const float rate = decay_rate(p.log_decay, h);
+    const int L = decay_length(p, b);
+    float4 x = first ? *reinterpret_cast<const float4 *>(first + slice * dd + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float *at = p.states + ((long long)kind * p.slices() + slice) * p.segs * dd + e;
+#pragma unroll 4
+    for (int k = 0; k < p.segs; ++k) {
+        const int s = back ? p.segs - 1 - k : k;
+        float4 *to = reinterpret_cast<float4 *>(at + (long long)s * dd);
+        const float4 t = k + 1 < p.segs ? *to : x;
+        *to = x;
+        const float keep = expf(rate * (float)decay_rows(p, s, L));
+        x.x = fmaf(x.x, keep, t.x), x.y = fmaf(x.y, keep, t.y), x.z = fmaf(x.z, keep, t.z), x.w = fmaf(x.w, keep, t.w);
+    }
+}
+
+CrossView lower(const View &v) { return CrossView{v.ptr, v.sb, v.sh, v.sn}; }
+
+// What a call reads and writes, to find overlaps.
+struct Regions {
+    struct Dense { const void *ptr; size_t bytes; };
+    View in[5], out[3];
+    Dense din[5], dout[1];
+    int nin = 0, nout = 0, ndin = 0, ndout = 0;
+    void reads(const void *ptr, size_t bytes) {
+        if (ptr && bytes) din[ndin++] = Dense{ptr, bytes};
+    }
+    void writes(const void *ptr, size_t bytes) {
+        if (ptr && bytes) dout[ndout++] = Dense{ptr, bytes};
+    }
+    bool overlap() const {
+        auto meets = [](const View &v, const Dense &x) { return bytes_overlap(v.ptr, (size_t)v.extent(), x.ptr, x.bytes); };
+        for (int o = 0; o < nout; ++o) {
+            for (int i = 0; i < nin; ++i)
+                if (views_overlap(out[o], in[i])) return true;
+            for (int i = 0; i < o; ++i)
+                if (views_overlap(out[o], out[i])) return true;
+            for (int i = 0; i < ndin; ++i)
+                if (meets(out[o], din[i])) return true;
+            for (int i = 0; i < ndout; ++i)
+                if (meets(out[o], dout[i])) return true;
+        }
+        for (int o = 0; o < ndout; ++o) {
+            for (int i = 0; i < nin; ++i)
+                if (meets(in[i], dout[o])) return true;
+            for (int i = 0; i < ndin; ++i)
+                if (bytes_overlap(dout[o].ptr, dout[o].bytes, din[i].ptr, din[i].bytes)) return true;
+        }
+        return false;
+    }
+};
+
+// The sizes that every call has.
+anchor_attn_status_t check_sizes(int dtype, int B, int heads, int n, int d, float scale) {
+    if ((dtype != 0 && dtype != 1) || B < 0 || heads < 0 || n < 0) return ANCHOR_ATTN_ERR_INVALID_ARG;
+    if (d != 16 && d != 32 && d != 64 && d != 128) return ANCHOR_ATTN_ERR_UNSUPPORTED;
+    if (!isfinite(scale)) return ANCHOR_ATTN_ERR_INVALID_ARG;
+    if (B == 0 || heads == 0) return ANCHOR_ATTN_OK;
+    if ((long long)B * heads > 1LL << 24 || (long long)n > (0x80000000LL - 1024) / ((long long)B * heads)) return ANCHOR_ATTN_ERR_UNSUPPORTED;
+    return ANCHOR_ATTN_OK;
+}
+
+bool misaligned(const void *p, unsigned bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
+
+// Segments: none where every SM has a CTA without.
+void plan(DecayProblem &p) {
+    const long long ctas = p.slices() * p.passes * (p.d == 128 ? 2 : 1);
+    const int most = std::max(1, p.n / 512);
+    const int want = ctas >= kPlanSMs ? 1 : (int)std::min<long long>(most, (2 * kPlanSMs + ctas - 1) / ctas);
+    p.seg = std::max(128, ((p.n + want - 1) / want + 127) / 128 * 128);
+    p.segs = std::max(1, (p.n + p.seg - 1) / p.seg);
+}
+
+// A call of few tokens goes token by token where the states are what it moves.
+bool by_steps(const anchor_attn_decay_t *a) { return a->n <= 8; }
+
+cudaError_t run(DecayProblem &p, cudaStream_t stream) {
+    cudaError_t e = cudaSuccess;
+    if (p.segs > 1) {
+        e = launch_decay_simt_states(p, stream);
+        const long long threads = p.slices() * (p.d * p.d / 4);
+        if (e == cudaSuccess) e = launch_pdl(decay_prefix_kernel, dim3((unsigned)((threads + 255) / 256), p.kinds), dim3(256), 0, stream, p);
+    }
+    return e == cudaSuccess ? launch_decay_simt(p, stream) : e;
+}
+
+anchor_attn_status_t finish(cudaError_t e) {
+    if (e == cudaSuccess) return ANCHOR_ATTN_OK;
+    cudaGetLastError();
+    return ANCHOR_ATTN_ERR_CUDA;
+}
+
+anchor_attn_status_t decay(const anchor_attn_decay_t *a, bool bwd, void *stream_v) {
+    if (!a) return ANCHOR_ATTN_ERR_INVALID_ARG;
+    cudaStream_t stream = (cudaStream_t)stream_v;
+    anchor_attn_status_t st = check_sizes(a->dtype, a->B, a->heads, a->n, a->d, a->scale);
+    if (st != ANCHOR_ATTN_OK || a->B == 0 || a->heads == 0) return st;
+    if (!a->log_decay || misaligned(a->log_decay, 4) || misaligned(a->lengths, 4)) return ANCHOR_ATTN_ERR_INVALID_ARG;
+    if (misaligned(a->state, 16) || misaligned(a->last, 16) || misaligned(a->dlast, 16) || misaligned(a->dstate, 16)) return ANCHOR_ATTN_ERR_INVALID_ARG;
+    const int es = a->dtype ? 4 : 2;
+    const size_t state_bytes = (size_t)a->B * a->heads * a->d * a->d * 4;
+    Regions g;
+    CrossView Q{}, K{}, V{}, H{}, dH{}, dQ{}, dK{}, dV{};
+    auto add = [&](const anchor_attn_view_t &v, bool writes, CrossView &to) {
+        if (st != ANCHOR_ATTN_OK || a->n == 0) return;
+        const View w = make_view(v, a->B, a->heads, a->n, a->d, es);
+        st = check_view(w, writes);
+        if (writes) g.out[g.nout++] = w;
+        else g.in[g.nin++] = w;
+        to = lower(w);
+    };
+    add(a->Q, false, Q);
+    add(a->K, false, K);
+    add(a->V, false, V);
+    g.reads(a->log_decay, (size_t)a->heads * 4);
+    g.reads(a->lengths, (size_t)a->B * 4);
+    g.reads(a->state, state_bytes);
+    if (!bwd) {
+        add(a->H, true, H);
+        g.writes(a->last, state_bytes);
+    } else {
+        add(a->dH, false, dH);
+        add(a->dQ, true, dQ);
+        add(a->dK, true, dK);
+        add(a->dV, true, dV);
+        g.reads(a->dlast, state_bytes);
+        g.writes(a->dstate, state_bytes);
+    }
+    if (st != ANCHOR_ATTN_OK) return st;
+    if (g.overlap()) return ANCHOR_ATTN_ERR_ALIAS;
+    if (a->n == 0) {
+        float *to = bwd ? a->dstate : a->last;
+        const float *from = bwd ? a->dlast : a->state;
+        if (!to) return ANCHOR_ATTN_OK;
+        return finish(from ? cudaMemcpyAsync(to, from, state_bytes, cudaMemcpyDeviceToDevice, stream) : cudaMemsetAsync(to, 0, state_bytes, stream));
+    }
+    if (!bwd && by_steps(a)) {
+        DecayStep s = {};
+        s.Q = Q, s.K = K, s.V = V, s.H = H, s.log_decay = a->log_decay, s.lengths = a->lengths, s.from = a->state, s.to = a->last;
+        s.B = a->B, s.heads = a->heads, s.n = a->n, s.d = a->d, s.count = a->B, s.scale = a->scale;
+        return finish(launch_decay_step(s, a->dtype == 1, stream));
+    }
+    DecayProblem p = {};
+    p.log_decay = a->log_decay, p.lengths = a->lengths, p.B = a->B, p.heads = a->heads, p.n = a->n, p.d = a->d, p.f32 = a->dtype == 1;
+    const float c = a->scale;
+    if (!bwd) {
+        p.passes = p.kinds = 1;
+        p.pass[0] = DecayPass{Q, K, V, H, c, c, 1.f, 0, 0, a->state, a->last, 0};
+    } else {
+        p.passes = 3, p.kinds = 2;
+        p.pass[0] = DecayPass{dH, V, K, dQ, c, c, 1.f, 0, 1, a->state, nullptr, 0};
+        p.pass[1] = DecayPass{V, dH, Q, dK, c, 1.f, c, 1, 1, a->dlast, nullptr, 1};
+        p.pass[2] = DecayPass{K, Q, dH, dV, c, 1.f, c, 1, 0, a->dlast, a->dstate, 1};
+    }
+    plan(p);
+    if (p.segs > 1) {
+        if (getenv("ANCHOR_ATTN_TEST_FAIL_ALLOC") != nullptr) return ANCHOR_ATTN_ERR_ALLOC;
+        if (workspace_alloc((void **)&p.states, state_bytes * p.segs * p.kinds, stream) != cudaSuccess) {
+            cudaGetLastError();
+            return ANCHOR_ATTN_ERR_ALLOC;
+        }
+    }
+    cudaError_t e = run(p, stream);
+    if (p.states) {
+        const cudaError_t ef = cudaFreeAsync(p.states, stream);
+        if (e == cudaSuccess) e = ef;
+    }
+    return finish(e);
+}
+
+anchor_attn_status_t decay_step(const anchor_attn_decay_step_t *a, void *stream_v) {
+    if (!a) return ANCHOR_ATTN_ERR_INVALID_ARG;
+    anchor_attn_status_t st = check_sizes(a->dtype, a->B, a->heads, a->n, a->d, a->scale);
+    if (st != ANCHOR_ATTN_OK) return st;
+    if (a->slot_count < 0 || (!a->slots && a->slot_count < a->B)) return ANCHOR_ATTN_ERR_INVALID_ARG;
+    if (a->heads > 0 && (long long)a->slot_count > (1LL << 40) / a->heads) return ANCHOR_ATTN_ERR_UNSUPPORTED;
+    if (a->B == 0 || a->heads == 0 || a->n == 0) return ANCHOR_ATTN_OK;
+    if (!a->log_decay || misaligned(a->log_decay, 4) || misaligned(a->slots, 4) || misaligned(a->states, 16)) return ANCHOR_ATTN_ERR_INVALID_ARG;
+    if (!a->states && a->slot_count > 0) return ANCHOR_ATTN_ERR_INVALID_ARG;
+    const int es = a->dtype ? 4 : 2;
+    Regions g;
+    DecayStep s = {};
+    const anchor_attn_view_t *in[3] = {&a->Q, &a->K, &a->V};
+    CrossView *to[3] = {&s.Q, &s.K, &s.V};
+    for (int i = 0; i < 3; ++i) {
+        const View w = make_view(*in[i], a->B, a->heads, a->n, a->d, es);
+        if ((st = check_view(w, false)) != ANCHOR_ATTN_OK) return st;
+        g.in[g.nin++] = w;
+        *to[i] = lower(w);
+    }
+    const View w = make_view(a->H, a->B, a->heads, a->n, a->d, es);
+    if ((st = check_view(w, true)) != ANCHOR_ATTN_OK) return st;
+    g.out[g.nout++] = w;
+    s.H = lower(w);
+    g.reads(a->log_decay, (size_t)a->heads * 4);
+    g.reads(a->slots, (size_t)a->B * 4);
+    g.writes(a->states, (size_t)a->slot_count * a->heads * a->d * a->d * 4);
+    if (g.overlap()) return ANCHOR_ATTN_ERR_ALIAS;
+    s.log_decay = a->log_decay, s.slots = a->slots, s.from = a->states, s.to = a->states;
+    s.B = a->B, s.heads = a->heads, s.n = a->n, s.d = a->d, s.count = a->slot_count, s.scale = a->scale;
+    return finish(launch_decay_step(s, a->dtype == 1, (cudaStream_t)stream_v));
+}
+
+}  // namespace
+}  // namespace anchor
+
+extern "C" {
+
+anchor_attn_status_t anchor_attn_decay_forward(const anchor_attn_decay_t *p, void *stream) { return anchor::decay(p, false, stream); }
+
+anchor_attn_status_t anchor_attn_decay_backward(const anchor_attn_decay_t *p, void *stream) { return anchor::decay(p, true, stream); }
+
+anchor_attn_status_t anchor_attn_decay_step(const anchor_attn_decay_step_t *p, void *stream) { return anchor::decay_step(p, stream); }
+
+}  // extern "C"

@@ -1,0 +1,74 @@
+// Attention with decaying states: the problem as the launches see it (formulas and layout in
+// include/anchor_attn.h).
+//
+// Forward and gradients have one form.  With g = exp(log_decay), a pass takes rows a, b, c and a state X,
+//   o_i = sum_{j <= i} p g^(i-j) (a_i . b_j) c_j + w g^(i+1) a_i X,   X' = g^L X + s sum_j g^(L-1-j) b_j^T c_j
+// and a pass backward in time the same with the rows of an entry in the other order, where the state that a row
+// sees is one step nearer (its own row's step is not taken: w g^i):
+//   H   (q, k, v)   X = state                        p = w = scale, s = 1
+//   dQ  (dh, v, k)  X = state transposed             p = w = scale, s = 1
+//   dK  (v, dh, q)  X = dlast transposed, backward   p = s = scale, w = 1
+//   dV  (k, q, dh)  X = dlast, backward              p = s = scale, w = 1;  its X' is dstate
+#pragma once
+
+#include "cross.cuh"
+
+#include <math.h>
+
+namespace anchor {
+
+struct DecayPass {
+    CrossView a, b, c, o;
+    float p, w, s;
+    int back;             // backward in time
+    int turned;           // the state is held transposed, [c][b]
+    const float *state;   // [B][heads][d][d] or null for zeros
+    float *last;          // the same, or null
+    int kind;             // of the state: which of the workspace's
+};
+
+// One pass whose state alone is wanted, for the segments of a sequence: b, c, s, back of the passes of its kind.
+struct DecayProblem {
+    DecayPass pass[3];
+    int passes;
+    const float *log_decay;  // [heads]
+    const int *lengths;      // [B] or null
+    int B, heads, n, d;
+    bool f32;
+    // A long sequence is cut into segments of `seg` rows.  states: [kind][B * heads][segs][d][d], first the sums of
+    // each segment alone, then the states that they begin with.
+    int segs, seg, kinds;
+    float *states;
+    __host__ __device__ long long slices() const { return (long long)B * heads; }
+};
+
+__device__ __forceinline__ int decay_length(const DecayProblem &p, int b) {
+    return p.lengths ? min(max(__ldg(p.lengths + b), 0), p.n) : p.n;
+}
+// log_decay as it is used: at most 0, and finite, so that its product with 0 is 0 (exp(-1e4) is 0).
+__device__ __forceinline__ float decay_rate(const float *log_decay, int h) {
+    const float g = __ldg(log_decay + h);
+    return g > 0.f ? 0.f : g < -1e4f ? -1e4f : g;
+}
+// the rows of segment `s` that count, of an entry with L
+__device__ __forceinline__ int decay_rows(const DecayProblem &p, int s, int L) { return min(max(L - s * p.seg, 0), p.seg); }
+
+// the sums of each segment but the last (in time) of each kind, the states that segments begin with, the passes
+cudaError_t launch_decay_prefix(const DecayProblem &p, cudaStream_t stream);
+cudaError_t launch_decay_simt_states(const DecayProblem &p, cudaStream_t stream);
+cudaError_t launch_decay_simt(const DecayProblem &p, cudaStream_t stream);
+
+// Token by token, the state in registers.
+struct DecayStep {
+    CrossView Q, K, V, H;
+    const float *log_decay;
+    const int *lengths;      // [B] or null
+    const int *slots;        // [B] or null: where an entry's state lies
+    const float *from;       // states before, or null for zeros
+    float *to;               // states behind, or null
+    int B, heads, n, d, count;  // count: of slots
+    float scale;
+};
+cudaError_t launch_decay_step(const DecayStep &p, bool f32, cudaStream_t stream);
+
+}  // namespace anchor

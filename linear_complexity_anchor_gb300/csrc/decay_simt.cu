@@ -1,0 +1,248 @@
+// Attention with decaying states on CUDA cores, fp32 throughout (formulas in decay.cuh).
+//
+// A CTA walks the rows of one batch entry's head (or of a segment of it) in chunks of 64, for CB columns of c
+// and of the state:
+//   S = a b^T (64 x 64), P = p g^(i-j) S below the diagonal, o = w g^(i+1) a X + P c,
+//   X = g^64 X + s sum_j g^(63-j) b_j^T c_j.
+// 16 x 16 threads; X is kept in registers, with a copy in shared memory for a X.  Every number is read from
+// shared memory for four uses at least.  Bound by the FMAs: (64 + CB) (64 + d) per row at CB columns, of which
+// 64 d are done again for each block of columns.
+#include "decay.cuh"
+
+namespace anchor {
+namespace {
+
+constexpr int kC = 64, kThreads = 256;
+
+template <int D, int CB> struct Geo {
+    static constexpr int kPitch = D + 4, kPitchC = CB + 4, kPitchP = kC + 4;
+    static constexpr int kA = 0, kB = kA + kC * kPitch, kCc = kB + kC * kPitch, kX = kCc + kC * kPitchC, kP = kX + D * kPitchC,
+                         kPow = kP + kC * kPitchP, kFloats = kPow + kC + 4;
+    static constexpr int kNC = CB / 16, kNB = D / 16;  // columns of c and rows of X of a thread
+};
+
+// rows [first, first + 64) of a view's columns [col, col + W), those from `rows` on zero
+template <typename T, int W>
+__device__ __forceinline__ void load(float *to, int pitch, const T *from, long long step, int rows, int col) {
+    constexpr int V = 16 / sizeof(T), kPer = W / V;
+    for (int x = threadIdx.x; x < kC * kPer; x += kThreads) {
+        const int r = x / kPer, e = x % kPer * V;
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (r < rows) raw = *reinterpret_cast<const uint4 *>(from + r * step + col + e);
+        float v[V];
+        if constexpr (V == 4) {
+            v[0] = __uint_as_float(raw.x), v[1] = __uint_as_float(raw.y), v[2] = __uint_as_float(raw.z), v[3] = __uint_as_float(raw.w);
+        } else {
+            const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+#pragma unroll
+        for (int i = 0; i < V; i += 4) *reinterpret_cast<float4 *>(to + r * pitch + e + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+}
+
+// N neighbouring floats, as wide as they are aligned
+template <int N> __device__ __forceinline__ void take(const float *p, float *v) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(v + i) = *reinterpret_cast<const float4 *>(p + i);
+    } else if constexpr (N == 2) {
+        *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(p);
+    } else {
+        v[0] = p[0];
+    }
+}
+template <int N> __device__ __forceinline__ void give(float *p, const float *v) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = v[i];
+}
+
+// acc[4][NC] += x[4 rows][k] y[k][NC columns], k < K: x rows of pitch px, y rows of pitch py
+template <int K, int NC>
+__device__ __forceinline__ void product(const float *x, int px, const float *y, int py, float (&acc)[4][NC]) {
+#pragma unroll 4
+    for (int k = 0; k < K; k += 4) {
+        float a[4][4], b[4][NC];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) take<4>(x + i * px + k, a[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) take<NC>(y + (k + j) * py, b[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) acc[i][c] = fmaf(a[i][j], b[j][c], acc[i][c]);
+    }
+}
+
+// STATES: the sums of a segment alone (of `kind` blockIdx.y), else a pass (blockIdx.y).
+template <typename T, int D, int CB, bool STATES>
+__global__ void __launch_bounds__(kThreads) decay_simt_kernel(const __grid_constant__ DecayProblem p) {
+    using G = Geo<D, CB>;
+    constexpr int NC = G::kNC, NB = G::kNB, kBlocks = D / CB;
+    extern __shared__ __align__(16) float sm[];
+    float *sA = sm + G::kA, *sB = sm + G::kB, *sC = sm + G::kCc, *sX = sm + G::kX, *sP = sm + G::kP, *pw = sm + G::kPow;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int cb = blockIdx.x % kBlocks, at = blockIdx.x / kBlocks;
+    const int segs = STATES ? p.segs - 1 : p.segs;
+    const long long slice = at / segs;
+    const int b = (int)(slice / p.heads), h = (int)(slice - (long long)b * p.heads);
+    int which = blockIdx.y;
+    if (STATES)
+        while (p.pass[which].kind != (int)blockIdx.y) ++which;  // a pass of that kind
+    const DecayPass &q = p.pass[which];
+    const bool back = q.back;
+    const int seg = at % segs + (STATES && back ? 1 : 0);  // the last one (in time) has no state behind it
+    const int L = decay_length(p, b), rows = decay_rows(p, seg, L), r0 = seg * p.seg;
+    const float rate = decay_rate(p.log_decay, h);
+    // STATES: b and c in the order of the kind, not turned
+    const bool turned = STATES ? false : q.turned;
+    const CrossView &vb = STATES && q.turned ? q.c : q.b, &vc = STATES && q.turned ? q.b : q.c;
+    const T *A = (const T *)q.a.ptr + b * q.a.sb + h * q.a.sh, *Bm = (const T *)vb.ptr + b * vb.sb + h * vb.sh,
+            *Cm = (const T *)vc.ptr + b * vc.sb + h * vc.sh;
+    T *O = (T *)q.o.ptr + b * q.o.sb + h * q.o.sh;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, c0 = cb * CB + tx * NC;
+    if (threadIdx.x <= kC) pw[threadIdx.x] = expf(rate * (float)threadIdx.x);
+
+    float x[NB][NC];
+    const long long slot = (long long)slice * D * D;
+    const float *from = STATES ? nullptr : p.segs > 1 ? p.states + (((long long)q.kind * p.slices() + slice) * p.segs + seg) * D * D
+                                                      : q.state ? q.state + slot : nullptr;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int r = ty * NB + i;
+            x[i][c] = !from ? 0.f : turned ? from[(c0 + c) * D + r] : from[r * D + c0 + c];
+        }
+    const int chunks = (rows + kC - 1) / kC;
+    for (int k = 0; k < chunks; ++k) {
+        const int first = (back ? chunks - 1 - k : k) * kC, count = min(kC, rows - first);
+        const long long r = r0 + first;
+        __syncthreads();
+        if (!STATES) {
+            load<T, D>(sA, G::kPitch, A + r * q.a.sn, q.a.sn, count, 0);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) give<NC>(sX + (ty * NB + i) * G::kPitchC + tx * NC, x[i]);
+        }
+        load<T, D>(sB, G::kPitch, Bm + r * vb.sn, vb.sn, count, 0);
+        load<T, CB>(sC, G::kPitchC, Cm + r * vc.sn, vc.sn, count, cb * CB);
+        __syncthreads();
+        if (!STATES) {
+            float s[4][4] = {};
+#pragma unroll 4
+            for (int e = 0; e < D; e += 4) {
+                float a4[4][4], b4[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) take<4>(sA + (ty * 4 + i) * G::kPitch + e, a4[i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) take<4>(sB + (tx + 16 * j) * G::kPitch + e, b4[j]);
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[i][j] = fmaf(a4[i][y], b4[j][y], s[i][j]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int y = ty * 4 + i, z = tx + 16 * j, far = back ? z - y : y - z;
+                    sP[y * G::kPitchP + z] = far >= 0 ? s[i][j] * (q.p * pw[far]) : 0.f;
+                }
+            float o[4][NC] = {};
+            product<D, NC>(sA + ty * 4 * G::kPitch, G::kPitch, sX + tx * NC, G::kPitchC, o);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int y = ty * 4 + i;
+                const float f = y < count ? q.w * pw[back ? count - 1 - y : y + 1] : 0.f;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) o[i][c] *= f;
+            }
+            product<kC, NC>(sP + ty * 4 * G::kPitchP, G::kPitchP, sC + tx * NC, G::kPitchC, o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int y = ty * 4 + i;
+                if (y >= count) continue;
+                T *to = O + (r + y) * q.o.sn + c0;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) to[c] = from_f32<T>(o[i][c]);
+            }
+        }
+        const float keep = pw[count];
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) x[i][c] *= keep;
+#pragma unroll 4
+        for (int j = 0; j < count; ++j) {
+            const float f = q.s * pw[back ? j + 1 : count - 1 - j];
+            float y[NB], z[NC];
+            take<NB>(sB + j * G::kPitch + ty * NB, y);
+            take<NC>(sC + j * G::kPitchC + tx * NC, z);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) z[c] *= f;
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) x[i][c] = fmaf(y[i], z[c], x[i][c]);
+        }
+    }
+    if (!STATES) {
+        // rows of the segment from the length on
+        const int end = min(p.seg, p.n - r0);
+        for (int e = threadIdx.x; e < max(end - rows, 0) * CB; e += kThreads)
+            O[(long long)(r0 + rows + e / CB) * q.o.sn + cb * CB + e % CB] = from_f32<T>(0.f);
+    }
+    float *to = STATES ? p.states + (((long long)blockIdx.y * p.slices() + slice) * p.segs + seg) * D * D
+                       : q.last && seg == (back ? 0 : p.segs - 1) ? q.last + slot : nullptr;
+    if (to) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int r = ty * NB + i;
+                if (turned) to[(c0 + c) * D + r] = x[i][c];
+                else to[r * D + c0 + c] = x[i][c];
+            }
+    }
+}
+
+template <typename T, int D, int CB, bool STATES>
+cudaError_t launch(const DecayProblem &p, cudaStream_t stream) {
+    static SmemOnce once;
+    constexpr size_t smem = Geo<D, CB>::kFloats * 4;
+    cudaError_t e = once(decay_simt_kernel<T, D, CB, STATES>, smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(p.slices() * (STATES ? p.segs - 1 : p.segs) * (D / CB)), STATES ? p.kinds : p.passes);
+    return launch_pdl(decay_simt_kernel<T, D, CB, STATES>, grid, dim3(kThreads), smem, stream, p);
+}
+
+// Heads of 64 and 128 columns go in blocks of 64, or of 32 where blocks of 64 leave SMs without one.
+template <typename T, bool STATES>
+cudaError_t launch(const DecayProblem &p, cudaStream_t stream) {
+    const long long ctas = p.slices() * p.segs * p.passes * (p.d / 64);
+    const bool narrow = ctas < kPlanSMs;
+    switch (p.d) {
+    case 16: return launch<T, 16, 16, STATES>(p, stream);
+    case 32: return launch<T, 32, 32, STATES>(p, stream);
+    case 64: return narrow ? launch<T, 64, 32, STATES>(p, stream) : launch<T, 64, 64, STATES>(p, stream);
+    default: return narrow ? launch<T, 128, 32, STATES>(p, stream) : launch<T, 128, 64, STATES>(p, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_decay_simt_states(const DecayProblem &p, cudaStream_t stream) {
+    return p.f32 ? launch<float, true>(p, stream) : launch<__nv_bfloat16, true>(p, stream);
+}
+cudaError_t launch_decay_simt(const DecayProblem &p, cudaStream_t stream) {
+    return p.f32 ? launch<float, false>(p, stream) : launch<__nv_bfloat16, false>(p, stream);
+}
+
+}  // namespace anchor
