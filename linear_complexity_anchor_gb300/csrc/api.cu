@@ -3,6 +3,7 @@
 #include "anchor_attn.h"
 #include "common.cuh"
 #include "cross.cuh"
+#include "decay.cuh"
 
 #include <math.h>
 #include <stdlib.h>
@@ -450,7 +451,7 @@ anchor_attn_status_t anchor_attn_release_workspaces(void) {
 
 anchor_attn_status_t anchor_attn_device_error(unsigned *code) {
     if (!code) return ANCHOR_ATTN_ERR_INVALID_ARG;
-    unsigned a = 0, b = 0, c = 0, e = 0, f = 0, g = 0, k = 0, l = 0, q = 0, r = 0, w = 0, x = 0, y = 0;
+    unsigned a = 0, b = 0, c = 0, e = 0, f = 0, g = 0, k = 0, l = 0, q = 0, r = 0, w = 0, x = 0, y = 0, z = 0;
     if (cudaDeviceSynchronize() != cudaSuccess || anchor::umma_read_and_clear_error(&a) != cudaSuccess ||
         anchor::simt_read_and_clear_error(&b) != cudaSuccess || anchor::bwd_read_and_clear_error(&c) != cudaSuccess ||
         anchor::causal_read_and_clear_error(&e) != cudaSuccess || anchor::block_read_and_clear_error(&f) != cudaSuccess ||
@@ -459,11 +460,11 @@ anchor_attn_status_t anchor_attn_device_error(unsigned *code) {
         anchor::causal_wide_read_and_clear_error(&r) != cudaSuccess ||
         anchor::bwd_wide_read_and_clear_error(&w) != cudaSuccess ||
         anchor::cross_fwd_read_and_clear_error(&x) != cudaSuccess ||
-        anchor::cross_bwd_read_and_clear_error(&y) != cudaSuccess) {
+        anchor::cross_bwd_read_and_clear_error(&y) != cudaSuccess || anchor::decay_read_and_clear_error(&z) != cudaSuccess) {
         cudaGetLastError();
         return ANCHOR_ATTN_ERR_CUDA;
     }
-    *code = a | b | c | e | f | g | k | l | q | r | w | x | y;
+    *code = a | b | c | e | f | g | k | l | q | r | w | x | y | z;
     return ANCHOR_ATTN_OK;
 }
 

@@ -100,11 +100,12 @@ bool by_steps(const anchor_attn_decay_t *a) { return a->n <= 8; }
 cudaError_t run(DecayProblem &p, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
     if (p.segs > 1) {
-        e = launch_decay_simt_states(p, stream);
+        e = p.f32 ? launch_decay_simt_states(p, stream) : launch_decay_tc_states(p, stream);
         const long long threads = p.slices() * (p.d * p.d / 4);
         if (e == cudaSuccess) e = launch_pdl(decay_prefix_kernel, dim3((unsigned)((threads + 255) / 256), p.kinds), dim3(256), 0, stream, p);
     }
-    return e == cudaSuccess ? launch_decay_simt(p, stream) : e;
+    if (e != cudaSuccess) return e;
+    return p.f32 ? launch_decay_simt(p, stream) : launch_decay_tc(p, stream);
 }
 
 anchor_attn_status_t finish(cudaError_t e) {

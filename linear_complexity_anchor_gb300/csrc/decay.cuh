@@ -55,8 +55,13 @@ __device__ __forceinline__ int decay_rows(const DecayProblem &p, int s, int L) {
 
 // the sums of each segment but the last (in time) of each kind, the states that segments begin with, the passes
 cudaError_t launch_decay_prefix(const DecayProblem &p, cudaStream_t stream);
+// fp32, CUDA cores
 cudaError_t launch_decay_simt_states(const DecayProblem &p, cudaStream_t stream);
 cudaError_t launch_decay_simt(const DecayProblem &p, cudaStream_t stream);
+// bf16, tensor cores
+cudaError_t launch_decay_tc_states(const DecayProblem &p, cudaStream_t stream);
+cudaError_t launch_decay_tc(const DecayProblem &p, cudaStream_t stream);
+cudaError_t decay_read_and_clear_error(unsigned *out);
 
 // Token by token, the state in registers.
 struct DecayStep {

@@ -22,23 +22,13 @@ template <int D, int CB> struct Geo {
 };
 
 // rows [first, first + 64) of a view's columns [col, col + W), those from `rows` on zero
-template <typename T, int W>
-__device__ __forceinline__ void load(float *to, int pitch, const T *from, long long step, int rows, int col) {
-    constexpr int V = 16 / sizeof(T), kPer = W / V;
+template <int W>
+__device__ __forceinline__ void load(float *to, int pitch, const float *from, long long step, int rows, int col) {
+    constexpr int kPer = W / 4;
     for (int x = threadIdx.x; x < kC * kPer; x += kThreads) {
-        const int r = x / kPer, e = x % kPer * V;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (r < rows) raw = *reinterpret_cast<const uint4 *>(from + r * step + col + e);
-        float v[V];
-        if constexpr (V == 4) {
-            v[0] = __uint_as_float(raw.x), v[1] = __uint_as_float(raw.y), v[2] = __uint_as_float(raw.z), v[3] = __uint_as_float(raw.w);
-        } else {
-            const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
-#pragma unroll
-        for (int i = 0; i < V; i += 4) *reinterpret_cast<float4 *>(to + r * pitch + e + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        const int r = x / kPer, e = x % kPer * 4;
+        *reinterpret_cast<float4 *>(to + r * pitch + e) =
+            r < rows ? *reinterpret_cast<const float4 *>(from + r * step + col + e) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
@@ -78,7 +68,7 @@ __device__ __forceinline__ void product(const float *x, int px, const float *y, 
 }
 
 // STATES: the sums of a segment alone (of `kind` blockIdx.y), else a pass (blockIdx.y).
-template <typename T, int D, int CB, bool STATES>
+template <int D, int CB, bool STATES>
 __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const __grid_constant__ DecayProblem p) {
     using G = Geo<D, CB>;
     constexpr int NC = G::kNC, NB = G::kNB, kBlocks = D / CB;
@@ -101,9 +91,9 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const __grid_const
     // STATES: b and c in the order of the kind, not turned
     const bool turned = STATES ? false : q.turned;
     const CrossView &vb = STATES && q.turned ? q.c : q.b, &vc = STATES && q.turned ? q.b : q.c;
-    const T *A = (const T *)q.a.ptr + b * q.a.sb + h * q.a.sh, *Bm = (const T *)vb.ptr + b * vb.sb + h * vb.sh,
-            *Cm = (const T *)vc.ptr + b * vc.sb + h * vc.sh;
-    T *O = (T *)q.o.ptr + b * q.o.sb + h * q.o.sh;
+    const float *A = (const float *)q.a.ptr + b * q.a.sb + h * q.a.sh, *Bm = (const float *)vb.ptr + b * vb.sb + h * vb.sh,
+            *Cm = (const float *)vc.ptr + b * vc.sb + h * vc.sh;
+    float *O = (float *)q.o.ptr + b * q.o.sb + h * q.o.sh;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, c0 = cb * CB + tx * NC;
     if (threadIdx.x <= kC) pw[threadIdx.x] = expf(rate * (float)threadIdx.x);
 
@@ -124,12 +114,12 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const __grid_const
         const long long r = r0 + first;
         __syncthreads();
         if (!STATES) {
-            load<T, D>(sA, G::kPitch, A + r * q.a.sn, q.a.sn, count, 0);
+            load<D>(sA, G::kPitch, A + r * q.a.sn, q.a.sn, count, 0);
 #pragma unroll
             for (int i = 0; i < NB; ++i) give<NC>(sX + (ty * NB + i) * G::kPitchC + tx * NC, x[i]);
         }
-        load<T, D>(sB, G::kPitch, Bm + r * vb.sn, vb.sn, count, 0);
-        load<T, CB>(sC, G::kPitchC, Cm + r * vc.sn, vc.sn, count, cb * CB);
+        load<D>(sB, G::kPitch, Bm + r * vb.sn, vb.sn, count, 0);
+        load<CB>(sC, G::kPitchC, Cm + r * vc.sn, vc.sn, count, cb * CB);
         __syncthreads();
         if (!STATES) {
             float s[4][4] = {};
@@ -169,9 +159,9 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const __grid_const
             for (int i = 0; i < 4; ++i) {
                 const int y = ty * 4 + i;
                 if (y >= count) continue;
-                T *to = O + (r + y) * q.o.sn + c0;
+                float *to = O + (r + y) * q.o.sn + c0;
 #pragma unroll
-                for (int c = 0; c < NC; ++c) to[c] = from_f32<T>(o[i][c]);
+                for (int c = 0; c < NC; ++c) to[c] = o[i][c];
             }
         }
         const float keep = pw[count];
@@ -197,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const __grid_const
         // rows of the segment from the length on
         const int end = min(p.seg, p.n - r0);
         for (int e = threadIdx.x; e < max(end - rows, 0) * CB; e += kThreads)
-            O[(long long)(r0 + rows + e / CB) * q.o.sn + cb * CB + e % CB] = from_f32<T>(0.f);
+            O[(long long)(r0 + rows + e / CB) * q.o.sn + cb * CB + e % CB] = 0.f;
     }
     float *to = STATES ? p.states + (((long long)blockIdx.y * p.slices() + slice) * p.segs + seg) * D * D
                        : q.last && seg == (back ? 0 : p.segs - 1) ? q.last + slot : nullptr;
@@ -213,36 +203,36 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const __grid_const
     }
 }
 
-template <typename T, int D, int CB, bool STATES>
+template <int D, int CB, bool STATES>
 cudaError_t launch(const DecayProblem &p, cudaStream_t stream) {
     static SmemOnce once;
     constexpr size_t smem = Geo<D, CB>::kFloats * 4;
-    cudaError_t e = once(decay_simt_kernel<T, D, CB, STATES>, smem);
+    cudaError_t e = once(decay_simt_kernel<D, CB, STATES>, smem);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(p.slices() * (STATES ? p.segs - 1 : p.segs) * (D / CB)), STATES ? p.kinds : p.passes);
-    return launch_pdl(decay_simt_kernel<T, D, CB, STATES>, grid, dim3(kThreads), smem, stream, p);
+    return launch_pdl(decay_simt_kernel<D, CB, STATES>, grid, dim3(kThreads), smem, stream, p);
 }
 
 // Heads of 64 and 128 columns go in blocks of 64, or of 32 where blocks of 64 leave SMs without one.
-template <typename T, bool STATES>
+template <bool STATES>
 cudaError_t launch(const DecayProblem &p, cudaStream_t stream) {
     const long long ctas = p.slices() * p.segs * p.passes * (p.d / 64);
     const bool narrow = ctas < kPlanSMs;
     switch (p.d) {
-    case 16: return launch<T, 16, 16, STATES>(p, stream);
-    case 32: return launch<T, 32, 32, STATES>(p, stream);
-    case 64: return narrow ? launch<T, 64, 32, STATES>(p, stream) : launch<T, 64, 64, STATES>(p, stream);
-    default: return narrow ? launch<T, 128, 32, STATES>(p, stream) : launch<T, 128, 64, STATES>(p, stream);
+    case 16: return launch<16, 16, STATES>(p, stream);
+    case 32: return launch<32, 32, STATES>(p, stream);
+    case 64: return narrow ? launch<64, 32, STATES>(p, stream) : launch<64, 64, STATES>(p, stream);
+    default: return narrow ? launch<128, 32, STATES>(p, stream) : launch<128, 64, STATES>(p, stream);
     }
 }
 
 }  // namespace
 
 cudaError_t launch_decay_simt_states(const DecayProblem &p, cudaStream_t stream) {
-    return p.f32 ? launch<float, true>(p, stream) : launch<__nv_bfloat16, true>(p, stream);
+    return launch<true>(p, stream);
 }
 cudaError_t launch_decay_simt(const DecayProblem &p, cudaStream_t stream) {
-    return p.f32 ? launch<float, false>(p, stream) : launch<__nv_bfloat16, false>(p, stream);
+    return launch<false>(p, stream);
 }
 
 }  // namespace anchor
