@@ -1,24 +1,27 @@
 // Attention with decaying states in bf16 on the tensor cores (formulas in decay.cuh).
 //
-// A CTA walks the rows of one batch entry's head (or of a segment of it) in chunks of 128.  With i, j rows of a
-// chunk of `count`, X the state before it (d x d, fp32, in tensor memory) and X~ its bf16 image in shared memory:
+// The work comes in items: the rows of one batch entry's head (or of a segment of it), for 64 columns of c and of
+// the state.  A CTA takes every gridDim.x-th item and walks its rows in chunks of 128; what loads, multiplies
+// and stores runs on from item to item.  With i, j rows of a chunk of `count`, X the state before it (d x 64, fp32,
+// in tensor memory) and X~ its bf16 image in shared memory:
 //   S = a b^T,  P = g^(i-j) S below the diagonal (bf16, over S),  o = p P c + w g^(i+1) (a X~)
-//   X <- g^count X + (s g^(count-1-j) b_j)^T c
+//   X <- g^count X + b^T (s g^(count-1-j) c_j)
 // (a pass backward in time: the other triangle, g^(j-i), g^(count-1-i), g^(j+1), chunks from the last to the first).
 //
-// Roundings: P and X~ to bf16, each once, where they meet c and a; the rows g^(count-1-j) b_j are two bf16
-// numbers (what the first leaves of them is the second), so that X is exact to 2^-17 or better: it is an fp32
+// Roundings: P and X~ to bf16, each once, where they meet c and a; the rows s g^(count-1-j) c_j are two bf16
+// numbers (what the first leaves of them is the second), so that X is exact to 2^-17: it is an fp32
 // result, and its own rounding in X~ stays the only one of the part of o that goes by it.  With one number o
 // would carry three roundings there, 1.7 times a lone one, against 1.4.
 //
-// Warps 0 to 3 (rows): P from S, and o from the two products; a thread a row.  Warps 4 to 7 (state): X~ and the decay of X, a
-// thread a row of X; the rows of b times their weights, in place, a thread a row, with their second numbers in a
-// tile of their own.  Warp 8 loads tiles by TMA into a ring (a, b, c of each chunk in turn), warp 9 issues
-// the products, in the order S, a X~, P c, X.  Tensor memory: S (P over it), the two products of o and X; at 64 columns a X~
-// lies over the half of S that P leaves, and two CTAs share an SM.
+// Sixteen row warps do all that is done by elements, one step after the other, so that four warps of each scheduler run
+// the same instructions (with warps of their own for each step, most of the time went into fetching instructions: at d =
+// 128 a chunk took 3.9 us against 2.65): for chunk k
+//   o of chunk k - 1 from its two products, out by TMA;  X~ and the decay of X;  the weighted rows of c;  P of chunk k + 1
+// a thread a row of each, and a quarter of its columns.  One warp loads tiles by TMA, one issues the products: P c, S of the
+// next chunk, a X~, X, each as soon as its operands are there; S has two buffers.
 //
 // STATES: the sums of a segment alone, s sum_j g^(rows-1-j) b_j^T c_j: the last product alone, with weights that count from the
-// segment's end, so that X needs no decay on the way; all eight warps weight rows.
+// segment's end, so that X needs no decay on the way.
 #include "cross_tc.cuh"
 #include "decay.cuh"
 
@@ -30,398 +33,564 @@ namespace {
 
 using namespace cross_tc;
 
-// D columns (heads of 16 and 32 are 64)
+constexpr int kColumns = 64;                      // of c, of the state and of o, an item
+constexpr int kTileC = kTile<kColumns>;
+constexpr int kRowWarps = 16, kWarpLoad = 16, kWarpIssue = 17, kThreads = 32 * 18;
+constexpr uint32_t kColS = 0, kColIn = 256, kColBy = 320, kColX = 384, kCols = 512;  // of tensor memory; S has two buffers
+
+// D columns of a and b (heads of 16 and 32 are 64)
 template <int D, bool STATES>
 struct Geo {
-    static constexpr int kPerSM = D == 64 ? 2 : 1;
-    static constexpr int kSlots = STATES && D == 128 ? 6 : 5, kPer = STATES ? 2 : 3;  // tiles of the ring and of a chunk
-    static constexpr int kImgBytes = D * D * 2;
-    // With 64 columns X's product has 128 rows all the same, of which the upper 64 are not read: their operand
-    // starts kHalf behind the tile's start, which has to be within the buffer.
-    static constexpr int kHalf = D == 64 ? kImgBytes : kBlock;
-    static constexpr int kLo = 0, kRing = kTile<D>, kImg = kRing + kSlots * kTile<D>;
-    static constexpr int kPow = kImg + (STATES && D == 128 ? 0 : kImgBytes);
-    static constexpr int kBars = kPow + 132 * 4, kNBars = 2 * kSlots + 8, kSmem = kBars + kNBars * 8 + 16 + 1024;
-    static constexpr int kLoad = 8, kIssue = 9, kThreads = 320;
-    static constexpr uint32_t kColS = 0, kColIn = 128, kColBy = D == 64 ? 64 : 256, kColX = STATES ? 0 : D == 64 ? 192 : 384;
-    static constexpr uint32_t kCols = STATES ? D : D == 64 ? 256 : 512;
-    static_assert((kSmem + 1024) * kPerSM <= 228 * 1024, "shared memory");
+    static constexpr int kStages = STATES ? 3 : D == 128 ? 2 : 3;
+    static constexpr int kA = 0, kB = STATES ? 0 : kTile<D>, kC = kB + kTile<D>, kStage = kC + kTileC;  // of a stage
+    static constexpr int kWeighted = STATES ? 2 : 1;  // buffers of the weighted rows of c
+    static constexpr int kRing = 0, kW = kRing + kStages * kStage, kImg = kW + kWeighted * 2 * kTileC, kOut = kImg + (STATES ? 0 : D * kColumns * 2);
+    static constexpr int kPow = kOut + (STATES ? 0 : kTileC), kBars = kPow + kRowWarps * 32 * 4;
+    static constexpr int kNBars = 5 * kStages + 20, kSmem = kBars + kNBars * 8 + 8;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
 struct TcParams {
     DecayProblem p;
-    TileMap a[3], b[3], c[3];
+    TileMap a[3], b[3], c[3], o[3];
+    int items, halves;
+    Divide by_segs, by_heads;
 };
 
-// The 16-byte chunks [from, to) of a row of b, times its weight w, as two bf16 numbers: the first in place, the second in `lo`.
-// `on`: the row counts (else zeros, whatever it holds).
-__device__ __forceinline__ void weight_row(uint8_t *tile, uint8_t *lo, int row, int from, int to, float w, bool on) {
-    const uint64_t w2 = f32x2(w, w);
-#pragma unroll 4
-    for (int c = from; c < to; ++c) {
-        const uint32_t at = chunk_at(row, c);
-        const uint4 raw = *reinterpret_cast<const uint4 *>(tile + at);
-        const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-        uint32_t h[4], l[4];
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void *src, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"((uint64_t)map),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
+}
+
+// One item, as every warp sees it.
+template <bool STATES>
+struct Item {
+    const DecayPass *q;
+    int which, b, h, slice, seg, half, r0, rows, K, end;  // end: rows of the segment
+    bool back, turned;
+    const float *from;  // states outside, or null
+    float *to;
+
+    __device__ __forceinline__ void set(const TcParams &a, int index) {
+        const DecayProblem &p = a.p;
+        const int kinds = STATES ? p.kinds : p.passes, segs = STATES ? p.segs - 1 : p.segs;
+        // the halves and passes of a segment are neighbours, so that what they share is read once
+        int x = a.halves == 2 ? index >> 1 : index;
+        half = index - x * a.halves;
+        const int y = kinds == 3 ? x / 3 : kinds == 2 ? x >> 1 : x, of = x - y * kinds;
+        slice = a.by_segs.of(y);
+        b = a.by_heads.of(slice), h = slice - b * p.heads;
+        which = of;
+        if (STATES)
+            while (p.pass[which].kind != of) ++which;  // a pass of that kind
+        q = &p.pass[which];
+        back = q->back, turned = STATES ? false : q->turned;
+        seg = y - slice * segs + (STATES && back ? 1 : 0);  // the last one (in time) has no state behind it
+        r0 = seg * p.seg, end = min(p.seg, p.n - r0);
+        rows = decay_rows(p, seg, decay_length(p, b));
+        K = (rows + kRows - 1) / kRows;
+        const long long dd = p.d * p.d;
+        float *in = p.states + (((long long)(STATES ? of : q->kind) * p.slices() + slice) * p.segs + seg) * dd;
+        from = STATES ? nullptr : p.segs > 1 ? in : q->state ? q->state + slice * dd : nullptr;
+        to = STATES ? in : q->last && seg == (back ? 0 : p.segs - 1) ? q->last + slice * dd : nullptr;
+    }
+    // chunk k: its first row in the segment, its rows; whether X takes it; whether there is a state before it
+    __device__ __forceinline__ int first(int k) const { return (back ? K - 1 - k : k) * kRows; }
+    __device__ __forceinline__ int count(int k) const { return min(kRows, rows - first(k)); }
+    __device__ __forceinline__ bool takes(int k) const { return STATES || k + 1 < K || to != nullptr; }
+    __device__ __forceinline__ bool has(int k) const { return k > 0 || from != nullptr; }
+};
+
+// Chunks `first` and first + 1 of a row of c times its weight w, as two bf16 numbers in two tiles.  `on`: the row counts (else
+// zeros, whatever it holds).  With w = u + v in bf16 (2^-18 of w is left out), h = c u rounded, and l = (c u - h) + c v, of
+// which the first part is exact: three instructions for two numbers.
+__device__ __forceinline__ void weight_row(const uint8_t *tile, uint8_t *hi, uint8_t *lo, int row, int first, float w, bool on) {
+    const __nv_bfloat16 u1 = __float2bfloat16_rn(w);
+    const __nv_bfloat162 u = __bfloat162bfloat162(u1), v = __float2bfloat162_rn(w - __bfloat162float(u1));
+    uint4 x4[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) x4[c] = *reinterpret_cast<const uint4 *>(tile + chunk_at(row, first + c));
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        uint4 h4, l4;
+        const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&x4[c]);
+        __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&h4), *l = reinterpret_cast<__nv_bfloat162 *>(&l4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint64_t x = mul_f32x2(f32x2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u)), w2);
-            float x0, x1, r0, r1;
-            f32x2_split(x, x0, x1);
-            h[i] = pack2(x0, x1);
-            // (what is left is exact)
-            f32x2_split(add_f32x2(x, f32x2(-__uint_as_float(h[i] << 16), -__uint_as_float(h[i] & 0xffff0000u))), r0, r1);
-            l[i] = pack2(r0, r1);
-            if (!on) h[i] = l[i] = 0u;
+            h[i] = __hmul2(x[i], u);
+            l[i] = __hfma2(x[i], v, __hfma2(x[i], u, __hneg2(h[i])));
         }
-        *reinterpret_cast<uint4 *>(tile + at) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4 *>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+        if (!on) h4 = l4 = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(hi + chunk_at(row, first + c)) = h4;
+        *reinterpret_cast<uint4 *>(lo + chunk_at(row, first + c)) = l4;
     }
 }
 
-// X += (hi + lo)^T c: both d x 128 operands contracted over the rows
-template <int D, int kHalf>
-__device__ __forceinline__ void product_x(uint32_t x, uint32_t hi, uint32_t lo, uint32_t c, bool add) {
-    constexpr uint32_t id = idesc_bf16_f32(kRows, D, true, true);
-    const uint64_t h = smem_desc_sw128(hi, kHalf, 1024), l = smem_desc_sw128(lo, kHalf, 1024), cd = desc_mn(c);
+// What the issuing warp does it does as a whole, one lane of it elected for each product: with uniform control the descriptors
+// are made by uniform instructions.  (Issued by a lane on a branch of its own a product took 75 to 140 cycles: 343 us for 4 x
+// 16 heads, 16384, d = 128, against 255.)
+__device__ __forceinline__ void product(uint32_t to, uint64_t a, uint64_t b, uint32_t id, uint32_t add) {
+    asm volatile(
+        "{\n .reg .pred e, p;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(to),
+        "l"(a), "l"(b), "r"(id), "r"(add)
+        : "memory");
+}
+__device__ __forceinline__ void product_tmem(uint32_t to, uint32_t a, uint64_t b, uint32_t id, uint32_t add) {
+    asm volatile(
+        "{\n .reg .pred e, p;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(to),
+        "r"(a), "l"(b), "r"(id), "r"(add)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, unsigned int *error) {
+    return __all_sync(0xffffffffu, bwait(bar, parity, error));
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t at, float *v) {
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+                   "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(at));
 #pragma unroll
-    for (int k = 0; k < kRows / 16; ++k) umma_bf16(x, h + step_mn(k), cd + step_mn(k), id, k > 0 || add ? 1u : 0u);
-#pragma unroll
-    for (int k = 0; k < kRows / 16; ++k) umma_bf16(x, l + step_mn(k), cd + step_mn(k), id, 1u);
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 template <int D, bool STATES>
-__global__ void __launch_bounds__(Geo<D, STATES>::kThreads, Geo<D, STATES>::kPerSM) decay_kernel(const __grid_constant__ TcParams a) {
+__global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constant__ TcParams a) {
     using G = Geo<D, STATES>;
-    constexpr int NS = G::kSlots, PER = G::kPer;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    float *pw = reinterpret_cast<float *>(sm + G::kPow);
+    constexpr int NS = G::kStages;
+    extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G::kBars);
-    uint64_t *full = bars, *empty = full + NS, *s_full = empty + NS, *p_full = s_full + 1, *o_full = p_full + 1, *o_free = o_full + 1,
-             *img_full = o_free + 1, *b_full = img_full + 1, *x_full = b_full + 1, *done = x_full + 1;
+    uint64_t *a_full = bars, *b_full = a_full + NS, *c_full = b_full + NS, *a_empty = c_full + NS, *bc_empty = a_empty + NS,
+             *s_full = bc_empty + NS /* [2] */, *p_full = s_full + 2 /* [2] */, *w_full = p_full + 2 /* [2] */, *o_full = w_full + 2,
+             *o_free = o_full + 1, *x_ready = o_free + 1, *x_full = x_ready + 1 /* [2] */, *staged = x_full + 2 /* [4] */, *sent = staged + 4 /* [4] */, *done = sent + 4;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + G::kNBars);
     const DecayProblem &p = a.p;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    unsigned int *error = &g_decay_error;
+    if (smem_u32(sm) & 1023u) {  // (there is no room to move the tiles: never seen)
+        if (threadIdx.x == 0) atomicOr(error, 1u);
+        return;
+    }
     if (threadIdx.x == 0) {
-        for (int s = 0; s < NS; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
-        mbar_init(s_full, 1);
-        mbar_init(p_full, 4);
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(a_full + s, 1);
+            mbar_init(b_full + s, 1);
+            mbar_init(c_full + s, 1);
+            mbar_init(a_empty + s, 1);
+            mbar_init(bc_empty + s, 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(s_full + s, 1);
+            mbar_init(p_full + s, kRowWarps);
+            mbar_init(w_full + s, kRowWarps);
+            mbar_init(x_full + s, 1);
+        }
+        for (int s = 0; s < 4; ++s) mbar_init(staged + s, 4), mbar_init(sent + s, 1);
         mbar_init(o_full, 1);
-        mbar_init(o_free, 4);
-        mbar_init(img_full, D / 32);
-        mbar_init(b_full, STATES ? 8 : 4);
-        mbar_init(x_full, 1);
+        mbar_init(o_free, kRowWarps);
+        mbar_init(x_ready, kRowWarps);
         mbar_init(done, 1);
         fence_mbar_init();
     }
-    if (warp == G::kIssue) tmem_alloc(s_tmem, G::kCols);
-    grid_dependency_wait();
-    grid_dependents_launch();
-
-    // the passes of a segment are neighbours, so that what they share is read once
-    const int kinds = STATES ? p.kinds : p.passes, index = blockIdx.x / kinds, of = blockIdx.x - index * kinds;
-    const int segs = STATES ? p.segs - 1 : p.segs;
-    const int slice = index / segs, b = slice / p.heads, h = slice - b * p.heads;
-    int which = of;
-    if (STATES)
-        while (p.pass[which].kind != of) ++which;  // a pass of that kind
-    const DecayPass &q = p.pass[which];
-    const bool back = q.back;
-    const int seg = index - slice * segs + (STATES && back ? 1 : 0);  // the last one (in time) has no state behind it
-    const int L = decay_length(p, b), rows = decay_rows(p, seg, L), r0 = seg * p.seg;
-    const float rate = decay_rate(p.log_decay, h);
-    if (threadIdx.x <= kRows) pw[threadIdx.x] = expf(rate * (float)threadIdx.x);
+    if (warp == kWarpIssue) tmem_alloc(s_tmem, kCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *s_tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
+    grid_dependency_wait();
+    grid_dependents_launch();
 
-    const bool turned = STATES ? false : q.turned;
-    // STATES: b and c in the order of the kind, not turned
-    const TileMap &map_a = a.a[which], &map_b = STATES && q.turned ? a.c[which] : a.b[which], &map_c = STATES && q.turned ? a.b[which] : a.c[which];
-    const int K = (rows + kRows - 1) / kRows;
-    const int dd = p.d * p.d;
-    const float *from = STATES ? nullptr : p.segs > 1 ? p.states + (((long long)q.kind * p.slices() + slice) * p.segs + seg) * dd
-                                                      : q.state ? q.state + (long long)slice * dd : nullptr;
-    float *to = STATES ? p.states + (((long long)of * p.slices() + slice) * p.segs + seg) * dd
-                       : q.last && seg == (back ? 0 : p.segs - 1) ? q.last + (long long)slice * dd : nullptr;
-    const bool begun = from != nullptr;
-    // chunk k's first row in the segment, its rows; whether X takes it
-    auto first_of = [&](int k) { return (back ? K - 1 - k : k) * kRows; };
-    auto count_of = [&](int k) { return min(kRows, rows - first_of(k)); };
-    auto takes = [&](int k) { return STATES || k + 1 < K || to != nullptr; };
-    unsigned int *error = &g_decay_error;
-    auto slot = [&](int t) { return sm + G::kRing + t % NS * kTile<D>; };
-    auto parity = [](int t) { return (uint32_t)((t / NS) & 1); };
+    Item<STATES> it;
+    auto stage = [&](int g) { return sm + G::kRing + g % NS * G::kStage; };
+    auto around = [](int g) { return (uint32_t)((g / NS) & 1); };  // parity of a stage's barriers
+    auto one = [](int g) { return (uint32_t)(g & 1); };            // of a barrier that each chunk passes,
+    auto two = [](int g) { return (uint32_t)((g >> 1) & 1); };     // and of a pair of barriers
 
-    if (warp == G::kLoad) {
+    if (warp == kWarpLoad) {
         if (lane == 0) {
-            int t = 0;
+            int g = 0;
             bool ok = true;
-            for (int k = 0; k < K && ok; ++k) {
-                const int row = r0 + first_of(k);
-#pragma unroll
-                for (int x = 0; x < PER; ++x, ++t) {
-                    if (t >= NS && !(ok = bwait(empty + t % NS, parity(t - NS), error))) break;
-                    const TileMap &m = PER == 2 ? (x == 0 ? map_b : map_c) : x == 0 ? map_a : x == 1 ? map_b : map_c;
-                    mbar_arrive_expect_tx(full + t % NS, kTile<D>);
-                    load_tile<D, kRows, kRows>(slot(t), m, full + t % NS, row, h, b);
+            for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
+                it.set(a, index);
+                // STATES: b and c in the order of the kind, not turned
+                const bool swap = STATES && it.q->turned;
+                const TileMap &ma = a.a[it.which], &mb = swap ? a.c[it.which] : a.b[it.which], &mc = swap ? a.b[it.which] : a.c[it.which];
+                for (int k = 0; k < it.K; ++k, ++g) {
+                    const int row = it.r0 + it.first(k), st = g % NS;
+                    uint8_t *to = stage(g);
+                    if (!STATES) {
+                        if (g >= NS && !(ok = bwait(a_empty + st, around(g - NS), error))) break;
+                        mbar_arrive_expect_tx(a_full + st, kTile<D>);
+                        load_tile<D, kRows, kRows>(to + G::kA, ma, a_full + st, row, it.h, it.b);
+                    }
+                    if (g >= NS && !(ok = bwait(bc_empty + st, around(g - NS), error))) break;
+                    mbar_arrive_expect_tx(b_full + st, kTile<D>);
+                    load_tile<D, kRows, kRows>(to + G::kB, mb, b_full + st, row, it.h, it.b);
+                    mbar_arrive_expect_tx(c_full + st, kTileC);
+                    tma_load_4d(to + G::kC, &mc.map, c_full + st, kColumns * it.half, row, it.h * mc.by_head, it.b * mc.by_batch);
                 }
             }
-            // the CTA leaves only once its copies have landed
-            for (int x = max(0, t - NS); x < t; ++x) bwait(full + x % NS, parity(x), error);
+            // the CTA leaves only once its copies have landed (after a wait that gave up, a's of a stage may be ahead)
+            for (int x = max(0, g - NS); x < g; ++x) {
+                if (!STATES) bwait(a_full + x % NS, around(x), error);
+                bwait(b_full + x % NS, around(x), error);
+                bwait(c_full + x % NS, around(x), error);
+            }
+            if (!ok && !STATES) bwait(a_full + g % NS, around(g), error);
         }
         __syncwarp();
-    } else if (warp == G::kIssue) {
-        if (lane == 0) {
-            const uint32_t base = smem_u32(sm), lo = base + G::kLo;
-            auto at = [&](int t) { return base + G::kRing + t % NS * kTile<D>; };
-            constexpr uint32_t idS = idesc_bf16_f32(kRows, kRows, false, false), idO = idesc_bf16_f32(kRows, D, false, true);
-            const int steps = (p.d + 15) / 16;
+    } else if (warp == kWarpIssue) {
+        {
+            const uint32_t base = smem_u32(sm);
+            auto at = [&](int g) { return base + G::kRing + g % NS * G::kStage; };
+            constexpr uint32_t idS = idesc_bf16_f32(kRows, kRows, false, false), idO = idesc_bf16_f32(kRows, kColumns, false, true),
+                               idX = idesc_bf16_f32(kRows, 2 * kColumns, true, true);
+            // X += b^T [hi | lo], in 128 columns whose halves are added later.  (With 64 columns of b the product has 128 rows all
+            // the same: the upper ones are made of the tile of c behind b's, and are not read.)
+            auto product_x = [&](int g, bool add) {
+                const uint64_t b = smem_desc_sw128(at(g) + G::kB, kBlock, 1024), w = desc_mn(base + G::kW + (STATES ? (g & 1) * 2 * kTileC : 0));
+#pragma unroll
+                for (int k = 0; k < kRows / 16; ++k) product(tmem + kColX, b + step_mn(k), w + step_mn(k), idX, k > 0 || add ? 1u : 0u);
+            };
+            int g = 0, items = 0, scored = 0;  // scored: chunks whose S has been issued
             bool ok = true;
-            int images = 0;
-            for (int k = 0; k < K && ok; ++k) {
-                const int t = k * PER;
-                const uint32_t par = (uint32_t)(k & 1), before = par ^ 1u;
-                if constexpr (STATES) {
-                    if (!(ok = bwait(full + (t + 1) % NS, parity(t + 1), error) && bwait(b_full, par, error))) break;
-                    tc_fence_after();
-                    product_x<D, G::kHalf>(tmem + G::kColX, at(t), lo, at(t + 1), k > 0);
-                    umma_commit(x_full);
-                    umma_commit(empty + t % NS);
-                    umma_commit(empty + (t + 1) % NS);
-                    continue;
-                }
-                const bool has = begun || k > 0, partial = count_of(k) < kRows;
-                if (!(ok = bwait(full + t % NS, parity(t), error) && bwait(full + (t + 1) % NS, parity(t + 1), error))) break;
-                if (D == 64 && k > 0 && !(ok = bwait(o_free, before, error))) break;
-                tc_fence_after();
-                product_k<D>(tmem + G::kColS, desc_k(at(t)), desc_k(at(t + 1)), idS, steps, [] {});
-                umma_commit(s_full);
-                if (D == 128 && k > 0 && !(ok = bwait(o_free, before, error))) break;
-                if (D == 64 && !(ok = bwait(p_full, par, error))) break;
-                if (has) {
-                    if (!(ok = bwait(img_full, (uint32_t)(images & 1), error))) break;
-                    ++images;
-                    tc_fence_after();
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        umma_bf16(tmem + G::kColBy, desc_k(at(t)) + step_k(s), desc_mn(base + G::kImg) + step_mn(s), idO, s > 0 ? 1u : 0u);
-                }
-                umma_commit(empty + t % NS);
-                if (D == 128 && !(ok = bwait(p_full, par, error))) break;
-                if (!(ok = bwait(full + (t + 2) % NS, parity(t + 2), error))) break;
-                // (rows of c behind the length are zeros by then)
-                if (partial && !(ok = bwait(b_full, par, error))) break;
-                tc_fence_after();
-                product_mn<64, kRows>(tmem + G::kColIn, tmem + G::kColS, desc_mn(at(t + 2)), idO, kRows / 16, false);
-                umma_commit(o_full);
-                if (takes(k)) {
-                    if (!partial && !(ok = bwait(b_full, par, error))) break;
-                    tc_fence_after();
-                    product_x<D, G::kHalf>(tmem + G::kColX, at(t + 1), lo, at(t + 2), has);
-                    umma_commit(x_full);
-                }
-                umma_commit(empty + (t + 1) % NS);
-                umma_commit(empty + (t + 2) % NS);
-            }
-            umma_commit(done);
-            bwait(done, 0u, error);
-        }
-        __syncwarp();
-    } else {
-        const int w4 = warp & 3, row = w4 * 32 + lane;
-        const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
-        if constexpr (STATES) {
-            // both groups: half of the columns each
-            const int half = warp >> 2;
-            bool ok = true;
-            for (int k = 0; k < K && ok; ++k) {
-                const int t = k * PER, first = first_of(k), count = count_of(k);
-                if (!(ok = bwait(full + t % NS, parity(t), error))) break;
-                if (count < kRows && !(ok = bwait(full + (t + 1) % NS, parity(t + 1), error))) break;
-                if (k > 0 && !(ok = bwait(x_full, (uint32_t)((k - 1) & 1), error))) break;
-                const float w = q.s * expf(rate * (float)(back ? first + row + 1 : rows - 1 - first - row));
-                weight_row(slot(t), sm + G::kLo, row, half * D / 16, (half + 1) * D / 16, w, row < count);
-                if (half == 0 && count < kRows) zero_rows<D>(slot(t + 1), row, count, kRows);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_full);
-            }
-            if (ok && K > 0) ok = bwait(x_full, (uint32_t)((K - 1) & 1), error);
-            tc_fence_after();
-            if (ok && w4 * 32 < D) {
-                const int c0 = half * D / 2;
-#pragma unroll
-                for (int c = 0; c < D / 2; c += 32) {
-                    float x[32];
-                    if (K > 0) {
-                        tmem_ld32(tmem + lanes + G::kColX + c0 + c, x);
-                        tmem_ld_wait();
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = 0.f;
-                    }
-                    if (row < p.d) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            if (c0 + c + i < p.d) *reinterpret_cast<float4 *>(to + row * p.d + c0 + c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-                    }
-                }
-            }
-        } else if (warp < 4) {
-            // ------------------------------------------------------------------ rows
-            __nv_bfloat16 *O = (__nv_bfloat16 *)q.o.ptr + b * q.o.sb + h * q.o.sh;
-            bool ok = true;
-            for (int k = 0; k < K && ok; ++k) {
-                const uint32_t par = (uint32_t)(k & 1);
-                const int count = count_of(k);
-                const bool has = begun || k > 0;
-                if (!(ok = bwait(s_full, par, error))) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int j0 = 0; j0 < kRows; j0 += 32) {
-                    uint32_t packed[16];
-                    // blocks on the other side of the diagonal are not read
-                    if (back ? j0 + 31 < w4 * 32 || j0 >= count : j0 > w4 * 32 + 31) {
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) packed[x] = 0u;
-                    } else {
-                        float s[32];
-                        tmem_ld32(tmem + lanes + G::kColS + j0, s);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) {
-                            const int j = j0 + x, far = back ? j - row : row - j;
-                            s[x] = far >= 0 && (!back || j < count) ? s[x] * pw[max(far, 0)] : 0.f;
+            for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
+                it.set(a, index);
+                for (int k = 0; k < it.K && ok; ++k, ++g) {
+                    const int st = g % NS;
+                    if constexpr (STATES) {
+                        if (k == 0) {  // the item before has been read
+                            if (!(ok = all_wait(x_ready, one(items), error))) break;
+                            ++items;
                         }
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) packed[x] = pack2(s[2 * x], s[2 * x + 1]);
-                    }
-                    tmem_st16(tmem + lanes + G::kColS + j0 / 2, packed);
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full);
-                if (!(ok = bwait(o_full, par, error))) break;
-                tc_fence_after();
-                const float f = q.w * pw[back ? max(count - 1 - row, 0) : row + 1];
-                __nv_bfloat16 *to_row = O + (long long)(r0 + first_of(k) + row) * q.o.sn;
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    float in[32];
-                    tmem_ld32(tmem + lanes + G::kColIn + c, in);
-                    if (has) {
-                        float by[32];
-                        tmem_ld32(tmem + lanes + G::kColBy + c, by);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) in[x] = fmaf(f, by[x], q.p * in[x]);
+                        if (!(ok = all_wait(b_full + st, around(g), error) && all_wait(w_full + (g & 1), two(g), error))) break;
+                        tc_fence_after();
+                        product_x(g, k > 0);
+                        commit(x_full + (g & 1));
+                        commit(bc_empty + st);
+                        if (k + 1 == it.K) commit(o_full);
                     } else {
-                        tmem_ld_wait();
+                        const bool partial = it.count(k) < kRows;
+#pragma unroll 1
+                        for (int part = 0; part < 3; ++part) {
+                            // S of this chunk, or, where its tiles have landed, of the next (which may be another item's)
+                            const int sst = scored % NS;
+                            bool score = scored == g;
+                            if (score) {
+                                if (!(ok = all_wait(a_full + sst, around(scored), error) && all_wait(b_full + sst, around(scored), error))) break;
+                            } else {
+                                score = part > 0 && scored == g + 1 && __all_sync(0xffffffffu, mbar_test(a_full + sst, around(scored)) && mbar_test(b_full + sst, around(scored)));
+                            }
+                            if (score) {
+                                tc_fence_after();
+                                const uint64_t ad = desc_k(at(scored) + G::kA), bd = desc_k(at(scored) + G::kB);
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) in[x] *= q.p;
-                    }
-                    if (c + 32 == D) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(o_free);
-                    }
-                    if (row < count) {
+                                for (int s = 0; s < D / 16; ++s) product(tmem + kColS + kRows * (scored & 1), ad + step_k(s), bd + step_k(s), idS, s > 0 ? 1u : 0u);
+                                commit(s_full + (scored & 1));
+                                ++scored;
+                            }
+                            if (part == 0) {
+                                if (!(ok = all_wait(c_full + st, around(g), error))) break;
+                                // (rows of c behind the length are zeros by then)
+                                if (partial && !(ok = all_wait(w_full, one(g), error))) break;
+                                if (g > 0 && !(ok = all_wait(o_free, one(g - 1), error))) break;
+                                if (!(ok = all_wait(p_full + (g & 1), two(g), error))) break;
+                                tc_fence_after();
+                                const uint64_t cd = desc_mn(at(g) + G::kC);
+                                const uint32_t pt = tmem + kColS + kRows * (g & 1);
 #pragma unroll
-                        for (int x = 0; x < 32; x += 8)
-                            if (c + x < p.d)
-                                *reinterpret_cast<uint4 *>(to_row + c + x) =
-                                    make_uint4(pack2(in[x], in[x + 1]), pack2(in[x + 2], in[x + 3]), pack2(in[x + 4], in[x + 5]), pack2(in[x + 6], in[x + 7]));
+                                for (int s = 0; s < kRows / 16; ++s) product_tmem(tmem + kColIn, pt + 32 * (s >> 1) + 8 * (s & 1), cd + step_mn(s), idO, s > 0 ? 1u : 0u);
+                            } else if (part == 1) {
+                                if (!(ok = all_wait(x_ready, one(g), error))) break;
+                                if (it.has(k)) {
+                                    tc_fence_after();
+#pragma unroll
+                                    for (int s = 0; s < D / 16; ++s)
+                                        product(tmem + kColBy, desc_k(at(g) + G::kA) + step_k(s), desc_mn(base + G::kImg) + step_mn(s), idO, s > 0 ? 1u : 0u);
+                                }
+                                commit(o_full);
+                                commit(a_empty + st);
+                            } else {
+                                if (!partial && !(ok = all_wait(w_full, one(g), error))) break;
+                                if (it.takes(k)) {
+                                    tc_fence_after();
+                                    product_x(g, it.has(k));
+                                }
+                                commit(x_full);
+                                commit(bc_empty + st);
+                            }
+                        }
                     }
                 }
             }
-            // rows of the segment from the length on
-            const int end = min(p.seg, p.n - r0), per = p.d / 8;
-            for (int e = threadIdx.x; e < max(end - rows, 0) * per; e += 128)
-                *reinterpret_cast<uint4 *>(O + (long long)(r0 + rows + e / per) * q.o.sn + e % per * 8) = make_uint4(0, 0, 0, 0);
-        } else {
-            // ------------------------------------------------------------------ state
-            const bool mine = w4 * 32 < D;  // the warp has rows of X
-            bool ok = true;
-            for (int k = 0; k < K && ok; ++k) {
-                const int t = k * PER, count = count_of(k);
-                if (k > 0 && !(ok = bwait(x_full, (uint32_t)((k - 1) & 1), error))) break;
-                tc_fence_after();
-                if ((begun || k > 0) && mine) {
-                    const float keep = pw[count];
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float x[32];
-                        if (k > 0) {
-                            tmem_ld32(tmem + lanes + G::kColX + c, x);
-                            tmem_ld_wait();
+            commit(done);
+            all_wait(done, 0u, error);
+        }
+    } else {
+        const int w4 = warp & 3, quarter = warp >> 2, row = w4 * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
+        const uint32_t tX = lanes + kColX + 16 * quarter;
+        const bool mine = w4 * 32 < D;  // the warp has rows of X
+        uint8_t *out = sm + G::kOut;
+        float *pc = reinterpret_cast<float *>(sm + G::kPow) + warp * 32;
+        int g = 0, items = 0;
+        bool ok = true;
+        // this thread's part of X: the sum of its two
+        auto take_x = [&](float *x) {
+            float lo[16];
+            tmem_ld16(tX, x);
+            tmem_ld16(tX + kColumns, lo);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] += lo[i];
+        };
+        for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
+            it.set(a, index);
+            const float rate = decay_rate(p.log_decay, it.h);
+            const int c0 = it.half * kColumns + 16 * quarter;  // this thread's columns of the state
+            // four columns of this thread's row of the state outside (zeros where there is none)
+            auto outside = [&](int c, float *x) {
+                if (!it.from || row >= p.d || c0 + c >= p.d) {
+                    x[0] = x[1] = x[2] = x[3] = 0.f;
+                } else if (it.turned) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = it.from[(c0 + c + i) * p.d + row];
+                } else {
+                    *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(it.from + row * p.d + c0 + c);
+                }
+            };
+            auto arrive = [&](uint64_t *bar) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar);
+            };
+            if constexpr (STATES) {
+                if (it.K > 0) {
+                    tc_fence_before();
+                    arrive(x_ready);  // the item before has been read
+                }
+                for (int k = 0; k < it.K; ++k, ++g) {
+                    const int first = it.first(k), count = it.count(k);
+                    const float w = it.q->s * expf(rate * (float)max(it.back ? first + row + 1 : it.rows - 1 - first - row, 0));
+                    if (!(ok = bwait(c_full + g % NS, around(g), error))) break;
+                    if (g > 1 && !(ok = bwait(x_full + (g & 1), two(g - 2), error))) break;
+                    uint8_t *hi = sm + G::kW + (g & 1) * 2 * kTileC;
+                    weight_row(stage(g) + G::kC, hi, hi + kTileC, row, 2 * quarter, w, row < count);
+                    if (count < kRows) {  // zeros, whatever is there, in the other operand too
+                        if (!(ok = bwait(b_full + g % NS, around(g), error))) break;
+                        if (quarter == 0) zero_rows<D>(stage(g) + G::kB, row, count, kRows);
+                    }
+                    fence_proxy_async_smem();
+                    arrive(w_full + (g & 1));
+                }
+                if (!ok || (it.K > 0 && !(ok = bwait(o_full, one(items), error)))) break;
+                items += it.K > 0;
+            } else {
+                const DecayPass &q = *it.q;
+                // factors of a chunk: of a X~, of X, of this thread's row of c
+                float by_w = 0.f, keep = 0.f, weight = 0.f;
+                int counted = -1;
+                const uint64_t p2 = f32x2(q.p, q.p);
+                // g^(i - j) = g^(i - (j0 + 31)) g^(j0 + 31 - j) (backward: g^(j0 - i) g^(j - j0)), both at most 1, but for the
+                // first on the diagonal: up to g^-31
+                const int j0 = 32 * quarter;
+                const bool diagonal = quarter == w4, steep = rate < -2.f;  // (fp32 ends far behind g^-31 for others)
+                const float pf = expf(rate * (float)(it.back ? j0 - row : row - j0 - 31));
+                const uint32_t on = !diagonal ? 0xffffffffu : it.back ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+                const bool other = it.back ? quarter < w4 : quarter > w4;  // the other side of the diagonal
+                __syncwarp();
+                pc[lane] = expf(rate * (float)(it.back ? lane : 31 - lane));
+                __syncwarp();
+                for (int k = -1; k <= it.K && it.K > 0; ++k) {
+                    if (k > 0) {
+                        // ------------------------------------------------------ o of the chunk before
+                        const int f = g + k - 1, count = it.count(k - 1), at = it.r0 + it.first(k - 1) + w4 * 32;
+                        const uint64_t f2 = f32x2(by_w, by_w);  // (still that chunk's)
+                        if (quarter == 0 && lane == 0 && f > 0) {  // the one before has left `out`
+                            bulk_wait_group_read0();
+                            mbar_arrive(sent + w4);
+                        }
+                        __syncwarp();
+                        if (!(ok = bwait(o_full, one(f), error))) break;
+                        tc_fence_after();
+                        float in[16], by[16];
+                        uint32_t u[8];
+                        tmem_ld16(lanes + kColIn + 16 * quarter, in);
+                        if (it.has(k - 1)) {
+                            tmem_ld16(lanes + kColBy + 16 * quarter, by);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                x[i] = row < p.d && c + i < p.d ? (turned ? from[(c + i) * p.d + row] : from[row * p.d + c + i]) : 0.f;
+                            for (int x = 0; x < 16; ++x) by[x] = 0.f;
                         }
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            *reinterpret_cast<uint4 *>(sm + G::kImg + chunk_at(row, (c + i) / 8)) =
-                                make_uint4(pack2(x[i], x[i + 1]), pack2(x[i + 2], x[i + 3]), pack2(x[i + 4], x[i + 5]), pack2(x[i + 6], x[i + 7]));
-                        if (takes(k)) {
-                            uint32_t y[32];
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(x[i] * keep);
-                            tmem_st32(tmem + lanes + G::kColX + c, y);
-                        }
-                    }
-                    tmem_st_wait();
-                    fence_proxy_async_smem();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(img_full);
-                }
-                if (takes(k)) {
-                    // the tile has landed, and S has read it
-                    if (!(ok = bwait(full + (t + 1) % NS, parity(t + 1), error) && bwait(s_full, (uint32_t)(k & 1), error))) break;
-                    weight_row(slot(t + 1), sm + G::kLo, row, 0, D / 8, q.s * pw[back ? row + 1 : max(count - 1 - row, 0)], row < count);
-                }
-                if (count < kRows) {
-                    if (!(ok = bwait(full + (t + 2) % NS, parity(t + 2), error))) break;
-                    zero_rows<D>(slot(t + 2), row, count, kRows);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_full);
-            }
-            if (to && mine && ok && (K == 0 || (ok = bwait(x_full, (uint32_t)((K - 1) & 1), error)))) {
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float x[32];
-                    if (K > 0) {
-                        tmem_ld32(tmem + lanes + G::kColX + c, x);
                         tmem_ld_wait();
-                    } else {
+                        tc_fence_before();
+                        arrive(o_free);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            x[i] = from && row < p.d && c + i < p.d ? (turned ? from[(c + i) * p.d + row] : from[row * p.d + c + i]) : 0.f;
-                    }
-                    if (row < p.d) {
+                        for (int x = 0; x < 8; ++x) {
+                            float y, z;
+                            f32x2_split(fma_f32x2(f2, f32x2(by[2 * x], by[2 * x + 1]), mul_f32x2(p2, f32x2(in[2 * x], in[2 * x + 1]))), y, z);
+                            u[x] = row < count ? pack2(y, z) : 0u;
+                        }
+                        if (f > 0 && !(ok = bwait(sent + w4, one(f - 1), error))) break;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i < p.d) {
-                                if (turned) to[(c + i) * p.d + row] = x[i];
-                                else to[row * p.d + c + i] = x[i];
+                        for (int x = 0; x < 2; ++x)
+                            *reinterpret_cast<uint4 *>(out + chunk_at(row, 2 * quarter + x)) = make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2], u[4 * x + 3]);
+                        // 32 rows of four warps (those behind the length are zeros; what is not in the tensor is not written)
+                        fence_proxy_async_smem();
+                        arrive(staged + w4);
+                        if (quarter == 0) {
+                            if (!(ok = bwait(staged + w4, one(f), error))) break;
+                            if (lane == 0 && at < p.n) {
+                                const TileMap &m = a.o[it.which];
+                                tma_store_4d(&m.map, out + w4 * 32 * 128, kColumns * it.half, at, it.h * m.by_head, it.b * m.by_batch);
+                                bulk_commit_group();
                             }
+                        }
                     }
+                    if (k >= 0 && k < it.K) {
+                        const int f = g + k, count = it.count(k);
+                        if (count != counted) {
+                            counted = count;
+                            const float up = expf(rate * (float)(row + 1)), down = expf(rate * (float)max(count - 1 - row, 0));
+                            by_w = q.w * (it.back ? down : up), weight = q.s * (it.back ? up : down), keep = expf(rate * (float)count);
+                        }
+                        // ------------------------------------------------------ the state (X of the chunk before is complete,
+                        // and X~ and the weighted rows have been read)
+                        if (f > 0 && !(ok = bwait(x_full, one(f - 1), error))) break;
+                        if (it.has(k) && mine) {
+                            float x[16];
+                            tc_fence_after();
+                            if (k > 0) {
+                                take_x(x);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 16; i += 4) outside(i, x + i);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; i += 8)
+                                *reinterpret_cast<uint4 *>(sm + G::kImg + chunk_at(row, 2 * quarter + i / 8)) =
+                                    make_uint4(pack2(x[i], x[i + 1]), pack2(x[i + 2], x[i + 3]), pack2(x[i + 4], x[i + 5]), pack2(x[i + 6], x[i + 7]));
+                            if (it.takes(k)) {
+                                const uint64_t keep2 = f32x2(keep, keep);
+                                uint32_t y[16];
+#pragma unroll
+                                for (int i = 0; i < 16; i += 2) {
+                                    float y0, y1;
+                                    f32x2_split(mul_f32x2(f32x2(x[i], x[i + 1]), keep2), y0, y1);
+                                    y[i] = __float_as_uint(y0), y[i + 1] = __float_as_uint(y1);
+                                }
+                                tmem_st16(tX, y);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) y[i] = 0u;
+                                tmem_st16(tX + kColumns, y);
+                                tmem_st_wait();
+                            }
+                            fence_proxy_async_smem();
+                        }
+                        tc_fence_before();
+                        arrive(x_ready);
+                        // ------------------------------------------------------ the rows of c
+                        if (!(ok = bwait(c_full + f % NS, around(f), error))) break;
+                        uint8_t *c = stage(f) + G::kC, *hi = sm + G::kW;
+                        if (it.takes(k)) weight_row(c, hi, hi + kTileC, row, 2 * quarter, weight, row < count);
+                        if (count < kRows) {
+                            // zeros, whatever is there, in both operands of X and in that of P c (S may be reading b: what it makes
+                            // of these rows is masked)
+                            if (!(ok = bwait(b_full + f % NS, around(f), error))) break;
+                            if (quarter == 0) zero_rows<D>(stage(f) + G::kB, row, count, kRows);
+                            if (row >= count)
+                                for (int x = 0; x < 2; ++x) *reinterpret_cast<uint4 *>(c + chunk_at(row, 2 * quarter + x)) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        arrive(w_full);
+                    }
+                    if (k + 1 < it.K) {
+                        // ------------------------------------------------------ P of the next chunk
+                        const int f = g + k + 1, count = it.count(k + 1);
+                        const uint32_t tS = lanes + kColS + kRows * (f & 1) + j0;  // P over this warp's own columns
+                        if (!(ok = bwait(s_full + (f & 1), two(f), error))) break;
+                        tc_fence_after();
+                        uint32_t packed[16];
+                        if (other || (it.back && j0 >= count)) {
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) packed[x] = 0u;
+                        } else {
+                            float s[32];
+                            tmem_ld32(tS, s);
+                            const uint64_t f2 = f32x2(pf, pf);
+                            tmem_ld_wait();
+                            if (diagonal && steep) {
+                                const float r2 = it.back ? -rate * kLog2e : rate * kLog2e, at = (float)lane;
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) s[x] *= ex2(r2 * (at - (float)x));
+                            } else {
+#pragma unroll
+                                for (int x = 0; x < 32; x += 4) {
+                                    const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(pc + x);
+                                    f32x2_split(mul_f32x2(f32x2(s[x], s[x + 1]), mul_f32x2(y.x, f2)), s[x], s[x + 1]);
+                                    f32x2_split(mul_f32x2(f32x2(s[x + 2], s[x + 3]), mul_f32x2(y.y, f2)), s[x + 2], s[x + 3]);
+                                }
+                            }
+                            const bool cut = it.back && j0 + 32 > count;
+                            if (diagonal || cut) {
+                                const uint32_t m = cut ? on & (0xffffffffu >> (j0 + 32 - count)) : on;
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) s[x] = m >> x & 1u ? s[x] : 0.f;
+                            }
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) packed[x] = pack2(s[2 * x], s[2 * x + 1]);
+                        }
+                        tmem_st16(tS, packed);
+                        tmem_st_wait();
+                        tc_fence_before();
+                        arrive(p_full + (f & 1));
+                    }
+                }
+                if (!ok) break;
+                g += it.K;
+                // chunks of the segment from the length on
+                __nv_bfloat16 *O = (__nv_bfloat16 *)q.o.ptr + it.b * q.o.sb + it.h * q.o.sh + it.half * kColumns;
+                const int per = min(p.d, kColumns) / 8, left = max(it.end - it.K * kRows, 0) * per;
+                for (int e = threadIdx.x; e < left; e += 32 * kRowWarps)
+                    *reinterpret_cast<uint4 *>(O + (long long)(it.r0 + it.K * kRows + e / per) * q.o.sn + e % per * 8) = make_uint4(0, 0, 0, 0);
+                if (it.to && it.K > 0 && !(ok = bwait(x_full, one(g - 1), error))) break;
+            }
+            if (!it.to || !mine) continue;
+            float x[16];
+            if (it.K > 0) {
+                tc_fence_after();
+                take_x(x);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) outside(i, x + i);
+            }
+            if (row >= p.d) continue;
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                if (c0 + i >= p.d) continue;
+                if (it.turned) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) it.to[(c0 + i + y) * p.d + row] = x[i + y];
+                } else {
+                    *reinterpret_cast<float4 *>(it.to + row * p.d + c0 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                 }
             }
         }
+        if (!STATES && lane == 0) bulk_wait_group0();
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == G::kIssue) tmem_dealloc(tmem, G::kCols);
+    if (warp == kWarpIssue) tmem_dealloc(tmem, kCols);
 }
 
 template <int D, bool STATES>
@@ -431,14 +600,17 @@ cudaError_t launch(const DecayProblem &p, cudaStream_t stream) {
     for (int i = 0; i < p.passes; ++i) {
         const DecayPass &q = p.pass[i];
         if (!make_tile_map(&a.a[i], q.a, p.B, p.heads, p.n, p.d, kRows) || !make_tile_map(&a.b[i], q.b, p.B, p.heads, p.n, p.d, kRows) ||
-            !make_tile_map(&a.c[i], q.c, p.B, p.heads, p.n, p.d, kRows))
+            !make_tile_map(&a.c[i], q.c, p.B, p.heads, p.n, p.d, kRows) || (!STATES && !make_tile_map(&a.o[i], q.o, p.B, p.heads, p.n, p.d, 32)))
             return cudaErrorInvalidValue;
     }
+    const int segs = STATES ? p.segs - 1 : p.segs;
+    a.halves = D / kColumns;
+    a.items = (int)(p.slices() * segs * (STATES ? p.kinds : p.passes) * a.halves);
+    a.by_segs = Divide((uint32_t)segs), a.by_heads = Divide((uint32_t)p.heads);
     static SmemOnce once;
     const cudaError_t e = once(decay_kernel<D, STATES>, Geo<D, STATES>::kSmem);
     if (e != cudaSuccess) return e;
-    const long long ctas = p.slices() * (STATES ? p.segs - 1 : p.segs) * (STATES ? p.kinds : p.passes);
-    return launch_pdl(decay_kernel<D, STATES>, dim3((unsigned)ctas), dim3(Geo<D, STATES>::kThreads), Geo<D, STATES>::kSmem, stream, a);
+    return launch_pdl(decay_kernel<D, STATES>, dim3((unsigned)std::min(a.items, kPlanSMs)), dim3(kThreads), Geo<D, STATES>::kSmem, stream, a);
 }
 
 }  // namespace
