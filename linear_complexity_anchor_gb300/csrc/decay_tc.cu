@@ -16,8 +16,8 @@
 // Sixteen row warps do all that is done by elements, one step after the other, so that four warps of each scheduler run
 // the same instructions (with warps of their own for each step, most of the time went into fetching instructions: at d =
 // 128 a chunk took 3.9 us against 2.65): for chunk k
-//   o of chunk k - 1 from its two products, out by TMA;  X~ and the decay of X;  the weighted rows of c;  P of chunk k + 1
-// a thread a row of each, and a quarter of its columns.  One warp loads tiles by TMA, one issues the products: P c, S of the
+//   o of chunk k - 1 from its two products;  X~ and the decay of X;  the weighted rows of c;  P of chunk k + 1
+// a thread a row of each, and a quarter of its columns.  One warp loads tiles by TMA, one stores o's, one issues the products: P c, S of the
 // next chunk, a X~, X, each as soon as its operands are there; S has two buffers.
 //
 // STATES: the sums of a segment alone, s sum_j g^(rows-1-j) b_j^T c_j: the last product alone, with weights that count from the
@@ -35,7 +35,9 @@ using namespace cross_tc;
 
 constexpr int kColumns = 64;                      // of c, of the state and of o, an item
 constexpr int kTileC = kTile<kColumns>;
-constexpr int kRowWarps = 16, kWarpLoad = 16, kWarpIssue = 17, kThreads = 32 * 18;
+constexpr int kParts = 2;  // threads of a row
+constexpr int kRowWarps = 4 * kParts, kWarpLoad = kRowWarps, kWarpIssue = kWarpLoad + 1, kWarpStore = kWarpLoad + 2, kThreads = 32 * (kWarpLoad + 3);
+constexpr int kSlice = kColumns / kParts;         // columns of o, of the state and of c of a thread, kRows / kParts of P
 constexpr uint32_t kColS = 0, kColIn = 256, kColBy = 320, kColX = 384, kCols = 512;  // of tensor memory; S has two buffers
 
 // D columns of a and b (heads of 16 and 32 are 64)
@@ -44,9 +46,9 @@ struct Geo {
     static constexpr int kStages = STATES ? 3 : D == 128 ? 2 : 3;
     static constexpr int kA = 0, kB = STATES ? 0 : kTile<D>, kC = kB + kTile<D>, kStage = kC + kTileC;  // of a stage
     static constexpr int kWeighted = STATES ? 2 : 1;  // buffers of the weighted rows of c
-    static constexpr int kRing = 0, kW = kRing + kStages * kStage, kImg = kW + kWeighted * 2 * kTileC, kOut = kImg + (STATES ? 0 : D * kColumns * 2);
-    static constexpr int kPow = kOut + (STATES ? 0 : kTileC), kBars = kPow + kRowWarps * 32 * 4;
-    static constexpr int kNBars = 5 * kStages + 20, kSmem = kBars + kNBars * 8 + 8;
+    static constexpr int kRing = 0, kW = kRing + kStages * kStage, kImg = kW + kWeighted * 2 * kTileC, kOut = kImg + (STATES ? 0 : D * kColumns * 2),
+                         kBars = kOut + (STATES ? 0 : kTileC);
+    static constexpr int kNBars = 5 * kStages + 14, kSmem = kBars + kNBars * 8 + 8;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -97,22 +99,23 @@ struct Item {
     }
     // chunk k: its first row in the segment, its rows; whether X takes it; whether there is a state before it
     __device__ __forceinline__ int first(int k) const { return (back ? K - 1 - k : k) * kRows; }
-    __device__ __forceinline__ int count(int k) const { return min(kRows, rows - first(k)); }
+    __device__ __forceinline__ int count(int k) const { return (back ? k == 0 : k + 1 == K) ? rows - (K - 1) * kRows : kRows; }
     __device__ __forceinline__ bool takes(int k) const { return STATES || k + 1 < K || to != nullptr; }
     __device__ __forceinline__ bool has(int k) const { return k > 0 || from != nullptr; }
 };
 
-// Chunks `first` and first + 1 of a row of c times its weight w, as two bf16 numbers in two tiles.  `on`: the row counts (else
+// This thread's columns of a row of c times its weight w, as two bf16 numbers in two tiles.  `on`: the row counts (else
 // zeros, whatever it holds).  With w = u + v in bf16 (2^-18 of w is left out), h = c u rounded, and l = (c u - h) + c v, of
 // which the first part is exact: three instructions for two numbers.
-__device__ __forceinline__ void weight_row(const uint8_t *tile, uint8_t *hi, uint8_t *lo, int row, int first, float w, bool on) {
+__device__ __forceinline__ void weight_row(const uint8_t *tile, uint8_t *hi, uint8_t *lo, int row, int part, float w, bool on) {
+    constexpr int N = kSlice / 8;
     const __nv_bfloat16 u1 = __float2bfloat16_rn(w);
     const __nv_bfloat162 u = __bfloat162bfloat162(u1), v = __float2bfloat162_rn(w - __bfloat162float(u1));
-    uint4 x4[2];
+    uint4 x4[N];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) x4[c] = *reinterpret_cast<const uint4 *>(tile + chunk_at(row, first + c));
+    for (int c = 0; c < N; ++c) x4[c] = on ? *reinterpret_cast<const uint4 *>(tile + chunk_at(row, N * part + c)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < N; ++c) {
         uint4 h4, l4;
         const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&x4[c]);
         __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&h4), *l = reinterpret_cast<__nv_bfloat162 *>(&l4);
@@ -121,9 +124,8 @@ __device__ __forceinline__ void weight_row(const uint8_t *tile, uint8_t *hi, uin
             h[i] = __hmul2(x[i], u);
             l[i] = __hfma2(x[i], v, __hfma2(x[i], u, __hneg2(h[i])));
         }
-        if (!on) h4 = l4 = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(hi + chunk_at(row, first + c)) = h4;
-        *reinterpret_cast<uint4 *>(lo + chunk_at(row, first + c)) = l4;
+        *reinterpret_cast<uint4 *>(hi + chunk_at(row, N * part + c)) = h4;
+        *reinterpret_cast<uint4 *>(lo + chunk_at(row, N * part + c)) = l4;
     }
 }
 
@@ -150,9 +152,22 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
         " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
         : "memory");
 }
-__device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, unsigned int *error) {
-    return __all_sync(0xffffffffu, bwait(bar, parity, error));
+// False once a phase has not come within kTries tries of up to 2 us each (the error word is set on the way out).  In a few
+// instructions: what waits take in the instruction cache is taken from the steps between them.
+constexpr int kTries = 1 << 20;
+__device__ __forceinline__ bool hold(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .s32 i;\n mov.s32 i, %3;\n"
+        "again:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n @p bra over;\n"
+        " sub.s32 i, i, 1;\n setp.gt.s32 q, i, 0;\n @q bra again;\n"
+        "over:\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "n"(kTries)
+        : "memory");
+    return ok != 0;
 }
+__device__ __forceinline__ bool all_hold(uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, hold(bar, parity)); }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t at, float *v) {
     uint32_t r[16];
@@ -163,6 +178,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t at, float *v) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+// kSlice columns
+__device__ __forceinline__ void take(uint32_t at, float *v) {
+    if constexpr (kSlice == 32) tmem_ld32(at, v);
+    else tmem_ld16(at, v);
+}
+__device__ __forceinline__ void give(uint32_t at, const uint32_t *v) {
+    if constexpr (kSlice == 32) tmem_st32(at, v);
+    else tmem_st16(at, v);
+}
 
 template <int D, bool STATES>
 __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constant__ TcParams a) {
@@ -172,13 +196,13 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G::kBars);
     uint64_t *a_full = bars, *b_full = a_full + NS, *c_full = b_full + NS, *a_empty = c_full + NS, *bc_empty = a_empty + NS,
              *s_full = bc_empty + NS /* [2] */, *p_full = s_full + 2 /* [2] */, *w_full = p_full + 2 /* [2] */, *o_full = w_full + 2,
-             *o_free = o_full + 1, *x_ready = o_free + 1, *x_full = x_ready + 1 /* [2] */, *staged = x_full + 2 /* [4] */, *sent = staged + 4 /* [4] */, *done = sent + 4;
+             *o_free = o_full + 1, *x_ready = o_free + 1, *x_full = x_ready + 1 /* [2] */, *staged = x_full + 2, *sent = staged + 1, *done = sent + 1;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + G::kNBars);
     const DecayProblem &p = a.p;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    unsigned int *error = &g_decay_error;
+    auto gave_up = [] { atomicOr(&g_decay_error, 1u); };
     if (smem_u32(sm) & 1023u) {  // (there is no room to move the tiles: never seen)
-        if (threadIdx.x == 0) atomicOr(error, 1u);
+        if (threadIdx.x == 0) gave_up();
         return;
     }
     if (threadIdx.x == 0) {
@@ -195,8 +219,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
             mbar_init(w_full + s, kRowWarps);
             mbar_init(x_full + s, 1);
         }
-        for (int s = 0; s < 4; ++s) mbar_init(staged + s, 4), mbar_init(sent + s, 1);
         mbar_init(o_full, 1);
+        mbar_init(staged, kRowWarps);
+        mbar_init(sent, 1);
         mbar_init(o_free, kRowWarps);
         mbar_init(x_ready, kRowWarps);
         mbar_init(done, 1);
@@ -229,11 +254,11 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     const int row = it.r0 + it.first(k), st = g % NS;
                     uint8_t *to = stage(g);
                     if (!STATES) {
-                        if (g >= NS && !(ok = bwait(a_empty + st, around(g - NS), error))) break;
+                        if (g >= NS && !(ok = hold(a_empty + st, around(g - NS)))) break;
                         mbar_arrive_expect_tx(a_full + st, kTile<D>);
                         load_tile<D, kRows, kRows>(to + G::kA, ma, a_full + st, row, it.h, it.b);
                     }
-                    if (g >= NS && !(ok = bwait(bc_empty + st, around(g - NS), error))) break;
+                    if (g >= NS && !(ok = hold(bc_empty + st, around(g - NS)))) break;
                     mbar_arrive_expect_tx(b_full + st, kTile<D>);
                     load_tile<D, kRows, kRows>(to + G::kB, mb, b_full + st, row, it.h, it.b);
                     mbar_arrive_expect_tx(c_full + st, kTileC);
@@ -241,12 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                 }
             }
             // the CTA leaves only once its copies have landed (after a wait that gave up, a's of a stage may be ahead)
-            for (int x = max(0, g - NS); x < g; ++x) {
-                if (!STATES) bwait(a_full + x % NS, around(x), error);
-                bwait(b_full + x % NS, around(x), error);
-                bwait(c_full + x % NS, around(x), error);
-            }
-            if (!ok && !STATES) bwait(a_full + g % NS, around(g), error);
+            bool landed = ok || STATES || hold(a_full + g % NS, around(g));
+            for (int x = max(0, g - NS); x < g; ++x)
+                landed = (STATES || hold(a_full + x % NS, around(x))) && hold(b_full + x % NS, around(x)) && hold(c_full + x % NS, around(x)) && landed;
+            if (!ok || !landed) gave_up();
         }
         __syncwarp();
     } else if (warp == kWarpIssue) {
@@ -255,12 +278,15 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
             auto at = [&](int g) { return base + G::kRing + g % NS * G::kStage; };
             constexpr uint32_t idS = idesc_bf16_f32(kRows, kRows, false, false), idO = idesc_bf16_f32(kRows, kColumns, false, true),
                                idX = idesc_bf16_f32(kRows, 2 * kColumns, true, true);
-            // X += b^T [hi | lo], in 128 columns whose halves are added later.  (With 64 columns of b the product has 128 rows all
-            // the same: the upper ones are made of the tile of c behind b's, and are not read.)
-            auto product_x = [&](int g, bool add) {
+            // X += b^T [hi | lo], in 128 columns whose halves are added by the rows, which leave the sum in the first: the second begins
+            // anew with each chunk (`add`: of the first).  With 64 columns of b the product has 128 rows all the same: the upper ones
+            // are made of the tile of c behind b's, and are not read.
+            auto product_x = [&](int g, bool add, bool both) {
                 const uint64_t b = smem_desc_sw128(at(g) + G::kB, kBlock, 1024), w = desc_mn(base + G::kW + (STATES ? (g & 1) * 2 * kTileC : 0));
+                product(tmem + kColX, b, w, idO | 1u << 15, add ? 1u : 0u);
+                product(tmem + kColX + kColumns, b, w + kTileC / 16, idO | 1u << 15, both ? 1u : 0u);
 #pragma unroll
-                for (int k = 0; k < kRows / 16; ++k) product(tmem + kColX, b + step_mn(k), w + step_mn(k), idX, k > 0 || add ? 1u : 0u);
+                for (int k = 1; k < kRows / 16; ++k) product(tmem + kColX, b + step_mn(k), w + step_mn(k), idX, 1u);
             };
             int g = 0, items = 0, scored = 0;  // scored: chunks whose S has been issued
             bool ok = true;
@@ -270,12 +296,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     const int st = g % NS;
                     if constexpr (STATES) {
                         if (k == 0) {  // the item before has been read
-                            if (!(ok = all_wait(x_ready, one(items), error))) break;
+                            if (!(ok = all_hold(x_ready, one(items)))) break;
                             ++items;
                         }
-                        if (!(ok = all_wait(b_full + st, around(g), error) && all_wait(w_full + (g & 1), two(g), error))) break;
+                        if (!(ok = all_hold(b_full + st, around(g)) && all_hold(w_full + (g & 1), two(g)))) break;
                         tc_fence_after();
-                        product_x(g, k > 0);
+                        product_x(g, k > 0, k > 0);
                         commit(x_full + (g & 1));
                         commit(bc_empty + st);
                         if (k + 1 == it.K) commit(o_full);
@@ -287,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                             const int sst = scored % NS;
                             bool score = scored == g;
                             if (score) {
-                                if (!(ok = all_wait(a_full + sst, around(scored), error) && all_wait(b_full + sst, around(scored), error))) break;
+                                if (!(ok = all_hold(a_full + sst, around(scored)) && all_hold(b_full + sst, around(scored)))) break;
                             } else {
                                 score = part > 0 && scored == g + 1 && __all_sync(0xffffffffu, mbar_test(a_full + sst, around(scored)) && mbar_test(b_full + sst, around(scored)));
                             }
@@ -300,18 +326,18 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                                 ++scored;
                             }
                             if (part == 0) {
-                                if (!(ok = all_wait(c_full + st, around(g), error))) break;
+                                if (!(ok = all_hold(c_full + st, around(g)))) break;
                                 // (rows of c behind the length are zeros by then)
-                                if (partial && !(ok = all_wait(w_full, one(g), error))) break;
-                                if (g > 0 && !(ok = all_wait(o_free, one(g - 1), error))) break;
-                                if (!(ok = all_wait(p_full + (g & 1), two(g), error))) break;
+                                if (partial && !(ok = all_hold(w_full, one(g)))) break;
+                                if (g > 0 && !(ok = all_hold(o_free, one(g - 1)))) break;
+                                if (!(ok = all_hold(p_full + (g & 1), two(g)))) break;
                                 tc_fence_after();
                                 const uint64_t cd = desc_mn(at(g) + G::kC);
                                 const uint32_t pt = tmem + kColS + kRows * (g & 1);
 #pragma unroll
-                                for (int s = 0; s < kRows / 16; ++s) product_tmem(tmem + kColIn, pt + 32 * (s >> 1) + 8 * (s & 1), cd + step_mn(s), idO, s > 0 ? 1u : 0u);
+                                for (int s = 0; s < kRows / 16; ++s) product_tmem(tmem + kColIn, pt + 16 * s / (kRows / kParts) * (kRows / kParts) + 16 * s % (kRows / kParts) / 2, cd + step_mn(s), idO, s > 0 ? 1u : 0u);
                             } else if (part == 1) {
-                                if (!(ok = all_wait(x_ready, one(g), error))) break;
+                                if (!(ok = all_hold(x_ready, one(g)))) break;
                                 if (it.has(k)) {
                                     tc_fence_after();
 #pragma unroll
@@ -321,10 +347,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                                 commit(o_full);
                                 commit(a_empty + st);
                             } else {
-                                if (!partial && !(ok = all_wait(w_full, one(g), error))) break;
+                                if (!partial && !(ok = all_hold(w_full, one(g)))) break;
                                 if (it.takes(k)) {
                                     tc_fence_after();
-                                    product_x(g, it.has(k));
+                                    product_x(g, it.has(k), false);
                                 }
                                 commit(x_full);
                                 commit(bc_empty + st);
@@ -334,30 +360,48 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                 }
             }
             commit(done);
-            all_wait(done, 0u, error);
+            if (!all_hold(done, 0u) || !ok) gave_up();
         }
+    } else if (warp == kWarpStore) {
+        if (!STATES && lane == 0) {
+            // o of a chunk (rows behind the length are zeros; what is not in the tensor is not written)
+            int g = 0;
+            bool ok = true;
+            for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
+                it.set(a, index);
+                const TileMap &m = a.o[it.which];
+                for (int k = 0; k < it.K; ++k, ++g) {
+                    if (!(ok = hold(staged, one(g)))) break;
+                    tma_store_4d(&m.map, sm + G::kOut, kColumns * it.half, it.r0 + it.first(k), it.h * m.by_head, it.b * m.by_batch);
+                    bulk_commit_group();
+                    bulk_wait_group_read0();
+                    mbar_arrive(sent);
+                }
+            }
+            bulk_wait_group0();
+            if (!ok) gave_up();
+        }
+        __syncwarp();
     } else {
-        const int w4 = warp & 3, quarter = warp >> 2, row = w4 * 32 + lane;
+        const int w4 = warp & 3, part = warp >> 2, row = w4 * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
-        const uint32_t tX = lanes + kColX + 16 * quarter;
+        const uint32_t tX = lanes + kColX + kSlice * part;
         const bool mine = w4 * 32 < D;  // the warp has rows of X
-        uint8_t *out = sm + G::kOut;
-        float *pc = reinterpret_cast<float *>(sm + G::kPow) + warp * 32;
         int g = 0, items = 0;
         bool ok = true;
         // this thread's part of X: the sum of its two
         auto take_x = [&](float *x) {
-            float lo[16];
-            tmem_ld16(tX, x);
-            tmem_ld16(tX + kColumns, lo);
+            float lo[kSlice];
+            take(tX, x);
+            take(tX + kColumns, lo);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] += lo[i];
+            for (int i = 0; i < kSlice; i += 2) f32x2_split(add_f32x2(f32x2(x[i], x[i + 1]), f32x2(lo[i], lo[i + 1])), x[i], x[i + 1]);
         };
         for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
             it.set(a, index);
             const float rate = decay_rate(p.log_decay, it.h);
-            const int c0 = it.half * kColumns + 16 * quarter;  // this thread's columns of the state
+            const int c0 = it.half * kColumns + kSlice * part;  // this thread's columns of the state
             // four columns of this thread's row of the state outside (zeros where there is none)
             auto outside = [&](int c, float *x) {
                 if (!it.from || row >= p.d || c0 + c >= p.d) {
@@ -381,80 +425,70 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                 for (int k = 0; k < it.K; ++k, ++g) {
                     const int first = it.first(k), count = it.count(k);
                     const float w = it.q->s * expf(rate * (float)max(it.back ? first + row + 1 : it.rows - 1 - first - row, 0));
-                    if (!(ok = bwait(c_full + g % NS, around(g), error))) break;
-                    if (g > 1 && !(ok = bwait(x_full + (g & 1), two(g - 2), error))) break;
+                    if (!(ok = hold(c_full + g % NS, around(g)))) break;
+                    if (g > 1 && !(ok = hold(x_full + (g & 1), two(g - 2)))) break;
                     uint8_t *hi = sm + G::kW + (g & 1) * 2 * kTileC;
-                    weight_row(stage(g) + G::kC, hi, hi + kTileC, row, 2 * quarter, w, row < count);
+                    weight_row(stage(g) + G::kC, hi, hi + kTileC, row, part, w, row < count);
                     if (count < kRows) {  // zeros, whatever is there, in the other operand too
-                        if (!(ok = bwait(b_full + g % NS, around(g), error))) break;
-                        if (quarter == 0) zero_rows<D>(stage(g) + G::kB, row, count, kRows);
+                        if (!(ok = hold(b_full + g % NS, around(g)))) break;
+                        if (part == 0) zero_rows<D>(stage(g) + G::kB, row, count, kRows);
                     }
                     fence_proxy_async_smem();
                     arrive(w_full + (g & 1));
                 }
-                if (!ok || (it.K > 0 && !(ok = bwait(o_full, one(items), error)))) break;
+                if (!ok || (it.K > 0 && !(ok = hold(o_full, one(items))))) break;
                 items += it.K > 0;
             } else {
                 const DecayPass &q = *it.q;
                 // factors of a chunk: of a X~, of X, of this thread's row of c
                 float by_w = 0.f, keep = 0.f, weight = 0.f;
                 int counted = -1;
-                const uint64_t p2 = f32x2(q.p, q.p);
-                // g^(i - j) = g^(i - (j0 + 31)) g^(j0 + 31 - j) (backward: g^(j0 - i) g^(j - j0)), both at most 1, but for the
-                // first on the diagonal: up to g^-31
-                const int j0 = 32 * quarter;
-                const bool diagonal = quarter == w4, steep = rate < -2.f;  // (fp32 ends far behind g^-31 for others)
-                const float pf = expf(rate * (float)(it.back ? j0 - row : row - j0 - 31));
-                const uint32_t on = !diagonal ? 0xffffffffu : it.back ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
-                const bool other = it.back ? quarter < w4 : quarter > w4;  // the other side of the diagonal
-                __syncwarp();
-                pc[lane] = expf(rate * (float)(it.back ? lane : 31 - lane));
-                __syncwarp();
+                // P's factors for this thread's columns, p g^(i - j) (backward g^(j - i)), 0 on the other side of the diagonal
+                constexpr int kP = kRows / kParts;
+                const int j0 = kP * part;
+                const float rate2 = rate * kLog2e;
+                uint64_t pf[kP / 2];
+#pragma unroll
+                for (int x = 0; x < kP; x += 2) {
+                    const int far = it.back ? j0 + x - row : row - j0 - x, then = it.back ? far + 1 : far - 1;
+                    pf[x / 2] = f32x2(far >= 0 ? q.p * ex2(rate2 * (float)far) : 0.f, then >= 0 ? q.p * ex2(rate2 * (float)then) : 0.f);
+                }
+                __nv_bfloat16 *O = (__nv_bfloat16 *)q.o.ptr + it.b * q.o.sb + it.h * q.o.sh + it.r0 * q.o.sn + it.half * kColumns;
                 for (int k = -1; k <= it.K && it.K > 0; ++k) {
                     if (k > 0) {
                         // ------------------------------------------------------ o of the chunk before
-                        const int f = g + k - 1, count = it.count(k - 1), at = it.r0 + it.first(k - 1) + w4 * 32;
+                        const int f = g + k - 1, count = it.count(k - 1);
                         const uint64_t f2 = f32x2(by_w, by_w);  // (still that chunk's)
-                        if (quarter == 0 && lane == 0 && f > 0) {  // the one before has left `out`
-                            bulk_wait_group_read0();
-                            mbar_arrive(sent + w4);
-                        }
-                        __syncwarp();
-                        if (!(ok = bwait(o_full, one(f), error))) break;
+                        if (!(ok = hold(o_full, one(f)))) break;
                         tc_fence_after();
-                        float in[16], by[16];
-                        uint32_t u[8];
-                        tmem_ld16(lanes + kColIn + 16 * quarter, in);
+                        float in[kSlice], by[kSlice];
+                        uint32_t u[kSlice / 2];
+                        take(lanes + kColIn + kSlice * part, in);
                         if (it.has(k - 1)) {
-                            tmem_ld16(lanes + kColBy + 16 * quarter, by);
+                            take(lanes + kColBy + kSlice * part, by);
                         } else {
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) by[x] = 0.f;
+                            for (int x = 0; x < kSlice; ++x) by[x] = 0.f;
                         }
                         tmem_ld_wait();
                         tc_fence_before();
                         arrive(o_free);
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) {
+                        for (int x = 0; x < kSlice / 2; ++x) {
                             float y, z;
-                            f32x2_split(fma_f32x2(f2, f32x2(by[2 * x], by[2 * x + 1]), mul_f32x2(p2, f32x2(in[2 * x], in[2 * x + 1]))), y, z);
-                            u[x] = row < count ? pack2(y, z) : 0u;
+                            f32x2_split(fma_f32x2(f2, f32x2(by[2 * x], by[2 * x + 1]), f32x2(in[2 * x], in[2 * x + 1])), y, z);
+                            u[x] = pack2(y, z);
                         }
-                        if (f > 0 && !(ok = bwait(sent + w4, one(f - 1), error))) break;
+                        if (row >= count) {
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            *reinterpret_cast<uint4 *>(out + chunk_at(row, 2 * quarter + x)) = make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2], u[4 * x + 3]);
-                        // 32 rows of four warps (those behind the length are zeros; what is not in the tensor is not written)
-                        fence_proxy_async_smem();
-                        arrive(staged + w4);
-                        if (quarter == 0) {
-                            if (!(ok = bwait(staged + w4, one(f), error))) break;
-                            if (lane == 0 && at < p.n) {
-                                const TileMap &m = a.o[it.which];
-                                tma_store_4d(&m.map, out + w4 * 32 * 128, kColumns * it.half, at, it.h * m.by_head, it.b * m.by_batch);
-                                bulk_commit_group();
-                            }
+                            for (int x = 0; x < kSlice / 2; ++x) u[x] = 0u;
                         }
+                        if (f > 0 && !(ok = hold(sent, one(f - 1)))) break;  // the chunk before has left `out`
+#pragma unroll
+                        for (int x = 0; x < kSlice / 8; ++x)
+                            *reinterpret_cast<uint4 *>(sm + G::kOut + chunk_at(row, kSlice / 8 * part + x)) = make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2], u[4 * x + 3]);
+                        fence_proxy_async_smem();
+                        arrive(staged);
                     }
                     if (k >= 0 && k < it.K) {
                         const int f = g + k, count = it.count(k);
@@ -465,33 +499,30 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                         }
                         // ------------------------------------------------------ the state (X of the chunk before is complete,
                         // and X~ and the weighted rows have been read)
-                        if (f > 0 && !(ok = bwait(x_full, one(f - 1), error))) break;
+                        if (f > 0 && !(ok = hold(x_full, one(f - 1)))) break;
                         if (it.has(k) && mine) {
-                            float x[16];
+                            float x[kSlice];
                             tc_fence_after();
                             if (k > 0) {
                                 take_x(x);
                             } else {
 #pragma unroll
-                                for (int i = 0; i < 16; i += 4) outside(i, x + i);
+                                for (int i = 0; i < kSlice; i += 4) outside(i, x + i);
                             }
 #pragma unroll
-                            for (int i = 0; i < 16; i += 8)
-                                *reinterpret_cast<uint4 *>(sm + G::kImg + chunk_at(row, 2 * quarter + i / 8)) =
+                            for (int i = 0; i < kSlice; i += 8)
+                                *reinterpret_cast<uint4 *>(sm + G::kImg + chunk_at(row, kSlice / 8 * part + i / 8)) =
                                     make_uint4(pack2(x[i], x[i + 1]), pack2(x[i + 2], x[i + 3]), pack2(x[i + 4], x[i + 5]), pack2(x[i + 6], x[i + 7]));
                             if (it.takes(k)) {
                                 const uint64_t keep2 = f32x2(keep, keep);
-                                uint32_t y[16];
+                                uint32_t y[kSlice];
 #pragma unroll
-                                for (int i = 0; i < 16; i += 2) {
+                                for (int i = 0; i < kSlice; i += 2) {
                                     float y0, y1;
                                     f32x2_split(mul_f32x2(f32x2(x[i], x[i + 1]), keep2), y0, y1);
                                     y[i] = __float_as_uint(y0), y[i + 1] = __float_as_uint(y1);
                                 }
-                                tmem_st16(tX, y);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) y[i] = 0u;
-                                tmem_st16(tX + kColumns, y);
+                                give(tX, y);
                                 tmem_st_wait();
                             }
                             fence_proxy_async_smem();
@@ -499,16 +530,16 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                         tc_fence_before();
                         arrive(x_ready);
                         // ------------------------------------------------------ the rows of c
-                        if (!(ok = bwait(c_full + f % NS, around(f), error))) break;
+                        if (!(ok = hold(c_full + f % NS, around(f)))) break;
                         uint8_t *c = stage(f) + G::kC, *hi = sm + G::kW;
-                        if (it.takes(k)) weight_row(c, hi, hi + kTileC, row, 2 * quarter, weight, row < count);
+                        if (it.takes(k)) weight_row(c, hi, hi + kTileC, row, part, weight, row < count);
                         if (count < kRows) {
                             // zeros, whatever is there, in both operands of X and in that of P c (S may be reading b: what it makes
                             // of these rows is masked)
-                            if (!(ok = bwait(b_full + f % NS, around(f), error))) break;
-                            if (quarter == 0) zero_rows<D>(stage(f) + G::kB, row, count, kRows);
+                            if (!(ok = hold(b_full + f % NS, around(f)))) break;
+                            if (part == 0) zero_rows<D>(stage(f) + G::kB, row, count, kRows);
                             if (row >= count)
-                                for (int x = 0; x < 2; ++x) *reinterpret_cast<uint4 *>(c + chunk_at(row, 2 * quarter + x)) = make_uint4(0, 0, 0, 0);
+                                for (int x = 0; x < kSlice / 8; ++x) *reinterpret_cast<uint4 *>(c + chunk_at(row, kSlice / 8 * part + x)) = make_uint4(0, 0, 0, 0);
                         }
                         fence_proxy_async_smem();
                         arrive(w_full);
@@ -517,39 +548,33 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                         // ------------------------------------------------------ P of the next chunk
                         const int f = g + k + 1, count = it.count(k + 1);
                         const uint32_t tS = lanes + kColS + kRows * (f & 1) + j0;  // P over this warp's own columns
-                        if (!(ok = bwait(s_full + (f & 1), two(f), error))) break;
+                        if (!(ok = hold(s_full + (f & 1), two(f)))) break;
                         tc_fence_after();
-                        uint32_t packed[16];
-                        if (other || (it.back && j0 >= count)) {
+                        uint32_t packed[kP / 2];
+                        if (it.back ? j0 + kP <= w4 * 32 || j0 >= count : j0 > w4 * 32 + 31) {
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) packed[x] = 0u;
+                            for (int x = 0; x < kP / 2; ++x) packed[x] = 0u;
                         } else {
-                            float s[32];
-                            tmem_ld32(tS, s);
-                            const uint64_t f2 = f32x2(pf, pf);
-                            tmem_ld_wait();
-                            if (diagonal && steep) {
-                                const float r2 = it.back ? -rate * kLog2e : rate * kLog2e, at = (float)lane;
 #pragma unroll
-                                for (int x = 0; x < 32; ++x) s[x] *= ex2(r2 * (at - (float)x));
-                            } else {
+                            for (int y = 0; y < kP; y += 32) {
+                                float s[32];
+                                tmem_ld32(tS + y, s);
+                                tmem_ld_wait();
+                                if (j0 + y + 32 > count) {  // (0 times what is there may be a NaN)
 #pragma unroll
-                                for (int x = 0; x < 32; x += 4) {
-                                    const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(pc + x);
-                                    f32x2_split(mul_f32x2(f32x2(s[x], s[x + 1]), mul_f32x2(y.x, f2)), s[x], s[x + 1]);
-                                    f32x2_split(mul_f32x2(f32x2(s[x + 2], s[x + 3]), mul_f32x2(y.y, f2)), s[x + 2], s[x + 3]);
+                                    for (int x = 0; x < 32; ++x)
+                                        if (j0 + y + x >= count) s[x] = 0.f;
+                                }
+#pragma unroll
+                                for (int x = 0; x < 16; ++x) {
+                                    float s0, s1;
+                                    f32x2_split(mul_f32x2(f32x2(s[2 * x], s[2 * x + 1]), pf[(y + 2 * x) / 2]), s0, s1);
+                                    packed[y / 2 + x] = pack2(s0, s1);
                                 }
                             }
-                            const bool cut = it.back && j0 + 32 > count;
-                            if (diagonal || cut) {
-                                const uint32_t m = cut ? on & (0xffffffffu >> (j0 + 32 - count)) : on;
-#pragma unroll
-                                for (int x = 0; x < 32; ++x) s[x] = m >> x & 1u ? s[x] : 0.f;
-                            }
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) packed[x] = pack2(s[2 * x], s[2 * x + 1]);
                         }
-                        tmem_st16(tS, packed);
+                        if constexpr (kP == 64) tmem_st32(tS, packed);
+                        else tmem_st16(tS, packed);
                         tmem_st_wait();
                         tc_fence_before();
                         arrive(p_full + (f & 1));
@@ -558,24 +583,23 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                 if (!ok) break;
                 g += it.K;
                 // chunks of the segment from the length on
-                __nv_bfloat16 *O = (__nv_bfloat16 *)q.o.ptr + it.b * q.o.sb + it.h * q.o.sh + it.half * kColumns;
                 const int per = min(p.d, kColumns) / 8, left = max(it.end - it.K * kRows, 0) * per;
                 for (int e = threadIdx.x; e < left; e += 32 * kRowWarps)
-                    *reinterpret_cast<uint4 *>(O + (long long)(it.r0 + it.K * kRows + e / per) * q.o.sn + e % per * 8) = make_uint4(0, 0, 0, 0);
-                if (it.to && it.K > 0 && !(ok = bwait(x_full, one(g - 1), error))) break;
+                    *reinterpret_cast<uint4 *>(O + (long long)(it.K * kRows + e / per) * q.o.sn + e % per * 8) = make_uint4(0, 0, 0, 0);
+                if (it.to && it.K > 0 && !(ok = hold(x_full, one(g - 1)))) break;
             }
             if (!it.to || !mine) continue;
-            float x[16];
+            float x[kSlice];
             if (it.K > 0) {
                 tc_fence_after();
                 take_x(x);
             } else {
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) outside(i, x + i);
+                for (int i = 0; i < kSlice; i += 4) outside(i, x + i);
             }
             if (row >= p.d) continue;
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
+            for (int i = 0; i < kSlice; i += 4) {
                 if (c0 + i >= p.d) continue;
                 if (it.turned) {
 #pragma unroll
@@ -585,8 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                 }
             }
         }
-        if (!STATES && lane == 0) bulk_wait_group0();
-        __syncwarp();
+        if (!ok) gave_up();
     }
     tc_fence_before();
     __syncthreads();
@@ -600,7 +623,7 @@ cudaError_t launch(const DecayProblem &p, cudaStream_t stream) {
     for (int i = 0; i < p.passes; ++i) {
         const DecayPass &q = p.pass[i];
         if (!make_tile_map(&a.a[i], q.a, p.B, p.heads, p.n, p.d, kRows) || !make_tile_map(&a.b[i], q.b, p.B, p.heads, p.n, p.d, kRows) ||
-            !make_tile_map(&a.c[i], q.c, p.B, p.heads, p.n, p.d, kRows) || (!STATES && !make_tile_map(&a.o[i], q.o, p.B, p.heads, p.n, p.d, 32)))
+            !make_tile_map(&a.c[i], q.c, p.B, p.heads, p.n, p.d, kRows) || (!STATES && !make_tile_map(&a.o[i], q.o, p.B, p.heads, p.n, p.d, kRows)))
             return cudaErrorInvalidValue;
     }
     const int segs = STATES ? p.segs - 1 : p.segs;
