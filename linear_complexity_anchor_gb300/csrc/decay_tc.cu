@@ -13,12 +13,11 @@
 // result, and its own rounding in X~ stays the only one of the part of o that goes by it.  With one number o
 // would carry three roundings there, 1.7 times a lone one, against 1.4.
 //
-// Sixteen row warps do all that is done by elements, one step after the other, so that four warps of each scheduler run
-// the same instructions (with warps of their own for each step, most of the time went into fetching instructions: at d =
-// 128 a chunk took 3.9 us against 2.65): for chunk k
-//   o of chunk k - 1 from its two products;  X~ and the decay of X;  the weighted rows of c;  P of chunk k + 1
-// a thread a row of each, and a quarter of its columns.  One warp loads tiles by TMA, one stores o's, one issues the products: P c, S of the
-// next chunk, a X~, X, each as soon as its operands are there; S has two buffers.
+// Two groups of eight warps, a thread half of a row: the first makes P of the next chunk, and o from its two products; the
+// second X~ and the decay of X, and the weighted rows of c.  What a chunk takes is the second's round, X, X~, weights, X; all
+// else is done beside it.  (One group for all, one step after the other: 1.7 us a chunk against XXX.  A group for each of
+// the four steps: 3.9, most of it spent on fetching instructions.)  One warp loads tiles by TMA, one stores o's, one issues
+// the products: P c, S of the next chunk, a X~, X, each as soon as its operands are there; S has two buffers.
 //
 // STATES: the sums of a segment alone, s sum_j g^(rows-1-j) b_j^T c_j: the last product alone, with weights that count from the
 // segment's end, so that X needs no decay on the way.
@@ -35,9 +34,12 @@ using namespace cross_tc;
 
 constexpr int kColumns = 64;                      // of c, of the state and of o, an item
 constexpr int kTileC = kTile<kColumns>;
-constexpr int kParts = 2;  // threads of a row
-constexpr int kRowWarps = 4 * kParts, kWarpLoad = kRowWarps, kWarpIssue = kWarpLoad + 1, kWarpStore = kWarpLoad + 2, kThreads = 32 * (kWarpLoad + 3);
+constexpr int kParts = 2;                         // threads of a row
+constexpr int kGroup = 4 * kParts;                // warps of a group
+constexpr int kWarpState = kGroup, kWarpLoad = 2 * kGroup, kWarpIssue = kWarpLoad + 1, kWarpStore = kWarpLoad + 2, kThreads = 32 * (kWarpLoad + 4);
 constexpr int kSlice = kColumns / kParts;         // columns of o, of the state and of c of a thread, kRows / kParts of P
+// Registers of a thread: 640 threads have 96 at launch, 1920 for a lane of each; 8 * 128 + 8 * 88 + 4 * 40 = 1888.
+constexpr int kRegsRows = 128, kRegsState = 88, kRegsOthers = 40;
 constexpr uint32_t kColS = 0, kColIn = 256, kColBy = 320, kColX = 384, kCols = 512;  // of tensor memory; S has two buffers
 
 // D columns of a and b (heads of 16 and 32 are 64)
@@ -48,7 +50,7 @@ struct Geo {
     static constexpr int kWeighted = STATES ? 2 : 1;  // buffers of the weighted rows of c
     static constexpr int kRing = 0, kW = kRing + kStages * kStage, kImg = kW + kWeighted * 2 * kTileC, kOut = kImg + (STATES ? 0 : D * kColumns * 2),
                          kBars = kOut + (STATES ? 0 : kTileC);
-    static constexpr int kNBars = 5 * kStages + 14, kSmem = kBars + kNBars * 8 + 8;
+    static constexpr int kNBars = 2 * kStages + 12, kSmem = kBars + kNBars * 8 + 8;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -178,25 +180,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t at, float *v) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-// kSlice columns
-__device__ __forceinline__ void take(uint32_t at, float *v) {
-    if constexpr (kSlice == 32) tmem_ld32(at, v);
-    else tmem_ld16(at, v);
-}
-__device__ __forceinline__ void give(uint32_t at, const uint32_t *v) {
-    if constexpr (kSlice == 32) tmem_st32(at, v);
-    else tmem_st16(at, v);
-}
-
 template <int D, bool STATES>
 __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constant__ TcParams a) {
     using G = Geo<D, STATES>;
     constexpr int NS = G::kStages;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G::kBars);
-    uint64_t *a_full = bars, *b_full = a_full + NS, *c_full = b_full + NS, *a_empty = c_full + NS, *bc_empty = a_empty + NS,
-             *s_full = bc_empty + NS /* [2] */, *p_full = s_full + 2 /* [2] */, *w_full = p_full + 2 /* [2] */, *o_full = w_full + 2,
-             *o_free = o_full + 1, *x_ready = o_free + 1, *x_full = x_ready + 1 /* [2] */, *staged = x_full + 2, *sent = staged + 1, *done = sent + 1;
+    // full: a stage's tiles have landed; over: the products of its chunk are complete; p_ready: P is there and the o before has
+    // been read; x_ready: so are X~, X and the weighted rows; x_full: X is complete
+    uint64_t *full = bars, *over = full + NS, *s_full = over + NS /* [2] */, *p_ready = s_full + 2, *x_ready = p_ready + 1 /* [2] */,
+             *x_full = x_ready + 2 /* [2] */, *x_read = x_full + 2, *staged = x_read + 1, *sent = staged + 1, *done = sent + 1;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + G::kNBars);
     const DecayProblem &p = a.p;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -206,24 +199,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
         return;
     }
     if (threadIdx.x == 0) {
-        for (int s = 0; s < NS; ++s) {
-            mbar_init(a_full + s, 1);
-            mbar_init(b_full + s, 1);
-            mbar_init(c_full + s, 1);
-            mbar_init(a_empty + s, 1);
-            mbar_init(bc_empty + s, 1);
-        }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(s_full + s, 1);
-            mbar_init(p_full + s, kRowWarps);
-            mbar_init(w_full + s, kRowWarps);
-            mbar_init(x_full + s, 1);
-        }
-        mbar_init(o_full, 1);
-        mbar_init(staged, kRowWarps);
+        for (int s = 0; s < NS; ++s) mbar_init(full + s, 1), mbar_init(over + s, 1);
+        for (int s = 0; s < 2; ++s) mbar_init(s_full + s, 1), mbar_init(x_ready + s, kGroup), mbar_init(x_full + s, 1);
+        mbar_init(p_ready, kGroup);
+        mbar_init(x_read, kGroup);
+        mbar_init(staged, kGroup);
         mbar_init(sent, 1);
-        mbar_init(o_free, kRowWarps);
-        mbar_init(x_ready, kRowWarps);
         mbar_init(done, 1);
         fence_mbar_init();
     }
@@ -237,10 +218,15 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
 
     Item<STATES> it;
     auto stage = [&](int g) { return sm + G::kRing + g % NS * G::kStage; };
+    auto arrive = [&](uint64_t *bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
     auto around = [](int g) { return (uint32_t)((g / NS) & 1); };  // parity of a stage's barriers
     auto one = [](int g) { return (uint32_t)(g & 1); };            // of a barrier that each chunk passes,
     auto two = [](int g) { return (uint32_t)((g >> 1) & 1); };     // and of a pair of barriers
 
+    if (!STATES && warp >= kWarpLoad) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOthers));
     if (warp == kWarpLoad) {
         if (lane == 0) {
             int g = 0;
@@ -253,23 +239,16 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                 for (int k = 0; k < it.K; ++k, ++g) {
                     const int row = it.r0 + it.first(k), st = g % NS;
                     uint8_t *to = stage(g);
-                    if (!STATES) {
-                        if (g >= NS && !(ok = hold(a_empty + st, around(g - NS)))) break;
-                        mbar_arrive_expect_tx(a_full + st, kTile<D>);
-                        load_tile<D, kRows, kRows>(to + G::kA, ma, a_full + st, row, it.h, it.b);
-                    }
-                    if (g >= NS && !(ok = hold(bc_empty + st, around(g - NS)))) break;
-                    mbar_arrive_expect_tx(b_full + st, kTile<D>);
-                    load_tile<D, kRows, kRows>(to + G::kB, mb, b_full + st, row, it.h, it.b);
-                    mbar_arrive_expect_tx(c_full + st, kTileC);
-                    tma_load_4d(to + G::kC, &mc.map, c_full + st, kColumns * it.half, row, it.h * mc.by_head, it.b * mc.by_batch);
+                    if (g >= NS && !(ok = hold(over + st, around(g - NS)))) break;
+                    mbar_arrive_expect_tx(full + st, G::kStage);
+                    if (!STATES) load_tile<D, kRows, kRows>(to + G::kA, ma, full + st, row, it.h, it.b);
+                    load_tile<D, kRows, kRows>(to + G::kB, mb, full + st, row, it.h, it.b);
+                    tma_load_4d(to + G::kC, &mc.map, full + st, kColumns * it.half, row, it.h * mc.by_head, it.b * mc.by_batch);
                 }
             }
-            // the CTA leaves only once its copies have landed (after a wait that gave up, a's of a stage may be ahead)
-            bool landed = ok || STATES || hold(a_full + g % NS, around(g));
-            for (int x = max(0, g - NS); x < g; ++x)
-                landed = (STATES || hold(a_full + x % NS, around(x))) && hold(b_full + x % NS, around(x)) && hold(c_full + x % NS, around(x)) && landed;
-            if (!ok || !landed) gave_up();
+            // the CTA leaves only once its copies have landed
+            for (int x = max(0, g - NS); x < g; ++x) ok = hold(full + x % NS, around(x)) && ok;
+            if (!ok) gave_up();
         }
         __syncwarp();
     } else if (warp == kWarpIssue) {
@@ -296,26 +275,25 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     const int st = g % NS;
                     if constexpr (STATES) {
                         if (k == 0) {  // the item before has been read
-                            if (!(ok = all_hold(x_ready, one(items)))) break;
+                            if (!(ok = all_hold(x_read, one(items)))) break;
                             ++items;
                         }
-                        if (!(ok = all_hold(b_full + st, around(g)) && all_hold(w_full + (g & 1), two(g)))) break;
+                        if (!(ok = all_hold(x_ready + (g & 1), two(g)))) break;
                         tc_fence_after();
                         product_x(g, k > 0, k > 0);
                         commit(x_full + (g & 1));
-                        commit(bc_empty + st);
-                        if (k + 1 == it.K) commit(o_full);
+                        commit(over + st);
+                        if (k + 1 == it.K) commit(s_full);
                     } else {
                         const bool partial = it.count(k) < kRows;
 #pragma unroll 1
-                        for (int part = 0; part < 3; ++part) {
+                        for (int part = 0; part < 2; ++part) {
                             // S of this chunk, or, where its tiles have landed, of the next (which may be another item's)
-                            const int sst = scored % NS;
                             bool score = scored == g;
                             if (score) {
-                                if (!(ok = all_hold(a_full + sst, around(scored)) && all_hold(b_full + sst, around(scored)))) break;
+                                if (!(ok = all_hold(full + scored % NS, around(scored)))) break;
                             } else {
-                                score = part > 0 && scored == g + 1 && __all_sync(0xffffffffu, mbar_test(a_full + sst, around(scored)) && mbar_test(b_full + sst, around(scored)));
+                                score = part > 0 && scored == g + 1 && __all_sync(0xffffffffu, mbar_test(full + scored % NS, around(scored)));
                             }
                             if (score) {
                                 tc_fence_after();
@@ -326,34 +304,27 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                                 ++scored;
                             }
                             if (part == 0) {
-                                if (!(ok = all_hold(c_full + st, around(g)))) break;
                                 // (rows of c behind the length are zeros by then)
-                                if (partial && !(ok = all_hold(w_full, one(g)))) break;
-                                if (g > 0 && !(ok = all_hold(o_free, one(g - 1)))) break;
-                                if (!(ok = all_hold(p_full + (g & 1), two(g)))) break;
+                                if (partial && !(ok = all_hold(x_ready, one(g)))) break;
+                                if (!(ok = all_hold(p_ready, one(g)))) break;
                                 tc_fence_after();
                                 const uint64_t cd = desc_mn(at(g) + G::kC);
                                 const uint32_t pt = tmem + kColS + kRows * (g & 1);
+                                constexpr int kP = kRows / kParts;  // columns of S that a thread has, with its P at their start
 #pragma unroll
-                                for (int s = 0; s < kRows / 16; ++s) product_tmem(tmem + kColIn, pt + 16 * s / (kRows / kParts) * (kRows / kParts) + 16 * s % (kRows / kParts) / 2, cd + step_mn(s), idO, s > 0 ? 1u : 0u);
-                            } else if (part == 1) {
-                                if (!(ok = all_hold(x_ready, one(g)))) break;
+                                for (int s = 0; s < kRows / 16; ++s)
+                                    product_tmem(tmem + kColIn, pt + 16 * s / kP * kP + 16 * s % kP / 2, cd + step_mn(s), idO, s > 0 ? 1u : 0u);
+                            } else {
+                                if (!partial && !(ok = all_hold(x_ready, one(g)))) break;
+                                tc_fence_after();
+                                if (it.takes(k)) product_x(g, it.has(k), false);
+                                commit(x_full);
                                 if (it.has(k)) {
-                                    tc_fence_after();
 #pragma unroll
                                     for (int s = 0; s < D / 16; ++s)
                                         product(tmem + kColBy, desc_k(at(g) + G::kA) + step_k(s), desc_mn(base + G::kImg) + step_mn(s), idO, s > 0 ? 1u : 0u);
                                 }
-                                commit(o_full);
-                                commit(a_empty + st);
-                            } else {
-                                if (!partial && !(ok = all_hold(w_full, one(g)))) break;
-                                if (it.takes(k)) {
-                                    tc_fence_after();
-                                    product_x(g, it.has(k), false);
-                                }
-                                commit(x_full);
-                                commit(bc_empty + st);
+                                commit(over + st);
                             }
                         }
                     }
@@ -382,21 +353,22 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
             if (!ok) gave_up();
         }
         __syncwarp();
-    } else {
-        const int w4 = warp & 3, part = warp >> 2, row = w4 * 32 + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
-        const uint32_t tX = lanes + kColX + kSlice * part;
+    } else if (warp >= kWarpState && warp < kWarpLoad) {
+        // ---------------------------------------------------------------------- the state, and the weighted rows of c
+        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsState));
+        const int w4 = warp & 3, part = (warp - kWarpState) >> 2, row = w4 * 32 + lane;
+        const uint32_t tX = tmem + ((uint32_t)(w4 * 32) << 16) + kColX + kSlice * part;
         const bool mine = w4 * 32 < D;  // the warp has rows of X
         int g = 0, items = 0;
         bool ok = true;
-        // this thread's part of X: the sum of its two
-        auto take_x = [&](float *x) {
-            float lo[kSlice];
-            take(tX, x);
-            take(tX + kColumns, lo);
+        // 16 columns of this thread's part of X: the sum of its two
+        auto take_x = [&](int c, float *x) {
+            float lo[16];
+            tmem_ld16(tX + c, x);
+            tmem_ld16(tX + c + kColumns, lo);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < kSlice; i += 2) f32x2_split(add_f32x2(f32x2(x[i], x[i + 1]), f32x2(lo[i], lo[i + 1])), x[i], x[i + 1]);
+            for (int i = 0; i < 16; i += 2) f32x2_split(add_f32x2(f32x2(x[i], x[i + 1]), f32x2(lo[i], lo[i + 1])), x[i], x[i + 1]);
         };
         for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
             it.set(a, index);
@@ -413,186 +385,90 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(it.from + row * p.d + c0 + c);
                 }
             };
-            auto arrive = [&](uint64_t *bar) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar);
-            };
             if constexpr (STATES) {
                 if (it.K > 0) {
                     tc_fence_before();
-                    arrive(x_ready);  // the item before has been read
+                    arrive(x_read);  // the item before has been read
                 }
                 for (int k = 0; k < it.K; ++k, ++g) {
                     const int first = it.first(k), count = it.count(k);
                     const float w = it.q->s * expf(rate * (float)max(it.back ? first + row + 1 : it.rows - 1 - first - row, 0));
-                    if (!(ok = hold(c_full + g % NS, around(g)))) break;
+                    if (!(ok = hold(full + g % NS, around(g)))) break;
                     if (g > 1 && !(ok = hold(x_full + (g & 1), two(g - 2)))) break;
                     uint8_t *hi = sm + G::kW + (g & 1) * 2 * kTileC;
                     weight_row(stage(g) + G::kC, hi, hi + kTileC, row, part, w, row < count);
                     if (count < kRows) {  // zeros, whatever is there, in the other operand too
-                        if (!(ok = hold(b_full + g % NS, around(g)))) break;
                         if (part == 0) zero_rows<D>(stage(g) + G::kB, row, count, kRows);
                     }
                     fence_proxy_async_smem();
-                    arrive(w_full + (g & 1));
+                    arrive(x_ready + (g & 1));
                 }
-                if (!ok || (it.K > 0 && !(ok = hold(o_full, one(items))))) break;
+                if (!ok || (it.K > 0 && !(ok = hold(s_full, one(items))))) break;
                 items += it.K > 0;
             } else {
-                const DecayPass &q = *it.q;
-                // factors of a chunk: of a X~, of X, of this thread's row of c
-                float by_w = 0.f, keep = 0.f, weight = 0.f;
+                // factors of a chunk: of X, of this thread's row of c
+                float keep = 0.f, weight = 0.f;
                 int counted = -1;
-                // P's factors for this thread's columns, p g^(i - j) (backward g^(j - i)), 0 on the other side of the diagonal
-                constexpr int kP = kRows / kParts;
-                const int j0 = kP * part;
-                const float rate2 = rate * kLog2e;
-                uint64_t pf[kP / 2];
-#pragma unroll
-                for (int x = 0; x < kP; x += 2) {
-                    const int far = it.back ? j0 + x - row : row - j0 - x, then = it.back ? far + 1 : far - 1;
-                    pf[x / 2] = f32x2(far >= 0 ? q.p * ex2(rate2 * (float)far) : 0.f, then >= 0 ? q.p * ex2(rate2 * (float)then) : 0.f);
-                }
-                __nv_bfloat16 *O = (__nv_bfloat16 *)q.o.ptr + it.b * q.o.sb + it.h * q.o.sh + it.r0 * q.o.sn + it.half * kColumns;
-                for (int k = -1; k <= it.K && it.K > 0; ++k) {
-                    if (k > 0) {
-                        // ------------------------------------------------------ o of the chunk before
-                        const int f = g + k - 1, count = it.count(k - 1);
-                        const uint64_t f2 = f32x2(by_w, by_w);  // (still that chunk's)
-                        if (!(ok = hold(o_full, one(f)))) break;
-                        tc_fence_after();
-                        float in[kSlice], by[kSlice];
-                        uint32_t u[kSlice / 2];
-                        take(lanes + kColIn + kSlice * part, in);
-                        if (it.has(k - 1)) {
-                            take(lanes + kColBy + kSlice * part, by);
-                        } else {
-#pragma unroll
-                            for (int x = 0; x < kSlice; ++x) by[x] = 0.f;
-                        }
-                        tmem_ld_wait();
-                        tc_fence_before();
-                        arrive(o_free);
-#pragma unroll
-                        for (int x = 0; x < kSlice / 2; ++x) {
-                            float y, z;
-                            f32x2_split(fma_f32x2(f2, f32x2(by[2 * x], by[2 * x + 1]), f32x2(in[2 * x], in[2 * x + 1])), y, z);
-                            u[x] = pack2(y, z);
-                        }
-                        if (row >= count) {
-#pragma unroll
-                            for (int x = 0; x < kSlice / 2; ++x) u[x] = 0u;
-                        }
-                        if (f > 0 && !(ok = hold(sent, one(f - 1)))) break;  // the chunk before has left `out`
-#pragma unroll
-                        for (int x = 0; x < kSlice / 8; ++x)
-                            *reinterpret_cast<uint4 *>(sm + G::kOut + chunk_at(row, kSlice / 8 * part + x)) = make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2], u[4 * x + 3]);
-                        fence_proxy_async_smem();
-                        arrive(staged);
+                for (int k = 0; k < it.K; ++k, ++g) {
+                    const int count = it.count(k);
+                    if (count != counted) {
+                        counted = count;
+                        weight = it.q->s * expf(rate * (float)(it.back ? row + 1 : max(count - 1 - row, 0))), keep = expf(rate * (float)count);
                     }
-                    if (k >= 0 && k < it.K) {
-                        const int f = g + k, count = it.count(k);
-                        if (count != counted) {
-                            counted = count;
-                            const float up = expf(rate * (float)(row + 1)), down = expf(rate * (float)max(count - 1 - row, 0));
-                            by_w = q.w * (it.back ? down : up), weight = q.s * (it.back ? up : down), keep = expf(rate * (float)count);
-                        }
-                        // ------------------------------------------------------ the state (X of the chunk before is complete,
-                        // and X~ and the weighted rows have been read)
-                        if (f > 0 && !(ok = hold(x_full, one(f - 1)))) break;
-                        if (it.has(k) && mine) {
-                            float x[kSlice];
-                            tc_fence_after();
+                    // the rows of c, once X of the chunk before is complete
+                    if (!(ok = hold(full + g % NS, around(g)))) break;
+                    if (g > 0 && !(ok = hold(x_full, one(g - 1)))) break;
+                    uint8_t *c = stage(g) + G::kC, *hi = sm + G::kW;
+                    if (it.takes(k)) weight_row(c, hi, hi + kTileC, row, part, weight, row < count);
+                    if (count < kRows) {
+                        // zeros, whatever is there, in both operands of X and in that of P c (S may be reading b: what it makes of
+                        // these rows is masked)
+                        if (part == 0) zero_rows<D>(stage(g) + G::kB, row, count, kRows);
+                        if (row >= count)
+                            for (int x = 0; x < kSlice / 8; ++x) *reinterpret_cast<uint4 *>(c + chunk_at(row, kSlice / 8 * part + x)) = make_uint4(0, 0, 0, 0);
+                    }
+                    // the state, once a X~ of the chunk before is complete too
+                    if (g > 0 && !(ok = hold(over + (g - 1) % NS, around(g - 1)))) break;
+                    if (it.has(k) && mine) {
+                        tc_fence_after();
+                        const uint64_t keep2 = f32x2(keep, keep);
+#pragma unroll
+                        for (int c = 0; c < kSlice; c += 16) {
+                            float x[16];
                             if (k > 0) {
-                                take_x(x);
+                                take_x(c, x);
                             } else {
 #pragma unroll
-                                for (int i = 0; i < kSlice; i += 4) outside(i, x + i);
+                                for (int i = 0; i < 16; i += 4) outside(c + i, x + i);
                             }
 #pragma unroll
-                            for (int i = 0; i < kSlice; i += 8)
-                                *reinterpret_cast<uint4 *>(sm + G::kImg + chunk_at(row, kSlice / 8 * part + i / 8)) =
+                            for (int i = 0; i < 16; i += 8)
+                                *reinterpret_cast<uint4 *>(sm + G::kImg + chunk_at(row, (kSlice * part + c + i) / 8)) =
                                     make_uint4(pack2(x[i], x[i + 1]), pack2(x[i + 2], x[i + 3]), pack2(x[i + 4], x[i + 5]), pack2(x[i + 6], x[i + 7]));
-                            if (it.takes(k)) {
-                                const uint64_t keep2 = f32x2(keep, keep);
-                                uint32_t y[kSlice];
+                            uint32_t y[16];
 #pragma unroll
-                                for (int i = 0; i < kSlice; i += 2) {
-                                    float y0, y1;
-                                    f32x2_split(mul_f32x2(f32x2(x[i], x[i + 1]), keep2), y0, y1);
-                                    y[i] = __float_as_uint(y0), y[i + 1] = __float_as_uint(y1);
-                                }
-                                give(tX, y);
-                                tmem_st_wait();
+                            for (int i = 0; i < 16; i += 2) {
+                                float y0, y1;
+                                f32x2_split(mul_f32x2(f32x2(x[i], x[i + 1]), keep2), y0, y1);
+                                y[i] = __float_as_uint(y0), y[i + 1] = __float_as_uint(y1);
                             }
-                            fence_proxy_async_smem();
+                            tmem_st16(tX + c, y);
                         }
-                        tc_fence_before();
-                        arrive(x_ready);
-                        // ------------------------------------------------------ the rows of c
-                        if (!(ok = hold(c_full + f % NS, around(f)))) break;
-                        uint8_t *c = stage(f) + G::kC, *hi = sm + G::kW;
-                        if (it.takes(k)) weight_row(c, hi, hi + kTileC, row, part, weight, row < count);
-                        if (count < kRows) {
-                            // zeros, whatever is there, in both operands of X and in that of P c (S may be reading b: what it makes
-                            // of these rows is masked)
-                            if (!(ok = hold(b_full + f % NS, around(f)))) break;
-                            if (part == 0) zero_rows<D>(stage(f) + G::kB, row, count, kRows);
-                            if (row >= count)
-                                for (int x = 0; x < kSlice / 8; ++x) *reinterpret_cast<uint4 *>(c + chunk_at(row, kSlice / 8 * part + x)) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        arrive(w_full);
-                    }
-                    if (k + 1 < it.K) {
-                        // ------------------------------------------------------ P of the next chunk
-                        const int f = g + k + 1, count = it.count(k + 1);
-                        const uint32_t tS = lanes + kColS + kRows * (f & 1) + j0;  // P over this warp's own columns
-                        if (!(ok = hold(s_full + (f & 1), two(f)))) break;
-                        tc_fence_after();
-                        uint32_t packed[kP / 2];
-                        if (it.back ? j0 + kP <= w4 * 32 || j0 >= count : j0 > w4 * 32 + 31) {
-#pragma unroll
-                            for (int x = 0; x < kP / 2; ++x) packed[x] = 0u;
-                        } else {
-#pragma unroll
-                            for (int y = 0; y < kP; y += 32) {
-                                float s[32];
-                                tmem_ld32(tS + y, s);
-                                tmem_ld_wait();
-                                if (j0 + y + 32 > count) {  // (0 times what is there may be a NaN)
-#pragma unroll
-                                    for (int x = 0; x < 32; ++x)
-                                        if (j0 + y + x >= count) s[x] = 0.f;
-                                }
-#pragma unroll
-                                for (int x = 0; x < 16; ++x) {
-                                    float s0, s1;
-                                    f32x2_split(mul_f32x2(f32x2(s[2 * x], s[2 * x + 1]), pf[(y + 2 * x) / 2]), s0, s1);
-                                    packed[y / 2 + x] = pack2(s0, s1);
-                                }
-                            }
-                        }
-                        if constexpr (kP == 64) tmem_st32(tS, packed);
-                        else tmem_st16(tS, packed);
                         tmem_st_wait();
-                        tc_fence_before();
-                        arrive(p_full + (f & 1));
                     }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    arrive(x_ready);
                 }
-                if (!ok) break;
-                g += it.K;
-                // chunks of the segment from the length on
-                const int per = min(p.d, kColumns) / 8, left = max(it.end - it.K * kRows, 0) * per;
-                for (int e = threadIdx.x; e < left; e += 32 * kRowWarps)
-                    *reinterpret_cast<uint4 *>(O + (long long)(it.K * kRows + e / per) * q.o.sn + e % per * 8) = make_uint4(0, 0, 0, 0);
-                if (it.to && it.K > 0 && !(ok = hold(x_full, one(g - 1)))) break;
+                // (the last product, before X is read here or X~ is written for the next item)
+                if (!ok || (it.to && it.K > 0 && !(ok = hold(x_full, one(g - 1))))) break;
             }
             if (!it.to || !mine) continue;
             float x[kSlice];
             if (it.K > 0) {
                 tc_fence_after();
-                take_x(x);
+#pragma unroll
+                for (int c = 0; c < kSlice; c += 16) take_x(c, x + c);
             } else {
 #pragma unroll
                 for (int i = 0; i < kSlice; i += 4) outside(i, x + i);
@@ -608,6 +484,106 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     *reinterpret_cast<float4 *>(it.to + row * p.d + c0 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                 }
             }
+        }
+        if (!ok) gave_up();
+    } else if (!STATES && warp < kWarpState) {
+        // ---------------------------------------------------------------------- P and o
+        if constexpr (!STATES) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
+        const int w4 = warp & 3, part = warp >> 2, row = w4 * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
+        int g = 0;
+        bool ok = true;
+        for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
+            it.set(a, index);
+            const DecayPass &q = *it.q;
+            const float rate = decay_rate(p.log_decay, it.h), rate2 = rate * kLog2e;
+            // P's factors for this thread's columns, p g^(i - j) (backward g^(j - i)), 0 on the other side of the diagonal
+            constexpr int kP = kRows / kParts;
+            const int j0 = kP * part;
+            uint64_t pf[kP / 2];
+#pragma unroll
+            for (int x = 0; x < kP; x += 2) {
+                const int far = it.back ? j0 + x - row : row - j0 - x, then = it.back ? far + 1 : far - 1;
+                pf[x / 2] = f32x2(far >= 0 ? q.p * ex2(rate2 * (float)far) : 0.f, then >= 0 ? q.p * ex2(rate2 * (float)then) : 0.f);
+            }
+            float by_w = 0.f;
+            int counted = -1;
+            for (int k = 0; k <= it.K && it.K > 0; ++k) {
+                if (k < it.K) {
+                    // P of chunk k, before o of the chunk before
+                    const int f = g + k, count = it.count(k);
+                    const uint32_t tS = lanes + kColS + kRows * (f & 1) + j0;  // P over this warp's own columns
+                    if (!(ok = hold(s_full + (f & 1), two(f)))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int y = 0; y < kP; y += 32) {
+                        uint32_t packed[16];
+                        // (blocks on the other side of the diagonal are not read)
+                        if (it.back ? j0 + y < w4 * 32 || j0 + y >= count : j0 + y > w4 * 32) {
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) packed[x] = 0u;
+                        } else {
+                            float s[32];
+                            tmem_ld32(tS + y, s);
+                            tmem_ld_wait();
+                            if (j0 + y + 32 > count) {  // (0 times what is there may be a NaN)
+#pragma unroll
+                                for (int x = 0; x < 32; ++x)
+                                    if (j0 + y + x >= count) s[x] = 0.f;
+                            }
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) {
+                                float s0, s1;
+                                f32x2_split(mul_f32x2(f32x2(s[2 * x], s[2 * x + 1]), pf[(y + 2 * x) / 2]), s0, s1);
+                                packed[x] = pack2(s0, s1);
+                            }
+                        }
+                        tmem_st16(tS + y / 2, packed);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    if (k == 0) arrive(p_ready);
+                }
+                if (k > 0) {
+                    // o of chunk k - 1
+                    const int f = g + k - 1, count = it.count(k - 1);
+                    if (count != counted) counted = count, by_w = q.w * expf(rate * (float)(it.back ? max(count - 1 - row, 0) : row + 1));
+                    const uint64_t f2 = f32x2(by_w, by_w);
+                    if (!(ok = hold(over + f % NS, around(f)))) break;
+                    tc_fence_after();
+                    float in[kSlice], by[kSlice];
+                    uint32_t u[kSlice / 2];
+                    tmem_ld32(lanes + kColIn + kSlice * part, in);
+                    if (it.has(k - 1)) {
+                        tmem_ld32(lanes + kColBy + kSlice * part, by);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < kSlice; ++x) by[x] = 0.f;
+                    }
+                    tmem_ld_wait();
+                    tc_fence_before();
+                    if (k < it.K) arrive(p_ready);
+#pragma unroll
+                    for (int x = 0; x < kSlice / 2; ++x) {
+                        float y, z;
+                        f32x2_split(fma_f32x2(f2, f32x2(by[2 * x], by[2 * x + 1]), f32x2(in[2 * x], in[2 * x + 1])), y, z);
+                        u[x] = row < count ? pack2(y, z) : 0u;
+                    }
+                    if (f > 0 && !(ok = hold(sent, one(f - 1)))) break;  // the chunk before has left `out`
+#pragma unroll
+                    for (int x = 0; x < kSlice / 8; ++x)
+                        *reinterpret_cast<uint4 *>(sm + G::kOut + chunk_at(row, kSlice / 8 * part + x)) = make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2], u[4 * x + 3]);
+                    fence_proxy_async_smem();
+                    arrive(staged);
+                }
+            }
+            if (!ok) break;
+            g += it.K;
+            // chunks of the segment from the length on
+            __nv_bfloat16 *O = (__nv_bfloat16 *)q.o.ptr + it.b * q.o.sb + it.h * q.o.sh + it.r0 * q.o.sn + it.half * kColumns;
+            const int per = min(p.d, kColumns) / 8, left = max(it.end - it.K * kRows, 0) * per;
+            for (int e = threadIdx.x; e < left; e += 32 * kGroup)
+                *reinterpret_cast<uint4 *>(O + (long long)(it.K * kRows + e / per) * q.o.sn + e % per * 8) = make_uint4(0, 0, 0, 0);
         }
         if (!ok) gave_up();
     }
