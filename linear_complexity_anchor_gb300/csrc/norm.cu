@@ -12,6 +12,7 @@
 // dw: a thread sums its columns over the rows that it walks, the block adds its rows' threads in order, and a
 // second launch adds the blocks in order; the grid depends on the shapes alone, so the bits do too.
 #include "cross.cuh"
+#include "ptx.cuh"
 
 #include <cuda_fp8.h>
 #include <math.h>
@@ -222,20 +223,54 @@ __global__ void __launch_bounds__(kBlock<TPR>) add_norm_kernel(const NormParams 
     }
 }
 
-// A block's rows are index, index + blocks, ...; each thread keeps its columns' dw.
+// Backward.  A block's rows are index, index + blocks, ...; each thread keeps its columns' dw and weights.  Short rows: sixteen
+// at a time, so that few blocks' sums are left to be added.  16-bit rows are bound by instructions as much as by memory, so two
+// columns go in one where they can (33600 x 768: 47 -> 41 us), and a row is unpacked once.
+template <int T> constexpr int kBackBlock = T > 32 ? T : 512;
+constexpr int kWays = 4;
+
+// four pairs of columns
+__device__ __forceinline__ void unpack2(const Raw16 &r, uint64_t *v) {
+    const uint32_t u[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = ptx::f32x2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void unpack2(const Raw32 &r, uint64_t *v) {
+    const uint32_t u[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = ptx::f32x2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+}
+__device__ __forceinline__ float sum2(uint64_t v) {
+    float a, b;
+    ptx::f32x2_split(v, a, b);
+    return a + b;
+}
+
 template <typename T, int TPR, int NC>
-__global__ void __launch_bounds__(kBlock<TPR>) add_norm_backward_kernel(const NormParams p) {
-    constexpr int kRows = kBlock<TPR> / TPR;
-    __shared__ float slots[2][TPR > 32 ? TPR / 32 : 1];
-    extern __shared__ float sum[];  // [kRows][D] where kRows > 1
+__global__ void __launch_bounds__(kBackBlock<TPR>) add_norm_backward_kernel(const NormParams p) {
+    using namespace ptx;
+    constexpr int kRows = kBackBlock<TPR> / TPR;
+    // weights, and what a row is unpacked to, stay in registers where they fit
+    constexpr bool kKeep = NC <= (sizeof(T) == 2 ? 3 : 2);
+    __shared__ float2 both[2][TPR > 32 ? TPR / 32 : 1];
+    extern __shared__ float sum[];  // [kWays][D] where kRows > 1
     grid_dependency_wait();
     grid_dependents_launch();
     const int t = threadIdx.x % TPR, g = threadIdx.x / TPR;
-    float dw[NC][8];
+    uint64_t dw2[NC][4], w_kept[kKeep ? NC : 1][4];
+    auto weights = [&](int c, uint64_t *w2) {
+        const int e = 8 * (c * TPR + t);
+        float w[8] = {};
+        if (e < p.D) load_weight<T>(p, e, w);
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+        for (int i = 0; i < 4; ++i) w2[i] = f32x2(w[2 * i], w[2 * i + 1]);
+    };
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dw[c][i] = 0.f;
+    for (int c = 0; c < NC; ++c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dw2[c][i] = 0ull;
+        if constexpr (kKeep) weights(c, w_kept[c]);
+    }
     int turn = 0;
     // (all threads of a block make the same number of steps)
     for (long long base = (long long)blockIdx.x * kRows; base < p.rows; base += (long long)gridDim.x * kRows, turn ^= 1) {
@@ -254,29 +289,27 @@ __global__ void __launch_bounds__(kBlock<TPR>) add_norm_backward_kernel(const No
             }
         }
         // sums of s^2 and of w dy s together: mean(w dy xhat) = r mean(w dy s)
-        float q = 0.f, z = 0.f;
+        uint64_t a_kept[kKeep ? NC : 1][4], q2 = 0ull, z2 = 0ull;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int e = 8 * (c * TPR + t);
-            if (e >= p.D) continue;
-            float a[8], b[8], w[8];
-            unpack(s[c], a);
-            unpack(y[c], b);
-            load_weight<T>(p, e, w);
+            uint64_t b[4], w_here[4], *a = a_kept[kKeep ? c : 0], *w2 = kKeep ? w_kept[kKeep ? c : 0] : w_here;
+            unpack2(s[c], a);
+            unpack2(y[c], b);
+            if constexpr (!kKeep) weights(c, w2);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                q = fmaf(a[i], a[i], q);
-                z = fmaf(a[i] * w[i], b[i], z);
+            for (int i = 0; i < 4; ++i) {
+                q2 = fma_f32x2(a[i], a[i], q2);
+                z2 = fma_f32x2(mul_f32x2(a[i], w2[i]), b[i], z2);
             }
+        }
+        float q = sum2(q2), z = sum2(z2);
+#pragma unroll
+        for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
+            q += __shfl_xor_sync(0xffffffffu, q, o);
+            z += __shfl_xor_sync(0xffffffffu, z, o);
         }
         if (TPR > 32) {
             // both through one barrier; a step's slots are free again behind the next step's barrier
-            __shared__ float2 both[2][TPR > 32 ? TPR / 32 : 1];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                q += __shfl_xor_sync(0xffffffffu, q, o);
-                z += __shfl_xor_sync(0xffffffffu, z, o);
-            }
             if ((threadIdx.x & 31) == 0) both[turn][threadIdx.x >> 5] = make_float2(q, z);
             __syncthreads();
             const float2 o2 = both[turn][(threadIdx.x & 31) % (TPR > 32 ? TPR / 32 : 1)];
@@ -286,31 +319,34 @@ __global__ void __launch_bounds__(kBlock<TPR>) add_norm_backward_kernel(const No
                 q += __shfl_xor_sync(0xffffffffu, q, o);
                 z += __shfl_xor_sync(0xffffffffu, z, o);
             }
-        } else {
-            q = over_row<TPR>(q, Sum(), slots[0]);
-            z = over_row<TPR>(z, Sum(), slots[1]);
         }
         const float rs = rsqrtf(fmaf(q, p.inv_d, p.eps));
-        const float mean = z * rs * p.inv_d;
+        const float mean = -z * rs * p.inv_d;
+        const uint64_t rs2 = f32x2(rs, rs), mean2 = f32x2(mean, mean);
         T *xp = row_of<T>(p, p.dx, row);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int e = 8 * (c * TPR + t);
             if (e >= p.D || !live) continue;
-            float a[8], b[8], w[8], o[8];
-            unpack(s[c], a);
-            unpack(y[c], b);
-            unpack(d[c], o);
-            load_weight<T>(p, e, w);
+            uint64_t b[4], o2[4], w_here[4], *a = a_kept[kKeep ? c : 0], *w2 = kKeep ? w_kept[kKeep ? c : 0] : w_here;
+            float o[8];
+            if constexpr (!kKeep) unpack2(s[c], a), weights(c, w2);
+            unpack2(y[c], b);
+            unpack2(d[c], o2);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float hat = a[i] * rs;
-                dw[c][i] = fmaf(b[i], hat, dw[c][i]);
-                o[i] = fmaf(rs, fmaf(-hat, mean, w[i] * b[i]), o[i]);
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t hat = mul_f32x2(a[i], rs2);
+                dw2[c][i] = fma_f32x2(b[i], hat, dw2[c][i]);
+                f32x2_split(fma_f32x2(rs2, fma_f32x2(hat, mean2, mul_f32x2(w2[i], b[i])), o2[i]), o[2 * i], o[2 * i + 1]);
             }
             put(xp + e, pack(o, (const T *)nullptr));
         }
     }
+    float dw[NC][8];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f32x2_split(dw2[c][i], dw[c][2 * i], dw[c][2 * i + 1]);
     if (!p.part) return;
     float *part = p.part + (size_t)blockIdx.x * p.D;
     if constexpr (kRows == 1) {
@@ -320,16 +356,25 @@ __global__ void __launch_bounds__(kBlock<TPR>) add_norm_backward_kernel(const No
             if (e < p.D) put(part + e, pack(dw[c], (const float *)nullptr));
         }
     } else {
+        // by four ways, each a quarter of the rows in order, then the ways in order
+        constexpr int kEach = kRows / kWays;
+        float *mine = sum + g / kEach * p.D;
+        for (int k = 0; k < kEach; ++k) {
+            if (g % kEach == k) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int e = 8 * (c * TPR + t);
-            if (e < p.D) put(sum + g * p.D + e, pack(dw[c], (const float *)nullptr));
+                for (int c = 0; c < NC; ++c) {
+                    const int e = 8 * (c * TPR + t);
+                    if (e >= p.D) continue;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mine[e + i] = k > 0 ? mine[e + i] + dw[c][i] : dw[c][i];
+                }
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        for (int e = threadIdx.x; e < p.D; e += kBlock<TPR>) {
+        for (int e = threadIdx.x; e < p.D; e += kBackBlock<TPR>) {
             float a = 0.f;
 #pragma unroll
-            for (int k = 0; k < kRows; ++k) a += sum[k * p.D + e];
+            for (int k = 0; k < kWays; ++k) a += sum[k * p.D + e];
             part[e] = a;
         }
     }
@@ -390,14 +435,10 @@ cudaError_t forward(const NormParams &p, int bits8, int group, cudaStream_t stre
                         : forward<T, 512, 4>(p, bits8, group, stream);
 }
 
-// Rows that a block of the backward holds at a time, for D columns.
-int backward_rows(int D) { return D <= 64 ? 16 : D <= 1024 ? 4 : 1; }
-
 template <typename T, int TPR, int NC>
 cudaError_t backward(const NormParams &p, int blocks, cudaStream_t stream) {
-    constexpr int kRows = kBlock<TPR> / TPR;
-    const size_t smem = kRows > 1 && p.part ? (size_t)kRows * p.D * 4 : 0;
-    return launch_pdl(add_norm_backward_kernel<T, TPR, NC>, dim3(blocks), dim3(kBlock<TPR>), smem, stream, p);
+    const size_t smem = kBackBlock<TPR> > TPR && p.part ? (size_t)kWays * p.D * 4 : 0;
+    return launch_pdl(add_norm_backward_kernel<T, TPR, NC>, dim3(blocks), dim3(kBackBlock<TPR>), smem, stream, p);
 }
 
 template <typename T>
@@ -408,10 +449,14 @@ cudaError_t backward(const NormParams &p, int blocks, cudaStream_t stream) {
            : D <= 512   ? backward<T, 32, 2>(p, blocks, stream)
            : D <= 768   ? backward<T, 32, 3>(p, blocks, stream)
            : D <= 1024  ? backward<T, 32, 4>(p, blocks, stream)
+           : D <= 2048  ? backward<T, 256, 1>(p, blocks, stream)
            : D <= 4096  ? backward<T, 256, 2>(p, blocks, stream)
            : D <= 8192  ? backward<T, 512, 2>(p, blocks, stream)
                         : backward<T, 512, 4>(p, blocks, stream);
 }
+// Rows that a block of the backward holds at a time, and blocks an SM, for D columns.
+int backward_rows(int D) { return D <= 64 ? kBackBlock<8> / 8 : D <= 1024 ? kBackBlock<32> / 32 : 1; }
+int backward_blocks(int D) { return D <= 256 ? 2 : D <= 1024 ? 1 : D <= 2048 ? 4 : D <= 4096 ? 2 : 1; }
 
 anchor_attn_status_t add_norm(const anchor_attn_add_norm_t *a, bool bwd, void *stream_v) {
     if (!a) return ANCHOR_ATTN_ERR_INVALID_ARG;
@@ -487,7 +532,7 @@ anchor_attn_status_t add_norm(const anchor_attn_add_norm_t *a, bool bwd, void *s
     if (!bwd) {
         e = a->dtype ? forward<float>(p, a->bits8, a->group, stream) : forward<__nv_bfloat16>(p, a->bits8, a->group, stream);
     } else {
-        const int held = backward_rows(a->D), most = kPlanSMs * 4;
+        const int held = backward_rows(a->D), most = kPlanSMs * backward_blocks(a->D);
         const int blocks = (int)std::min<long long>(((long long)p.rows + held - 1) / held, most);
         if (a->dweight) {
             if (getenv("ANCHOR_ATTN_TEST_FAIL_ALLOC") != nullptr) return ANCHOR_ATTN_ERR_ALLOC;
