@@ -85,14 +85,27 @@ anchor_attn_status_t check_sizes(int dtype, int B, int heads, int n, int d, floa
 
 bool misaligned(const void *p, unsigned bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
 
-// Segments of a sequence: as many as one wave of CTAs takes, of 512 rows at least.  They read b and c twice: none where that
-// would not fill the SMs better (bf16, d = 128, 4 x 16 heads x 16384, 128 items: 255 us with one segment, 324 with two;
-// 2 x 16 x 8192, 64 items: 128 with one, 106 with two, 129 with three).
+// Segments of a sequence: as many as take the least time, by what 128 rows of an item (64 columns of one pass of one head) take, as
+// segments' sums and in a pass, in us, what an item takes to begin and to end, rounds of items over the SMs, two launches more, and
+// their states, one after the other and through L2.  None where the items fill the SMs: segments read b and c twice.  Measured (us): bf16, d = 128, 4 x 16 heads x 16384: one segment 247, two 320; 2 x 16 x
+// 8192: 121, 105, three 130; 16 x 16384: one 231, two 172, four 113, eight 128; 16 x 2049: one 35, four 37; d = 64, 12 x 16384:
+// one 160, ten 46; one head of 32768: one 312, ten 60, 32: 35.
 void plan(DecayProblem &p) {
-    const long long items = p.slices() * p.passes * (p.d == 128 ? 2 : 1);
-    const int want = (int)std::max<long long>(1, std::min<long long>(kPlanSMs / items, p.n / 512));
-    p.seg = std::max(128, ((p.n + want - 1) / want + 127) / 128 * 128);
-    p.segs = (p.n + p.seg - 1) / p.seg;
+    const float pass = p.f32 ? 10.f : p.d == 128 ? 1.87f : 1.35f, sums = pass * 0.48f, item = 2.2f, launches = 16.f;
+    const long long slices = p.slices(), halves = p.d == 128 ? 2 : 1;
+    const int tiles = (p.n + 127) / 128, most = (int)std::max<long long>(1, std::min<long long>(4 * kPlanSMs / (slices * halves), tiles / 2));
+    auto rounds = [](long long items) { return (float)((items + kPlanSMs - 1) / kPlanSMs); };
+    float best = 0.f;
+    int want = 1;
+    for (int s = 1; s <= most; ++s) {
+        const float each = (float)((tiles + s - 1) / s);
+        float t = rounds(slices * halves * p.passes * s) * (each * pass + item);
+        if (s > 1)
+            t += rounds(slices * halves * p.kinds * (s - 1)) * (each * sums + item) + launches + 0.15f * (float)s + (float)(slices * p.kinds * s) * (float)(p.d * p.d) * 3e-6f;
+        if (s == 1 || t < best) best = t, want = s;
+    }
+    p.seg = (tiles + want - 1) / want * 128;
+    p.segs = std::max(1, (p.n + p.seg - 1) / p.seg);
 }
 
 // A call of few tokens goes token by token where the states are what it moves.

@@ -15,8 +15,8 @@
 //
 // Two groups of eight warps, a thread half of a row: the first makes P of the next chunk, and o from its two products; the
 // second X~ and the decay of X, and the weighted rows of c.  What a chunk takes is the second's round, X, X~, weights, X; all
-// else is done beside it.  (One group for all, one step after the other: 1.7 us a chunk against XXX.  A group for each of
-// the four steps: 3.9, most of it spent on fetching instructions.)  One warp loads tiles by TMA, one stores o's, one issues
+// else is done beside it.  (A chunk takes 1.35 us at d = 64 and 1.87 at 128, from L2; with one group for all, one step after
+// the other, 1.6 and 1.8; with a group for each of the four steps 3.9, most of it spent on fetching instructions.)  One warp loads tiles by TMA, one stores o's, one issues
 // the products: P c, S of the next chunk, a X~, X, each as soon as its operands are there; S has two buffers.
 //
 // STATES: the sums of a segment alone, s sum_j g^(rows-1-j) b_j^T c_j: the last product alone, with weights that count from the
@@ -38,8 +38,8 @@ constexpr int kParts = 2;                         // threads of a row
 constexpr int kGroup = 4 * kParts;                // warps of a group
 constexpr int kWarpState = kGroup, kWarpLoad = 2 * kGroup, kWarpIssue = kWarpLoad + 1, kWarpStore = kWarpLoad + 2, kThreads = 32 * (kWarpLoad + 4);
 constexpr int kSlice = kColumns / kParts;         // columns of o, of the state and of c of a thread, kRows / kParts of P
-// Registers of a thread: 640 threads have 96 at launch, 1920 for a lane of each; 8 * 128 + 8 * 88 + 4 * 40 = 1888.
-constexpr int kRegsRows = 128, kRegsState = 88, kRegsOthers = 40;
+// Registers of a thread: 640 threads have 96 at launch, 1920 for a lane of each warp; 8 * 136 + 8 * 80 + 4 * 40 = 1888.
+constexpr int kRegsRows = 136, kRegsState = 80, kRegsOthers = 40;
 constexpr uint32_t kColS = 0, kColIn = 256, kColBy = 320, kColX = 384, kCols = 512;  // of tensor memory; S has two buffers
 
 // D columns of a and b (heads of 16 and 32 are 64)
@@ -49,7 +49,7 @@ struct Geo {
     static constexpr int kA = 0, kB = STATES ? 0 : kTile<D>, kC = kB + kTile<D>, kStage = kC + kTileC;  // of a stage
     static constexpr int kWeighted = STATES ? 2 : 1;  // buffers of the weighted rows of c
     static constexpr int kRing = 0, kW = kRing + kStages * kStage, kImg = kW + kWeighted * 2 * kTileC, kOut = kImg + (STATES ? 0 : D * kColumns * 2),
-                         kBars = kOut + (STATES ? 0 : kTileC);
+                         kPow = kOut + (STATES ? 0 : kTileC), kBars = kPow + (STATES ? 0 : kGroup * 64 * 4);
     static constexpr int kNBars = 2 * kStages + 12, kSmem = kBars + kNBars * 8 + 8;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -73,18 +73,36 @@ struct Item {
     const DecayPass *q;
     int which, b, h, slice, seg, half, r0, rows, K, end;  // end: rows of the segment
     bool back, turned;
+    float rate;
     const float *from;  // states outside, or null
     float *to;
+    int next_length;    // what is read for the next item is asked for while this one is walked
+    float next_rate;
 
+    __device__ __forceinline__ int place(const TcParams &a, int index, int &of) {
+        const int kinds = STATES ? a.p.kinds : a.p.passes;
+        // the halves and passes of a segment are neighbours, so that what they share is read once
+        const int x = a.halves == 2 ? index >> 1 : index, y = kinds == 3 ? x / 3 : kinds == 2 ? x >> 1 : x;
+        half = index - x * a.halves, of = x - y * kinds;
+        return y;
+    }
+    __device__ __forceinline__ void ask(const TcParams &a, int index) {
+        if (index >= a.items) return;
+        int of, was = half;
+        const int slice = a.by_segs.of(place(a, index, of)), b = a.by_heads.of(slice);
+        half = was;
+        next_length = decay_length(a.p, b), next_rate = decay_rate(a.p.log_decay, slice - b * a.p.heads);
+    }
     __device__ __forceinline__ void set(const TcParams &a, int index) {
         const DecayProblem &p = a.p;
-        const int kinds = STATES ? p.kinds : p.passes, segs = STATES ? p.segs - 1 : p.segs;
-        // the halves and passes of a segment are neighbours, so that what they share is read once
-        int x = a.halves == 2 ? index >> 1 : index;
-        half = index - x * a.halves;
-        const int y = kinds == 3 ? x / 3 : kinds == 2 ? x >> 1 : x, of = x - y * kinds;
+        const int segs = STATES ? p.segs - 1 : p.segs;
+        int of;
+        const int y = place(a, index, of);
         slice = a.by_segs.of(y);
         b = a.by_heads.of(slice), h = slice - b * p.heads;
+        const int length = next_length;
+        rate = next_rate;
+        ask(a, index + (int)gridDim.x);
         which = of;
         if (STATES)
             while (p.pass[which].kind != of) ++which;  // a pass of that kind
@@ -92,7 +110,7 @@ struct Item {
         back = q->back, turned = STATES ? false : q->turned;
         seg = y - slice * segs + (STATES && back ? 1 : 0);  // the last one (in time) has no state behind it
         r0 = seg * p.seg, end = min(p.seg, p.n - r0);
-        rows = decay_rows(p, seg, decay_length(p, b));
+        rows = decay_rows(p, seg, length);
         K = (rows + kRows - 1) / kRows;
         const long long dd = p.d * p.d;
         float *in = p.states + (((long long)(STATES ? of : q->kind) * p.slices() + slice) * p.segs + seg) * dd;
@@ -217,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
     grid_dependents_launch();
 
     Item<STATES> it;
+    it.ask(a, blockIdx.x);
     auto stage = [&](int g) { return sm + G::kRing + g % NS * G::kStage; };
     auto arrive = [&](uint64_t *bar) {
         __syncwarp();
@@ -372,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
         };
         for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
             it.set(a, index);
-            const float rate = decay_rate(p.log_decay, it.h);
+            const float rate = it.rate;
             const int c0 = it.half * kColumns + kSlice * part;  // this thread's columns of the state
             // four columns of this thread's row of the state outside (zeros where there is none)
             auto outside = [&](int c, float *x) {
@@ -491,99 +510,123 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
         if constexpr (!STATES) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
         const int w4 = warp & 3, part = warp >> 2, row = w4 * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
-        int g = 0;
+        constexpr int kP = kRows / kParts;
+        const int j0 = kP * part;
+        uint64_t pf[kP / 2];
+        float *table = reinterpret_cast<float *>(sm + G::kPow) + warp * 64;
+        int index = (int)blockIdx.x - (int)gridDim.x, k = 0, counted = -1;
+        int count = 0, count_o = 0;      // rows of this chunk, and of the one whose o comes next
+        float by = 0.f, by_o = 0.f;      // factors of a X~
+        bool has = false, has_o = false;
         bool ok = true;
-        for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
-            it.set(a, index);
-            const DecayPass &q = *it.q;
-            const float rate = decay_rate(p.log_decay, it.h), rate2 = rate * kLog2e;
-            // P's factors for this thread's columns, p g^(i - j) (backward g^(j - i)), 0 on the other side of the diagonal
-            constexpr int kP = kRows / kParts;
-            const int j0 = kP * part;
-            uint64_t pf[kP / 2];
-#pragma unroll
-            for (int x = 0; x < kP; x += 2) {
-                const int far = it.back ? j0 + x - row : row - j0 - x, then = it.back ? far + 1 : far - 1;
-                pf[x / 2] = f32x2(far >= 0 ? q.p * ex2(rate2 * (float)far) : 0.f, then >= 0 ? q.p * ex2(rate2 * (float)then) : 0.f);
-            }
-            float by_w = 0.f;
-            int counted = -1;
-            for (int k = 0; k <= it.K && it.K > 0; ++k) {
-                if (k < it.K) {
-                    // P of chunk k, before o of the chunk before
-                    const int f = g + k, count = it.count(k);
-                    const uint32_t tS = lanes + kColS + kRows * (f & 1) + j0;  // P over this warp's own columns
-                    if (!(ok = hold(s_full + (f & 1), two(f)))) break;
-                    tc_fence_after();
+        it.K = 0;
+        for (int g = 0;; ++g) {
+            // the next chunk, which may be another item's: its P comes before the o of the chunk before
+            bool more = true;
+            if (++k >= it.K) {
+                do {
+                    index += gridDim.x;
+                    if (!(more = index < a.items)) break;
+                    it.set(a, index);
+                    // chunks of the segment from the length on
+                    __nv_bfloat16 *O = (__nv_bfloat16 *)it.q->o.ptr + it.b * it.q->o.sb + it.h * it.q->o.sh + it.r0 * it.q->o.sn + it.half * kColumns;
+                    const int per = min(p.d, kColumns) / 8, left = max(it.end - it.K * kRows, 0) * per;
+                    for (int e = threadIdx.x; e < left; e += 32 * kGroup)
+                        *reinterpret_cast<uint4 *>(O + (long long)(it.K * kRows + e / per) * it.q->o.sn + e % per * 8) = make_uint4(0, 0, 0, 0);
+                } while (it.K == 0);
+                if (more) {
+                    // P's factors for this thread's columns, p g^(i - j) (backward g^(j - i)), 0 on the other side of the diagonal
+                    const float rate2 = it.rate * kLog2e, scale = it.q->p;
+                    // 32 columns of 32 rows have 63 distances (and one more: there is no column 32)
 #pragma unroll
                     for (int y = 0; y < kP; y += 32) {
-                        uint32_t packed[16];
-                        // (blocks on the other side of the diagonal are not read)
-                        if (it.back ? j0 + y < w4 * 32 || j0 + y >= count : j0 + y > w4 * 32) {
+                        const int least = it.back ? j0 + y - w4 * 32 - 31 : w4 * 32 - j0 - y - 31;  // of lane 0 (backward 31) and column 31 (0)
+                        __syncwarp();
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) packed[x] = 0u;
-                        } else {
-                            float s[32];
-                            tmem_ld32(tS + y, s);
-                            tmem_ld_wait();
-                            if (j0 + y + 32 > count) {  // (0 times what is there may be a NaN)
-#pragma unroll
-                                for (int x = 0; x < 32; ++x)
-                                    if (j0 + y + x >= count) s[x] = 0.f;
-                            }
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                float s0, s1;
-                                f32x2_split(mul_f32x2(f32x2(s[2 * x], s[2 * x + 1]), pf[(y + 2 * x) / 2]), s0, s1);
-                                packed[x] = pack2(s0, s1);
-                            }
+                        for (int x = 0; x < 64; x += 32) {
+                            const int far = least + x + lane;
+                            table[x + lane] = far >= 0 ? scale * ex2(rate2 * (float)far) : 0.f;
                         }
-                        tmem_st16(tS + y / 2, packed);
-                    }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    if (k == 0) arrive(p_ready);
-                }
-                if (k > 0) {
-                    // o of chunk k - 1
-                    const int f = g + k - 1, count = it.count(k - 1);
-                    if (count != counted) counted = count, by_w = q.w * expf(rate * (float)(it.back ? max(count - 1 - row, 0) : row + 1));
-                    const uint64_t f2 = f32x2(by_w, by_w);
-                    if (!(ok = hold(over + f % NS, around(f)))) break;
-                    tc_fence_after();
-                    float in[kSlice], by[kSlice];
-                    uint32_t u[kSlice / 2];
-                    tmem_ld32(lanes + kColIn + kSlice * part, in);
-                    if (it.has(k - 1)) {
-                        tmem_ld32(lanes + kColBy + kSlice * part, by);
-                    } else {
+                        __syncwarp();
+                        const float *at = table + (it.back ? 31 - lane : 31 + lane);
 #pragma unroll
-                        for (int x = 0; x < kSlice; ++x) by[x] = 0.f;
+                        for (int x = 0; x < 32; x += 2) pf[(y + x) / 2] = it.back ? f32x2(at[x], at[x + 1]) : f32x2(at[-x], at[-x - 1]);
                     }
-                    tmem_ld_wait();
-                    tc_fence_before();
-                    if (k < it.K) arrive(p_ready);
-#pragma unroll
-                    for (int x = 0; x < kSlice / 2; ++x) {
-                        float y, z;
-                        f32x2_split(fma_f32x2(f2, f32x2(by[2 * x], by[2 * x + 1]), f32x2(in[2 * x], in[2 * x + 1])), y, z);
-                        u[x] = row < count ? pack2(y, z) : 0u;
-                    }
-                    if (f > 0 && !(ok = hold(sent, one(f - 1)))) break;  // the chunk before has left `out`
-#pragma unroll
-                    for (int x = 0; x < kSlice / 8; ++x)
-                        *reinterpret_cast<uint4 *>(sm + G::kOut + chunk_at(row, kSlice / 8 * part + x)) = make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2], u[4 * x + 3]);
-                    fence_proxy_async_smem();
-                    arrive(staged);
+                    k = 0, counted = -1;
                 }
             }
-            if (!ok) break;
-            g += it.K;
-            // chunks of the segment from the length on
-            __nv_bfloat16 *O = (__nv_bfloat16 *)q.o.ptr + it.b * q.o.sb + it.h * q.o.sh + it.r0 * q.o.sn + it.half * kColumns;
-            const int per = min(p.d, kColumns) / 8, left = max(it.end - it.K * kRows, 0) * per;
-            for (int e = threadIdx.x; e < left; e += 32 * kGroup)
-                *reinterpret_cast<uint4 *>(O + (long long)(it.K * kRows + e / per) * q.o.sn + e % per * 8) = make_uint4(0, 0, 0, 0);
+            if (more) {
+                has = it.has(k), count = it.count(k);
+                if (count != counted) {
+                    counted = count;
+                    by = it.q->w * expf(it.rate * (float)(it.back ? max(count - 1 - row, 0) : row + 1));
+                }
+                const uint32_t tS = lanes + kColS + kRows * (g & 1) + j0;  // P over this warp's own columns
+                if (!(ok = hold(s_full + (g & 1), two(g)))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int y = 0; y < kP; y += 32) {
+                    uint32_t packed[16];
+                    // (blocks on the other side of the diagonal are not read)
+                    if (it.back ? j0 + y < w4 * 32 || j0 + y >= count : j0 + y > w4 * 32) {
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) packed[x] = 0u;
+                    } else {
+                        float s[32];
+                        tmem_ld32(tS + y, s);
+                        tmem_ld_wait();
+                        if (j0 + y + 32 > count) {  // (0 times what is there may be a NaN)
+#pragma unroll
+                            for (int x = 0; x < 32; ++x)
+                                if (j0 + y + x >= count) s[x] = 0.f;
+                        }
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            float s0, s1;
+                            f32x2_split(mul_f32x2(f32x2(s[2 * x], s[2 * x + 1]), pf[(y + 2 * x) / 2]), s0, s1);
+                            packed[x] = pack2(s0, s1);
+                        }
+                    }
+                    tmem_st16(tS + y / 2, packed);
+                }
+                tmem_st_wait();
+            }
+            uint32_t u[kSlice / 2];
+            if (g > 0) {
+                if (!(ok = hold(over + (g - 1) % NS, around(g - 1)))) break;
+                tc_fence_after();
+                const uint64_t f2 = f32x2(by_o, by_o);
+#pragma unroll
+                for (int c = 0; c < kSlice; c += 16) {
+                    float in[16], x[16];
+                    tmem_ld16(lanes + kColIn + kSlice * part + c, in);
+                    if (has_o) {
+                        tmem_ld16(lanes + kColBy + kSlice * part + c, x);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] = 0.f;
+                    }
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float y, z;
+                        f32x2_split(fma_f32x2(f2, f32x2(x[2 * i], x[2 * i + 1]), f32x2(in[2 * i], in[2 * i + 1])), y, z);
+                        u[c / 2 + i] = row < count_o ? pack2(y, z) : 0u;
+                    }
+                }
+            }
+            tc_fence_before();
+            if (more) arrive(p_ready);
+            if (g > 0) {
+                if (g > 1 && !(ok = hold(sent, one(g - 2)))) break;  // the chunk before has left `out`
+#pragma unroll
+                for (int x = 0; x < kSlice / 8; ++x)
+                    *reinterpret_cast<uint4 *>(sm + G::kOut + chunk_at(row, kSlice / 8 * part + x)) = make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2], u[4 * x + 3]);
+                fence_proxy_async_smem();
+                arrive(staged);
+            }
+            if (!more) break;
+            has_o = has, count_o = count, by_o = by;
         }
         if (!ok) gave_up();
     }
