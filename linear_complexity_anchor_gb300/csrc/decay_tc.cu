@@ -247,29 +247,36 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
 
     if (!STATES && warp >= kWarpLoad) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOthers));
     if (warp == kWarpLoad) {
-        if (lane == 0) {
-            int g = 0;
-            bool ok = true;
-            for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
-                it.set(a, index);
-                // STATES: b and c in the order of the kind, not turned
-                const bool swap = STATES && it.q->turned;
-                const TileMap &ma = a.a[it.which], &mb = swap ? a.c[it.which] : a.b[it.which], &mc = swap ? a.b[it.which] : a.c[it.which];
-                for (int k = 0; k < it.K; ++k, ++g) {
-                    const int row = it.r0 + it.first(k), st = g % NS;
-                    uint8_t *to = stage(g);
-                    if (g >= NS && !(ok = hold(over + st, around(g - NS)))) break;
+        int g = 0;
+        bool ok = true;
+        for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
+            it.set(a, index);
+            if (it.from) {  // the state that the item begins with, into L2: it is read some chunks from now
+                const int bytes = p.d * min(p.d, kColumns) * 4;
+                for (int o = 128 * lane; o < bytes; o += 128 * 32) {
+                    const int at = p.d <= kColumns || it.turned ? it.half * bytes + o : o / 256 * (p.d * 4) + it.half * 256 + o % 256;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(it.from) + at));
+                }
+            }
+            // STATES: b and c in the order of the kind, not turned
+            const bool swap = STATES && it.q->turned;
+            const TileMap &ma = a.a[it.which], &mb = swap ? a.c[it.which] : a.b[it.which], &mc = swap ? a.b[it.which] : a.c[it.which];
+            for (int k = 0; k < it.K; ++k, ++g) {
+                const int row = it.r0 + it.first(k), st = g % NS;
+                uint8_t *to = stage(g);
+                if (g >= NS && !(ok = all_hold(over + st, around(g - NS)))) break;
+                if (lane == 0) {
                     mbar_arrive_expect_tx(full + st, G::kStage);
                     if (!STATES) load_tile<D, kRows, kRows>(to + G::kA, ma, full + st, row, it.h, it.b);
                     load_tile<D, kRows, kRows>(to + G::kB, mb, full + st, row, it.h, it.b);
                     tma_load_4d(to + G::kC, &mc.map, full + st, kColumns * it.half, row, it.h * mc.by_head, it.b * mc.by_batch);
                 }
+                __syncwarp();
             }
-            // the CTA leaves only once its copies have landed
-            for (int x = max(0, g - NS); x < g; ++x) ok = hold(full + x % NS, around(x)) && ok;
-            if (!ok) gave_up();
         }
-        __syncwarp();
+        // the CTA leaves only once its copies have landed
+        for (int x = max(0, g - NS); x < g; ++x) ok = all_hold(full + x % NS, around(x)) && ok;
+        if (!ok) gave_up();
     } else if (warp == kWarpIssue) {
         {
             const uint32_t base = smem_u32(sm);
