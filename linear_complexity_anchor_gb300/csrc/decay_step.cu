@@ -12,7 +12,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32, kColumns = 32;
 
 template <typename T, int D, int CB>
-__global__ void __launch_bounds__(kThreads) decay_step_kernel(const __grid_constant__ DecayStep p) {
+__global__ void __launch_bounds__(kThreads, 6) decay_step_kernel(const __grid_constant__ DecayStep p) {
     constexpr int W = CB / 4, R = kThreads / W, N = (D + R - 1) / R, kBlocks = D / CB;  // threads a row, rows at a time, rows a thread
     __shared__ __align__(16) float sq[2][D], sk[2][D], sv[2][CB];
     __shared__ float4 part[2][kWarps][W];
