@@ -4,23 +4,27 @@
 // the state.  A CTA takes every gridDim.x-th item and walks its rows in chunks of 128; what loads, multiplies
 // and stores runs on from item to item.  With i, j rows of a chunk of `count`, X the state before it (d x 64, fp32,
 // in tensor memory) and X~ its bf16 image in shared memory:
-//   S = a b^T,  P = g^(i-j) S below the diagonal (bf16, over S),  o = p P c + w g^(i+1) (a X~)
+//   S = a b^T,  P = g^(i-j) S below the diagonal (bf16),  o = p P c + w g^(i+1) (a X~)
 //   X <- g^count X + b^T (s g^(count-1-j) c_j)
 // (a pass backward in time: the other triangle, g^(j-i), g^(count-1-i), g^(j+1), chunks from the last to the first).
 //
 // Roundings: P and X~ to bf16, each once, where they meet c and a; the rows s g^(count-1-j) c_j are two bf16
-// numbers (what the first leaves of them is the second), so that X is exact to 2^-17: it is an fp32
+// numbers (what the first leaves of them is the second), so that X is off by 3.9e-6 of itself: it is an fp32
 // result, and its own rounding in X~ stays the only one of the part of o that goes by it.  With one number o
-// would carry three roundings there, 1.7 times a lone one, against 1.4.
+// would carry three roundings there, 1.7 times a lone one, against 1.4.  What a chunk adds to X is a sum of its own, added by
+// the rows, to nearest: the tensor cores' sums are cut off, which over many chunks would add up where X decays slowly (6e-6
+// of a state that reaches 3717 rows back, without a bound at a decay of 0; a loop that sums X there takes 3 % less at d = 64,
+// nothing less at 128).  With X in registers a chunk takes 1.45 and 1.89 us.
 //
 // Two groups of eight warps, a thread half of a row: the first makes P of the next chunk, and o from its two products; the
-// second X~ and the decay of X, and the weighted rows of c.  What a chunk takes is the second's round, X, X~, weights, X; all
-// else is done beside it.  (A chunk takes 1.35 us at d = 64 and 1.87 at 128, from L2; with one group for all, one step after
-// the other, 1.6 and 1.8; with a group for each of the four steps 3.9, most of it spent on fetching instructions.)  One warp loads tiles by TMA, one stores o's, one issues
-// the products: P c, S of the next chunk, a X~, X, each as soon as its operands are there; S has two buffers.
+// second the weighted rows of c, X~ and X.  One warp loads tiles by TMA, one stores o's, one issues the products: P c, S of the
+// next chunk, X, a X~, each as soon as its operands are there.  What a chunk takes is the second group's round (weights, X's
+// product, X~, a X~) and the products' operands, which take three quarters of what the shared memory gives; all else is done
+// beside it: 1.38 us at d = 64 and 1.88 at 128, from L2.  With one group for all, one step after the other, 1.6 and 1.9;
+// with a group for each of the four steps 3.9, most of it spent on fetching instructions.
 //
 // STATES: the sums of a segment alone, s sum_j g^(rows-1-j) b_j^T c_j: the last product alone, with weights that count from the
-// segment's end, so that X needs no decay on the way.
+// segment's end, so that no chunk's sum decays and those of kSums chunks are made in tensor memory.
 #include "cross_tc.cuh"
 #include "decay.cuh"
 
@@ -37,10 +41,11 @@ constexpr int kTileC = kTile<kColumns>;
 constexpr int kParts = 2;                         // threads of a row
 constexpr int kGroup = 4 * kParts;                // warps of a group
 constexpr int kWarpState = kGroup, kWarpLoad = 2 * kGroup, kWarpIssue = kWarpLoad + 1, kWarpStore = kWarpLoad + 2, kThreads = 32 * (kWarpLoad + 4);
+constexpr int kSums = 4;                          // STATES: chunks whose sum is made in tensor memory
 constexpr int kSlice = kColumns / kParts;         // columns of o, of the state and of c of a thread, kRows / kParts of P
 // Registers of a thread: 640 threads have 96 at launch, 1920 for a lane of each warp; 8 * 136 + 8 * 80 + 4 * 40 = 1888.
 constexpr int kRegsRows = 136, kRegsState = 80, kRegsOthers = 40;
-constexpr uint32_t kColS = 0, kColIn = 256, kColBy = 320, kColX = 384, kCols = 512;  // of tensor memory; S has two buffers
+constexpr uint32_t kColS = 0, kColP = 128, kColIn = 192, kColBy = 256, kColX = 320, kColAdd = 384, kCols = 512;  // of tensor memory
 
 // D columns of a and b (heads of 16 and 32 are 64)
 template <int D, bool STATES>
@@ -50,7 +55,7 @@ struct Geo {
     static constexpr int kWeighted = STATES ? 2 : 1;  // buffers of the weighted rows of c
     static constexpr int kRing = 0, kW = kRing + kStages * kStage, kImg = kW + kWeighted * 2 * kTileC, kOut = kImg + (STATES ? 0 : D * kColumns * 2),
                          kPow = kOut + (STATES ? 0 : kTileC), kBars = kPow + (STATES ? 0 : kGroup * 64 * 4);
-    static constexpr int kNBars = 2 * kStages + 12, kSmem = kBars + kNBars * 8 + 8;
+    static constexpr int kNBars = 2 * kStages + 10, kSmem = kBars + kNBars * 8 + 8;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -126,7 +131,8 @@ struct Item {
 
 // This thread's columns of a row of c times its weight w, as two bf16 numbers in two tiles.  `on`: the row counts (else
 // zeros, whatever it holds).  With w = u + v in bf16 (2^-18 of w is left out), h = c u rounded, and l = (c u - h) + c v, of
-// which the first part is exact: three instructions for two numbers.
+// which the first part is exact: three instructions for two numbers.  (From fp32 products
+// the states are off by 2.4e-6 of themselves instead of 3.9e-6, and a chunk takes 3 % more.)
 __device__ __forceinline__ void weight_row(const uint8_t *tile, uint8_t *hi, uint8_t *lo, int row, int part, float w, bool on) {
     constexpr int N = kSlice / 8;
     const __nv_bfloat16 u1 = __float2bfloat16_rn(w);
@@ -205,9 +211,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G::kBars);
     // full: a stage's tiles have landed; over: the products of its chunk are complete; p_ready: P is there and the o before has
-    // been read; x_ready: so are X~, X and the weighted rows; x_full: X is complete
+    // been read; x_ready: so are X~, X and the weighted rows; x_full: so is what the chunk adds to X
     uint64_t *full = bars, *over = full + NS, *s_full = over + NS /* [2] */, *p_ready = s_full + 2, *x_ready = p_ready + 1 /* [2] */,
-             *x_full = x_ready + 2 /* [2] */, *x_read = x_full + 2, *staged = x_read + 1, *sent = staged + 1, *done = sent + 1;
+             *x_full = x_ready + 2 /* [2] */, *staged = x_full + 2, *sent = staged + 1, *done = sent + 1;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + G::kNBars);
     const DecayProblem &p = a.p;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -220,7 +226,6 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
         for (int s = 0; s < NS; ++s) mbar_init(full + s, 1), mbar_init(over + s, 1);
         for (int s = 0; s < 2; ++s) mbar_init(s_full + s, 1), mbar_init(x_ready + s, kGroup), mbar_init(x_full + s, 1);
         mbar_init(p_ready, kGroup);
-        mbar_init(x_read, kGroup);
         mbar_init(staged, kGroup);
         mbar_init(sent, 1);
         mbar_init(done, 1);
@@ -283,33 +288,25 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
             auto at = [&](int g) { return base + G::kRing + g % NS * G::kStage; };
             constexpr uint32_t idS = idesc_bf16_f32(kRows, kRows, false, false), idO = idesc_bf16_f32(kRows, kColumns, false, true),
                                idX = idesc_bf16_f32(kRows, 2 * kColumns, true, true);
-            // X += b^T [hi | lo], in 128 columns whose halves are added by the rows, which leave the sum in the first: the second begins
-            // anew with each chunk (`add`: of the first).  With 64 columns of b the product has 128 rows all the same: the upper ones
-            // are made of the tile of c behind b's, and are not read.
-            auto product_x = [&](int g, bool add, bool both) {
+            // What chunks add to X, b^T [hi | lo], in 128 columns whose halves are added by the rows (fresh: begun anew).  With 64
+            // columns of b the product has 128 rows all the same: the upper ones are made of the tile of c behind b's, and are not read.
+            auto product_x = [&](int g, uint32_t to, bool fresh) {
                 const uint64_t b = smem_desc_sw128(at(g) + G::kB, kBlock, 1024), w = desc_mn(base + G::kW + (STATES ? (g & 1) * 2 * kTileC : 0));
-                product(tmem + kColX, b, w, idO | 1u << 15, add ? 1u : 0u);
-                product(tmem + kColX + kColumns, b, w + kTileC / 16, idO | 1u << 15, both ? 1u : 0u);
 #pragma unroll
-                for (int k = 1; k < kRows / 16; ++k) product(tmem + kColX, b + step_mn(k), w + step_mn(k), idX, 1u);
+                for (int k = 0; k < kRows / 16; ++k) product(tmem + to, b + step_mn(k), w + step_mn(k), idX, !fresh || k > 0 ? 1u : 0u);
             };
-            int g = 0, items = 0, scored = 0;  // scored: chunks whose S has been issued
+            int g = 0, scored = 0;  // scored: chunks whose S has been issued
             bool ok = true;
             for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
                 it.set(a, index);
                 for (int k = 0; k < it.K && ok; ++k, ++g) {
                     const int st = g % NS;
                     if constexpr (STATES) {
-                        if (k == 0) {  // the item before has been read
-                            if (!(ok = all_hold(x_read, one(items)))) break;
-                            ++items;
-                        }
                         if (!(ok = all_hold(x_ready + (g & 1), two(g)))) break;
                         tc_fence_after();
-                        product_x(g, k > 0, k > 0);
+                        product_x(g, 2 * kColumns * (k / kSums & 1), k % kSums == 0);
                         commit(x_full + (g & 1));
                         commit(over + st);
-                        if (k + 1 == it.K) commit(s_full);
                     } else {
                         const bool partial = it.count(k) < kRows;
 #pragma unroll 1
@@ -325,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                                 tc_fence_after();
                                 const uint64_t ad = desc_k(at(scored) + G::kA), bd = desc_k(at(scored) + G::kB);
 #pragma unroll
-                                for (int s = 0; s < D / 16; ++s) product(tmem + kColS + kRows * (scored & 1), ad + step_k(s), bd + step_k(s), idS, s > 0 ? 1u : 0u);
+                                for (int s = 0; s < D / 16; ++s) product(tmem + kColS, ad + step_k(s), bd + step_k(s), idS, s > 0 ? 1u : 0u);
                                 commit(s_full + (scored & 1));
                                 ++scored;
                             }
@@ -335,15 +332,13 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                                 if (!(ok = all_hold(p_ready, one(g)))) break;
                                 tc_fence_after();
                                 const uint64_t cd = desc_mn(at(g) + G::kC);
-                                const uint32_t pt = tmem + kColS + kRows * (g & 1);
-                                constexpr int kP = kRows / kParts;  // columns of S that a thread has, with its P at their start
 #pragma unroll
                                 for (int s = 0; s < kRows / 16; ++s)
-                                    product_tmem(tmem + kColIn, pt + 16 * s / kP * kP + 16 * s % kP / 2, cd + step_mn(s), idO, s > 0 ? 1u : 0u);
+                                    product_tmem(tmem + kColIn, tmem + kColP + 8 * s, cd + step_mn(s), idO, s > 0 ? 1u : 0u);
                             } else {
                                 if (!partial && !(ok = all_hold(x_ready, one(g)))) break;
                                 tc_fence_after();
-                                if (it.takes(k)) product_x(g, it.has(k), false);
+                                if (it.takes(k)) product_x(g, kColAdd, true);
                                 commit(x_full);
                                 if (it.has(k)) {
 #pragma unroll
@@ -385,16 +380,18 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
         const int w4 = warp & 3, part = (warp - kWarpState) >> 2, row = w4 * 32 + lane;
         const uint32_t tX = tmem + ((uint32_t)(w4 * 32) << 16) + kColX + kSlice * part;
         const bool mine = w4 * 32 < D;  // the warp has rows of X
-        int g = 0, items = 0;
+        int g = 0;
         bool ok = true;
-        // 16 columns of this thread's part of X: the sum of its two
+        // 16 columns of this thread's part of X, with what the chunk before has added
         auto take_x = [&](int c, float *x) {
-            float lo[16];
+            float hi[16], lo[16];
             tmem_ld16(tX + c, x);
-            tmem_ld16(tX + c + kColumns, lo);
+            tmem_ld16(tX + kColAdd - kColX + c, hi);
+            tmem_ld16(tX + kColAdd - kColX + kColumns + c, lo);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) f32x2_split(add_f32x2(f32x2(x[i], x[i + 1]), f32x2(lo[i], lo[i + 1])), x[i], x[i + 1]);
+            for (int i = 0; i < 16; i += 2)
+                f32x2_split(add_f32x2(f32x2(x[i], x[i + 1]), add_f32x2(f32x2(hi[i], hi[i + 1]), f32x2(lo[i], lo[i + 1]))), x[i], x[i + 1]);
         };
         for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
             it.set(a, index);
@@ -411,11 +408,25 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(it.from + row * p.d + c0 + c);
                 }
             };
+            float y[kSlice];  // what is written to `to`
             if constexpr (STATES) {
-                if (it.K > 0) {
+#pragma unroll
+                for (int i = 0; i < kSlice; ++i) y[i] = 0.f;
+                // y plus the sum of kSums chunks
+                auto add = [&](int sum) {
+                    if (!mine) return;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < kSlice; c += 16) {
+                        float hi[16], lo[16];
+                        tmem_ld16(tX - kColX + 2 * kColumns * (sum & 1) + c, hi);
+                        tmem_ld16(tX - kColX + 2 * kColumns * (sum & 1) + kColumns + c, lo);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) y[c + i] += hi[i] + lo[i];
+                    }
                     tc_fence_before();
-                    arrive(x_read);  // the item before has been read
-                }
+                };
                 for (int k = 0; k < it.K; ++k, ++g) {
                     const int first = it.first(k), count = it.count(k);
                     const float w = it.q->s * expf(rate * (float)max(it.back ? first + row + 1 : it.rows - 1 - first - row, 0));
@@ -428,20 +439,29 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     }
                     fence_proxy_async_smem();
                     arrive(x_ready + (g & 1));
+                    if (k > 0 && k % kSums == 0) {
+                        if (!(ok = hold(x_full + ((g - 1) & 1), two(g - 1)))) break;
+                        add(k / kSums - 1);
+                    }
                 }
-                if (!ok || (it.K > 0 && !(ok = hold(s_full, one(items))))) break;
-                items += it.K > 0;
+                if (!ok) break;
+                if (it.K > 0) {
+                    if (!(ok = hold(x_full + ((g - 1) & 1), two(g - 1)))) break;
+                    add((it.K - 1) / kSums);
+                }
             } else {
-                // factors of a chunk: of X, of this thread's row of c
-                float keep = 0.f, weight = 0.f;
+                // factors of a chunk: of X (mend: what fp32 leaves of 32 of them, which would add up), of this thread's row of c
+                float keep = 0.f, mend = 0.f, weight = 0.f;
                 int counted = -1;
                 for (int k = 0; k < it.K; ++k, ++g) {
                     const int count = it.count(k);
                     if (count != counted) {
                         counted = count;
                         weight = it.q->s * expf(rate * (float)(it.back ? row + 1 : max(count - 1 - row, 0))), keep = expf(rate * (float)count);
+                        mend = 0.f;
+                        if (it.K > 31 && keep > 0.5f) mend = 32.f * (expm1f(rate * (float)count) - (keep - 1.f));
                     }
-                    // the rows of c, once X of the chunk before is complete
+                    // the rows of c, once the product of the chunk before is complete
                     if (!(ok = hold(full + g % NS, around(g)))) break;
                     if (g > 0 && !(ok = hold(x_full, one(g - 1)))) break;
                     uint8_t *c = stage(g) + G::kC, *hi = sm + G::kW;
@@ -453,11 +473,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                         if (row >= count)
                             for (int x = 0; x < kSlice / 8; ++x) *reinterpret_cast<uint4 *>(c + chunk_at(row, kSlice / 8 * part + x)) = make_uint4(0, 0, 0, 0);
                     }
-                    // the state, once a X~ of the chunk before is complete too
+                    // X~ and X, once a X~ of the chunk before is complete too
                     if (g > 0 && !(ok = hold(over + (g - 1) % NS, around(g - 1)))) break;
-                    if (it.has(k) && mine) {
+                    if ((k == 0 || it.has(k)) && mine) {
                         tc_fence_after();
-                        const uint64_t keep2 = f32x2(keep, keep);
+                        const float by = (k & 31) == 31 ? keep + mend : keep;
+                        const uint64_t keep2 = f32x2(by, by);
 #pragma unroll
                         for (int c = 0; c < kSlice; c += 16) {
                             float x[16];
@@ -471,14 +492,14 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                             for (int i = 0; i < 16; i += 8)
                                 *reinterpret_cast<uint4 *>(sm + G::kImg + chunk_at(row, (kSlice * part + c + i) / 8)) =
                                     make_uint4(pack2(x[i], x[i + 1]), pack2(x[i + 2], x[i + 3]), pack2(x[i + 4], x[i + 5]), pack2(x[i + 6], x[i + 7]));
-                            uint32_t y[16];
+                            uint32_t z[16];
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
                                 float y0, y1;
                                 f32x2_split(mul_f32x2(f32x2(x[i], x[i + 1]), keep2), y0, y1);
-                                y[i] = __float_as_uint(y0), y[i + 1] = __float_as_uint(y1);
+                                z[i] = __float_as_uint(y0), z[i + 1] = __float_as_uint(y1);
                             }
-                            tmem_st16(tX + c, y);
+                            tmem_st16(tX + c, z);
                         }
                         tmem_st_wait();
                     }
@@ -490,14 +511,15 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                 if (!ok || (it.to && it.K > 0 && !(ok = hold(x_full, one(g - 1))))) break;
             }
             if (!it.to || !mine) continue;
-            float x[kSlice];
-            if (it.K > 0) {
-                tc_fence_after();
+            if constexpr (!STATES) {
+                if (it.K > 0) {
+                    tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < kSlice; c += 16) take_x(c, x + c);
-            } else {
+                    for (int c = 0; c < kSlice; c += 16) take_x(c, y + c);
+                } else {
 #pragma unroll
-                for (int i = 0; i < kSlice; i += 4) outside(i, x + i);
+                    for (int i = 0; i < kSlice; i += 4) outside(i, y + i);
+                }
             }
             if (row >= p.d) continue;
 #pragma unroll
@@ -505,9 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                 if (c0 + i >= p.d) continue;
                 if (it.turned) {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) it.to[(c0 + i + y) * p.d + row] = x[i + y];
+                    for (int e = 0; e < 4; ++e) it.to[(c0 + i + e) * p.d + row] = y[i + e];
                 } else {
-                    *reinterpret_cast<float4 *>(it.to + row * p.d + c0 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                    *reinterpret_cast<float4 *>(it.to + row * p.d + c0 + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
                 }
             }
         }
@@ -568,7 +590,6 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     counted = count;
                     by = it.q->w * expf(it.rate * (float)(it.back ? max(count - 1 - row, 0) : row + 1));
                 }
-                const uint32_t tS = lanes + kColS + kRows * (g & 1) + j0;  // P over this warp's own columns
                 if (!(ok = hold(s_full + (g & 1), two(g)))) break;
                 tc_fence_after();
 #pragma unroll
@@ -580,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                         for (int x = 0; x < 16; ++x) packed[x] = 0u;
                     } else {
                         float s[32];
-                        tmem_ld32(tS + y, s);
+                        tmem_ld32(lanes + kColS + j0 + y, s);
                         tmem_ld_wait();
                         if (j0 + y + 32 > count) {  // (0 times what is there may be a NaN)
 #pragma unroll
@@ -594,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                             packed[x] = pack2(s0, s1);
                         }
                     }
-                    tmem_st16(tS + y / 2, packed);
+                    tmem_st16(lanes + kColP + (j0 + y) / 2, packed);
                 }
                 tmem_st_wait();
             }

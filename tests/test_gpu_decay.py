@@ -117,6 +117,24 @@ def test_rounding(aa, dtype, d):
         assert rel(t, name) <= 1e-5, name
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("heads", [1, 160], ids=["segments", "whole"])
+def test_a_state_that_loses_nothing(aa, dtype, heads):
+    # Positive numbers whose sum is longer than 2^8 chunks: a sum that is cut off, not rounded, loses half a step of itself at each
+    # addition.  One rounding to nearest a chunk (of 64 rows at least: 2^-24 each), and the sum of a chunk, of 16 products
+    # at a time, each of which may lose as many last bits (8 products of 2^-20 x 2^-1 at most).
+    n, d = 32768, 64
+    g = torch.Generator(device="cuda").manual_seed(heads)
+    K, V = ((torch.rand(1, 1, n, d, generator=g, device="cuda") + 0.5).to(DT[dtype]).expand(1, heads, n, d).contiguous() for _ in range(2))
+    last = aa.decay_forward(K, K, V, torch.zeros(heads, device="cuda"), None, return_state=True)[1]
+    want = K[0, 0].double().t() @ V[0, 0].double()
+    off = ((last.double() - want) / want).abs().max().item()
+    assert off < (n // 64) * 2.0 ** -24 + 8 * 2.0 ** -21, off
+    # bf16 rows count as they are (weights of 1): chunks of 128
+    if dtype == "bf16":
+        assert off < (n // 128) * 2.0 ** -24 + 8 * 2.0 ** -21, off
+
+
 @pytest.mark.parametrize("d", [16, 64, 128])
 def test_gradients_by_differences(aa, d):
     """H and the last states are linear in each of Q, K, V and the first states, so that a difference of any size is the
