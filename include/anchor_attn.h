@@ -439,7 +439,7 @@ ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_cross_backward(const anchor_att
  *   token (NULL: zeros) and behind the last one that counts (NULL: not wanted), and their gradients
  * Rows of H, dQ, dK and dV from an entry's length on are zero; what the inputs hold there does not matter.  (Before it
  * an infinity or a NaN at a token may reach the rows of up to 127 tokens before it.)  Heads or entries that share
- * rows by a stride of 0 get gradients of their own.
+ * rows by a stride of 0 get gradients of their own.  An infinity in a row or a state counts as a NaN.
  * bf16 in and out (tensor cores: bf16 operands and fp32 accumulators; the weights of pairs and the state are rounded
  * to bf16 where they meet c and a, the state itself is kept in fp32) or fp32 (CUDA cores, fp32 throughout).
  * d in {16, 32, 64, 128}; B * heads <= 2^24, B * heads * n <= 2^31 - 1024.  No output may overlap an input or another

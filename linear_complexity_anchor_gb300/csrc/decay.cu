@@ -85,11 +85,12 @@ anchor_attn_status_t check_sizes(int dtype, int B, int heads, int n, int d, floa
 
 bool misaligned(const void *p, unsigned bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
 
-// Segments of a sequence: as many as take the least time, by what 128 rows of an item (64 columns of one pass of one head) take, as
-// segments' sums and in a pass, in us, what an item takes to begin and to end, rounds of items over the SMs, two launches more, and
-// their states, one after the other and through L2.  None where the items fill the SMs: segments read b and c twice.  Measured (us): bf16, d = 128, 4 x 16 heads x 16384: one segment 247, two 320; 2 x 16 x
-// 8192: 121, 105, three 130; 16 x 16384: one 231, two 172, four 113, eight 128; 16 x 2049: one 35, four 37; d = 64, 12 x 16384:
-// one 160, ten 46; one head of 32768: one 312, ten 60, 32: 35.
+// Segments of a sequence: as many as take the least time, by what 128 rows of an item (64 columns of one pass of one head) take,
+// in a pass and for a segment's sums, in us, what an item takes to begin and to end, rounds of items over the SMs, two launches
+// more, and the segments' states, one after the other and through L2.  None where the items fill the SMs: segments read b and c
+// twice.  Measured (us): bf16, d = 128, 4 x 16 heads x 16384: one segment 247, two 320; 2 x 16 x 8192: 121, 105, three 130;
+// 16 x 16384: one 231, two 172, four 113, eight 128; 16 x 2049: one 35, four 37; d = 64, 12 x 16384: one 160, ten 46; one head
+// of 32768: one 312, ten 60, 32: 35.
 void plan(DecayProblem &p) {
     const float pass = p.f32 ? 10.f : p.d == 128 ? 1.88f : 1.38f, sums = pass * 0.48f, item = 2.2f, launches = 16.f;
     const long long slices = p.slices(), halves = p.d == 128 ? 2 : 1;
@@ -105,7 +106,7 @@ void plan(DecayProblem &p) {
         if (s == 1 || t < best) best = t, want = s;
     }
     p.seg = (tiles + want - 1) / want * 128;
-    p.segs = std::max(1, (p.n + p.seg - 1) / p.seg);
+    p.segs = std::max(1, (int)(((long long)p.n + p.seg - 1) / p.seg));
 }
 
 // A call of few tokens goes token by token, which costs more with each, where a chunk costs the same for all (64 x 32 heads, d =

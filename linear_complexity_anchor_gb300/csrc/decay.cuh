@@ -27,7 +27,6 @@ struct DecayPass {
     int kind;             // of the state: which of the workspace's
 };
 
-// One pass whose state alone is wanted, for the segments of a sequence: b, c, s, back of the passes of its kind.
 struct DecayProblem {
     DecayPass pass[3];
     int passes;
@@ -50,12 +49,17 @@ __device__ __forceinline__ float decay_rate(const float *log_decay, int h) {
     const float g = __ldg(log_decay + h);
     return g > 0.f ? 0.f : g < -1e4f ? -1e4f : g;
 }
+// What fp32 leaves of `of` factors keep = exp(x).  Rounded the same way each time, it would add up over a sequence that keeps most
+// of its state: 3e-8 of it a factor.  For x above -1/16 (below, sixteen factors are all that matters): exp(x) - 1 by its series,
+// which is off by 1e-10 there, less keep - 1, which is exact.
+__device__ __forceinline__ float decay_rest(float x, float keep, float of) {
+    const float e = x * fmaf(x, fmaf(x, fmaf(x, fmaf(x, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f), 1.f);
+    return x > -0.0625f ? of * (e - (keep - 1.f)) : 0.f;
+}
 // the rows of segment `s` that count, of an entry with L
 __device__ __forceinline__ int decay_rows(const DecayProblem &p, int s, int L) { return min(max(L - s * p.seg, 0), p.seg); }
 
-// the sums of each segment but the last (in time) of each kind, the states that segments begin with, the passes
-cudaError_t launch_decay_prefix(const DecayProblem &p, cudaStream_t stream);
-// fp32, CUDA cores
+// The sums of each segment but the last (in time) of each kind, and the passes: fp32, CUDA cores
 cudaError_t launch_decay_simt_states(const DecayProblem &p, cudaStream_t stream);
 cudaError_t launch_decay_simt(const DecayProblem &p, cudaStream_t stream);
 // bf16, tensor cores

@@ -164,7 +164,8 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const __grid_const
                 for (int c = 0; c < NC; ++c) to[c] = o[i][c];
             }
         }
-        const float keep = pw[count];
+        float keep = pw[count];
+        if ((k & 31) == 31) keep += decay_rest(rate * (float)count, keep, 32.f);
 #pragma unroll
         for (int i = 0; i < NB; ++i)
 #pragma unroll
@@ -186,7 +187,8 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const __grid_const
     if (!STATES) {
         // rows of the segment from the length on
         const int end = min(p.seg, p.n - r0);
-        for (int e = threadIdx.x; e < max(end - rows, 0) * CB; e += kThreads)
+        const long long left = max(end - rows, 0) * (long long)CB;
+        for (long long e = threadIdx.x; e < left; e += kThreads)
             O[(long long)(r0 + rows + e / CB) * q.o.sn + cb * CB + e % CB] = 0.f;
     }
     float *to = STATES ? p.states + (((long long)blockIdx.y * p.slices() + slice) * p.segs + seg) * D * D

@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kThreads, 6) decay_step_kernel(const __grid_co
         x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (held && p.from && (D % R == 0 || r < D)) x[i] = *reinterpret_cast<const float4 *>(p.from + offset + (long long)(r + i * R) * D);
     }
-    const float rate = decay_rate(p.log_decay, h), g = expf(rate);
+    const float rate = decay_rate(p.log_decay, h), g = expf(rate), rest = decay_rest(rate, g, 1.f);
     // Entries that share a slot are taken in order by the CTA of the first.
     bool more = false;
     if (p.slots && held) {
@@ -70,8 +70,8 @@ __global__ void __launch_bounds__(kThreads, 6) decay_step_kernel(const __grid_co
             for (int i = 0; i < N; ++i) {
                 if (D % R != 0 && r >= D) continue;
                 const float k = sk[buf][r + i * R], q = sq[buf][r + i * R];
-                x[i].x = fmaf(x[i].x, g, k * v.x), x[i].y = fmaf(x[i].y, g, k * v.y);
-                x[i].z = fmaf(x[i].z, g, k * v.z), x[i].w = fmaf(x[i].w, g, k * v.w);
+                x[i].x = fmaf(x[i].x, g, fmaf(x[i].x, rest, k * v.x)), x[i].y = fmaf(x[i].y, g, fmaf(x[i].y, rest, k * v.y));
+                x[i].z = fmaf(x[i].z, g, fmaf(x[i].z, rest, k * v.z)), x[i].w = fmaf(x[i].w, g, fmaf(x[i].w, rest, k * v.w));
                 o.x = fmaf(q, x[i].x, o.x), o.y = fmaf(q, x[i].y, o.y), o.z = fmaf(q, x[i].z, o.z), o.w = fmaf(q, x[i].w, o.w);
             }
 #pragma unroll

@@ -458,8 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     if (count != counted) {
                         counted = count;
                         weight = it.q->s * expf(rate * (float)(it.back ? row + 1 : max(count - 1 - row, 0))), keep = expf(rate * (float)count);
-                        mend = 0.f;
-                        if (it.K > 31 && keep > 0.5f) mend = 32.f * (expm1f(rate * (float)count) - (keep - 1.f));
+                        mend = it.K > 31 ? decay_rest(rate * (float)count, keep, 32.f) : 0.f;
                     }
                     // the rows of c, once the product of the chunk before is complete
                     if (!(ok = hold(full + g % NS, around(g)))) break;
@@ -559,9 +558,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     it.set(a, index);
                     // chunks of the segment from the length on
                     __nv_bfloat16 *O = (__nv_bfloat16 *)it.q->o.ptr + it.b * it.q->o.sb + it.h * it.q->o.sh + it.r0 * it.q->o.sn + it.half * kColumns;
-                    const int per = min(p.d, kColumns) / 8, left = max(it.end - it.K * kRows, 0) * per;
-                    for (int e = threadIdx.x; e < left; e += 32 * kGroup)
-                        *reinterpret_cast<uint4 *>(O + (long long)(it.K * kRows + e / per) * it.q->o.sn + e % per * 8) = make_uint4(0, 0, 0, 0);
+                    const int per = min(p.d, kColumns) / 8, col = (int)threadIdx.x % per * 8;
+                    for (int x = it.K * kRows + (int)threadIdx.x / per; x < it.end; x += 32 * kGroup / per)
+                        *reinterpret_cast<uint4 *>(O + (long long)x * it.q->o.sn + col) = make_uint4(0, 0, 0, 0);
                 } while (it.K == 0);
                 if (more) {
                     // P's factors for this thread's columns, p g^(i - j) (backward g^(j - i)), 0 on the other side of the diagonal

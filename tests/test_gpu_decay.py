@@ -135,6 +135,30 @@ def test_a_state_that_loses_nothing(aa, dtype, heads):
         assert off < (n // 128) * 2.0 ** -24 + 8 * 2.0 ** -21, off
 
 
+@pytest.mark.parametrize("dtype,B,n", [("bf16", 8, 65536), ("f32", 8, 32768), ("f32", 1, 32768), ("bf16", 1, 4096), ("f32", 1, 4096)],
+                         ids=["bf16", "f32", "segments", "steps-bf16", "steps-f32"])
+def test_a_state_that_fades_slowly(aa, dtype, B, n):
+    # Tokens of zeros: the state behind them is exp(n log_decay) of the one before.  A factor that is rounded the same way each time
+    # would add up to n / 64 2^-25 of it (token by token: n 2^-25).  What may be left: one rounding to nearest for each
+    # factor, of 2^-24 / sqrt(12) in the mean, and what is made good every 32 factors only.
+    heads, d = 32, 64
+    steps = n == 4096
+    g = torch.Generator(device="cuda").manual_seed(n + B)
+    zero = torch.zeros(B, heads, n, d, device="cuda", dtype=DT[dtype])
+    rate = -1.0 / torch.linspace(2000 if steps else n, 6000 if steps else 4 * n, heads, device="cuda")
+    X = torch.randn(B, heads, d, d, generator=g, device="cuda")
+    if steps:
+        last = X.clone()
+        aa.decay_step(zero, zero, zero, rate, last)
+    else:
+        last = aa.decay_forward(zero, zero, zero, rate, None, state=X, return_state=True)[1]
+    want = X.double() * torch.exp(rate.double() * n).view(1, heads, 1, 1)
+    off = ((last - want).square().sum((0, 2, 3)) / want.square().sum((0, 2, 3))).sqrt()
+    factors = n if steps else n // 64
+    bound = 2 * (factors * 2.0 ** -48 / 12) ** 0.5 + (2.0 ** -24 if steps else 32 * 2.0 ** -25)
+    assert off.max().item() < 2 * bound, (off.max().item(), bound)
+
+
 @pytest.mark.parametrize("d", [16, 64, 128])
 def test_gradients_by_differences(aa, d):
     """H and the last states are linear in each of Q, K, V and the first states, so that a difference of any size is the
