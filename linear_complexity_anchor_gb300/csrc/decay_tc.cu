@@ -9,24 +9,28 @@
 // (a pass backward in time: the other triangle, g^(j-i), g^(count-1-i), g^(j+1), chunks from the last to the first).
 //
 // Roundings: P and X~ to bf16, each once, where they meet c and a; the rows s g^(count-1-j) c_j are two bf16
-// numbers (what the first leaves of them is the second), so that X is off by 3.9e-6 of itself: it is an fp32
-// result, and its own rounding in X~ stays the only one of the part of o that goes by it.  With one number o
-// would carry three roundings there, 1.7 times a lone one, against 1.4.  What a chunk adds to X is a sum of its own, added by
-// the rows, to nearest: the tensor cores' sums are cut off, which over many chunks would add up where X decays slowly (6e-6
-// of a state that reaches 3717 rows back, without a bound at a decay of 0; a loop that sums X there takes 3 % less at d = 64,
-// nothing less at 128).  With X in registers a chunk takes 1.45 and 1.89 us.
+// numbers (what the first leaves of them is the second), so that X's own rounding in X~ stays the only one of the part of o
+// that goes by it (with one number o would carry three, 1.7 times a lone one, against 1.4).  A state that the caller is
+// given is an fp32 result, which two numbers leave off by 3.9e-6 of itself: the chunks that count in it take a third, in the
+// place of c once P c is complete, which leaves 4 to 6e-7, what sums in fp32 do (such a chunk takes 0.5 us more: 4 x 16 heads
+// x 16384, d = 128: 255 us without any, 271, and 279 with those down to e^-2.5; made with the first two, before the products: 281).
+// What a chunk adds to X is a sum of its own, added by the rows, to nearest: the tensor cores' sums are cut off, which over many
+// chunks would add up where X decays slowly (6e-6 of a state that reaches 3717 rows back, without a bound at a decay of 0; a
+// loop that sums X there takes 3 % less at d = 64, nothing less at 128).  With X in registers a chunk took 5 % more at d = 64.
 //
 // Two groups of eight warps, a thread half of a row: the first makes P of the next chunk, and o from its two products; the
 // second the weighted rows of c, X~ and X.  One warp loads tiles by TMA, one stores o's, one issues the products: P c, S of the
 // next chunk, X, a X~, each as soon as its operands are there.  What a chunk takes is the second group's round (weights, X's
 // product, X~, a X~) and the products' operands, which take three quarters of what the shared memory gives; all else is done
-// beside it: 1.38 us at d = 64 and 1.88 at 128, from L2.  With one group for all, one step after the other, 1.6 and 1.9;
+// beside it: 1.40 us at d = 64 and 1.94 at 128, from L2.  With one group for all, one step after the other, 1.6 and 1.9;
 // with a group for each of the four steps 3.9, most of it spent on fetching instructions.
 //
 // STATES: the sums of a segment alone, s sum_j g^(rows-1-j) b_j^T c_j: the last product alone, with weights that count from the
 // segment's end, so that no chunk's sum decays and those of kSums chunks are made in tensor memory.
 #include "cross_tc.cuh"
 #include "decay.cuh"
+
+#include <limits.h>
 
 namespace anchor {
 
@@ -55,7 +59,7 @@ struct Geo {
     static constexpr int kWeighted = STATES ? 2 : 1;  // buffers of the weighted rows of c
     static constexpr int kRing = 0, kW = kRing + kStages * kStage, kImg = kW + kWeighted * 2 * kTileC, kOut = kImg + (STATES ? 0 : D * kColumns * 2),
                          kPow = kOut + (STATES ? 0 : kTileC), kBars = kPow + (STATES ? 0 : kGroup * 64 * 4);
-    static constexpr int kNBars = 2 * kStages + 10, kSmem = kBars + kNBars * 8 + 8;
+    static constexpr int kNBars = 2 * kStages + 12, kSmem = kBars + kNBars * 8 + 8;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -76,7 +80,7 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void 
 template <bool STATES>
 struct Item {
     const DecayPass *q;
-    int which, b, h, slice, seg, half, r0, rows, K, end;  // end: rows of the segment
+    int which, b, h, slice, seg, half, r0, rows, K, end, of, length;  // end: rows of the segment; length: of the entry
     bool back, turned;
     float rate;
     const float *from;  // states outside, or null
@@ -101,11 +105,10 @@ struct Item {
     __device__ __forceinline__ void set(const TcParams &a, int index) {
         const DecayProblem &p = a.p;
         const int segs = STATES ? p.segs - 1 : p.segs;
-        int of;
         const int y = place(a, index, of);
         slice = a.by_segs.of(y);
         b = a.by_heads.of(slice), h = slice - b * p.heads;
-        const int length = next_length;
+        length = next_length;
         rate = next_rate;
         ask(a, index + (int)gridDim.x);
         which = of;
@@ -126,13 +129,23 @@ struct Item {
     __device__ __forceinline__ int first(int k) const { return (back ? K - 1 - k : k) * kRows; }
     __device__ __forceinline__ int count(int k) const { return (back ? k == 0 : k + 1 == K) ? rows - (K - 1) * kRows : kRows; }
     __device__ __forceinline__ bool takes(int k) const { return STATES || k + 1 < K || to != nullptr; }
+    // The chunks that count in a state that the caller is given, from the first (in time), so that their weighted rows are three
+    // numbers: not those of which the decay leaves less than e^-2.
+    __device__ __forceinline__ int first_fine(const TcParams &a) const {
+        bool given = !STATES && to;
+        if (STATES)
+            for (int x = 0; x < a.p.passes; ++x) given = given || (a.p.pass[x].kind == of && a.p.pass[x].last);
+        if (!given) return INT_MAX;
+        const float far = ((float)(back ? K * kRows + r0 : length - r0) + __fdividef(2.f, rate)) * (1.f / kRows);  // (rate 0: all)
+        return far >= 1.f ? (int)far : 0;
+    }
     __device__ __forceinline__ bool has(int k) const { return k > 0 || from != nullptr; }
 };
 
 // This thread's columns of a row of c times its weight w, as two bf16 numbers in two tiles.  `on`: the row counts (else
 // zeros, whatever it holds).  With w = u + v in bf16 (2^-18 of w is left out), h = c u rounded, and l = (c u - h) + c v, of
 // which the first part is exact: three instructions for two numbers.  (From fp32 products
-// the states are off by 2.4e-6 of themselves instead of 3.9e-6, and a chunk takes 3 % more.)
+// the states would be off by 2.4e-6 of themselves instead of 3.9e-6, and a chunk takes 3 to 8 % more.)
 __device__ __forceinline__ void weight_row(const uint8_t *tile, uint8_t *hi, uint8_t *lo, int row, int part, float w, bool on) {
     constexpr int N = kSlice / 8;
     const __nv_bfloat16 u1 = __float2bfloat16_rn(w);
@@ -152,6 +165,23 @@ __device__ __forceinline__ void weight_row(const uint8_t *tile, uint8_t *hi, uin
         }
         *reinterpret_cast<uint4 *>(hi + chunk_at(row, N * part + c)) = h4;
         *reinterpret_cast<uint4 *>(lo + chunk_at(row, N * part + c)) = l4;
+    }
+}
+// What those two leave of the row, a third number, over the row itself.
+__device__ __forceinline__ void rest_row(uint8_t *tile, const uint8_t *hi, const uint8_t *lo, int row, int part, float w) {
+    constexpr int N = kSlice / 8;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+        const int at = chunk_at(row, N * part + c);
+        uint4 *to = reinterpret_cast<uint4 *>(tile + at);
+        const uint4 x4 = *to, h4 = *reinterpret_cast<const uint4 *>(hi + at), l4 = *reinterpret_cast<const uint4 *>(lo + at);
+        auto rest = [&](uint32_t x, uint32_t h, uint32_t l) {
+            const float a = fmaf(__uint_as_float(x << 16), w, -__uint_as_float(h << 16)) - __uint_as_float(l << 16);
+            const uint32_t top = 0xffff0000u;
+            const float b = fmaf(__uint_as_float(x & top), w, -__uint_as_float(h & top)) - __uint_as_float(l & top);
+            return pack2(a, b);
+        };
+        *to = make_uint4(rest(x4.x, h4.x, l4.x), rest(x4.y, h4.y, l4.y), rest(x4.z, h4.z, l4.z), rest(x4.w, h4.w, l4.w));
     }
 }
 
@@ -211,9 +241,11 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G::kBars);
     // full: a stage's tiles have landed; over: the products of its chunk are complete; p_ready: P is there and the o before has
-    // been read; x_ready: so are X~, X and the weighted rows; x_full: so is what the chunk adds to X
+    // been read; x_ready: so are X~, X and the weighted rows; x_full: so is what the chunk adds to X;
+    // c_free: (of a chunk with third numbers) P c is complete; m_ready: they are in the place of c
     uint64_t *full = bars, *over = full + NS, *s_full = over + NS /* [2] */, *p_ready = s_full + 2, *x_ready = p_ready + 1 /* [2] */,
-             *x_full = x_ready + 2 /* [2] */, *staged = x_full + 2, *sent = staged + 1, *done = sent + 1;
+             *x_full = x_ready + 2 /* [2] */, *staged = x_full + 2, *sent = staged + 1, *done = sent + 1,
+             *c_free = done + 1, *m_ready = c_free + 1;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + G::kNBars);
     const DecayProblem &p = a.p;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -229,6 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
         mbar_init(staged, kGroup);
         mbar_init(sent, 1);
         mbar_init(done, 1);
+        mbar_init(c_free, 1);
+        mbar_init(m_ready, kGroup);
         fence_mbar_init();
     }
     if (warp == kWarpIssue) tmem_alloc(s_tmem, kCols);
@@ -295,16 +329,24 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
 #pragma unroll
                 for (int k = 0; k < kRows / 16; ++k) product(tmem + to, b + step_mn(k), w + step_mn(k), idX, !fresh || k > 0 ? 1u : 0u);
             };
-            int g = 0, scored = 0;  // scored: chunks whose S has been issued
+            // and b^T times the third numbers, to the second half
+            auto product_m = [&](int g, uint32_t to) {
+                const uint64_t b = smem_desc_sw128(at(g) + G::kB, kBlock, 1024), m = desc_mn(at(g) + G::kC);
+#pragma unroll
+                for (int k = 0; k < kRows / 16; ++k) product(tmem + to + kColumns, b + step_mn(k), m + step_mn(k), idO | 1u << 15, 1u);
+            };
+            int g = 0, scored = 0, fines = 0;  // scored: chunks whose S has been issued; fines: chunks with third numbers
             bool ok = true;
             for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
                 it.set(a, index);
+                const int fine = it.first_fine(a);
                 for (int k = 0; k < it.K && ok; ++k, ++g) {
                     const int st = g % NS;
                     if constexpr (STATES) {
                         if (!(ok = all_hold(x_ready + (g & 1), two(g)))) break;
                         tc_fence_after();
                         product_x(g, 2 * kColumns * (k / kSums & 1), k % kSums == 0);
+                        if (k >= fine) product_m(g, 2 * kColumns * (k / kSums & 1));
                         commit(x_full + (g & 1));
                         commit(over + st);
                     } else {
@@ -335,10 +377,17 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
 #pragma unroll
                                 for (int s = 0; s < kRows / 16; ++s)
                                     product_tmem(tmem + kColIn, tmem + kColP + 8 * s, cd + step_mn(s), idO, s > 0 ? 1u : 0u);
+                                if (k >= fine) commit(c_free);
                             } else {
                                 if (!partial && !(ok = all_hold(x_ready, one(g)))) break;
                                 tc_fence_after();
                                 if (it.takes(k)) product_x(g, kColAdd, true);
+                                if (k >= fine) {
+                                    if (!(ok = all_hold(m_ready, one(fines)))) break;
+                                    ++fines;
+                                    tc_fence_after();
+                                    product_m(g, kColAdd);
+                                }
                                 commit(x_full);
                                 if (it.has(k)) {
 #pragma unroll
@@ -380,8 +429,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
         const int w4 = warp & 3, part = (warp - kWarpState) >> 2, row = w4 * 32 + lane;
         const uint32_t tX = tmem + ((uint32_t)(w4 * 32) << 16) + kColX + kSlice * part;
         const bool mine = w4 * 32 < D;  // the warp has rows of X
-        int g = 0;
+        int g = 0, fines = 0;
         bool ok = true;
+        // this thread's part of a row of c
+        auto zero_part = [&](uint8_t *c) {
+            for (int x = 0; x < kSlice / 8; ++x) *reinterpret_cast<uint4 *>(c + chunk_at(row, kSlice / 8 * part + x)) = make_uint4(0, 0, 0, 0);
+        };
         // 16 columns of this thread's part of X, with what the chunk before has added
         auto take_x = [&](int c, float *x) {
             float hi[16], lo[16];
@@ -396,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
         for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
             it.set(a, index);
             const float rate = it.rate;
+            const int fine = it.first_fine(a);
             const int c0 = it.half * kColumns + kSlice * part;  // this thread's columns of the state
             // four columns of this thread's row of the state outside (zeros where there is none)
             auto outside = [&](int c, float *x) {
@@ -433,10 +487,13 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     if (!(ok = hold(full + g % NS, around(g)))) break;
                     if (g > 1 && !(ok = hold(x_full + (g & 1), two(g - 2)))) break;
                     uint8_t *hi = sm + G::kW + (g & 1) * 2 * kTileC;
-                    weight_row(stage(g) + G::kC, hi, hi + kTileC, row, part, w, row < count);
+                    uint8_t *c = stage(g) + G::kC;
+                    weight_row(c, hi, hi + kTileC, row, part, w, row < count);
                     if (count < kRows) {  // zeros, whatever is there, in the other operand too
                         if (part == 0) zero_rows<D>(stage(g) + G::kB, row, count, kRows);
+                        if (row >= count) zero_part(c);
                     }
+                    if (k >= fine) rest_row(c, hi, hi + kTileC, row, part, w);
                     fence_proxy_async_smem();
                     arrive(x_ready + (g & 1));
                     if (k > 0 && k % kSums == 0) {
@@ -469,8 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                         // zeros, whatever is there, in both operands of X and in that of P c (S may be reading b: what it makes of
                         // these rows is masked)
                         if (part == 0) zero_rows<D>(stage(g) + G::kB, row, count, kRows);
-                        if (row >= count)
-                            for (int x = 0; x < kSlice / 8; ++x) *reinterpret_cast<uint4 *>(c + chunk_at(row, kSlice / 8 * part + x)) = make_uint4(0, 0, 0, 0);
+                        if (row >= count) zero_part(c);
                     }
                     // X~ and X, once a X~ of the chunk before is complete too
                     if (g > 0 && !(ok = hold(over + (g - 1) % NS, around(g - 1)))) break;
@@ -505,6 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     fence_proxy_async_smem();
                     tc_fence_before();
                     arrive(x_ready);
+                    if (k >= fine) {
+                        if (!(ok = hold(c_free, one(fines)))) break;
+                        ++fines;
+                        rest_row(c, hi, hi + kTileC, row, part, weight);
+                        fence_proxy_async_smem();
+                        arrive(m_ready);
+                    }
                 }
                 // (the last product, before X is read here or X~ is written for the next item)
                 if (!ok || (it.to && it.K > 0 && !(ok = hold(x_full, one(g - 1))))) break;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from tests.conftest import gpu_available
-from tests.decay_reference import decay_reference
+from tests.decay_reference import decay_reference, lengths_of, powers
 from tests.ops_reference import assert_within, half_step
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a CUDA GPU")]
@@ -157,6 +157,24 @@ def test_a_state_that_fades_slowly(aa, dtype, B, n):
     factors = n if steps else n // 64
     bound = 2 * (factors * 2.0 ** -48 / 12) ** 0.5 + (2.0 ** -24 if steps else 32 * 2.0 ** -25)
     assert off.max().item() < 2 * bound, (off.max().item(), bound)
+
+
+@pytest.mark.parametrize("B,heads,n,d", [(4, 8, 197, 64), (2, 8, 3000, 64), (1, 8, 9000, 128), (40, 8, 1000, 32), (20, 8, 700, 128)])
+def test_states_are_fp32_results(aa, B, heads, n, d):
+    # What the rows of bf16 leave is less than 2^-18 in the mean where the decay leaves e^-2 of it, 2^-24 elsewhere; the sum of a
+    # chunk is cut off at each of 8 products (2^-25 in the mean), and one rounding a chunk is to nearest: 0.8e-6 in all.
+    x = make(d + n, B, heads, n, d, "bf16", state=True, train=True, ragged=True)
+    x["log_decay"] = -1.0 / torch.tensor([3.0, 30.0, 60.0, 130.0, 400.0, 900.0, 4000.0, 1e6], device="cuda")
+    last, first = forward(aa, x, scale=0.5)[1], backward(aa, x, scale=0.5)[3]
+    L, i = lengths_of(x["lengths"], B, n, "cuda"), torch.arange(n, device="cuda")
+    on = (i[None] < L[:, None])[:, None, :, None]
+    q, k, v, dh = (torch.where(on, x[name].double(), 0.0) for name in ("Q", "K", "V", "dH"))
+    whole = powers(x["log_decay"], L).transpose(0, 1)[..., None, None]
+    rest = powers(x["log_decay"], L[:, None] - 1 - i[None]).transpose(0, 1)[..., None]
+    ahead = powers(x["log_decay"], i + 1)[None, ..., None]
+    for got, want in ((last, (k * rest).mT @ v + whole * x["state"].double()), (first, 0.5 * (q * ahead).mT @ dh + whole * x["dlast"].double())):
+        off = ((got.double() - want).square().sum((0, 2, 3)) / want.square().sum((0, 2, 3))).sqrt()
+        assert off.max().item() < 1e-6, off
 
 
 @pytest.mark.parametrize("d", [16, 64, 128])
