@@ -11,9 +11,12 @@
 // Roundings: P and X~ to bf16, each once, where they meet c and a; the rows s g^(count-1-j) c_j are two bf16
 // numbers (what the first leaves of them is the second), so that X's own rounding in X~ stays the only one of the part of o
 // that goes by it (with one number o would carry three, 1.7 times a lone one, against 1.4).  A state that the caller is
-// given is an fp32 result, which two numbers leave off by 3.9e-6 of itself: the chunks that count in it take a third, in the
-// place of c once P c is complete, which leaves 4 to 6e-7, what sums in fp32 do (such a chunk takes 0.5 us more: 4 x 16 heads
-// x 16384, d = 128: 255 us without any, 271, and 279 with those down to e^-2.5; made with the first two, before the products: 281).
+// given is an fp32 result, which two numbers leave off by 3.9e-6 of itself.  So the chunks that count in it take a third
+// product.  Heads that keep 0.73 of a state over a chunk: with m the weight of its middle row, b^T c itself and b^T times the
+// rows of weight w / m - 1, whose roundings are less by as much; X takes m times their sum (such a chunk takes 0.2 us more).
+// Others: the rows in three numbers, the third in the place of c once P c is complete (0.5 us).  A state is then off by 4 to 7e-7,
+// as sums in fp32 are.  (4 x 16 heads x 16384, d = 128: 255 us without, 261, and 271 with three numbers throughout; made with the
+// first two, before the products, 281; 128 x 12 x 197, d = 64: 78, 90.)
 // What a chunk adds to X is a sum of its own, added by the rows, to nearest: the tensor cores' sums are cut off, which over many
 // chunks would add up where X decays slowly (6e-6 of a state that reaches 3717 rows back, without a bound at a decay of 0; a
 // loop that sums X there takes 3 % less at d = 64, nothing less at 128).  With X in registers a chunk took 5 % more at d = 64.
@@ -22,7 +25,7 @@
 // second the weighted rows of c, X~ and X.  One warp loads tiles by TMA, one stores o's, one issues the products: P c, S of the
 // next chunk, X, a X~, each as soon as its operands are there.  What a chunk takes is the second group's round (weights, X's
 // product, X~, a X~) and the products' operands, which take three quarters of what the shared memory gives; all else is done
-// beside it: 1.40 us at d = 64 and 1.94 at 128, from L2.  With one group for all, one step after the other, 1.6 and 1.9;
+// beside it: 1.42 us at d = 64 and 1.94 at 128, from L2.  With one group for all, one step after the other, 1.6 and 1.9;
 // with a group for each of the four steps 3.9, most of it spent on fetching instructions.
 //
 // STATES: the sums of a segment alone, s sum_j g^(rows-1-j) b_j^T c_j: the last product alone, with weights that count from the
@@ -139,6 +142,8 @@ struct Item {
         const float far = ((float)(back ? K * kRows + r0 : length - r0) + __fdividef(2.f, rate)) * (1.f / kRows);  // (rate 0: all)
         return far >= 1.f ? (int)far : 0;
     }
+    // of these, those of a head that keeps most of a state over a chunk: weights apart from the one of the middle row
+    __device__ __forceinline__ bool centred() const { return !STATES && rate > -0.0025f; }
     __device__ __forceinline__ bool has(int k) const { return k > 0 || from != nullptr; }
 };
 
@@ -340,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
             for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
                 it.set(a, index);
                 const int fine = it.first_fine(a);
+                const bool centred = it.centred();
                 for (int k = 0; k < it.K && ok; ++k, ++g) {
                     const int st = g % NS;
                     if constexpr (STATES) {
@@ -377,15 +383,17 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
 #pragma unroll
                                 for (int s = 0; s < kRows / 16; ++s)
                                     product_tmem(tmem + kColIn, tmem + kColP + 8 * s, cd + step_mn(s), idO, s > 0 ? 1u : 0u);
-                                if (k >= fine) commit(c_free);
+                                if (k >= fine && !centred) commit(c_free);
                             } else {
                                 if (!partial && !(ok = all_hold(x_ready, one(g)))) break;
                                 tc_fence_after();
                                 if (it.takes(k)) product_x(g, kColAdd, true);
                                 if (k >= fine) {
-                                    if (!(ok = all_hold(m_ready, one(fines)))) break;
-                                    ++fines;
-                                    tc_fence_after();
+                                    if (!centred) {
+                                        if (!(ok = all_hold(m_ready, one(fines)))) break;
+                                        ++fines;
+                                        tc_fence_after();
+                                    }
                                     product_m(g, kColAdd);
                                 }
                                 commit(x_full);
@@ -436,7 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
             for (int x = 0; x < kSlice / 8; ++x) *reinterpret_cast<uint4 *>(c + chunk_at(row, kSlice / 8 * part + x)) = make_uint4(0, 0, 0, 0);
         };
         // 16 columns of this thread's part of X, with what the chunk before has added
-        auto take_x = [&](int c, float *x) {
+        auto take_x = [&](int c, float *x, float f) {
+            const uint64_t f2 = f32x2(f, f);
             float hi[16], lo[16];
             tmem_ld16(tX + c, x);
             tmem_ld16(tX + kColAdd - kColX + c, hi);
@@ -444,12 +453,13 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 16; i += 2)
-                f32x2_split(add_f32x2(f32x2(x[i], x[i + 1]), add_f32x2(f32x2(hi[i], hi[i + 1]), f32x2(lo[i], lo[i + 1]))), x[i], x[i + 1]);
+                f32x2_split(fma_f32x2(f2, add_f32x2(f32x2(hi[i], hi[i + 1]), f32x2(lo[i], lo[i + 1])), f32x2(x[i], x[i + 1])), x[i], x[i + 1]);
         };
         for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
             it.set(a, index);
             const float rate = it.rate;
             const int fine = it.first_fine(a);
+            const bool centred = it.centred();
             const int c0 = it.half * kColumns + kSlice * part;  // this thread's columns of the state
             // four columns of this thread's row of the state outside (zeros where there is none)
             auto outside = [&](int c, float *x) {
@@ -462,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(it.from + row * p.d + c0 + c);
                 }
             };
-            float y[kSlice];  // what is written to `to`
+            float y[kSlice], mid = 1.f;  // what is written to `to`; the weight that chunks are taken apart from
             if constexpr (STATES) {
 #pragma unroll
                 for (int i = 0; i < kSlice; ++i) y[i] = 0.f;
@@ -508,13 +518,17 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                 }
             } else {
                 // factors of a chunk: of X (mend: what fp32 leaves of 32 of them, which would add up), of this thread's row of c
-                float keep = 0.f, mend = 0.f, weight = 0.f;
+                float keep = 0.f, mend = 0.f, weight = 0.f, was = 1.f;
                 int counted = -1;
                 for (int k = 0; k < it.K; ++k, ++g) {
                     const int count = it.count(k);
-                    if (count != counted) {
+                    was = mid;
+                    if (count != counted || k == fine) {
                         counted = count;
-                        weight = it.q->s * expf(rate * (float)(it.back ? row + 1 : max(count - 1 - row, 0))), keep = expf(rate * (float)count);
+                        const float far = (float)(it.back ? row + 1 : max(count - 1 - row, 0));
+                        if (centred && k >= fine) weight = expf(rate * (far - 64.f)) - 1.f, mid = it.q->s * expf(rate * 64.f);
+                        else weight = it.q->s * expf(rate * far);
+                        keep = expf(rate * (float)count);
                         mend = it.K > 31 ? decay_rest(rate * (float)count, keep, 32.f) : 0.f;
                     }
                     // the rows of c, once the product of the chunk before is complete
@@ -538,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                         for (int c = 0; c < kSlice; c += 16) {
                             float x[16];
                             if (k > 0) {
-                                take_x(c, x);
+                                take_x(c, x, was);
                             } else {
 #pragma unroll
                                 for (int i = 0; i < 16; i += 4) outside(c + i, x + i);
@@ -561,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     fence_proxy_async_smem();
                     tc_fence_before();
                     arrive(x_ready);
-                    if (k >= fine) {
+                    if (k >= fine && !centred) {
                         if (!(ok = hold(c_free, one(fines)))) break;
                         ++fines;
                         rest_row(c, hi, hi + kTileC, row, part, weight);
@@ -577,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                 if (it.K > 0) {
                     tc_fence_after();
 #pragma unroll
-                    for (int c = 0; c < kSlice; c += 16) take_x(c, y + c);
+                    for (int c = 0; c < kSlice; c += 16) take_x(c, y + c, mid);
                 } else {
 #pragma unroll
                     for (int i = 0; i < kSlice; i += 4) outside(i, y + i);
