@@ -92,7 +92,7 @@ bool misaligned(const void *p, unsigned bytes) { return ((uintptr_t)p & (bytes -
 // 16 x 16384: one 231, two 172, four 113, eight 128; 16 x 2049: one 35, four 37; d = 64, 12 x 16384: one 160, ten 46; one head
 // of 32768: one 312, ten 60, 32: 35.
 void plan(DecayProblem &p) {
-    const float pass = p.f32 ? 10.f : p.d == 128 ? 1.94f : 1.42f, sums = pass * 0.48f, item = 2.2f, launches = 16.f;
+    const float pass = p.f32 ? 10.f : p.d == 128 ? 1.88f : 1.38f, sums = pass * 0.48f, item = 2.2f, launches = 16.f;
     const long long slices = p.slices(), halves = p.d == 128 ? 2 : 1;
     const int tiles = (p.n + 127) / 128, most = (int)std::max<long long>(1, std::min<long long>(4 * kPlanSMs / (slices * halves), tiles / 2));
     auto rounds = [](long long items) { return (float)((items + kPlanSMs - 1) / kPlanSMs); };

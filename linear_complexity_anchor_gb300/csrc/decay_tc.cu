@@ -25,11 +25,12 @@
 // second the weighted rows of c, X~ and X.  One warp loads tiles by TMA, one stores o's, one issues the products: P c, S of the
 // next chunk, X, a X~, each as soon as its operands are there.  What a chunk takes is the second group's round (weights, X's
 // product, X~, a X~) and the products' operands, which take three quarters of what the shared memory gives; all else is done
-// beside it: 1.42 us at d = 64 and 1.94 at 128, from L2.  With one group for all, one step after the other, 1.6 and 1.9;
+// beside it: 1.38 us at d = 64 and 1.88 at 128, from L2, without a state for the caller.  With one group for all, one step after the other, 1.6 and 1.9;
 // with a group for each of the four steps 3.9, most of it spent on fetching instructions.
 //
 // STATES: the sums of a segment alone, s sum_j g^(rows-1-j) b_j^T c_j: the last product alone, with weights that count from the
 // segment's end, so that no chunk's sum decays and those of kSums chunks are made in tensor memory.
+// KEPT: a state is given to the caller.  (A call without one takes 3 % less in a kernel without that code.)
 #include "cross_tc.cuh"
 #include "decay.cuh"
 
@@ -239,7 +240,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t at, float *v) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-template <int D, bool STATES>
+template <int D, bool STATES, bool KEPT>
 __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constant__ TcParams a) {
     using G = Geo<D, STATES>;
     constexpr int NS = G::kStages;
@@ -344,15 +345,16 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
             bool ok = true;
             for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
                 it.set(a, index);
-                const int fine = it.first_fine(a);
+                const int first_fine = KEPT ? it.first_fine(a) : 0;
                 const bool centred = it.centred();
+                auto fine = [&](int k) { return KEPT && k >= first_fine; };
                 for (int k = 0; k < it.K && ok; ++k, ++g) {
                     const int st = g % NS;
                     if constexpr (STATES) {
                         if (!(ok = all_hold(x_ready + (g & 1), two(g)))) break;
                         tc_fence_after();
                         product_x(g, 2 * kColumns * (k / kSums & 1), k % kSums == 0);
-                        if (k >= fine) product_m(g, 2 * kColumns * (k / kSums & 1));
+                        if (fine(k)) product_m(g, 2 * kColumns * (k / kSums & 1));
                         commit(x_full + (g & 1));
                         commit(over + st);
                     } else {
@@ -383,12 +385,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
 #pragma unroll
                                 for (int s = 0; s < kRows / 16; ++s)
                                     product_tmem(tmem + kColIn, tmem + kColP + 8 * s, cd + step_mn(s), idO, s > 0 ? 1u : 0u);
-                                if (k >= fine && !centred) commit(c_free);
+                                if (fine(k) && !centred) commit(c_free);
                             } else {
                                 if (!partial && !(ok = all_hold(x_ready, one(g)))) break;
                                 tc_fence_after();
                                 if (it.takes(k)) product_x(g, kColAdd, true);
-                                if (k >= fine) {
+                                if (fine(k)) {
                                     if (!centred) {
                                         if (!(ok = all_hold(m_ready, one(fines)))) break;
                                         ++fines;
@@ -458,8 +460,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
         for (int index = blockIdx.x; index < a.items && ok; index += gridDim.x) {
             it.set(a, index);
             const float rate = it.rate;
-            const int fine = it.first_fine(a);
+            const int first_fine = KEPT ? it.first_fine(a) : 0;
             const bool centred = it.centred();
+            auto fine = [&](int k) { return KEPT && k >= first_fine; };
             const int c0 = it.half * kColumns + kSlice * part;  // this thread's columns of the state
             // four columns of this thread's row of the state outside (zeros where there is none)
             auto outside = [&](int c, float *x) {
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                         if (part == 0) zero_rows<D>(stage(g) + G::kB, row, count, kRows);
                         if (row >= count) zero_part(c);
                     }
-                    if (k >= fine) rest_row(c, hi, hi + kTileC, row, part, w);
+                    if (fine(k)) rest_row(c, hi, hi + kTileC, row, part, w);
                     fence_proxy_async_smem();
                     arrive(x_ready + (g & 1));
                     if (k > 0 && k % kSums == 0) {
@@ -523,10 +526,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                 for (int k = 0; k < it.K; ++k, ++g) {
                     const int count = it.count(k);
                     was = mid;
-                    if (count != counted || k == fine) {
+                    if (count != counted || (KEPT && k == first_fine)) {
                         counted = count;
                         const float far = (float)(it.back ? row + 1 : max(count - 1 - row, 0));
-                        if (centred && k >= fine) weight = expf(rate * (far - 64.f)) - 1.f, mid = it.q->s * expf(rate * 64.f);
+                        if (centred && fine(k)) weight = expf(rate * (far - 64.f)) - 1.f, mid = it.q->s * expf(rate * 64.f);
                         else weight = it.q->s * expf(rate * far);
                         keep = expf(rate * (float)count);
                         mend = it.K > 31 ? decay_rest(rate * (float)count, keep, 32.f) : 0.f;
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     fence_proxy_async_smem();
                     tc_fence_before();
                     arrive(x_ready);
-                    if (k >= fine && !centred) {
+                    if (fine(k) && !centred) {
                         if (!(ok = hold(c_free, one(fines)))) break;
                         ++fines;
                         rest_row(c, hi, hi + kTileC, row, part, weight);
@@ -739,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
     if (warp == kWarpIssue) tmem_dealloc(tmem, kCols);
 }
 
-template <int D, bool STATES>
+template <int D, bool STATES, bool KEPT>
 cudaError_t launch(const DecayProblem &p, cudaStream_t stream) {
     TcParams a;
     a.p = p;
@@ -754,19 +757,23 @@ cudaError_t launch(const DecayProblem &p, cudaStream_t stream) {
     a.items = (int)(p.slices() * segs * (STATES ? p.kinds : p.passes) * a.halves);
     a.by_segs = Divide((uint32_t)segs), a.by_heads = Divide((uint32_t)p.heads);
     static SmemOnce once;
-    const cudaError_t e = once(decay_kernel<D, STATES>, Geo<D, STATES>::kSmem);
+    const cudaError_t e = once(decay_kernel<D, STATES, KEPT>, Geo<D, STATES>::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(decay_kernel<D, STATES>, dim3((unsigned)std::min(a.items, kPlanSMs)), dim3(kThreads), Geo<D, STATES>::kSmem, stream, a);
+    return launch_pdl(decay_kernel<D, STATES, KEPT>, dim3((unsigned)std::min(a.items, kPlanSMs)), dim3(kThreads), Geo<D, STATES>::kSmem, stream, a);
+}
+
+template <bool STATES>
+cudaError_t launch(const DecayProblem &p, cudaStream_t stream) {
+    bool kept = false;
+    for (int i = 0; i < p.passes; ++i) kept = kept || p.pass[i].last;
+    return p.d == 128 ? (kept ? launch<128, STATES, true>(p, stream) : launch<128, STATES, false>(p, stream))
+                      : (kept ? launch<64, STATES, true>(p, stream) : launch<64, STATES, false>(p, stream));
 }
 
 }  // namespace
 
-cudaError_t launch_decay_tc_states(const DecayProblem &p, cudaStream_t stream) {
-    return p.d == 128 ? launch<128, true>(p, stream) : launch<64, true>(p, stream);
-}
-cudaError_t launch_decay_tc(const DecayProblem &p, cudaStream_t stream) {
-    return p.d == 128 ? launch<128, false>(p, stream) : launch<64, false>(p, stream);
-}
+cudaError_t launch_decay_tc_states(const DecayProblem &p, cudaStream_t stream) { return launch<true>(p, stream); }
+cudaError_t launch_decay_tc(const DecayProblem &p, cudaStream_t stream) { return launch<false>(p, stream); }
 cudaError_t decay_read_and_clear_error(unsigned *out) {
     const unsigned zero = 0;
     const cudaError_t e = cudaMemcpyFromSymbol(out, g_decay_error, sizeof(unsigned));
