@@ -179,8 +179,8 @@ def device_error() -> int:
 
 
 def release_workspaces() -> None:
-    """Give the workspaces that cross attention and the norms' backward keep between calls (up to 512 MB a device, outside
-    of torch's allocator) back to the current device; those of calls that have not been waited for stay."""
+    """Give the workspaces that cross attention, the decaying states' segments and the norms' backward keep between calls (up
+    to 512 MB a device, outside of torch's allocator) back to the current device; those of calls that have not been waited for stay."""
     _raise(load().anchor_attn_release_workspaces(), "release_workspaces")
 
 

@@ -140,7 +140,7 @@ struct Item {
         if (STATES)
             for (int x = 0; x < a.p.passes; ++x) given = given || (a.p.pass[x].kind == of && a.p.pass[x].last);
         if (!given) return INT_MAX;
-        const float far = ((float)(back ? K * kRows + r0 : length - r0) + __fdividef(2.f, rate)) * (1.f / kRows);  // (rate 0: all)
+        const float far = ((float)(back ? K * kRows + r0 : length - r0) - __fdividef(2.f, fabsf(rate))) * (1.f / kRows);  // (rate 0: all)
         return far >= 1.f ? (int)far : 0;
     }
     // of these, those of a head that keeps most of a state over a chunk: weights apart from the one of the middle row

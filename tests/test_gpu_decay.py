@@ -177,6 +177,17 @@ def test_states_are_fp32_results(aa, B, heads, n, d):
         assert off.max().item() < 1e-6, off
 
 
+@pytest.mark.parametrize("rate", [0.0, -0.0, 0.7, -1e-30], ids=["zero", "minus-zero", "above", "tiny"])
+@pytest.mark.parametrize("B,n", [(1, 2000), (30, 500)])
+def test_states_of_heads_that_lose_nothing_are_fp32_results(aa, B, n, rate):
+    # as above, with weights that are a scale alone, which is no bf16 number
+    x = make(n, B, 6, n, 64, "bf16", state=True, train=True)
+    x["log_decay"] = torch.full((6,), rate, device="cuda")
+    first = backward(aa, x, scale=0.3)[3].double()
+    want = 0.3 * x["Q"].double().mT @ x["dH"].double() + x["dlast"].double()
+    assert ((first - want).square().sum() / want.square().sum()).sqrt().item() < 1e-6
+
+
 @pytest.mark.parametrize("d", [16, 64, 128])
 def test_gradients_by_differences(aa, d):
     """H and the last states are linear in each of Q, K, V and the first states, so that a difference of any size is the
