@@ -514,7 +514,7 @@ ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_add_norm(const anchor_attn_add_
 ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_add_norm_backward(const anchor_attn_add_norm_t *p, void *stream);
 
 /*
- * Workspaces of cross attention and of the norms' weight gradients come from a pool of the library, one per device, which
+ * Workspaces of cross attention, of the decaying states' segments and of the norms' weight gradients come from a pool of the library, one per device, which
  * keeps up to 512 MB of them between calls (a call after a synchronisation would otherwise map its workspace again,
  * 0.2 ms).  This gives what the current device's pool keeps back to the device; workspaces of calls that have not been
  * waited for stay.  Later calls take memory anew.  Not to be called while a stream is captured.
