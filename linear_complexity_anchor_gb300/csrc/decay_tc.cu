@@ -15,8 +15,8 @@
 // product.  Heads that keep 0.73 of a state over a chunk: with m the weight of its middle row, b^T c itself and b^T times the
 // rows of weight w / m - 1, whose roundings are less by as much; X takes m times their sum (such a chunk takes 0.2 us more).
 // Others: the rows in three numbers, the third in the place of c once P c is complete (0.5 us).  A state is then off by 4 to 7e-7,
-// as sums in fp32 are.  (4 x 16 heads x 16384, d = 128: 255 us without, 261, and 271 with three numbers throughout; made with the
-// first two, before the products, 281; 128 x 12 x 197, d = 64: 78, 90.)
+// as sums in fp32 are.  (4 x 16 heads x 16384, d = 128: 255 us without, 260, and 271 with three numbers throughout; made with the
+// first two, before the products, 281.)
 // What a chunk adds to X is a sum of its own, added by the rows, to nearest: the tensor cores' sums are cut off, which over many
 // chunks would add up where X decays slowly (6e-6 of a state that reaches 3717 rows back, without a bound at a decay of 0; a
 // loop that sums X there takes 3 % less at d = 64, nothing less at 128).  With X in registers a chunk took 5 % more at d = 64.
@@ -65,6 +65,7 @@ struct Geo {
                          kPow = kOut + (STATES ? 0 : kTileC), kBars = kPow + (STATES ? 0 : kGroup * 64 * 4);
     static constexpr int kNBars = 2 * kStages + 12, kSmem = kBars + kNBars * 8 + 8;
     static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(kSlice == 32, "a row's part of a state fills two halves of its weighted rows");
 };
 
 struct TcParams {
@@ -600,17 +601,20 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     for (int i = 0; i < kSlice; i += 4) outside(i, y + i);
                 }
             }
-            if (row >= p.d) continue;
+            // By way of this warp's part of the weighted rows, whose product is complete, so that rows go out 128 bytes at a
+            // time (each thread its own row, 16 bytes at a time: 1.5 us).  Rolled: what an item does once is mostly fetched (128 x
+            // 12 x 197, d = 64: 80 us unrolled, 76).
+            auto at = [&](int r, int x) { return reinterpret_cast<float4 *>(sm + G::kW + (x >> 2) * kTileC + chunk_at(r, 4 * part + (x & 3))); };
 #pragma unroll
-            for (int i = 0; i < kSlice; i += 4) {
-                if (c0 + i >= p.d) continue;
-                if (it.turned) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) it.to[(c0 + i + e) * p.d + row] = y[i + e];
-                } else {
-                    *reinterpret_cast<float4 *>(it.to + row * p.d + c0 + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-                }
+            for (int i = 0; i < 8; ++i) *at(row, i) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            __syncwarp();
+            const int x = lane & 7;
+#pragma unroll 1
+            for (int i = 0; i < 32; i += 4) {
+                const int r = w4 * 32 + i + (lane >> 3);
+                if (r < p.d && c0 + 4 * x < p.d) *reinterpret_cast<float4 *>(it.to + r * p.d + c0 + 4 * x) = *at(r, x);
             }
+            __syncwarp();
         }
         if (!ok) gave_up();
     } else if (!STATES && warp < kWarpState) {
@@ -636,29 +640,31 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                     index += gridDim.x;
                     if (!(more = index < a.items)) break;
                     it.set(a, index);
-                    // chunks of the segment from the length on
-                    __nv_bfloat16 *O = (__nv_bfloat16 *)it.q->o.ptr + it.b * it.q->o.sb + it.h * it.q->o.sh + it.r0 * it.q->o.sn + it.half * kColumns;
-                    const int per = min(p.d, kColumns) / 8, col = (int)threadIdx.x % per * 8;
-                    for (int x = it.K * kRows + (int)threadIdx.x / per; x < it.end; x += 32 * kGroup / per)
-                        *reinterpret_cast<uint4 *>(O + (long long)x * it.q->o.sn + col) = make_uint4(0, 0, 0, 0);
+                    if (it.K * kRows < it.end) {  // chunks of the segment from the length on
+                        __nv_bfloat16 *O = (__nv_bfloat16 *)it.q->o.ptr + it.b * it.q->o.sb + it.h * it.q->o.sh + it.r0 * it.q->o.sn + it.half * kColumns;
+                        const int per = p.d == 16 ? 1 : p.d == 32 ? 2 : 3, col = (int)threadIdx.x % (1 << per) * 8;
+                        for (int x = it.K * kRows + ((int)threadIdx.x >> per); x < it.end; x += 32 * kGroup >> per)
+                            *reinterpret_cast<uint4 *>(O + (long long)x * it.q->o.sn + col) = make_uint4(0, 0, 0, 0);
+                    }
                 } while (it.K == 0);
                 if (more) {
                     // P's factors for this thread's columns, p g^(i - j) (backward g^(j - i)), 0 on the other side of the diagonal
                     const float rate2 = it.rate * kLog2e, scale = it.q->p;
-                    // 32 columns of 32 rows have 63 distances (and one more: there is no column 32)
+                    // 32 columns of 32 rows have 63 distances (and one more, that is not read), in the order in which a row reads them
 #pragma unroll
                     for (int y = 0; y < kP; y += 32) {
+                        if (it.back ? j0 + y < w4 * 32 : j0 + y > w4 * 32) continue;  // (not read)
                         const int least = it.back ? j0 + y - w4 * 32 - 31 : w4 * 32 - j0 - y - 31;  // of lane 0 (backward 31) and column 31 (0)
                         __syncwarp();
 #pragma unroll
                         for (int x = 0; x < 64; x += 32) {
-                            const int far = least + x + lane;
+                            const int far = it.back ? least + x + lane : least + 62 - x - lane;
                             table[x + lane] = far >= 0 ? scale * ex2(rate2 * (float)far) : 0.f;
                         }
                         __syncwarp();
-                        const float *at = table + (it.back ? 31 - lane : 31 + lane);
+                        const float *at = table + 31 - lane;
 #pragma unroll
-                        for (int x = 0; x < 32; x += 2) pf[(y + x) / 2] = it.back ? f32x2(at[x], at[x + 1]) : f32x2(at[-x], at[-x - 1]);
+                        for (int x = 0; x < 32; x += 2) pf[(y + x) / 2] = f32x2(at[x], at[x + 1]);
                     }
                     k = 0, counted = -1;
                 }
