@@ -8,7 +8,9 @@ namespace anchor {
 namespace {
 
 // Four elements of one slice's states a thread: along the segments in time, the sums of a segment alone
-// are replaced by the state before it.  Bound by memory (the sums come from L2).
+// are replaced by the state before it.  Bound by the latency of loads from L2, of which kAhead are in flight (2 heads, d = 128, 16384
+// rows: 6.8 us, one at a time 13.2).
+constexpr int kAhead = 8;
 __global__ void __launch_bounds__(256) decay_prefix_kernel(const __grid_constant__ DecayProblem p) {
     grid_dependency_wait();
     grid_dependents_launch();
@@ -26,14 +28,22 @@ __global__ void __launch_bounds__(256) decay_prefix_kernel(const __grid_constant
     const int L = decay_length(p, b);
     float4 x = first ? *reinterpret_cast<const float4 *>(first + slice * dd + e) : make_float4(0.f, 0.f, 0.f, 0.f);
     float *at = p.states + ((long long)kind * p.slices() + slice) * p.segs * dd + e;
-#pragma unroll 4
-    for (int k = 0; k < p.segs; ++k) {
-        const int s = back ? p.segs - 1 - k : k;
-        float4 *to = reinterpret_cast<float4 *>(at + (long long)s * dd);
-        const float4 t = k + 1 < p.segs ? *to : x;
-        *to = x;
-        const float keep = expf(rate * (float)decay_rows(p, s, L));
-        x.x = fmaf(x.x, keep, t.x), x.y = fmaf(x.y, keep, t.y), x.z = fmaf(x.z, keep, t.z), x.w = fmaf(x.w, keep, t.w);
+    for (int k0 = 0; k0 < p.segs; k0 += kAhead) {
+        float4 t[kAhead];
+        float keep[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int k = k0 + i, s = back ? p.segs - 1 - k : k;
+            keep[i] = k < p.segs ? expf(rate * (float)decay_rows(p, s, L)) : 0.f;
+            // (nothing is behind the last one)
+            t[i] = k + 1 < p.segs ? __ldcg(reinterpret_cast<const float4 *>(at + (long long)s * dd)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int k = k0 + i, s = back ? p.segs - 1 - k : k;
+            if (k < p.segs) *reinterpret_cast<float4 *>(at + (long long)s * dd) = x;
+            x.x = fmaf(x.x, keep[i], t[i].x), x.y = fmaf(x.y, keep[i], t[i].y), x.z = fmaf(x.z, keep[i], t[i].z), x.w = fmaf(x.w, keep[i], t[i].w);
+        }
     }
 }
 

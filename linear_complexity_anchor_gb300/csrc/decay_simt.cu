@@ -5,8 +5,8 @@
 //   S = a b^T (64 x 64), P = p g^(i-j) S below the diagonal, o = w g^(i+1) a X + P c,
 //   X = g^64 X + s sum_j g^(63-j) b_j^T c_j.
 // 16 x 16 threads; X is kept in registers, with a copy in shared memory for a X.  Every number is read from
-// shared memory for four uses at least.  Bound by the FMAs: (64 + CB) (64 + d) per row at CB columns, of which
-// 64 d are done again for each block of columns.
+// shared memory for four uses at least.  Bound by the FMAs and shared memory's reads for them: (64 + CB) (64 + d) per row at
+// CB columns, of which 64 d are done again for each block of columns.  8 x 12 heads, 4200, d = 64: 994 us forward, 1308 backward.
 #include "decay.cuh"
 
 namespace anchor {
@@ -215,7 +215,8 @@ cudaError_t launch(const DecayProblem &p, cudaStream_t stream) {
     return launch_pdl(decay_simt_kernel<D, CB, STATES>, grid, dim3(kThreads), smem, stream, p);
 }
 
-// Heads of 64 and 128 columns go in blocks of 64, or of 32 where blocks of 64 leave SMs without one.
+// Heads of 64 and 128 columns go in blocks of 64, or of 32 where blocks of 64 leave SMs without one (4 x 6 heads x 197, d = 64: 40 us,
+// in blocks of 64 48; 8 x 12 x 4200 backward: in blocks of 64 1308, of 32 1942).
 template <bool STATES>
 cudaError_t launch(const DecayProblem &p, cudaStream_t stream) {
     const long long ctas = p.slices() * p.segs * p.passes * (p.d / 64);

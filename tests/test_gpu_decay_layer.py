@@ -169,3 +169,39 @@ def test_scores_of_any_size(aa):
         assert torch.equal(aa.decay_forward(q * 2.0 ** 60, k, v, rate, scale=2.0 ** -60), base)
         assert torch.equal(aa.decay_forward(q, k * 2.0 ** 50, v * 2.0 ** -50, rate, scale=1.0), base)
         assert math.isfinite(float(aa.decay_forward(q, k, v, rate, scale=2.0 ** 100).float().abs().max()))
+
+
+def test_two_graphs_at_once(aa):
+    # both take workspaces (segments, sums of a weight's gradient), and are replayed on streams of their own
+    g = torch.Generator(device="cuda").manual_seed(21)
+    graphs, wants, outs, runs = [], [], [], []
+    for B, heads, n, d in ((1, 2, 1700, 64), (1, 3, 1500, 128)):
+        Q, K, V, dH = (torch.randn(B, heads, n, d, generator=g, device="cuda").bfloat16() for _ in range(4))
+        X, dY = (torch.randn(n, heads * d, generator=g, device="cuda").bfloat16() for _ in range(2))
+        w = torch.rand(heads * d, generator=g, device="cuda")
+        rate = -1.0 / torch.linspace(30.0, 900.0, heads, device="cuda")
+
+        def run(Q=Q, K=K, V=V, dH=dH, X=X, dY=dY, w=w, rate=rate):
+            H, last = aa.decay_forward(Q, K, V, rate, return_state=True)
+            return (H, last, *aa.decay_backward(Q, K, V, dH, rate)[:3], *aa.add_norm_backward(X, dY, w))
+
+        runs.append(run)  # (with its inputs, which the graphs read)
+        wants.append([t.clone() for t in run()])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(run())
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(5):
+        for out in outs:
+            for t in out:
+                t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for stream, graph in zip(streams, graphs):
+            with torch.cuda.stream(stream):
+                graph.replay()
+                graph.replay()
+        torch.cuda.synchronize()
+        for out, want in zip(outs, wants):
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
