@@ -98,11 +98,11 @@ bool misaligned(const void *p, unsigned bytes) { return ((uintptr_t)p & (bytes -
 // Segments of a sequence: as many as take the least time, by what 128 rows of an item (64 columns of one pass of one head) take,
 // in a pass and for a segment's sums, in us, what an item takes to begin and to end, rounds of items over the SMs, two launches
 // more, and the segments' states, one after the other and through L2.  None where the items fill the SMs: segments read b and c
-// twice.  Measured (us): bf16, d = 128, 4 x 16 heads x 16384: one segment 247, two 320; 2 x 16 x 8192: 121, 105, three 130;
-// 16 x 16384: one 231, two 172, four 113, eight 128; 16 x 2049: one 35, four 37; d = 64, 12 x 16384: one 160, ten 46; one head
-// of 32768: one 312, ten 60, 32: 35.
+// twice.  Measured (us): bf16, d = 128, 4 x 16 heads x 16384: one segment 248, two 314; 2 x 16 x 8192: 121, 101, three 121;
+// 16 x 16384: one 231, two 170, four 104, eight 110; 16 x 2049: one 36, four 30; d = 64, 8 x 12 x 4200: one 51, two 77; 12 x
+// 16384: one 164, ten 44; one head of 32768: one 319, ten 61, 32: 32.
 void plan(DecayProblem &p) {
-    const float pass = p.f32 ? 10.f : p.d == 128 ? 1.88f : 1.38f, sums = pass * 0.48f, item = 2.2f, launches = 16.f;
+    const float pass = p.f32 ? 10.f : p.d == 128 ? 1.88f : 1.38f, sums = pass * 0.48f, item = 2.2f, launches = 8.f;
     const long long slices = p.slices(), halves = p.d == 128 ? 2 : 1;
     const int tiles = (p.n + 127) / 128, most = (int)std::max<long long>(1, std::min<long long>(4 * kPlanSMs / (slices * halves), tiles / 2));
     auto rounds = [](long long items) { return (float)((items + kPlanSMs - 1) / kPlanSMs); };
@@ -112,8 +112,9 @@ void plan(DecayProblem &p) {
         const float each = (float)((tiles + s - 1) / s);
         float t = rounds(slices * halves * p.passes * s) * (each * pass + item);
         if (s > 1)
-            t += rounds(slices * halves * p.kinds * (s - 1)) * (each * sums + item) + launches + 0.15f * (float)s + (float)(slices * p.kinds * s) * (float)(p.d * p.d) * 3e-6f;
-        if (s == 1 || t < best) best = t, want = s;
+            t += rounds(slices * halves * p.kinds * (s - 1)) * (each * sums + item) + launches + 0.1f * (float)s + (float)(slices * p.kinds * s) * (float)(p.d * p.d) * 3e-6f;
+        if (s == 1) best = t - 2.f;  // (the host's part of a call grows too: 12 x 1500, d = 64: 20 us, in segments 25)
+        else if (t < best) best = t, want = s;
     }
     p.seg = (tiles + want - 1) / want * 128;
     p.segs = std::max(1, (int)(((long long)p.n + p.seg - 1) / p.seg));
