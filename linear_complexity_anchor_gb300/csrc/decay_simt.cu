@@ -6,7 +6,7 @@
 //   X = g^64 X + s sum_j g^(63-j) b_j^T c_j.
 // 16 x 16 threads; X is kept in registers, with a copy in shared memory for a X.  Every number is read from
 // shared memory for four uses at least.  Bound by the FMAs and shared memory's reads for them: (64 + CB) (64 + d) per row at
-// CB columns, of which 64 d are done again for each block of columns.  8 x 12 heads, 4200, d = 64: 994 us forward, 1308 backward.
+// CB columns, of which 64 d are done again for each block of columns.  8 x 12 heads, 4200, d = 64: 974 us forward, 1308 backward.
 #include "decay.cuh"
 
 namespace anchor {
@@ -215,12 +215,13 @@ cudaError_t launch(const DecayProblem &p, cudaStream_t stream) {
     return launch_pdl(decay_simt_kernel<D, CB, STATES>, grid, dim3(kThreads), smem, stream, p);
 }
 
-// Heads of 64 and 128 columns go in blocks of 64, or of 32 where blocks of 64 leave SMs without one (4 x 6 heads x 197, d = 64: 40 us,
-// in blocks of 64 48; 8 x 12 x 4200 backward: in blocks of 64 1308, of 32 1942).
+// Heads of 64 and 128 columns go in blocks of 64, or of 32 where blocks of 64 leave half of the SMs without one (us in blocks of
+// 64 and 32: 4 x 6 heads x 197, d = 64, 24 CTAs of 64 columns 48, 40, backward, 72: 50, 42; 4 heads x 1000, d = 128, backward, 96:
+// 106, 124; 8 x 12 x 4200, d = 64, 96: 974, 994; 4 x 16 x 4096, d = 128, 128: 1184, 1344).
 template <bool STATES>
 cudaError_t launch(const DecayProblem &p, cudaStream_t stream) {
     const long long ctas = p.slices() * p.segs * p.passes * (p.d / 64);
-    const bool narrow = ctas < kPlanSMs;
+    const bool narrow = 2 * ctas <= kPlanSMs;
     switch (p.d) {
     case 16: return launch<16, 16, STATES>(p, stream);
     case 32: return launch<32, 32, STATES>(p, stream);
