@@ -100,19 +100,27 @@ bool misaligned(const void *p, unsigned bytes) { return ((uintptr_t)p & (bytes -
 // more, and the segments' states, one after the other and through L2.  None where the items fill the SMs: segments read b and c
 // twice.  Measured (us): bf16, d = 128, 4 x 16 heads x 16384: one segment 248, two 314; 2 x 16 x 8192: 121, 101, three 121;
 // 16 x 16384: one 231, two 170, four 104, eight 110; 16 x 2049: one 36, four 30; d = 64, 8 x 12 x 4200: one 51, two 77; 12 x
-// 16384: one 164, ten 44; one head of 32768: one 319, ten 61, 32: 32.
+// 16384: one 164, ten 44; one head of 32768: one 319, ten 61, 32: 32; fp32, d = 64, 8 x 12 x 4200: one 957, three 621; 4 x 12 x
+// 2000: one 363, six 180; d = 128, 4 x 16 x 4096: one 1171, two 1451; d = 32, 16 x 12 x 2000: one 337, four 309.
 void plan(DecayProblem &p) {
-    const float pass = p.f32 ? 10.f : p.d == 128 ? 1.88f : 1.38f, sums = pass * 0.48f, item = 2.2f, launches = 8.f;
     const long long slices = p.slices(), halves = p.d == 128 ? 2 : 1;
+    const float item = 2.2f, launches = 8.f;
+    // fp32: CTAs an SM (by their shared memory), each of which takes 0.3 more for each beside it; narrow ones take three quarters
+    const int beside = !p.f32 || p.d == 128 ? 1 : p.d == 64 ? 2 : 4;
+    const float each128 = p.f32 ? p.d == 128 ? 37.f : p.d == 64 ? 29.f : 16.f : p.d == 128 ? 1.88f : 1.38f;
     const int tiles = (p.n + 127) / 128, most = (int)std::max<long long>(1, std::min<long long>(4 * kPlanSMs / (slices * halves), tiles / 2));
-    auto rounds = [](long long items) { return (float)((items + kPlanSMs - 1) / kPlanSMs); };
+    auto time = [&](long long items, float rows128) {
+        const long long a_sm = (items + kPlanSMs - 1) / kPlanSMs;
+        const float pass = p.f32 && p.d >= 64 && 2 * items <= kPlanSMs ? 0.75f * each128 : each128;
+        return (float)((a_sm + beside - 1) / beside) * (rows128 * pass * (0.7f + 0.3f * (float)std::min<long long>(beside, a_sm)) + item);
+    };
     float best = 0.f;
     int want = 1;
     for (int s = 1; s <= most; ++s) {
         const float each = (float)((tiles + s - 1) / s);
-        float t = rounds(slices * halves * p.passes * s) * (each * pass + item);
+        float t = time(slices * halves * p.passes * s, each);
         if (s > 1)
-            t += rounds(slices * halves * p.kinds * (s - 1)) * (each * sums + item) + launches + 0.1f * (float)s + (float)(slices * p.kinds * s) * (float)(p.d * p.d) * 3e-6f;
+            t += time(slices * halves * p.kinds * (s - 1), 0.48f * each) + launches + 0.1f * (float)s + (float)(slices * p.kinds * s) * (float)(p.d * p.d) * 3e-6f;
         if (s == 1) best = t - 2.f;  // (the host's part of a call grows too: 12 x 1500, d = 64: 20 us, in segments 25)
         else if (t < best) best = t, want = s;
     }
