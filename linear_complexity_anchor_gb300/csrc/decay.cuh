@@ -49,12 +49,26 @@ __device__ __forceinline__ float decay_rate(const float *log_decay, int h) {
     const float g = __ldg(log_decay + h);
     return g > 0.f ? 0.f : g < -1e4f ? -1e4f : g;
 }
-// What fp32 leaves of `of` factors keep = exp(x).  Rounded the same way each time, it would add up over a sequence that keeps most
-// of its state: 3e-8 of it a factor.  For x above -1/16 (below, sixteen factors are all that matters): exp(x) - 1 by its series,
-// which is off by 1e-10 there, less keep - 1, which is exact.
-__device__ __forceinline__ float decay_rest(float x, float keep, float of) {
-    const float e = x * fmaf(x, fmaf(x, fmaf(x, fmaf(x, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f), 1.f);
-    return x > -0.0625f ? of * (e - (keep - 1.f)) : 0.f;
+// What fp32 leaves of a factor keep = exp(x), x = rate count.  Rounded the same way each time, the factors of a sequence's chunks would add
+// up (2^-24 of a state for each), so what they leave is made good.  For x above -1/2 from the series of exp(x) - 1, with what
+// the square and the product x leave too: off by 2^-26 at most (half a step of x^3 / 6 and what follows), by 2^-31 above -1/8.
+// Below, none: by the time that n factors' 2^-24 have added up no more than e^(-n / 2) is left.
+__device__ __forceinline__ float decay_rest(float rate, float count, float keep) {
+    const float x = rate * count, s = x * x;
+    float u = 1.f / 362880.f;
+    u = fmaf(x, u, 1.f / 40320.f), u = fmaf(x, u, 1.f / 5040.f), u = fmaf(x, u, 1.f / 720.f), u = fmaf(x, u, 1.f / 120.f);
+    u = fmaf(x, u, 1.f / 24.f), u = fmaf(x, u, 1.f / 6.f), u = fmaf(s * x, u, 0.5f * fmaf(x, x, -s));
+    // 1 + x + s / 2 + u, the larger ones first, each sum with what it leaves
+    const float a = fmaf(0.5f, s, x), one = 1.f + a, left = ((1.f - one) + a) + (fmaf(0.5f, s, x - a) + u) + fmaf(rate, count, -x);
+    return x > -0.5f ? (one - keep) + left : 0.f;
+}
+// The factor of the next chunk, with what those before have left (`owed`), and what it leaves itself: the product of a
+// sequence's factors is never off by more than a rounding.
+__device__ __forceinline__ float decay_next(float keep, float rest, float &owed) {
+    owed += rest;
+    const float by = keep + owed;
+    owed = (keep - by) + owed;
+    return by;
 }
 // the rows of segment `s` that count, of an entry with L
 __device__ __forceinline__ int decay_rows(const DecayProblem &p, int s, int L) { return min(max(L - s * p.seg, 0), p.seg); }

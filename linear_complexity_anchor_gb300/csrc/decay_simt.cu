@@ -110,6 +110,8 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const __grid_const
             x[i][c] = !from ? 0.f : turned ? from[(c0 + c) * D + r] : from[r * D + c0 + c];
         }
     const int chunks = (rows + kC - 1) / kC;
+    float rest = 0.f, owed = 0.f;  // what fp32 leaves of a chunk's factor of X, and has left of those before
+    int counted = 0;
     for (int k = 0; k < chunks; ++k) {
         const int first = (back ? chunks - 1 - k : k) * kC, count = min(kC, rows - first);
         const long long r = r0 + first;
@@ -165,8 +167,8 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const __grid_const
                 for (int c = 0; c < NC; ++c) to[c] = o[i][c];
             }
         }
-        float keep = pw[count];
-        if ((k & 31) == 31) keep += decay_rest(rate * (float)count, keep, 32.f);
+        if (count != counted) counted = count, rest = decay_rest(rate, (float)count, pw[count]);
+        const float keep = decay_next(pw[count], rest, owed);
 #pragma unroll
         for (int i = 0; i < NB; ++i)
 #pragma unroll

@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kThreads, 6) decay_step_kernel(const __grid_co
         x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (held && p.from && (D % R == 0 || r < D)) x[i] = *reinterpret_cast<const float4 *>(p.from + offset + (long long)(r + i * R) * D);
     }
-    const float rate = decay_rate(p.log_decay, h), g = expf(rate), rest = decay_rest(rate, g, 1.f);
+    const float rate = decay_rate(p.log_decay, h), g = expf(rate), rest = decay_rest(rate, 1.f, g);
     // Entries that share a slot are taken in order by the CTA of the first.
     bool more = false;
     if (p.slots && held) {
