@@ -9,8 +9,19 @@ namespace {
 
 // Four elements of one slice's states a thread: along the segments in time, the sums of a segment alone
 // are replaced by the state before it.  Bound by the latency of loads from L2, of which kAhead are in flight (2 heads, d = 128, 16384
-// rows: 6.8 us, one at a time 13.2).
+// rows: 6.8 us, one at a time 13.2).  The walk is carried as two numbers, and its factors with what fp32 leaves of them, so that a state is
+// rounded once, however many segments there are.
 constexpr int kAhead = 8;
+struct Walk {
+    float x, left = 0.f;
+    // x <- x keep (1 + what fp32 leaves of keep) + t
+    __device__ __forceinline__ void step(float keep, float rest, float t) {
+        const float p = x * keep, s = p + t, b = s - p;
+        left = fmaf(left, keep, fmaf(x, rest, fmaf(x, keep, -p))) + ((p - (s - b)) + (t - b));
+        x = s + left;
+        left = (s - x) + left;
+    }
+};
 __global__ void __launch_bounds__(256) decay_prefix_kernel(const __grid_constant__ DecayProblem p) {
     grid_dependency_wait();
     grid_dependents_launch();
@@ -26,23 +37,31 @@ __global__ void __launch_bounds__(256) decay_prefix_kernel(const __grid_constant
     const float *first = p.pass[which].state;
     const float rate = decay_rate(p.log_decay, h);
     const int L = decay_length(p, b);
-    float4 x = first ? *reinterpret_cast<const float4 *>(first + slice * dd + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 from = first ? *reinterpret_cast<const float4 *>(first + slice * dd + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    Walk x{from.x}, y{from.y}, z{from.z}, w{from.w};
+    // factors of whole segments, and of the one that the length ends in
+    auto factor = [&](int rows) {
+        const float keep = expf(rate * (float)rows);
+        return make_float2(keep, decay_rest(rate, (float)rows, keep));
+    };
+    float2 whole, part;
+    const float2 none = make_float2(1.f, 0.f);
     float *at = p.states + ((long long)kind * p.slices() + slice) * p.segs * dd + e;
     for (int k0 = 0; k0 < p.segs; k0 += kAhead) {
         float4 t[kAhead];
-        float keep[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int k = k0 + i, s = back ? p.segs - 1 - k : k;
-            keep[i] = k < p.segs ? expf(rate * (float)decay_rows(p, s, L)) : 0.f;
             // (nothing is behind the last one)
             t[i] = k + 1 < p.segs ? __ldcg(reinterpret_cast<const float4 *>(at + (long long)s * dd)) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        if (k0 == 0) whole = factor(p.seg), part = factor(L % p.seg);  // (while the first loads are under way)
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int k = k0 + i, s = back ? p.segs - 1 - k : k;
-            if (k < p.segs) *reinterpret_cast<float4 *>(at + (long long)s * dd) = x;
-            x.x = fmaf(x.x, keep[i], t[i].x), x.y = fmaf(x.y, keep[i], t[i].y), x.z = fmaf(x.z, keep[i], t[i].z), x.w = fmaf(x.w, keep[i], t[i].w);
+            const int k = k0 + i, s = back ? p.segs - 1 - k : k, rows = decay_rows(p, s, L);
+            if (k < p.segs) *reinterpret_cast<float4 *>(at + (long long)s * dd) = make_float4(x.x, y.x, z.x, w.x);
+            const float2 f = rows == p.seg ? whole : rows > 0 ? part : none;
+            if (k + 1 < p.segs) x.step(f.x, f.y, t[i].x), y.step(f.x, f.y, t[i].y), z.step(f.x, f.y, t[i].z), w.step(f.x, f.y, t[i].w);
         }
     }
 }

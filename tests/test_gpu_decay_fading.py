@@ -40,6 +40,22 @@ def rounded(chunks):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("heads,n", [(1, 32768), (1, 131072), (3, 50021), (1, 9999)])
+def test_over_segments(aa, dtype, heads, n):
+    # A few heads: up to 256 segments.  The walk along them is one rounding of its result; the last segment's chunks one each: at most 25 (of
+    # 3200 rows: 3 heads of 50021 bf16 tokens, backward).
+    d = 64
+    X = torch.randn(1, heads, d, d, generator=torch.Generator(device="cuda").manual_seed(n), device="cuda")
+    L = torch.full((1,), n, dtype=torch.int32, device="cuda")
+    worst = 0.0
+    for part in (0.1, 0.35, 0.8, 1.7, 3.1, 6.0):
+        rate = torch.full((heads,), -part / n, device="cuda") * torch.linspace(1, 1.1, heads, device="cuda")
+        for got in left(aa, dtype, 1, heads, n, d, rate, L, X):
+            worst = max(worst, off_by(got, X, rate, L).max().item())
+    assert worst < rounded(25), (worst, rounded(25))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_lengths_that_end_inside_a_chunk(aa, dtype):
     # Entries of one segment (as many heads as there are places), whose last chunk, of 128 rows or of 64, is the 31st, 32nd or 64th, whole and not.
     lengths = [31 * 128 + 1, 31 * 128 + 42, 32 * 128, 31 * 128, 30 * 128 + 7, 32 * 128 + 1, 63 * 128 + 100, 64 * 128 - 1, 64 * 128, 33 * 128 + 5,
@@ -54,6 +70,20 @@ def test_lengths_that_end_inside_a_chunk(aa, dtype):
     for got in left(aa, dtype, B, heads, n, d, rate, L, X):
         off = off_by(got, X, rate, L)
         assert bool((off < bound).all()), (off / bound).max()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [16, 128])
+def test_other_widths(aa, dtype, d):
+    # Segments of 896 rows at most: fourteen chunks of 64.  Four of these at 3 / 3977 are factors below e^-1/2, of which nothing is carried: each
+    # is off by a step of its own (expf's error: one unit in the last place, 2 f of a number above 1/2) that all numbers share.
+    for heads, n in ((1, 20000), (5, 31 * 128 + 9)):
+        X = torch.randn(1, heads, d, d, generator=torch.Generator(device="cuda").manual_seed(d), device="cuda")
+        L = torch.full((1,), n, dtype=torch.int32, device="cuda")
+        rate = -torch.linspace(0.3, 3.0, heads, device="cuda") / n
+        for got in left(aa, dtype, 1, heads, n, d, rate, L, X):
+            off = off_by(got, X, rate, L)
+            assert off.max().item() < rounded(14) + 4 * 2 * F, (heads, off)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
