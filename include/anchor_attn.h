@@ -487,11 +487,13 @@ ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_decay_step(const anchor_attn_de
  *   s = x + r (rounded to the rows' type),  y = weight o s / sqrt(mean(s^2) + eps),
  * with y in the rows' type, or (bits8 = 1) as e4m3 numbers with fp32 scales for each row, or for each
  * `group` columns of it: scale = max |y| / 448, y8 = y / scale, rounded to nearest.  Where max |y| is 0 the
- * scale is 0.  An infinity or a NaN in a row shows in its y and scales.  Sums are taken in fp32; the norm is that
+ * scale is 0.  An infinity or a NaN in a row shows in its y and scales.  Sums are taken in fp32, of rows of any finite size: those
+ * whose squares leave its range are scaled by a power of two.  A row of zeros has y = 0, with eps = 0 too.  The norm is that
  * of s as it is written.  R.ptr = NULL: s is x, and S is not written.  S may be X or R itself (the same view).
  * Backward, from s, dy and (dS.ptr may be NULL) the gradient ds that reaches s by another way, xhat = s / sqrt(...):
  *   dx = (weight o dy - xhat mean(weight o dy o xhat)) / sqrt(...) + ds,  dweight = sum over rows of dy o xhat;
- * dx is the gradient of x and of r.  dX may be dY or dS itself.  Otherwise no output may overlap an input or another
+ * dx is the gradient of x and of r.  With eps = 0 a row of zeros has dx = ds and no part of dweight; 1 / sqrt(...) counts as the largest
+ * fp32 number where it would pass it (rows below 2^-128).  dX may be dY or dS itself.  Otherwise no output may overlap an input or another
  * output (ANCHOR_ATTN_ERR_ALIAS).
  * Rows lie in [B][n][D] views (of one head: `head` is not looked at).  D is a multiple of 16, 16 to 16384;
  * B * n <= 2^31 - 1025.  The backward with a dweight takes a workspace on `stream` and one launch more; results are

@@ -96,7 +96,8 @@ def add_norm(X, R=None, weight=None, *, eps: float = 1e-6, S=None, stream=None):
     """(Y, S): the residual sum S = X + R in the rows' type, and its norm Y = weight S / sqrt(mean(S^2) + eps).
 
     X, R: [n, D] or [B, n, D] (bf16 or fp32; strides as they are, the last axis dense; D a multiple of 16 up to
-    16384); weight: [D], of the rows' type or fp32 (None: ones).  Without R the norm is X's, and S is X.  S may be
+    16384); weight: [D], of the rows' type or fp32 (None: ones).  Rows may be of any finite size; those of zeros have Y = 0, with
+    eps = 0 too.  Without R the norm is X's, and S is X.  S may be
     given, to write the sum over X or R or elsewhere.  Asynchronous on ``stream`` or the current stream."""
     Y, _, S = _forward(X, R, weight, eps, S, 0, 0, stream)
     return Y, S

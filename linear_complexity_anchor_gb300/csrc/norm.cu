@@ -131,12 +131,27 @@ __device__ __forceinline__ float over_row(float v, Op op, float *slots) {
     return v;
 }
 
+// Rows whose squares leave fp32's range: mean s^2 + eps is not above 2^-100 (squares below 2^-126 have lost bits) or not finite.  They are
+// summed again, scaled by a power of two, 2^100 (numbers below 2^-43 by then) or 2^-72: both leave room for 16384 squares.  One test a
+// row, and a branch that ordinary rows do not take.
+struct Far {
+    bool odd;
+    float scale;
+    __device__ __forceinline__ explicit Far(float mean) : odd(!(mean > 0x1p-100f && mean < INFINITY)), scale(!odd ? 1.f : mean < 1.f ? 0x1p100f : 0x1p-72f) {}
+    // 1 / sqrt(mean + eps) of the scaled numbers, from the sum of their squares: 0 for a row of zeros and eps = 0
+    __device__ __forceinline__ float root(float sum, float inv_d, float eps) const {
+        const float mean = fmaf(sum, inv_d, eps * scale * scale);
+        return mean == 0.f ? 0.f : rsqrtf(mean);
+    }
+};
+
 // Threads of a block: a long row's, or those of several rows.
 template <int T> constexpr int kBlock = T > 32 ? T : 128;
 
-// BITS8: GROUP columns share a scale (0: the row).
+// BITS8: GROUP columns share a scale (0: the row).  Five blocks an SM where a thread holds 64 columns of bf16 (65536 x 1040 in 8 bits, scales
+// of 128 columns: 109 us, 16 bytes spilt; four, with two registers a thread more: 122).
 template <typename T, int TPR, int NC, bool BITS8, int GROUP>
-__global__ void __launch_bounds__(kBlock<TPR>) add_norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kBlock<TPR>, NC == 8 && sizeof(T) == 2 ? 5 : 0) add_norm_kernel(const NormParams p) {
     __shared__ float slots[2][TPR > 32 ? TPR / 32 : 1];
     grid_dependency_wait();
     grid_dependents_launch();
@@ -178,7 +193,22 @@ __global__ void __launch_bounds__(kBlock<TPR>) add_norm_kernel(const NormParams 
     for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) q = fmaf(v[c][i], v[c][i], q);
-    const float rs = rsqrtf(fmaf(over_row<TPR>(q, Sum(), slots[0]), p.inv_d, p.eps));
+    q = fmaf(over_row<TPR>(q, Sum(), slots[0]), p.inv_d, p.eps);
+    float rs = rsqrtf(q);
+    const Far far(q);
+    if (__any_sync(0xffffffffu, far.odd)) {  // (the same for all warps of a row)
+        q = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float x = v[c][i] * far.scale;
+                q = fmaf(x, x, q);
+                if (far.scale > 1.f) v[c][i] = x;  // (1 / sqrt of the smallest numbers is none of fp32)
+            }
+        if (TPR > 32) __syncthreads();  // the slots are free again
+        rs = far.root(over_row<TPR>(q, Sum(), slots[0]), p.inv_d, p.eps) * fminf(far.scale, 1.f);
+    }
     float top = 0.f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -304,26 +334,55 @@ __global__ void __launch_bounds__(kBackBlock<TPR>) add_norm_backward_kernel(cons
                 z2 = fma_f32x2(mul_f32x2(a[i], w2[i]), b[i], z2);
             }
         }
-        float q = sum2(q2), z = sum2(z2);
+        float q, z;
+        auto total = [&](float q_here, float z_here, bool again) {
+            q = q_here, z = z_here;
 #pragma unroll
-        for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
-            q += __shfl_xor_sync(0xffffffffu, q, o);
-            z += __shfl_xor_sync(0xffffffffu, z, o);
-        }
-        if (TPR > 32) {
-            // both through one barrier; a step's slots are free again behind the next step's barrier
-            if ((threadIdx.x & 31) == 0) both[turn][threadIdx.x >> 5] = make_float2(q, z);
-            __syncthreads();
-            const float2 o2 = both[turn][(threadIdx.x & 31) % (TPR > 32 ? TPR / 32 : 1)];
-            q = o2.x, z = o2.y;
-#pragma unroll
-            for (int o = TPR / 64; o > 0; o >>= 1) {
+            for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
                 q += __shfl_xor_sync(0xffffffffu, q, o);
                 z += __shfl_xor_sync(0xffffffffu, z, o);
             }
+            if (TPR > 32) {
+                // both through one barrier; a step's slots are free again behind the next step's barrier
+                if (again) __syncthreads();
+                if ((threadIdx.x & 31) == 0) both[turn][threadIdx.x >> 5] = make_float2(q, z);
+                __syncthreads();
+                const float2 o2 = both[turn][(threadIdx.x & 31) % (TPR > 32 ? TPR / 32 : 1)];
+                q = o2.x, z = o2.y;
+#pragma unroll
+                for (int o = TPR / 64; o > 0; o >>= 1) {
+                    q += __shfl_xor_sync(0xffffffffu, q, o);
+                    z += __shfl_xor_sync(0xffffffffu, z, o);
+                }
+            }
+        };
+        total(sum2(q2), sum2(z2), false);
+        const float size = fmaf(q, p.inv_d, p.eps);
+        float rs = rsqrtf(size), mean = -z * rs * p.inv_d;
+        const Far far(size);
+        if (__any_sync(0xffffffffu, far.odd)) {
+            const uint64_t scale2 = f32x2(far.scale, far.scale);
+            q2 = z2 = 0ull;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                uint64_t a[4], b[4], w_here[4], *w2 = kKeep ? w_kept[kKeep ? c : 0] : w_here;
+                unpack2(s[c], a);
+                unpack2(y[c], b);
+                if constexpr (!kKeep) weights(c, w2);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t x = mul_f32x2(a[i], scale2);
+                    q2 = fma_f32x2(x, x, q2);
+                    z2 = fma_f32x2(mul_f32x2(x, w2[i]), b[i], z2);
+                }
+            }
+            total(sum2(q2), sum2(z2), true);
+            // (of the warp's other rows these are the same numbers again)
+            rs = far.root(q, p.inv_d, p.eps);
+            if (far.scale > 1.f && rs > 0x1.fffffep27f) rs = 0x1.fffffep27f;  // (FLT_MAX / scale: 1 / sqrt counts as the largest number)
+            mean = -z * rs * p.inv_d;
+            rs *= far.scale;
         }
-        const float rs = rsqrtf(fmaf(q, p.inv_d, p.eps));
-        const float mean = -z * rs * p.inv_d;
         const uint64_t rs2 = f32x2(rs, rs), mean2 = f32x2(mean, mean);
         T *xp = row_of<T>(p, p.dx, row);
 #pragma unroll
