@@ -437,14 +437,17 @@ ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_cross_backward(const anchor_att
  *   lengths: device int32 [B], each taken into [0, n]: the tokens of an entry that count; NULL: n for all
  *   state, last, dlast, dstate: fp32, dense [B][heads][d (of k)][d (of v)], on 16 bytes: the states before the first
  *   token (NULL: zeros) and behind the last one that counts (NULL: not wanted), and their gradients
- * Rows of H, dQ, dK and dV from an entry's length on are zero; what the inputs hold there does not matter.  (Before it
- * an infinity or a NaN at a token may reach the rows of up to 127 tokens before it.)  Heads or entries that share
+ * Rows of H, dQ, dK and dV from an entry's length on are zero; what the inputs hold there does not matter.  Before it
+ * an infinity or a NaN at a token shows where the formulas have it (a NaN in K, V at the rows of H and dQ from there on, in Q, dH at those of dK
+ * and dV up to there) and, but in forward calls of up to 8 (bf16) or 16 (fp32) tokens, at the rows of its chunk on the other side too: of
+ * the 128 tokens (fp32: 64) from a multiple of as many on, whose products give it a weight of 0.  Heads or entries that share
  * rows by a stride of 0 get gradients of their own.  An infinity in a row or a state counts as a NaN.
  * bf16 in and out (tensor cores: bf16 operands and fp32 accumulators; the weights of pairs and the state are rounded
  * to bf16 where they meet c and a, the state itself is kept in fp32) or fp32 (CUDA cores, fp32 throughout).
  * d in {16, 32, 64, 128}; B * heads <= 2^24, B * heads * n <= 2^31 - 1024.  No output may overlap an input or another
- * output (ANCHOR_ATTN_ERR_ALIAS).  Results are bit-identical from run to run.  Workspaces come from the library's pool on
- * `stream`, as cross attention's.
+ * output (ANCHOR_ATTN_ERR_ALIAS).  Results are bit-identical from run to run.  In bf16 a call with `last` may differ from one without in single
+ * bits of H (rows that count in a state that is given out are three bf16 numbers, else two), and so may one with `dstate` in those of dK and dV.
+ * Workspaces come from the library's pool on `stream`, as cross attention's.
  */
 typedef struct {
     int dtype;                  /* 0 = bf16, 1 = fp32                                         */
@@ -467,7 +470,7 @@ ANCHOR_ATTN_API anchor_attn_status_t anchor_attn_decay_backward(const anchor_att
  *   states: fp32, dense [slot_count][heads][d][d], on 16 bytes; slots: device int32 [B], where each request's state
  *   lies; NULL: request b's is b (slot_count >= B)
  * A request whose slot is negative or not below slot_count has H = 0 and moves no state.  Requests that share a slot
- * are taken one after the other, in their order.  Slots of no request are left as they are.
+ * are taken one after the other, in their order (all B slots are read for every 32 columns of a state, 16 KB of it at d = 128).  Slots of no request are left as they are.
  */
 typedef struct {
     int dtype;

@@ -62,7 +62,8 @@ def decay_forward(Q, K, V, log_decay, lengths=None, *, state=None, H=None, scale
     0; lengths: int32 [B] on the device, the tokens of each entry that count (None: all; the rows behind them are 0).
     state: fp32 [B, heads, d, d], the sum of k v^T (decayed) that the entries begin with; None: zeros.  scale defaults to
     1/sqrt(d).  Returns H in Q's order of axes, and with return_state the states behind the last tokens, which a next
-    call or ``decay_step`` goes on from.  Asynchronous on ``stream`` or the current stream."""
+    call or ``decay_step`` goes on from (in bf16 single bits of H may differ then).  A NaN or an infinity in K or V shows at the tokens from
+    there on, and at those before it in its chunk: of the 128 (fp32: 64) from a multiple of that on.  Asynchronous on ``stream`` or the current stream."""
     device, numbers, scale, views, at_decay = _problem(Q, K, V, log_decay, scale)
     shape = Q.shape
     states = (shape[0], shape[1], shape[3], shape[3])
@@ -88,7 +89,8 @@ def decay_forward(Q, K, V, log_decay, lengths=None, *, state=None, H=None, scale
 def decay_backward(Q, K, V, dH, log_decay, lengths=None, *, state=None, dstate=None, scale: float | None = None, stream=None):
     """(dQ, dK, dV, dstate) for the upstream gradients dH of ``decay_forward``'s H and dstate (None: zero) of the states
     that it returns; the other arguments are those of that call.  The last is the gradient of its ``state``, None without
-    one.  Rows from an entry's length on are zero.  Heads or entries that share rows by an expanded axis get a gradient
+    one.  Rows from an entry's length on are zero.  A NaN or an infinity in Q or dH shows at dK and dV of the tokens up to
+    there, and of those behind it in its chunk; in K or V as in the forward.  Heads or entries that share rows by an expanded axis get a gradient
     each; the decays get none."""
     device, numbers, scale, views, at_decay = _problem(Q, K, V, log_decay, scale)
     shape = Q.shape
