@@ -9,7 +9,7 @@ namespace {
 
 // Four elements of one slice's states a thread: along the segments in time, the sums of a segment alone
 // are replaced by the state before it.  Bound by the latency of loads from L2, of which kAhead are in flight (2 heads, d = 128, 16384
-// rows: 6.8 us, one at a time 13.2).  The walk is carried as two numbers, and its factors with what fp32 leaves of them, so that a state is
+// rows: 9.4 us; in one number and with one load at a time it took 13.2, with eight 8.1).  The walk is carried as two numbers, and its factors with what fp32 leaves of them, so that a state is
 // rounded once, however many segments there are.
 constexpr int kAhead = 8;
 struct Walk {
@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(256) decay_prefix_kernel(const __grid_constant
     grid_dependency_wait();
     grid_dependents_launch();
     const int dd = p.d * p.d, per = dd / 4;
-    const long long f = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long f = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     const int kind = blockIdx.y;
     if (f >= p.slices() * per) return;
     const long long slice = f / per;
@@ -156,7 +156,10 @@ cudaError_t run(DecayProblem &p, cudaStream_t stream) {
     if (p.segs > 1) {
         e = p.f32 ? launch_decay_simt_states(p, stream) : launch_decay_tc_states(p, stream);
         const long long threads = p.slices() * (p.d * p.d / 4);
-        if (e == cudaSuccess) e = launch_pdl(decay_prefix_kernel, dim3((unsigned)((threads + 255) / 256), p.kinds), dim3(256), 0, stream, p);
+        // few threads are spread over the SMs (2 heads, d = 128, 16384 rows: 9.4 us, in CTAs of 256 10.4; one head of 64: 13.0, 15.2; but 16
+        // heads, d = 128, 2049 rows: a call takes 32.2 us with CTAs of 64, 31.5 with 256)
+        const int each = threads <= kPlanSMs * 256 ? 64 : 256;
+        if (e == cudaSuccess) e = launch_pdl(decay_prefix_kernel, dim3((unsigned)((threads + each - 1) / each), p.kinds), dim3(each), 0, stream, p);
     }
     if (e != cudaSuccess) return e;
     return p.f32 ? launch_decay_simt(p, stream) : launch_decay_tc(p, stream);

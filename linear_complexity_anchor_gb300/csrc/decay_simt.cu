@@ -110,8 +110,9 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const __grid_const
             x[i][c] = !from ? 0.f : turned ? from[(c0 + c) * D + r] : from[r * D + c0 + c];
         }
     const int chunks = (rows + kC - 1) / kC;
-    float rest = 0.f, owed = 0.f;  // what fp32 leaves of a chunk's factor of X, and has left of those before
-    int counted = 0;
+    // what fp32 leaves of a whole chunk's factor of X (one that is not whole adds a rounding), and has left of those before
+    const float rest = decay_rest(rate, (float)kC, expf(rate * (float)kC));
+    float owed = 0.f;
     for (int k = 0; k < chunks; ++k) {
         const int first = (back ? chunks - 1 - k : k) * kC, count = min(kC, rows - first);
         const long long r = r0 + first;
@@ -167,8 +168,8 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const __grid_const
                 for (int c = 0; c < NC; ++c) to[c] = o[i][c];
             }
         }
-        if (count != counted) counted = count, rest = decay_rest(rate, (float)count, pw[count]);
-        const float keep = decay_next(pw[count], rest, owed);
+        float keep = pw[count];
+        if (count == kC) keep = decay_next(keep, rest, owed);
 #pragma unroll
         for (int i = 0; i < NB; ++i)
 #pragma unroll

@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_kernel(const __grid_constan
                         if (centred && fine(k)) weight = expf(rate * (far - 64.f)) - 1.f, mid = it.q->s * expf(rate * 64.f);
                         else weight = it.q->s * expf(rate * far);
                         keep = expf(rate * (float)count);
-                        // (few factors do without: 128 x 12 x 197 would take 82 us instead of 78)
+                        // (few factors do without: 128 x 12 x 197 would take 82 us instead of 77)
                         rest = it.K > 4 ? decay_rest(rate, (float)count, keep) : 0.f;
                     }
                     // the rows of c, once the product of the chunk before is complete
