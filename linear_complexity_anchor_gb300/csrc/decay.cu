@@ -117,10 +117,10 @@ bool misaligned(const void *p, unsigned bytes) { return ((uintptr_t)p & (bytes -
 // Segments of a sequence: as many as take the least time, by what 128 rows of an item (64 columns of one pass of one head) take,
 // in a pass and for a segment's sums, in us, what an item takes to begin and to end, rounds of items over the SMs, two launches
 // more, and the segments' states, one after the other and through L2.  None where the items fill the SMs: segments read b and c
-// twice.  Measured (us): bf16, d = 128, 4 x 16 heads x 16384: one segment 248, two 314; 2 x 16 x 8192: 121, 101, three 121;
+// twice.  Measured (us): bf16, d = 128, 4 x 16 heads x 16384: one segment 250, two 314; 2 x 16 x 8192: 121, 101, three 121;
 // 16 x 16384: one 231, two 170, four 104, eight 110; 16 x 2049: one 36, four 30; d = 64, 8 x 12 x 4200: one 51, two 77; 12 x
-// 16384: one 164, ten 44; one head of 32768: one 319, ten 61, 32: 32; fp32, d = 64, 8 x 12 x 4200: one 957, three 621; 4 x 12 x
-// 2000: one 363, six 180; d = 128, 4 x 16 x 4096: one 1171, two 1451; d = 32, 16 x 12 x 2000: one 337, four 309.
+// 16384: one 164, ten 44; one head of 32768: one 319, ten 61, 32: 32; fp32, d = 64, 8 x 12 x 4200: one 957, three 611; 4 x 12 x
+// 2000: one 363, six 180; d = 128, 4 x 16 x 4096: one 1168, two 1451; d = 32, 16 x 12 x 2000: one 337, four 309.
 void plan(DecayProblem &p) {
     const long long slices = p.slices(), halves = p.d == 128 ? 2 : 1;
     const float item = 2.2f, launches = 8.f;
@@ -147,8 +147,12 @@ void plan(DecayProblem &p) {
     p.segs = std::max(1, (int)(((long long)p.n + p.seg - 1) / p.seg));
 }
 
-// A call of few tokens goes token by token, which costs more with each, where a chunk costs the same for all (64 x 32 heads, d =
-// 128, with states, us: bf16 8 tokens 149 against 205, 12: 210 against 204; fp32 16: 282 against 418, 32: 540 against 458).
+// A call of few tokens goes token by token, which costs more with each, where a chunk costs the same for all.  Measured (us, by tokens and in a
+// chunk, states in and out / neither): bf16, 64 x 32 heads, d = 128, 8 tokens: 137, 197 / 109, 109; 12: 194, 196 / 159, 108; d = 64, 8: 49, 82 / 45, 51;
+// 12: 70, 82 / 63, 51; d = 16, 8: 25, 72 / 25, 51; 24: 66, 72 / 65, 52; 256 x 12, d = 64, 8: 76, 122 / 65, 74; 12: 107, 121 / 93, 74.  fp32,
+// 64 x 32, d = 128, 16 tokens: 263, 415 / 215, 342; 32: 503, 455 / 489, 411; d = 64, 16: 99, 107 / 81, 96; 24: 146, 122 / 120, 103; d = 16, 12: 35, 37 / 34, 36; 16:
+// 45, 38 / 44, 37.  Few heads take 13 to 20 both ways.  With states bf16 could go on to 12 to 24 tokens by d; the bits of H would
+// then depend on whether there are any.
 bool by_steps(const anchor_attn_decay_t *a) { return a->n <= (a->dtype ? 16 : 8); }
 
 cudaError_t run(DecayProblem &p, cudaStream_t stream) {

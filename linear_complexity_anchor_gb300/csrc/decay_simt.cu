@@ -4,10 +4,12 @@
 // and of the state:
 //   S = a b^T (64 x 64), P = p g^(i-j) S below the diagonal, o = w g^(i+1) a X + P c,
 //   X = g^64 X + s sum_j g^(63-j) b_j^T c_j.
-// 16 x 16 threads; X is kept in registers, with a copy in shared memory for a X.  Every number is read from
-// shared memory for four uses at least.  Bound by the FMAs and shared memory's reads for them: (64 + CB) (64 + d) per row at
-// CB columns, of which 64 d are done again for each block of columns.  8 x 12 heads, 4200, d = 64: 621 us forward (three
-// segments; one: 958), 1300 backward.
+// 16 x 16 threads; X is kept in registers, with a copy in shared memory for a X.  In blocks of 64 columns every number is read from
+// shared memory for four uses at least, in blocks of 32 those of a and P for two, of 16 for one.  (64 + CB) (64 + d) FMAs per row at CB columns, of
+// which 64 d are done again for each block of columns.  4 x 16 heads, 4096, d = 128: 1168 us forward, of which the FMAs would take 320: with
+// eight warps an SM (137 KB of shared memory each CTA, whose tiles are fetched between two barriers, one chunk at a time, and nothing runs
+// meanwhile) an instruction is issued every other cycle, and a warp waits 0.9 cycles of each 3.9 for tiles and 0.75 for shared memory.  8 x 12 heads,
+// 4200, d = 64: 611 us forward (three segments; one: 958), 1293 backward.
 #include "decay.cuh"
 
 namespace anchor {

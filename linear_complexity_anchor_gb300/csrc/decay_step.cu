@@ -5,6 +5,9 @@
 // threads, four columns a thread and every (256 / (CB / 4))-th row; a token's h is summed over a warp's rows by
 // shuffles and over the warps through shared memory, in a fixed order.  Bound by reading and writing the states: 64 requests, 32
 // heads, d = 128, bf16: 46 us, 5.8 TB/s with six CTAs an SM (48.5 with as many as the registers gave; 16 columns a CTA 67, 64: 49).
+// Several tokens are bound by latency, one after the other, each fetched and summed between barriers: 2 tokens 58, 4: 81, 8: 136.  Shared
+// slots: each CTA reads all B slots, which counts from about a thousand requests on (with slots and without: 1024 x 4 heads, d = 128: 98, 84; 4096 x 2: 235,
+// 164; 16384 x 1, d = 64: 374, 112).
 // One size for all, so that a request's bits do not depend on the batch.
 #include "decay.cuh"
 

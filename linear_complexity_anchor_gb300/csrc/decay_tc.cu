@@ -19,7 +19,8 @@
 // first two, before the products, 281.)
 // What a chunk adds to X is a sum of its own, added by the rows, to nearest: the tensor cores' sums are cut off, which over many
 // chunks would add up where X decays slowly (6e-6 of a state that reaches 3717 rows back, without a bound at a decay of 0; a
-// loop that sums X there takes 3 % less at d = 64, nothing less at 128).  With X in registers a chunk took 5 % more at d = 64.
+// loop that sums X there takes 3 % less at d = 64, nothing less at 128).  With X in registers a chunk took 5 % more at d = 64.  What fp32
+// leaves of the factors g^count is carried from chunk to chunk (decay.cuh), for the same reason.
 //
 // Two groups of eight warps, a thread half of a row: the first makes P of the next chunk, and o from its two products; the
 // second the weighted rows of c, X~ and X.  One warp loads tiles by TMA, one stores o's, one issues the products: P c, S of the
@@ -55,7 +56,8 @@ constexpr int kSlice = kColumns / kParts;         // columns of o, of the state 
 constexpr int kRegsRows = 136, kRegsState = 80, kRegsOthers = 40;
 constexpr uint32_t kColS = 0, kColP = 128, kColIn = 192, kColBy = 256, kColX = 320, kColAdd = 384, kCols = 512;  // of tensor memory
 
-// D columns of a and b (heads of 16 and 32 are 64)
+// D columns of a and b.  Heads of 16 and 32 are 64, whose other columns are zeros: a chunk takes what 64 take (8 x 12 heads x 4200, us: d = 64 51, 32:
+// 49, 16: 47).
 template <int D, bool STATES>
 struct Geo {
     static constexpr int kStages = STATES ? 3 : D == 128 ? 2 : 3;

@@ -7,7 +7,10 @@
 // Rows of up to 2048 columns (backward: 1024, whose registers end there) belong to a warp, which needs no barrier; longer ones
 // to a block.  (bf16, 8 bits: 65536 x 1024 by a warp 73 us, by four 86; 65536 x 2048 139, by eight 170; in 16 bits the
 // same to 1 %.  Backward: 65536 x 1024 93, by four 94; 65536 x 2048 by a warp 1236, by eight 178.)  65536 x 2048 in 8 bits:
-// 138 us, 6.8 TB/s; 33600 x 768 backward: 40 us with the second launch, 5.2 TB/s.
+// 138 us, 6.8 TB/s; 33600 x 768 backward: 40 us with the second launch, 5.2 TB/s.  (fp32, the same layouts: forward 32768 x 1024 81 us,
+// 6.6 TB/s, 16384 x 2048 83; backward with ds and dw 32768 x 768 69 us, 5.8 TB/s, x 1024 102, 5.3, where a warp's columns do not fit its registers, x 1040
+// 104, 16384 x 2048 86, 6.2, 4096 x 8192 96, 3000 x 16384 158, 5.0, which do not fit either.  bf16: 65536 x 1024 108 us, 5.0 TB/s, x 1040 159, 3.4:
+// 130 of a block's 256 threads have columns; 6000 x 16384 166, 4.8.)
 //
 // Backward: xhat = s r, r = 1 / sqrt(mean s^2 + eps):
 //   dx = r (w o dy - xhat mean(w o dy o xhat)) + ds,  dw += dy o xhat.
